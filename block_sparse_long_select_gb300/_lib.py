@@ -7,6 +7,7 @@ from functools import lru_cache
 
 MSA_BF16, MSA_FP32 = 0, 1
 MSA_OP_INDEX_SELECT, MSA_OP_PREFILL, MSA_OP_DECODE, MSA_OP_DECODE_STEP, MSA_OP_KL_AUX, MSA_OP_BACKWARD = 0, 1, 2, 3, 4, 5
+MSA_OP_FULL_PREFILL, MSA_OP_FULL_BACKWARD, MSA_OP_FULL_DECODE, MSA_OP_PAGED_APPEND = 8, 9, 10, 11
 MSA_FORCE_LOCAL, MSA_FORCE_START = 1, 2
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_WORKSPACE",
                 4: "MSA_ERR_CUDA", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_BOUNDS"}
@@ -22,6 +23,11 @@ SIGNATURES = {
     "msa_decode_step": (_i32, [_vp] * 9 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "msa_kl_aux_forward": (_i32, [_vp] * 8 + [_i32] * 9 + [_f32, _i32, _vp, _vp, _sz, _vp]),
     "msa_sparse_attn_backward": (_i32, [_vp] * 9 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "msa_paged_append": (_i32, [_vp] * 7 + [_i32] * 12 + [_vp] * 4 + [_sz, _vp]),
+    "msa_full_attn_decode": (_i32, [_vp] * 5 + [_i32] * 7 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "msa_full_attn_prefill": (_i32, [_vp] * 5 + [_i32] * 6 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "msa_full_attn_prefill_paged": (_i32, [_vp] * 6 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "msa_full_attn_backward": (_i32, [_vp] * 8 + [_i32] * 6 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "msa_read_status": (_i32, [_vp, _vp]),
     "msa_status_string": (ctypes.c_char_p, [_i32]),
     "msa_index_select_noalloc": (_i32, [_vp, _vp, _vp, _vp] + [_i32] * 8 + [_vp, _vp, _vp]),
@@ -309,4 +315,223 @@ def msa_sparse_attn_backward(q, k, v, out, dout, lse, sel, q_offset, kv_len, Bs,
                                                    Bs, K, float(scale), dt, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
                                                    ws.numel(), _stream(stream, q.device))
     _check(code, "msa_sparse_attn_backward")
+    return dq, dk, dv
+
+
+# ---- full attention and paged caches -----------------------------------------
+def _check_like(ref, **ts):
+    """Contiguous CUDA tensors of ``ref``'s dtype and device, of the given shapes
+    (name=(tensor, shape); None is skipped): the library reads and writes them
+    through raw pointers."""
+    for name, (t, shape) in ts.items():
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.dtype != ref.dtype or t.device != ref.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, of dtype {ref.dtype} on {ref.device}")
+
+
+def _check_typed(ref, dtype, **ts):
+    """The same for tensors of another dtype (offsets, lengths, tables, lse)."""
+    for name, (t, shape) in ts.items():
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, of dtype {dtype} on {ref.device}")
+
+
+def _rows(name, t, dims=3):
+    """A packed-row tensor [rows, heads, d] (or a cache, dims 4): its shape after the checks every call makes."""
+    if t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor with {dims} dimensions")
+    return t.shape
+
+
+class _on:
+    """Makes ``stream`` (and its device) current, so that what a wrapper
+    allocates belongs to it and launches go to the tensors' device; nothing to
+    do where both are current already."""
+
+    __slots__ = ("ctx", "ptr")
+
+    def __init__(self, stream, device):
+        import torch
+
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+            self.ptr = stream.cuda_stream
+        else:
+            self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _full_ws(ws, ref, op, B, Nq, Nk, Hkv, Hq, d, dt):
+    if ws is None:
+        ws = workspace(msa_workspace_size(op, B, Nq, Nk, Hkv, Hq, d, 0, 0, 0, dt), ref.device)
+    elif ws.device != ref.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {ref.device}")
+    return ws
+
+
+def msa_paged_append(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache, v_cache, interleaved=False,
+                     q_out=None, ws=None, stream=None):
+    """Append packed new tokens to a paged cache and rotate keys and queries by
+    position (see include/msa.h). q [T,Hq,d] or None, k_new, v_new [T,Hkv,d],
+    rope [max_pos, rot/2, 2] fp32 or None, cu_new [B+1] or None (one token per
+    sequence), kv_len [B] (the new tokens counted), page_table [B, max_pages],
+    caches [num_pages, page_size, Hkv, d]. Returns the rotated queries (None
+    without q); ``q_out=q`` rotates in place."""
+    import torch
+
+    T, Hkv, d = _rows("k_new", k_new)
+    num_pages, page_size = _rows("k_cache", k_cache, 4)[:2]
+    B, max_pages = page_table.shape
+    if q is not None:
+        Hq = _rows("q", q)[1]
+        _check_like(k_new, q=(q, (T, Hq, d)), q_out=(q_out, (T, Hq, d)))
+    else:
+        Hq = Hkv
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+    _check_like(k_new, v_new=(v_new, (T, Hkv, d)), k_cache=(k_cache, (num_pages, page_size, Hkv, d)),
+                v_cache=(v_cache, (num_pages, page_size, Hkv, d)))
+    _check_typed(k_new, torch.int32, cu_new=(cu_new, (B + 1,)), kv_len=(kv_len, (B,)),
+                 page_table=(page_table, (B, max_pages)))
+    max_pos = half = 0
+    if rope is not None:
+        max_pos, half = rope.shape[:2]
+        _check_typed(k_new, torch.float32, rope=(rope, (max_pos, half, 2)))
+    dt = _dtype_code(k_new)
+    with _on(stream, k_new.device) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q)
+        ws = _full_ws(ws, k_new, MSA_OP_PAGED_APPEND, B, T, 0, Hkv, Hq, d, dt)
+        code = load_library().msa_paged_append(_addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(rope),
+                                               _addr(cu_new), kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, Hkv,
+                                               d, 2 * half, int(interleaved), max_pos, num_pages, page_size,
+                                               max_pages, dt, _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                                               ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    _check(code, "msa_paged_append")
+    return q_out
+
+
+def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out=None, lse=None, ws=None,
+                         stream=None):
+    """One query row per sequence over its whole paged cache (see include/msa.h):
+    q [B,Hq,d], caches [num_pages, page_size, Hkv, d] -> out [B,Hq,d]."""
+    import torch
+
+    B, Hq, d = _rows("q", q)
+    num_pages, page_size, Hkv, _ = _rows("k_cache", k_cache, 4)
+    max_pages = page_table.shape[1]
+    _check_like(q, k_cache=(k_cache, (num_pages, page_size, Hkv, d)), v_cache=(v_cache, k_cache.shape),
+                out=(out, q.shape))
+    _check_typed(q, torch.int32, kv_len=(kv_len, (B,)), page_table=(page_table, (B, max_pages)))
+    _check_typed(q, torch.float32, lse=(lse, (B, Hq)))
+    dt = _dtype_code(q)
+    with _on(stream, q.device) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        ws = _full_ws(ws, q, MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv, Hq, d, dt)
+        code = load_library().msa_full_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                   page_table.data_ptr(), kv_len.data_ptr(), B, Hq, Hkv, d, num_pages,
+                                                   page_size, max_pages, float(scale), dt, out.data_ptr(),
+                                                   _addr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    _check(code, "msa_full_attn_decode")
+    return out
+
+
+def msa_full_attn_prefill(q, k, v, cu_q, cu_k, scale=0.0, out=None, lse=None, ws=None, stream=None):
+    """Causal attention over packed sequences (see include/msa.h): q [Tq,Hq,d],
+    k, v [Tk,Hkv,d], cu_q, cu_k [B+1] int32 -> out [Tq,Hq,d]."""
+    import torch
+
+    Tq, Hq, d = _rows("q", q)
+    Tk, Hkv, _ = _rows("k", k)
+    B = cu_q.shape[0] - 1
+    _check_like(q, k=(k, (Tk, Hkv, d)), v=(v, (Tk, Hkv, d)), out=(out, q.shape))
+    _check_typed(q, torch.int32, cu_q=(cu_q, (B + 1,)), cu_k=(cu_k, (B + 1,)))
+    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    dt = _dtype_code(q)
+    with _on(stream, q.device) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, Tk, Hkv, Hq, d, dt)
+        code = load_library().msa_full_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+                                                    cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, d, float(scale), dt,
+                                                    out.data_ptr(), _addr(lse), ws.data_ptr(),
+                                                    ws.numel() * ws.element_size(), s)
+    _check(code, "msa_full_attn_prefill")
+    return out
+
+
+def msa_full_attn_prefill_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, scale=0.0, out=None, lse=None,
+                                ws=None, stream=None):
+    """msa_full_attn_prefill with each sequence's kv_len[b] keys in a paged cache
+    (see include/msa.h): q [Tq,Hq,d], cu_q [B+1], page_table [B, max_pages] -> out [Tq,Hq,d]."""
+    import torch
+
+    Tq, Hq, d = _rows("q", q)
+    num_pages, page_size, Hkv, _ = _rows("k_cache", k_cache, 4)
+    B, max_pages = page_table.shape
+    _check_like(q, k_cache=(k_cache, (num_pages, page_size, Hkv, d)), v_cache=(v_cache, k_cache.shape),
+                out=(out, q.shape))
+    _check_typed(q, torch.int32, kv_len=(kv_len, (B,)), cu_q=(cu_q, (B + 1,)),
+                 page_table=(page_table, (B, max_pages)))
+    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    dt = _dtype_code(q)
+    with _on(stream, q.device) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, max_pages * page_size, Hkv, Hq, d, dt)
+        code = load_library().msa_full_attn_prefill_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                          page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+                                                          B, Tq, Hq, Hkv, d, num_pages, page_size, max_pages,
+                                                          float(scale), dt, out.data_ptr(), _addr(lse),
+                                                          ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    _check(code, "msa_full_attn_prefill_paged")
+    return out
+
+
+def msa_full_attn_backward(q, k, v, out, dout, lse, cu_q, cu_k, dq=None, dk=None, dv=None, scale=0.0, ws=None,
+                           stream=None):
+    """Gradients of msa_full_attn_prefill (see include/msa.h) from its output,
+    its lse [Tq,Hq] and the output gradient ``dout``. Returns (dq, dk, dv)."""
+    import torch
+
+    Tq, Hq, d = _rows("q", q)
+    Tk, Hkv, _ = _rows("k", k)
+    B = cu_q.shape[0] - 1
+    _check_like(q, k=(k, (Tk, Hkv, d)), v=(v, (Tk, Hkv, d)), out=(out, q.shape), dout=(dout, q.shape),
+                dq=(dq, q.shape), dk=(dk, k.shape), dv=(dv, k.shape))
+    _check_typed(q, torch.int32, cu_q=(cu_q, (B + 1,)), cu_k=(cu_k, (B + 1,)))
+    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    dt = _dtype_code(q)
+    with _on(stream, q.device) as s:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        ws = _full_ws(ws, q, MSA_OP_FULL_BACKWARD, B, Tq, Tk, Hkv, Hq, d, dt)
+        code = load_library().msa_full_attn_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                                     dout.data_ptr(), lse.data_ptr(), cu_q.data_ptr(),
+                                                     cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, d, float(scale), dt,
+                                                     dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                                     ws.numel() * ws.element_size(), s)
+    _check(code, "msa_full_attn_backward")
     return dq, dk, dv

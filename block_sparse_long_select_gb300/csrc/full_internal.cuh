@@ -1,0 +1,125 @@
+// Shared by the full-attention and paged-cache kernels: where a sequence's
+// rows and keys lie, the searches over packed offsets, and the launchers.
+#pragma once
+
+#include "msa_internal.cuh"
+
+namespace msa {
+
+constexpr int kMaxFullHpg = 64;  // query heads per key/value head
+
+// Pages of a cache [num_pages, page_size, Hkv, d] and the table that maps
+// sequences to them. table == nullptr: keys are packed rows instead.
+struct PageMap {
+  const int32_t* table;
+  int num_pages, page_log2, max_pages;
+};
+
+// Rows and keys of a batch: query rows packed by cu_q (nullptr: row b is
+// sequence b's only one); keys packed by cu_k, or kv_len[b] keys in pages.
+struct SeqMap {
+  const int32_t* cu_q;
+  const int32_t* cu_k;    // packed keys
+  const int32_t* kv_len;  // paged keys
+  int B, Tq, Tk;          // Tk: packed key rows, or max_pages * page_size
+};
+struct SeqSpan {
+  int q0, Lq, k0, Lk;  // k0: first packed key row (0 for paged keys)
+  bool rows_ok, ok;    // rows_ok: q0 and Lq can be trusted; ok: the keys too
+};
+__device__ __forceinline__ SeqSpan seq_span(const SeqMap& m, int b) {
+  SeqSpan s;
+  s.q0 = b;
+  s.Lq = 1;
+  if (m.cu_q) {
+    const int a = m.cu_q[b], e = m.cu_q[b + 1];
+    s.q0 = a;
+    s.rows_ok = a >= 0 && a <= e && e <= m.Tq;
+    s.Lq = e - a;
+  } else {
+    s.rows_ok = true;
+  }
+  if (m.kv_len) {
+    s.k0 = 0;
+    s.Lk = m.kv_len[b];
+    s.ok = s.rows_ok && s.Lk >= 0 && s.Lk <= m.Tk;
+  } else {
+    const int a = m.cu_k[b], e = m.cu_k[b + 1];
+    s.k0 = a;
+    s.ok = s.rows_ok && a >= 0 && a <= e && e <= m.Tk;
+    s.Lk = e - a;
+  }
+  return s;
+}
+
+// Warp-wide 32-ary search: the number of indices i in [1, n] with f(i) true,
+// for f true up to some index and false after it (2 rounds of loads up to
+// n = 1023). Terminates with a value in [0, n] whatever f says.
+template <typename F>
+__device__ __forceinline__ int warp_count_true(int n, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + 31) >> 5;
+    const int probe = min((lane + 1) * step, n);
+    const int c = __popc(__ballot_sync(0xffffffffu, f(lo + probe)));
+    if (c == 32) return lo + n;
+    const int from = min(c * step, n), to = min((c + 1) * step, n);
+    lo += from;
+    n = max(to - from - 1, 0);
+  }
+  return lo;
+}
+
+// The sequence that owns packed row t, or -1 (whole warp).
+__device__ __forceinline__ int find_row_seq(const int32_t* cu, int B, int t) {
+  const int b = warp_count_true(B, [&](int i) { return cu[i] <= t; });
+  return b < B && cu[b] <= t && t < cu[b + 1] ? b : -1;
+}
+
+// Tiles of `tt` rows that start at each sequence's first row, in slots:
+// tile j of sequence b has slot cu[b] / tt + b + j. Slots are unique (a
+// sequence of n rows needs at most ceil(n / tt) of them and the + b leaves
+// room for its ragged end), so T / tt + B slots cover every tile and a slot's
+// tile is found by one search; some slots hold none. Returns the sequence
+// of slot `i` and its tile (b = -1: none). Whole warp.
+__device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, int i, int& tile) {
+  // largest b with cu[b] / tt + b <= i
+  const int b = warp_count_true(B, [&](int x) { return x < B && cu[x] / tt + x <= i; });
+  tile = i - (cu[b] / tt + b);
+  return tile >= 0 && tile < (cu[b + 1] - cu[b] + tt - 1) / tt ? b : -1;
+}
+
+// ---- launchers ---------------------------------------------------------------
+struct FullArgs {
+  const void *q, *k, *v;
+  SeqMap seq;
+  PageMap pages;
+  int Hq, Hkv, d, dtype;
+  float scale;
+  void* out;
+  float* lse;
+  void* ws;
+};
+struct FullBwdArgs {
+  FullArgs f;  // out: the forward's output (read)
+  const void* dout;
+  void *dq, *dk, *dv;
+};
+size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d, int dtype);
+size_t full_backward_ws_bytes(int Tq, int Hq, int dtype);
+// CUDA cores, any dtype
+cudaError_t launch_full_rows(const FullArgs& a, cudaStream_t stream);
+cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream);
+struct AppendArgs {
+  const void *q, *k_new, *v_new;
+  const float* rope;
+  const int32_t *cu_new, *kv_len;
+  PageMap pages;
+  int B, T, Hq, Hkv, d, rot, interleaved, max_pos, dtype;
+  void *q_out, *k_cache, *v_cache;
+  uint32_t* status;
+};
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream);
+
+}  // namespace msa

@@ -138,7 +138,7 @@ using namespace msa;
 
 extern "C" size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int Hq, int d, int di, int Bs, int K,
                                      int dtype) {
-  const bool rowless = op == MSA_OP_DECODE || op == MSA_OP_DECODE_STEP;  // Nq is ignored
+  const bool rowless = op == MSA_OP_DECODE || op == MSA_OP_DECODE_STEP || op == MSA_OP_FULL_DECODE;  // Nq is ignored
   if (empty_batch(B, rowless ? 1 : Nq)) {
     // only the status header, if the call is valid for one row
     const size_t one = msa_workspace_size(op, 1, 1, one_key_min(Nk), G, Hq, d, di, Bs, K, dtype);
@@ -172,6 +172,11 @@ extern "C" size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int H
       if (!attn_backward_supported(dtype, Hq, G, d, Bs, K)) return 0;
       return attn_backward_ws_bytes(B, Nq, Nk, Hq, G, d, Bs, K);
     }
+    case MSA_OP_FULL_PREFILL:
+    case MSA_OP_FULL_BACKWARD:
+    case MSA_OP_FULL_DECODE:
+    case MSA_OP_PAGED_APPEND:
+      return full_ws_bytes(op, B, Nq, Nk, G, Hq, d, dtype);
     default:
       return 0;
   }

@@ -145,6 +145,9 @@ cudaError_t invert_chunk(const int32_t* sel, const int32_t* q_offset, const int3
 // points that select: the other arguments are checked as for one row.
 msa_status_t index_select_empty_status(int Nk, int G, int di, int Bs, int K, int dtype);
 
+// Workspace of a full-attention or paged-cache operation (full_api.cu); 0: not supported.
+size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype);
+
 // ---- launchers (host) ------------------------------------------------------
 // Index Branch, CUDA-core table path: block maxima for every visible block.
 cudaError_t launch_index_blockmax_table(int dtype, const void* iq, const void* ik, const int32_t* q_offset,

@@ -1,0 +1,139 @@
+// Appends new tokens' keys and values to a paged cache and rotates keys and
+// queries by their positions on the way:
+//   (x, y) -> (x cos - y sin, y cos + x sin) on the pairs of the first `rot`
+// dims, fp32 inside, rounded once.
+//
+// Streaming work, bound by HBM (or, for a step of single tokens, by launch
+// latency): one CTA per token; a thread's unit is one 16-byte chunk of a head
+// row and, for split pairs, the chunk rot / 2 dims further, so both elements
+// of every pair are in one thread's registers and q may be rotated in place.
+#include "full_internal.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kAppThreads = 128;
+
+template <typename T>
+struct Chunk {
+  static constexpr int N = 16 / sizeof(T);  // elements of a 16-byte chunk
+  float x[N];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f(e[i]);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    uint4 raw;
+    T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = from_f<T>(x[i]);
+    *reinterpret_cast<uint4*>(p) = raw;
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendArgs a) {
+  constexpr int N = Chunk<T>::N;
+  const int t = blockIdx.x;
+  // every warp finds the token's sequence itself: no barrier
+  const int b = a.cu_new ? find_row_seq(a.cu_new, a.B, t) : t;
+  if (b < 0) return;
+  const int last = a.cu_new ? a.cu_new[b + 1] : t + 1;
+  const int64_t pos = int64_t(a.kv_len[b]) - (last - t);
+  const int psz = 1 << a.pages.page_log2;
+  int64_t row = -1;
+  if (pos >= 0 && last <= a.T && pos < (int64_t(a.pages.max_pages) << a.pages.page_log2) &&
+      (a.rot == 0 || pos < a.max_pos)) {
+    const int page = a.pages.table[int64_t(b) * a.pages.max_pages + (pos >> a.pages.page_log2)];
+    if (page >= 0 && page < a.pages.num_pages) row = int64_t(page) * psz + (pos & (psz - 1));
+  }
+  if (row < 0 && threadIdx.x == 0) set_status(a.status, MSA_ERR_BOUNDS);
+  const int qh = a.q ? a.Hq : 0;
+  if (row < 0 && !a.q) return;
+  // units of a head row: rot / 2 / N pair units (two chunks each; adjacent
+  // chunks if interleaved), then the unrotated chunks
+  const int half = a.rot / 2, pu = half / N, units = pu + (a.d - a.rot) / N, chunks = a.d / N;
+  const int qk = (qh + a.Hkv) * units, total = qk + a.Hkv * chunks;
+  const float* cs = a.rope ? a.rope + pos * a.rot : nullptr;
+  for (int u = threadIdx.x; u < total; u += kAppThreads) {
+    if (u >= qk) {  // values: copied
+      if (row < 0) continue;
+      const int h = (u - qk) / chunks, c = (u - qk) % chunks;
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.v_cache) + (row * a.Hkv + h) * a.d + c * N) =
+          *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_new) + (int64_t(t) * a.Hkv + h) * a.d + c * N);
+      continue;
+    }
+    const int hh = u / units, w = u % units;
+    const bool is_q = hh < qh;
+    const int h = is_q ? hh : hh - qh;
+    const T* src = is_q ? static_cast<const T*>(a.q) + (int64_t(t) * a.Hq + h) * a.d
+                        : static_cast<const T*>(a.k_new) + (int64_t(t) * a.Hkv + h) * a.d;
+    T* dst = is_q ? static_cast<T*>(a.q_out) + (int64_t(t) * a.Hq + h) * a.d
+                  : static_cast<T*>(a.k_cache) + (row * a.Hkv + h) * a.d;
+    if (row < 0) {
+      if (!is_q) continue;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      if (w < pu) {
+        *reinterpret_cast<uint4*>(dst + (a.interleaved ? 2 * w * N : w * N)) = z;
+        *reinterpret_cast<uint4*>(dst + (a.interleaved ? 2 * w * N + N : half + w * N)) = z;
+      } else {
+        *reinterpret_cast<uint4*>(dst + a.rot + (w - pu) * N) = z;
+      }
+      continue;
+    }
+    if (w >= pu) {  // past the rotated dims
+      const int o = a.rot + (w - pu) * N;
+      *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(src + o);
+      continue;
+    }
+    const int o0 = a.interleaved ? 2 * w * N : w * N, o1 = a.interleaved ? o0 + N : half + o0;
+    Chunk<T> c0, c1;
+    c0.load(src + o0);
+    c1.load(src + o1);
+    const float4* r4 = reinterpret_cast<const float4*>(cs + 2 * w * N);  // N (cos, sin) pairs
+    float cc[N], ss[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float4 f = __ldg(r4 + i);
+      cc[2 * i] = f.x;
+      ss[2 * i] = f.y;
+      cc[2 * i + 1] = f.z;
+      ss[2 * i + 1] = f.w;
+    }
+    if (a.interleaved) {  // pairs (2i, 2i + 1) of the two adjacent chunks
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float x = c0.x[2 * i], y = c0.x[2 * i + 1];
+        c0.x[2 * i] = x * cc[i] - y * ss[i];
+        c0.x[2 * i + 1] = y * cc[i] + x * ss[i];
+        const float z = c1.x[2 * i], w1 = c1.x[2 * i + 1];
+        c1.x[2 * i] = z * cc[N / 2 + i] - w1 * ss[N / 2 + i];
+        c1.x[2 * i + 1] = w1 * cc[N / 2 + i] + z * ss[N / 2 + i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x = c0.x[i], y = c1.x[i];
+        c0.x[i] = x * cc[i] - y * ss[i];
+        c1.x[i] = y * cc[i] + x * ss[i];
+      }
+    }
+    c0.store(dst + o0);
+    c1.store(dst + o1);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
+  ProfScope pf("paged_append", stream);
+  if (a.dtype == MSA_BF16)
+    paged_append_kernel<__nv_bfloat16><<<a.T, kAppThreads, 0, stream>>>(a);
+  else
+    paged_append_kernel<float><<<a.T, kAppThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

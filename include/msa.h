@@ -81,7 +81,11 @@ typedef enum {
   MSA_OP_DECODE = 2,
   MSA_OP_DECODE_STEP = 3,
   MSA_OP_KL_AUX = 4,
-  MSA_OP_BACKWARD = 5
+  MSA_OP_BACKWARD = 5,
+  MSA_OP_FULL_PREFILL = 8, /* msa_full_attn_prefill and _paged (6 and 7 name no operation) */
+  MSA_OP_FULL_BACKWARD = 9,
+  MSA_OP_FULL_DECODE = 10,
+  MSA_OP_PAGED_APPEND = 11
 } msa_op_t;
 
 /* Bytes of scratch `ws` the entry point `op` needs for these sizes (the same
@@ -89,8 +93,10 @@ typedef enum {
  * the attention ops, Hq and d for MSA_OP_INDEX_SELECT; for MSA_OP_DECODE and
  * MSA_OP_DECODE_STEP, Nq is ignored and Nk is Lmax; MSA_OP_DECODE_STEP and
  * MSA_OP_KL_AUX use every other argument, with G = Hkv; MSA_OP_BACKWARD uses
- * all but di, with G = Hkv). Returns 0 when the arguments are invalid or not
- * supported, and 256 for a valid empty batch. */
+ * all but di, with G = Hkv; the MSA_OP_FULL_* operations and
+ * MSA_OP_PAGED_APPEND use B, Nq = packed rows Tq (T), Nk = packed keys Tk or
+ * max_pages * page_size, G = Hkv, Hq, d and dtype). Returns 0 when the
+ * arguments are invalid or not supported, and 256 for a valid empty batch. */
 size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int Hq, int d, int di, int Bs, int K, int dtype);
 
 /* Index Branch: block selection for every (query row, group).
@@ -284,6 +290,111 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
                                       const int32_t* kv_len, int B, int Nq, int Nk, int Hq, int Hkv, int d, int Bs,
                                       int K, float scale, int dtype, void* dq, void* dk, void* dv, void* ws,
                                       size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Full (dense causal) attention over packed sequences and paged caches ---
+ * The Main Branch without a selection: what MSA's layers are continued from
+ * and stand next to (hyper.ai summary of paper 2606.13392, "方法": MSA is
+ * layered on grouped-query attention; "实验": MSA-CPT starts from a full
+ * attention checkpoint, against which it is compared).
+ *
+ * Notation of this section, besides that at the top:
+ *  Packed rows   the rows of all sequences back to back, without padding.
+ *                cu [B + 1] int32: sequence b owns rows [cu[b], cu[b+1]).
+ *                Need 0 <= cu[b] <= cu[b+1] <= the row count (T, Tq or Tk);
+ *                a sequence may be empty. Rows before cu[0] and from cu[B] on
+ *                belong to no sequence: they are never read as data and stay
+ *                as they were in every output.
+ *  Paged cache   k_cache, v_cache [num_pages, page_size, Hkv, d]; key j of
+ *                sequence b is row j % page_size of page
+ *                page_table[b][j / page_size], page_table [B, max_pages]
+ *                int32. Entries past a sequence's last page are not read, and
+ *                rows of a page past kv_len[b] never reach a result, whatever
+ *                they hold. page_size is 16, 32, 64 or 128. Two sequences may
+ *                share pages that are only read.
+ *  Visibility    query row i of Lq sees keys j <= Lk - Lq + i of Lk: the last
+ *                row sees every key. If Lq > Lk the first Lq - Lk rows see
+ *                none: their output and gradient are 0 and their lse -inf.
+ * Supported by all: d in {64, 128}; Hq / Hkv an integer up to 64; BF16 (tensor
+ * cores, fp32 accumulation) or FP32 (CUDA cores).
+ * Device-side checks: a sequence whose cu, kv_len or page entry is out of
+ * range sets MSA_ERR_BOUNDS in the workspace status and nothing out of range is
+ * read or written for it. If its rows are known (its cu is in range) its
+ * output rows are 0 and their lse -inf; otherwise they stay as they were. */
+
+/* Appends the keys and values of T packed new tokens to a paged cache, with
+ * the position rotation applied on the way to keys and queries.
+ * (quant_prune_distill post 751, "Метод", and hyper.ai summary, "一句话总结":
+ *  the decode side, where every new token joins the cache before it attends.)
+ * Token i of sequence b's n = cu_new[b+1] - cu_new[b] new tokens takes position
+ * pos = kv_len[b] - n + i. Pair p of the first `rot` dims of a head, (x, y),
+ * becomes (x cos - y sin, y cos + x sin) with rope[pos][p]; the other dims are
+ * copied. The pairs are (p, p + rot/2), or (2p, 2p + 1) if `interleaved`.
+ *
+ *  q        [T, Hq, d] or NULL (then q_out must be NULL); k_new, v_new [T, Hkv, d]
+ *  rope     [max_pos, rot/2, 2] fp32: cos, sin of each position and pair. NULL
+ *           with rot = 0: nothing is rotated
+ *  cu_new   [B + 1] int32, or NULL for one token per sequence (T == B)
+ *  kv_len   [B] int32: lengths with the new tokens counted; not changed
+ *  page_table, k_cache, v_cache: the paged cache, written at the new positions
+ *  q_out    [T, Hq, d], out: the rotated queries (q_out == q is allowed)
+ *  Supported: 0 <= rot <= d, a multiple of 16. The rotation is in fp32, rounded
+ *  once; pointers to rows are 16-byte aligned. A token whose position is
+ *  negative, not below max_pos or past the table, or whose page is out of
+ *  range, sets MSA_ERR_BOUNDS and is skipped (its q_out row is 0). No two
+ *  tokens of a call may map to one cache row. */
+msa_status_t msa_paged_append(const void* q, const void* k_new, const void* v_new, const float* rope,
+                              const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table, int B, int T,
+                              int Hq, int Hkv, int d, int rot, int interleaved, int max_pos, int num_pages,
+                              int page_size, int max_pages, int dtype, void* q_out, void* k_cache, void* v_cache,
+                              void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Decode: one query row per sequence over the whole of its paged cache.
+ *  q [B, Hq, d]; kv_len [B] int32, 0 <= kv_len[b] <= max_pages * page_size; a
+ *  sequence of length 0 (a padded batch entry) gives out 0 and lse -inf
+ *  out [B, Hq, d] (dtype); lse [B, Hq] fp32 or NULL
+ *  ws: msa_workspace_size(MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv,
+ *  Hq, d, 0, 0, 0, dtype) (the size does not depend on the lengths)
+ *  Deterministic: partial sums are joined in the order of the keys. */
+msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                  const int32_t* kv_len, int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                  int max_pages, float scale, int dtype, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/* Prefill: causal attention of packed query rows over packed keys.
+ *  q [Tq, Hq, d]; k, v [Tk, Hkv, d]; cu_q, cu_k [B + 1] int32
+ *  scale  softmax scale; <= 0 selects 1/sqrt(d)
+ *  out [Tq, Hq, d] (dtype); lse [Tq, Hq] fp32 or NULL (as msa_sparse_attn_prefill)
+ *  Deterministic. BF16 rounds each key's weight exp(s - m) to bf16 before its
+ *  product with v; the weights' sum takes it unrounded. Key and value rows of
+ *  one sequence are multiplied by weight 0 where they lie behind a query, so
+ *  an infinity or NaN in a sequence's own values can reach its earlier rows. */
+msa_status_t msa_full_attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,
+                                   const int32_t* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int d, float scale,
+                                   int dtype, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The same with the keys of each sequence in a paged cache: kv_len[b] keys, the
+ * last of which are the query rows' own (msa_paged_append first). Serves whole
+ * prompts, chunks of prompts behind a cached prefix, and single tokens. */
+msa_status_t msa_full_attn_prefill_paged(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len, int B,
+                                         int Tq, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                                         float scale, int dtype, void* out, float* lse, void* ws, size_t ws_bytes,
+                                         cudaStream_t stream);
+
+/* Gradients of msa_full_attn_prefill (formulas at msa_sparse_attn_backward).
+ *  q, out, dout [Tq, Hq, d]; k, v [Tk, Hkv, d]; lse [Tq, Hq] fp32 (required);
+ *  cu_q, cu_k, scale as in the forward
+ *  dq [Tq, Hq, d]; dk, dv [Tk, Hkv, d] (dtype), out: fp32 accumulation, rounded
+ *  once. Keys of a sequence without query rows get 0.
+ *  ws: msa_workspace_size(MSA_OP_FULL_BACKWARD, B, Tq, Tk, Hkv, Hq, d, 0, 0, 0,
+ *  dtype)
+ *  Deterministic: no atomics, every sum in a fixed order. BF16 rounds P and dS
+ *  to bf16 before the products that read them. Tq == 0 with Tk > 0 writes dk
+ *  and dv only; the query-row pointers may then be NULL. */
+msa_status_t msa_full_attn_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                                    const float* lse, const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk,
+                                    int Hq, int Hkv, int d, float scale, int dtype, void* dq, void* dk, void* dv,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Synchronises `stream`, returns the sticky device status of workspace `ws`
  * (MSA_OK, MSA_ERR_TIMEOUT or MSA_ERR_BOUNDS) and clears it. Returns
