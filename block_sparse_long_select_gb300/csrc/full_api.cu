@@ -23,7 +23,9 @@ bool rows_ok(int64_t rows, int heads) { return rows * heads < (int64_t(1) << 31)
 msa_status_t check_pages(int num_pages, int page_size, int max_pages, PageMap* pm) {
   if (num_pages < 1 || max_pages < 1 || page_size < 1) return MSA_ERR_INVALID_ARG;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return MSA_ERR_UNSUPPORTED;
-  if (int64_t(max_pages) * page_size >= (int64_t(1) << 31)) return MSA_ERR_UNSUPPORTED;
+  // key positions and cache rows are 32-bit (TMA coordinates)
+  if (int64_t(max_pages) * page_size >= (int64_t(1) << 31) || int64_t(num_pages) * page_size >= (int64_t(1) << 31))
+    return MSA_ERR_UNSUPPORTED;
   pm->num_pages = num_pages;
   pm->max_pages = max_pages;
   pm->page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
@@ -38,6 +40,12 @@ msa_status_t check_full_ws(void* ws, size_t ws_bytes, size_t need) {
 }
 
 inline msa_status_t launched(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
+// Prefill: tensor cores for bf16. With no key at all (Tk == 0) there is
+// nothing to map for TMA, and the row kernel writes the empty rows.
+cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
+  return a.dtype == MSA_BF16 && a.seq.Tk > 0 ? launch_full_prefill_tc(a, stream) : launch_full_rows(a, stream);
+}
+
 inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale : 1.0f / sqrtf(float(d)); }
 
 }  // namespace
@@ -156,7 +164,7 @@ extern "C" msa_status_t msa_full_attn_prefill(const void* q, const void* k, cons
   a.out = out;
   a.lse = lse;
   a.ws = ws;
-  return launched(launch_full_rows(a, stream));
+  return launched(prefill(a, stream));
 }
 
 extern "C" msa_status_t msa_full_attn_prefill_paged(const void* q, const void* k_cache, const void* v_cache,
@@ -189,7 +197,7 @@ extern "C" msa_status_t msa_full_attn_prefill_paged(const void* q, const void* k
   a.out = out;
   a.lse = lse;
   a.ws = ws;
-  return launched(launch_full_rows(a, stream));
+  return launched(prefill(a, stream));
 }
 
 extern "C" msa_status_t msa_full_attn_backward(const void* q, const void* k, const void* v, const void* out,

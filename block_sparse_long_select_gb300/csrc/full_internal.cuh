@@ -111,6 +111,8 @@ size_t full_backward_ws_bytes(int Tq, int Hq, int dtype);
 // CUDA cores, any dtype
 cudaError_t launch_full_rows(const FullArgs& a, cudaStream_t stream);
 cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream);
+// tcgen05 prefill (bf16); needs Tk > 0
+cudaError_t launch_full_prefill_tc(const FullArgs& a, cudaStream_t stream);
 struct AppendArgs {
   const void *q, *k_new, *v_new;
   const float* rope;
