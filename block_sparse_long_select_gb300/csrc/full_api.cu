@@ -52,7 +52,7 @@ inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale :
 
 size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
-  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader : 0;
+  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(B, Hq, Hkv, d) : 0;
   if (Nq < 0 || !rows_ok(Nq, Hq) || !rows_ok(op == MSA_OP_PAGED_APPEND ? Nq : Nk, Hkv)) return 0;
   return kWsHeader;
 }
@@ -135,7 +135,7 @@ extern "C" msa_status_t msa_full_attn_decode(const void* q, const void* k_cache,
   a.out = out;
   a.lse = lse;
   a.ws = ws;
-  return launched(launch_full_rows(a, stream));
+  return launched(launch_full_decode(a, stream));
 }
 
 extern "C" msa_status_t msa_full_attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,

@@ -1,0 +1,694 @@
+// Full attention, decode: one query row per sequence over the whole of its
+// paged cache, all heads of a group per pass over its keys.
+//
+//   out = sum_j exp(s_j - lse) v_j,  s_j = scale q . k_j,  j < kv_len
+//
+// Bound: HBM (every key and value is read once; 4 hpg FLOPs per element).
+//
+// Work: the keys of every (sequence, key/value head, group of up to 16 query
+// heads) -- an item -- are cut into units of 64, the units of all items are
+// numbered through, and each CTA of a fixed grid takes an equal run of them,
+// so ragged lengths balance whatever they are, without the host knowing them.
+// In a unit each warp takes 16 keys, which lie in one page, and works alone:
+// its own ring of cp.async copies (keys past the end arrive as zeros), scores,
+// running maximum and sum, products. Warps meet only where an item ends in the
+// CTA: their states are joined in shared memory. An item that lies in several
+// CTAs leaves a partial (maximum, sum, unnormalised output) per CTA, and the
+// CTA that arrives last joins them in the order of the keys.
+//
+// bf16: mma.sync m16n8k16 with keys (then head dims) along M and the heads
+// along N = 8: the tensor work is a fraction of the time the bytes take, so
+// tcgen05's larger tiles would only pad. fp32: FMAs, one key per lane pair for
+// the scores, four head dims per lane for the products.
+#include "full_internal.cuh"
+#include "tc_utils.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kFdWarps = 4, kFdThreads = kFdWarps * 32;
+constexpr int kSub = 16;                  // keys of a warp's step: never across a page
+constexpr int kUnit = kFdWarps * kSub;    // keys of a unit
+constexpr int kFdMaxHeads = 16;           // query heads of an item
+constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
+// The maximum only moves when a step exceeds it by 2^8: weights stay below
+// 2^8 and their common factor drops out in the division by their sum.
+constexpr float kFdLazy = 8.f;
+
+__device__ __forceinline__ float ex2d(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8x8 b16 matrix across the warp, transposed
+__device__ __forceinline__ uint32_t trans8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float qmax(float x) {  // over the 8 lanes that share lane & 3
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float qsum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Address of 16-byte chunk c of row r in a [rows][row_bytes] tile whose chunks
+// are exchanged within 128 bytes by the row's low bits (conflict-free ldmatrix
+// and vector reads down a column).
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row_bytes, int r, int c) {
+  return base + uint32_t(r * row_bytes) + (uint32_t(c ^ (r & 7)) << 4);
+}
+
+// ---- a warp's state: bf16 ------------------------------------------------------
+// O^T (head dims along M) and the scores share the column = head layout: lane
+// (gq = lane / 4, tq = lane % 4) holds heads 2 tq and 2 tq + 1 of each tile of 8.
+template <typename T, int D, int HN>
+struct Core;
+
+template <int D, int HN>
+struct Core<__nv_bfloat16, D, HN> {
+  using T = __nv_bfloat16;
+  static constexpr int kRow = D * 2, kTile = kSub * kRow, kStage = 2 * kTile, kExtra = 0;
+  static constexpr int kM = 2 * HN, kAcc = HN * D / 4;
+  uint32_t qf[HN][D / 16][2];
+  float m[kM], l[kM], acc[kAcc];  // acc[(t * D / 16 + mt) * 4 + e]
+
+  __device__ __forceinline__ void start(const T* q, int heads, uint32_t) {
+    const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+#pragma unroll
+    for (int t = 0; t < HN; ++t) {
+      const T* qh = q + (t * 8 + gq) * D;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          qf[t][ks][x] = t * 8 + gq < heads ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 2 * tq + 8 * x) : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < kM; ++x) m[x] = -INFINITY, l[x] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
+  }
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t, int valid, float scale_log2) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2;
+    const uint32_t vt = kt + kTile;
+    float s[HN][4];
+#pragma unroll
+    for (int t = 0; t < HN; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4];
+      ldm4(chunk_at(kt, kRow, (lane & 7) + 8 * ((lane >> 3) & 1), ks * 2 + (lane >> 4)), a);
+#pragma unroll
+      for (int t = 0; t < HN; ++t) mma16816(s[t], a, qf[t][ks][0], qf[t][ks][1]);
+    }
+    float mt[kM];
+    bool up = false;
+#pragma unroll
+    for (int t = 0; t < HN; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = gq + 8 * (e >> 1) < valid ? s[t][e] * scale_log2 : -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mt[2 * t + x] = qmax(fmaxf(s[t][x], s[t][2 + x]));
+        up |= mt[2 * t + x] > m[2 * t + x] + kFdLazy || (m[2 * t + x] == -INFINITY && mt[2 * t + x] > -INFINITY);
+      }
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int t = 0; t < HN; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * t + x;
+          const float mn = fmaxf(m[i], mt[i]);
+          const float a = mn == m[i] ? 1.f : ex2d(m[i] - mn);
+          m[i] = mn;
+          l[i] *= a;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            acc[(t * (D / 16) + k) * 4 + x] *= a;
+            acc[(t * (D / 16) + k) * 4 + 2 + x] *= a;
+          }
+        }
+    }
+    uint32_t b[HN][2];
+#pragma unroll
+    for (int t = 0; t < HN; ++t) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float mm = m[2 * t + (e & 1)];
+        p[e] = ex2d(s[t][e] - (mm == -INFINITY ? 0.f : mm));
+        l[2 * t + (e & 1)] += p[e];  // unrounded; the product below takes bf16 weights
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(p[0], p[1]), hi = __floats2bfloat162_rn(p[2], p[3]);
+      b[t][0] = trans8(reinterpret_cast<const uint32_t&>(lo));
+      b[t][1] = trans8(reinterpret_cast<const uint32_t&>(hi));
+    }
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t a[4];
+      const int mi = lane >> 3;
+      ldm4t(chunk_at(vt, kRow, (lane & 7) + 8 * (mi >> 1), k * 2 + (mi & 1)), a);
+#pragma unroll
+      for (int t = 0; t < HN; ++t) {
+        float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[(t * (D / 16) + k) * 4]);
+        mma16816(c, a, b[t][0], b[t][1]);
+      }
+    }
+  }
+  // f(head, index of its maximum, dim, value) for all that this lane holds
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+#pragma unroll
+    for (int t = 0; t < HN; ++t)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f(t * 8 + 2 * tq + (e & 1), 2 * t + (e & 1), k * 16 + gq + 8 * (e >> 1), acc[(t * (D / 16) + k) * 4 + e]);
+  }
+  __device__ __forceinline__ void sum_l() {
+#pragma unroll
+    for (int x = 0; x < kM; ++x) l[x] = qsum(l[x]);
+  }
+  // f(head, index): the heads whose maximum and sum this lane reports
+  template <typename F>
+  __device__ __forceinline__ void each_head(F f) const {
+    const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+    if (gq == 0) {
+#pragma unroll
+      for (int x = 0; x < kM; ++x) f((x >> 1) * 8 + 2 * tq + (x & 1), x);
+    }
+  }
+  __device__ __forceinline__ static int m_index(int x) { return 2 * (x / (D / 4)) + (x & 1); }  // acc[x]'s head
+};
+
+// ---- a warp's state: fp32 ------------------------------------------------------
+// Scores: lane pair (lane, lane ^ 16) shares key lane & 15, half the dims each.
+// Products: lane holds D / 32 dims of every head. Maxima are equal in all lanes.
+template <int D, int HN>
+struct Core<float, D, HN> {
+  using T = float;
+  static constexpr int H = 8 * HN, P = D / 32;
+  static constexpr int kRow = D * 4, kTile = kSub * kRow, kStage = 2 * kTile;
+  static constexpr int kExtra = (H * D + kSub * H) * 4;  // per warp: queries, weights
+  static constexpr int kM = H, kAcc = H * P;
+  float m[kM], l[kM], acc[kAcc];  // acc[h * P + x]
+
+  __device__ __forceinline__ void start(const T* q, int heads, uint32_t extra) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    for (int x = lane; x < H * D; x += 32) {
+      const float v = x / D < heads ? q[x] : 0.f;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(extra + x * 4), "f"(v) : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < kM; ++x) m[x] = -INFINITY, l[x] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
+  }
+  __device__ __forceinline__ static float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+  }
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t extra, int valid, float scale_log2) {
+    const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
+    const uint32_t vt = kt + kTile, ps = extra + H * D * 4;
+    float s[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) s[h] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const int ch = half * (D / 8) + c;
+      const float4 k4 = lds4(chunk_at(kt, kRow, key, ch));
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float4 q4 = lds4(extra + (h * D + ch * 4) * 4);
+        s[h] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[h]))));
+      }
+    }
+    bool up = false;
+    float mt[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+      s[h] = key < valid ? s[h] * scale_log2 : -INFINITY;
+      mt[h] = tc::warp_max_f32(s[h]);
+      up |= mt[h] > m[h] + kFdLazy || (m[h] == -INFINITY && mt[h] > -INFINITY);
+    }
+    if (up) {  // equal in all lanes
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float mn = fmaxf(m[h], mt[h]);
+        const float a = mn == m[h] ? 1.f : ex2d(m[h] - mn);
+        m[h] = mn;
+        l[h] *= a;
+#pragma unroll
+        for (int x = 0; x < P; ++x) acc[h * P + x] *= a;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const float p = ex2d(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+      if (half == 0) {
+        l[h] += p;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(ps + (key * H + h) * 4), "f"(p) : "memory");
+      }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < kSub; ++j) {
+      float v[P];
+      if constexpr (P == 4) {
+        const float4 v4 = lds4(chunk_at(vt, kRow, j, lane));
+        v[0] = v4.x, v[1] = v4.y, v[2] = v4.z, v[3] = v4.w;
+      } else {
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(v[0]), "=f"(v[1])
+                     : "r"(chunk_at(vt, kRow, j, lane >> 1) + (lane & 1) * 8));
+      }
+#pragma unroll
+      for (int h4 = 0; h4 < H / 4; ++h4) {
+        const float4 p4 = lds4(ps + (j * H + h4 * 4) * 4);
+        const float pp[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int x = 0; x < P; ++x) acc[(h4 * 4 + y) * P + x] = fmaf(pp[y], v[x], acc[(h4 * 4 + y) * P + x]);
+      }
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int x = 0; x < P; ++x) f(h, h, lane * P + x, acc[h * P + x]);
+  }
+  __device__ __forceinline__ void sum_l() {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+  }
+  template <typename F>
+  __device__ __forceinline__ void each_head(F f) const {
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) f(h, h);
+    }
+  }
+  __device__ __forceinline__ static int m_index(int x) { return x / P; }
+};
+
+struct FdParams {
+  const void *q, *k, *v;
+  const int32_t* kv_len;
+  PageMap pages;
+  int B, Hq, Hkv, hpg, ngr, cap;  // ngr: head groups (items) per key/value head; cap: most keys
+  float scale_log2;
+  float* part_o;   // [2 * grid][16][D]
+  float* part_ml;  // [2 * grid][16][2]: maximum (log2 units), sum; a negative sum marks a page out of range
+  int* arrivals;   // [B * Hkv * ngr], zero between calls
+  void* out;
+  float* lse;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ int units_of(const FdParams& p, int b) {
+  const int L = p.kv_len[b];
+  return L > 0 && L <= p.cap ? (L + kUnit - 1) / kUnit : 0;
+}
+
+// A walk over a CTA's run of units in order.
+struct Walk {
+  int b, it, u, n;  // sequence, item within it, unit within the item, units of the item
+  __device__ __forceinline__ void next(const FdParams& p) {
+    if (++u < n) return;
+    u = 0;
+    if (++it < p.Hkv * p.ngr) return;
+    it = 0;
+    do {
+      n = ++b < p.B ? units_of(p, b) : 1;  // past the last sequence the walk is over
+    } while (n == 0);
+  }
+};
+
+template <typename T, int D, int HN>
+struct FdShape {
+  using C = Core<T, D, HN>;
+  static constexpr int kStages = sizeof(T) == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);
+  static constexpr int kRing = kStages * C::kStage;                       // per warp
+  static constexpr int kJoin = 3 * (C::kAcc + 2 * C::kM + 1) * 32 * 4;   // three warps' states
+  static constexpr int kBytes = kFdWarps * (kRing + C::kExtra) + kJoin;
+};
+
+template <typename T, int D, int HN>
+__global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1) full_decode_kernel(const FdParams p) {
+  using SH = FdShape<T, D, HN>;
+  using C = typename SH::C;
+  constexpr int NS = SH::kStages;
+  constexpr int kCpr = D * int(sizeof(T)) / 16;  // 16-byte chunks of a row
+  extern __shared__ __align__(128) uint8_t fd_smem[];
+  __shared__ int last_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = tc::smem_u32(fd_smem) + warp * SH::kRing;
+  const uint32_t extra = tc::smem_u32(fd_smem) + kFdWarps * SH::kRing + warp * C::kExtra;
+  float* join = reinterpret_cast<float*>(fd_smem + kFdWarps * (SH::kRing + C::kExtra));
+  const int items = p.Hkv * p.ngr;
+  T* out = static_cast<T*>(p.out);
+
+  // ---- this CTA's run of units (every warp finds it alone) ----
+  int64_t total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int x = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
+    int64_t y = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    total += y;
+  }
+  total *= items;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t run0 = blockIdx.x * per, run1 = min(run0 + per, total);
+  // sequences without keys: nobody's run holds them
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (units_of(p, b) > 0) continue;
+    if (threadIdx.x == 0 && (p.kv_len[b] < 0 || p.kv_len[b] > p.cap)) set_status(p.status, MSA_ERR_BOUNDS);
+    for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
+    if (p.lse)
+      for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
+  }
+  if (run0 >= run1) return;
+  Walk at{};
+  int64_t first = 0;  // number of the walk's sequence's first unit
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int mine = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
+    int64_t incl = int64_t(mine) * items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      at.b = b0 + src;
+      at.n = __shfl_sync(0xffffffffu, mine, src);
+      first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
+      break;
+    }
+    first += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  at.it = int((run0 - first) / at.n);
+  at.u = int((run0 - first) % at.n);
+  int64_t item_first = first + int64_t(at.it) * at.n;  // number of the item's first unit
+
+  // ---- copies: the walk `ld` runs ahead of `at` ----
+  Walk ld = at;
+  int64_t ld_left = run1 - run0;
+  uint32_t bad_ring = 0;  // stage x's page was out of range
+  auto page_of = [&](const Walk& w) {
+    const int key = w.u * kUnit + warp * kSub;
+    return key < p.kv_len[w.b] ? p.pages.table[int64_t(w.b) * p.pages.max_pages + (key >> p.pages.page_log2)] : 0;
+  };
+  int page = page_of(ld);
+  auto issue = [&](int st) {
+    if (ld_left > 0) {
+      const int L = p.kv_len[ld.b], key = ld.u * kUnit + warp * kSub;
+      const int valid = L - key;
+      const bool bad = valid > 0 && (page < 0 || page >= p.pages.num_pages);
+      bad_ring = bad ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
+      const int g = ld.it / p.ngr;
+      const int64_t row0 = bad || valid <= 0 ? 0
+                                             : (int64_t(page) << p.pages.page_log2) +
+                                                   (key & ((1 << p.pages.page_log2) - 1));
+      const T* kp = static_cast<const T*>(p.k) + (row0 * p.Hkv + g) * D;
+      const T* vp = static_cast<const T*>(p.v) + (row0 * p.Hkv + g) * D;
+      const uint32_t dst = ring + st * C::kStage;
+#pragma unroll
+      for (int x = lane; x < kSub * kCpr; x += 32) {
+        const int r = x / kCpr, c = x % kCpr;
+        const bool in = r < valid && !bad;
+        const int64_t off = in ? int64_t(r) * p.Hkv * D + c * (16 / int(sizeof(T))) : 0;
+        cp16z(chunk_at(dst, C::kRow, r, c), kp + off, in);
+      }
+#pragma unroll
+      for (int x = lane; x < kSub * kCpr; x += 32) {
+        const int r = x / kCpr, c = x % kCpr;
+        const bool in = r < valid && !bad;
+        const int64_t off = in ? int64_t(r) * p.Hkv * D + c * (16 / int(sizeof(T))) : 0;
+        cp16z(chunk_at(dst + C::kTile, C::kRow, r, c), vp + off, in);
+      }
+      if (--ld_left > 0) {
+        ld.next(p);
+        page = page_of(ld);
+      }
+    }
+    cp_commit_group();
+  };
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(st);
+
+  C c;
+  bool fresh = true, bad = false;
+  int st = 0;
+  for (int64_t z = run0; z < run1; ++z) {
+    const int g = at.it / p.ngr, h0 = g * p.hpg + (at.it % p.ngr) * kFdMaxHeads;
+    const int heads = min(p.hpg - (at.it % p.ngr) * kFdMaxHeads, kFdMaxHeads);
+    const int L = p.kv_len[at.b];
+    if (fresh) {
+      c.start(static_cast<const T*>(p.q) + (int64_t(at.b) * p.Hq + h0) * D, heads, extra);
+      fresh = bad = false;
+    }
+    issue((st + NS - 1) % NS);
+    cp_wait<NS - 1>();
+    __syncwarp();
+    bad |= (bad_ring >> st) & 1u;
+    const int valid = L - (at.u * kUnit + warp * kSub);
+    if (valid > 0) c.step(ring + st * C::kStage, extra, valid, p.scale_log2);
+    __syncwarp();
+    st = (st + 1) % NS;
+    const int b = at.b, item = b * items + at.it, n = at.n;
+    const bool ends = at.u + 1 == at.n;
+    if (!ends && z + 1 < run1) {
+      ++at.u;
+      continue;
+    }
+    // ---- the item ends here: join the four warps' states (4 -> 2 -> 1) ----
+    fresh = true;
+    constexpr int kRegs = C::kAcc + 2 * C::kM + 1;
+    auto put = [&](float* to) {
+#pragma unroll
+      for (int x = 0; x < C::kAcc; ++x) to[x * 32 + lane] = c.acc[x];
+#pragma unroll
+      for (int x = 0; x < C::kM; ++x) {
+        to[(C::kAcc + x) * 32 + lane] = c.m[x];
+        to[(C::kAcc + C::kM + x) * 32 + lane] = c.l[x];
+      }
+      to[(kRegs - 1) * 32 + lane] = bad ? 1.f : 0.f;
+    };
+    auto take = [&](const float* from) {
+      float wa[C::kM], wb[C::kM];
+#pragma unroll
+      for (int x = 0; x < C::kM; ++x) {
+        const float mo = from[(C::kAcc + x) * 32 + lane], mn = fmaxf(c.m[x], mo);
+        wa[x] = c.m[x] == mn ? 1.f : ex2d(c.m[x] - mn);
+        wb[x] = mo == mn ? 1.f : ex2d(mo - mn);
+        c.m[x] = mn;
+        c.l[x] = c.l[x] * wa[x] + from[(C::kAcc + C::kM + x) * 32 + lane] * wb[x];
+      }
+#pragma unroll
+      for (int x = 0; x < C::kAcc; ++x)
+        c.acc[x] = c.acc[x] * wa[C::m_index(x)] + from[x * 32 + lane] * wb[C::m_index(x)];
+      bad |= from[(kRegs - 1) * 32 + lane] != 0.f;
+    };
+    if (warp >= 2) put(join + (warp - 2) * kRegs * 32);
+    __syncthreads();
+    if (warp < 2) take(join + warp * kRegs * 32);
+    __syncthreads();
+    // a slot of its own: warps 2 and 3 may be at the next item's end while warp 0 reads this one
+    if (warp == 1) put(join + 2 * kRegs * 32);
+    __syncthreads();
+    const bool whole = item_first >= run0 && ends;
+    const int slot = 2 * int(blockIdx.x) + (item_first >= run0 ? 1 : 0);
+    if (warp == 0) {
+      take(join + 2 * kRegs * 32);
+      c.sum_l();
+      if (__any_sync(0xffffffffu, bad)) {
+        bad = true;
+        if (lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
+      }
+      if (whole) {
+        float inv[C::kM];
+#pragma unroll
+        for (int x = 0; x < C::kM; ++x) inv[x] = bad ? 0.f : 1.f / c.l[x];
+        c.each([&](int h, int x, int dim, float val) {
+          if (h < heads)
+            out[(int64_t(b) * p.Hq + h0 + h) * D + dim] = from_f<T>(bad ? 0.f : val * inv[x]);
+        });
+        if (p.lse)
+          c.each_head([&](int h, int x) {
+            if (h < heads) p.lse[int64_t(b) * p.Hq + h0 + h] = bad ? -INFINITY : (c.m[x] + log2f(c.l[x])) * kFdLn2;
+          });
+      } else {
+        float* po = p.part_o + int64_t(slot) * kFdMaxHeads * D;
+        float* pm = p.part_ml + int64_t(slot) * kFdMaxHeads * 2;
+        c.each([&](int h, int, int dim, float val) {
+          if (h < heads) po[h * D + dim] = val;
+        });
+        c.each_head([&](int h, int x) {
+          if (h < heads) {
+            pm[2 * h] = c.m[x];
+            pm[2 * h + 1] = bad ? -1.f : c.l[x];
+          }
+        });
+      }
+    }
+    if (!whole) {
+      // the item's units lie in CTAs c0..c1: the last to arrive joins them
+      const int c0 = int(item_first / per), c1 = int((item_first + n - 1) / per);
+      if (warp == 0) {
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();  // after the warp's stores (ordered by __syncwarp)
+          const int old = atomicAdd(&p.arrivals[item], 1);
+          last_s = old == c1 - c0;
+          if (last_s) p.arrivals[item] = 0;  // ready for the next call
+          __threadfence();
+        }
+      }
+      __syncthreads();
+      if (last_s) {
+        const float* pm = p.part_ml;
+        auto slot_of = [&](int cta) { return int64_t(2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0)); };
+        for (int o = threadIdx.x; o < heads * D; o += kFdThreads) {
+          const int h = o / D;
+          float M = -INFINITY;
+          bool spoilt = false;
+#pragma unroll 4
+          for (int cta = c0; cta <= c1; ++cta) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pm + (slot_of(cta) * kFdMaxHeads + h) * 2));
+            M = fmaxf(M, ml.x);
+            spoilt |= ml.y < 0.f;
+          }
+          float den = 0.f, sum = 0.f;
+#pragma unroll 4
+          for (int cta = c0; cta <= c1; ++cta) {
+            const int64_t s = slot_of(cta) * kFdMaxHeads + h;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pm + s * 2));
+            const float w = ml.x == M ? 1.f : ex2d(ml.x - M);
+            den = fmaf(w, ml.y, den);
+            sum = fmaf(w, __ldcg(p.part_o + s * D + o % D), sum);
+          }
+          out[(int64_t(b) * p.Hq + h0 + h) * D + o % D] = from_f<T>(spoilt ? 0.f : sum / den);
+          if (p.lse && o % D == 0)
+            p.lse[int64_t(b) * p.Hq + h0 + h] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
+        }
+      }
+      __syncthreads();  // last_s is read before the next item sets it
+    }
+    if (ends) item_first += n;
+    const int was = at.b;
+    at.next(p);
+    if (at.b != was) item_first = z + 1;
+  }
+  cp_wait<0>();
+}
+
+// Fixed grid: two CTAs per SM (the smaller shapes' shared memory allows it).
+int fd_grid() { return 2 * kNumSMs; }
+
+template <typename T, int D, int HN>
+cudaError_t decode(const FdParams& p, cudaStream_t stream) {
+  auto kern = full_decode_kernel<T, D, HN>;
+  constexpr int bytes = FdShape<T, D, HN>::kBytes;
+  static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  ProfScope pf("full_decode", stream);
+  kern<<<fd_grid(), kFdThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+int head_groups(int hpg) { return (hpg + kFdMaxHeads - 1) / kFdMaxHeads; }
+
+}  // namespace
+
+size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d) {
+  const size_t slots = 2 * size_t(fd_grid());
+  return up256(slots * kFdMaxHeads * d * 4) + up256(slots * kFdMaxHeads * 8) +
+         up256(size_t(B) * Hkv * head_groups(Hq / Hkv) * 4);
+}
+
+cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream) {
+  FdParams p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.kv_len = a.seq.kv_len;
+  p.pages = a.pages;
+  p.B = a.seq.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.hpg = a.Hq / a.Hkv;
+  p.ngr = head_groups(p.hpg);
+  p.cap = a.seq.Tk;
+  p.scale_log2 = a.scale * kFdLog2e;
+  const size_t slots = 2 * size_t(fd_grid());
+  char* w = static_cast<char*>(a.ws) + kWsHeader;
+  p.part_o = reinterpret_cast<float*>(w);
+  w += up256(slots * kFdMaxHeads * a.d * 4);
+  p.part_ml = reinterpret_cast<float*>(w);
+  w += up256(slots * kFdMaxHeads * 8);
+  p.arrivals = reinterpret_cast<int*>(w);
+  p.out = a.out;
+  p.lse = a.lse;
+  p.status = &static_cast<WsHeader*>(a.ws)->status;
+  const bool two = p.hpg > 8;  // 8 heads per tile: one tile up to 8, two beyond
+  if (a.dtype == MSA_BF16) {
+    if (a.d == 128) return two ? decode<__nv_bfloat16, 128, 2>(p, stream) : decode<__nv_bfloat16, 128, 1>(p, stream);
+    return two ? decode<__nv_bfloat16, 64, 2>(p, stream) : decode<__nv_bfloat16, 64, 1>(p, stream);
+  }
+  if (a.d == 128) return two ? decode<float, 128, 2>(p, stream) : decode<float, 128, 1>(p, stream);
+  return two ? decode<float, 64, 2>(p, stream) : decode<float, 64, 1>(p, stream);
+}
+
+}  // namespace msa

@@ -106,11 +106,13 @@ struct FullBwdArgs {
   const void* dout;
   void *dq, *dk, *dv;
 };
-size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d, int dtype);
+size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d);  // behind the header
 size_t full_backward_ws_bytes(int Tq, int Hq, int dtype);
 // CUDA cores, any dtype
 cudaError_t launch_full_rows(const FullArgs& a, cudaStream_t stream);
 cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream);
+// decode over pages, any dtype
+cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream);
 // tcgen05 prefill (bf16); needs Tk > 0
 cudaError_t launch_full_prefill_tc(const FullArgs& a, cudaStream_t stream);
 struct AppendArgs {
