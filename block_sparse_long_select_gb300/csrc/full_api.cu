@@ -54,6 +54,7 @@ size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int 
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
   if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(B, Hq, Hkv, d) : 0;
   if (Nq < 0 || !rows_ok(Nq, Hq) || !rows_ok(op == MSA_OP_PAGED_APPEND ? Nq : Nk, Hkv)) return 0;
+  if (op == MSA_OP_FULL_BACKWARD && dtype == MSA_BF16) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
   return kWsHeader;
 }
 
@@ -235,5 +236,7 @@ extern "C" msa_status_t msa_full_attn_backward(const void* q, const void* k, con
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  // tensor cores for bf16; without rows or keys there is nothing to map for TMA
+  if (dtype == MSA_BF16 && Tq > 0 && Tk > 0) return launched(launch_full_backward_tc(a, stream));
   return launched(launch_full_rows_backward(a, stream));
 }

@@ -1,0 +1,738 @@
+// Full attention, backward, bf16 on tcgen05 (sm_103a), packed sequences:
+//   P_ij = exp(s_ij - lse_i),  delta_i = dout_i . out_i
+//   dS_ij = P_ij (dout_i . v_j - delta_i)
+//   dv_j = sum_i P_ij dout_i;  dk_j = scale sum_i dS_ij q_i;  dq_i = scale sum_j dS_ij k_j
+//
+// Two kernels, each of which owns what it sums, so that nothing is added
+// atomically and every run gives the same bits: dk and dv per key tile over the
+// rows that see it, dq per row tile over the keys it sees. That is seven
+// products per tile pair instead of the five that one kernel with atomic dq
+// sums would take; the order of its sums would change from run to run, and
+// each pair would send 64 KB of fp32 adds to L2. Row tiles are 128 / hpg tokens x
+// the hpg heads of a group, as in the forward: the sum over a group's heads is
+// part of the product.
+//
+// Bound: the tensor cores. Both kernels split their epilogue in two so that the
+// tensor cores work through it: from the scores to P (kept in registers) while
+// the products of the tile before and dP run, then from dP to dS while the next
+// scores run. P and dS are rounded to bf16 for the products that read them
+// (2^-8 each, averaging out over the sums); sums stay in fp32.
+//
+// Warps of both: 0 loads (TMA; zeroes rows of other sequences, whose
+// infinities a weight of 0 would not silence), 1 MMA issue and TMEM, 4-11
+// epilogue: two threads per TMEM lane, 64 columns each. dkv: 2-3 fetch the
+// rows' lse and delta. Every wait is bounded.
+#include "full_tc.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kFbThreads = 384;
+
+struct FbParams {
+  SeqMap seq;
+  int Hq, Hkv, hpg, tpt, nslots;
+  float scale, scale_log2;
+  const float2* rows;  // [Hkv][Tq][hpg]: lse * log2(e) (+inf where no key is seen), delta
+  __nv_bfloat16 *dq, *dk, *dv;
+  uint32_t* status;
+};
+
+// ---- per row: lse in log2 units and delta, laid out as the row tiles --------------
+template <int D>
+__global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restrict__ out, const uint4* __restrict__ dout,
+                                                            const float* __restrict__ lse, int Tq, int Hq, int hpg,
+                                                            float2* __restrict__ rows) {
+  constexpr int kLanes = D / 8;  // a row's 16-byte chunks
+  const int64_t x = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  const int c = threadIdx.x % kLanes;
+  const bool in = x < int64_t(Tq) * Hq;
+  float s = 0.f;
+  if (in) {
+    const uint4 a = out[x * kLanes + c], b = dout[x * kLanes + c];
+    const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
+    const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 fa = __bfloat1622float2(a2[i]), fb = __bfloat1622float2(b2[i]);
+      s = fmaf(fa.x, fb.x, fmaf(fa.y, fb.y, s));
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (in && c == 0) {
+    const int64_t t = x / Hq;
+    const int h = int(x % Hq);
+    const float l = lse[x];
+    rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, s);
+  }
+}
+
+template <int D>
+struct FbSmem {
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr int kRowSlots = 4;  // row data of four tiles (dkv)
+  // two resident tiles, then a ring of two slots for each of two streamed operands
+  static constexpr uint32_t oA = 0, oB = kTile, oC = 2 * kTile, oE = 4 * kTile, oRow = 6 * kTile;
+  static constexpr uint32_t oBar = oRow + kRowSlots * 2 * kRows * 4;
+  static constexpr int kBars = 1 + 8 + 4 + 2 * kRowSlots + 3;
+  static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
+};
+struct FbBars {
+  uint64_t *res_full, *c_full, *c_empty, *e_full, *e_empty, *s_full, *p_full, *dp_full, *ds_full, *r_full, *r_empty,
+      *acc_full, *tail, *done;
+  __device__ __forceinline__ FbBars(uint64_t* b, int slots) {
+    res_full = b;
+    c_full = b + 1;
+    c_empty = b + 3;
+    e_full = b + 5;
+    e_empty = b + 7;
+    s_full = b + 9;
+    p_full = b + 10;
+    dp_full = b + 11;
+    ds_full = b + 12;
+    r_full = b + 13;
+    r_empty = r_full + slots;
+    acc_full = r_empty + slots;
+    tail = acc_full + 1;
+    done = tail + 1;
+  }
+};
+
+// bf16 pairs of 64 columns go over the first half of the 64 columns they came
+// from, so neither epilogue warpgroup writes where the other still reads.
+__device__ __forceinline__ uint32_t a_col(int kk) { return uint32_t((kk >> 2) * 64 + (kk & 3) * 8); }
+
+template <int D>
+__device__ __forceinline__ void store_acc(uint32_t taddr, int cols, __nv_bfloat16* dst, float mul, bool in) {
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t o[32];
+    tc::tmem_ld_32x32b_x32(taddr + c, o);
+    tc::tmem_ld_wait();
+    if (in) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t u[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          u[y] = pack_bf16(__uint_as_float(o[x * 8 + 2 * y]) * mul, __uint_as_float(o[x * 8 + 2 * y + 1]) * mul);
+        reinterpret_cast<uint4*>(dst + c)[x] = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// dk, dv of 128 keys of one (sequence, key/value head)
+// TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV, dK
+// ---------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kFbThreads, 1)
+    full_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const FbParams p) {
+  using SM = FbSmem<D>;
+  constexpr int NH = D / 64, NR = SM::kRowSlots;
+  constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
+  constexpr uint32_t kColDv = 256, kColDk = 256 + D;
+  extern __shared__ __align__(1024) uint8_t fb_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (tc::smem_u32(fb_smem) & 1023u) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
+    return;
+  }
+  const int g = blockIdx.x % p.Hkv;
+  int kt;
+  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, int(blockIdx.x / p.Hkv), kt);  // early keys: most rows
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.seq, b);
+  if (!s.ok) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    return;
+  }
+  const int j0 = kt * kKeys;
+  const int off = s.Lk - s.Lq;              // row i sees keys j <= off + i
+  const int r0 = max(j0 - off, 0) / p.tpt;  // first row tile that sees one of these keys
+  const int n = max((s.Lq + p.tpt - 1) / p.tpt - r0, 0);
+  if (n == 0) {  // no row sees them
+    for (int x = threadIdx.x; x < min(kKeys, s.Lk - j0) * (D / 8); x += kFbThreads) {
+      const int64_t o = ((int64_t(s.k0) + j0 + x / (D / 8)) * p.Hkv + g) * (D / 8) + x % (D / 8);
+      reinterpret_cast<uint4*>(p.dk)[o] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(p.dv)[o] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
+  const FbBars bar(bars, NR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* rowd = reinterpret_cast<float*>(fb_smem + SM::oRow);  // slot x: lse2 [128], delta [128]
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
+    tc::mbar_init(bar.p_full, 8);
+    tc::mbar_init(bar.ds_full, 8);
+    for (int x = 0; x < NR; ++x) {
+      tc::mbar_init(bar.r_full + x, 2);
+      tc::mbar_init(bar.r_empty + x, 8);
+    }
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    set_status(p.status, MSA_ERR_TIMEOUT);
+  };
+
+  if (warp == 0) {
+    // ------------------------------ loads ------------------------------
+    const int rows = p.tpt * p.hpg;
+    if (rows < kRows) {  // rows that no box fills: zero for good
+#pragma unroll
+      for (int x = 0; x < 4; ++x) zero_rows<NH>(fb_smem + SM::oC + x * SM::kTile, rows, kRows);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+    }
+    auto keys = [&]() {
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar.res_full, 2 * SM::kTile);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          tc::tma_load_3d(fb_smem + SM::oA + h * kHalfTile, &tmK, bar.res_full, h * 64, g, s.k0 + j0);
+          tc::tma_load_3d(fb_smem + SM::oB + h * kHalfTile, &tmV, bar.res_full, h * 64, g, s.k0 + j0);
+        }
+      }
+    };
+    auto box = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int tok) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) tc::tma_load_4d(dst + h * kHalfTile, map, full, h * 64, 0, g, tok);
+    };
+    keys();
+    bool ok = true;
+    int nc = 0, ne = 0, tails = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      const int st = i & 1, ph = (i >> 1) & 1, t0 = (r0 + i) * p.tpt;
+      uint8_t* qd = fb_smem + SM::oC + st * SM::kTile;
+      uint8_t* od = fb_smem + SM::oE + st * SM::kTile;
+      const uint32_t bytes = uint32_t(rows) * D * 2;
+      if (!(ok = warp_wait(bar.c_empty + st, ph ^ 1, abort_flag))) break;
+      const int valid = (s.Lq - t0) * p.hpg;
+      if (valid >= rows) {
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.c_full + st, bytes);
+          box(&tmQ, qd, bar.c_full + st, s.q0 + t0);
+        }
+        ++nc;
+        if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.e_full + st, bytes);
+          box(&tmO, od, bar.e_full + st, s.q0 + t0);
+        }
+        ++ne;
+      } else {  // the sequence ends in this tile: the rows behind it become zeros
+        if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.tail, 2 * bytes);
+          box(&tmQ, qd, bar.tail, s.q0 + t0);
+          box(&tmO, od, bar.tail, s.q0 + t0);
+        }
+        ++tails;
+        if (!(ok = warp_wait(bar.tail, 0, abort_flag))) break;
+        zero_rows<NH>(qd, valid, rows);
+        zero_rows<NH>(od, valid, rows);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(bar.c_full + st);
+          tc::mbar_arrive(bar.e_full + st);
+        }
+      }
+    }
+    if (!ok) {
+      fail();
+      int zero = 0;
+      tc::mbar_wait(bar.res_full, 0, &zero);
+      for (int x = max(nc - 2, 0); x < nc; ++x) tc::mbar_wait(bar.c_full + (x & 1), (x >> 1) & 1, &zero);
+      for (int x = max(ne - 2, 0); x < ne; ++x) tc::mbar_wait(bar.e_full + (x & 1), (x >> 1) & 1, &zero);
+      if (tails) tc::mbar_wait(bar.tail, 0, &zero);
+    }
+  } else if (warp == 1) {
+    // ----------------------------- MMA issue -----------------------------
+    if (lane == 0) {
+      constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
+      const uint32_t sb = tc::smem_u32(fb_smem);
+      auto major = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, 16); };           // K-major along d
+      auto minor = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, kHalfTile); };    // rows along K
+      auto dots = [&](uint32_t col, uint32_t a0, uint32_t b0) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
+          tc::mma_f16_ss_lo<kHi>(tmem + col, a0 + o, b0 + o, kIdS, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto sums = [&](uint32_t dst, uint32_t src, uint32_t b0, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          tc::mma_f16_ts_lo<kHi>(tmem + dst, tmem + src + a_col(kk), b0 + ((kk * 16 * 128) >> 4), kIdA,
+                                 first && kk == 0 ? 0u : 1u);
+      };
+      const uint32_t ka = major(SM::oA), va = major(SM::oB);
+      bool ok = tc::mbar_wait(bar.res_full, 0, abort_flag) && tc::mbar_wait(bar.c_full, 0, abort_flag);
+      if (ok) {
+        tc::fence_after_sync();
+        dots(0, ka, major(SM::oC));
+        tc::mma_commit(bar.s_full);
+        ok = tc::mbar_wait(bar.e_full, 0, abort_flag);
+      }
+      if (ok) {
+        dots(128, va, major(SM::oE));
+        tc::mma_commit(bar.dp_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t st = i & 1, q = SM::oC + st * SM::kTile, o = SM::oE + st * SM::kTile;
+        const uint32_t st1 = st ^ 1, ph1 = ((i + 1) >> 1) & 1;
+        const uint32_t q1 = SM::oC + st1 * SM::kTile, o1 = SM::oE + st1 * SM::kTile;
+        if (!(ok = tc::mbar_wait(bar.p_full, i & 1, abort_flag))) break;
+        tc::fence_after_sync();
+        sums(kColDv, 0, minor(o), i == 0);
+        // dP of this tile is complete before the epilogue can hand over dS, but
+        // dO's slot is free only behind dV: issued here, tracked by this commit
+        tc::mma_commit(bar.e_empty + st);
+        if (i + 1 < n) {  // over P, behind the product that reads it
+          if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
+          dots(0, ka, major(q1));
+          tc::mma_commit(bar.s_full);
+        }
+        if (!(ok = tc::mbar_wait(bar.ds_full, i & 1, abort_flag))) break;
+        tc::fence_after_sync();
+        sums(kColDk, 128, minor(q), i == 0);
+        tc::mma_commit(bar.c_empty + st);
+        if (i + 1 < n) {
+          if (!(ok = tc::mbar_wait(bar.e_full + st1, ph1, abort_flag))) break;
+          dots(128, va, major(o1));
+          tc::mma_commit(bar.dp_full);
+        } else {
+          tc::mma_commit(bar.acc_full);
+        }
+      }
+      if (!ok) fail();
+      int zero = 0;
+      tc::mma_commit(bar.done);
+      tc::mbar_wait(bar.done, 0, &zero);
+    }
+  } else if (warp < 4) {
+    // --------------------------- lse and delta ---------------------------
+    const int x0 = (warp - 2) * 64 + lane;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int sl = i % NR, t0 = (r0 + i) * p.tpt;
+      const int valid = min(s.Lq - t0, p.tpt) * p.hpg;
+      const float2* src = p.rows + (int64_t(g) * p.seq.Tq + s.q0 + t0) * p.hpg;
+      float2 v[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) v[y] = x0 + 32 * y < valid ? src[x0 + 32 * y] : make_float2(INFINITY, 0.f);
+      if (!(ok = warp_wait(bar.r_empty + sl, ((i / NR) & 1) ^ 1, abort_flag))) break;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        rowd[sl * 2 * kRows + x0 + 32 * y] = v[y].x;
+        rowd[sl * 2 * kRows + kRows + x0 + 32 * y] = v[y].y;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar.r_full + sl);
+    }
+    if (!ok) fail();
+  } else {
+    // ------------------------------ epilogue ------------------------------
+    const int w = (warp - 4) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    const uint32_t sbase = tmem + (uint32_t(quarter * 32) << 16);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int sl = i % NR;
+      // row r (token t0 + r / hpg) sees this key from row rmin on
+      const int rmin = (j0 + key - off - (r0 + i) * p.tpt) * p.hpg - w * 64;
+      const bool mask = j0 + kKeys - 1 - off > (r0 + i) * p.tpt;  // some key of the tile is hidden from its first row
+      if (!(ok = warp_wait(bar.r_full + sl, (i / NR) & 1, abort_flag) && warp_wait(bar.s_full, i & 1, abort_flag)))
+        break;
+      tc::fence_after_sync();
+      const float4* l4 = reinterpret_cast<const float4*>(rowd + sl * 2 * kRows + w * 64);
+      const float4* d4 = reinterpret_cast<const float4*>(rowd + sl * 2 * kRows + kRows + w * 64);
+      float pr[64];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32], pk[16];
+        tc::tmem_ld_32x32b_x32(sbase + w * 64 + c * 32, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float4 l = l4[c * 8 + x];
+          pr[c * 32 + 4 * x] = ex2(fmaf(__uint_as_float(v[4 * x]), p.scale_log2, -l.x));
+          pr[c * 32 + 4 * x + 1] = ex2(fmaf(__uint_as_float(v[4 * x + 1]), p.scale_log2, -l.y));
+          pr[c * 32 + 4 * x + 2] = ex2(fmaf(__uint_as_float(v[4 * x + 2]), p.scale_log2, -l.z));
+          pr[c * 32 + 4 * x + 3] = ex2(fmaf(__uint_as_float(v[4 * x + 3]), p.scale_log2, -l.w));
+        }
+        if (mask) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (c * 32 + x < rmin) pr[c * 32 + x] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(pr[c * 32 + 2 * x], pr[c * 32 + 2 * x + 1]);
+        tc::tmem_st_32x32b_x16(sbase + w * 64 + c * 16, pk);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar.p_full);
+      if (!(ok = warp_wait(bar.dp_full, i & 1, abort_flag))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32], pk[16];
+        tc::tmem_ld_32x32b_x32(sbase + 128 + w * 64 + c * 32, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float4 d = d4[c * 8 + x];
+          const float* q = pr + c * 32 + 4 * x;
+          pk[2 * x] = pack_bf16(q[0] * (__uint_as_float(v[4 * x]) - d.x), q[1] * (__uint_as_float(v[4 * x + 1]) - d.y));
+          pk[2 * x + 1] =
+              pack_bf16(q[2] * (__uint_as_float(v[4 * x + 2]) - d.z), q[3] * (__uint_as_float(v[4 * x + 3]) - d.w));
+        }
+        tc::tmem_st_32x32b_x16(sbase + 128 + w * 64 + c * 16, pk);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(bar.ds_full);
+        tc::mbar_arrive(bar.r_empty + sl);
+      }
+    }
+    if (ok) ok = warp_wait(bar.acc_full, 0, abort_flag);
+    if (ok) {
+      tc::fence_after_sync();
+      const int64_t row = (int64_t(s.k0) + j0 + key) * p.Hkv + g;
+      if (w == 0)
+        store_acc<D>(sbase + kColDv, D, p.dv + row * D, 1.f, j0 + key < s.Lk);
+      else
+        store_acc<D>(sbase + kColDk, D, p.dk + row * D, p.scale, j0 + key < s.Lk);
+    } else {
+      fail();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// dq of one row tile over its keys
+// TMEM: S of even tiles [0, 128), dP [128, 256) (dS over it), dQ [256, 256 + D), S of odd tiles [384, 512)
+// ---------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kFbThreads, 1)
+    full_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const FbParams p) {
+  using SM = FbSmem<D>;
+  constexpr int NH = D / 64;
+  constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
+  constexpr uint32_t kColDq = 256;
+  extern __shared__ __align__(1024) uint8_t fb_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (tc::smem_u32(fb_smem) & 1023u) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
+    return;
+  }
+  const int g = blockIdx.x % p.Hkv;
+  int rt;
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.nslots - 1 - int(blockIdx.x / p.Hkv), rt);  // late rows first
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.seq, b);
+  if (!s.rows_ok) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    return;
+  }
+  const int i0 = rt * p.tpt, i1 = min(i0 + p.tpt, s.Lq);
+  const int vis_last = s.ok ? s.Lk - s.Lq + i1 : 0;
+  const int n = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
+  if (n == 0) {
+    if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    for (int x = threadIdx.x; x < (i1 - i0) * p.hpg * (D / 8); x += kFbThreads) {
+      const int r = x / (D / 8);
+      const int64_t row = (int64_t(s.q0) + i0 + r / p.hpg) * p.Hq + g * p.hpg + r % p.hpg;
+      reinterpret_cast<uint4*>(p.dq + row * D)[x % (D / 8)] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
+  const FbBars bar(bars, SM::kRowSlots);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
+    tc::mbar_init(bar.p_full, 8);
+    tc::mbar_init(bar.ds_full, 8);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    set_status(p.status, MSA_ERR_TIMEOUT);
+  };
+  auto s_col = [](int j) { return (j & 1) ? 384u : 0u; };
+
+  if (warp == 0) {
+    // ------------------------------ loads ------------------------------
+    auto box = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int row) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) tc::tma_load_3d(dst + h * kHalfTile, map, full, h * 64, g, row);
+    };
+    if (lane == 0) {
+      tc::mbar_arrive_expect_tx(bar.res_full, 2 * uint32_t(p.tpt * p.hpg) * D * 2);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        tc::tma_load_4d(fb_smem + SM::oA + h * kHalfTile, &tmQ, bar.res_full, h * 64, 0, g, s.q0 + i0);
+        tc::tma_load_4d(fb_smem + SM::oB + h * kHalfTile, &tmO, bar.res_full, h * 64, 0, g, s.q0 + i0);
+      }
+    }
+    bool ok = true;
+    int nc = 0, ne = 0, tails = 0;
+    for (int j = 0; j < n && ok; ++j) {
+      const int st = j & 1, ph = (j >> 1) & 1, valid = s.Lk - j * kKeys;
+      uint8_t* kd = fb_smem + SM::oC + st * SM::kTile;
+      uint8_t* vd = fb_smem + SM::oE + st * SM::kTile;
+      if (!(ok = warp_wait(bar.c_empty + st, ph ^ 1, abort_flag))) break;
+      if (valid >= kKeys) {
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.c_full + st, SM::kTile);
+          box(&tmK, kd, bar.c_full + st, s.k0 + j * kKeys);
+        }
+        ++nc;
+        if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.e_full + st, SM::kTile);
+          box(&tmV, vd, bar.e_full + st, s.k0 + j * kKeys);
+        }
+        ++ne;
+      } else {  // the keys behind the sequence's end become zeros
+        if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar.tail, 2 * SM::kTile);
+          box(&tmK, kd, bar.tail, s.k0 + j * kKeys);
+          box(&tmV, vd, bar.tail, s.k0 + j * kKeys);
+        }
+        ++tails;
+        if (!(ok = warp_wait(bar.tail, 0, abort_flag))) break;
+        zero_rows<NH>(kd, valid, kKeys);
+        zero_rows<NH>(vd, valid, kKeys);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(bar.c_full + st);
+          tc::mbar_arrive(bar.e_full + st);
+        }
+      }
+    }
+    if (!ok) {
+      fail();
+      int zero = 0;
+      tc::mbar_wait(bar.res_full, 0, &zero);
+      for (int x = max(nc - 2, 0); x < nc; ++x) tc::mbar_wait(bar.c_full + (x & 1), (x >> 1) & 1, &zero);
+      for (int x = max(ne - 2, 0); x < ne; ++x) tc::mbar_wait(bar.e_full + (x & 1), (x >> 1) & 1, &zero);
+      if (tails) tc::mbar_wait(bar.tail, 0, &zero);
+    }
+  } else if (warp == 1) {
+    // ----------------------------- MMA issue -----------------------------
+    if (lane == 0) {
+      constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
+      const uint32_t sb = tc::smem_u32(fb_smem);
+      auto major = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, 16); };
+      auto minor = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, kHalfTile); };
+      auto dots = [&](uint32_t col, uint32_t a0, uint32_t b0) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
+          tc::mma_f16_ss_lo<kHi>(tmem + col, a0 + o, b0 + o, kIdS, kk > 0 ? 1u : 0u);
+        }
+      };
+      const uint32_t qa = major(SM::oA), oa = major(SM::oB);
+      bool ok = tc::mbar_wait(bar.res_full, 0, abort_flag) && tc::mbar_wait(bar.c_full, 0, abort_flag);
+      if (ok) {
+        tc::fence_after_sync();
+        dots(s_col(0), qa, major(SM::oC));
+        tc::mma_commit(bar.s_full);
+        ok = tc::mbar_wait(bar.e_full, 0, abort_flag);
+      }
+      if (ok) {
+        dots(128, oa, major(SM::oE));
+        tc::mma_commit(bar.dp_full);
+        tc::mma_commit(bar.e_empty);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t st = j & 1, st1 = st ^ 1, ph1 = ((j + 1) >> 1) & 1;
+        if (j + 1 < n) {
+          // the other S buffer: its tile j - 1 was read before dS(j - 1), whose product is issued
+          if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
+          dots(s_col(j + 1), qa, major(SM::oC + st1 * SM::kTile));
+          tc::mma_commit(bar.s_full);
+        }
+        if (!(ok = tc::mbar_wait(bar.ds_full, j & 1, abort_flag))) break;
+        tc::fence_after_sync();
+        const uint32_t kb = minor(SM::oC + st * SM::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc::mma_f16_ts_lo<kHi>(tmem + kColDq, tmem + 128 + a_col(kk), kb + ((kk * 16 * 128) >> 4), kIdA,
+                                 j == 0 && kk == 0 ? 0u : 1u);
+        tc::mma_commit(bar.c_empty + st);
+        if (j + 1 < n) {
+          if (!(ok = tc::mbar_wait(bar.e_full + st1, ph1, abort_flag))) break;
+          dots(128, oa, major(SM::oE + st1 * SM::kTile));
+          tc::mma_commit(bar.dp_full);
+          tc::mma_commit(bar.e_empty + st1);
+        } else {
+          tc::mma_commit(bar.acc_full);
+        }
+      }
+      if (!ok) fail();
+      int zero = 0;
+      tc::mma_commit(bar.done);
+      tc::mbar_wait(bar.done, 0, &zero);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------ epilogue ------------------------------
+    const int w = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lbase = tmem + (uint32_t(quarter * 32) << 16);
+    const int i = i0 + r / p.hpg;
+    const bool valid = r < p.tpt * p.hpg && i < i1;
+    float2 rd = make_float2(INFINITY, 0.f);
+    if (valid) rd = p.rows[(int64_t(g) * p.seq.Tq + s.q0 + i) * p.hpg + r % p.hpg];
+    const int vis = s.Lk - s.Lq + i + 1;
+    const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys;  // tiles below it are seen whole by every row
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = warp_wait(bar.s_full, j & 1, abort_flag))) break;
+      tc::fence_after_sync();
+      const int lim = vis - j * kKeys - w * 64;  // columns below it are seen
+      float pr[64];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tc::tmem_ld_32x32b_x32(lbase + s_col(j) + w * 64 + c * 32, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) pr[c * 32 + x] = ex2(fmaf(__uint_as_float(v[x]), p.scale_log2, -rd.x));
+      }
+      if (j >= j_mask) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+          if (x >= lim) pr[x] = 0.f;
+      }
+      if (!(ok = warp_wait(bar.dp_full, j & 1, abort_flag))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32], pk[16];
+        tc::tmem_ld_32x32b_x32(lbase + 128 + w * 64 + c * 32, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          pk[x] = pack_bf16(pr[c * 32 + 2 * x] * (__uint_as_float(v[2 * x]) - rd.y),
+                            pr[c * 32 + 2 * x + 1] * (__uint_as_float(v[2 * x + 1]) - rd.y));
+        tc::tmem_st_32x32b_x16(lbase + 128 + w * 64 + c * 16, pk);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar.ds_full);
+    }
+    if (ok) ok = warp_wait(bar.acc_full, 0, abort_flag);
+    if (ok) {
+      tc::fence_after_sync();
+      const int64_t row = (int64_t(s.q0) + i) * p.Hq + g * p.hpg + r % p.hpg;
+      store_acc<D>(lbase + kColDq + w * (D / 2), D / 2, p.dq + row * D + w * (D / 2), p.scale, valid);
+    } else {
+      fail();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
+  const FullArgs& f = a.f;
+  FbParams p{};
+  p.seq = f.seq;
+  p.Hq = f.Hq;
+  p.Hkv = f.Hkv;
+  p.hpg = f.Hq / f.Hkv;
+  p.tpt = kRows / p.hpg;
+  p.scale = f.scale;
+  p.scale_log2 = f.scale * kLog2e;
+  p.rows = reinterpret_cast<float2*>(static_cast<char*>(f.ws) + kWsHeader);
+  p.dq = static_cast<__nv_bfloat16*>(a.dq);
+  p.dk = static_cast<__nv_bfloat16*>(a.dk);
+  p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.status = &static_cast<WsHeader*>(f.ws)->status;
+  const int qslots = f.seq.Tq / p.tpt + f.seq.B, kslots = f.seq.Tk / kKeys + f.seq.B;
+  const int64_t qc = int64_t(qslots) * f.Hkv, kc = int64_t(kslots) * f.Hkv;
+  if (qc >= (int64_t(1) << 31) || kc >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  CUtensorMap tmQ, tmO, tmK, tmV;
+  if (!map_rows(&tmQ, f.q, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) || !map_rows(&tmO, a.dout, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) ||
+      !map_keys(&tmK, f.k, f.seq.Tk, f.Hkv, D, kKeys) || !map_keys(&tmV, f.v, f.seq.Tk, f.Hkv, D, kKeys))
+    return cudaErrorInvalidValue;
+  constexpr int bytes = FbSmem<D>::kTotal;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(full_bwd_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) ||
+      (e = cudaFuncSetAttribute(full_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
+    return e;
+  {
+    ProfScope pf("full_bwd_rows", stream);
+    const int64_t threads = int64_t(f.seq.Tq) * f.Hq * (D / 8);
+    full_bwd_rows_kernel<D><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(
+        static_cast<const uint4*>(f.out), static_cast<const uint4*>(a.dout), f.lse, f.seq.Tq, f.Hq, p.hpg,
+        const_cast<float2*>(p.rows));
+    if ((e = cudaGetLastError())) return e;
+  }
+  {
+    ProfScope pf("full_bwd_dkv", stream);
+    p.nslots = kslots;
+    full_bwd_dkv_kernel<D><<<unsigned(kc), kFbThreads, bytes, stream>>>(tmQ, tmO, tmK, tmV, p);
+    if ((e = cudaGetLastError())) return e;
+  }
+  ProfScope pf("full_bwd_dq", stream);
+  p.nslots = qslots;
+  full_bwd_dq_kernel<D><<<unsigned(qc), kFbThreads, bytes, stream>>>(tmQ, tmO, tmK, tmV, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t full_backward_ws_bytes(int Tq, int Hq) { return (size_t(Tq) * Hq * sizeof(float2) + 255) & ~size_t(255); }
+
+cudaError_t launch_full_backward_tc(const FullBwdArgs& a, cudaStream_t stream) {
+  return a.f.d == 128 ? backward<128>(a, stream) : backward<64>(a, stream);
+}
+
+}  // namespace msa

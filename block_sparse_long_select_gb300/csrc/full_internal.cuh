@@ -107,7 +107,7 @@ struct FullBwdArgs {
   void *dq, *dk, *dv;
 };
 size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d);  // behind the header
-size_t full_backward_ws_bytes(int Tq, int Hq, int dtype);
+size_t full_backward_ws_bytes(int Tq, int Hq);  // bf16, behind the header
 // CUDA cores, any dtype
 cudaError_t launch_full_rows(const FullArgs& a, cudaStream_t stream);
 cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream);
@@ -115,6 +115,8 @@ cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream)
 cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream);
 // tcgen05 prefill (bf16); needs Tk > 0
 cudaError_t launch_full_prefill_tc(const FullArgs& a, cudaStream_t stream);
+// tcgen05 backward (bf16); needs Tq, Tk > 0
+cudaError_t launch_full_backward_tc(const FullBwdArgs& a, cudaStream_t stream);
 struct AppendArgs {
   const void *q, *k_new, *v_new;
   const float* rope;

@@ -23,32 +23,13 @@
 // Warps: 0 loads (TMA; zeroes the value rows behind a sequence's end, which
 // may hold anything), 1 MMA issue and TMEM, 4-7 and 8-11 the two softmax
 // warpgroups, one thread per row. Every wait is bounded.
-#include "full_internal.cuh"
-#include "tc_utils.cuh"
+#include "full_tc.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kRows = 128, kKeys = 128;
 constexpr int kPfThreads = 384;
-constexpr float kLog2e = 1.4426950408889634f, kLn2f = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // log2 of the largest weight
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return reinterpret_cast<const uint32_t&>(h);
-}
-
-// A wait of a whole warp: every lane gets the same answer, so that none leaves
-// a loop whose warp-wide operations the others still run.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
-}
 
 struct PfParams {
   SeqMap seq;
@@ -63,7 +44,6 @@ struct PfParams {
 template <int D>
 struct PfSmem {
   static constexpr int kStages = D == 128 ? 2 : 4;   // K ring and V ring
-  static constexpr uint32_t kHalf = kRows * 128;     // one 64-wide half of 128 rows
   static constexpr uint32_t kTile = kRows * D * 2;
   static constexpr uint32_t oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile, oBar = oV + kStages * kTile;
   static constexpr int kBars = 2 + 4 * kStages + 2 + 2 + 2 + 1 + 1;
@@ -176,7 +156,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (row >= 0) {
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-          tc::tma_load_3d(dst + h * SM::kHalf + lane * box_rows * 128, map, bar, h * 64, g, row);
+          tc::tma_load_3d(dst + h * kHalfTile + lane * box_rows * 128, map, bar, h * 64, g, row);
       }
     };
     auto load_q = [&](int w) {
@@ -184,7 +164,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc::mbar_arrive_expect_tx(&q_full[w], uint32_t(p.tpt * p.hpg) * D * 2);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-          tc::tma_load_4d(pf_smem + SM::oQ + w * SM::kTile + h * SM::kHalf, &tmQ, &q_full[w], h * 64, 0, g,
+          tc::tma_load_4d(pf_smem + SM::oQ + w * SM::kTile + h * kHalfTile, &tmQ, &q_full[w], h * 64, 0, g,
                           s.q0 + i0 + w * p.tpt);
       }
     };
@@ -211,10 +191,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         boxes(vt, &tmV, tail_bar, row);
         ++tails;
         if (!(ok = warp_wait(tail_bar, 0, abort_flag))) break;
-        for (int x = lane; x < (kKeys - valid) * 8 * NH; x += 32) {
-          const int h = x / ((kKeys - valid) * 8), y = x % ((kKeys - valid) * 8);
-          *reinterpret_cast<uint4*>(vt + h * SM::kHalf + valid * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-        }
+        zero_rows<NH>(vt, valid, kKeys);
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&v_full[st]);
@@ -236,12 +213,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
       const uint32_t qa = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oQ), 16);
       const uint32_t ka = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oK), 16);
-      const uint32_t va = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oV), SM::kHalf);
+      const uint32_t va = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oV), kHalfTile);
       auto scores = [&](int w, int j) {  // S_w = Q_w K_j^T
         const uint32_t q0 = qa + ((w * SM::kTile) >> 4), k0 = ka + (((j % NS) * SM::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4;
+          const uint32_t off = ((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
           tc::mma_f16_ss_lo<kHi>(tmem + w * 128, q0 + off, k0 + off, kIdS, kk > 0 ? 1u : 0u);
         }
         tc::mma_commit(&s_full[w]);
@@ -417,17 +394,10 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
   p.status = &static_cast<WsHeader*>(a.ws)->status;
   const bool paged = a.pages.table != nullptr;
   const uint64_t krows = paged ? uint64_t(a.pages.num_pages) << a.pages.page_log2 : uint64_t(a.seq.Tk);
+  const int box = paged ? 1 << a.pages.page_log2 : kKeys;
   CUtensorMap tmQ, tmK, tmV;
-  const uint64_t e = 2, d = D;
-  const uint64_t qd[4] = {d, uint64_t(p.hpg), uint64_t(a.Hkv), uint64_t(a.seq.Tq)};
-  const uint64_t qs[3] = {d * e, d * e * p.hpg, d * e * a.Hq};
-  const uint32_t qb[4] = {64, uint32_t(p.hpg), 1, uint32_t(p.tpt)};
-  const uint64_t kd[3] = {d, uint64_t(a.Hkv), krows};
-  const uint64_t ks[2] = {d * e, d * e * a.Hkv};
-  const uint32_t kb[3] = {64, 1, paged ? 1u << a.pages.page_log2 : uint32_t(kKeys)};
-  if (!make_tmap_bf16(&tmQ, a.q, 4, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_bf16(&tmK, a.k, 3, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_bf16(&tmV, a.v, 3, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!map_rows(&tmQ, a.q, a.seq.Tq, a.Hq, a.Hkv, D, p.tpt) || !map_keys(&tmK, a.k, krows, a.Hkv, D, box) ||
+      !map_keys(&tmV, a.v, krows, a.Hkv, D, box))
     return cudaErrorInvalidValue;
   const int64_t ctas = int64_t(p.nslots) * a.Hkv;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
