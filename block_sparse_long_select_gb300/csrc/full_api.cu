@@ -40,10 +40,12 @@ msa_status_t check_full_ws(void* ws, size_t ws_bytes, size_t need) {
 }
 
 inline msa_status_t launched(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
-// Prefill: tensor cores for bf16. With no key at all (Tk == 0) there is
-// nothing to map for TMA, and the row kernel writes the empty rows.
+// Prefill: tensor cores for bf16, CUDA cores for fp32. With no key at all
+// (Tk == 0) there is nothing to map for TMA: the rows are empty.
 cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
-  return a.dtype == MSA_BF16 && a.seq.Tk > 0 ? launch_full_prefill_tc(a, stream) : launch_full_rows(a, stream);
+  if (a.seq.Tk == 0)
+    return launch_full_zero(a.seq.cu_q, a.seq.B, a.seq.Tq, a.Hq, a.d, a.dtype, a.out, nullptr, a.lse, stream);
+  return a.dtype == MSA_BF16 ? launch_full_prefill_tc(a, stream) : launch_full_f32(a, stream);
 }
 
 inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale : 1.0f / sqrtf(float(d)); }
@@ -54,7 +56,7 @@ size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int 
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
   if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(B, Hq, Hkv, d) : 0;
   if (Nq < 0 || !rows_ok(Nq, Hq) || !rows_ok(op == MSA_OP_PAGED_APPEND ? Nq : Nk, Hkv)) return 0;
-  if (op == MSA_OP_FULL_BACKWARD && dtype == MSA_BF16) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
+  if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
   return kWsHeader;
 }
 
@@ -236,7 +238,7 @@ extern "C" msa_status_t msa_full_attn_backward(const void* q, const void* k, con
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  // tensor cores for bf16; without rows or keys there is nothing to map for TMA
-  if (dtype == MSA_BF16 && Tq > 0 && Tk > 0) return launched(launch_full_backward_tc(a, stream));
-  return launched(launch_full_rows_backward(a, stream));
+  if (Tq == 0) return launched(launch_full_zero(cu_k, B, Tk, Hkv, d, dtype, dk, dv, nullptr, stream));
+  if (Tk == 0) return launched(launch_full_zero(cu_q, B, Tq, Hq, d, dtype, dq, nullptr, nullptr, stream));
+  return launched(dtype == MSA_BF16 ? launch_full_backward_tc(a, stream) : launch_full_f32_backward(a, stream));
 }

@@ -33,40 +33,10 @@ struct FbParams {
   SeqMap seq;
   int Hq, Hkv, hpg, tpt, nslots;
   float scale, scale_log2;
-  const float2* rows;  // [Hkv][Tq][hpg]: lse * log2(e) (+inf where no key is seen), delta
+  const float2* rows;  // [Hkv][Tq][hpg]: lse in log2 units, delta (full_common.cu)
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* status;
 };
-
-// ---- per row: lse in log2 units and delta, laid out as the row tiles --------------
-template <int D>
-__global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restrict__ out, const uint4* __restrict__ dout,
-                                                            const float* __restrict__ lse, int Tq, int Hq, int hpg,
-                                                            float2* __restrict__ rows) {
-  constexpr int kLanes = D / 8;  // a row's 16-byte chunks
-  const int64_t x = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
-  const int c = threadIdx.x % kLanes;
-  const bool in = x < int64_t(Tq) * Hq;
-  float s = 0.f;
-  if (in) {
-    const uint4 a = out[x * kLanes + c], b = dout[x * kLanes + c];
-    const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
-    const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 fa = __bfloat1622float2(a2[i]), fb = __bfloat1622float2(b2[i]);
-      s = fmaf(fa.x, fb.x, fmaf(fa.y, fb.y, s));
-    }
-  }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (in && c == 0) {
-    const int64_t t = x / Hq;
-    const int h = int(x % Hq);
-    const float l = lse[x];
-    rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, s);
-  }
-}
 
 template <int D>
 struct FbSmem {
@@ -707,14 +677,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(full_bwd_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) ||
       (e = cudaFuncSetAttribute(full_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
     return e;
-  {
-    ProfScope pf("full_bwd_rows", stream);
-    const int64_t threads = int64_t(f.seq.Tq) * f.Hq * (D / 8);
-    full_bwd_rows_kernel<D><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(
-        static_cast<const uint4*>(f.out), static_cast<const uint4*>(a.dout), f.lse, f.seq.Tq, f.Hq, p.hpg,
-        const_cast<float2*>(p.rows));
-    if ((e = cudaGetLastError())) return e;
-  }
+  if ((e = launch_full_bwd_rows(a, stream))) return e;
   {
     ProfScope pf("full_bwd_dkv", stream);
     p.nslots = kslots;
@@ -728,8 +691,6 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
-
-size_t full_backward_ws_bytes(int Tq, int Hq) { return (size_t(Tq) * Hq * sizeof(float2) + 255) & ~size_t(255); }
 
 cudaError_t launch_full_backward_tc(const FullBwdArgs& a, cudaStream_t stream) {
   return a.f.d == 128 ? backward<128>(a, stream) : backward<64>(a, stream);

@@ -1,0 +1,81 @@
+// Full attention: what every element type shares. The rows' lse and delta for
+// the backward, and the outputs of calls without any key or any query row.
+#include "full_internal.cuh"
+
+namespace msa {
+namespace {
+
+// Per row: lse in log2 units (+inf where no key is seen, so that the row's
+// weights are 0) and delta = dout . out, laid out as the backward's row tiles,
+// [Hkv][Tq][hpg]. A thread per 16-byte chunk; bound by HBM (out and dout once).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restrict__ out, const uint4* __restrict__ dout,
+                                                            const float* __restrict__ lse, int Tq, int Hq, int hpg,
+                                                            float2* __restrict__ rows) {
+  constexpr int kPer = 16 / sizeof(T), kLanes = D / kPer;
+  const int64_t x = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  const int c = threadIdx.x % kLanes;
+  const bool in = x < int64_t(Tq) * Hq;
+  float s = 0.f;
+  if (in) {
+    const uint4 a = out[x * kLanes + c], b = dout[x * kLanes + c];
+    const T *ta = reinterpret_cast<const T*>(&a), *tb = reinterpret_cast<const T*>(&b);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s = fmaf(to_f(ta[i]), to_f(tb[i]), s);
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (in && c == 0) {
+    const int64_t t = x / Hq;
+    const int h = int(x % Hq);
+    const float l = lse[x];
+    rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] =
+        make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+  }
+}
+
+template <typename T, int D>
+cudaError_t bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
+  const FullArgs& f = a.f;
+  const int64_t threads = int64_t(f.seq.Tq) * f.Hq * (D * int(sizeof(T)) / 16);
+  ProfScope pf("full_bwd_rows", stream);
+  full_bwd_rows_kernel<T, D><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(
+      static_cast<const uint4*>(f.out), static_cast<const uint4*>(a.dout), f.lse, f.seq.Tq, f.Hq, f.Hq / f.Hkv,
+      reinterpret_cast<float2*>(static_cast<char*>(f.ws) + kWsHeader));
+  return cudaGetLastError();
+}
+
+// Zeroes every sequence's rows (one warp per row of row_bytes); lse, if given, becomes -inf.
+__global__ void __launch_bounds__(128) full_zero_kernel(const int32_t* __restrict__ cu, int B, int T, int row_bytes,
+                                                        uint4* __restrict__ a, uint4* __restrict__ b,
+                                                        float* __restrict__ lse, int heads) {
+  const int t = blockIdx.x * 4 + int(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= T || find_row_seq(cu, B, t) < 0) return;
+  for (int x = lane; x < row_bytes / 16; x += 32) {
+    const int64_t o = int64_t(t) * (row_bytes / 16) + x;
+    a[o] = make_uint4(0, 0, 0, 0);
+    if (b) b[o] = make_uint4(0, 0, 0, 0);
+  }
+  if (lse)
+    for (int x = lane; x < heads; x += 32) lse[int64_t(t) * heads + x] = -INFINITY;
+}
+
+}  // namespace
+
+size_t full_backward_ws_bytes(int Tq, int Hq) { return (size_t(Tq) * Hq * sizeof(float2) + 255) & ~size_t(255); }
+
+cudaError_t launch_full_bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
+  if (a.f.dtype == MSA_BF16)
+    return a.f.d == 128 ? bwd_rows<__nv_bfloat16, 128>(a, stream) : bwd_rows<__nv_bfloat16, 64>(a, stream);
+  return a.f.d == 128 ? bwd_rows<float, 128>(a, stream) : bwd_rows<float, 64>(a, stream);
+}
+
+cudaError_t launch_full_zero(const int32_t* cu, int B, int T, int heads, int d, int dtype, void* a, void* b, float* lse,
+                             cudaStream_t stream) {
+  ProfScope pf("full_zero", stream);
+  full_zero_kernel<<<(T + 3) / 4, 128, 0, stream>>>(cu, B, T, heads * d * (dtype == MSA_BF16 ? 2 : 4),
+                                                    static_cast<uint4*>(a), static_cast<uint4*>(b), lse, heads);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

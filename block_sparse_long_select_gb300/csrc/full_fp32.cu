@@ -1,0 +1,459 @@
+// Full attention in fp32 on CUDA cores: forward over packed or paged keys, and
+// the backward over packed ones (formulas at full_prefill_tc.cu and
+// full_backward_tc.cu).
+//
+// Bound: FMAs (the tensor cores have no fp32 products; tf32 would keep 11 bits).
+// Every kernel is the same small matrix engine: a CTA of 128 threads keeps a
+// tile of 32 rows in shared memory (queries x group heads; in dkv, keys) and
+// streams 64 rows of the other side past it. A thread computes 4 x 4 dot
+// products, 4 LDS.128 of either side for 64 FMAs; the 32 x 64 results go
+// through shared memory to the second product, where it owns 4 rows x D / 16
+// columns. 32 rows and not 64 because several small CTAs per SM hide each
+// other's barriers, and short calls need the number of CTAs. Rows that belong
+// to no pair arrive as zeros.
+#include "full_internal.cuh"
+#include "tc_utils.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kF32Threads = 128, kA = 32, kB = 64;  // resident rows, streamed rows
+constexpr int kPitch = kB + 4;                      // floats of a row of the 32 x 64 results
+constexpr float kF32Log2e = 1.4426950408889634f, kF32Ln2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2s(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16f(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit_f() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait_f() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+// 16-byte chunk c of row r; chunks are exchanged within 128 bytes by the row's
+// low bits, so reads down a column are free of bank conflicts.
+template <int D>
+__device__ __forceinline__ uint32_t at(uint32_t base, int r, int c) {
+  return base + uint32_t(r * D * 4) + (uint32_t(c ^ (r & 7)) << 4);
+}
+
+// Copies NR rows of D floats into a tile: row(r) is a row's address, or null for zeros.
+template <int D, int NR, typename F>
+__device__ __forceinline__ void load_tile(uint32_t dst, const float* any, F row) {
+  constexpr int kC = D / 4, kStep = kF32Threads / kC;
+  const int c = threadIdx.x % kC;
+#pragma unroll 4
+  for (int r = threadIdx.x / kC; r < NR; r += kStep) {
+    const float* src = row(r);
+    cp16f(at<D>(dst, r, c), src ? src + c * 4 : any, src != nullptr);
+  }
+}
+
+// acc[i][k] = A row (4 ty + i) . B row (tx + 16 k)
+template <int D>
+__device__ __forceinline__ void dots(uint32_t a, uint32_t b, float (&acc)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D / 4; ++c) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lds4(at<D>(a, ty * 4 + i, c));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = lds4(at<D>(b, tx + 16 * k, c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[i][k] = fmaf(x[i].x, y[k].x, acc[i][k]);
+        acc[i][k] = fmaf(x[i].y, y[k].y, acc[i][k]);
+        acc[i][k] = fmaf(x[i].z, y[k].z, acc[i][k]);
+        acc[i][k] = fmaf(x[i].w, y[k].w, acc[i][k]);
+      }
+  }
+}
+// The thread's 4 x 4 results into the 32 x 64 matrix.
+__device__ __forceinline__ void put(uint32_t m, const float (&v)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(m + ((ty * 4 + i) * kPitch + tx + 16 * k) * 4), "f"(v[i][k]) : "memory");
+}
+// acc[i][..] += sum over the 64 streamed rows of m[4 ty + i][row] * row's columns;
+// the thread's columns are the 16-byte chunks tx, tx + 16, ...
+template <int D>
+__device__ __forceinline__ void sums(uint32_t m, uint32_t b, float (&acc)[4][D / 16]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int j = 0; j < kB; j += 4) {
+    float w[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = lds4(m + ((ty * 4 + i) * kPitch + j) * 4);
+      w[i][0] = f.x, w[i][1] = f.y, w[i][2] = f.z, w[i][3] = f.w;
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 f = lds4(at<D>(b, j + y, tx + 16 * c));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][4 * c] = fmaf(w[i][y], f.x, acc[i][4 * c]);
+          acc[i][4 * c + 1] = fmaf(w[i][y], f.y, acc[i][4 * c + 1]);
+          acc[i][4 * c + 2] = fmaf(w[i][y], f.z, acc[i][4 * c + 2]);
+          acc[i][4 * c + 3] = fmaf(w[i][y], f.w, acc[i][4 * c + 3]);
+        }
+      }
+  }
+}
+__device__ __forceinline__ float row_max(float x) {  // over the 16 threads of a row
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+template <int D>
+__device__ __forceinline__ void store_rows(float* dst, const float (&acc)[D / 16], float mul) {
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    reinterpret_cast<float4*>(dst)[tx + 16 * c] =
+        make_float4(acc[4 * c] * mul, acc[4 * c + 1] * mul, acc[4 * c + 2] * mul, acc[4 * c + 3] * mul);
+}
+
+struct F32Params {
+  const float *q, *k, *v, *dout;
+  SeqMap seq;
+  PageMap pages;
+  int Hq, Hkv, hpg, nslots;
+  float scale, scale_log2;
+  const float2* rows;  // [Hkv][Tq][hpg]: lse in log2 units, delta (full_common.cu)
+  float *out, *lse, *dq, *dk, *dv;
+  uint32_t* status;
+};
+
+// Row x (token x / hpg, head x % hpg of group g) of a sequence in a [Tq, Hq] array.
+__device__ __forceinline__ int64_t row_of(const F32Params& p, const SeqSpan& s, int g, int x) {
+  return (int64_t(s.q0) + x / p.hpg) * p.Hq + g * p.hpg + x % p.hpg;
+}
+
+// ---------------------------------------------------------------------------------
+// forward: 32 rows; smem Q | K | V | P
+// ---------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p) {
+  extern __shared__ __align__(128) uint8_t f32_smem[];
+  const uint32_t sq = tc::smem_u32(f32_smem), sk = sq + kA * D * 4, sv = sk + kB * D * 4, sp = sv + kB * D * 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int g = blockIdx.x % p.Hkv;
+  int tile;
+  const int b =
+      find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - int(blockIdx.x / p.Hkv), tile, p.hpg);  // late rows first
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.seq, b);
+  if (!s.rows_ok) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    return;
+  }
+  const int x0 = tile * kA, x1 = min(x0 + kA, s.Lq * p.hpg);
+  const int32_t* table = p.pages.table ? p.pages.table + int64_t(b) * p.pages.max_pages : nullptr;
+  bool bad = !s.ok;
+  if (!bad && table) {  // every page of the sequence in range, for all its rows alike
+    const int np = (s.Lk + (1 << p.pages.page_log2) - 1) >> p.pages.page_log2;
+    for (int x = threadIdx.x; x < np; x += kF32Threads) bad |= table[x] < 0 || table[x] >= p.pages.num_pages;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+  const int n = bad ? 0 : (max(s.Lk - s.Lq + (x1 - 1) / p.hpg + 1, 0) + kB - 1) / kB;
+  auto key = [&](const float* base, int j) -> const float* {
+    if (j >= s.Lk) return nullptr;
+    const int64_t row = table ? (int64_t(table[j >> p.pages.page_log2]) << p.pages.page_log2) +
+                                    (j & ((1 << p.pages.page_log2) - 1))
+                              : int64_t(s.k0) + j;
+    return base + (row * p.Hkv + g) * D;
+  };
+  load_tile<D, kA>(sq, p.q, [&](int r) { return x0 + r < x1 ? p.q + row_of(p, s, g, x0 + r) * D : nullptr; });
+  if (n > 0) load_tile<D, kB>(sk, p.k, [&](int r) { return key(p.k, r); });
+  cp_commit_f();
+  if (n > 0) load_tile<D, kB>(sv, p.v, [&](int r) { return key(p.v, r); });
+  cp_commit_f();
+  int vis[4];  // keys the thread's rows see
+  float m[4], l[4], acc[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    vis[i] = s.Lk - s.Lq + (x0 + ty * 4 + i) / p.hpg + 1;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+  }
+  for (int j = 0; j < n; ++j) {
+    cp_wait_f<1>();
+    __syncthreads();
+    float sc[4][4];
+    dots<D>(sq, sk, sc);
+    __syncthreads();  // K is read
+    if (j + 1 < n) load_tile<D, kB>(sk, p.k, [&](int r) { return key(p.k, (j + 1) * kB + r); });
+    cp_commit_f();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sc[i][k] = j * kB + tx + 16 * k < vis[i] ? sc[i][k] * p.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, sc[i][k]);
+      }
+      const float mn = fmaxf(m[i], row_max(mx));
+      const float a = m[i] == mn ? 1.f : ex2s(m[i] - mn), z = mn == -INFINITY ? 0.f : mn;
+      m[i] = mn;
+      l[i] *= a;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) acc[i][c] *= a;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sc[i][k] = ex2s(sc[i][k] - z);
+        l[i] += sc[i][k];
+      }
+    }
+    put(sp, sc);
+    cp_wait_f<1>();
+    __syncthreads();
+    sums<D>(sp, sv, acc);
+    __syncthreads();  // V and P are read
+    if (j + 1 < n) load_tile<D, kB>(sv, p.v, [&](int r) { return key(p.v, (j + 1) * kB + r); });
+    cp_commit_f();
+  }
+  cp_wait_f<0>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float den = row_sum(l[i]);
+    const int x = x0 + ty * 4 + i;
+    if (x >= x1) continue;
+    const int64_t row = row_of(p, s, g, x);
+    const bool some = den > 0.f || den != den;
+    store_rows<D>(p.out + row * D, acc[i], some ? 1.f / den : 0.f);
+    if (p.lse && tx == 0) p.lse[row] = some ? (m[i] + log2f(den)) * kF32Ln2 : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// dq: 32 rows; smem Q | dO | K | V | dS
+// ---------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Params p) {
+  extern __shared__ __align__(128) uint8_t f32_smem[];
+  const uint32_t sq = tc::smem_u32(f32_smem), so = sq + kA * D * 4, sk = so + kA * D * 4, sv = sk + kB * D * 4,
+                 sp = sv + kB * D * 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int g = blockIdx.x % p.Hkv;
+  int tile;
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - int(blockIdx.x / p.Hkv), tile, p.hpg);
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.seq, b);
+  if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+  if (!s.rows_ok) return;
+  const int x0 = tile * kA, x1 = min(x0 + kA, s.Lq * p.hpg);
+  const int n = s.ok ? (max(s.Lk - s.Lq + (x1 - 1) / p.hpg + 1, 0) + kB - 1) / kB : 0;
+  auto key = [&](const float* base, int j) -> const float* {
+    return j < s.Lk ? base + ((int64_t(s.k0) + j) * p.Hkv + g) * D : nullptr;
+  };
+  load_tile<D, kA>(sq, p.q, [&](int r) { return x0 + r < x1 ? p.q + row_of(p, s, g, x0 + r) * D : nullptr; });
+  load_tile<D, kA>(so, p.q, [&](int r) { return x0 + r < x1 ? p.dout + row_of(p, s, g, x0 + r) * D : nullptr; });
+  int vis[4];
+  float2 rd[4];
+  float acc[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = x0 + ty * 4 + i;
+    vis[i] = s.Lk - s.Lq + x / p.hpg + 1;
+    rd[i] = x < x1 ? p.rows[(int64_t(g) * p.seq.Tq + s.q0) * p.hpg + x] : make_float2(INFINITY, 0.f);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+  }
+  for (int j = 0; j < n; ++j) {
+    load_tile<D, kB>(sk, p.k, [&](int r) { return key(p.k, j * kB + r); });
+    load_tile<D, kB>(sv, p.k, [&](int r) { return key(p.v, j * kB + r); });
+    cp_commit_f();
+    cp_wait_f<0>();
+    __syncthreads();
+    float sc[4][4], dp[4][4];
+    dots<D>(sq, sk, sc);
+    dots<D>(so, sv, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float pr = ex2s(fmaf(sc[i][k], p.scale_log2, -rd[i].x));
+        sc[i][k] = j * kB + tx + 16 * k < vis[i] ? pr * (dp[i][k] - rd[i].y) : 0.f;
+      }
+    put(sp, sc);
+    __syncthreads();
+    sums<D>(sp, sk, acc);
+    __syncthreads();  // K, V and dS are read
+  }
+  cp_commit_f();
+  cp_wait_f<0>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = x0 + ty * 4 + i;
+    if (x < x1) store_rows<D>(p.dq + row_of(p, s, g, x) * D, acc[i], p.scale);
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// dk, dv: 32 keys; smem K | V | Q | dO | P^T | dS^T | lse, delta
+// ---------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Params p) {
+  extern __shared__ __align__(128) uint8_t f32_smem[];
+  const uint32_t sk = tc::smem_u32(f32_smem), sv = sk + kA * D * 4, sq = sv + kA * D * 4, so = sq + kB * D * 4,
+                 sp = so + kB * D * 4, sd = sp + kA * kPitch * 4;
+  float2* srow = reinterpret_cast<float2*>(f32_smem + (2 * kA + 2 * kB) * D * 4 + 2 * kA * kPitch * 4);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int g = blockIdx.x % p.Hkv;
+  int tile;
+  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kA, int(blockIdx.x / p.Hkv), tile);  // early keys: most rows
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.seq, b);
+  if (!s.ok) {
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    return;
+  }
+  const int j0 = tile * kA, off = s.Lk - s.Lq, xn = s.Lq * p.hpg;
+  auto key = [&](const float* base, int j) -> const float* {
+    return j < s.Lk ? base + ((int64_t(s.k0) + j) * p.Hkv + g) * D : nullptr;
+  };
+  load_tile<D, kA>(sk, p.k, [&](int r) { return key(p.k, j0 + r); });
+  load_tile<D, kA>(sv, p.k, [&](int r) { return key(p.v, j0 + r); });
+  int from[4];  // first row that sees the thread's keys
+  float ak[4][D / 16], av[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    from[i] = max(j0 + ty * 4 + i - off, 0) * p.hpg;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+  }
+  for (int x0 = max(j0 - off, 0) * p.hpg / kB * kB; x0 < xn; x0 += kB) {
+    load_tile<D, kB>(sq, p.k, [&](int r) { return x0 + r < xn ? p.q + row_of(p, s, g, x0 + r) * D : nullptr; });
+    load_tile<D, kB>(so, p.k, [&](int r) { return x0 + r < xn ? p.dout + row_of(p, s, g, x0 + r) * D : nullptr; });
+    cp_commit_f();
+    if (threadIdx.x < kB)
+      srow[threadIdx.x] = x0 + int(threadIdx.x) < xn
+                              ? p.rows[(int64_t(g) * p.seq.Tq + s.q0) * p.hpg + x0 + threadIdx.x]
+                              : make_float2(INFINITY, 0.f);
+    cp_wait_f<0>();
+    __syncthreads();
+    float sc[4][4], dp[4][4];
+    dots<D>(sk, sq, sc);
+    dots<D>(sv, so, dp);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 rd = srow[tx + 16 * k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float pr = ex2s(fmaf(sc[i][k], p.scale_log2, -rd.x));
+        sc[i][k] = x0 + tx + 16 * k >= from[i] ? pr : 0.f;
+        dp[i][k] = sc[i][k] * (dp[i][k] - rd.y);
+      }
+    }
+    put(sp, sc);
+    put(sd, dp);
+    __syncthreads();
+    sums<D>(sp, so, av);
+    sums<D>(sd, sq, ak);
+    __syncthreads();
+  }
+  cp_commit_f();
+  cp_wait_f<0>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = j0 + ty * 4 + i;
+    if (j >= s.Lk) continue;
+    const int64_t row = ((int64_t(s.k0) + j) * p.Hkv + g) * D;
+    store_rows<D>(p.dk + row, ak[i], p.scale);
+    store_rows<D>(p.dv + row, av[i], 1.f);
+  }
+}
+
+F32Params params(const FullArgs& a) {
+  F32Params p{};
+  p.q = static_cast<const float*>(a.q);
+  p.k = static_cast<const float*>(a.k);
+  p.v = static_cast<const float*>(a.v);
+  p.seq = a.seq;
+  p.pages = a.pages;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.hpg = a.Hq / a.Hkv;
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kF32Log2e;
+  p.status = &static_cast<WsHeader*>(a.ws)->status;
+  return p;
+}
+
+template <typename K>
+cudaError_t run(const char* name, K kern, F32Params p, int slots, int bytes, cudaStream_t stream) {
+  const int64_t ctas = int64_t(slots) * p.Hkv;
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  ProfScope pf(name, stream);
+  p.nslots = slots;
+  kern<<<unsigned(ctas), kF32Threads, bytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t forward(const FullArgs& a, cudaStream_t stream) {
+  F32Params p = params(a);
+  p.out = static_cast<float*>(a.out);
+  p.lse = a.lse;
+  return run("full_f32", full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B,
+             (kA + 2 * kB) * D * 4 + kA * kPitch * 4, stream);
+}
+template <int D>
+cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
+  const FullArgs& f = a.f;
+  F32Params p = params(f);
+  p.dout = static_cast<const float*>(a.dout);
+  p.rows = reinterpret_cast<float2*>(static_cast<char*>(f.ws) + kWsHeader);
+  p.dq = static_cast<float*>(a.dq);
+  p.dk = static_cast<float*>(a.dk);
+  p.dv = static_cast<float*>(a.dv);
+  if (cudaError_t e = launch_full_bwd_rows(a, stream)) return e;
+  constexpr int m = kA * kPitch * 4;
+  if (cudaError_t e = run("full_f32_dkv", full_f32_dkv_kernel<D>, p, f.seq.Tk / kA + f.seq.B,
+                          (2 * kA + 2 * kB) * D * 4 + 2 * m + kB * 8, stream))
+    return e;
+  return run("full_f32_dq", full_f32_dq_kernel<D>, p, int(int64_t(f.seq.Tq) * p.hpg / kA) + f.seq.B,
+             (2 * kA + 2 * kB) * D * 4 + m, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_full_f32(const FullArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? forward<128>(a, stream) : forward<64>(a, stream);
+}
+cudaError_t launch_full_f32_backward(const FullBwdArgs& a, cudaStream_t stream) {
+  return a.f.d == 128 ? backward<128>(a, stream) : backward<64>(a, stream);
+}
+
+}  // namespace msa

@@ -77,17 +77,21 @@ __device__ __forceinline__ int find_row_seq(const int32_t* cu, int B, int t) {
   return b < B && cu[b] <= t && t < cu[b + 1] ? b : -1;
 }
 
-// Tiles of `tt` rows that start at each sequence's first row, in slots:
-// tile j of sequence b has slot cu[b] / tt + b + j. Slots are unique (a
-// sequence of n rows needs at most ceil(n / tt) of them and the + b leaves
-// room for its ragged end), so T / tt + B slots cover every tile and a slot's
-// tile is found by one search; some slots hold none. Returns the sequence
-// of slot `i` and its tile (b = -1: none). Whole warp.
-__device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, int i, int& tile) {
-  // largest b with cu[b] / tt + b <= i
-  const int b = warp_count_true(B, [&](int x) { return x < B && cu[x] / tt + x <= i; });
-  tile = i - (cu[b] / tt + b);
-  return tile >= 0 && tile < (cu[b + 1] - cu[b] + tt - 1) / tt ? b : -1;
+// Tiles of `tt` rows that start at each sequence's first row, in slots: a
+// sequence's token count times `mul` rows, cut into tiles. Tile j of sequence b
+// has slot cu[b] * mul / tt + b + j. Slots are unique (a sequence of n rows
+// needs at most ceil(n / tt) of them and the + b leaves room for its ragged
+// end), so T * mul / tt + B slots cover every tile and a slot's tile is found
+// by one search; some slots hold none. Returns the sequence of slot `i` and
+// its tile (-1: none). Whole warp. cu[x] is not checked here: out of range
+// values give a tile whose sequence seq_span refuses.
+__device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, int i, int& tile, int mul = 1) {
+  auto slot0 = [&](int x) { return int64_t(cu[x]) * mul / tt + x; };
+  // largest b whose first slot is at most i
+  const int b = warp_count_true(B, [&](int x) { return x < B && slot0(x) <= i; });
+  const int64_t j = i - slot0(b);
+  tile = int(j);
+  return j >= 0 && j < (int64_t(cu[b + 1] - cu[b]) * mul + tt - 1) / tt ? b : -1;
 }
 
 // ---- launchers ---------------------------------------------------------------
@@ -107,10 +111,15 @@ struct FullBwdArgs {
   void *dq, *dk, *dv;
 };
 size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d);  // behind the header
-size_t full_backward_ws_bytes(int Tq, int Hq);  // bf16, behind the header
-// CUDA cores, any dtype
-cudaError_t launch_full_rows(const FullArgs& a, cudaStream_t stream);
-cudaError_t launch_full_rows_backward(const FullBwdArgs& a, cudaStream_t stream);
+size_t full_backward_ws_bytes(int Tq, int Hq);  // behind the header
+// fp32 prefill and backward
+cudaError_t launch_full_f32(const FullArgs& a, cudaStream_t stream);
+cudaError_t launch_full_f32_backward(const FullBwdArgs& a, cudaStream_t stream);
+// the backward's per-row lse and delta, into the workspace behind the header
+cudaError_t launch_full_bwd_rows(const FullBwdArgs& a, cudaStream_t stream);
+// every sequence's rows of a (and b, if given) zero, lse (if given) -inf
+cudaError_t launch_full_zero(const int32_t* cu, int B, int T, int heads, int d, int dtype, void* a, void* b, float* lse,
+                             cudaStream_t stream);
 // decode over pages, any dtype
 cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream);
 // tcgen05 prefill (bf16); needs Tk > 0
