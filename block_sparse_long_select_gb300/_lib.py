@@ -319,62 +319,44 @@ def msa_sparse_attn_backward(q, k, v, out, dout, lse, sel, q_offset, kv_len, Bs,
 
 
 # ---- full attention and paged caches -----------------------------------------
-def _check_like(ref, **ts):
-    """Contiguous CUDA tensors of ``ref``'s dtype and device, of the given shapes
-    (name=(tensor, shape); None is skipped): the library reads and writes them
-    through raw pointers."""
-    for name, (t, shape) in ts.items():
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.dtype != ref.dtype or t.device != ref.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, of dtype {ref.dtype} on {ref.device}")
+# These calls serve single tokens too, where the host's time counts: a tensor's
+# checks are one call each, and streams and devices are only switched if needed.
+def _fits(t, dtype, dev, shape) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
 
 
-def _check_typed(ref, dtype, **ts):
-    """The same for tensors of another dtype (offsets, lengths, tables, lse)."""
-    for name, (t, shape) in ts.items():
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, of dtype {dtype} on {ref.device}")
+def _need(name, t, dtype, dev, shape):
+    """Raises unless ``t`` is contiguous, of this dtype, device and shape: the
+    library reads and writes it through a raw pointer."""
+    if t is None or not _fits(t, dtype, dev, shape):
+        got = "None" if t is None else f"{t.dtype}, {tuple(t.shape)} on {t.device}"
+        raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)} on cuda:{dev}; got {got}")
 
 
 def _rows(name, t, dims=3):
-    """A packed-row tensor [rows, heads, d] (or a cache, dims 4): its shape after the checks every call makes."""
-    if t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+    """Shape of a packed-row tensor [rows, heads, d] (or a cache, dims 4)."""
+    if not t.is_cuda or t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor with {dims} dimensions")
     return t.shape
 
 
-class _on:
-    """Makes ``stream`` (and its device) current, so that what a wrapper
-    allocates belongs to it and launches go to the tensors' device; nothing to
-    do where both are current already."""
+def _elsewhere(stream, dev):
+    """None if a call on ``stream`` (None: the current one) for tensors on device
+    ``dev`` can go ahead; else the context that makes that stream and device
+    current, so that what the call allocates belongs to the stream as well."""
+    import torch
 
-    __slots__ = ("ctx", "ptr")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        return torch.cuda.stream(stream)
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
-    def __init__(self, stream, device):
-        import torch
 
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-            self.ptr = stream.cuda_stream
-        else:
-            self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-            self.ptr = torch.cuda.current_stream(device).cuda_stream
+def _raw_stream(dev):
+    import torch
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.ptr
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _addr(t):
@@ -383,8 +365,8 @@ def _addr(t):
 
 def _full_ws(ws, ref, op, B, Nq, Nk, Hkv, Hq, d, dt):
     if ws is None:
-        ws = workspace(msa_workspace_size(op, B, Nq, Nk, Hkv, Hq, d, 0, 0, 0, dt), ref.device)
-    elif ws.device != ref.device or not ws.is_contiguous():
+        return workspace(msa_workspace_size(op, B, Nq, Nk, Hkv, Hq, d, 0, 0, 0, dt), ref.device)
+    if ws.get_device() != ref.get_device() or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous on {ref.device}")
     return ws
 
@@ -399,34 +381,44 @@ def msa_paged_append(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache,
     without q); ``q_out=q`` rotates in place."""
     import torch
 
-    T, Hkv, d = _rows("k_new", k_new)
+    shape = _rows("k_new", k_new)
+    T, Hkv, d = shape
+    dev, dtype, i32 = k_new.get_device(), k_new.dtype, torch.int32
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_paged_append(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache, v_cache, interleaved,
+                                    q_out, ws)
     num_pages, page_size = _rows("k_cache", k_cache, 4)[:2]
     B, max_pages = page_table.shape
+    Hq = Hkv
     if q is not None:
         Hq = _rows("q", q)[1]
-        _check_like(k_new, q=(q, (T, Hq, d)), q_out=(q_out, (T, Hq, d)))
-    else:
-        Hq = Hkv
-        if q_out is not None:
-            raise ValueError("q_out needs q")
-    _check_like(k_new, v_new=(v_new, (T, Hkv, d)), k_cache=(k_cache, (num_pages, page_size, Hkv, d)),
-                v_cache=(v_cache, (num_pages, page_size, Hkv, d)))
-    _check_typed(k_new, torch.int32, cu_new=(cu_new, (B + 1,)), kv_len=(kv_len, (B,)),
-                 page_table=(page_table, (B, max_pages)))
+        _need("q", q, dtype, dev, (T, Hq, d))
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _need("q_out", q_out, dtype, dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _need("v_new", v_new, dtype, dev, shape)
+    _need("k_cache", k_cache, dtype, dev, (num_pages, page_size, Hkv, d))
+    _need("v_cache", v_cache, dtype, dev, k_cache.shape)
+    if cu_new is not None:
+        _need("cu_new", cu_new, i32, dev, (B + 1,))
+    _need("kv_len", kv_len, i32, dev, (B,))
+    _need("page_table", page_table, i32, dev, (B, max_pages))
     max_pos = half = 0
     if rope is not None:
-        max_pos, half = rope.shape[:2]
-        _check_typed(k_new, torch.float32, rope=(rope, (max_pos, half, 2)))
+        max_pos, half, _ = rope.shape
+        _need("rope", rope, torch.float32, dev, (max_pos, half, 2))
     dt = _dtype_code(k_new)
-    with _on(stream, k_new.device) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty_like(q)
-        ws = _full_ws(ws, k_new, MSA_OP_PAGED_APPEND, B, T, 0, Hkv, Hq, d, dt)
-        code = load_library().msa_paged_append(_addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(rope),
-                                               _addr(cu_new), kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, Hkv,
-                                               d, 2 * half, int(interleaved), max_pos, num_pages, page_size,
-                                               max_pages, dt, _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-                                               ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    ws = _full_ws(ws, k_new, MSA_OP_PAGED_APPEND, B, T, 0, Hkv, Hq, d, dt)
+    code = load_library().msa_paged_append(_addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(rope), _addr(cu_new),
+                                           kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, Hkv, d, 2 * half,
+                                           interleaved, max_pos, num_pages, page_size, max_pages, dt, _addr(q_out),
+                                           k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                           _raw_stream(dev))
     _check(code, "msa_paged_append")
     return q_out
 
@@ -437,22 +429,31 @@ def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out
     q [B,Hq,d], caches [num_pages, page_size, Hkv, d] -> out [B,Hq,d]."""
     import torch
 
-    B, Hq, d = _rows("q", q)
+    shape = _rows("q", q)
+    B, Hq, d = shape
+    dev, dtype = q.get_device(), q.dtype
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale, out, lse, ws)
     num_pages, page_size, Hkv, _ = _rows("k_cache", k_cache, 4)
     max_pages = page_table.shape[1]
-    _check_like(q, k_cache=(k_cache, (num_pages, page_size, Hkv, d)), v_cache=(v_cache, k_cache.shape),
-                out=(out, q.shape))
-    _check_typed(q, torch.int32, kv_len=(kv_len, (B,)), page_table=(page_table, (B, max_pages)))
-    _check_typed(q, torch.float32, lse=(lse, (B, Hq)))
+    _need("k_cache", k_cache, dtype, dev, (num_pages, page_size, Hkv, d))
+    _need("v_cache", v_cache, dtype, dev, k_cache.shape)
+    _need("kv_len", kv_len, torch.int32, dev, (B,))
+    _need("page_table", page_table, torch.int32, dev, (B, max_pages))
+    if lse is not None:
+        _need("lse", lse, torch.float32, dev, (B, Hq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, dtype, dev, shape)
     dt = _dtype_code(q)
-    with _on(stream, q.device) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        ws = _full_ws(ws, q, MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv, Hq, d, dt)
-        code = load_library().msa_full_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                                   page_table.data_ptr(), kv_len.data_ptr(), B, Hq, Hkv, d, num_pages,
-                                                   page_size, max_pages, float(scale), dt, out.data_ptr(),
-                                                   _addr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    ws = _full_ws(ws, q, MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                               page_table.data_ptr(), kv_len.data_ptr(), B, Hq, Hkv, d, num_pages,
+                                               page_size, max_pages, scale, dt, out.data_ptr(), _addr(lse),
+                                               ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     _check(code, "msa_full_attn_decode")
     return out
 
@@ -462,21 +463,30 @@ def msa_full_attn_prefill(q, k, v, cu_q, cu_k, scale=0.0, out=None, lse=None, ws
     k, v [Tk,Hkv,d], cu_q, cu_k [B+1] int32 -> out [Tq,Hq,d]."""
     import torch
 
-    Tq, Hq, d = _rows("q", q)
+    shape = _rows("q", q)
+    Tq, Hq, d = shape
+    dev, dtype = q.get_device(), q.dtype
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_prefill(q, k, v, cu_q, cu_k, scale, out, lse, ws)
     Tk, Hkv, _ = _rows("k", k)
     B = cu_q.shape[0] - 1
-    _check_like(q, k=(k, (Tk, Hkv, d)), v=(v, (Tk, Hkv, d)), out=(out, q.shape))
-    _check_typed(q, torch.int32, cu_q=(cu_q, (B + 1,)), cu_k=(cu_k, (B + 1,)))
-    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    _need("k", k, dtype, dev, (Tk, Hkv, d))
+    _need("v", v, dtype, dev, k.shape)
+    _need("cu_q", cu_q, torch.int32, dev, (B + 1,))
+    _need("cu_k", cu_k, torch.int32, dev, (B + 1,))
+    if lse is not None:
+        _need("lse", lse, torch.float32, dev, (Tq, Hq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, dtype, dev, shape)
     dt = _dtype_code(q)
-    with _on(stream, q.device) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, Tk, Hkv, Hq, d, dt)
-        code = load_library().msa_full_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
-                                                    cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, d, float(scale), dt,
-                                                    out.data_ptr(), _addr(lse), ws.data_ptr(),
-                                                    ws.numel() * ws.element_size(), s)
+    ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, Tk, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+                                                cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, d, scale, dt, out.data_ptr(),
+                                                _addr(lse), ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     _check(code, "msa_full_attn_prefill")
     return out
 
@@ -487,24 +497,33 @@ def msa_full_attn_prefill_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, s
     (see include/msa.h): q [Tq,Hq,d], cu_q [B+1], page_table [B, max_pages] -> out [Tq,Hq,d]."""
     import torch
 
-    Tq, Hq, d = _rows("q", q)
+    shape = _rows("q", q)
+    Tq, Hq, d = shape
+    dev, dtype = q.get_device(), q.dtype
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_prefill_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, scale, out, lse, ws)
     num_pages, page_size, Hkv, _ = _rows("k_cache", k_cache, 4)
     B, max_pages = page_table.shape
-    _check_like(q, k_cache=(k_cache, (num_pages, page_size, Hkv, d)), v_cache=(v_cache, k_cache.shape),
-                out=(out, q.shape))
-    _check_typed(q, torch.int32, kv_len=(kv_len, (B,)), cu_q=(cu_q, (B + 1,)),
-                 page_table=(page_table, (B, max_pages)))
-    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    _need("k_cache", k_cache, dtype, dev, (num_pages, page_size, Hkv, d))
+    _need("v_cache", v_cache, dtype, dev, k_cache.shape)
+    _need("kv_len", kv_len, torch.int32, dev, (B,))
+    _need("cu_q", cu_q, torch.int32, dev, (B + 1,))
+    _need("page_table", page_table, torch.int32, dev, (B, max_pages))
+    if lse is not None:
+        _need("lse", lse, torch.float32, dev, (Tq, Hq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, dtype, dev, shape)
     dt = _dtype_code(q)
-    with _on(stream, q.device) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, max_pages * page_size, Hkv, Hq, d, dt)
-        code = load_library().msa_full_attn_prefill_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                                          page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
-                                                          B, Tq, Hq, Hkv, d, num_pages, page_size, max_pages,
-                                                          float(scale), dt, out.data_ptr(), _addr(lse),
-                                                          ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    ws = _full_ws(ws, q, MSA_OP_FULL_PREFILL, B, Tq, max_pages * page_size, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_prefill_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                      page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), B, Tq,
+                                                      Hq, Hkv, d, num_pages, page_size, max_pages, scale, dt,
+                                                      out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes,
+                                                      _raw_stream(dev))
     _check(code, "msa_full_attn_prefill_paged")
     return out
 
@@ -515,23 +534,37 @@ def msa_full_attn_backward(q, k, v, out, dout, lse, cu_q, cu_k, dq=None, dk=None
     its lse [Tq,Hq] and the output gradient ``dout``. Returns (dq, dk, dv)."""
     import torch
 
-    Tq, Hq, d = _rows("q", q)
-    Tk, Hkv, _ = _rows("k", k)
+    shape = _rows("q", q)
+    Tq, Hq, d = shape
+    dev, dtype = q.get_device(), q.dtype
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_backward(q, k, v, out, dout, lse, cu_q, cu_k, dq, dk, dv, scale, ws)
+    kshape = _rows("k", k)
+    Tk, Hkv, _ = kshape
     B = cu_q.shape[0] - 1
-    _check_like(q, k=(k, (Tk, Hkv, d)), v=(v, (Tk, Hkv, d)), out=(out, q.shape), dout=(dout, q.shape),
-                dq=(dq, q.shape), dk=(dk, k.shape), dv=(dv, k.shape))
-    _check_typed(q, torch.int32, cu_q=(cu_q, (B + 1,)), cu_k=(cu_k, (B + 1,)))
-    _check_typed(q, torch.float32, lse=(lse, (Tq, Hq)))
+    _need("k", k, dtype, dev, (Tk, Hkv, d))
+    _need("v", v, dtype, dev, kshape)
+    _need("out", out, dtype, dev, shape)
+    _need("dout", dout, dtype, dev, shape)
+    if dq is not None:
+        _need("dq", dq, dtype, dev, shape)
+    if dk is not None:
+        _need("dk", dk, dtype, dev, kshape)
+    if dv is not None:
+        _need("dv", dv, dtype, dev, kshape)
+    _need("cu_q", cu_q, torch.int32, dev, (B + 1,))
+    _need("cu_k", cu_k, torch.int32, dev, (B + 1,))
+    _need("lse", lse, torch.float32, dev, (Tq, Hq))
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     dt = _dtype_code(q)
-    with _on(stream, q.device) as s:
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        ws = _full_ws(ws, q, MSA_OP_FULL_BACKWARD, B, Tq, Tk, Hkv, Hq, d, dt)
-        code = load_library().msa_full_attn_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                                     dout.data_ptr(), lse.data_ptr(), cu_q.data_ptr(),
-                                                     cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, d, float(scale), dt,
-                                                     dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
-                                                     ws.numel() * ws.element_size(), s)
+    ws = _full_ws(ws, q, MSA_OP_FULL_BACKWARD, B, Tq, Tk, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                                 dout.data_ptr(), lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), B,
+                                                 Tq, Tk, Hq, Hkv, d, scale, dt, dq.data_ptr(), dk.data_ptr(),
+                                                 dv.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     _check(code, "msa_full_attn_backward")
     return dq, dk, dv

@@ -94,12 +94,13 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row_bytes, int r
 // ---- a warp's state: bf16 ------------------------------------------------------
 // O^T (head dims along M) and the scores share the column = head layout: lane
 // (gq = lane / 4, tq = lane % 4) holds heads 2 tq and 2 tq + 1 of each tile of 8.
-template <typename T, int D, int HN>
+template <typename T, int D, int H>  // H: most heads of an item
 struct Core;
 
-template <int D, int HN>
-struct Core<__nv_bfloat16, D, HN> {
+template <int D, int H>
+struct Core<__nv_bfloat16, D, H> {
   using T = __nv_bfloat16;
+  static constexpr int HN = (H + 7) / 8;
   static constexpr int kRow = D * 2, kTile = kSub * kRow, kStage = 2 * kTile, kExtra = 0;
   static constexpr int kM = 2 * HN, kAcc = HN * D / 4;
   uint32_t qf[HN][D / 16][2];
@@ -220,10 +221,10 @@ struct Core<__nv_bfloat16, D, HN> {
 // ---- a warp's state: fp32 ------------------------------------------------------
 // Scores: lane pair (lane, lane ^ 16) shares key lane & 15, half the dims each.
 // Products: lane holds D / 32 dims of every head. Maxima are equal in all lanes.
-template <int D, int HN>
-struct Core<float, D, HN> {
+template <int D, int H>
+struct Core<float, D, H> {
   using T = float;
-  static constexpr int H = 8 * HN, P = D / 32;
+  static constexpr int P = D / 32;
   static constexpr int kRow = D * 4, kTile = kSub * kRow, kStage = 2 * kTile;
   static constexpr int kExtra = (H * D + kSub * H) * 4;  // per warp: queries, weights
   static constexpr int kM = H, kAcc = H * P;
@@ -372,18 +373,18 @@ struct Walk {
   }
 };
 
-template <typename T, int D, int HN>
+template <typename T, int D, int H>
 struct FdShape {
-  using C = Core<T, D, HN>;
+  using C = Core<T, D, H>;
   static constexpr int kStages = sizeof(T) == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);
   static constexpr int kRing = kStages * C::kStage;                       // per warp
   static constexpr int kJoin = 3 * (C::kAcc + 2 * C::kM + 1) * 32 * 4;   // three warps' states
   static constexpr int kBytes = kFdWarps * (kRing + C::kExtra) + kJoin;
 };
 
-template <typename T, int D, int HN>
-__global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1) full_decode_kernel(const FdParams p) {
-  using SH = FdShape<T, D, HN>;
+template <typename T, int D, int H>
+__global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel(const FdParams p) {
+  using SH = FdShape<T, D, H>;
   using C = typename SH::C;
   constexpr int NS = SH::kStages;
   constexpr int kCpr = D * int(sizeof(T)) / 16;  // 16-byte chunks of a row
@@ -398,9 +399,9 @@ __global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1)
 
   // ---- this CTA's run of units (every warp finds it alone) ----
   int64_t total = 0;
+  const int units0 = lane < p.B ? units_of(p, lane) : 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int x = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
-    int64_t y = x;
+    int64_t y = b0 == 0 ? units0 : b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
     total += y;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1)
   Walk at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int mine = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
+    const int mine = b0 == 0 ? units0 : b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
     int64_t incl = int64_t(mine) * items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -588,37 +589,55 @@ __global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1)
       if (warp == 0) {
         __syncwarp();
         if (lane == 0) {
-          __threadfence();  // after the warp's stores (ordered by __syncwarp)
-          const int old = atomicAdd(&p.arrivals[item], 1);
+          // releases the warp's stores (ordered by __syncwarp), acquires the others'
+          int old;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.arrivals + item) : "memory");
           last_s = old == c1 - c0;
           if (last_s) p.arrivals[item] = 0;  // ready for the next call
-          __threadfence();
         }
       }
       __syncthreads();
       if (last_s) {
-        const float* pm = p.part_ml;
-        auto slot_of = [&](int cta) { return int64_t(2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0)); };
-        for (int o = threadIdx.x; o < heads * D; o += kFdThreads) {
+        auto slot_of = [&](int cta) { return 2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0); };
+        constexpr int kBatch = 8;  // partials in flight: the loads of a batch do not wait for each other
+        for (int o = threadIdx.x * 4; o < heads * D; o += kFdThreads * 4) {
           const int h = o / D;
-          float M = -INFINITY;
+          float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
           bool spoilt = false;
-#pragma unroll 4
-          for (int cta = c0; cta <= c1; ++cta) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pm + (slot_of(cta) * kFdMaxHeads + h) * 2));
-            M = fmaxf(M, ml.x);
-            spoilt |= ml.y < 0.f;
+          for (int cta = c0; cta <= c1; cta += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              const int64_t s = int64_t(slot_of(min(cta + x, c1))) * kFdMaxHeads + h;
+              ml[x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + s * 2));
+              v[x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + s * D + o % D));
+            }
+            float mn = M;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              spoilt |= ml[x].y < 0.f;
+              mn = fmaxf(mn, ml[x].x);
+            }
+            const float a = M == mn ? 1.f : ex2d(M - mn);
+            M = mn;
+            den *= a;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) sum[y] *= a;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              const float w = cta + x > c1 ? 0.f : ml[x].x == M ? 1.f : ex2d(ml[x].x - M);
+              den = fmaf(w, ml[x].y, den);
+              sum[0] = fmaf(w, v[x].x, sum[0]);
+              sum[1] = fmaf(w, v[x].y, sum[1]);
+              sum[2] = fmaf(w, v[x].z, sum[2]);
+              sum[3] = fmaf(w, v[x].w, sum[3]);
+            }
           }
-          float den = 0.f, sum = 0.f;
-#pragma unroll 4
-          for (int cta = c0; cta <= c1; ++cta) {
-            const int64_t s = slot_of(cta) * kFdMaxHeads + h;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pm + s * 2));
-            const float w = ml.x == M ? 1.f : ex2d(ml.x - M);
-            den = fmaf(w, ml.y, den);
-            sum = fmaf(w, __ldcg(p.part_o + s * D + o % D), sum);
-          }
-          out[(int64_t(b) * p.Hq + h0 + h) * D + o % D] = from_f<T>(spoilt ? 0.f : sum / den);
+          const float inv = 1.f / den;
+          T* dst = out + (int64_t(b) * p.Hq + h0 + h) * D + o % D;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt ? 0.f : sum[y] * inv);
           if (p.lse && o % D == 0)
             p.lse[int64_t(b) * p.Hq + h0 + h] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
         }
@@ -636,10 +655,10 @@ __global__ void __launch_bounds__(kFdThreads, sizeof(T) == 2 && HN == 1 ? 2 : 1)
 // Fixed grid: two CTAs per SM (the smaller shapes' shared memory allows it).
 int fd_grid() { return 2 * kNumSMs; }
 
-template <typename T, int D, int HN>
+template <typename T, int D, int H>
 cudaError_t decode(const FdParams& p, cudaStream_t stream) {
-  auto kern = full_decode_kernel<T, D, HN>;
-  constexpr int bytes = FdShape<T, D, HN>::kBytes;
+  auto kern = full_decode_kernel<T, D, H>;
+  constexpr int bytes = FdShape<T, D, H>::kBytes;
   static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
   ProfScope pf("full_decode", stream);
@@ -682,13 +701,16 @@ cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream) {
   p.out = a.out;
   p.lse = a.lse;
   p.status = &static_cast<WsHeader*>(a.ws)->status;
-  const bool two = p.hpg > 8;  // 8 heads per tile: one tile up to 8, two beyond
+  // bf16: a tile holds 8 heads, so fewer cost the same. fp32: the FMAs and
+  // shared-memory reads are those of H heads, so up to 4 get a variant of half the work.
+  const bool wide = p.hpg > 8, few = p.hpg <= 4;
   if (a.dtype == MSA_BF16) {
-    if (a.d == 128) return two ? decode<__nv_bfloat16, 128, 2>(p, stream) : decode<__nv_bfloat16, 128, 1>(p, stream);
-    return two ? decode<__nv_bfloat16, 64, 2>(p, stream) : decode<__nv_bfloat16, 64, 1>(p, stream);
+    if (a.d == 128) return wide ? decode<__nv_bfloat16, 128, 16>(p, stream) : decode<__nv_bfloat16, 128, 8>(p, stream);
+    return wide ? decode<__nv_bfloat16, 64, 16>(p, stream) : decode<__nv_bfloat16, 64, 8>(p, stream);
   }
-  if (a.d == 128) return two ? decode<float, 128, 2>(p, stream) : decode<float, 128, 1>(p, stream);
-  return two ? decode<float, 64, 2>(p, stream) : decode<float, 64, 1>(p, stream);
+  if (a.d == 128)
+    return wide ? decode<float, 128, 16>(p, stream) : few ? decode<float, 128, 4>(p, stream) : decode<float, 128, 8>(p, stream);
+  return wide ? decode<float, 64, 16>(p, stream) : few ? decode<float, 64, 4>(p, stream) : decode<float, 64, 8>(p, stream);
 }
 
 }  // namespace msa
