@@ -92,6 +92,30 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, int cols, __nv_bfloat1
   }
 }
 
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int c, const float (&o)[8], float mul) {
+  reinterpret_cast<uint4*>(row)[c] =
+      make_uint4(pack_bf16(o[0] * mul, o[1] * mul), pack_bf16(o[2] * mul, o[3] * mul),
+                 pack_bf16(o[4] * mul, o[5] * mul), pack_bf16(o[6] * mul, o[7] * mul));
+}
+// This rank's slice of `rows` rows summed over the ranks that had tiles, in
+// rank order: f(row, chunk of 8 columns, sums).
+template <int D, typename F>
+__device__ __forceinline__ void sum_partials(uint32_t part, int rows, int rank, int cl, int tiles, F f) {
+  const int per = rows / cl;
+  for (int x = threadIdx.x; x < per * (D / 8); x += kFbThreads) {
+    const int r = rank * per + x / (D / 8), c = x % (D / 8);
+    float o[8] = {};
+    for (int y = 0; y < cl; ++y) {
+      if (int64_t(tiles) * y / cl == int64_t(tiles) * (y + 1) / cl) continue;
+      const float4 u = ld_peer4(peer_addr(part_at<D>(part, r, 2 * c), y));
+      const float4 v = ld_peer4(peer_addr(part_at<D>(part, r, 2 * c + 1), y));
+      o[0] += u.x, o[1] += u.y, o[2] += u.z, o[3] += u.w;
+      o[4] += v.x, o[5] += v.y, o[6] += v.z, o[7] += v.w;
+    }
+    f(r, c, o);
+  }
+}
+
 // ---------------------------------------------------------------------------------
 // dk, dv of 128 keys of one (sequence, key/value head)
 // TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV, dK
@@ -111,9 +135,10 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
     return;
   }
-  const int g = blockIdx.x % p.Hkv;
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
+  const int g = work % p.Hkv;
   int kt;
-  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, int(blockIdx.x / p.Hkv), kt);  // early keys: most rows
+  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, work / p.Hkv, kt);  // early keys: most rows
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.ok) {
@@ -122,9 +147,10 @@ __global__ void __launch_bounds__(kFbThreads, 1)
   }
   const int j0 = kt * kKeys;
   const int off = s.Lk - s.Lq;              // row i sees keys j <= off + i
-  const int r0 = max(j0 - off, 0) / p.tpt;  // first row tile that sees one of these keys
-  const int n = max((s.Lq + p.tpt - 1) / p.tpt - r0, 0);
-  if (n == 0) {  // no row sees them
+  const int rf = max(j0 - off, 0) / p.tpt;  // first row tile that sees one of these keys
+  const int tiles = max((s.Lq + p.tpt - 1) / p.tpt - rf, 0);
+  if (tiles == 0) {  // no row sees them
+    if (rank > 0) return;
     for (int x = threadIdx.x; x < min(kKeys, s.Lk - j0) * (D / 8); x += kFbThreads) {
       const int64_t o = ((int64_t(s.k0) + j0 + x / (D / 8)) * p.Hkv + g) * (D / 8) + x % (D / 8);
       reinterpret_cast<uint4*>(p.dk)[o] = make_uint4(0, 0, 0, 0);
@@ -132,6 +158,8 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     }
     return;
   }
+  // this CTA's row tiles [r0, r0 + n)
+  const int r0 = rf + int(int64_t(tiles) * rank / cl), n = rf + int(int64_t(tiles) * (rank + 1) / cl) - r0;
   uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
   const FbBars bar(bars, NR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -183,7 +211,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
 #pragma unroll
       for (int h = 0; h < NH; ++h) tc::tma_load_4d(dst + h * kHalfTile, map, full, h * 64, 0, g, tok);
     };
-    keys();
+    if (n > 0) keys();
     bool ok = true;
     int nc = 0, ne = 0, tails = 0;
     for (int i = 0; i < n && ok; ++i) {
@@ -234,7 +262,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------- MMA issue -----------------------------
-    if (lane == 0) {
+    if (lane == 0 && n > 0) {
       constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
       const uint32_t sb = tc::smem_u32(fb_smem);
       auto major = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, 16); };           // K-major along d
@@ -384,16 +412,17 @@ __global__ void __launch_bounds__(kFbThreads, 1)
         tc::mbar_arrive(bar.r_empty + sl);
       }
     }
-    if (ok) ok = warp_wait(bar.acc_full, 0, abort_flag);
-    if (ok) {
+    if (ok && n > 0) ok = warp_wait(bar.acc_full, 0, abort_flag);
+    if (!ok) fail();
+    if (ok && n > 0) {
       tc::fence_after_sync();
       const int64_t row = (int64_t(s.k0) + j0 + key) * p.Hkv + g;
-      if (w == 0)
+      if (cl > 1)  // w 0: dv, w 1: dk; every product is done, the operands' space is free
+        put_partial<D>(tc::smem_u32(fb_smem), w * kKeys + key, 0, sbase + (w == 0 ? kColDv : kColDk), D);
+      else if (w == 0)
         store_acc<D>(sbase + kColDv, D, p.dv + row * D, 1.f, j0 + key < s.Lk);
       else
         store_acc<D>(sbase + kColDk, D, p.dk + row * D, p.scale, j0 + key < s.Lk);
-    } else {
-      fail();
     }
   }
   tc::fence_before_sync();
@@ -402,6 +431,15 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
+  if (cl == 1) return;
+  cluster_sync();
+  sum_partials<D>(tc::smem_u32(fb_smem), 2 * kKeys, rank, cl, tiles, [&](int r, int c, float (&o)[8]) {
+    const int key = r % kKeys;
+    if (j0 + key >= s.Lk) return;
+    const int64_t row = (int64_t(s.k0) + j0 + key) * p.Hkv + g;
+    store8(r < kKeys ? p.dv + row * D : p.dk + row * D, c, o, r < kKeys ? 1.f : p.scale);
+  });
+  cluster_sync();  // nobody leaves while its partial is read
 }
 
 // ---------------------------------------------------------------------------------
@@ -423,9 +461,10 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
     return;
   }
-  const int g = blockIdx.x % p.Hkv;
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
+  const int g = work % p.Hkv;
   int rt;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.nslots - 1 - int(blockIdx.x / p.Hkv), rt);  // late rows first
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.nslots - 1 - work / p.Hkv, rt);  // late rows first
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.rows_ok) {
@@ -434,9 +473,10 @@ __global__ void __launch_bounds__(kFbThreads, 1)
   }
   const int i0 = rt * p.tpt, i1 = min(i0 + p.tpt, s.Lq);
   const int vis_last = s.ok ? s.Lk - s.Lq + i1 : 0;
-  const int n = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
-  if (n == 0) {
+  const int tiles = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
+  if (tiles == 0) {
     if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    if (rank > 0) return;
     for (int x = threadIdx.x; x < (i1 - i0) * p.hpg * (D / 8); x += kFbThreads) {
       const int r = x / (D / 8);
       const int64_t row = (int64_t(s.q0) + i0 + r / p.hpg) * p.Hq + g * p.hpg + r % p.hpg;
@@ -444,6 +484,8 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     }
     return;
   }
+  // this CTA's key tiles [jb, jb + n)
+  const int jb = int(int64_t(tiles) * rank / cl), n = int(int64_t(tiles) * (rank + 1) / cl) - jb;
   uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
   const FbBars bar(bars, SM::kRowSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -474,7 +516,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
 #pragma unroll
       for (int h = 0; h < NH; ++h) tc::tma_load_3d(dst + h * kHalfTile, map, full, h * 64, g, row);
     };
-    if (lane == 0) {
+    if (lane == 0 && n > 0) {
       tc::mbar_arrive_expect_tx(bar.res_full, 2 * uint32_t(p.tpt * p.hpg) * D * 2);
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -485,28 +527,28 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     bool ok = true;
     int nc = 0, ne = 0, tails = 0;
     for (int j = 0; j < n && ok; ++j) {
-      const int st = j & 1, ph = (j >> 1) & 1, valid = s.Lk - j * kKeys;
+      const int st = j & 1, ph = (j >> 1) & 1, valid = s.Lk - (jb + j) * kKeys;
       uint8_t* kd = fb_smem + SM::oC + st * SM::kTile;
       uint8_t* vd = fb_smem + SM::oE + st * SM::kTile;
       if (!(ok = warp_wait(bar.c_empty + st, ph ^ 1, abort_flag))) break;
       if (valid >= kKeys) {
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.c_full + st, SM::kTile);
-          box(&tmK, kd, bar.c_full + st, s.k0 + j * kKeys);
+          box(&tmK, kd, bar.c_full + st, s.k0 + (jb + j) * kKeys);
         }
         ++nc;
         if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.e_full + st, SM::kTile);
-          box(&tmV, vd, bar.e_full + st, s.k0 + j * kKeys);
+          box(&tmV, vd, bar.e_full + st, s.k0 + (jb + j) * kKeys);
         }
         ++ne;
       } else {  // the keys behind the sequence's end become zeros
         if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.tail, 2 * SM::kTile);
-          box(&tmK, kd, bar.tail, s.k0 + j * kKeys);
-          box(&tmV, vd, bar.tail, s.k0 + j * kKeys);
+          box(&tmK, kd, bar.tail, s.k0 + (jb + j) * kKeys);
+          box(&tmV, vd, bar.tail, s.k0 + (jb + j) * kKeys);
         }
         ++tails;
         if (!(ok = warp_wait(bar.tail, 0, abort_flag))) break;
@@ -530,7 +572,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------- MMA issue -----------------------------
-    if (lane == 0) {
+    if (lane == 0 && n > 0) {
       constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
       const uint32_t sb = tc::smem_u32(fb_smem);
       auto major = [&](uint32_t o) { return tc::smem_desc_lo(sb + o, 16); };
@@ -594,12 +636,12 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     float2 rd = make_float2(INFINITY, 0.f);
     if (valid) rd = p.rows[(int64_t(g) * p.seq.Tq + s.q0 + i) * p.hpg + r % p.hpg];
     const int vis = s.Lk - s.Lq + i + 1;
-    const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys;  // tiles below it are seen whole by every row
+    const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys - jb;  // tiles below it are seen whole by every row
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!(ok = warp_wait(bar.s_full, j & 1, abort_flag))) break;
       tc::fence_after_sync();
-      const int lim = vis - j * kKeys - w * 64;  // columns below it are seen
+      const int lim = vis - (jb + j) * kKeys - w * 64;  // columns below it are seen
       float pr[64];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -632,13 +674,15 @@ __global__ void __launch_bounds__(kFbThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar.ds_full);
     }
-    if (ok) ok = warp_wait(bar.acc_full, 0, abort_flag);
-    if (ok) {
+    if (ok && n > 0) ok = warp_wait(bar.acc_full, 0, abort_flag);
+    if (!ok) fail();
+    if (ok && n > 0) {
       tc::fence_after_sync();
       const int64_t row = (int64_t(s.q0) + i) * p.Hq + g * p.hpg + r % p.hpg;
-      store_acc<D>(lbase + kColDq + w * (D / 2), D / 2, p.dq + row * D + w * (D / 2), p.scale, valid);
-    } else {
-      fail();
+      if (cl > 1)
+        put_partial<D>(tc::smem_u32(fb_smem), r, w * (D / 8), lbase + kColDq + w * (D / 2), D / 2);
+      else
+        store_acc<D>(lbase + kColDq + w * (D / 2), D / 2, p.dq + row * D + w * (D / 2), p.scale, valid);
     }
   }
   tc::fence_before_sync();
@@ -647,6 +691,14 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
+  if (cl == 1) return;
+  cluster_sync();
+  sum_partials<D>(tc::smem_u32(fb_smem), kRows, rank, cl, tiles, [&](int r, int c, float (&o)[8]) {
+    const int i = i0 + r / p.hpg;
+    if (r >= p.tpt * p.hpg || i >= i1) return;
+    store8(p.dq + ((int64_t(s.q0) + i) * p.Hq + g * p.hpg + r % p.hpg) * D, c, o, p.scale);
+  });
+  cluster_sync();  // nobody leaves while its partial is read
 }
 
 template <int D>
@@ -667,27 +719,24 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.status = &static_cast<WsHeader*>(f.ws)->status;
   const int qslots = f.seq.Tq / p.tpt + f.seq.B, kslots = f.seq.Tk / kKeys + f.seq.B;
   const int64_t qc = int64_t(qslots) * f.Hkv, kc = int64_t(kslots) * f.Hkv;
-  if (qc >= (int64_t(1) << 31) || kc >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   CUtensorMap tmQ, tmO, tmK, tmV;
   if (!map_rows(&tmQ, f.q, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) || !map_rows(&tmO, a.dout, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) ||
       !map_keys(&tmK, f.k, f.seq.Tk, f.Hkv, D, kKeys) || !map_keys(&tmV, f.v, f.seq.Tk, f.Hkv, D, kKeys))
     return cudaErrorInvalidValue;
   constexpr int bytes = FbSmem<D>::kTotal;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(full_bwd_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) ||
-      (e = cudaFuncSetAttribute(full_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
-    return e;
   if ((e = launch_full_bwd_rows(a, stream))) return e;
   {
     ProfScope pf("full_bwd_dkv", stream);
     p.nslots = kslots;
-    full_bwd_dkv_kernel<D><<<unsigned(kc), kFbThreads, bytes, stream>>>(tmQ, tmO, tmK, tmV, p);
-    if ((e = cudaGetLastError())) return e;
+    if ((e = launch_clusters(full_bwd_dkv_kernel<D>, kc, cluster_split(kc, (f.seq.Tq + p.tpt - 1) / p.tpt), kFbThreads,
+                             bytes, stream, tmQ, tmO, tmK, tmV, p)))
+      return e;
   }
   ProfScope pf("full_bwd_dq", stream);
   p.nslots = qslots;
-  full_bwd_dq_kernel<D><<<unsigned(qc), kFbThreads, bytes, stream>>>(tmQ, tmO, tmK, tmV, p);
-  return cudaGetLastError();
+  return launch_clusters(full_bwd_dq_kernel<D>, qc, cluster_split(qc, (f.seq.Tk + kKeys - 1) / kKeys), kFbThreads, bytes,
+                         stream, tmQ, tmO, tmK, tmV, p);
 }
 
 }  // namespace

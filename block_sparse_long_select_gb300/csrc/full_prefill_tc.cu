@@ -29,6 +29,13 @@ namespace msa {
 namespace {
 
 constexpr int kPfThreads = 384;
+// Registers per thread: 168 at launch (3 warpgroups x 128 threads x 168), of
+// which the load / MMA warpgroup hands 2 x 48 to the softmax warpgroups, whose
+// threads hold a row of 128 scores. Given once, never taken back: a warp that
+// asked for registers again could get them before the softmax warps do, and
+// those would wait for good.
+constexpr uint32_t kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
+static_assert(kRegsFew + 2 * kRegsMany <= 3 * kRegsLaunch, "the shares come out of the launch's registers");
 constexpr float kLazy = 8.f;  // log2 of the largest weight
 
 struct PfParams {
@@ -46,8 +53,10 @@ struct PfSmem {
   static constexpr int kStages = D == 128 ? 2 : 4;   // K ring and V ring
   static constexpr uint32_t kTile = kRows * D * 2;
   static constexpr uint32_t oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile, oBar = oV + kStages * kTile;
-  static constexpr int kBars = 2 + 4 * kStages + 2 + 2 + 2 + 1 + 1;
-  static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
+  static constexpr int kBars = 2 + 4 * kStages + 2 + 4 + 2 + 1 + 1;
+  static constexpr uint32_t oStat = (oBar + kBars * 8 + 16 + 15) & ~15u;
+  static constexpr uint32_t kTotal = oStat + 2 * kRows * 8;
+  static_assert(2 * kRows * D * 4 <= oBar, "the partial fits where the operands were");
 };
 
 template <int D>
@@ -67,9 +76,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   }
 
   // ---- which rows: heavy (late) tiles of a sequence first ----
-  const int g = blockIdx.x % p.Hkv;
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
+  const int g = work % p.Hkv;
   int tile;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, 2 * p.tpt, p.nslots - 1 - int(blockIdx.x / p.Hkv), tile);
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, 2 * p.tpt, p.nslots - 1 - work / p.Hkv, tile);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.rows_ok) {
@@ -86,9 +96,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   }
   bad = __syncthreads_or(bad);
   const int vis_last = bad ? 0 : s.Lk - s.Lq + i1;  // keys the last row sees
-  const int n = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
-  if (n == 0) {  // no row sees a key
+  const int tiles = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
+  if (tiles == 0) {  // no row sees a key
     if (bad && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    if (rank > 0) return;
     const int chunks = (i1 - i0) * p.hpg * (D / 8);
     for (int x = threadIdx.x; x < chunks; x += kPfThreads) {
       const int r = x / (D / 8), tok = s.q0 + i0 + r / p.hpg, h = g * p.hpg + r % p.hpg;
@@ -99,6 +110,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     return;
   }
 
+  // this CTA's key tiles [jb, jb + n)
+  const int jb = int(int64_t(tiles) * rank / cl), n = int(int64_t(tiles) * (rank + 1) / cl) - jb;
+
   uint64_t* bars = reinterpret_cast<uint64_t*>(pf_smem + SM::oBar);
   uint64_t* q_full = bars;             // [2]
   uint64_t* k_full = bars + 2;         // [NS]
@@ -106,16 +120,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t* v_full = k_empty + NS;     // [NS]
   uint64_t* v_empty = v_full + NS;     // [NS]
   uint64_t* s_full = v_empty + NS;     // [2]
-  uint64_t* p_full = s_full + 2;       // [2]
-  uint64_t* o_full = p_full + 2;       // [2]
+  uint64_t* p_full = s_full + 2;       // [2][2]: row tile, half of the keys
+  uint64_t* o_full = p_full + 4;       // [2]
   uint64_t* tail_bar = o_full + 2;     // the copies of a value tile whose last rows are then zeroed
   uint64_t* done_bar = tail_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float2* stats = reinterpret_cast<float2*>(pf_smem + SM::oStat);  // [2][128] maximum, sum (clusters only)
   if (threadIdx.x == 0) {
     for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
-    tc::mbar_init(&p_full[0], 4);
-    tc::mbar_init(&p_full[1], 4);
+    for (int x = 0; x < 4; ++x) tc::mbar_init(p_full + x, 4);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -131,6 +145,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     set_status(p.status, MSA_ERR_TIMEOUT);
   };
 
+  if (warp < 4) {
+  tc::regs_dec<kRegsFew>();
   if (warp == 0) {
     // ------------------------------ loads ------------------------------
     if (lane == 0) {
@@ -145,8 +161,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int np = paged ? (s.Lk + psz - 1) >> p.pages.page_log2 : 0;
     const int32_t* table = paged ? p.pages.table + int64_t(b) * p.pages.max_pages : nullptr;
     auto first_row = [&](int j) {  // this lane's box of tile j: its first row, -1 if it has none
-      if (!paged) return lane == 0 ? s.k0 + j * kKeys : -1;
-      const int pi = j * per + lane;
+      if (!paged) return lane == 0 ? s.k0 + (jb + j) * kKeys : -1;
+      const int pi = (jb + j) * per + lane;
       return lane < per && pi < np ? table[pi] << p.pages.page_log2 : -1;
     };
     auto boxes = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row) {
@@ -171,7 +187,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     int row = first_row(0);
     bool ok = true;
     int nk = 0, nv = 0, tails = 0;
-    load_q(0);
+    if (n > 0) load_q(0);
     for (int j = 0; j < n && ok; ++j) {
       const int st = j % NS, ph = (j / NS) & 1;
       const int next = j + 1 < n ? first_row(j + 1) : -1;  // in flight while this tile is issued
@@ -181,7 +197,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (j == 0) load_q(1);
       if (!(ok = warp_wait(&v_empty[st], ph ^ 1, abort_flag))) break;
       uint8_t* vt = pf_smem + SM::oV + st * SM::kTile;
-      const int valid = s.Lk - j * kKeys;
+      const int valid = s.Lk - (jb + j) * kKeys;
       if (valid >= kKeys) {
         boxes(vt, &tmV, &v_full[st], row);
         ++nv;
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (!ok) {  // let the copies land before the CTA gives its shared memory up
       fail();
       int zero = 0;
-      tc::mbar_wait(&q_full[0], 0, &zero);
+      tc::mbar_wait(&q_full[0], 0, &zero);  // n > 0 here
       if (nk > 0) tc::mbar_wait(&q_full[1], 0, &zero);
       for (int x = max(nk - NS, 0); x < nk; ++x) tc::mbar_wait(&k_full[x % NS], (x / NS) & 1, &zero);
       for (int x = max(nv - NS, 0); x < nv; ++x) tc::mbar_wait(&v_full[x % NS], (x / NS) & 1, &zero);
@@ -209,7 +225,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------- MMA issue -----------------------------
-    if (lane == 0) {
+    if (lane == 0 && n > 0) {
       constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
       const uint32_t qa = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oQ), 16);
       const uint32_t ka = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oK), 16);
@@ -223,12 +239,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         tc::mma_commit(&s_full[w]);
       };
-      auto values = [&](int w, int j) {  // O_w += P_w V_j
+      auto values = [&](int w, int j, int half) {  // O_w += P_w V_j over half of the keys
         const uint32_t v0 = va + (((j % NS) * SM::kTile) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
+        for (int x = 0; x < kKeys / 32; ++x) {
+          const int kk = half * (kKeys / 32) + x;
           tc::mma_f16_ts_lo<kHi>(tmem + kColO + w * D, tmem + w * 128 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdO,
                                  (j > 0 || kk > 0) ? 1u : 0u);
+        }
       };
       bool ok = tc::mbar_wait(&q_full[0], 0, abort_flag) && tc::mbar_wait(&k_full[0], 0, abort_flag);
       if (ok) {
@@ -246,9 +264,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int st1 = (j + 1) % NS, ph1 = ((j + 1) / NS) & 1;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (!(ok = tc::mbar_wait(&p_full[w], j & 1, abort_flag))) break;
+          // the first half's product runs while the softmax forms the second half
+          if (!(ok = tc::mbar_wait(&p_full[2 * w], j & 1, abort_flag))) break;
           tc::fence_after_sync();
-          values(w, j);
+          values(w, j, 0);
+          if (!(ok = tc::mbar_wait(&p_full[2 * w + 1], j & 1, abort_flag))) break;
+          tc::fence_after_sync();
+          values(w, j, 1);
           if (w == 1) tc::mma_commit(&v_empty[st]);
           if (j + 1 < n) {
             // in issue order behind the product that reads P: S may go over it
@@ -265,8 +287,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc::mma_commit(done_bar);
       tc::mbar_wait(done_bar, 0, &zero);
     }
-  } else if (warp >= 4) {
-    // ------------------------------ softmax ------------------------------
+  }
+  } else {
+    // ------------------------------ softmax
+    tc::regs_inc<kRegsMany>();
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t sbase = tmem + (uint32_t(quarter * 32) << 16) + w * 128;
@@ -275,7 +299,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const bool valid = r < p.tpt * p.hpg && i < i1;
     const int vis = s.Lk - s.Lq + i + 1;       // keys it sees
     // tiles below j_mask are seen whole by every row of the tile (its first sees least)
-    const int j_mask = max(s.Lk - s.Lq + i0 + w * p.tpt + 1, 0) / kKeys;
+    const int j_mask = max(s.Lk - s.Lq + i0 + w * p.tpt + 1, 0) / kKeys - jb;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -293,7 +317,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld_32x32b_x32(sbase + c * 32, v + c * 32);
         tc::tmem_ld_wait();
-        const int lim = vis - j * kKeys;
+        const int lim = vis - (jb + j) * kKeys;
         mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) {
@@ -321,7 +345,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       const float neg = m == -INFINITY ? 0.f : -m;
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t pk[32];
@@ -329,22 +352,38 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int x = 0; x < 32; ++x) {
           const float p0 = ex2(fmaf(__uint_as_float(v[c * 64 + 2 * x]), p.scale_log2, neg));
           const float p1 = ex2(fmaf(__uint_as_float(v[c * 64 + 2 * x + 1]), p.scale_log2, neg));
-          l4[x & 3] += p0 + p1;
+          v[c * 64 + x] = __float_as_uint(p0 + p1);
           pk[x] = pack_bf16(p0, p1);
         }
         tc::tmem_st_32x32b_x32(sbase + c * 32, pk);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[2 * w + c]);
       }
+      // the sum, off the tensor cores' path
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 0; x < 32; ++x) l4[x & 3] += __uint_as_float(v[c * 64 + x]);
       l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_full[w]);
     }
-    if (ok) ok = warp_wait(&o_full[w], 0, abort_flag);
-    if (ok) {
+    if (ok && n > 0) {
+      ok = warp_wait(&o_full[w], 0, abort_flag);
+      // a partial goes where the operands were: the other tile's products have to be done, too
+      if (ok && cl > 1) ok = warp_wait(&o_full[w ^ 1], 0, abort_flag);
+    }
+    if (!ok) fail();
+    if (ok && cl > 1) {
+      tc::fence_after_sync();
+      const uint32_t part = tc::smem_u32(pf_smem);
+      if (n > 0) put_partial<D>(part, w * kRows + r, 0, obase, D);
+      stats[w * kRows + r] = n > 0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+    } else if (ok) {
       tc::fence_after_sync();
       const int64_t row = int64_t(s.q0 + i) * p.Hq + g * p.hpg + r % p.hpg;
-      const bool some = l > 0.f;
+      const bool some = l > 0.f || l != l;
       const float inv = some ? 1.f / l : 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -366,8 +405,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       if (valid && p.lse) p.lse[row] = some ? (m + log2f(l)) * kLn2f : -INFINITY;
-    } else {
-      fail();
     }
   }
   tc::fence_before_sync();
@@ -376,6 +413,37 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
+  if (cl == 1) return;
+  // ---- the ranks' partials of the 256 rows, a slice of rows per rank ----
+  cluster_sync();
+  const uint32_t part = tc::smem_u32(pf_smem), stat = tc::smem_u32(stats);
+  const int per = 2 * kRows / cl;
+  // the softmax warpgroups, which have the registers
+  for (int x = int(threadIdx.x) - 128; x >= 0 && x < per * (D / 8); x += 256) {
+    const int r = rank * per + x / (D / 8), c = x % (D / 8), w = r / kRows, rr = r % kRows;
+    const int i = i0 + w * p.tpt + rr / p.hpg;
+    if (rr >= p.tpt * p.hpg || i >= i1) continue;
+    float M = -INFINITY, den = 0.f, o[8] = {};
+    for (int y = 0; y < cl; ++y) M = fmaxf(M, ld_peer2(peer_addr(stat + r * 8, y)).x);
+    for (int y = 0; y < cl; ++y) {
+      const float2 ml = ld_peer2(peer_addr(stat + r * 8, y));
+      if (!(ml.y > 0.f) && ml.y == ml.y) continue;  // no key there (its partial may hold nothing)
+      const float a = ml.x == M ? 1.f : ex2(ml.x - M);
+      const float4 u = ld_peer4(peer_addr(part_at<D>(part, r, 2 * c), y));
+      const float4 v = ld_peer4(peer_addr(part_at<D>(part, r, 2 * c + 1), y));
+      den = fmaf(a, ml.y, den);
+      o[0] = fmaf(a, u.x, o[0]), o[1] = fmaf(a, u.y, o[1]), o[2] = fmaf(a, u.z, o[2]), o[3] = fmaf(a, u.w, o[3]);
+      o[4] = fmaf(a, v.x, o[4]), o[5] = fmaf(a, v.y, o[5]), o[6] = fmaf(a, v.z, o[6]), o[7] = fmaf(a, v.w, o[7]);
+    }
+    const bool some = den > 0.f || den != den;
+    const float inv = some ? 1.f / den : 0.f;
+    const int64_t row = int64_t(s.q0 + i) * p.Hq + g * p.hpg + rr % p.hpg;
+    reinterpret_cast<uint4*>(p.out + row * D)[c] =
+        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+    if (p.lse && c == 0) p.lse[row] = some ? (M + log2f(den)) * kLn2f : -INFINITY;
+  }
+  cluster_sync();  // nobody leaves while its partial is read
 }
 
 template <int D>
@@ -400,13 +468,13 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
       !map_keys(&tmV, a.v, krows, a.Hkv, D, box))
     return cudaErrorInvalidValue;
   const int64_t ctas = int64_t(p.nslots) * a.Hkv;
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  auto kern = full_prefill_kernel<D>;
-  if (cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfSmem<D>::kTotal))
-    return err;
+  // a launch with other registers could not cover the warpgroups' shares
+  cudaFuncAttributes fa;
+  if (cudaError_t e = cudaFuncGetAttributes(&fa, full_prefill_kernel<D>)) return e;
+  if (fa.numRegs != int(kRegsLaunch)) return cudaErrorInvalidConfiguration;
   ProfScope pf("full_prefill", stream);
-  kern<<<unsigned(ctas), kPfThreads, PfSmem<D>::kTotal, stream>>>(tmQ, tmK, tmV, p);
-  return cudaGetLastError();
+  return launch_clusters(full_prefill_kernel<D>, ctas, cluster_split(ctas, (int64_t(a.seq.Tk) + kKeys - 1) / kKeys),
+                         kPfThreads, int(PfSmem<D>::kTotal), stream, tmQ, tmK, tmV, p);
 }
 
 }  // namespace

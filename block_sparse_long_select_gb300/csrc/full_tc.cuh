@@ -33,6 +33,90 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to) {
     *reinterpret_cast<uint4*>(tile + (x / per) * kHalfTile + from * 128 + (x % per) * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// ---- work split over a cluster ------------------------------------------------
+// A call with few tiles gives each to a cluster of CTAs: they share the walk
+// over the other side, leave fp32 partials in their own shared memory, and
+// each adds up a slice of everybody's in rank order (deterministic) over
+// distributed shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all CTAs of the cluster; shared memory written before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// 16-byte chunk c of row r of a fp32 partial [rows][D]; chunks are exchanged by
+// the row's low bits, so that a thread per row writes without bank conflicts.
+template <int D>
+__device__ __forceinline__ uint32_t part_at(uint32_t base, int r, int c) {
+  return base + uint32_t(r) * (D * 4) + (uint32_t(c ^ (r & 7)) << 4);
+}
+// One thread's row: `cols` columns of TMEM into row r of a partial, from chunk c0 on (whole warp).
+template <int D>
+__device__ __forceinline__ void put_partial(uint32_t base, int r, int c0, uint32_t taddr, int cols) {
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t o[32];
+    tc::tmem_ld_32x32b_x32(taddr + c, o);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(part_at<D>(base, r, c0 + c / 4 + x)), "r"(o[4 * x]),
+                   "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+                   : "memory");
+  }
+}
+// CTAs of a cluster for `ctas` tiles that walk up to `steps` each: doubled until
+// the grid fills the SMs about three times (a shorter tail of the last wave),
+// as long as every CTA keeps two steps.
+inline int cluster_split(int64_t ctas, int64_t steps) {
+  int c = 1;
+  while (c < 8 && ctas * c < 3 * kNumSMs && steps >= 4 * c) c *= 2;
+  return c;
+}
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kern)(P...), int64_t ctas, int cluster, int threads, int smem, cudaStream_t stream,
+                            A... args) {
+  if (ctas * cluster >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas * cluster));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // TMA maps: row tiles [tokens][hpg heads][64 dims] of a [Tq, Hq, d] tensor, and
 // key tiles [rows][1 head][64 dims] of a [rows, Hkv, d] one.
 inline bool map_rows(CUtensorMap* m, const void* p, int Tq, int Hq, int Hkv, int d, int tpt) {
