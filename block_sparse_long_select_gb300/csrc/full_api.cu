@@ -35,6 +35,7 @@ msa_status_t check_pages(int num_pages, int page_size, int max_pages, PageMap* p
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 msa_status_t check_full_ws(void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return MSA_ERR_UNSUPPORTED;  // sizes that msa_workspace_size refuses
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < need) return MSA_ERR_WORKSPACE;
   return MSA_OK;
 }
@@ -55,7 +56,8 @@ inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale :
 size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
   if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(B, Hq, Hkv, d) : 0;
-  if (Nq < 0 || !rows_ok(Nq, Hq) || !rows_ok(op == MSA_OP_PAGED_APPEND ? Nq : Nk, Hkv)) return 0;
+  if (Nq < 0 || !rows_ok(Nq, Hq) || (op == MSA_OP_FULL_BACKWARD && !rows_ok(Nk, Hkv))) return 0;
+  if (op == MSA_OP_FULL_PREFILL && dtype == MSA_BF16) return kWsHeader + full_prefill_ws_bytes(d, Nk);
   if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
   return kWsHeader;
 }
@@ -185,7 +187,8 @@ extern "C" msa_status_t msa_full_attn_prefill_paged(const void* q, const void* k
   if (B == 0 || Tq == 0) return MSA_OK;
   if (!q || !k_cache || !v_cache || !page_table || !cu_q || !kv_len || !out) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
-  st = check_full_ws(ws, ws_bytes, kWsHeader);
+  st = check_full_ws(ws, ws_bytes,
+                     full_ws_bytes(MSA_OP_FULL_PREFILL, B, Tq, max_pages * page_size, Hkv, Hq, d, dtype));
   if (st != MSA_OK) return st;
   a.q = q;
   a.k = k_cache;

@@ -368,7 +368,8 @@ extern "C" msa_status_t msa_read_status(void* ws, cudaStream_t stream) {
     return MSA_ERR_CUDA;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MSA_ERR_CUDA;
   if (host != 0) {
-    if (cudaMemsetAsync(status_word(ws), 0, sizeof(uint32_t), stream) != cudaSuccess) return MSA_ERR_CUDA;
+    // the whole header: a call that timed out may have left arrivals behind
+    if (cudaMemsetAsync(ws, 0, kWsHeader, stream) != cudaSuccess) return MSA_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return MSA_ERR_CUDA;
   }
   return static_cast<msa_status_t>(host);

@@ -18,8 +18,12 @@ constexpr int kMaxBs = 1024;
 struct WsHeader {
   uint32_t status;        // sticky msa_status_t set by kernels
   uint32_t work_counter;  // persistent-grid work queue head (reset per launch)
-  uint32_t reserved[62];
+  // full-attention prefill: a byte per CTA of its grid, zero between calls; a
+  // call that timed out may leave counts, which msa_read_status clears
+  uint32_t arrivals[(kNumSMs + 3) / 4];
+  uint32_t reserved[62 - (kNumSMs + 3) / 4];
 };
+static_assert(sizeof(WsHeader) == kWsHeader, "the header is the workspace's first 256 bytes");
 
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t code) {
   atomicCAS(status, 0u, code);  // the first error wins
