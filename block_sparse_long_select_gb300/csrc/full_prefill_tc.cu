@@ -18,10 +18,11 @@
 // bf16 for its product (2^-8 of each weight, which averages out over the keys);
 // the sum takes the unrounded weights in fp32.
 //
-// The grid is persistent, one CTA per SM with an equal share of all tiles
-// (full_sched.cuh): the loads and first scores of the next item run under the
-// end of the one before, and ragged or few items leave no SM idle. Rows of an
-// item that several CTAs share are joined by the last of them to arrive.
+// The grid is persistent, one CTA per SM: the loads and first scores of the next
+// item run under the end of the one before. Many items are handed out whole,
+// long ones first; few or very long ones are divided into equal shares
+// (full_sched.cuh), and the rows of an item that several CTAs share are joined
+// by the last of them to arrive.
 //
 // Bound: the tensor cores (4 Hq d FLOPs per visible pair).
 //
@@ -52,13 +53,14 @@ constexpr int kPfFixed = 256, kPfLeast = 4 * kKeys + kPfFixed, kPfWhole = 8 * kK
 struct PfParams {
   SeqMap seq;
   PageMap pages;
-  int Hq, Hkv, hpg, tpt;
+  int Hq, Hkv, hpg, tpt, nslots;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
   float* part;    // [2 * grid][D / 4][256][4] fp32: unnormalised rows of split items
   float2* stat;   // [2 * grid][256]: their maximum (log2 units) and sum
   uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
+  uint32_t* queue;     // next item to hand out, zero between calls
   uint32_t* status;
 };
 
@@ -334,37 +336,63 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         ++it;
       };
-      if (sh.init(blockIdx.x, gridDim.x)) {
+      // an item's description; false: its pages are out of range
+      auto describe = [&](PfItem& d, int sb, int g, int slot_tile, const SeqSpan& s) {
+        d.b = sb;
+        d.g = g;
+        d.i0 = slot_tile * w2;
+        d.i1 = min(d.i0 + w2, s.Lq);
+        d.q0 = s.q0;
+        d.k0 = s.k0;
+        d.Lq = s.Lq;
+        d.Lk = s.Lk;
+        d.tiles = (s.Lk - s.Lq + d.i1 + kKeys - 1) / kKeys;
+        if (p.pages.table && checked != sb) {  // every page of the sequence in range, for all its rows alike
+          checked = sb;
+          const int32_t* row = p.pages.table + int64_t(sb) * p.pages.max_pages;
+          const int np = (s.Lk + (1 << p.pages.page_log2) - 1) >> p.pages.page_log2;
+          bad = false;
+#pragma unroll 4
+          for (int x = lane; x < np; x += 32) bad |= row[x] < 0 || row[x] >= p.pages.num_pages;
+          bad = __any_sync(0xffffffffu, bad);
+          if (bad && lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
+        }
+        if (bad) d.mode = 2;
+      };
+      if (!sh.measure(gridDim.x)) {
+        // no row sees a key
+      } else if (sh.hand_out()) {
+        const int all = p.nslots * p.Hkv;
+        for (int next = 0; ok && next < all;) {
+          if (lane == 0) {
+            next = int(atomicAdd(p.queue, 1u));
+            // the last of the calls that find the queue empty leaves it ready for the next launch
+            if (next == all + int(gridDim.x) - 1) atomicExch(p.queue, 0u);
+          }
+          next = __shfl_sync(0xffffffffu, next, 0);
+          if (next >= all) break;
+          int tile;
+          const int sb = find_slot_tile(p.seq.cu_q, p.seq.B, w2, p.nslots - 1 - next / p.Hkv, tile);  // late rows first
+          if (sb < 0) continue;
+          const SeqSpan s = seq_span(p.seq, sb);
+          if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: warp 3
+          PfItem d{};
+          describe(d, sb, next % p.Hkv, tile, s);
+          d.n = d.mode == 2 ? 0 : d.tiles;
+          publish(d);
+        }
+      } else if (sh.init(blockIdx.x)) {
         for (; ok && !sh.done(); sh.next()) {
           const SeqSpan s = seq_span(p.seq, sh.cur.b);
-          const int off = s.Lk - s.Lq, s0 = off < 0 ? -off / w2 : 0;
+          const int off = s.Lk - s.Lq;
           PfItem d{};
-          d.b = sh.cur.b;
-          d.g = sh.cur.g;
-          d.i0 = (s0 + sh.cur.x) * w2;
-          d.i1 = min(d.i0 + w2, s.Lq);
-          d.q0 = s.q0;
-          d.k0 = s.k0;
-          d.Lq = s.Lq;
-          d.Lk = s.Lk;
-          d.tiles = (off + d.i1 + kKeys - 1) / kKeys;
+          describe(d, sh.cur.b, sh.cur.g, (off < 0 ? -off / w2 : 0) + sh.cur.x, s);
           int to;
           sh.tiles(d.tiles, d.jb, to);
           d.n = to - d.jb;
           if (d.n == 0) continue;
-          if (p.pages.table && checked != d.b) {  // every page of the sequence in range, for all its rows alike
-            checked = d.b;
-            const int32_t* row = p.pages.table + int64_t(d.b) * p.pages.max_pages;
-            const int np = (s.Lk + (1 << p.pages.page_log2) - 1) >> p.pages.page_log2;
-            bad = false;
-#pragma unroll 4
-            for (int x = lane; x < np; x += 32) bad |= row[x] < 0 || row[x] >= p.pages.num_pages;
-            bad = __any_sync(0xffffffffu, bad);
-            if (bad && lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
-          }
-          if (bad) {
+          if (d.mode == 2) {
             if (d.jb > 0) continue;  // whoever holds the first tile writes the rows
-            d.mode = 2;
             d.n = 0;
           } else if (d.n < d.tiles) {
             d.mode = 1;
@@ -710,12 +738,15 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.hpg = a.Hq / a.Hkv;
   p.tpt = kRows / p.hpg;
+  p.nslots = a.seq.Tq / (2 * p.tpt) + a.seq.B;
   p.scale_log2 = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   WsHeader* header = static_cast<WsHeader*>(a.ws);
   p.status = &header->status;
   p.arrivals = header->arrivals;
+  p.queue = &header->queue;
+  if (int64_t(p.nslots) * a.Hkv >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
   if (pf_splits(a.seq.Tk)) {
     char* w = static_cast<char*>(a.ws) + kWsHeader;
     p.part = reinterpret_cast<float*>(w);

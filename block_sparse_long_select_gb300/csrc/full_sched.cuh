@@ -58,6 +58,7 @@ struct Share {
   int64_t total, each;  // all cost; a share's (the first `more` shares have one more)
   int G, more;
   int64_t lo, hi;  // the share, in cost
+  int longest;     // cost of the longest item
   Place cur;
 
   __device__ __forceinline__ int64_t border(int i) const { return each * i + min(i, more); }
@@ -108,8 +109,10 @@ struct Share {
     if (item_len(place->w, p.step, place->x) > p.whole) return pos;
     return pos - place->at < c / 2 ? place->at : place->at + c;
   }
-  __device__ __forceinline__ bool init(int cta, int ctas) {
+  // All cost, and whether there is any.
+  __device__ __forceinline__ bool measure(int ctas) {
     total = 0;
+    longest = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int lane = threadIdx.x & 31;
       const SeqWork w = b0 + lane < B ? f(b0 + lane) : SeqWork{0, 0, 0, 0};
@@ -117,12 +120,21 @@ struct Share {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
       total += y;
+      longest = max(longest, __reduce_max_sync(0xffffffffu, w.items > 0 ? item_len(w, p.step, w.items - 1) : 0));
     }
     total *= Hkv;
     G = int(max(min(total / p.least_run, int64_t(ctas)), int64_t(1)));
-    if (total == 0 || cta >= G) return false;
     each = total / G;
     more = int(total - each * G);
+    return total > 0;
+  }
+  // Where equal shares would hold several items each, items are handed out
+  // whole, one after the other, long ones first: no joins, and the last ones
+  // are short. Equal shares serve few or very long items.
+  __device__ __forceinline__ bool hand_out() const { return longest + p.fixed <= each / 2; }
+  // The CTA's share (measure first).
+  __device__ __forceinline__ bool init(int cta) {
+    if (cta >= G) return false;
     Place other;
     lo = settle(border(cta), &cur);
     hi = settle(border(cta + 1), &other);

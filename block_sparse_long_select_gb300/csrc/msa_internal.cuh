@@ -21,7 +21,8 @@ struct WsHeader {
   // full-attention prefill: a byte per CTA of its grid, zero between calls; a
   // call that timed out may leave counts, which msa_read_status clears
   uint32_t arrivals[(kNumSMs + 3) / 4];
-  uint32_t reserved[62 - (kNumSMs + 3) / 4];
+  uint32_t queue;  // full-attention prefill: next item to hand out, zero between calls
+  uint32_t reserved[61 - (kNumSMs + 3) / 4];
 };
 static_assert(sizeof(WsHeader) == kWsHeader, "the header is the workspace's first 256 bytes");
 
