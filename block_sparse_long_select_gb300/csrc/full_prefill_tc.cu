@@ -27,9 +27,9 @@
 // Bound: the tensor cores (4 Hq d FLOPs per visible pair).
 //
 // Warps: 0 loads (TMA; zeroes the value rows behind a sequence's end, which
-// may hold anything), 1 MMA issue and TMEM, 2 the items, 3 rows that see no
-// key, 4-7 and 8-11 the two softmax warpgroups, one thread per row. Every wait
-// is bounded.
+// may hold anything), 1 MMA issue and TMEM, 2 the items and the rows
+// that see no key (3 idles), 4-7 and 8-11 the two softmax warpgroups, one thread per
+// row. Every wait is bounded.
 #include "full_sched.cuh"
 #include "full_tc.cuh"
 
@@ -81,7 +81,7 @@ struct PfSmem {
   static constexpr uint32_t oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile, oStore = oV + kStages * kTile;
   static constexpr uint32_t kStore = 32 * 128;  // per softmax warp: 32 rows x 64 columns
   static constexpr uint32_t oItem = oStore + 8 * kStore, oBar = oItem + kItems * sizeof(PfItem);
-  static constexpr int kBars = 4 + 4 * kStages + 2 + 4 + 4 + 2 * kItems + 2 + 2;
+  static constexpr int kBars = 4 + 4 * kStages + 2 + 2 + 4 + 2 * kItems + 2 + 2;
   static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
 };
 
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t* v_full = k_empty + NS;      // [NS]
   uint64_t* v_empty = v_full + NS;      // [NS]
   uint64_t* s_full = v_empty + NS;      // [2]
-  uint64_t* p_full = s_full + 2;        // [2][2]: row tile, half of the keys
-  uint64_t* o_full = p_full + 4;        // [2]
+  uint64_t* p_full = s_full + 2;        // [2]
+  uint64_t* o_full = p_full + 2;        // [2]
   uint64_t* o_empty = o_full + 2;       // [2]
   uint64_t* item_full = o_empty + 2;    // [NI]
   uint64_t* item_empty = item_full + NI;  // [NI]
@@ -123,8 +123,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   volatile int* last_flag = abort_flag + 1;
   if (threadIdx.x == 0) {
     for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
-    for (int x = 0; x < 4; ++x) tc::mbar_init(p_full + x, 4);
-    for (int x = 0; x < 2; ++x) tc::mbar_init(o_empty + x, 4);
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(p_full + x, 4);
+      tc::mbar_init(o_empty + x, 4);
+    }
     for (int x = 0; x < NI; ++x) tc::mbar_init(item_empty + x, 10);  // loads, MMA, 8 softmax warps
     tc::mbar_init(part_bar, 8);
     *abort_flag = 0;
@@ -240,13 +242,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     } else if (warp == 1) {
       // ----------------------------- MMA issue -----------------------------
+      // One thread for both row tiles: issued by a thread each, their products
+      // interleave and both finish late (504 us instead of 431 at 8K tokens).
       if (lane == 0) {
         constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
         const uint32_t qa = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oQ), 16);
         const uint32_t ka = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oK), 16);
         const uint32_t va = tc::smem_desc_lo(tc::smem_u32(pf_smem + SM::oV), kHalfTile);
-        auto scores = [&](int w, int z) {  // S_w = Q_w K^T
-          const uint32_t q0 = qa + ((w * SM::kTile) >> 4), k0 = ka + (((z % NS) * SM::kTile) >> 4);
+        auto scores = [&](int w, uint32_t st) {  // S_w = Q_w K^T
+          const uint32_t q0 = qa + ((w * SM::kTile) >> 4), k0 = ka + ((st * SM::kTile) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
@@ -254,17 +258,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           tc::mma_commit(&s_full[w]);
         };
-        auto values = [&](int w, int z, int half, bool first) {  // O_w += P_w V over half of the keys
-          const uint32_t v0 = va + (((z % NS) * SM::kTile) >> 4);
-#pragma unroll
-          for (int x = 0; x < kKeys / 32; ++x) {
-            const int kk = half * (kKeys / 32) + x;
-            tc::mma_f16_ts_lo<kHi>(tmem + kColO + w * D, tmem + w * 128 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdO,
-                                   first && kk == 0 ? 0u : 1u);
-          }
-        };
         bool ok = true;
-        int z = 0, used = 0;  // tiles and items so far
+        uint32_t z = 0, used = 0;  // tiles and items so far
         for (int it = 0; ok; ++it) {
           if (!(ok = tc::mbar_wait(&item_full[it % NI], (it / NI) & 1, abort_flag))) break;
           const int mode = items[it % NI].mode, n = items[it % NI].n;
@@ -276,35 +271,37 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                      tc::mbar_wait(&k_full[z % NS], (z / NS) & 1, abort_flag)))
             break;
           tc::fence_after_sync();
-          scores(0, z);
+          scores(0, z % NS);
           if (n == 1) tc::mma_commit(&q_empty[0]);
           if (!(ok = tc::mbar_wait(&q_full[1], used & 1, abort_flag))) break;
-          scores(1, z);
+          scores(1, z % NS);
           if (n == 1) tc::mma_commit(&q_empty[1]);
           tc::mma_commit(&k_empty[z % NS]);
           for (int j = 0; j < n && ok; ++j, ++z) {
-            const int st = z % NS, st1 = (z + 1) % NS;
-            if (!(ok = tc::mbar_wait(&v_full[st], (z / NS) & 1, abort_flag))) break;
+            const uint32_t st = z % NS, st1 = (z + 1) % NS;
+            // what is ready early is waited for first: every wait between products costs the pipe
+            if (!(ok = tc::mbar_wait(&v_full[st], (z / NS) & 1, abort_flag) &&
+                       (j + 1 == n || tc::mbar_wait(&k_full[st1], ((z + 1) / NS) & 1, abort_flag))))
+              break;
+            const uint32_t v0 = va + ((st * SM::kTile) >> 4);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               // O of the item before has been read
               if (j == 0 && !(ok = tc::mbar_wait(&o_empty[w], (used & 1) ^ 1, abort_flag))) break;
-              // the first half's product runs while the softmax forms the second half
-              if (!(ok = tc::mbar_wait(&p_full[2 * w], z & 1, abort_flag))) break;
+              if (!(ok = tc::mbar_wait(&p_full[w], z & 1, abort_flag))) break;
               tc::fence_after_sync();
-              values(w, z, 0, j == 0);
-              if (!(ok = tc::mbar_wait(&p_full[2 * w + 1], z & 1, abort_flag))) break;
-              tc::fence_after_sync();
-              values(w, z, 1, false);
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)  // O_w += P_w V
+                tc::mma_f16_ts_lo<kHi>(tmem + kColO + w * D, tmem + w * 128 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdO,
+                                       j > 0 || kk > 0 ? 1u : 0u);
+              if (j + 1 < n)
+                scores(w, st1);  // in issue order behind the product that reads P: S may go over it
+              else
+                tc::mma_commit(&o_full[w]);
               if (w == 1) tc::mma_commit(&v_empty[st]);
               if (j + 1 < n) {
-                // in issue order behind the product that reads P: S may go over it
-                if (w == 0 && !(ok = tc::mbar_wait(&k_full[st1], ((z + 1) / NS) & 1, abort_flag))) break;
-                scores(w, z + 1);
-                if (j + 2 == n) tc::mma_commit(&q_empty[w]);
                 if (w == 1) tc::mma_commit(&k_empty[st1]);
-              } else {
-                tc::mma_commit(&o_full[w]);
+                if (j + 2 == n) tc::mma_commit(&q_empty[w]);
               }
             }
           }
@@ -375,7 +372,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const int sb = find_slot_tile(p.seq.cu_q, p.seq.B, w2, p.nslots - 1 - next / p.Hkv, tile);  // late rows first
           if (sb < 0) continue;
           const SeqSpan s = seq_span(p.seq, sb);
-          if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: warp 3
+          if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
           PfItem d{};
           describe(d, sb, next % p.Hkv, tile, s);
           d.n = d.mode == 2 ? 0 : d.tiles;
@@ -411,9 +408,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         publish(d);
       }
       if (!ok) fail();
-    } else {
       // --------------------- rows that see no key ---------------------
-      const int w2 = 2 * p.tpt;
       for (int b0 = 0; b0 < p.seq.B; b0 += 32) {
         SeqSpan s{};
         int rows = 0;  // of the sequence, from its first on
@@ -530,11 +525,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           return m == -INFINITY ? 0.f : -m;
         };
-        auto hand_over = [&](int half) {
+        auto hand_over = [&]() {
           tc::tmem_st_wait();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&p_full[2 * w + half]);
+          if (lane == 0) tc::mbar_arrive(&p_full[w]);
         };
         if (j < j_mask) {  // every row sees the whole tile
           uint32_t v[kKeys];
@@ -554,8 +549,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               pk[x] = pack_bf16(p0, p1);
             }
             tc::tmem_st_32x32b_x32(sbase + c * 32, pk);
-            hand_over(c);
           }
+          hand_over();
           // the sum, off the tensor cores' path
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -599,8 +594,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               for (int x = 0; x < 16; ++x) pk[x] = 0u;
             }
             tc::tmem_st_32x32b_x16(sbase + c * 16, pk);
-            if (c & 1) hand_over(c >> 1);
           }
+          hand_over();
           l += l2[0] + l2[1];
         }
       }
