@@ -3,16 +3,16 @@
 //   dS_ij = P_ij (dout_i . v_j - delta_i)
 //   dv_j = sum_i P_ij dout_i;  dk_j = scale sum_i dS_ij q_i;  dq_i = scale sum_j dS_ij k_j
 //
-// Two kernels, each of which owns what it sums, so that nothing is added
-// atomically and every run gives the same bits: dk and dv per key tile over the
-// rows that see it, dq per row tile over the keys it sees. That is seven
+// Two kinds of CTAs in one launch, each of which owns what it sums, so that
+// nothing is added atomically and every run gives the same bits: dk and dv per
+// key tile over the rows that see it, dq per row tile over the keys it sees. That is seven
 // products per tile pair instead of the five that one kernel with atomic dq
 // sums would take; the order of its sums would change from run to run, and
 // each pair would send 64 KB of fp32 adds to L2. Row tiles are 128 / hpg tokens x
 // the hpg heads of a group, as in the forward: the sum over a group's heads is
 // part of the product.
 //
-// Bound: the tensor cores. Both kernels split their epilogue in two so that the
+// Bound: the tensor cores. Both kinds split their epilogue in two so that the
 // tensor cores work through it: from the scores to P (kept in registers) while
 // the products of the tile before and dP run, then from dP to dS while the next
 // scores run. P and dS are rounded to bf16 for the products that read them
@@ -31,7 +31,7 @@ constexpr int kFbThreads = 384;
 
 struct FbParams {
   SeqMap seq;
-  int Hq, Hkv, hpg, tpt, nslots;
+  int Hq, Hkv, hpg, tpt, kslots, qslots;
   float scale, scale_log2;
   const float2* rows;  // [Hkv][Tq][hpg]: lse in log2 units, delta (full_common.cu)
   __nv_bfloat16 *dq, *dk, *dv;
@@ -121,21 +121,14 @@ __device__ __forceinline__ void sum_partials(uint32_t part, int rows, int rank, 
 // TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV, dK
 // ---------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kFbThreads, 1)
-    full_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const FbParams p) {
+__device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
+                                        const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work, int cl,
+                                        int rank) {
   using SM = FbSmem<D>;
   constexpr int NH = D / 64, NR = SM::kRowSlots;
   constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
   constexpr uint32_t kColDv = 256, kColDk = 256 + D;
-  extern __shared__ __align__(1024) uint8_t fb_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (tc::smem_u32(fb_smem) & 1023u) {
-    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
-    return;
-  }
-  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   const int g = work % p.Hkv;
   int kt;
   const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, work / p.Hkv, kt);  // early keys: most rows
@@ -299,9 +292,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
         if (!(ok = tc::mbar_wait(bar.p_full, i & 1, abort_flag))) break;
         tc::fence_after_sync();
         sums(kColDv, 0, minor(o), i == 0);
-        // dP of this tile is complete before the epilogue can hand over dS, but
-        // dO's slot is free only behind dV: issued here, tracked by this commit
-        tc::mma_commit(bar.e_empty + st);
+        tc::mma_commit(bar.e_empty + st);  // dP and dV of this tile have read dO
         if (i + 1 < n) {  // over P, behind the product that reads it
           if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
           dots(0, ka, major(q1));
@@ -447,24 +438,17 @@ __global__ void __launch_bounds__(kFbThreads, 1)
 // TMEM: S of even tiles [0, 128), dP [128, 256) (dS over it), dQ [256, 256 + D), S of odd tiles [384, 512)
 // ---------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kFbThreads, 1)
-    full_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const FbParams p) {
+__device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
+                                       const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work, int cl,
+                                       int rank) {
   using SM = FbSmem<D>;
   constexpr int NH = D / 64;
   constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
   constexpr uint32_t kColDq = 256;
-  extern __shared__ __align__(1024) uint8_t fb_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (tc::smem_u32(fb_smem) & 1023u) {
-    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
-    return;
-  }
-  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   const int g = work % p.Hkv;
   int rt;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.nslots - 1 - work / p.Hkv, rt);  // late rows first
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.qslots - 1 - work / p.Hkv, rt);  // late rows first
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.rows_ok) {
@@ -605,7 +589,9 @@ __global__ void __launch_bounds__(kFbThreads, 1)
           dots(s_col(j + 1), qa, major(SM::oC + st1 * SM::kTile));
           tc::mma_commit(bar.s_full);
         }
-        if (!(ok = tc::mbar_wait(bar.ds_full, j & 1, abort_flag))) break;
+        if (!(ok = (j + 1 == n || tc::mbar_wait(bar.e_full + st1, ph1, abort_flag)) &&
+                   tc::mbar_wait(bar.ds_full, j & 1, abort_flag)))
+          break;
         tc::fence_after_sync();
         const uint32_t kb = minor(SM::oC + st * SM::kTile);
 #pragma unroll
@@ -614,7 +600,6 @@ __global__ void __launch_bounds__(kFbThreads, 1)
                                  j == 0 && kk == 0 ? 0u : 1u);
         tc::mma_commit(bar.c_empty + st);
         if (j + 1 < n) {
-          if (!(ok = tc::mbar_wait(bar.e_full + st1, ph1, abort_flag))) break;
           dots(128, oa, major(SM::oE + st1 * SM::kTile));
           tc::mma_commit(bar.dp_full);
           tc::mma_commit(bar.e_empty + st1);
@@ -701,6 +686,25 @@ __global__ void __launch_bounds__(kFbThreads, 1)
   cluster_sync();  // nobody leaves while its partial is read
 }
 
+// Key tiles first (their walks over rows x heads are the longest), then row
+// tiles, which fill the SMs as the former run out.
+template <int D>
+__global__ void __launch_bounds__(kFbThreads, 1)
+    full_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ FbParams p) {
+  extern __shared__ __align__(1024) uint8_t fb_smem[];
+  if (tc::smem_u32(fb_smem) & 1023u) {  // the swizzled operands need 1024-byte alignment
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
+    return;
+  }
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl, nk = p.kslots * p.Hkv;
+  if (work < nk)
+    bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, fb_smem, work, cl, rank);
+  else
+    bwd_dq<D>(tmQ, tmO, tmK, tmV, p, fb_smem, work - nk, cl, rank);
+}
+
 template <int D>
 cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   const FullArgs& f = a.f;
@@ -717,8 +721,9 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.status = &static_cast<WsHeader*>(f.ws)->status;
-  const int qslots = f.seq.Tq / p.tpt + f.seq.B, kslots = f.seq.Tk / kKeys + f.seq.B;
-  const int64_t qc = int64_t(qslots) * f.Hkv, kc = int64_t(kslots) * f.Hkv;
+  p.qslots = f.seq.Tq / p.tpt + f.seq.B;
+  p.kslots = f.seq.Tk / kKeys + f.seq.B;
+  const int64_t ctas = (int64_t(p.qslots) + p.kslots) * f.Hkv;
   CUtensorMap tmQ, tmO, tmK, tmV;
   if (!map_rows(&tmQ, f.q, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) || !map_rows(&tmO, a.dout, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) ||
       !map_keys(&tmK, f.k, f.seq.Tk, f.Hkv, D, kKeys) || !map_keys(&tmV, f.v, f.seq.Tk, f.Hkv, D, kKeys))
@@ -726,16 +731,8 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   constexpr int bytes = FbSmem<D>::kTotal;
   cudaError_t e;
   if ((e = launch_full_bwd_rows(a, stream))) return e;
-  {
-    ProfScope pf("full_bwd_dkv", stream);
-    p.nslots = kslots;
-    if ((e = launch_clusters(full_bwd_dkv_kernel<D>, kc, cluster_split(kc, (f.seq.Tq + p.tpt - 1) / p.tpt), kFbThreads,
-                             bytes, stream, tmQ, tmO, tmK, tmV, p)))
-      return e;
-  }
-  ProfScope pf("full_bwd_dq", stream);
-  p.nslots = qslots;
-  return launch_clusters(full_bwd_dq_kernel<D>, qc, cluster_split(qc, (f.seq.Tk + kKeys - 1) / kKeys), kFbThreads, bytes,
+  ProfScope pf("full_bwd", stream);
+  return launch_clusters(full_bwd_kernel<D>, ctas, cluster_split(ctas, (f.seq.Tk + kKeys - 1) / kKeys), kFbThreads, bytes,
                          stream, tmQ, tmO, tmK, tmV, p);
 }
 

@@ -8,36 +8,44 @@ namespace {
 // Per row: lse in log2 units (+inf where no key is seen, so that the row's
 // weights are 0) and delta = dout . out, laid out as the backward's row tiles,
 // [Hkv][Tq][hpg]. A thread per 16-byte chunk; bound by HBM (out and dout once).
+constexpr int kRowsPer = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restrict__ out, const uint4* __restrict__ dout,
                                                             const float* __restrict__ lse, int Tq, int Hq, int hpg,
                                                             float2* __restrict__ rows) {
-  constexpr int kPer = 16 / sizeof(T), kLanes = D / kPer;
-  const int64_t x = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  constexpr int kPer = 16 / sizeof(T), kLanes = D / kPer, kStep = 256 / kLanes;
+  const int64_t n = int64_t(Tq) * Hq, x0 = int64_t(blockIdx.x) * kStep * kRowsPer + threadIdx.x / kLanes;
   const int c = threadIdx.x % kLanes;
-  const bool in = x < int64_t(Tq) * Hq;
-  float s = 0.f;
-  if (in) {
-    const uint4 a = out[x * kLanes + c], b = dout[x * kLanes + c];
-    const T *ta = reinterpret_cast<const T*>(&a), *tb = reinterpret_cast<const T*>(&b);
+  uint4 a[kRowsPer], b[kRowsPer];  // all loads in flight at once
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s = fmaf(to_f(ta[i]), to_f(tb[i]), s);
+  for (int r = 0; r < kRowsPer; ++r) {
+    const int64_t x = min(x0 + r * kStep, n - 1);
+    a[r] = out[x * kLanes + c];
+    b[r] = dout[x * kLanes + c];
   }
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (in && c == 0) {
-    const int64_t t = x / Hq;
-    const int h = int(x % Hq);
-    const float l = lse[x];
-    rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] =
-        make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+  for (int r = 0; r < kRowsPer; ++r) {
+    const int64_t x = x0 + r * kStep;
+    const T *ta = reinterpret_cast<const T*>(&a[r]), *tb = reinterpret_cast<const T*>(&b[r]);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s = fmaf(to_f(ta[i]), to_f(tb[i]), s);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (x < n && c == 0) {
+      const int64_t t = x / Hq;
+      const int h = int(x % Hq);
+      const float l = lse[x];
+      rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] =
+          make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+    }
   }
 }
 
 template <typename T, int D>
 cudaError_t bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
   const FullArgs& f = a.f;
-  const int64_t threads = int64_t(f.seq.Tq) * f.Hq * (D * int(sizeof(T)) / 16);
+  const int64_t threads = (int64_t(f.seq.Tq) * f.Hq + kRowsPer - 1) / kRowsPer * (D * int(sizeof(T)) / 16);
   ProfScope pf("full_bwd_rows", stream);
   full_bwd_rows_kernel<T, D><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(
       static_cast<const uint4*>(f.out), static_cast<const uint4*>(a.dout), f.lse, f.seq.Tq, f.Hq, f.Hq / f.Hkv,
