@@ -11,21 +11,14 @@
 // columns. 32 rows and not 64 because several small CTAs per SM hide each
 // other's barriers, and short calls need the number of CTAs. Rows that belong
 // to no pair arrive as zeros.
-#include "full_internal.cuh"
-#include "tc_utils.cuh"
+#include "full_tc.cuh"
 
 namespace msa {
 namespace {
 
 constexpr int kF32Threads = 128, kA = 32, kB = 64;  // resident rows, streamed rows
 constexpr int kPitch = kB + 4;                      // floats of a row of the 32 x 64 results
-constexpr float kF32Log2e = 1.4426950408889634f, kF32Ln2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float ex2s(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void cp16f(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -140,6 +133,37 @@ __device__ __forceinline__ void store_rows(float* dst, const float (&acc)[D / 16
         make_float4(acc[4 * c] * mul, acc[4 * c + 1] * mul, acc[4 * c + 2] * mul, acc[4 * c + 3] * mul);
 }
 
+// The thread's 4 rows into a partial [rows][D] in shared memory, from row r0 on.
+template <int D>
+__device__ __forceinline__ void put_rows(uint32_t part, int r0, const float (&acc)[4][D / 16]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at<D>(part, r0 + ty * 4 + i, tx + 16 * c)),
+                   "f"(acc[i][4 * c]), "f"(acc[i][4 * c + 1]), "f"(acc[i][4 * c + 2]), "f"(acc[i][4 * c + 3])
+                   : "memory");
+}
+// This rank's slice of `rows` rows, summed over the cluster in rank order:
+// dst(row) is where a row goes (null: nowhere), mul(row) its factor.
+template <int D, typename F, typename M>
+__device__ __forceinline__ void sum_ranks(uint32_t part, int rows, int rank, int cl, F dst, M mul) {
+  const int per = rows / cl;
+  for (int x = threadIdx.x; x < per * (D / 4); x += kF32Threads) {
+    const int r = rank * per + x / (D / 4), c = x % (D / 4);
+    float* to = dst(r);
+    if (!to) continue;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int y = 0; y < cl; ++y) {
+      const float4 f = ld_peer4(peer_addr(at<D>(part, r, c), y));
+      s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+    }
+    const float m = mul(r);
+    reinterpret_cast<float4*>(to)[c] = make_float4(s.x * m, s.y * m, s.z * m, s.w * m);
+  }
+}
+
 struct F32Params {
   const float *q, *k, *v, *dout;
   SeqMap seq;
@@ -223,14 +247,14 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
         mx = fmaxf(mx, sc[i][k]);
       }
       const float mn = fmaxf(m[i], row_max(mx));
-      const float a = m[i] == mn ? 1.f : ex2s(m[i] - mn), z = mn == -INFINITY ? 0.f : mn;
+      const float a = m[i] == mn ? 1.f : ex2(m[i] - mn), z = mn == -INFINITY ? 0.f : mn;
       m[i] = mn;
       l[i] *= a;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) acc[i][c] *= a;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        sc[i][k] = ex2s(sc[i][k] - z);
+        sc[i][k] = ex2(sc[i][k] - z);
         l[i] += sc[i][k];
       }
     }
@@ -251,7 +275,7 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
     const int64_t row = row_of(p, s, g, x);
     const bool some = den > 0.f || den != den;
     store_rows<D>(p.out + row * D, acc[i], some ? 1.f / den : 0.f);
-    if (p.lse && tx == 0) p.lse[row] = some ? (m[i] + log2f(den)) * kF32Ln2 : -INFINITY;
+    if (p.lse && tx == 0) p.lse[row] = some ? (m[i] + log2f(den)) * kLn2f : -INFINITY;
   }
 }
 
@@ -264,9 +288,10 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
   const uint32_t sq = tc::smem_u32(f32_smem), so = sq + kA * D * 4, sk = so + kA * D * 4, sv = sk + kB * D * 4,
                  sp = sv + kB * D * 4;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int g = blockIdx.x % p.Hkv;
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
+  const int g = work % p.Hkv;
   int tile;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - int(blockIdx.x / p.Hkv), tile, p.hpg);
+  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - work / p.Hkv, tile, p.hpg);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
@@ -289,7 +314,7 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
   }
-  for (int j = 0; j < n; ++j) {
+  for (int j = n * rank / cl; j < n * (rank + 1) / cl; ++j) {  // this CTA's key tiles
     load_tile<D, kB>(sk, p.k, [&](int r) { return key(p.k, j * kB + r); });
     load_tile<D, kB>(sv, p.k, [&](int r) { return key(p.v, j * kB + r); });
     cp_commit_f();
@@ -302,7 +327,7 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float pr = ex2s(fmaf(sc[i][k], p.scale_log2, -rd[i].x));
+        const float pr = ex2(fmaf(sc[i][k], p.scale_log2, -rd[i].x));
         sc[i][k] = j * kB + tx + 16 * k < vis[i] ? pr * (dp[i][k] - rd[i].y) : 0.f;
       }
     put(sp, sc);
@@ -312,11 +337,19 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
   }
   cp_commit_f();
   cp_wait_f<0>();
+  if (cl == 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int x = x0 + ty * 4 + i;
-    if (x < x1) store_rows<D>(p.dq + row_of(p, s, g, x) * D, acc[i], p.scale);
+    for (int i = 0; i < 4; ++i) {
+      const int x = x0 + ty * 4 + i;
+      if (x < x1) store_rows<D>(p.dq + row_of(p, s, g, x) * D, acc[i], p.scale);
+    }
+    return;
   }
+  put_rows<D>(sk, 0, acc);  // K is read
+  cluster_sync();
+  sum_ranks<D>(sk, kA, rank, cl, [&](int r) { return x0 + r < x1 ? p.dq + row_of(p, s, g, x0 + r) * D : nullptr; },
+               [&](int) { return p.scale; });
+  cluster_sync();  // nobody leaves while its partial is read
 }
 
 // ---------------------------------------------------------------------------------
@@ -329,9 +362,10 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
                  sp = so + kB * D * 4, sd = sp + kA * kPitch * 4;
   float2* srow = reinterpret_cast<float2*>(f32_smem + (2 * kA + 2 * kB) * D * 4 + 2 * kA * kPitch * 4);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int g = blockIdx.x % p.Hkv;
+  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
+  const int g = work % p.Hkv;
   int tile;
-  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kA, int(blockIdx.x / p.Hkv), tile);  // early keys: most rows
+  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kA, work / p.Hkv, tile);  // early keys: most rows
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.ok) {
@@ -352,7 +386,9 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
   }
-  for (int x0 = max(j0 - off, 0) * p.hpg / kB * kB; x0 < xn; x0 += kB) {
+  const int xs = max(j0 - off, 0) * p.hpg / kB * kB, n = max(xn - xs + kB - 1, 0) / kB;
+  for (int z = n * rank / cl; z < n * (rank + 1) / cl; ++z) {  // this CTA's row tiles
+    const int x0 = xs + z * kB;
     load_tile<D, kB>(sq, p.k, [&](int r) { return x0 + r < xn ? p.q + row_of(p, s, g, x0 + r) * D : nullptr; });
     load_tile<D, kB>(so, p.k, [&](int r) { return x0 + r < xn ? p.dout + row_of(p, s, g, x0 + r) * D : nullptr; });
     cp_commit_f();
@@ -370,7 +406,7 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
       const float2 rd = srow[tx + 16 * k];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float pr = ex2s(fmaf(sc[i][k], p.scale_log2, -rd.x));
+        const float pr = ex2(fmaf(sc[i][k], p.scale_log2, -rd.x));
         sc[i][k] = x0 + tx + 16 * k >= from[i] ? pr : 0.f;
         dp[i][k] = sc[i][k] * (dp[i][k] - rd.y);
       }
@@ -384,14 +420,27 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
   }
   cp_commit_f();
   cp_wait_f<0>();
+  if (cl == 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = j0 + ty * 4 + i;
-    if (j >= s.Lk) continue;
-    const int64_t row = ((int64_t(s.k0) + j) * p.Hkv + g) * D;
-    store_rows<D>(p.dk + row, ak[i], p.scale);
-    store_rows<D>(p.dv + row, av[i], 1.f);
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + ty * 4 + i;
+      if (j >= s.Lk) continue;
+      const int64_t row = ((int64_t(s.k0) + j) * p.Hkv + g) * D;
+      store_rows<D>(p.dk + row, ak[i], p.scale);
+      store_rows<D>(p.dv + row, av[i], 1.f);
+    }
+    return;
   }
+  put_rows<D>(sq, 0, ak);  // Q is read
+  put_rows<D>(sq, kA, av);
+  cluster_sync();
+  sum_ranks<D>(sq, 2 * kA, rank, cl,
+               [&](int r) {
+                 const int j = j0 + r % kA;
+                 return j < s.Lk ? (r < kA ? p.dk : p.dv) + ((int64_t(s.k0) + j) * p.Hkv + g) * D : nullptr;
+               },
+               [&](int r) { return r < kA ? p.scale : 1.f; });
+  cluster_sync();  // nobody leaves while its partial is read
 }
 
 F32Params params(const FullArgs& a) {
@@ -405,20 +454,23 @@ F32Params params(const FullArgs& a) {
   p.Hkv = a.Hkv;
   p.hpg = a.Hq / a.Hkv;
   p.scale = a.scale;
-  p.scale_log2 = a.scale * kF32Log2e;
+  p.scale_log2 = a.scale * kLog2e;
   p.status = &static_cast<WsHeader*>(a.ws)->status;
   return p;
 }
 
+// `split`: steps that a tile's walk may have at most, if a cluster may share it.
+// About four CTAs of this size per SM hide each other's latencies, so a cluster
+// is doubled until there are that many (a walk of 31 steps in 60 CTAs: 182 us
+// alone).
 template <typename K>
-cudaError_t run(const char* name, K kern, F32Params p, int slots, int bytes, cudaStream_t stream) {
+cudaError_t run(const char* name, K kern, F32Params p, int slots, int64_t split, int bytes, cudaStream_t stream) {
   const int64_t ctas = int64_t(slots) * p.Hkv;
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  int c = 1;
+  while (c < 8 && ctas * c * 2 <= 4 * kNumSMs && split >= 4 * c) c *= 2;
   ProfScope pf(name, stream);
   p.nslots = slots;
-  kern<<<unsigned(ctas), kF32Threads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_clusters(kern, ctas, c, kF32Threads, bytes, stream, p);
 }
 
 template <int D>
@@ -426,7 +478,7 @@ cudaError_t forward(const FullArgs& a, cudaStream_t stream) {
   F32Params p = params(a);
   p.out = static_cast<float*>(a.out);
   p.lse = a.lse;
-  return run("full_f32", full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B,
+  return run("full_f32", full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B, 1,
              (kA + 2 * kB) * D * 4 + kA * kPitch * 4, stream);
 }
 template <int D>
@@ -441,10 +493,11 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   if (cudaError_t e = launch_full_bwd_rows(a, stream)) return e;
   constexpr int m = kA * kPitch * 4;
   if (cudaError_t e = run("full_f32_dkv", full_f32_dkv_kernel<D>, p, f.seq.Tk / kA + f.seq.B,
+                          int64_t(f.seq.Tq) * p.hpg / kB,
                           (2 * kA + 2 * kB) * D * 4 + 2 * m + kB * 8, stream))
     return e;
   return run("full_f32_dq", full_f32_dq_kernel<D>, p, int(int64_t(f.seq.Tq) * p.hpg / kA) + f.seq.B,
-             (2 * kA + 2 * kB) * D * 4 + m, stream);
+             f.seq.Tk / kB, (2 * kA + 2 * kB) * D * 4 + m, stream);
 }
 
 }  // namespace
