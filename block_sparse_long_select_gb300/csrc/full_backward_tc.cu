@@ -22,6 +22,8 @@
 // infinities a weight of 0 would not silence), 1 MMA issue and TMEM, 4-11
 // epilogue: two threads per TMEM lane, 64 columns each. dkv: 2-3 fetch the
 // rows' lse and delta. Every wait is bounded.
+#include <type_traits>
+
 #include "full_tc.cuh"
 
 namespace msa {
@@ -72,6 +74,51 @@ struct FbBars {
 // bf16 pairs of 64 columns go over the first half of the 64 columns they came
 // from, so neither epilogue warpgroup writes where the other still reads.
 __device__ __forceinline__ uint32_t a_col(int kk) { return uint32_t((kk >> 2) * 64 + (kk & 3) * 8); }
+// Walks of up to this many tiles keep what the rounding of dS to bf16 leaves off
+// as a second bf16 term with a product of its own. With few terms to average
+// over, the rounding can cost a gradient half of its last bit again; and here a
+// product more costs nothing, the time is latency. Long walks would pay a
+// quarter (dk) or a third (dq) more tensor work for an error that stays below
+// that of rounding the result.
+constexpr int kFineTiles = 4;
+// 64 columns of dP become dS (in pr, by `make` 32 at a time) and go back over
+// them: bf16 pairs in the first half, their remainders, if wanted, in the second.
+template <typename F>
+__device__ __forceinline__ void put_ds(uint32_t taddr, float (&pr)[64], bool fine, F make) {
+  if (!fine) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t v[32], pk[16];
+      tc::tmem_ld_32x32b_x32(taddr + c * 32, v);
+      tc::tmem_ld_wait();
+      make(c, v);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(pr[c * 32 + 2 * x], pr[c * 32 + 2 * x + 1]);
+      tc::tmem_st_32x32b_x16(taddr + c * 16, pk);
+    }
+    return;
+  }
+  // the remainders go where the second half of dP is: all of it is read first
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[32];
+    tc::tmem_ld_32x32b_x32(taddr + c * 32, v);
+    tc::tmem_ld_wait();
+    make(c, v);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16], lo[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float a = pr[c * 32 + 2 * x], b = pr[c * 32 + 2 * x + 1];
+      pk[x] = pack_bf16(a, b);
+      lo[x] = pack_bf16(a - __uint_as_float(pk[x] << 16), b - __uint_as_float(pk[x] & 0xffff0000u));
+    }
+    tc::tmem_st_32x32b_x16(taddr + c * 16, pk);
+    tc::tmem_st_32x32b_x16(taddr + 32 + c * 16, lo);
+  }
+}
 
 template <int D>
 __device__ __forceinline__ void store_acc(uint32_t taddr, int cols, __nv_bfloat16* dst, float mul, bool in) {
@@ -153,6 +200,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   }
   // this CTA's row tiles [r0, r0 + n)
   const int r0 = rf + int(int64_t(tiles) * rank / cl), n = rf + int(int64_t(tiles) * (rank + 1) / cl) - r0;
+  const bool fine = tiles <= kFineTiles;
   uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
   const FbBars bar(bars, NR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -285,31 +333,39 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
         dots(128, va, major(SM::oE));
         tc::mma_commit(bar.dp_full);
       }
-      for (int i = 0; i < n && ok; ++i) {
-        const uint32_t st = i & 1, q = SM::oC + st * SM::kTile, o = SM::oE + st * SM::kTile;
-        const uint32_t st1 = st ^ 1, ph1 = ((i + 1) >> 1) & 1;
-        const uint32_t q1 = SM::oC + st1 * SM::kTile, o1 = SM::oE + st1 * SM::kTile;
-        if (!(ok = tc::mbar_wait(bar.p_full, i & 1, abort_flag))) break;
-        tc::fence_after_sync();
-        sums(kColDv, 0, minor(o), i == 0);
-        tc::mma_commit(bar.e_empty + st);  // dP and dV of this tile have read dO
-        if (i + 1 < n) {  // over P, behind the product that reads it
-          if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
-          dots(0, ka, major(q1));
-          tc::mma_commit(bar.s_full);
+      // a loop of its own for walks with the second term: a branch in the issuing thread's loop costs 8 %
+      auto walk = [&](auto second) {
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t st = i & 1, q = SM::oC + st * SM::kTile, o = SM::oE + st * SM::kTile;
+          const uint32_t st1 = st ^ 1, ph1 = ((i + 1) >> 1) & 1;
+          const uint32_t q1 = SM::oC + st1 * SM::kTile, o1 = SM::oE + st1 * SM::kTile;
+          if (!(ok = tc::mbar_wait(bar.p_full, i & 1, abort_flag))) break;
+          tc::fence_after_sync();
+          sums(kColDv, 0, minor(o), i == 0);
+          tc::mma_commit(bar.e_empty + st);  // dP and dV of this tile have read dO
+          if (i + 1 < n) {  // over P, behind the product that reads it
+            if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
+            dots(0, ka, major(q1));
+            tc::mma_commit(bar.s_full);
+          }
+          if (!(ok = tc::mbar_wait(bar.ds_full, i & 1, abort_flag))) break;
+          tc::fence_after_sync();
+          sums(kColDk, 128, minor(q), i == 0);
+          if constexpr (decltype(second)::value) sums(kColDk, 128 + 32, minor(q), false);
+          tc::mma_commit(bar.c_empty + st);
+          if (i + 1 < n) {
+            if (!(ok = tc::mbar_wait(bar.e_full + st1, ph1, abort_flag))) break;
+            dots(128, va, major(o1));
+            tc::mma_commit(bar.dp_full);
+          } else {
+            tc::mma_commit(bar.acc_full);
+          }
         }
-        if (!(ok = tc::mbar_wait(bar.ds_full, i & 1, abort_flag))) break;
-        tc::fence_after_sync();
-        sums(kColDk, 128, minor(q), i == 0);
-        tc::mma_commit(bar.c_empty + st);
-        if (i + 1 < n) {
-          if (!(ok = tc::mbar_wait(bar.e_full + st1, ph1, abort_flag))) break;
-          dots(128, va, major(o1));
-          tc::mma_commit(bar.dp_full);
-        } else {
-          tc::mma_commit(bar.acc_full);
-        }
-      }
+      };
+      if (fine)
+        walk(std::true_type{});
+      else
+        walk(std::false_type{});
       if (!ok) fail();
       int zero = 0;
       tc::mma_commit(bar.done);
@@ -380,21 +436,18 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
       if (lane == 0) tc::mbar_arrive(bar.p_full);
       if (!(ok = warp_wait(bar.dp_full, i & 1, abort_flag))) break;
       tc::fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32], pk[16];
-        tc::tmem_ld_32x32b_x32(sbase + 128 + w * 64 + c * 32, v);
-        tc::tmem_ld_wait();
+      auto ds_of = [&](int c, const uint32_t* v) {  // over P
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           const float4 d = d4[c * 8 + x];
-          const float* q = pr + c * 32 + 4 * x;
-          pk[2 * x] = pack_bf16(q[0] * (__uint_as_float(v[4 * x]) - d.x), q[1] * (__uint_as_float(v[4 * x + 1]) - d.y));
-          pk[2 * x + 1] =
-              pack_bf16(q[2] * (__uint_as_float(v[4 * x + 2]) - d.z), q[3] * (__uint_as_float(v[4 * x + 3]) - d.w));
+          float* q = pr + c * 32 + 4 * x;
+          q[0] *= __uint_as_float(v[4 * x]) - d.x;
+          q[1] *= __uint_as_float(v[4 * x + 1]) - d.y;
+          q[2] *= __uint_as_float(v[4 * x + 2]) - d.z;
+          q[3] *= __uint_as_float(v[4 * x + 3]) - d.w;
         }
-        tc::tmem_st_32x32b_x16(sbase + 128 + w * 64 + c * 16, pk);
-      }
+      };
+      put_ds(sbase + 128 + w * 64, pr, fine, ds_of);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -470,6 +523,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   }
   // this CTA's key tiles [jb, jb + n)
   const int jb = int(int64_t(tiles) * rank / cl), n = int(int64_t(tiles) * (rank + 1) / cl) - jb;
+  const bool fine = tiles <= kFineTiles;
   uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
   const FbBars bar(bars, SM::kRowSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -581,32 +635,42 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
         tc::mma_commit(bar.dp_full);
         tc::mma_commit(bar.e_empty);
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t st = j & 1, st1 = st ^ 1, ph1 = ((j + 1) >> 1) & 1;
-        if (j + 1 < n) {
-          // the other S buffer: its tile j - 1 was read before dS(j - 1), whose product is issued
-          if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
-          dots(s_col(j + 1), qa, major(SM::oC + st1 * SM::kTile));
-          tc::mma_commit(bar.s_full);
+      auto walk = [&](auto second) {
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t st = j & 1, st1 = st ^ 1, ph1 = ((j + 1) >> 1) & 1;
+          if (j + 1 < n) {
+            // the other S buffer: its tile j - 1 was read before dS(j - 1), whose product is issued
+            if (!(ok = tc::mbar_wait(bar.c_full + st1, ph1, abort_flag))) break;
+            dots(s_col(j + 1), qa, major(SM::oC + st1 * SM::kTile));
+            tc::mma_commit(bar.s_full);
+          }
+          if (!(ok = (j + 1 == n || tc::mbar_wait(bar.e_full + st1, ph1, abort_flag)) &&
+                     tc::mbar_wait(bar.ds_full, j & 1, abort_flag)))
+            break;
+          tc::fence_after_sync();
+          const uint32_t kb = minor(SM::oC + st * SM::kTile);
+          auto sums = [&](uint32_t src, bool first) {
+  #pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc::mma_f16_ts_lo<kHi>(tmem + kColDq, tmem + src + a_col(kk), kb + ((kk * 16 * 128) >> 4), kIdA,
+                                     first && kk == 0 ? 0u : 1u);
+          };
+          sums(128, j == 0);
+          if constexpr (decltype(second)::value) sums(128 + 32, false);
+          tc::mma_commit(bar.c_empty + st);
+          if (j + 1 < n) {
+            dots(128, oa, major(SM::oE + st1 * SM::kTile));
+            tc::mma_commit(bar.dp_full);
+            tc::mma_commit(bar.e_empty + st1);
+          } else {
+            tc::mma_commit(bar.acc_full);
+          }
         }
-        if (!(ok = (j + 1 == n || tc::mbar_wait(bar.e_full + st1, ph1, abort_flag)) &&
-                   tc::mbar_wait(bar.ds_full, j & 1, abort_flag)))
-          break;
-        tc::fence_after_sync();
-        const uint32_t kb = minor(SM::oC + st * SM::kTile);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_f16_ts_lo<kHi>(tmem + kColDq, tmem + 128 + a_col(kk), kb + ((kk * 16 * 128) >> 4), kIdA,
-                                 j == 0 && kk == 0 ? 0u : 1u);
-        tc::mma_commit(bar.c_empty + st);
-        if (j + 1 < n) {
-          dots(128, oa, major(SM::oE + st1 * SM::kTile));
-          tc::mma_commit(bar.dp_full);
-          tc::mma_commit(bar.e_empty + st1);
-        } else {
-          tc::mma_commit(bar.acc_full);
-        }
-      }
+      };
+      if (fine)
+        walk(std::true_type{});
+      else
+        walk(std::false_type{});
       if (!ok) fail();
       int zero = 0;
       tc::mma_commit(bar.done);
@@ -643,17 +707,10 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
       }
       if (!(ok = warp_wait(bar.dp_full, j & 1, abort_flag))) break;
       tc::fence_after_sync();
+      put_ds(lbase + 128 + w * 64, pr, fine, [&](int c, const uint32_t* v) {  // over P
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32], pk[16];
-        tc::tmem_ld_32x32b_x32(lbase + 128 + w * 64 + c * 32, v);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          pk[x] = pack_bf16(pr[c * 32 + 2 * x] * (__uint_as_float(v[2 * x]) - rd.y),
-                            pr[c * 32 + 2 * x + 1] * (__uint_as_float(v[2 * x + 1]) - rd.y));
-        tc::tmem_st_32x32b_x16(lbase + 128 + w * 64 + c * 16, pk);
-      }
+        for (int x = 0; x < 32; ++x) pr[c * 32 + x] *= __uint_as_float(v[x]) - rd.y;
+      });
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
