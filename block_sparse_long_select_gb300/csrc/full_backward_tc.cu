@@ -205,7 +205,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   const FbBars bar(bars, NR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* rowd = reinterpret_cast<float*>(fb_smem + SM::oRow);  // slot x: lse2 [128], delta [128]
+  float* rowd = reinterpret_cast<float*>(fb_smem + SM::oRow);  // slot x: -lse2 [128], -delta [128]
   if (threadIdx.x == 0) {
     for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
     tc::mbar_init(bar.p_full, 8);
@@ -385,8 +385,8 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
       if (!(ok = warp_wait(bar.r_empty + sl, ((i / NR) & 1) ^ 1, abort_flag))) break;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        rowd[sl * 2 * kRows + x0 + 32 * y] = v[y].x;
-        rowd[sl * 2 * kRows + kRows + x0 + 32 * y] = v[y].y;
+        rowd[sl * 2 * kRows + x0 + 32 * y] = -v[y].x;
+        rowd[sl * 2 * kRows + kRows + x0 + 32 * y] = -v[y].y;
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar.r_full + sl);
@@ -395,6 +395,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   } else {
     // ------------------------------ epilogue ------------------------------
     const int w = (warp - 4) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
     const uint32_t sbase = tmem + (uint32_t(quarter * 32) << 16);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
@@ -415,11 +416,14 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
         tc::tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const float4 l = l4[c * 8 + x];
-          pr[c * 32 + 4 * x] = ex2(fmaf(__uint_as_float(v[4 * x]), p.scale_log2, -l.x));
-          pr[c * 32 + 4 * x + 1] = ex2(fmaf(__uint_as_float(v[4 * x + 1]), p.scale_log2, -l.y));
-          pr[c * 32 + 4 * x + 2] = ex2(fmaf(__uint_as_float(v[4 * x + 2]), p.scale_log2, -l.z));
-          pr[c * 32 + 4 * x + 3] = ex2(fmaf(__uint_as_float(v[4 * x + 3]), p.scale_log2, -l.w));
+          const float4 l = l4[c * 8 + x];  // negated
+          const float2 t0 = split(fma2(pair(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1])), scale2, pair(l.x, l.y)));
+          const float2 t1 =
+              split(fma2(pair(__uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3])), scale2, pair(l.z, l.w)));
+          pr[c * 32 + 4 * x] = ex2(t0.x);
+          pr[c * 32 + 4 * x + 1] = ex2(t0.y);
+          pr[c * 32 + 4 * x + 2] = ex2(t1.x);
+          pr[c * 32 + 4 * x + 3] = ex2(t1.y);
         }
         if (mask) {
 #pragma unroll
@@ -439,12 +443,12 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
       auto ds_of = [&](int c, const uint32_t* v) {  // over P
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const float4 d = d4[c * 8 + x];
+          const float4 d = d4[c * 8 + x];  // negated
           float* q = pr + c * 32 + 4 * x;
-          q[0] *= __uint_as_float(v[4 * x]) - d.x;
-          q[1] *= __uint_as_float(v[4 * x + 1]) - d.y;
-          q[2] *= __uint_as_float(v[4 * x + 2]) - d.z;
-          q[3] *= __uint_as_float(v[4 * x + 3]) - d.w;
+          const float2 t0 = split(mul2(pair(q[0], q[1]), add2(pair(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1])), pair(d.x, d.y))));
+          const float2 t1 = split(
+              mul2(pair(q[2], q[3]), add2(pair(__uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3])), pair(d.z, d.w))));
+          q[0] = t0.x, q[1] = t0.y, q[2] = t1.x, q[3] = t1.y;
         }
       };
       put_ds(sbase + 128 + w * 64, pr, fine, ds_of);
@@ -684,6 +688,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     const bool valid = r < p.tpt * p.hpg && i < i1;
     float2 rd = make_float2(INFINITY, 0.f);
     if (valid) rd = p.rows[(int64_t(g) * p.seq.Tq + s.q0 + i) * p.hpg + r % p.hpg];
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), lse2 = pair(-rd.x, -rd.x), dlt2 = pair(-rd.y, -rd.y);
     const int vis = s.Lk - s.Lq + i + 1;
     const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys - jb;  // tiles below it are seen whole by every row
     bool ok = true;
@@ -698,7 +703,11 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
         tc::tmem_ld_32x32b_x32(lbase + s_col(j) + w * 64 + c * 32, v);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) pr[c * 32 + x] = ex2(fmaf(__uint_as_float(v[x]), p.scale_log2, -rd.x));
+        for (int x = 0; x < 16; ++x) {
+          const float2 t = split(fma2(pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), scale2, lse2));
+          pr[c * 32 + 2 * x] = ex2(t.x);
+          pr[c * 32 + 2 * x + 1] = ex2(t.y);
+        }
       }
       if (j >= j_mask) {
 #pragma unroll
@@ -709,7 +718,11 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
       tc::fence_after_sync();
       put_ds(lbase + 128 + w * 64, pr, fine, [&](int c, const uint32_t* v) {  // over P
 #pragma unroll
-        for (int x = 0; x < 32; ++x) pr[c * 32 + x] *= __uint_as_float(v[x]) - rd.y;
+        for (int x = 0; x < 16; ++x) {
+          float* q = pr + c * 32 + 2 * x;
+          const float2 t = split(mul2(pair(q[0], q[1]), add2(pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), dlt2)));
+          q[0] = t.x, q[1] = t.y;
+        }
       });
       tc::tmem_st_wait();
       tc::fence_before_sync();

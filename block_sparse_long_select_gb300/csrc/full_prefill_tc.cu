@@ -538,26 +538,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int c = 0; c < 4; ++c) m4[c] = tc::tmem_ld_max_32x32b_x32(sbase + c * 32, v + c * 32);
           tc::tmem_ld_wait();
           const float neg = raise(fmaxf(tc::fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.scale_log2);
+          const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[32];
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const float p0 = ex2(fmaf(__uint_as_float(v[c * 64 + 2 * x]), p.scale_log2, neg));
-              const float p1 = ex2(fmaf(__uint_as_float(v[c * 64 + 2 * x + 1]), p.scale_log2, neg));
-              v[c * 64 + x] = __float_as_uint(p0 + p1);
+              uint32_t* e = v + c * 64 + 2 * x;
+              const float2 t = split(fma2(pair(__uint_as_float(e[0]), __uint_as_float(e[1])), scale2, neg2));
+              const float p0 = ex2(t.x), p1 = ex2(t.y);
+              e[0] = __float_as_uint(p0);
+              e[1] = __float_as_uint(p1);
               pk[x] = pack_bf16(p0, p1);
             }
             tc::tmem_st_32x32b_x32(sbase + c * 32, pk);
           }
           hand_over();
           // the sum, off the tensor cores' path
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int x = 0; x < 32; ++x) l4[x & 3] += __uint_as_float(v[c * 64 + x]);
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          for (int x = 0; x < kKeys / 2; ++x)
+            l2[x & 1] = add2(l2[x & 1], pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])));
+          const float2 ls = split(add2(l2[0], l2[1]));
+          l += ls.x + ls.y;
         } else {
           // the causal edge, 32 columns at a time; those that no row of the warp sees are only zeroed
           const int lim = vis - j * kKeys;  // columns below it are seen
