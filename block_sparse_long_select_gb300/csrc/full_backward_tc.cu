@@ -374,6 +374,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   } else if (warp < 4) {
     // --------------------------- lse and delta ---------------------------
     const int x0 = (warp - 2) * 64 + lane;
+    tc::griddep_wait();  // the rows' data are the previous grid's
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int sl = i % NR, t0 = (r0 + i) * p.tpt;
@@ -686,6 +687,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     const uint32_t lbase = tmem + (uint32_t(quarter * 32) << 16);
     const int i = i0 + r / p.hpg;
     const bool valid = r < p.tpt * p.hpg && i < i1;
+    tc::griddep_wait();  // the rows' data are the previous grid's
     float2 rd = make_float2(INFINITY, 0.f);
     if (valid) rd = p.rows[(int64_t(g) * p.seq.Tq + s.q0 + i) * p.hpg + r % p.hpg];
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), lse2 = pair(-rd.x, -rd.x), dlt2 = pair(-rd.y, -rd.y);
@@ -803,7 +805,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   if ((e = launch_full_bwd_rows(a, stream))) return e;
   ProfScope pf("full_bwd", stream);
   return launch_clusters(full_bwd_kernel<D>, ctas, cluster_split(ctas, (f.seq.Tk + kKeys - 1) / kKeys), kFbThreads, bytes,
-                         stream, tmQ, tmO, tmK, tmV, p);
+                         true, stream, tmQ, tmO, tmK, tmV, p);
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // Full attention: what every element type shares. The rows' lse and delta for
 // the backward, and the outputs of calls without any key or any query row.
 #include "full_internal.cuh"
+#include "tc_utils.cuh"
 
 namespace msa {
 namespace {
@@ -16,6 +17,7 @@ __global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restr
   constexpr int kPer = 16 / sizeof(T), kLanes = D / kPer, kStep = 256 / kLanes;
   const int64_t n = int64_t(Tq) * Hq, x0 = int64_t(blockIdx.x) * kStep * kRowsPer + threadIdx.x / kLanes;
   const int c = threadIdx.x % kLanes;
+  tc::griddep_launch_dependents();  // the next grid waits for this one's writes
   uint4 a[kRowsPer], b[kRowsPer];  // all loads in flight at once
 #pragma unroll
   for (int r = 0; r < kRowsPer; ++r) {

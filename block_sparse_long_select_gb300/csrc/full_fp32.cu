@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
   }
+  tc::griddep_wait();  // the rows' data are the previous grid's
   const int xs = max(j0 - off, 0) * p.hpg / kB * kB, n = max(xn - xs + kB - 1, 0) / kB;
   for (int z = n * rank / cl; z < n * (rank + 1) / cl; ++z) {  // this CTA's row tiles
     const int x0 = xs + z * kB;
@@ -464,13 +465,14 @@ F32Params params(const FullArgs& a) {
 // is doubled until there are that many (a walk of 31 steps in 60 CTAs: 182 us
 // alone).
 template <typename K>
-cudaError_t run(const char* name, K kern, F32Params p, int slots, int64_t split, int bytes, cudaStream_t stream) {
+cudaError_t run(const char* name, K kern, F32Params p, int slots, int64_t split, int bytes, bool early,
+                cudaStream_t stream) {
   const int64_t ctas = int64_t(slots) * p.Hkv;
   int c = 1;
   while (c < 8 && ctas * c * 2 <= 4 * kNumSMs && split >= 4 * c) c *= 2;
   ProfScope pf(name, stream);
   p.nslots = slots;
-  return launch_clusters(kern, ctas, c, kF32Threads, bytes, stream, p);
+  return launch_clusters(kern, ctas, c, kF32Threads, bytes, early, stream, p);
 }
 
 template <int D>
@@ -479,7 +481,7 @@ cudaError_t forward(const FullArgs& a, cudaStream_t stream) {
   p.out = static_cast<float*>(a.out);
   p.lse = a.lse;
   return run("full_f32", full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B, 1,
-             (kA + 2 * kB) * D * 4 + kA * kPitch * 4, stream);
+             (kA + 2 * kB) * D * 4 + kA * kPitch * 4, false, stream);
 }
 template <int D>
 cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
@@ -494,10 +496,10 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   constexpr int m = kA * kPitch * 4;
   if (cudaError_t e = run("full_f32_dkv", full_f32_dkv_kernel<D>, p, f.seq.Tk / kA + f.seq.B,
                           int64_t(f.seq.Tq) * p.hpg / kB,
-                          (2 * kA + 2 * kB) * D * 4 + 2 * m + kB * 8, stream))
+                          (2 * kA + 2 * kB) * D * 4 + 2 * m + kB * 8, true, stream))
     return e;
   return run("full_f32_dq", full_f32_dq_kernel<D>, p, int(int64_t(f.seq.Tq) * p.hpg / kA) + f.seq.B,
-             f.seq.Tk / kB, (2 * kA + 2 * kB) * D * 4 + m, stream);
+             f.seq.Tk / kB, (2 * kA + 2 * kB) * D * 4 + m, false, stream);
 }
 
 }  // namespace

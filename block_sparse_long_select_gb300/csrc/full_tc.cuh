@@ -127,9 +127,11 @@ inline int cluster_split(int64_t ctas, int64_t steps) {
   while (c < 8 && ctas * c * 2 <= kNumSMs && steps >= 8 * c) c *= 2;
   return c;
 }
+// `early`: the grid may start while the one before it in the stream ends (it
+// waits for that one's writes itself).
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kern)(P...), int64_t ctas, int cluster, int threads, int smem, cudaStream_t stream,
-                            A... args) {
+cudaError_t launch_clusters(void (*kern)(P...), int64_t ctas, int cluster, int threads, int smem, bool early,
+                            cudaStream_t stream, A... args) {
   if (ctas * cluster >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
   cudaLaunchConfig_t cfg{};
@@ -137,12 +139,14 @@ cudaError_t launch_clusters(void (*kern)(P...), int64_t ctas, int cluster, int t
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
