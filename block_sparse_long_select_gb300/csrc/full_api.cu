@@ -55,7 +55,7 @@ inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale :
 
 size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
-  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(B, Hq, Hkv, d) : 0;
+  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
   if (Nq < 0 || !rows_ok(Nq, Hq) || (op == MSA_OP_FULL_BACKWARD && !rows_ok(Nk, Hkv))) return 0;
   if (op == MSA_OP_FULL_PREFILL && dtype == MSA_BF16) return kWsHeader + full_prefill_ws_bytes(d, Nk);
   if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);

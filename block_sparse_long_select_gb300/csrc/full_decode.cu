@@ -7,8 +7,8 @@
 //
 // Work: the keys of every (sequence, key/value head, group of up to 16 query
 // heads) -- an item -- are cut into units of 64, the units of all items are
-// numbered through, and each CTA of a fixed grid takes an equal run of them,
-// so ragged lengths balance whatever they are, without the host knowing them.
+// numbered through, and each CTA of a fixed grid (one per SM) takes an equal run
+// of them, so ragged lengths balance whatever they are, without the host knowing them.
 // In a unit each warp takes 16 keys, which lie in one page, and works alone:
 // its own ring of cp.async copies (keys past the end arrive as zeros), scores,
 // running maximum and sum, products. Warps meet only where an item ends in the
@@ -26,9 +26,7 @@
 namespace msa {
 namespace {
 
-constexpr int kFdWarps = 4, kFdThreads = kFdWarps * 32;
 constexpr int kSub = 16;                  // keys of a warp's step: never across a page
-constexpr int kUnit = kFdWarps * kSub;    // keys of a unit
 constexpr int kFdMaxHeads = 16;           // query heads of an item
 constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
@@ -348,18 +346,20 @@ struct FdParams {
   float scale_log2;
   float* part_o;   // [2 * grid][16][D]
   float* part_ml;  // [2 * grid][16][2]: maximum (log2 units), sum; a negative sum marks a page out of range
-  int* arrivals;   // [B * Hkv * ngr], zero between calls
+  uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
   void* out;
   float* lse;
   uint32_t* status;
 };
 
+template <int UNIT>
 __device__ __forceinline__ int units_of(const FdParams& p, int b) {
   const int L = p.kv_len[b];
-  return L > 0 && L <= p.cap ? (L + kUnit - 1) / kUnit : 0;
+  return L > 0 && L <= p.cap ? (L + UNIT - 1) / UNIT : 0;
 }
 
 // A walk over a CTA's run of units in order.
+template <int UNIT>
 struct Walk {
   int b, it, u, n;  // sequence, item within it, unit within the item, units of the item
   __device__ __forceinline__ void next(const FdParams& p) {
@@ -368,25 +368,31 @@ struct Walk {
     if (++it < p.Hkv * p.ngr) return;
     it = 0;
     do {
-      n = ++b < p.B ? units_of(p, b) : 1;  // past the last sequence the walk is over
+      n = ++b < p.B ? units_of<UNIT>(p, b) : 1;  // past the last sequence the walk is over
     } while (n == 0);
   }
 };
 
+// Eight warps where their rings fit, one CTA per SM: the copies in flight are
+// what covers HBM's latency.
 template <typename T, int D, int H>
 struct FdShape {
   using C = Core<T, D, H>;
-  static constexpr int kStages = sizeof(T) == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);
-  static constexpr int kRing = kStages * C::kStage;                       // per warp
-  static constexpr int kJoin = 3 * (C::kAcc + 2 * C::kM + 1) * 32 * 4;   // three warps' states
-  static constexpr int kBytes = kFdWarps * (kRing + C::kExtra) + kJoin;
+  static constexpr bool kWide = sizeof(T) == 4 && D == 128;
+  static constexpr int kWarps = kWide ? 4 : 8, kThreads = kWarps * 32;
+  static constexpr int kUnit = kWarps * kSub;  // keys of a unit
+  static constexpr int kStages = kWide ? 2 : sizeof(T) == 4 ? (H <= 4 ? 3 : 2) : D == 64 ? (H <= 8 ? 6 : 4) : H <= 8 ? 3 : 2;
+  static constexpr int kRing = kStages * C::kStage;                                   // per warp
+  static constexpr int kState = (C::kAcc + 2 * C::kM + 1) * 32;                       // floats of a warp's state
+  static constexpr int kJoin = (kWarps - 1) * kState * 4;                             // a slot per hand-over
+  static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
 };
 
 template <typename T, int D, int H>
-__global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel(const FdParams p) {
+__global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_kernel(const FdParams p) {
   using SH = FdShape<T, D, H>;
   using C = typename SH::C;
-  constexpr int NS = SH::kStages;
+  constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads, kUnit = SH::kUnit;
   constexpr int kCpr = D * int(sizeof(T)) / 16;  // 16-byte chunks of a row
   extern __shared__ __align__(128) uint8_t fd_smem[];
   __shared__ int last_s;
@@ -399,9 +405,9 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
 
   // ---- this CTA's run of units (every warp finds it alone) ----
   int64_t total = 0;
-  const int units0 = lane < p.B ? units_of(p, lane) : 0;
+  const int units0 = lane < p.B ? units_of<kUnit>(p, lane) : 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int64_t y = b0 == 0 ? units0 : b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
+    int64_t y = b0 == 0 ? units0 : b0 + lane < p.B ? units_of<kUnit>(p, b0 + lane) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
     total += y;
@@ -411,17 +417,17 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
   const int64_t run0 = blockIdx.x * per, run1 = min(run0 + per, total);
   // sequences without keys: nobody's run holds them
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (units_of(p, b) > 0) continue;
+    if (units_of<kUnit>(p, b) > 0) continue;
     if (threadIdx.x == 0 && (p.kv_len[b] < 0 || p.kv_len[b] > p.cap)) set_status(p.status, MSA_ERR_BOUNDS);
     for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
     if (p.lse)
       for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
   }
   if (run0 >= run1) return;
-  Walk at{};
+  Walk<kUnit> at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int mine = b0 == 0 ? units0 : b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
+    const int mine = b0 == 0 ? units0 : b0 + lane < p.B ? units_of<kUnit>(p, b0 + lane) : 0;
     int64_t incl = int64_t(mine) * items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -443,10 +449,10 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
   int64_t item_first = first + int64_t(at.it) * at.n;  // number of the item's first unit
 
   // ---- copies: the walk `ld` runs ahead of `at` ----
-  Walk ld = at;
+  Walk<kUnit> ld = at;
   int64_t ld_left = run1 - run0;
   uint32_t bad_ring = 0;  // stage x's page was out of range
-  auto page_of = [&](const Walk& w) {
+  auto page_of = [&](const Walk<kUnit>& w) {
     const int key = w.u * kUnit + warp * kSub;
     return key < p.kv_len[w.b] ? p.pages.table[int64_t(w.b) * p.pages.max_pages + (key >> p.pages.page_log2)] : 0;
   };
@@ -507,13 +513,13 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
     if (valid > 0) c.step(ring + st * C::kStage, extra, valid, p.scale_log2);
     __syncwarp();
     st = (st + 1) % NS;
-    const int b = at.b, item = b * items + at.it, n = at.n;
+    const int b = at.b, n = at.n;
     const bool ends = at.u + 1 == at.n;
     if (!ends && z + 1 < run1) {
       ++at.u;
       continue;
     }
-    // ---- the item ends here: join the four warps' states (4 -> 2 -> 1) ----
+    // ---- the item ends here: join the warps' states, halving their number ----
     fresh = true;
     constexpr int kRegs = C::kAcc + 2 * C::kM + 1;
     auto put = [&](float* to) {
@@ -541,17 +547,17 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
         c.acc[x] = c.acc[x] * wa[C::m_index(x)] + from[x * 32 + lane] * wb[C::m_index(x)];
       bad |= from[(kRegs - 1) * 32 + lane] != 0.f;
     };
-    if (warp >= 2) put(join + (warp - 2) * kRegs * 32);
-    __syncthreads();
-    if (warp < 2) take(join + warp * kRegs * 32);
-    __syncthreads();
-    // a slot of its own: warps 2 and 3 may be at the next item's end while warp 0 reads this one
-    if (warp == 1) put(join + 2 * kRegs * 32);
-    __syncthreads();
+    // Every hand-over has a slot of its own: the upper warps may be at the next
+    // item's end while the lower ones still read this one's.
+#pragma unroll
+    for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
+      if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
+      __syncthreads();
+      if (warp < half) take(join + (slot0 + warp) * SH::kState);
+    }
     const bool whole = item_first >= run0 && ends;
     const int slot = 2 * int(blockIdx.x) + (item_first >= run0 ? 1 : 0);
     if (warp == 0) {
-      take(join + 2 * kRegs * 32);
       c.sum_l();
       if (__any_sync(0xffffffffu, bad)) {
         bad = true;
@@ -590,10 +596,14 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
         __syncwarp();
         if (lane == 0) {
           // releases the warp's stores (ordered by __syncwarp), acquires the others'
-          int old;
-          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.arrivals + item) : "memory");
-          last_s = old == c1 - c0;
-          if (last_s) p.arrivals[item] = 0;  // ready for the next call
+          const int sh = 8 * (c0 & 3);
+          uint32_t old;
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+                       : "=r"(old)
+                       : "l"(p.arrivals + (c0 >> 2)), "r"(1u << sh)
+                       : "memory");
+          last_s = int((old >> sh) & 0xffu) == c1 - c0;
+          if (last_s) atomicSub(p.arrivals + (c0 >> 2), uint32_t(c1 - c0 + 1) << sh);  // ready for the next call
         }
       }
       __syncthreads();
@@ -652,8 +662,7 @@ __global__ void __launch_bounds__(kFdThreads, H <= 8 ? 2 : 1) full_decode_kernel
   cp_wait<0>();
 }
 
-// Fixed grid: two CTAs per SM (the smaller shapes' shared memory allows it).
-int fd_grid() { return 2 * kNumSMs; }
+int fd_grid() { return kNumSMs; }
 
 template <typename T, int D, int H>
 cudaError_t decode(const FdParams& p, cudaStream_t stream) {
@@ -662,7 +671,7 @@ cudaError_t decode(const FdParams& p, cudaStream_t stream) {
   static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
   ProfScope pf("full_decode", stream);
-  kern<<<fd_grid(), kFdThreads, bytes, stream>>>(p);
+  kern<<<fd_grid(), FdShape<T, D, H>::kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -671,10 +680,9 @@ int head_groups(int hpg) { return (hpg + kFdMaxHeads - 1) / kFdMaxHeads; }
 
 }  // namespace
 
-size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d) {
+size_t full_decode_ws_bytes(int d) {
   const size_t slots = 2 * size_t(fd_grid());
-  return up256(slots * kFdMaxHeads * d * 4) + up256(slots * kFdMaxHeads * 8) +
-         up256(size_t(B) * Hkv * head_groups(Hq / Hkv) * 4);
+  return up256(slots * kFdMaxHeads * d * 4) + up256(slots * kFdMaxHeads * 8);
 }
 
 cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream) {
@@ -696,8 +704,7 @@ cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream) {
   p.part_o = reinterpret_cast<float*>(w);
   w += up256(slots * kFdMaxHeads * a.d * 4);
   p.part_ml = reinterpret_cast<float*>(w);
-  w += up256(slots * kFdMaxHeads * 8);
-  p.arrivals = reinterpret_cast<int*>(w);
+  p.arrivals = static_cast<WsHeader*>(a.ws)->arrivals;
   p.out = a.out;
   p.lse = a.lse;
   p.status = &static_cast<WsHeader*>(a.ws)->status;

@@ -110,7 +110,7 @@ struct FullBwdArgs {
   const void* dout;
   void *dq, *dk, *dv;
 };
-size_t full_decode_ws_bytes(int B, int Hq, int Hkv, int d);  // behind the header
+size_t full_decode_ws_bytes(int d);  // behind the header
 size_t full_backward_ws_bytes(int Tq, int Hq);  // behind the header
 size_t full_prefill_ws_bytes(int d, int64_t most_keys);  // bf16, behind the header
 // fp32 prefill and backward

@@ -18,8 +18,9 @@ constexpr int kMaxBs = 1024;
 struct WsHeader {
   uint32_t status;        // sticky msa_status_t set by kernels
   uint32_t work_counter;  // persistent-grid work queue head (reset per launch)
-  // full-attention prefill: a byte per CTA of its grid, zero between calls; a
-  // call that timed out may leave counts, which msa_read_status clears
+  // full-attention prefill and decode: a byte per CTA of their grids, zero
+  // between calls (in the header, because other operations write all that lies
+  // behind it); a call that timed out may leave counts, which msa_read_status clears
   uint32_t arrivals[(kNumSMs + 3) / 4];
   uint32_t queue;  // full-attention prefill: next item to hand out, zero between calls
   uint32_t reserved[61 - (kNumSMs + 3) / 4];
