@@ -359,7 +359,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (!sh.measure(gridDim.x)) {
         // no row sees a key
       } else if (sh.hand_out()) {
-        const int all = p.nslots * p.Hkv;
+        // Up to 32 sequences: a lane each, items by their place x in their sequence,
+        // the last places (the longest walks) first. More: by slots, where the
+        // last places of a sequence come first.
+        const bool few = p.seq.B <= 32;
+        const int mine = few && lane < p.seq.B ? work(lane).items : 0;
+        const int all = (few ? __reduce_add_sync(0xffffffffu, mine) : p.nslots) * p.Hkv;
+        int x = __reduce_max_sync(0xffffffffu, mine) - 1, before = 0;  // place; items before it
         for (int next = 0; ok && next < all;) {
           if (lane == 0) {
             next = int(atomicAdd(p.queue, 1u));
@@ -368,13 +374,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           next = __shfl_sync(0xffffffffu, next, 0);
           if (next >= all) break;
-          int tile;
-          const int sb = find_slot_tile(p.seq.cu_q, p.seq.B, w2, p.nslots - 1 - next / p.Hkv, tile);  // late rows first
-          if (sb < 0) continue;
-          const SeqSpan s = seq_span(p.seq, sb);
-          if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
+          int tile, sb, g = next % p.Hkv;
+          SeqSpan s;
+          if (few) {
+            uint32_t longer = __ballot_sync(0xffffffffu, mine > x);
+            while (next >= before + __popc(longer) * p.Hkv) {
+              before += __popc(longer) * p.Hkv;
+              --x;
+              longer = __ballot_sync(0xffffffffu, mine > x);
+            }
+            const int nth = (next - before) / p.Hkv;  // of the sequences that reach this place
+            g = (next - before) % p.Hkv;
+            sb = __ffs(__ballot_sync(0xffffffffu, mine > x && __popc(longer & ((1u << lane) - 1u)) == nth)) - 1;
+            s = seq_span(p.seq, sb);
+            tile = x + (s.Lk < s.Lq ? (s.Lq - s.Lk) / w2 : 0);
+          } else {
+            sb = find_slot_tile(p.seq.cu_q, p.seq.B, w2, p.nslots - 1 - next / p.Hkv, tile);
+            if (sb < 0) continue;
+            s = seq_span(p.seq, sb);
+            if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
+          }
           PfItem d{};
-          describe(d, sb, next % p.Hkv, tile, s);
+          describe(d, sb, g, tile, s);
           d.n = d.mode == 2 ? 0 : d.tiles;
           publish(d);
         }
