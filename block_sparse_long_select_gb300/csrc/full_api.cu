@@ -23,8 +23,8 @@ bool rows_ok(int64_t rows, int heads) { return rows * heads < (int64_t(1) << 31)
 msa_status_t check_pages(int num_pages, int page_size, int max_pages, PageMap* pm) {
   if (num_pages < 1 || max_pages < 1 || page_size < 1) return MSA_ERR_INVALID_ARG;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return MSA_ERR_UNSUPPORTED;
-  // key positions and cache rows are 32-bit (TMA coordinates)
-  if (int64_t(max_pages) * page_size >= (int64_t(1) << 31) || int64_t(num_pages) * page_size >= (int64_t(1) << 31))
+  // key positions and cache rows are 32-bit (TMA coordinates), with room for a tile behind the last
+  if (int64_t(max_pages) * page_size > (int64_t(1) << 30) || int64_t(num_pages) * page_size > (int64_t(1) << 30))
     return MSA_ERR_UNSUPPORTED;
   pm->num_pages = num_pages;
   pm->max_pages = max_pages;

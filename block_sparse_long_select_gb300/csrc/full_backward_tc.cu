@@ -181,14 +181,12 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, work / p.Hkv, kt);  // early keys: most rows
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
-  if (!s.ok) {
-    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-    return;
-  }
+  if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+  if (!s.keys_ok) return;
   const int j0 = kt * kKeys;
   const int off = s.Lk - s.Lq;              // row i sees keys j <= off + i
   const int rf = max(j0 - off, 0) / p.tpt;  // first row tile that sees one of these keys
-  const int tiles = max((s.Lq + p.tpt - 1) / p.tpt - rf, 0);
+  const int tiles = s.ok ? max((s.Lq + p.tpt - 1) / p.tpt - rf, 0) : 0;
   if (tiles == 0) {  // no row sees them
     if (rank > 0) return;
     for (int x = threadIdx.x; x < min(kKeys, s.Lk - j0) * (D / 8); x += kFbThreads) {

@@ -25,7 +25,8 @@ struct SeqMap {
 };
 struct SeqSpan {
   int q0, Lq, k0, Lk;  // k0: first packed key row (0 for paged keys)
-  bool rows_ok, ok;    // rows_ok: q0 and Lq can be trusted; ok: the keys too
+  bool rows_ok, keys_ok;  // q0 and Lq, k0 and Lk can be trusted
+  bool ok;                // both
 };
 __device__ __forceinline__ SeqSpan seq_span(const SeqMap& m, int b) {
   SeqSpan s;
@@ -42,13 +43,14 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqMap& m, int b) {
   if (m.kv_len) {
     s.k0 = 0;
     s.Lk = m.kv_len[b];
-    s.ok = s.rows_ok && s.Lk >= 0 && s.Lk <= m.Tk;
+    s.keys_ok = s.Lk >= 0 && s.Lk <= m.Tk;
   } else {
     const int a = m.cu_k[b], e = m.cu_k[b + 1];
     s.k0 = a;
-    s.ok = s.rows_ok && a >= 0 && a <= e && e <= m.Tk;
+    s.keys_ok = a >= 0 && a <= e && e <= m.Tk;
     s.Lk = e - a;
   }
+  s.ok = s.rows_ok && s.keys_ok;
   return s;
 }
 

@@ -304,12 +304,14 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  *                a sequence may be empty. Rows before cu[0] and from cu[B] on
  *                belong to no sequence: they are never read as data and stay
  *                as they were in every output.
+ *  Outputs overlap no input and no other output, except where a call allows it.
  *  Paged cache   k_cache, v_cache [num_pages, page_size, Hkv, d]; key j of
  *                sequence b is row j % page_size of page
  *                page_table[b][j / page_size], page_table [B, max_pages]
  *                int32. Entries past a sequence's last page are not read, and
  *                rows of a page past kv_len[b] never reach a result, whatever
- *                they hold. page_size is 16, 32, 64 or 128. Two sequences may
+ *                they hold. page_size is 16, 32, 64 or 128; num_pages and
+ *                max_pages times page_size are at most 2^30. Two sequences may
  *                share pages that are only read.
  *  Visibility    query row i of Lq sees keys j <= Lk - Lq + i of Lk: the last
  *                row sees every key. If Lq > Lk the first Lq - Lk rows see
@@ -319,7 +321,8 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  * Device-side checks: a sequence whose cu, kv_len or page entry is out of
  * range sets MSA_ERR_BOUNDS in the workspace status and nothing out of range is
  * read or written for it. If its rows are known (its cu is in range) its
- * output rows are 0 and their lse -inf; otherwise they stay as they were. */
+ * output rows are 0 and their lse -inf; otherwise they stay as they were.
+ * A workspace may serve all operations in turn, if it has the largest size. */
 
 /* Appends the keys and values of T packed new tokens to a paged cache, with
  * the position rotation applied on the way to keys and queries.
@@ -351,6 +354,7 @@ msa_status_t msa_paged_append(const void* q, const void* k_new, const void* v_ne
 /* Decode: one query row per sequence over the whole of its paged cache.
  *  q [B, Hq, d]; kv_len [B] int32, 0 <= kv_len[b] <= max_pages * page_size; a
  *  sequence of length 0 (a padded batch entry) gives out 0 and lse -inf
+ *  scale  softmax scale; <= 0 selects 1/sqrt(d)
  *  out [B, Hq, d] (dtype); lse [B, Hq] fp32 or NULL
  *  ws: msa_workspace_size(MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv,
  *  Hq, d, 0, 0, 0, dtype) (the size does not depend on the lengths)
@@ -364,6 +368,8 @@ msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void
  *  q [Tq, Hq, d]; k, v [Tk, Hkv, d]; cu_q, cu_k [B + 1] int32
  *  scale  softmax scale; <= 0 selects 1/sqrt(d)
  *  out [Tq, Hq, d] (dtype); lse [Tq, Hq] fp32 or NULL (as msa_sparse_attn_prefill)
+ *  ws: msa_workspace_size(MSA_OP_FULL_PREFILL, B, Tq, Tk, Hkv, Hq, d, 0, 0, 0,
+ *  dtype), with Tk = max_pages * page_size for the paged form
  *  Deterministic. BF16 rounds each key's weight exp(s - m) to bf16 before its
  *  product with v; the weights' sum takes it unrounded. Key and value rows of
  *  one sequence are multiplied by weight 0 where they lie behind a query, so

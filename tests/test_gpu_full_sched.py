@@ -164,3 +164,68 @@ def test_two_streams_at_once():
     for o in outs[0] + outs[1]:
         assert torch.equal(o, outs[0][0])
     fp.assert_within(outs[0][0], want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_backward_bad_offsets(dtype):
+    """Offsets out of range: reported; gradients whose rows are known become zero, the others stay."""
+    spans = [(40, 40), (30, 50), (20, 20)]
+    q, k, v, cu_q, cu_k, rows, ks, vs, g = make(spans, 8, 2, 64, dtype, 19)
+    fwd = fp.prefill(q, ks, vs, rows, 0.125, dtype)
+    dout = torch.randn(q.shape, generator=g).to(dtype)
+    good = [x.to(DEV) for x in (q, k, v, fwd[0].to(dtype), dout, fwd[1].float())]
+    ws = msa.workspace(1 << 20, DEV)
+
+    def run(cq, ck):
+        grads = [torch.full(x.shape, 7.0, dtype=dtype, device=DEV) for x in (q, k, v)]
+        msa.msa_full_attn_backward(*good, cq.to(DEV), ck.to(DEV), *grads, ws=ws)
+        assert msa.msa_read_status(ws) == 6
+        return grads
+
+    want, tol = fp.backward(*[x[:40].double() for x in (q, k, v, fwd[0].to(dtype), dout)], fwd[1][:40].float().double(),
+                            0.125, dtype)
+    bad = cu_q.clone()
+    bad[3] = 91
+    dq, dk, dv = run(bad, cu_k)
+    assert (dq[70:] == 7.0).all() and (dk[90:] == 0).all() and (dv[90:] == 0).all()
+    fp.assert_within(dk[:40], want[1], tol[1], "dk")
+    bad = cu_k.clone()
+    bad[3] = 111
+    dq, dk, dv = run(cu_q, bad)
+    assert (dq[70:] == 0).all() and (dk[90:] == 7.0).all() and (dv[90:] == 7.0).all()
+    fp.assert_within(dq[:40], want[0], tol[0], "dq")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_captured_training_step(dtype):
+    """Prefill (split items among them) and backward in a graph, replayed on new inputs."""
+    spans = [(200, 200), (7, 1500), (33, 33)]
+    first = make(spans, 8, 2, 64, dtype, 20)
+    d = [x.to(DEV) for x in first[:5]]
+    dout = torch.randn(first[0].shape, generator=first[8]).to(dtype)
+    out, lse, do = torch.empty_like(d[0]), torch.empty(d[0].shape[:2], device=DEV), dout.to(DEV)
+    grads = [torch.empty_like(x) for x in d[:3]]
+    size = max(msa.msa_workspace_size(op, 3, d[0].shape[0], d[1].shape[0], 2, 8, 64, 0, 0, 0, 0 if dtype == BF16 else 1)
+               for op in (msa.MSA_OP_FULL_PREFILL, msa.MSA_OP_FULL_BACKWARD))
+    ws = msa.workspace(size, DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        msa.msa_full_attn_prefill(*d, out=out, lse=lse, ws=ws)
+        msa.msa_full_attn_backward(*d[:3], out, do, lse, d[3], d[4], *grads, ws=ws)
+    for seed in (20, 21, 22):
+        q, k, v, _, _, rows, ks, vs, _ = make(spans, 8, 2, 64, dtype, seed)
+        for dst, src in zip(d, (q, k, v)):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert msa.msa_read_status(ws) == 0
+        want = fp.prefill(q, ks, vs, rows, 0.125, dtype)
+        fp.assert_within(out, want[0], want[2], "out")
+        k0 = 0
+        for (q0, Lq), kb, vb in zip(rows, ks, vs):
+            sl = slice(q0, q0 + Lq)
+            w, t = fp.backward(*[x.double() for x in (q[sl], kb, vb, out[sl].cpu(), dout[sl], lse[sl].cpu())], 0.125, dtype)
+            for name, gr, s2, x, y in zip(("dq", "dk", "dv"), grads, (sl, *[slice(k0, k0 + len(kb))] * 2), w, t):
+                fp.assert_within(gr[s2], x, y, name)
+            k0 += len(kb)
