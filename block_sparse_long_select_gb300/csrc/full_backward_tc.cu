@@ -495,8 +495,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
 // ---------------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
-                                       const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work, int cl,
-                                       int rank) {
+                                       const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work) {
   using SM = FbSmem<D>;
   constexpr int NH = D / 64;
   constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
@@ -513,10 +512,9 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   }
   const int i0 = rt * p.tpt, i1 = min(i0 + p.tpt, s.Lq);
   const int vis_last = s.ok ? s.Lk - s.Lq + i1 : 0;
-  const int tiles = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
-  if (tiles == 0) {
+  const int n = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
+  if (n == 0) {
     if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-    if (rank > 0) return;
     for (int x = threadIdx.x; x < (i1 - i0) * p.hpg * (D / 8); x += kFbThreads) {
       const int r = x / (D / 8);
       const int64_t row = (int64_t(s.q0) + i0 + r / p.hpg) * p.Hq + g * p.hpg + r % p.hpg;
@@ -524,9 +522,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     }
     return;
   }
-  // this CTA's key tiles [jb, jb + n)
-  const int jb = int(int64_t(tiles) * rank / cl), n = int(int64_t(tiles) * (rank + 1) / cl) - jb;
-  const bool fine = tiles <= kFineTiles;
+  const bool fine = n <= kFineTiles;
   uint64_t* bars = reinterpret_cast<uint64_t*>(fb_smem + SM::oBar);
   const FbBars bar(bars, SM::kRowSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -557,7 +553,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
 #pragma unroll
       for (int h = 0; h < NH; ++h) tc::tma_load_3d(dst + h * kHalfTile, map, full, h * 64, g, row);
     };
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       tc::mbar_arrive_expect_tx(bar.res_full, 2 * uint32_t(p.tpt * p.hpg) * D * 2);
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -568,28 +564,28 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     bool ok = true;
     int nc = 0, ne = 0, tails = 0;
     for (int j = 0; j < n && ok; ++j) {
-      const int st = j & 1, ph = (j >> 1) & 1, valid = s.Lk - (jb + j) * kKeys;
+      const int st = j & 1, ph = (j >> 1) & 1, valid = s.Lk - j * kKeys;
       uint8_t* kd = fb_smem + SM::oC + st * SM::kTile;
       uint8_t* vd = fb_smem + SM::oE + st * SM::kTile;
       if (!(ok = warp_wait(bar.c_empty + st, ph ^ 1, abort_flag))) break;
       if (valid >= kKeys) {
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.c_full + st, SM::kTile);
-          box(&tmK, kd, bar.c_full + st, s.k0 + (jb + j) * kKeys);
+          box(&tmK, kd, bar.c_full + st, s.k0 + j * kKeys);
         }
         ++nc;
         if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.e_full + st, SM::kTile);
-          box(&tmV, vd, bar.e_full + st, s.k0 + (jb + j) * kKeys);
+          box(&tmV, vd, bar.e_full + st, s.k0 + j * kKeys);
         }
         ++ne;
       } else {  // the keys behind the sequence's end become zeros
         if (!(ok = warp_wait(bar.e_empty + st, ph ^ 1, abort_flag))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar.tail, 2 * SM::kTile);
-          box(&tmK, kd, bar.tail, s.k0 + (jb + j) * kKeys);
-          box(&tmV, vd, bar.tail, s.k0 + (jb + j) * kKeys);
+          box(&tmK, kd, bar.tail, s.k0 + j * kKeys);
+          box(&tmV, vd, bar.tail, s.k0 + j * kKeys);
         }
         ++tails;
         if (!(ok = warp_wait(bar.tail, 0, abort_flag))) break;
@@ -690,12 +686,12 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     if (valid) rd = p.rows[(int64_t(g) * p.seq.Tq + s.q0 + i) * p.hpg + r % p.hpg];
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), lse2 = pair(-rd.x, -rd.x), dlt2 = pair(-rd.y, -rd.y);
     const int vis = s.Lk - s.Lq + i + 1;
-    const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys - jb;  // tiles below it are seen whole by every row
+    const int j_mask = max(s.Lk - s.Lq + i0 + 1, 0) / kKeys;  // tiles below it are seen whole by every row
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!(ok = warp_wait(bar.s_full, j & 1, abort_flag))) break;
       tc::fence_after_sync();
-      const int lim = vis - (jb + j) * kKeys - w * 64;  // columns below it are seen
+      const int lim = vis - j * kKeys - w * 64;  // columns below it are seen
       float pr[64];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -729,15 +725,13 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar.ds_full);
     }
-    if (ok && n > 0) ok = warp_wait(bar.acc_full, 0, abort_flag);
-    if (!ok) fail();
-    if (ok && n > 0) {
+    if (ok) ok = warp_wait(bar.acc_full, 0, abort_flag);
+    if (ok) {
       tc::fence_after_sync();
       const int64_t row = (int64_t(s.q0) + i) * p.Hq + g * p.hpg + r % p.hpg;
-      if (cl > 1)
-        put_partial<D>(tc::smem_u32(fb_smem), r, w * (D / 8), lbase + kColDq + w * (D / 2), D / 2);
-      else
-        store_acc<D>(lbase + kColDq + w * (D / 2), D / 2, p.dq + row * D + w * (D / 2), p.scale, valid);
+      store_acc<D>(lbase + kColDq + w * (D / 2), D / 2, p.dq + row * D + w * (D / 2), p.scale, valid);
+    } else {
+      fail();
     }
   }
   tc::fence_before_sync();
@@ -746,14 +740,6 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
-  if (cl == 1) return;
-  cluster_sync();
-  sum_partials<D>(tc::smem_u32(fb_smem), kRows, rank, cl, tiles, [&](int r, int c, float (&o)[8]) {
-    const int i = i0 + r / p.hpg;
-    if (r >= p.tpt * p.hpg || i >= i1) return;
-    store8(p.dq + ((int64_t(s.q0) + i) * p.Hq + g * p.hpg + r % p.hpg) * D, c, o, p.scale);
-  });
-  cluster_sync();  // nobody leaves while its partial is read
 }
 
 // Key tiles first (their walks over rows x heads are the longest), then row
@@ -768,11 +754,12 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
     return;
   }
-  const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl, nk = p.kslots * p.Hkv;
-  if (work < nk)
-    bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, fb_smem, work, cl, rank);
-  else
-    bwd_dq<D>(tmQ, tmO, tmK, tmV, p, fb_smem, work - nk, cl, rank);
+  // a cluster shares a key tile; row tiles are a CTA each
+  const int cl = cluster_size(), nk = p.kslots * p.Hkv, row = int(blockIdx.x) - nk * cl;
+  if (row < 0)
+    bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, fb_smem, blockIdx.x / cl, cl, cluster_rank());
+  else if (row < p.qslots * p.Hkv)  // the last cluster may have CTAs to spare
+    bwd_dq<D>(tmQ, tmO, tmK, tmV, p, fb_smem, row);
 }
 
 template <int D>
@@ -793,7 +780,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.status = &static_cast<WsHeader*>(f.ws)->status;
   p.qslots = f.seq.Tq / p.tpt + f.seq.B;
   p.kslots = f.seq.Tk / kKeys + f.seq.B;
-  const int64_t ctas = (int64_t(p.qslots) + p.kslots) * f.Hkv;
+  const int64_t kc = int64_t(p.kslots) * f.Hkv, qc = int64_t(p.qslots) * f.Hkv;
   CUtensorMap tmQ, tmO, tmK, tmV;
   if (!map_rows(&tmQ, f.q, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) || !map_rows(&tmO, a.dout, f.seq.Tq, f.Hq, f.Hkv, D, p.tpt) ||
       !map_keys(&tmK, f.k, f.seq.Tk, f.Hkv, D, kKeys) || !map_keys(&tmV, f.v, f.seq.Tk, f.Hkv, D, kKeys))
@@ -802,8 +789,9 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if ((e = launch_full_bwd_rows(a, stream))) return e;
   ProfScope pf("full_bwd", stream);
-  return launch_clusters(full_bwd_kernel<D>, ctas, cluster_split(ctas, (f.seq.Tk + kKeys - 1) / kKeys), kFbThreads, bytes,
-                         true, stream, tmQ, tmO, tmK, tmV, p);
+  const int c = cluster_split(kc, f.seq.Tq / f.seq.B / p.tpt);
+  return launch_clusters(full_bwd_kernel<D>, kc + (qc + c - 1) / c, c, kFbThreads, bytes, true, stream, tmQ, tmO, tmK, tmV,
+                         p);
 }
 
 }  // namespace

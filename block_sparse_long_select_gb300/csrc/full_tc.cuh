@@ -118,13 +118,15 @@ __device__ __forceinline__ void put_partial(uint32_t base, int r, int c0, uint32
                    : "memory");
   }
 }
-// CTAs of a cluster for `ctas` tiles that walk up to `steps` each: doubled while
-// the grid stays within one wave of SMs and every CTA keeps several steps. A CTA's
-// start and end cost about five steps, so splitting more than fills the SMs
-// loses (84 tiles of up to 28 steps: 47 us whole, 80 us in clusters of 8).
+// CTAs of a cluster for `ctas` tiles that walk `steps` each on average: doubled
+// while the grid stays within one wave of SMs and every CTA keeps several steps
+// (33 tiles of up to 512 steps: 774 us alone, 399 in twos, 210 in fours); once
+// more than that into two waves where walks are long and ragged (76 tiles of up
+// to 28 steps: 46.5 us alone, 39.1 in twos, 53.5 in fours; but 80 tiles of 3
+// steps: 28.7 alone, 38.7 in twos, because a CTA's start and end cost about five).
 inline int cluster_split(int64_t ctas, int64_t steps) {
   int c = 1;
-  while (c < 8 && ctas * c * 2 <= kNumSMs && steps >= 8 * c) c *= 2;
+  while (c < 8 && steps >= 8 * c && (ctas * c * 2 <= kNumSMs || (c == 1 && ctas <= kNumSMs))) c *= 2;
   return c;
 }
 // `early`: the grid may start while the one before it in the stream ends (it
