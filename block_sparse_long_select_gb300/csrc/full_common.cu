@@ -35,10 +35,10 @@ __global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restr
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (x < n && c == 0) {
-      const int64_t t = x / Hq;
-      const int h = int(x % Hq);
+      // rows are counted in 32 bits: a 64-bit division would cost more than the row's bytes
+      const uint32_t t = uint32_t(x) / uint32_t(Hq), h = uint32_t(x) % uint32_t(Hq);
       const float l = lse[x];
-      rows[(int64_t(h / hpg) * Tq + t) * hpg + h % hpg] =
+      rows[(int64_t(h / uint32_t(hpg)) * Tq + t) * hpg + h % uint32_t(hpg)] =
           make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
     }
   }
