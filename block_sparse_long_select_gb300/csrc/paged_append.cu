@@ -7,12 +7,24 @@
 // latency): one CTA per token; a thread's unit is one 16-byte chunk of a head
 // row and, for split pairs, the chunk rot / 2 dims further, so both elements
 // of every pair are in one thread's registers and q may be rotated in place.
+// A few tokens (a decode step) get as many threads as a token has units, so that
+// all loads are in flight at once (64 tokens: 7.4 us instead of 8.7 with 128
+// threads); with more tokens than fill the SMs, 128 threads each, which share
+// the search for the sequence among fewer warps (20924 tokens: 93 us instead of
+// 160).
 #include "full_internal.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kAppThreads = 128;
+constexpr int kAppThreads = 128, kAppMostThreads = 512, kAppFewTokens = 4 * kNumSMs;
+
+// x / d, exact while x d is below 2^32, by the rounded-up reciprocal 2^32 / d
+struct SmallDiv {
+  uint32_t m, d;
+  __host__ __device__ explicit SmallDiv(int n) : m(n > 1 ? uint32_t(0x100000000ull / uint32_t(n)) + 1u : 0u), d(n) {}
+  __device__ __forceinline__ int of(int x) const { return d == 1 ? x : int(__umulhi(uint32_t(x), m)); }
+};
 
 template <typename T>
 struct Chunk {
@@ -34,7 +46,8 @@ struct Chunk {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppMostThreads) paged_append_kernel(const AppendArgs a, const SmallDiv by_units,
+                                                                  const SmallDiv by_chunks) {
   constexpr int N = Chunk<T>::N;
   const int t = blockIdx.x;
   // every warp finds the token's sequence itself: no barrier
@@ -57,15 +70,15 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
   const int half = a.rot / 2, pu = half / N, units = pu + (a.d - a.rot) / N, chunks = a.d / N;
   const int qk = (qh + a.Hkv) * units, total = qk + a.Hkv * chunks;
   const float* cs = a.rope ? a.rope + pos * a.rot : nullptr;
-  for (int u = threadIdx.x; u < total; u += kAppThreads) {
+  for (int u = threadIdx.x; u < total; u += blockDim.x) {
     if (u >= qk) {  // values: copied
       if (row < 0) continue;
-      const int h = (u - qk) / chunks, c = (u - qk) % chunks;
+      const int h = by_chunks.of(u - qk), c = (u - qk) - h * chunks;
       *reinterpret_cast<uint4*>(static_cast<T*>(a.v_cache) + (row * a.Hkv + h) * a.d + c * N) =
           *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_new) + (int64_t(t) * a.Hkv + h) * a.d + c * N);
       continue;
     }
-    const int hh = u / units, w = u % units;
+    const int hh = by_units.of(u), w = u - hh * units;
     const bool is_q = hh < qh;
     const int h = is_q ? hh : hh - qh;
     const T* src = is_q ? static_cast<const T*>(a.q) + (int64_t(t) * a.Hq + h) * a.d
@@ -127,13 +140,21 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
 
 }  // namespace
 
-cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
+namespace {
+template <typename T>
+cudaError_t append(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int N = Chunk<T>::N;
+  const int units = a.rot / 2 / N + (a.d - a.rot) / N, chunks = a.d / N;
+  const int total = ((a.q ? a.Hq : 0) + a.Hkv) * units + a.Hkv * chunks;
+  const int threads = a.T > kAppFewTokens ? kAppThreads : total >= kAppMostThreads ? kAppMostThreads : (total + 31) / 32 * 32;
   ProfScope pf("paged_append", stream);
-  if (a.dtype == MSA_BF16)
-    paged_append_kernel<__nv_bfloat16><<<a.T, kAppThreads, 0, stream>>>(a);
-  else
-    paged_append_kernel<float><<<a.T, kAppThreads, 0, stream>>>(a);
+  paged_append_kernel<T><<<a.T, threads, 0, stream>>>(a, SmallDiv(units), SmallDiv(chunks));
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
+  return a.dtype == MSA_BF16 ? append<__nv_bfloat16>(a, stream) : append<float>(a, stream);
 }
 
 }  // namespace msa
