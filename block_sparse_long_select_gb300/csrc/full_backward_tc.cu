@@ -18,6 +18,9 @@
 // scores run. P and dS are rounded to bf16 for the products that read them
 // (2^-8 each, averaging out over the sums); sums stay in fp32.
 //
+// Measured (Hq 32, Hkv 8, d 128): 8192 tokens 1.29 ms alone, 1.35 ms in a loop
+// (74 % of the measured tensor rate on the seven products, 52 % on five).
+//
 // Warps of both: 0 loads (TMA; zeroes rows of other sequences, whose
 // infinities a weight of 0 would not silence), 1 MMA issue and TMEM, 4-11
 // epilogue: two threads per TMEM lane, 64 columns each. dkv: 2-3 fetch the
@@ -649,7 +652,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
           tc::fence_after_sync();
           const uint32_t kb = minor(SM::oC + st * SM::kTile);
           auto sums = [&](uint32_t src, bool first) {
-  #pragma unroll
+#pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
               tc::mma_f16_ts_lo<kHi>(tmem + kColDq, tmem + src + a_col(kk), kb + ((kk * 16 * 128) >> 4), kIdA,
                                      first && kk == 0 ? 0u : 1u);

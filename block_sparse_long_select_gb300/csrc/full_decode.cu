@@ -4,6 +4,8 @@
 //   out = sum_j exp(s_j - lse) v_j,  s_j = scale q . k_j,  j < kv_len
 //
 // Bound: HBM (every key and value is read once; 4 hpg FLOPs per element).
+// Measured (Hq 32, Hkv 8, d 128, bf16): 16 sequences of 4 K to 128 K keys 557 us,
+// 6.55 TB/s (97 % of the measured copy rate); one of 777 keys 12 us, latency.
 //
 // Work: the keys of every (sequence, key/value head, group of up to 16 query
 // heads) -- an item -- are cut into units of 64, the units of all items are

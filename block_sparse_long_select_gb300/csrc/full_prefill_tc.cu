@@ -24,7 +24,10 @@
 // (full_sched.cuh), and the rows of an item that several CTAs share are joined
 // by the last of them to arrive.
 //
-// Bound: the tensor cores (4 Hq d FLOPs per visible pair).
+// Bound: the tensor cores (4 Hq d FLOPs per visible pair); in fact the chain from
+// a tile's scores to its weights, about 1.4 us a tile of 2 x 128 rows where the
+// products alone take 1.05. Measured (Hq 32, Hkv 8, d 128): 8192 tokens 393 us
+// alone, 405 us in a loop (71 % of the measured tensor rate).
 //
 // Warps: 0 loads (TMA; zeroes the value rows behind a sequence's end, which
 // may hold anything), 1 MMA issue and TMEM, 2 the items and the rows
