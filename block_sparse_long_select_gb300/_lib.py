@@ -321,14 +321,17 @@ def msa_sparse_attn_backward(q, k, v, out, dout, lse, sel, q_offset, kv_len, Bs,
 # ---- full attention and paged caches -----------------------------------------
 # These calls serve single tokens too, where the host's time counts: a tensor's
 # checks are one call each, and streams and devices are only switched if needed.
-def _fits(t, dtype, dev, shape) -> bool:
-    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
+@lru_cache(maxsize=None)
+def _torch():
+    import torch
+
+    return torch
 
 
 def _need(name, t, dtype, dev, shape):
     """Raises unless ``t`` is contiguous, of this dtype, device and shape: the
     library reads and writes it through a raw pointer."""
-    if t is None or not _fits(t, dtype, dev, shape):
+    if t is None or t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         got = "None" if t is None else f"{t.dtype}, {tuple(t.shape)} on {t.device}"
         raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)} on cuda:{dev}; got {got}")
 
@@ -344,19 +347,15 @@ def _elsewhere(stream, dev):
     """None if a call on ``stream`` (None: the current one) for tensors on device
     ``dev`` can go ahead; else the context that makes that stream and device
     current, so that what the call allocates belongs to the stream as well."""
-    import torch
-
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-        return torch.cuda.stream(stream)
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+        return _torch().cuda.stream(stream)
+    return None if dev == _torch()._C._cuda_getDevice() else _torch().cuda.device(dev)
 
 
 def _raw_stream(dev):
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _addr(t):
@@ -379,8 +378,7 @@ def msa_paged_append(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache,
     sequence), kv_len [B] (the new tokens counted), page_table [B, max_pages],
     caches [num_pages, page_size, Hkv, d]. Returns the rotated queries (None
     without q); ``q_out=q`` rotates in place."""
-    import torch
-
+    torch = _torch()
     shape = _rows("k_new", k_new)
     T, Hkv, d = shape
     dev, dtype, i32 = k_new.get_device(), k_new.dtype, torch.int32
@@ -427,8 +425,7 @@ def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out
                          stream=None):
     """One query row per sequence over its whole paged cache (see include/msa.h):
     q [B,Hq,d], caches [num_pages, page_size, Hkv, d] -> out [B,Hq,d]."""
-    import torch
-
+    torch = _torch()
     shape = _rows("q", q)
     B, Hq, d = shape
     dev, dtype = q.get_device(), q.dtype
@@ -461,8 +458,7 @@ def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out
 def msa_full_attn_prefill(q, k, v, cu_q, cu_k, scale=0.0, out=None, lse=None, ws=None, stream=None):
     """Causal attention over packed sequences (see include/msa.h): q [Tq,Hq,d],
     k, v [Tk,Hkv,d], cu_q, cu_k [B+1] int32 -> out [Tq,Hq,d]."""
-    import torch
-
+    torch = _torch()
     shape = _rows("q", q)
     Tq, Hq, d = shape
     dev, dtype = q.get_device(), q.dtype
@@ -495,8 +491,7 @@ def msa_full_attn_prefill_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, s
                                 ws=None, stream=None):
     """msa_full_attn_prefill with each sequence's kv_len[b] keys in a paged cache
     (see include/msa.h): q [Tq,Hq,d], cu_q [B+1], page_table [B, max_pages] -> out [Tq,Hq,d]."""
-    import torch
-
+    torch = _torch()
     shape = _rows("q", q)
     Tq, Hq, d = shape
     dev, dtype = q.get_device(), q.dtype
@@ -532,8 +527,7 @@ def msa_full_attn_backward(q, k, v, out, dout, lse, cu_q, cu_k, dq=None, dk=None
                            stream=None):
     """Gradients of msa_full_attn_prefill (see include/msa.h) from its output,
     its lse [Tq,Hq] and the output gradient ``dout``. Returns (dq, dk, dv)."""
-    import torch
-
+    torch = _torch()
     shape = _rows("q", q)
     Tq, Hq, d = shape
     dev, dtype = q.get_device(), q.dtype

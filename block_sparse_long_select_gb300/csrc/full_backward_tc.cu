@@ -793,8 +793,9 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   if ((e = launch_full_bwd_rows(a, stream))) return e;
   ProfScope pf("full_bwd", stream);
   const int c = cluster_split(kc, f.seq.Tq / f.seq.B / p.tpt);
-  return launch_clusters(full_bwd_kernel<D>, kc + (qc + c - 1) / c, c, kFbThreads, bytes, true, stream, tmQ, tmO, tmK, tmV,
-                         p);
+  static KernelReady ready;
+  return launch_clusters(ready, full_bwd_kernel<D>, kc + (qc + c - 1) / c, c, kFbThreads, bytes, true, stream, tmQ, tmO,
+                         tmK, tmV, p);
 }
 
 }  // namespace

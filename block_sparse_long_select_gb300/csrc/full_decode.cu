@@ -671,7 +671,8 @@ cudaError_t decode(const FdParams& p, cudaStream_t stream) {
   auto kern = full_decode_kernel<T, D, H>;
   constexpr int bytes = FdShape<T, D, H>::kBytes;
   static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
-  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  static KernelReady ready;
+  if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes)) return e;
   ProfScope pf("full_decode", stream);
   kern<<<fd_grid(), FdShape<T, D, H>::kThreads, bytes, stream>>>(p);
   return cudaGetLastError();

@@ -466,14 +466,14 @@ F32Params params(const FullArgs& a) {
 // is doubled until there are that many (a walk of 31 steps in 60 CTAs: 182 us
 // alone).
 template <typename K>
-cudaError_t run(const char* name, K kern, F32Params p, int slots, int64_t split, int bytes, bool early,
+cudaError_t run(const char* name, KernelReady& ready, K kern, F32Params p, int slots, int64_t split, int bytes, bool early,
                 cudaStream_t stream) {
   const int64_t ctas = int64_t(slots) * p.Hkv;
   int c = 1;
   while (c < 8 && ctas * c * 2 <= 4 * kNumSMs && split >= 4 * c) c *= 2;
   ProfScope pf(name, stream);
   p.nslots = slots;
-  return launch_clusters(kern, ctas, c, kF32Threads, bytes, early, stream, p);
+  return launch_clusters(ready, kern, ctas, c, kF32Threads, bytes, early, stream, p);
 }
 
 template <int D>
@@ -481,7 +481,8 @@ cudaError_t forward(const FullArgs& a, cudaStream_t stream) {
   F32Params p = params(a);
   p.out = static_cast<float*>(a.out);
   p.lse = a.lse;
-  return run("full_f32", full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B, 1,
+  static KernelReady ready;
+  return run("full_f32", ready, full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B, 1,
              (kA + 2 * kB) * D * 4 + kA * kPitch * 4, false, stream);
 }
 template <int D>
@@ -495,11 +496,12 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.dv = static_cast<float*>(a.dv);
   if (cudaError_t e = launch_full_bwd_rows(a, stream)) return e;
   constexpr int m = kA * kPitch * 4;
-  if (cudaError_t e = run("full_f32_dkv", full_f32_dkv_kernel<D>, p, f.seq.Tk / kA + f.seq.B,
+  static KernelReady dkv, dq;
+  if (cudaError_t e = run("full_f32_dkv", dkv, full_f32_dkv_kernel<D>, p, f.seq.Tk / kA + f.seq.B,
                           int64_t(f.seq.Tq) * p.hpg / kB,
                           (2 * kA + 2 * kB) * D * 4 + 2 * m + kB * 8, true, stream))
     return e;
-  return run("full_f32_dq", full_f32_dq_kernel<D>, p, int(int64_t(f.seq.Tq) * p.hpg / kA) + f.seq.B,
+  return run("full_f32_dq", dq, full_f32_dq_kernel<D>, p, int(int64_t(f.seq.Tq) * p.hpg / kA) + f.seq.B,
              f.seq.Tk / kB, (2 * kA + 2 * kB) * D * 4 + m, false, stream);
 }
 

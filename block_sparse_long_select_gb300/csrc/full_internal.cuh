@@ -2,6 +2,8 @@
 // rows and keys lie, the searches over packed offsets, and the launchers.
 #pragma once
 
+#include <atomic>
+
 #include "msa_internal.cuh"
 
 namespace msa {
@@ -97,6 +99,31 @@ __device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, 
 }
 
 // ---- launchers ---------------------------------------------------------------
+// Prepares a kernel once per device: its dynamic shared memory, and, where its
+// warpgroups exchange registers, that it was built with `regs` per thread (0:
+// not checked). One instance per kernel; safe from several threads.
+class KernelReady {
+ public:
+  cudaError_t on_device(const void* kern, int smem, int regs = 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if (regs) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+      if (fa.numRegs != regs) return cudaErrorInvalidConfiguration;
+    }
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    done_.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
 struct FullArgs {
   const void *q, *k, *v;
   SeqMap seq;

@@ -785,11 +785,8 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
   constexpr int bytes = int(PfSmem<D>::kTotal);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // a launch with other registers could not cover the warpgroups' shares
-  cudaFuncAttributes fa;
-  cudaError_t e;
-  if ((e = cudaFuncGetAttributes(&fa, kern))) return e;
-  if (fa.numRegs != int(kRegsLaunch)) return cudaErrorInvalidConfiguration;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e;
+  static KernelReady ready;
+  if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes, int(kRegsLaunch))) return e;
   ProfScope pf("full_prefill", stream);
   kern<<<kNumSMs, kPfThreads, bytes, stream>>>(tmQ, tmK, tmV, p);
   return cudaGetLastError();

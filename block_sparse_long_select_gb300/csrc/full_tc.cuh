@@ -132,10 +132,10 @@ inline int cluster_split(int64_t ctas, int64_t steps) {
 // `early`: the grid may start while the one before it in the stream ends (it
 // waits for that one's writes itself).
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kern)(P...), int64_t ctas, int cluster, int threads, int smem, bool early,
-                            cudaStream_t stream, A... args) {
+cudaError_t launch_clusters(KernelReady& ready, void (*kern)(P...), int64_t ctas, int cluster, int threads, int smem,
+                            bool early, cudaStream_t stream, A... args) {
   if (ctas * cluster >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), smem)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(ctas * cluster));
   cfg.blockDim = dim3(threads);
