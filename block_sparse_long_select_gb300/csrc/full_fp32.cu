@@ -183,6 +183,44 @@ __device__ __forceinline__ int64_t row_of(const F32Params& p, const SeqSpan& s, 
   return (int64_t(s.q0) + x / p.hpg) * p.Hq + g * p.hpg + x % p.hpg;
 }
 
+// The row tile of CTA (or cluster) `work` of `works`: sequence, head, tile (-1:
+// none). Up to 32 sequences: tiles ordered by their place in their sequence,
+// the last places (the longest walks) first, and the order turned round on
+// every second lap over the SMs. These CTAs are small and most calls put all of
+// them on the SMs at once, a lap after the other, so what counts is that each
+// SM's laps add up alike (three prompts of up to 999 tokens: the busiest SM had
+// 1.7 times the average). More sequences: by slots, late places first. Whole warp.
+__device__ __forceinline__ int find_row_tile(const F32Params& p, int work, int works, int& g, int& tile) {
+  if (p.seq.B > 32) {
+    g = work % p.Hkv;
+    return find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - work / p.Hkv, tile, p.hpg);
+  }
+  const int lane = threadIdx.x & 31, lap = work / kNumSMs, at = work % kNumSMs;
+  const int rank = lap * kNumSMs + (lap & 1 ? min(kNumSMs, works - lap * kNumSMs) - 1 - at : at);
+  int mine = 0;
+  if (lane < p.seq.B) {
+    const SeqSpan s = seq_span(p.seq, lane);
+    mine = s.rows_ok ? (s.Lq * p.hpg + kA - 1) / kA : 0;
+    if (!s.rows_ok && work == 0 && lane < p.seq.B) set_status(p.status, MSA_ERR_BOUNDS);
+  }
+  // tiles at places >= x, of all heads
+  auto from = [&](int x) { return int(__reduce_add_sync(0xffffffffu, max(mine - x, 0))) * p.Hkv; };
+  if (rank >= from(0)) return -1;
+  int lo = 0, hi = __reduce_max_sync(0xffffffffu, mine);  // from(lo) > rank >= from(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (from(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int nth = (rank - from(hi)) / p.Hkv;  // of the sequences that reach place lo
+  g = (rank - from(hi)) % p.Hkv;
+  tile = lo;
+  const uint32_t reach = __ballot_sync(0xffffffffu, mine > lo);
+  return __ffs(__ballot_sync(0xffffffffu, mine > lo && __popc(reach & ((1u << lane) - 1u)) == nth)) - 1;
+}
+
 // ---------------------------------------------------------------------------------
 // forward: 32 rows; smem Q | K | V | P
 // ---------------------------------------------------------------------------------
@@ -191,10 +229,8 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
   extern __shared__ __align__(128) uint8_t f32_smem[];
   const uint32_t sq = tc::smem_u32(f32_smem), sk = sq + kA * D * 4, sv = sk + kB * D * 4, sp = sv + kB * D * 4;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int g = blockIdx.x % p.Hkv;
-  int tile;
-  const int b =
-      find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - int(blockIdx.x / p.Hkv), tile, p.hpg);  // late rows first
+  int g, tile;
+  const int b = find_row_tile(p, blockIdx.x, gridDim.x, g, tile);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.rows_ok) {
@@ -292,9 +328,8 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
                  sp = sv + kB * D * 4;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
-  const int g = work % p.Hkv;
-  int tile;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - work / p.Hkv, tile, p.hpg);
+  int g, tile;
+  const int b = find_row_tile(p, work, gridDim.x / cl, g, tile);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
