@@ -4,8 +4,8 @@
 //
 // Bound: FMAs (the tensor cores have no fp32 products; tf32 would keep 11 bits);
 // in fact the shared-memory reads beside them. Measured (Hq 8, Hkv 2, d 64): three
-// prompts of up to 999 tokens 72 us (15.6 TFLOP/s), the gradients of three
-// documents of up to 500 tokens 45 us (dk, dv) and 35 us (dq).
+// prompts of up to 999 tokens 65 us (17 TFLOP/s), the gradients of three
+// documents of up to 500 tokens 45 us (dk, dv) and 31 us (dq).
 // Every kernel is the same small matrix engine: a CTA of 128 threads keeps a
 // tile of 32 rows in shared memory (queries x group heads; in dkv, keys) and
 // streams 64 rows of the other side past it. A thread computes 4 x 4 dot
