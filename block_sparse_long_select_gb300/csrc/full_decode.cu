@@ -407,13 +407,10 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
 
   // ---- this CTA's run of units (every warp finds it alone) ----
   int64_t total = 0;
-  const int units0 = lane < p.B ? units_of<kUnit>(p, lane) : 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int64_t y = b0 == 0 ? units0 : b0 + lane < p.B ? units_of<kUnit>(p, b0 + lane) : 0;
+#pragma unroll 8
+  for (int b = lane; b < p.B; b += 32) total += units_of<kUnit>(p, b);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    total += y;
-  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= items;
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
   const int64_t run0 = blockIdx.x * per, run1 = min(run0 + per, total);
@@ -428,8 +425,10 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
   if (run0 >= run1) return;
   Walk<kUnit> at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
+  int ahead = lane < p.B ? units_of<kUnit>(p, lane) : 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int mine = b0 == 0 ? units0 : b0 + lane < p.B ? units_of<kUnit>(p, b0 + lane) : 0;
+    const int mine = ahead;
+    ahead = b0 + 32 + lane < p.B ? units_of<kUnit>(p, b0 + 32 + lane) : 0;  // in flight during the scan
     int64_t incl = int64_t(mine) * items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

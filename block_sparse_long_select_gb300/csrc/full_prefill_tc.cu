@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         ++it;
       };
-      // an item's description; false: its pages are out of range
+      // an item's description; mode 2 if its pages are out of range
       auto describe = [&](PfItem& d, int sb, int g, int slot_tile, const SeqSpan& s) {
         d.b = sb;
         d.g = g;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const int32_t* row = p.pages.table + int64_t(sb) * p.pages.max_pages;
           const int np = (s.Lk + (1 << p.pages.page_log2) - 1) >> p.pages.page_log2;
           bad = false;
-#pragma unroll 4
+#pragma unroll 16
           for (int x = lane; x < np; x += 32) bad |= row[x] < 0 || row[x] >= p.pages.num_pages;
           bad = __any_sync(0xffffffffu, bad);
           if (bad && lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
@@ -433,19 +433,26 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       if (!ok) fail();
       // --------------------- rows that see no key ---------------------
-      for (int b0 = 0; b0 < p.seq.B; b0 += 32) {
+      // Up to as many sequences as CTAs: each sequence's rows are dealt out to all CTAs. More: whole
+      // sequences are, so that no CTA reads every span again (4096 sequences, a third without keys:
+      // 614 us with rows dealt out, 367 us with sequences).
+      const int ctas = gridDim.x, me = blockIdx.x;
+      const bool by_row = p.seq.B <= ctas;
+      const int lane_step = by_row ? 1 : ctas;
+      for (int64_t b0 = by_row ? 0 : me; b0 < p.seq.B; b0 += 32 * lane_step) {
+        const int64_t b = b0 + int64_t(lane) * lane_step;
         SeqSpan s{};
         int rows = 0;  // of the sequence, from its first on
-        if (b0 + lane < p.seq.B) {
-          s = seq_span(p.seq, b0 + lane);
-          if (!s.ok && blockIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+        if (b < p.seq.B) {
+          s = seq_span(p.seq, int(b));
+          if (!s.ok) set_status(p.status, MSA_ERR_BOUNDS);
           if (s.rows_ok) rows = !s.ok || s.Lk == 0 ? s.Lq : s.Lk < s.Lq ? (s.Lq - s.Lk) / w2 * w2 : 0;
         }
         uint32_t some = __ballot_sync(0xffffffffu, rows > 0);
         for (; some; some &= some - 1) {
           const int src = __ffs(some) - 1;
           const int q0 = __shfl_sync(0xffffffffu, s.q0, src), cnt = __shfl_sync(0xffffffffu, rows, src);
-          for (int r = blockIdx.x; r < cnt; r += gridDim.x) {
+          for (int r = by_row ? me : 0; r < cnt; r += by_row ? ctas : 1) {
             const int64_t row = int64_t(q0 + r) * p.Hq;
             uint4* dst = reinterpret_cast<uint4*>(p.out + row * D);
             for (int x = lane; x < p.Hq * (D / 8); x += 32) dst[x] = make_uint4(0, 0, 0, 0);

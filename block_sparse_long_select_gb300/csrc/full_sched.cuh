@@ -113,15 +113,15 @@ struct Share {
   __device__ __forceinline__ bool measure(int ctas) {
     total = 0;
     longest = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      const int lane = threadIdx.x & 31;
-      const SeqWork w = b0 + lane < B ? f(b0 + lane) : SeqWork{0, 0, 0, 0};
-      int64_t y = items_cost(w, p, w.items);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      total += y;
-      longest = max(longest, __reduce_max_sync(0xffffffffu, w.items > 0 ? item_len(w, p.step, w.items - 1) : 0));
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < B; b += 32) {  // a lane's sequences; their loads are in flight together
+      const SeqWork w = f(b);
+      total += items_cost(w, p, w.items);
+      longest = max(longest, w.items > 0 ? item_len(w, p.step, w.items - 1) : 0);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    longest = __reduce_max_sync(0xffffffffu, longest);
     total *= Hkv;
     G = int(max(min(total / p.least_run, int64_t(ctas)), int64_t(1)));
     each = total / G;

@@ -28,6 +28,12 @@ def test_many_short_sequences(heads):
     check_prefill([(n % 40, n % 40 + o) for n, o in zip(lens, old)], *heads, BF16, paged=32, seed=3)
 
 
+def test_many_sequences_with_rows_without_keys():
+    spans = [(n % 90, (n * 7) % 60) for n in range(200)]
+    check_prefill(spans, 4, 2, 64, BF16, seed=23)
+    check_prefill(spans, 4, 2, 64, BF16, paged=16, seed=24)
+
+
 def test_many_sequences_of_one_token():
     check_prefill([(1, 1 + (7 * b) % 40) for b in range(600)], 8, 2, 64, BF16, paged=16, seed=4)
     check_prefill([(1, 1)] * 300, 8, 2, 64, FP32, seed=5)
