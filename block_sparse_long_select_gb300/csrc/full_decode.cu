@@ -17,6 +17,8 @@
 // CTA: their states are joined in shared memory. An item that lies in several
 // CTAs leaves a partial (maximum, sum, unnormalised output) per CTA, and the
 // CTA that arrives last joins them in the order of the keys.
+// Many short items: their ends would cost more than their keys (a join takes as
+// long as a unit), so single warps take whole items instead, with nothing to join.
 //
 // bf16: mma.sync m16n8k16 with keys (then head dims) along M and the heads
 // along N = 8: the tensor work is a fraction of the time the bytes take, so
@@ -28,7 +30,7 @@
 namespace msa {
 namespace {
 
-constexpr int kSub = 16;                  // keys of a warp's step: never across a page
+constexpr int kSub = 16, kSubLog2 = 4;    // keys of a warp's step: never across a page
 constexpr int kFdMaxHeads = 16;           // query heads of an item
 constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
@@ -354,23 +356,34 @@ struct FdParams {
   uint32_t* status;
 };
 
-template <int UNIT>
-__device__ __forceinline__ int units_of(const FdParams& p, int b) {
+__device__ __forceinline__ int units_of(const FdParams& p, int b, int unit_log2) {
   const int L = p.kv_len[b];
-  return L > 0 && L <= p.cap ? (L + UNIT - 1) / UNIT : 0;
+  return L > 0 && L <= p.cap ? ((L - 1) >> unit_log2) + 1 : 0;
 }
 
-// A walk over a CTA's run of units in order.
-template <int UNIT>
+// A walk over units in order: those of a CTA's run, or (SOLO) of every hop-th item.
 struct Walk {
   int b, it, u, n;  // sequence, item within it, unit within the item, units of the item
-  __device__ __forceinline__ void next(const FdParams& p) {
+  template <bool SOLO>
+  __device__ __forceinline__ void next(const FdParams& p, int hop, int unit_log2) {
     if (++u < n) return;
     u = 0;
+    if constexpr (SOLO) return seek(p, hop, hop);
     if (++it < p.Hkv * p.ngr) return;
     it = 0;
     do {
-      n = ++b < p.B ? units_of<UNIT>(p, b) : 1;  // past the last sequence the walk is over
+      n = ++b < p.B ? units_of(p, b, unit_log2) : 1;  // past the last sequence the walk is over
+    } while (n == 0);
+  }
+  // To the first item with keys among those `by`, `by` + hop, ... further on.
+  __device__ __forceinline__ void seek(const FdParams& p, int by, int hop) {
+    const int items = p.Hkv * p.ngr;
+    do {
+      it += by;
+      b += it / items;
+      it %= items;
+      by = hop;
+      n = b < p.B ? units_of(p, b, kSubLog2) : 1;
     } while (n == 0);
   }
 };
@@ -390,8 +403,9 @@ struct FdShape {
   static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
 };
 
-template <typename T, int D, int H>
-__global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_kernel(const FdParams p) {
+// SOLO: whole items for single warps; else the CTA's run of the `total` units.
+template <typename T, int D, int H, bool SOLO>
+__device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   using SH = FdShape<T, D, H>;
   using C = typename SH::C;
   constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads, kUnit = SH::kUnit;
@@ -405,62 +419,56 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
   const int items = p.Hkv * p.ngr;
   T* out = static_cast<T*>(p.out);
 
-  // ---- this CTA's run of units (every warp finds it alone) ----
-  int64_t total = 0;
-#pragma unroll 8
-  for (int b = lane; b < p.B; b += 32) total += units_of<kUnit>(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= items;
+  constexpr int kUnitLog2 = kUnit == 64 ? 6 : 7;
+  static_assert(1 << kUnitLog2 == kUnit, "keys of a unit");
+  constexpr int ulog = SOLO ? kSubLog2 : kUnitLog2;
+  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = SOLO ? 0 : warp * kSub;
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t run0 = blockIdx.x * per, run1 = min(run0 + per, total);
-  // sequences without keys: nobody's run holds them
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (units_of<kUnit>(p, b) > 0) continue;
-    if (threadIdx.x == 0 && (p.kv_len[b] < 0 || p.kv_len[b] > p.cap)) set_status(p.status, MSA_ERR_BOUNDS);
-    for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
-    if (p.lse)
-      for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
-  }
+  const int64_t run0 = SOLO ? 0 : blockIdx.x * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);
   if (run0 >= run1) return;
-  Walk<kUnit> at{};
+  Walk at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
-  int ahead = lane < p.B ? units_of<kUnit>(p, lane) : 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int mine = ahead;
-    ahead = b0 + 32 + lane < p.B ? units_of<kUnit>(p, b0 + 32 + lane) : 0;  // in flight during the scan
-    int64_t incl = int64_t(mine) * items;
+  int64_t item_first = 0;  // number of the item's first unit
+  if constexpr (SOLO) {
+    at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop);
+  } else {
+    int ahead = lane < p.B ? units_of(p, lane, kUnitLog2) : 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int mine = ahead;
+      ahead = b0 + 32 + lane < p.B ? units_of(p, b0 + 32 + lane, kUnitLog2) : 0;  // in flight during the scan
+      int64_t incl = int64_t(mine) * items;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        at.b = b0 + src;
+        at.n = __shfl_sync(0xffffffffu, mine, src);
+        first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      at.b = b0 + src;
-      at.n = __shfl_sync(0xffffffffu, mine, src);
-      first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
-      break;
-    }
-    first += __shfl_sync(0xffffffffu, incl, 31);
+    at.it = int((run0 - first) / at.n);
+    at.u = int((run0 - first) % at.n);
+    item_first = first + int64_t(at.it) * at.n;
   }
-  at.it = int((run0 - first) / at.n);
-  at.u = int((run0 - first) % at.n);
-  int64_t item_first = first + int64_t(at.it) * at.n;  // number of the item's first unit
 
   // ---- copies: the walk `ld` runs ahead of `at` ----
-  Walk<kUnit> ld = at;
-  int64_t ld_left = run1 - run0;
+  Walk ld = at;
+  int64_t ld_left = !SOLO || ld.b < p.B ? run1 - run0 : 0;
   uint32_t bad_ring = 0;  // stage x's page was out of range
-  auto page_of = [&](const Walk<kUnit>& w) {
-    const int key = w.u * kUnit + warp * kSub;
+  auto page_of = [&](const Walk& w) {
+    const int key = (w.u << ulog) + sub0;
     return key < p.kv_len[w.b] ? p.pages.table[int64_t(w.b) * p.pages.max_pages + (key >> p.pages.page_log2)] : 0;
   };
-  int page = page_of(ld);
+  int page = ld_left > 0 ? page_of(ld) : 0;
   auto issue = [&](int st) {
     if (ld_left > 0) {
-      const int L = p.kv_len[ld.b], key = ld.u * kUnit + warp * kSub;
+      const int L = p.kv_len[ld.b], key = (ld.u << ulog) + sub0;
       const int valid = L - key;
       const bool bad = valid > 0 && (page < 0 || page >= p.pages.num_pages);
       bad_ring = bad ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
@@ -486,8 +494,11 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
         cp16z(chunk_at(dst + C::kTile, C::kRow, r, c), vp + off, in);
       }
       if (--ld_left > 0) {
-        ld.next(p);
-        page = page_of(ld);
+        ld.next<SOLO>(p, hop, ulog);
+        if (!SOLO || ld.b < p.B)
+          page = page_of(ld);
+        else
+          ld_left = 0;
       }
     }
     cp_commit_group();
@@ -498,7 +509,7 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
   C c;
   bool fresh = true, bad = false;
   int st = 0;
-  for (int64_t z = run0; z < run1; ++z) {
+  for (int64_t z = run0; z < run1 && (!SOLO || at.b < p.B); ++z) {
     const int g = at.it / p.ngr, h0 = g * p.hpg + (at.it % p.ngr) * kFdMaxHeads;
     const int heads = min(p.hpg - (at.it % p.ngr) * kFdMaxHeads, kFdMaxHeads);
     const int L = p.kv_len[at.b];
@@ -510,7 +521,7 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
     cp_wait<NS - 1>();
     __syncwarp();
     bad |= (bad_ring >> st) & 1u;
-    const int valid = L - (at.u * kUnit + warp * kSub);
+    const int valid = L - ((at.u << ulog) + sub0);
     if (valid > 0) c.step(ring + st * C::kStage, extra, valid, p.scale_log2);
     __syncwarp();
     st = (st + 1) % NS;
@@ -550,15 +561,17 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
     };
     // Every hand-over has a slot of its own: the upper warps may be at the next
     // item's end while the lower ones still read this one's.
+    if constexpr (!SOLO) {
 #pragma unroll
-    for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
-      if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
-      __syncthreads();
-      if (warp < half) take(join + (slot0 + warp) * SH::kState);
+      for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
+        if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
+        __syncthreads();
+        if (warp < half) take(join + (slot0 + warp) * SH::kState);
+      }
     }
-    const bool whole = item_first >= run0 && ends;
+    const bool whole = SOLO || (item_first >= run0 && ends);
     const int slot = 2 * int(blockIdx.x) + (item_first >= run0 ? 1 : 0);
-    if (warp == 0) {
+    if (SOLO || warp == 0) {
       c.sum_l();
       if (__any_sync(0xffffffffu, bad)) {
         bad = true;
@@ -657,10 +670,54 @@ __global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_ker
     }
     if (ends) item_first += n;
     const int was = at.b;
-    at.next(p);
+    at.next<SOLO>(p, hop, ulog);
     if (at.b != was) item_first = z + 1;
   }
   cp_wait<0>();
+}
+
+template <typename T, int D, int H>
+__global__ void __launch_bounds__(FdShape<T, D, H>::kThreads, 1) full_decode_kernel(const FdParams p) {
+  using SH = FdShape<T, D, H>;
+  constexpr int kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
+  const int lane = threadIdx.x & 31, items = p.Hkv * p.ngr;
+  T* out = static_cast<T*>(p.out);
+
+  // ---- all units (every warp counts alone) ----
+  int64_t total = 0;
+  int longest = 0;  // in warps' steps
+#pragma unroll 8
+  for (int b = lane; b < p.B; b += 32) {
+    const int steps = units_of(p, b, kSubLog2);
+    total += (steps + kFdWarps - 1) / kFdWarps;
+    longest = max(longest, steps);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  total *= items;
+  // Whole items for single warps, or shared-out units? A unit and a warp's step
+  // both take about 1.1 us, and so does an item's end or start; single warps
+  // come out ahead from 1.25 times the other count on. Measured both ways (Hq 32,
+  // Hkv 8, d 128, bf16; lengths within a factor of 2):
+  //   1280 items up to 64 keys   19 (single) : 29 us     2560 up to 256   65 :  70 us
+  //   10240 items up to 128      99 : 177 us             2560 up to 512  119 : 109 us
+  //   640 items up to 128        18 :  20 us              320 up to 128   17 :  16 us
+  const int warps = int(gridDim.x) * kFdWarps;
+  const int64_t all = int64_t(p.B) * items, rounds = (all + warps - 1) / warps;
+  const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
+  // sequences without keys: nobody's run holds them
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (units_of(p, b, kSubLog2) > 0) continue;
+    if (threadIdx.x == 0 && (p.kv_len[b] < 0 || p.kv_len[b] > p.cap)) set_status(p.status, MSA_ERR_BOUNDS);
+    for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
+    if (p.lse)
+      for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
+  }
+  if (solo)
+    decode_run<T, D, H, true>(p, total);
+  else
+    decode_run<T, D, H, false>(p, total);
 }
 
 int fd_grid() { return kNumSMs; }

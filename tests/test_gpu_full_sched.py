@@ -9,7 +9,7 @@ import torch
 
 import block_sparse_long_select_gb300 as msa
 import full_plain as fp
-from test_gpu_full_attn import BF16, DEV, FP32, check_backward, check_prefill, make
+from test_gpu_full_attn import BF16, DEV, FP32, _decode_case, check_backward, check_decode, check_prefill, make
 
 pytestmark = pytest.mark.gpu
 
@@ -81,6 +81,36 @@ def test_split_items_bad_page():
         assert (out[:8] == 0).all() and (lse[:8] == -math.inf).all()
         want = fp.prefill(q, ks, vs, [(0, 8), (8, 12)], 0.125, BF16)
         fp.assert_within(out[8:], want[0][8:], want[2][8:], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads", [(16, 2, 64), (32, 8, 128), (4, 4, 64), (6, 2, 128), (40, 2, 64), (34, 1, 128)])
+def test_decode_whole_items_per_warp(heads, dtype):
+    """Many short sequences, some without keys, and one long one among them (units shared out)."""
+    lens = [(13 * b) % 41 for b in range(650)]
+    check_decode(lens, *heads, dtype, 16, seed=25)
+    check_decode([0] * 200 + lens[:350] + [0] * 100, *heads, dtype, 32, seed=26)
+    check_decode([0] * 600, *heads, dtype, 16, seed=27, max_pages=1)
+    check_decode(lens[:400] + [1500] + lens[400:], *heads, dtype, 64, seed=28)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_whole_items_bad_pages(dtype):
+    lens = [1 + (29 * b) % 60 for b in range(900)]
+    q, kc, vc, table, kv, want = _decode_case(lens, 8, 2, 64, dtype, 16, 29)
+    bad = [0, 17, 433, 899]
+    table[0, 0], kv[17], kv[433] = -1, -1, table.shape[1] * 16 + 1
+    table[899, (lens[899] - 1) // 16] = kc.shape[0]
+    ws = msa.workspace(msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE, 900, 1, table.shape[1] * 16, 2, 8, 64, 0, 0, 0,
+                                              0 if dtype == BF16 else 1), DEV)
+    good = [b for b in range(900) if b not in bad]
+    for _ in range(2):
+        lse = torch.empty(900, 8, device=DEV)
+        out = msa.msa_full_attn_decode(*[x.to(DEV) for x in (q, kc, vc, table, kv)], lse=lse, ws=ws)
+        assert msa.msa_read_status(ws) == 6
+        assert (out[bad] == 0).all() and (lse[bad] == -math.inf).all()
+        fp.assert_within(out[good], want[0][good], want[2][good], "out")
+        fp.assert_within(lse[good], want[1][good], want[3][good], "lse")
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
