@@ -13,7 +13,7 @@ bool full_dtype_ok(int dtype) { return dtype == MSA_BF16 || dtype == MSA_FP32; }
 // Heads, head dim and element type, shared by every entry point.
 msa_status_t check_heads(int Hq, int Hkv, int d, int dtype) {
   if (Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0 || !full_dtype_ok(dtype)) return MSA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || Hq / Hkv > kMaxFullHpg) return MSA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || Hq / Hkv > kMaxFullHpg || Hq > kMaxFullHeads) return MSA_ERR_UNSUPPORTED;
   return MSA_OK;
 }
 

@@ -9,6 +9,7 @@
 namespace msa {
 
 constexpr int kMaxFullHpg = 64;  // query heads per key/value head
+constexpr int kMaxFullHeads = 1 << 16;  // a row's elements are counted in 32 bits
 
 // Pages of a cache [num_pages, page_size, Hkv, d] and the table that maps
 // sequences to them. table == nullptr: keys are packed rows instead.

@@ -316,8 +316,8 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  *  Visibility    query row i of Lq sees keys j <= Lk - Lq + i of Lk: the last
  *                row sees every key. If Lq > Lk the first Lq - Lk rows see
  *                none: their output and gradient are 0 and their lse -inf.
- * Supported by all: d in {64, 128}; Hq / Hkv an integer up to 64; BF16 (tensor
- * cores, fp32 accumulation) or FP32 (CUDA cores).
+ * Supported by all: d in {64, 128}; Hq / Hkv an integer up to 64, Hq up to
+ * 65536; BF16 (tensor cores, fp32 accumulation) or FP32 (CUDA cores).
  * Device-side checks: a sequence whose cu, kv_len or page entry is out of
  * range sets MSA_ERR_BOUNDS in the workspace status and nothing out of range is
  * read or written for it. If its rows are known (its cu is in range) its
@@ -395,7 +395,9 @@ msa_status_t msa_full_attn_prefill_paged(const void* q, const void* k_cache, con
  *  ws: msa_workspace_size(MSA_OP_FULL_BACKWARD, B, Tq, Tk, Hkv, Hq, d, 0, 0, 0,
  *  dtype)
  *  Deterministic: no atomics, every sum in a fixed order. BF16 rounds P and dS
- *  to bf16 before the products that read them. Tq == 0 with Tk > 0 writes dk
+ *  to bf16 before the products that read them. As in the forward, hidden
+ *  pairs have weight 0 but are multiplied: an infinity or NaN in a sequence's
+ *  own rows can reach any of its gradients, never another sequence's. Tq == 0 with Tk > 0 writes dk
  *  and dv only; the query-row pointers may then be NULL. */
 msa_status_t msa_full_attn_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
                                     const float* lse, const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk,

@@ -67,6 +67,13 @@ def test_refusals_shared(lib, call):
     assert call(lib, **big) == 2                # rows x heads past 31 bits
 
 
+@pytest.mark.parametrize("call", ALL)
+def test_refuses_too_many_heads(lib, call):
+    one = {"B": 1} if call is decode else {"B": 1, "T": 1} if call is append else {"B": 1, "Tq": 1}
+    assert call(lib, Hq=(1 << 16) + 64, Hkv=(1 << 10) + 1, **one) == 2
+    assert call(lib, Hq=1 << 16, Hkv=1 << 10, ws=None, **one) == 3
+
+
 @pytest.mark.parametrize("call", (append, decode, prefill_paged))
 def test_refusals_pages(lib, call):
     assert call(lib, page=0) == 1
