@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kFbThreads, 1)
   extern __shared__ __align__(1024) uint8_t fb_smem[];
   if (tc::smem_u32(fb_smem) & 1023u) {  // the swizzled operands need 1024-byte alignment
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
-    return;
+    return tc::griddep_wait();
   }
   // a cluster shares a key tile; row tiles are a CTA each
   const int cl = cluster_size(), nk = p.kslots * p.Hkv, row = int(blockIdx.x) - nk * cl;
@@ -763,6 +763,9 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, fb_smem, blockIdx.x / cl, cl, cluster_rank());
   else if (row < p.qslots * p.Hkv)  // the last cluster may have CTAs to spare
     bwd_dq<D>(tmQ, tmO, tmK, tmV, p, fb_smem, row);
+  // Also CTAs without work: this grid must not be over before the one that still
+  // writes the rows' data, or the workspace's next user would run beside it.
+  tc::griddep_wait();
 }
 
 template <int D>

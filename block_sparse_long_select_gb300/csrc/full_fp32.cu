@@ -404,10 +404,11 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
   const int g = work % p.Hkv;
   int tile;
   const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kA, work / p.Hkv, tile);  // early keys: most rows
-  if (b < 0) return;
+  // also CTAs without work wait: this grid must not be over before the one that still writes the rows' data
+  if (b < 0) return tc::griddep_wait();
   const SeqSpan s = seq_span(p.seq, b);
   if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-  if (!s.keys_ok) return;
+  if (!s.keys_ok) return tc::griddep_wait();
   const int j0 = tile * kA, off = s.ok ? s.Lk - s.Lq : 0, xn = s.ok ? s.Lq * p.hpg : 0;
   auto key = [&](const float* base, int j) -> const float* {
     return j < s.Lk ? base + ((int64_t(s.k0) + j) * p.Hkv + g) * D : nullptr;

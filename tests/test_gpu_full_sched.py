@@ -185,6 +185,27 @@ def test_one_workspace_for_all_operations():
         assert msa.msa_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_backward_of_no_sequence_then_another_call(dtype):
+    """Rows that belong to no sequence: nothing is written, and the workspace's next user follows at once."""
+    g = torch.Generator().manual_seed(30)
+    q, k = torch.randn(6000, 16, 64, generator=g).to(dtype).to(DEV), torch.randn(300, 2, 64, generator=g).to(dtype).to(DEV)
+    lse, none = torch.zeros(6000, 16, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    qc, kc, vc, table, kv, want = _decode_case([700, 3000, 1], 16, 2, 64, dtype, 16, 31)
+    d = [x.to(DEV) for x in (qc, kc, vc, table, kv)]
+    dt = 0 if dtype == BF16 else 1
+    ws = msa.workspace(max(msa.msa_workspace_size(msa.MSA_OP_FULL_BACKWARD, 3, 6000, 300, 2, 16, 64, 0, 0, 0, dt),
+                           msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE, 3, 1, table.shape[1] * 16, 2, 16, 64, 0, 0, 0,
+                                                  dt)), DEV)
+    dq, dk, dv = torch.full_like(q, 7.0), torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+    for _ in range(20):
+        msa.msa_full_attn_backward(q, k, k, q, q, lse, none, none, dq=dq, dk=dk, dv=dv, ws=ws)
+        out = msa.msa_full_attn_decode(*d, ws=ws)
+        fp.assert_within(out, want[0], want[2], "out")
+    assert msa.msa_read_status(ws) == 0
+    assert (dq == 7.0).all() and (dk == 7.0).all() and (dv == 7.0).all()
+
+
 def test_two_streams_at_once():
     """Two calls in flight on two streams, a workspace each."""
     q, k, v, cu_q, cu_k, rows, ks, vs, _ = make([(64, 8000), (300, 300)], 8, 2, 64, BF16, 18)
