@@ -2,14 +2,17 @@
 // the backward over packed ones (formulas at full_prefill_tc.cu and
 // full_backward_tc.cu).
 //
-// Bound: FMAs (the tensor cores have no fp32 products; tf32 would keep 11 bits);
-// in fact the shared-memory reads beside them. Measured (Hq 8, Hkv 2, d 64): three
-// prompts of up to 999 tokens 65 us (17 TFLOP/s), the gradients of three
-// documents of up to 500 tokens 45 us (dk, dv) and 31 us (dq).
+// Bound: FMAs (the tensor cores have no fp32 products; tf32 would keep 11 bits),
+// which the shared-memory reads beside them just keep up with; short calls are
+// bound by the walk of their longest tile. Measured (d 64): one prompt of 4096
+// tokens (Hq 32, Hkv 8) 1.81 ms, 38 TFLOP/s, half of the FMA rate; (Hq 8, Hkv 2)
+// three prompts of up to 999 tokens 55 us (20 TFLOP/s), the gradients of three
+// documents of up to 500 tokens 43 us (dk, dv) and 27 us (dq).
 // Every kernel is the same small matrix engine: a CTA of 128 threads keeps a
 // tile of 32 rows in shared memory (queries x group heads; in dkv, keys) and
 // streams 64 rows of the other side past it. A thread computes 4 x 4 dot
-// products, 4 LDS.128 of either side for 64 FMAs; the 32 x 64 results go
+// products, 4 16-byte loads of either side for 64 FMAs (two to an
+// instruction); the 32 x 64 results go
 // through shared memory to the second product, where it owns 4 rows x D / 16
 // columns. 32 rows and not 64 because several small CTAs per SM hide each
 // other's barriers, and short calls need the number of CTAs. Rows that belong
@@ -21,6 +24,19 @@ namespace {
 
 constexpr int kF32Threads = 128, kA = 32, kB = 64;  // resident rows, streamed rows
 constexpr int kPitch = kB + 4;                      // floats of a row of the 32 x 64 results
+// CTAs per SM that registers are kept for: what shared memory allows, in fp32
+// tiles of D columns (left to itself the compiler spills to fit a fourth: 66 us
+// for prompts up to 999 tokens instead of 62).
+template <int D>
+constexpr int kF32Ctas = D == 64 ? 3 : 2;
+
+// A thread's place in the 16 x 8 grid over a tile: a warp has 16 columns and 2
+// rows, the lanes l and l ^ 1 share a column. A 16-byte shared load of a warp
+// takes 2 cycles if within every quad no more than two addresses occur, else 4
+// (measured). So the 8 loads per 64 FMAs take 16 cycles, as the FMAs do; with
+// half warps as rows they took 24 (prompts up to 999 tokens 60 -> 55 us).
+__device__ __forceinline__ int tile_x() { return int((threadIdx.x & 31) >> 1); }
+__device__ __forceinline__ int tile_y() { return int((threadIdx.x >> 5 << 1) | (threadIdx.x & 1)); }
 
 __device__ __forceinline__ void cp16f(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -33,6 +49,14 @@ __device__ __forceinline__ void cp_wait_f() {
 __device__ __forceinline__ float4 lds4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+struct Pairs {
+  uint64_t lo, hi;  // two floats each
+};
+__device__ __forceinline__ Pairs lds_pairs(uint32_t a) {
+  Pairs v;
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.lo), "=l"(v.hi) : "r"(a));
   return v;
 }
 // 16-byte chunk c of row r; chunks are exchanged within 128 bytes by the row's
@@ -57,32 +81,48 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const float* any, F row)
 // acc[i][k] = A row (4 ty + i) . B row (tx + 16 k)
 template <int D>
 __device__ __forceinline__ void dots(uint32_t a, uint32_t b, float (&acc)[4][4]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tile_x(), ty = tile_y();
+  uint64_t sum[4][4];  // of even and of odd columns
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < D / 4; ++c) {
-    float4 x[4], y[4];
+    for (int k = 0; k < 4; ++k) sum[i][k] = 0;
+  // at<D>() with what is common to four chunks taken out: the low two bits of a
+  // row's exchange are added to a chunk's, the third flips a group of four
+  const uint32_t xa = a + uint32_t(ty * 4 * D * 4), ya = b + uint32_t(tx * D * 4);
+  const int xs = (ty & 1) << 2, ys = tx & 4;
+#pragma unroll 2
+  for (int c0 = 0; c0 < D / 4; c0 += 4) {
+    const uint32_t xc = xa + uint32_t((c0 ^ xs) << 4), yc = ya + uint32_t((c0 ^ ys) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lds4(at<D>(a, ty * 4 + i, c));
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t yo = yc + uint32_t((c ^ (tx & 3)) << 4);
+      Pairs x[4], y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = lds4(at<D>(b, tx + 16 * k, c));
+      for (int i = 0; i < 4; ++i) x[i] = lds_pairs(xc + uint32_t(i * D * 4 + ((c ^ i) << 4)));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < 4; ++k) y[k] = lds_pairs(yo + uint32_t(16 * k * D * 4));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[i][k] = fmaf(x[i].x, y[k].x, acc[i][k]);
-        acc[i][k] = fmaf(x[i].y, y[k].y, acc[i][k]);
-        acc[i][k] = fmaf(x[i].z, y[k].z, acc[i][k]);
-        acc[i][k] = fmaf(x[i].w, y[k].w, acc[i][k]);
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[i][k] = fma2(x[i].lo, y[k].lo, sum[i][k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[i][k] = fma2(x[i].hi, y[k].hi, sum[i][k]);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = split(sum[i][k]);
+      acc[i][k] = f.x + f.y;
+    }
 }
 // The thread's 4 x 4 results into the 32 x 64 matrix.
 __device__ __forceinline__ void put(uint32_t m, const float (&v)[4][4]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tile_x(), ty = tile_y();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -91,9 +131,10 @@ __device__ __forceinline__ void put(uint32_t m, const float (&v)[4][4]) {
 }
 // acc[i][..] += sum over the 64 streamed rows of m[4 ty + i][row] * row's columns;
 // the thread's columns are the 16-byte chunks tx, tx + 16, ...
+// (pairs: columns 2 e and 2 e + 1 in acc[i][e]).
 template <int D>
-__device__ __forceinline__ void sums(uint32_t m, uint32_t b, float (&acc)[4][D / 16]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+__device__ __forceinline__ void sums(uint32_t m, uint32_t b, uint64_t (&acc)[4][D / 32]) {
+  const int tx = tile_x(), ty = tile_y();
 #pragma unroll 2
   for (int j = 0; j < kB; j += 4) {
     float w[4][4];
@@ -106,46 +147,46 @@ __device__ __forceinline__ void sums(uint32_t m, uint32_t b, float (&acc)[4][D /
     for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const float4 f = lds4(at<D>(b, j + y, tx + 16 * c));
+        const Pairs f = lds_pairs(at<D>(b, j + y, tx + 16 * c));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[i][4 * c] = fmaf(w[i][y], f.x, acc[i][4 * c]);
-          acc[i][4 * c + 1] = fmaf(w[i][y], f.y, acc[i][4 * c + 1]);
-          acc[i][4 * c + 2] = fmaf(w[i][y], f.z, acc[i][4 * c + 2]);
-          acc[i][4 * c + 3] = fmaf(w[i][y], f.w, acc[i][4 * c + 3]);
+          const uint64_t ww = pair(w[i][y], w[i][y]);
+          acc[i][2 * c] = fma2(ww, f.lo, acc[i][2 * c]);
+          acc[i][2 * c + 1] = fma2(ww, f.hi, acc[i][2 * c + 1]);
         }
       }
   }
 }
 __device__ __forceinline__ float row_max(float x) {  // over the 16 threads of a row
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int o = 16; o > 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 16; o > 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 template <int D>
-__device__ __forceinline__ void store_rows(float* dst, const float (&acc)[D / 16], float mul) {
-  const int tx = threadIdx.x & 15;
+__device__ __forceinline__ void store_rows(float* dst, const uint64_t (&acc)[D / 32], float mul) {
+  const int tx = tile_x();
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c)
-    reinterpret_cast<float4*>(dst)[tx + 16 * c] =
-        make_float4(acc[4 * c] * mul, acc[4 * c + 1] * mul, acc[4 * c + 2] * mul, acc[4 * c + 3] * mul);
+  for (int c = 0; c < D / 64; ++c) {
+    const float2 lo = split(acc[2 * c]), hi = split(acc[2 * c + 1]);
+    reinterpret_cast<float4*>(dst)[tx + 16 * c] = make_float4(lo.x * mul, lo.y * mul, hi.x * mul, hi.y * mul);
+  }
 }
 
 // The thread's 4 rows into a partial [rows][D] in shared memory, from row r0 on.
 template <int D>
-__device__ __forceinline__ void put_rows(uint32_t part, int r0, const float (&acc)[4][D / 16]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+__device__ __forceinline__ void put_rows(uint32_t part, int r0, const uint64_t (&acc)[4][D / 32]) {
+  const int tx = tile_x(), ty = tile_y();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at<D>(part, r0 + ty * 4 + i, tx + 16 * c)),
-                   "f"(acc[i][4 * c]), "f"(acc[i][4 * c + 1]), "f"(acc[i][4 * c + 2]), "f"(acc[i][4 * c + 3])
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at<D>(part, r0 + ty * 4 + i, tx + 16 * c)),
+                   "l"(acc[i][2 * c]), "l"(acc[i][2 * c + 1])
                    : "memory");
 }
 // This rank's slice of `rows` rows, summed over the cluster in rank order:
@@ -225,10 +266,10 @@ __device__ __forceinline__ int find_row_tile(const F32Params& p, int work, int w
 // forward: 32 rows; smem Q | K | V | P
 // ---------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p) {
+__global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_kernel(const F32Params p) {
   extern __shared__ __align__(128) uint8_t f32_smem[];
   const uint32_t sq = tc::smem_u32(f32_smem), sk = sq + kA * D * 4, sv = sk + kB * D * 4, sp = sv + kB * D * 4;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tile_x(), ty = tile_y();
   int g, tile;
   const int b = find_row_tile(p, blockIdx.x, gridDim.x, g, tile);
   if (b < 0) return;
@@ -260,14 +301,15 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
   if (n > 0) load_tile<D, kB>(sv, p.v, [&](int r) { return key(p.v, r); });
   cp_commit_f();
   int vis[4];  // keys the thread's rows see
-  float m[4], l[4], acc[4][D / 16];
+  float m[4], l[4];
+  uint64_t acc[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     vis[i] = s.Lk - s.Lq + (x0 + ty * 4 + i) / p.hpg + 1;
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) acc[i][c] = 0;
   }
   for (int j = 0; j < n; ++j) {
     cp_wait_f<1>();
@@ -286,11 +328,12 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
         mx = fmaxf(mx, sc[i][k]);
       }
       const float mn = fmaxf(m[i], row_max(mx));
-      const float a = m[i] == mn ? 1.f : ex2(m[i] - mn), z = mn == -INFINITY ? 0.f : mn;
+      const float z = mn == -INFINITY ? 0.f : mn, a = ex2(m[i] - z);  // no branch: rows of a warp differ
       m[i] = mn;
       l[i] *= a;
+      const uint64_t aa = pair(a, a);
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) acc[i][c] *= a;
+      for (int c = 0; c < D / 32; ++c) acc[i][c] = mul2(acc[i][c], aa);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         sc[i][k] = ex2(sc[i][k] - z);
@@ -322,11 +365,11 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_kernel(const F32Params p
 // dq: 32 rows; smem Q | dO | K | V | dS
 // ---------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Params p) {
+__global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_dq_kernel(const F32Params p) {
   extern __shared__ __align__(128) uint8_t f32_smem[];
   const uint32_t sq = tc::smem_u32(f32_smem), so = sq + kA * D * 4, sk = so + kA * D * 4, sv = sk + kB * D * 4,
                  sp = sv + kB * D * 4;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tile_x(), ty = tile_y();
   const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   int g, tile;
   const int b = find_row_tile(p, work, gridDim.x / cl, g, tile);
@@ -343,14 +386,14 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
   load_tile<D, kA>(so, p.q, [&](int r) { return x0 + r < x1 ? p.dout + row_of(p, s, g, x0 + r) * D : nullptr; });
   int vis[4];
   float2 rd[4];
-  float acc[4][D / 16];
+  uint64_t acc[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int x = x0 + ty * 4 + i;
     vis[i] = s.Lk - s.Lq + x / p.hpg + 1;
     rd[i] = x < x1 ? p.rows[(int64_t(g) * p.seq.Tq + s.q0) * p.hpg + x] : make_float2(INFINITY, 0.f);
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) acc[i][c] = 0;
   }
   for (int j = n * rank / cl; j < n * (rank + 1) / cl; ++j) {  // this CTA's key tiles
     load_tile<D, kB>(sk, p.k, [&](int r) { return key(p.k, j * kB + r); });
@@ -394,12 +437,12 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dq_kernel(const F32Param
 // dk, dv: 32 keys; smem K | V | Q | dO | P^T | dS^T | lse, delta
 // ---------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Params p) {
+__global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_dkv_kernel(const F32Params p) {
   extern __shared__ __align__(128) uint8_t f32_smem[];
   const uint32_t sk = tc::smem_u32(f32_smem), sv = sk + kA * D * 4, sq = sv + kA * D * 4, so = sq + kB * D * 4,
                  sp = so + kB * D * 4, sd = sp + kA * kPitch * 4;
   float2* srow = reinterpret_cast<float2*>(f32_smem + (2 * kA + 2 * kB) * D * 4 + 2 * kA * kPitch * 4);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tile_x(), ty = tile_y();
   const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   const int g = work % p.Hkv;
   int tile;
@@ -416,12 +459,12 @@ __global__ void __launch_bounds__(kF32Threads) full_f32_dkv_kernel(const F32Para
   load_tile<D, kA>(sk, p.k, [&](int r) { return key(p.k, j0 + r); });
   load_tile<D, kA>(sv, p.k, [&](int r) { return key(p.v, j0 + r); });
   int from[4];  // first row that sees the thread's keys
-  float ak[4][D / 16], av[4][D / 16];
+  uint64_t ak[4][D / 32], av[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     from[i] = max(j0 + ty * 4 + i - off, 0) * p.hpg;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) ak[i][c] = av[i][c] = 0;
   }
   tc::griddep_wait();  // the rows' data are the previous grid's
   const int xs = max(j0 - off, 0) * p.hpg / kB * kB, n = max(xn - xs + kB - 1, 0) / kB;
