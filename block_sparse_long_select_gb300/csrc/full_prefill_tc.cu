@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const int32_t* row = p.pages.table + int64_t(sb) * p.pages.max_pages;
           const int np = (s.Lk + (1 << p.pages.page_log2) - 1) >> p.pages.page_log2;
           bad = false;
-#pragma unroll 16
+#pragma unroll 4
           for (int x = lane; x < np; x += 32) bad |= row[x] < 0 || row[x] >= p.pages.num_pages;
           bad = __any_sync(0xffffffffu, bad);
           if (bad && lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
