@@ -11,12 +11,11 @@
 // Every kernel is the same small matrix engine: a CTA of 128 threads keeps a
 // tile of 32 rows in shared memory (queries x group heads; in dkv, keys) and
 // streams 64 rows of the other side past it. A thread computes 4 x 4 dot
-// products, 4 16-byte loads of either side for 64 FMAs (two to an
-// instruction); the 32 x 64 results go
-// through shared memory to the second product, where it owns 4 rows x D / 16
-// columns. 32 rows and not 64 because several small CTAs per SM hide each
-// other's barriers, and short calls need the number of CTAs. Rows that belong
-// to no pair arrive as zeros.
+// products, 4 16-byte loads of either side for 64 FMAs (two to an instruction);
+// the 32 x 64 results go through shared memory to the second product, where it
+// owns 4 rows x D / 16 columns. 32 rows and not 64 because several small CTAs
+// per SM hide each other's barriers, and short calls need the number of CTAs.
+// Rows that belong to no pair arrive as zeros.
 #include "full_tc.cuh"
 
 namespace msa {
