@@ -107,7 +107,7 @@ extern "C" msa_status_t msa_paged_append(const void* q, const void* k_new, const
   a.q_out = q_out;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
-  a.status = &static_cast<WsHeader*>(ws)->status;
+  a.ws = static_cast<WsHeader*>(ws);
   return launched(launch_paged_append(a, stream));
 }
 

@@ -1,5 +1,5 @@
-// Full attention: what every element type shares. The rows' lse and delta for
-// the backward, and the outputs of calls without any key or any query row.
+// Full attention: what every element type shares. Whether offsets are in order,
+// the rows' lse and delta for the backward, and the outputs of calls without any key or any query row.
 #include "full_internal.cuh"
 #include "tc_utils.cuh"
 
@@ -55,6 +55,14 @@ cudaError_t bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+__global__ void __launch_bounds__(1024) full_order_kernel(const SeqMap m, uint32_t* disorder) {
+  bool bad = false;
+#pragma unroll 4
+  for (int b = threadIdx.x; b < m.B; b += 1024) bad |= !span_in_order(m, seq_span(m, b));
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *disorder = bad;
+}
+
 // Zeroes every sequence's rows (one warp per row of row_bytes); lse, if given, becomes -inf.
 __global__ void __launch_bounds__(128) full_zero_kernel(const int32_t* __restrict__ cu, int B, int T, int row_bytes,
                                                         uint4* __restrict__ a, uint4* __restrict__ b,
@@ -73,6 +81,13 @@ __global__ void __launch_bounds__(128) full_zero_kernel(const int32_t* __restric
 }  // namespace
 
 size_t full_backward_ws_bytes(int Tq, int Hq) { return (size_t(Tq) * Hq * sizeof(float2) + 255) & ~size_t(255); }
+
+cudaError_t launch_order_check(const SeqMap& m, void* ws, cudaStream_t stream) {
+  if (m.B <= kSelfChecked) return cudaSuccess;
+  ProfScope pf("full_order", stream);
+  full_order_kernel<<<1, 1024, 0, stream>>>(m, &static_cast<WsHeader*>(ws)->disorder);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_full_bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
   if (a.f.dtype == MSA_BF16)

@@ -57,6 +57,67 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqMap& m, int b) {
   return s;
 }
 
+// ---- offsets out of order ------------------------------------------------------
+// The searches below take packed offsets as ordered, 0 <= cu[0] <= ... <= cu[B]
+// <= T: one offset that is not can lead them past tiles of every other sequence.
+// So all offsets are looked at first, and where they are not in order the
+// sequences are gone through one after the other instead: slow, but none is lost.
+// Up to kSelfChecked sequences each CTA looks by itself, beside its search's
+// loads; for more, a grid of one CTA does it ahead of the call's (about 2 us;
+// append of 67614 tokens of 4096 sequences: 144 us unchecked, 232 us if every CTA
+// looks, 148 us with the grid; 30446 of 1000: 66, 74 and 70; 12473 of 256: 21, then
+// 25 either way).
+constexpr int kSelfChecked = 256;
+__device__ __forceinline__ bool span_in_order(const SeqMap& m, const SeqSpan& s) {
+  return s.rows_ok && (m.kv_len || s.keys_ok);  // a wrong kv_len misleads no search
+}
+// Whole CTA (a barrier): whether all packed offsets are in order. `disorder` is
+// what launch_order_check left, ahead of the grid, for batches that it serves.
+__device__ __forceinline__ bool cta_in_order(const SeqMap& m, const uint32_t* disorder) {
+  if (m.B > kSelfChecked) return *disorder == 0;
+  bool bad = false;
+  for (int b = threadIdx.x; b < m.B; b += blockDim.x) bad |= !span_in_order(m, seq_span(m, b));
+  bad = __any_sync(0xffffffffu, bad);  // the compiler then knows that warps go one way (append: 30 registers, 50 without)
+  return !__syncthreads_or(bad);
+}
+// Whole warp, 32 sequences at a time from the first on, a lane each: offsets
+// below an earlier one within [0, T] are out of range too, so that no two
+// sequences in range own the same row.
+struct SpanFloor {
+  int q = 0, k = 0;  // largest offsets within range so far
+  // the largest of the earlier lanes' x and `most`, which then takes in all lanes'
+  __device__ __forceinline__ static int before(int x, int& most) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = max(x, y);
+    }
+    const int up = __shfl_up_sync(0xffffffffu, x, 1), r = lane > 0 ? max(up, most) : most;
+    most = max(most, __shfl_sync(0xffffffffu, x, 31));
+    return r;
+  }
+  __device__ __forceinline__ void apply(const SeqMap& m, SeqSpan& s) {
+    if (m.cu_q) s.rows_ok &= s.q0 >= before(s.q0 >= 0 && s.q0 <= m.Tq ? s.q0 : 0, q);
+    if (!m.kv_len) s.keys_ok &= s.k0 >= before(s.k0 >= 0 && s.k0 <= m.Tk ? s.k0 : 0, k);
+    s.ok = s.rows_ok && s.keys_ok;
+  }
+};
+// f(b, span) with the whole warp for 32 sequences at a time (b >= B: an empty
+// span out of range), until it returns true.
+template <typename F>
+__device__ __forceinline__ void each_32_seqs(const SeqMap& m, F f) {
+  SpanFloor floor;
+  for (int b0 = 0; b0 < m.B; b0 += 32) {
+    const int b = b0 + int(threadIdx.x & 31);
+    SeqSpan s{};
+    if (b < m.B) s = seq_span(m, b);
+    floor.apply(m, s);
+    if (b >= m.B) s.rows_ok = s.keys_ok = s.ok = false;
+    if (f(b, s)) return;
+  }
+}
+
 // Warp-wide 32-ary search: the number of indices i in [1, n] with f(i) true,
 // for f true up to some index and false after it (2 rounds of loads up to
 // n = 1023). Terminates with a value in [0, n] whatever f says.
@@ -76,10 +137,22 @@ __device__ __forceinline__ int warp_count_true(int n, F f) {
   return lo;
 }
 
-// The sequence that owns packed row t, or -1 (whole warp).
+// The sequence that owns packed row t, or -1 (whole warp; offsets in order).
 __device__ __forceinline__ int find_row_seq(const int32_t* cu, int B, int t) {
   const int b = warp_count_true(B, [&](int i) { return cu[i] <= t; });
   return b < B && cu[b] <= t && t < cu[b + 1] ? b : -1;
+}
+
+// The same whatever the offsets are; a row's owner is in range.
+__device__ __forceinline__ int scan_row_seq(const SeqMap& m, bool keys, int t) {
+  int r = -1;
+  each_32_seqs(m, [&](int b, const SeqSpan& s) {
+    const int from = keys ? s.k0 : s.q0, n = keys ? s.Lk : s.Lq;
+    const uint32_t hit = __ballot_sync(0xffffffffu, (keys ? s.keys_ok : s.rows_ok) && from <= t && t < from + n);
+    if (hit) r = __shfl_sync(0xffffffffu, b, __ffs(hit) - 1);
+    return hit != 0;
+  });
+  return r;
 }
 
 // Tiles of `tt` rows that start at each sequence's first row, in slots: a
@@ -143,6 +216,8 @@ struct FullBwdArgs {
 size_t full_decode_ws_bytes(int d);  // behind the header
 size_t full_backward_ws_bytes(int Tq, int Hq);  // behind the header
 size_t full_prefill_ws_bytes(int d, int64_t most_keys);  // bf16, behind the header
+// WsHeader::disorder for the calls of more than kSelfChecked sequences
+cudaError_t launch_order_check(const SeqMap& m, void* ws, cudaStream_t stream);
 // fp32 prefill and backward
 cudaError_t launch_full_f32(const FullArgs& a, cudaStream_t stream);
 cudaError_t launch_full_f32_backward(const FullBwdArgs& a, cudaStream_t stream);
@@ -164,7 +239,7 @@ struct AppendArgs {
   PageMap pages;
   int B, T, Hq, Hkv, d, rot, interleaved, max_pos, dtype;
   void *q_out, *k_cache, *v_cache;
-  uint32_t* status;
+  WsHeader* ws;
 };
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream);
 

@@ -23,7 +23,8 @@ struct WsHeader {
   // behind it); a call that timed out may leave counts, which msa_read_status clears
   uint32_t arrivals[(kNumSMs + 3) / 4];
   uint32_t queue;  // full-attention prefill: next item to hand out, zero between calls
-  uint32_t reserved[61 - (kNumSMs + 3) / 4];
+  uint32_t disorder;  // full attention: packed offsets of this call are not in order (launch_order_check)
+  uint32_t reserved[60 - (kNumSMs + 3) / 4];
 };
 static_assert(sizeof(WsHeader) == kWsHeader, "the header is the workspace's first 256 bytes");
 

@@ -45,24 +45,35 @@ struct Chunk {
   }
 };
 
+// rows by cu_new; lengths are looked at token by token
+__host__ __device__ SeqMap seqs_of(const AppendArgs& a) { return SeqMap{a.cu_new, nullptr, a.kv_len, a.B, a.T, 0}; }
+
 template <typename T>
 __global__ void __launch_bounds__(kAppMostThreads) paged_append_kernel(const AppendArgs a, const SmallDiv by_units,
                                                                   const SmallDiv by_chunks) {
   constexpr int N = Chunk<T>::N;
   const int t = blockIdx.x;
-  // every warp finds the token's sequence itself: no barrier
-  const int b = a.cu_new ? find_row_seq(a.cu_new, a.B, t) : t;
-  if (b < 0) return;
+  int b = t;
+  if (a.cu_new) {  // every warp finds the token's sequence itself
+    const SeqMap m = seqs_of(a);
+    if (cta_in_order(m, &a.ws->disorder)) {
+      b = find_row_seq(a.cu_new, a.B, t);
+    } else {
+      if (threadIdx.x == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
+      b = scan_row_seq(m, false, t);
+    }
+    if (b < 0) return;
+  }
   const int last = a.cu_new ? a.cu_new[b + 1] : t + 1;
   const int64_t pos = int64_t(a.kv_len[b]) - (last - t);
   const int psz = 1 << a.pages.page_log2;
   int64_t row = -1;
-  if (pos >= 0 && last <= a.T && pos < (int64_t(a.pages.max_pages) << a.pages.page_log2) &&
+  if (pos >= 0 && pos < (int64_t(a.pages.max_pages) << a.pages.page_log2) &&
       (a.rot == 0 || pos < a.max_pos)) {
     const int page = a.pages.table[int64_t(b) * a.pages.max_pages + (pos >> a.pages.page_log2)];
     if (page >= 0 && page < a.pages.num_pages) row = int64_t(page) * psz + (pos & (psz - 1));
   }
-  if (row < 0 && threadIdx.x == 0) set_status(a.status, MSA_ERR_BOUNDS);
+  if (row < 0 && threadIdx.x == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
   const int qh = a.q ? a.Hq : 0;
   if (row < 0 && !a.q) return;
   // units of a head row: rot / 2 / N pair units (two chunks each; adjacent
@@ -147,6 +158,8 @@ cudaError_t append(const AppendArgs& a, cudaStream_t stream) {
   const int units = a.rot / 2 / N + (a.d - a.rot) / N, chunks = a.d / N;
   const int total = ((a.q ? a.Hq : 0) + a.Hkv) * units + a.Hkv * chunks;
   const int threads = a.T > kAppFewTokens ? kAppThreads : total >= kAppMostThreads ? kAppMostThreads : (total + 31) / 32 * 32;
+  if (a.cu_new)
+    if (cudaError_t e = launch_order_check(seqs_of(a), a.ws, stream)) return e;
   ProfScope pf("paged_append", stream);
   paged_append_kernel<T><<<a.T, threads, 0, stream>>>(a, SmallDiv(units), SmallDiv(chunks));
   return cudaGetLastError();

@@ -301,7 +301,10 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  *  Packed rows   the rows of all sequences back to back, without padding.
  *                cu [B + 1] int32: sequence b owns rows [cu[b], cu[b+1]).
  *                Need 0 <= cu[b] <= cu[b+1] <= the row count (T, Tq or Tk);
- *                a sequence may be empty. Rows before cu[0] and from cu[B] on
+ *                a sequence may be empty. A sequence is out of range where
+ *                this does not hold, and also where cu[b] lies below an
+ *                earlier offset within [0, row count], so that no row has two
+ *                owners. Rows before cu[0] and from cu[B] on
  *                belong to no sequence: they are never read as data and stay
  *                as they were in every output.
  *  Outputs overlap no input and no other output, except where a call allows it.
@@ -320,8 +323,9 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  * 65536; BF16 (tensor cores, fp32 accumulation) or FP32 (CUDA cores).
  * Device-side checks: a sequence whose cu, kv_len or page entry is out of
  * range sets MSA_ERR_BOUNDS in the workspace status and nothing out of range is
- * read or written for it. If its rows are known (its cu is in range) its
- * output rows are 0 and their lse -inf; otherwise they stay as they were.
+ * read or written for it; the other sequences get their results. If its rows
+ * are known (its cu is in range) its output rows are 0 and their lse -inf;
+ * otherwise they stay as they were.
  * A workspace may serve all operations in turn, if it has the largest size. */
 
 /* Appends the keys and values of T packed new tokens to a paged cache, with
@@ -343,8 +347,9 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  *  Supported: 0 <= rot <= d, a multiple of 16. The rotation is in fp32, rounded
  *  once; pointers to rows are 16-byte aligned. A token whose position is
  *  negative, not below max_pos or past the table, or whose page is out of
- *  range, sets MSA_ERR_BOUNDS and is skipped (its q_out row is 0). No two
- *  tokens of a call may map to one cache row. */
+ *  range, sets MSA_ERR_BOUNDS and is skipped (its q_out row is 0). Tokens of a
+ *  sequence whose cu_new is out of range are skipped, their q_out rows stay. No
+ *  two tokens of a call may map to one cache row. */
 msa_status_t msa_paged_append(const void* q, const void* k_new, const void* v_new, const float* rope,
                               const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table, int B, int T,
                               int Hq, int Hkv, int d, int rot, int interleaved, int max_pos, int num_pages,
