@@ -45,7 +45,7 @@ inline msa_status_t launched(cudaError_t e) { return e == cudaSuccess ? MSA_OK :
 // (Tk == 0) there is nothing to map for TMA: the rows are empty.
 cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
   if (a.seq.Tk == 0)
-    return launch_full_zero(a.seq.cu_q, a.seq.B, a.seq.Tq, a.Hq, a.d, a.dtype, a.out, nullptr, a.lse, stream);
+    return launch_full_zero(a.seq, false, a.Hq, a.d, a.dtype, a.out, nullptr, a.lse, a.ws, stream);
   return a.dtype == MSA_BF16 ? launch_full_prefill_tc(a, stream) : launch_full_f32(a, stream);
 }
 
@@ -241,7 +241,7 @@ extern "C" msa_status_t msa_full_attn_backward(const void* q, const void* k, con
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  if (Tq == 0) return launched(launch_full_zero(cu_k, B, Tk, Hkv, d, dtype, dk, dv, nullptr, stream));
-  if (Tk == 0) return launched(launch_full_zero(cu_q, B, Tq, Hq, d, dtype, dq, nullptr, nullptr, stream));
+  if (Tq == 0) return launched(launch_full_zero(a.f.seq, true, Hkv, d, dtype, dk, dv, nullptr, ws, stream));
+  if (Tk == 0) return launched(launch_full_zero(a.f.seq, false, Hq, d, dtype, dq, nullptr, nullptr, ws, stream));
   return launched(dtype == MSA_BF16 ? launch_full_backward_tc(a, stream) : launch_full_f32_backward(a, stream));
 }

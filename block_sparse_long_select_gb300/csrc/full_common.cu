@@ -63,12 +63,16 @@ __global__ void __launch_bounds__(1024) full_order_kernel(const SeqMap m, uint32
   if (threadIdx.x == 0) *disorder = bad;
 }
 
-// Zeroes every sequence's rows (one warp per row of row_bytes); lse, if given, becomes -inf.
-__global__ void __launch_bounds__(128) full_zero_kernel(const int32_t* __restrict__ cu, int B, int T, int row_bytes,
-                                                        uint4* __restrict__ a, uint4* __restrict__ b,
-                                                        float* __restrict__ lse, int heads) {
+// Zeroes the rows (`keys`: key rows) of every sequence whose own offsets are in
+// range, one warp per row of row_bytes; lse, if given, becomes -inf.
+__global__ void __launch_bounds__(128) full_zero_kernel(const SeqMap m, bool keys, int row_bytes, uint4* __restrict__ a,
+                                                        uint4* __restrict__ b, float* __restrict__ lse, int heads,
+                                                        WsHeader* ws) {
   const int t = blockIdx.x * 4 + int(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= T || find_row_seq(cu, B, t) < 0) return;
+  const bool in_order = cta_in_order(m, &ws->disorder);
+  if (!in_order && threadIdx.x == 0) set_status(&ws->status, MSA_ERR_BOUNDS);
+  if (t >= (keys ? m.Tk : m.Tq)) return;
+  if ((in_order ? find_row_seq(keys ? m.cu_k : m.cu_q, m.B, t) : scan_row_seq(m, keys, t)) < 0) return;
   for (int x = lane; x < row_bytes / 16; x += 32) {
     const int64_t o = int64_t(t) * (row_bytes / 16) + x;
     a[o] = make_uint4(0, 0, 0, 0);
@@ -95,11 +99,13 @@ cudaError_t launch_full_bwd_rows(const FullBwdArgs& a, cudaStream_t stream) {
   return a.f.d == 128 ? bwd_rows<float, 128>(a, stream) : bwd_rows<float, 64>(a, stream);
 }
 
-cudaError_t launch_full_zero(const int32_t* cu, int B, int T, int heads, int d, int dtype, void* a, void* b, float* lse,
-                             cudaStream_t stream) {
+cudaError_t launch_full_zero(const SeqMap& m, bool keys, int heads, int d, int dtype, void* a, void* b, float* lse,
+                             void* ws, cudaStream_t stream) {
+  if (cudaError_t e = launch_order_check(m, ws, stream)) return e;
   ProfScope pf("full_zero", stream);
-  full_zero_kernel<<<(T + 3) / 4, 128, 0, stream>>>(cu, B, T, heads * d * (dtype == MSA_BF16 ? 2 : 4),
-                                                    static_cast<uint4*>(a), static_cast<uint4*>(b), lse, heads);
+  full_zero_kernel<<<((keys ? m.Tk : m.Tq) + 3) / 4, 128, 0, stream>>>(
+      m, keys, heads * d * (dtype == MSA_BF16 ? 2 : 4), static_cast<uint4*>(a), static_cast<uint4*>(b), lse, heads,
+      static_cast<WsHeader*>(ws));
   return cudaGetLastError();
 }
 

@@ -223,9 +223,9 @@ cudaError_t launch_full_f32(const FullArgs& a, cudaStream_t stream);
 cudaError_t launch_full_f32_backward(const FullBwdArgs& a, cudaStream_t stream);
 // the backward's per-row lse and delta, into the workspace behind the header
 cudaError_t launch_full_bwd_rows(const FullBwdArgs& a, cudaStream_t stream);
-// every sequence's rows of a (and b, if given) zero, lse (if given) -inf
-cudaError_t launch_full_zero(const int32_t* cu, int B, int T, int heads, int d, int dtype, void* a, void* b, float* lse,
-                             cudaStream_t stream);
+// every sequence's rows (or keys) of a (and b, if given) zero, lse (if given) -inf
+cudaError_t launch_full_zero(const SeqMap& m, bool keys, int heads, int d, int dtype, void* a, void* b, float* lse,
+                             void* ws, cudaStream_t stream);
 // decode over pages, any dtype
 cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream);
 // tcgen05 prefill (bf16); needs Tk > 0

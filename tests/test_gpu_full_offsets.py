@@ -59,6 +59,35 @@ def _rand(g, n, h, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_no_keys_or_no_rows_at_all(dtype):
+    """Calls without any key, or any row, look at both sides' offsets as well."""
+    g = torch.Generator().manual_seed(5)
+    x, y = _rand(g, 30, 4, 64, dtype).to(DEV), _rand(g, 0, 4, 64, dtype).to(DEV)
+    lse, none = torch.zeros(30, 4, device=DEV), torch.zeros(0, 4, device=DEV)
+    ws = msa.workspace(1 << 20, DEV)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    # own side's offsets, the other's, rows that become zero
+    for own, other, zero in [((0, 10, 20, 30), (0, 0, 5, 0), (0, 30)), ((0, 10, 20, 31), (0, 0, 0, 0), (0, 20)),
+                             ((0, 10, -3, 30), (0, 0, 0, 0), (0, 10)), ((0, 99, 20, 30), (0, 0, 0, 0), (20, 30)),
+                             ((-1, 10, 20, 30), (0, 0, 0, 0), (10, 30))]:
+        keep = torch.ones(30, dtype=torch.bool)
+        keep[slice(*zero)] = False
+        filled = lambda: torch.full_like(x, 7.0)  # noqa: E731
+        out, l2 = filled(), torch.full_like(lse, 7.0)
+        msa.msa_full_attn_prefill(x, y, y, ints(*own), ints(*other), out=out, lse=l2, ws=ws)
+        assert msa.msa_read_status(ws) == 6
+        dq = filled()
+        msa.msa_full_attn_backward(x, y, y, x, x, lse, ints(*own), ints(*other), dq=dq, ws=ws)
+        assert msa.msa_read_status(ws) == 6
+        dk, dv = filled(), filled()
+        msa.msa_full_attn_backward(y, x, x, y, y, none, ints(*other), ints(*own), dk=dk, dv=dv, ws=ws)
+        assert msa.msa_read_status(ws) == 6
+        for t in (out, dq, dk, dv):
+            assert (t.cpu()[keep] == 7.0).all() and (t.cpu()[~keep] == 0).all()
+        assert (l2.cpu()[keep] == 7.0).all() and (l2.cpu()[~keep] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("B", SIZES)
 def test_append(B, dtype):
     Hq, Hkv, d, page = 4, 2, 64, 16
