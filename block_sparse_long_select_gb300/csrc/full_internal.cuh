@@ -161,8 +161,7 @@ __device__ __forceinline__ int scan_row_seq(const SeqMap& m, bool keys, int t) {
 // needs at most ceil(n / tt) of them and the + b leaves room for its ragged
 // end), so T * mul / tt + B slots cover every tile and a slot's tile is found
 // by one search; some slots hold none. Returns the sequence of slot `i` and
-// its tile (-1: none). Whole warp. cu[x] is not checked here: out of range
-// values give a tile whose sequence seq_span refuses.
+// its tile (-1: none). Whole warp; offsets in order.
 __device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, int i, int& tile, int mul = 1) {
   auto slot0 = [&](int x) { return int64_t(cu[x]) * mul / tt + x; };
   // largest b whose first slot is at most i
@@ -170,6 +169,34 @@ __device__ __forceinline__ int find_slot_tile(const int32_t* cu, int B, int tt, 
   const int64_t j = i - slot0(b);
   tile = int(j);
   return j >= 0 && j < (int64_t(cu[b + 1] - cu[b]) * mul + tt - 1) / tt ? b : -1;
+}
+
+// The same whatever the offsets are: the i-th tile (`keys`: key tile) of the
+// sequences in range, which own no row together, so that as many slots do.
+__device__ __forceinline__ int scan_tile(const SeqMap& m, bool keys, int tt, int mul, int i, int& tile, SeqSpan& s) {
+  const int lane = threadIdx.x & 31;
+  int r = -1;
+  int64_t before = 0;
+  each_32_seqs(m, [&](int b, const SeqSpan& x) {
+    const int64_t n = (keys ? x.keys_ok : x.rows_ok) ? (int64_t(keys ? x.Lk : x.Lq) * mul + tt - 1) / tt : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > i);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+      r = of(b);
+      tile = i - int(__shfl_sync(0xffffffffu, before + incl - n, src));
+      s = SeqSpan{of(x.q0), of(x.Lq), of(x.k0), of(x.Lk), of(x.rows_ok) != 0, of(x.keys_ok) != 0, of(x.ok) != 0};
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    return hit != 0;
+  });
+  return r;
 }
 
 // ---- launchers ---------------------------------------------------------------

@@ -318,8 +318,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     } else if (warp == 2) {
       // ------------------------------ items ------------------------------
       const int w2 = 2 * p.tpt;
+      bool disorder = false;  // whether offsets are out of order (full_internal.cuh), known once all work is measured
       auto work = [&](int b) {  // items of 2 tpt rows that see keys
         const SeqSpan s = seq_span(p.seq, b);
+        disorder |= !span_in_order(p.seq, s);
         if (!s.ok || s.Lq == 0 || s.Lk == 0) return SeqWork{0, 0, 0, 0};
         const int off = s.Lk - s.Lq, s0 = off < 0 ? -off / w2 : 0;
         return seq_work((s.Lq + w2 - 1) / w2 - s0, int(min(int64_t(off) + int64_t(s0 + 1) * w2, int64_t(s.Lk))), s.Lk, w2);
@@ -359,8 +361,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         if (bad) d.mode = 2;
       };
-      if (!sh.measure(gridDim.x)) {
+      const bool some_work = sh.measure(gridDim.x);
+      disorder = __any_sync(0xffffffffu, disorder);
+      if (!some_work) {
         // no row sees a key
+      } else if (disorder) {  // items dealt out, each found sequence by sequence
+        for (int i = blockIdx.x; ok && i < p.nslots * p.Hkv; i += gridDim.x) {
+          int tile;
+          SeqSpan s;
+          const int sb = scan_tile(p.seq, false, w2, 1, i / p.Hkv, tile, s);
+          if (sb < 0 || !s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
+          PfItem d{};
+          describe(d, sb, i % p.Hkv, tile, s);
+          d.n = d.mode == 2 ? 0 : d.tiles;
+          publish(d);
+        }
       } else if (sh.hand_out()) {
         // Up to 32 sequences: a lane each, items by their place x in their sequence,
         // the last places (the longest walks) first. More: by slots, where the
@@ -437,14 +452,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // sequences are, so that no CTA reads every span again (4096 sequences, a third without keys:
       // 614 us with rows dealt out, 367 us with sequences).
       const int ctas = gridDim.x, me = blockIdx.x;
-      const bool by_row = p.seq.B <= ctas;
+      const bool by_row = disorder || p.seq.B <= ctas;
+      SpanFloor floor;
       const int lane_step = by_row ? 1 : ctas;
       for (int64_t b0 = by_row ? 0 : me; b0 < p.seq.B; b0 += 32 * lane_step) {
         const int64_t b = b0 + int64_t(lane) * lane_step;
         SeqSpan s{};
         int rows = 0;  // of the sequence, from its first on
+        if (b < p.seq.B) s = seq_span(p.seq, int(b));
+        if (disorder) floor.apply(p.seq, s);
         if (b < p.seq.B) {
-          s = seq_span(p.seq, int(b));
           if (!s.ok) set_status(p.status, MSA_ERR_BOUNDS);
           if (s.rows_ok) rows = !s.ok || s.Lk == 0 ? s.Lq : s.Lk < s.Lq ? (s.Lq - s.Lk) / w2 * w2 : 0;
         }

@@ -58,6 +58,91 @@ def _rand(g, n, h, d, dtype):
     return torch.randn(n, h, d, generator=g).to(dtype)
 
 
+def _workspace(op, B, Nq, Nk, Hkv, Hq, d, dtype):
+    return msa.workspace(msa.msa_workspace_size(op, B, Nq, Nk, Hkv, Hq, d, 0, 0, 0, 0 if dtype == BF16 else 1), DEV)
+
+
+def _want(q, k, v, cu_q, cu_k, dtype):
+    """out, lse and bounds, and the sequences in range on either side."""
+    rows, keys = in_range(cu_q, q.shape[0]), {b: (a, n) for b, a, n in in_range(cu_k, k.shape[0])}
+    spans, ks, vs = [], [], []
+    for b, a, n in rows:
+        k0, m = keys.get(b, (0, 0))  # keys out of range: as without any
+        spans.append((a, n))
+        ks.append(k[k0:k0 + m])
+        vs.append(v[k0:k0 + m])
+    return fp.prefill(q, ks, vs, spans, q.shape[-1] ** -0.5, dtype), rows, keys
+
+
+def _check_prefill(call, want, shape, dtype, ws, what):
+    out, lse = torch.full(shape, 7.0, dtype=dtype, device=DEV), torch.full(shape[:2], 7.0, device=DEV)
+    call(out, lse)
+    assert msa.msa_read_status(ws) == 6, what
+    none = want[1].isnan()
+    assert (out.cpu()[none] == 7.0).all() and (lse.cpu()[none] == 7.0).all(), f"{what}: rows of no sequence"
+    fp.assert_within(out, want[0], want[2], f"out, {what}")
+    fp.assert_within(lse, want[1], want[3], f"lse, {what}")
+
+
+@pytest.mark.parametrize("side", ["rows", "keys", "both"])
+@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("B", SIZES)
+def test_prefill(B, dtype, side):
+    Hq, Hkv, d = 4, 2, 64
+    lens = _lens(B, B)
+    T = sum(lens)
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (_rand(g, T, h, d, dtype) for h in (Hq, Hkv, Hkv))
+    dev, fine = [x.to(DEV) for x in (q, k, v)], fp.offsets(lens)
+    ws = _workspace(msa.MSA_OP_FULL_PREFILL, B, T, T, Hkv, Hq, d, dtype)
+    for bad in cases(lens, T):
+        cu_q, cu_k = (bad if side in ("rows", "both") else fine), (bad if side in ("keys", "both") else fine)
+        want, _, _ = _want(q, k, v, cu_q, cu_k, dtype)
+        on = [x.to(DEV) for x in (cu_q, cu_k)]
+        if side == "both":
+            on[1] = on[0]
+        _check_prefill(lambda out, lse: msa.msa_full_attn_prefill(*dev, *on, out=out, lse=lse, ws=ws), want, q.shape, dtype,
+                       ws, f"{side} {bad.tolist()[:8]}")
+
+
+@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("B", SIZES)
+def test_prefill_paged(B, dtype):
+    Hq, Hkv, d, page = 8, 2, 64, 16
+    lens = [n % 23 for n in _lens(B, B)]
+    T = sum(lens)
+    g = torch.Generator().manual_seed(2)
+    kv = [n + (7 * b) % 50 for b, n in enumerate(lens)]
+    q, ks, vs = _rand(g, T, Hq, d, dtype), *([_rand(g, n, Hkv, d, dtype) for n in kv] for _ in range(2))
+    kc, vc, table = fp.paged(ks, vs, page, g)
+    dev = [x.to(DEV) for x in (q, kc, vc, table)]
+    kvd = torch.tensor(kv, dtype=torch.int32, device=DEV)
+    ws = _workspace(msa.MSA_OP_FULL_PREFILL, B, T, table.shape[1] * page, Hkv, Hq, d, dtype)
+    for bad in cases(lens, T):
+        rows = in_range(bad, T)
+        want = fp.prefill(q, [ks[b] for b, _, _ in rows], [vs[b] for b, _, _ in rows], [r[1:] for r in rows], d ** -0.5, dtype)
+        cu = bad.to(DEV)
+        _check_prefill(lambda out, lse: msa.msa_full_attn_prefill_paged(*dev, cu, kvd, out=out, lse=lse, ws=ws), want,
+                       q.shape, dtype, ws, f"{bad.tolist()[:8]}")
+
+
+@pytest.mark.parametrize("dtype", [BF16])
+def test_prefill_long_sequences(dtype):
+    """Few long sequences, whose work is divided into equal shares when the offsets are in order."""
+    Hq, Hkv, d, lens = 2, 1, 64, [900, 40, 1700]
+    T = sum(lens)
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (_rand(g, T, h, d, dtype) for h in (Hq, Hkv, Hkv))
+    dev = [x.to(DEV) for x in (q, k, v)]
+    ws = _workspace(msa.MSA_OP_FULL_PREFILL, 3, T, T, Hkv, Hq, d, dtype)
+    for cu in ([0, 900, 940, T + 1], [0, -1, 940, T], [0, 900, 850, T], [-5, 900, 940, T], [0, 1_000_000, 940, T]):
+        cu = torch.tensor(cu, dtype=torch.int32)
+        want, _, _ = _want(q, k, v, cu, cu, dtype)
+        on = cu.to(DEV)
+        _check_prefill(lambda out, lse: msa.msa_full_attn_prefill(*dev, on, on, out=out, lse=lse, ws=ws), want, q.shape, dtype,
+                       ws, f"{cu.tolist()}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_no_keys_or_no_rows_at_all(dtype):
     """Calls without any key, or any row, look at both sides' offsets as well."""
