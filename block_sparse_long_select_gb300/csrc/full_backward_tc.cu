@@ -41,6 +41,7 @@ struct FbParams {
   const float2* rows;  // [Hkv][Tq][hpg]: lse in log2 units, delta (full_common.cu)
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* status;
+  const uint32_t* disorder;
 };
 
 template <int D>
@@ -172,8 +173,8 @@ __device__ __forceinline__ void sum_partials(uint32_t part, int rows, int rank, 
 // ---------------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
-                                        const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work, int cl,
-                                        int rank) {
+                                        const CUtensorMap& tmV, const FbParams& p, bool in_order, uint8_t* fb_smem,
+                                        int work, int cl, int rank) {
   using SM = FbSmem<D>;
   constexpr int NH = D / 64, NR = SM::kRowSlots;
   constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
@@ -181,11 +182,9 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = work % p.Hkv;
   int kt;
-  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kKeys, work / p.Hkv, kt);  // early keys: most rows
+  SeqSpan s;
+  const int b = find_tile(p.seq, in_order, true, kKeys, 1, work / p.Hkv, kt, s);  // early keys: most rows
   if (b < 0) return;
-  const SeqSpan s = seq_span(p.seq, b);
-  if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-  if (!s.keys_ok) return;
   const int j0 = kt * kKeys;
   const int off = s.Lk - s.Lq;              // row i sees keys j <= off + i
   const int rf = max(j0 - off, 0) / p.tpt;  // first row tile that sees one of these keys
@@ -498,7 +497,8 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
 // ---------------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
-                                       const CUtensorMap& tmV, const FbParams& p, uint8_t* fb_smem, int work) {
+                                       const CUtensorMap& tmV, const FbParams& p, bool in_order, uint8_t* fb_smem,
+                                       int work) {
   using SM = FbSmem<D>;
   constexpr int NH = D / 64;
   constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128), kIdA = tc::idesc_bf16_f32(128, D, true);
@@ -506,18 +506,13 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = work % p.Hkv;
   int rt;
-  const int b = find_slot_tile(p.seq.cu_q, p.seq.B, p.tpt, p.qslots - 1 - work / p.Hkv, rt);  // late rows first
+  SeqSpan s;
+  const int b = find_tile(p.seq, in_order, false, p.tpt, 1, p.qslots - 1 - work / p.Hkv, rt, s);  // late rows first
   if (b < 0) return;
-  const SeqSpan s = seq_span(p.seq, b);
-  if (!s.rows_ok) {
-    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-    return;
-  }
   const int i0 = rt * p.tpt, i1 = min(i0 + p.tpt, s.Lq);
   const int vis_last = s.ok ? s.Lk - s.Lq + i1 : 0;
   const int n = vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0;
   if (n == 0) {
-    if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
     for (int x = threadIdx.x; x < (i1 - i0) * p.hpg * (D / 8); x += kFbThreads) {
       const int r = x / (D / 8);
       const int64_t row = (int64_t(s.q0) + i0 + r / p.hpg) * p.Hq + g * p.hpg + r % p.hpg;
@@ -757,12 +752,14 @@ __global__ void __launch_bounds__(kFbThreads, 1)
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
     return tc::griddep_wait();
   }
+  const bool in_order = cta_in_order(p.seq, p.disorder);
+  if (!in_order && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
   // a cluster shares a key tile; row tiles are a CTA each
   const int cl = cluster_size(), nk = p.kslots * p.Hkv, row = int(blockIdx.x) - nk * cl;
   if (row < 0)
-    bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, fb_smem, blockIdx.x / cl, cl, cluster_rank());
+    bwd_dkv<D>(tmQ, tmO, tmK, tmV, p, in_order, fb_smem, blockIdx.x / cl, cl, cluster_rank());
   else if (row < p.qslots * p.Hkv)  // the last cluster may have CTAs to spare
-    bwd_dq<D>(tmQ, tmO, tmK, tmV, p, fb_smem, row);
+    bwd_dq<D>(tmQ, tmO, tmK, tmV, p, in_order, fb_smem, row);
   // Also CTAs without work: this grid must not be over before the one that still
   // writes the rows' data, or the workspace's next user would run beside it.
   tc::griddep_wait();
@@ -784,6 +781,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.status = &static_cast<WsHeader*>(f.ws)->status;
+  p.disorder = &static_cast<WsHeader*>(f.ws)->disorder;
   p.qslots = f.seq.Tq / p.tpt + f.seq.B;
   p.kslots = f.seq.Tk / kKeys + f.seq.B;
   const int64_t kc = int64_t(p.kslots) * f.Hkv, qc = int64_t(p.qslots) * f.Hkv;
@@ -793,7 +791,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   constexpr int bytes = FbSmem<D>::kTotal;
   cudaError_t e;
-  if ((e = launch_full_bwd_rows(a, stream))) return e;
+  if ((e = launch_order_check(f.seq, f.ws, stream)) || (e = launch_full_bwd_rows(a, stream))) return e;
   ProfScope pf("full_bwd", stream);
   const int c = cluster_split(kc, f.seq.Tq / f.seq.B / p.tpt);
   static KernelReady ready;

@@ -199,6 +199,15 @@ __device__ __forceinline__ int scan_tile(const SeqMap& m, bool keys, int tt, int
   return r;
 }
 
+// A CTA's tile by either way, and its sequence's span (`keys`: a key tile).
+__device__ __forceinline__ int find_tile(const SeqMap& m, bool in_order, bool keys, int tt, int mul, int i, int& tile,
+                                         SeqSpan& s) {
+  if (!in_order) return scan_tile(m, keys, tt, mul, i, tile, s);
+  const int b = find_slot_tile(keys ? m.cu_k : m.cu_q, m.B, tt, i, tile, mul);
+  if (b >= 0) s = seq_span(m, b);
+  return b;
+}
+
 // ---- launchers ---------------------------------------------------------------
 // Prepares a kernel once per device: its dynamic shared memory, and, where its
 // warpgroups exchange registers, that it was built with `regs` per thread (0:

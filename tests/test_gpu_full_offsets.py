@@ -143,6 +143,46 @@ def test_prefill_long_sequences(dtype):
                        ws, f"{cu.tolist()}")
 
 
+@pytest.mark.parametrize("side", ["rows", "keys", "both"])
+@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("B", SIZES)
+def test_backward(B, dtype, side):
+    Hq, Hkv, d = 4, 2, 64
+    lens = _lens(B, B)
+    T = sum(lens)
+    g = torch.Generator().manual_seed(4)
+    q, k, v, dout = (_rand(g, T, h, d, dtype) for h in (Hq, Hkv, Hkv, Hq))
+    fine = fp.offsets(lens)
+    ws = _workspace(msa.MSA_OP_FULL_BACKWARD, B, T, T, Hkv, Hq, d, dtype)
+    for bad in cases(lens, T):
+        cu_q, cu_k = (bad if side in ("rows", "both") else fine), (bad if side in ("keys", "both") else fine)
+        what = f"{side} {bad.tolist()[:8]}"
+        want, rows, keys = _want(q, k, v, cu_q, cu_k, dtype)
+        out, lse = want[0].nan_to_num(0.0).to(dtype), want[1].nan_to_num(0.0, neginf=-math.inf).float()
+        grads = [torch.full(x.shape, 7.0, dtype=dtype, device=DEV) for x in (q, k, v)]
+        on = [x.to(DEV) for x in (cu_q, cu_k)]
+        if side == "both":
+            on[1] = on[0]
+        msa.msa_full_attn_backward(*[x.to(DEV) for x in (q, k, v, out, dout, lse)], *on, *grads, ws=ws)
+        assert msa.msa_read_status(ws) == 6, what
+        ref = [torch.full(x.shape, 7.0, dtype=torch.float64) for x in (q, k, v)]
+        tol = [torch.zeros(x.shape, dtype=torch.float64) for x in (q, k, v)]
+        for b, a, n in rows:
+            ref[0][a:a + n] = 0
+        for b, (a, n) in keys.items():
+            ref[1][a:a + n] = ref[2][a:a + n] = 0
+        for b, a, n in rows:
+            if b not in keys or n == 0 or keys[b][1] == 0:
+                continue
+            k0, m = keys[b]
+            r, c = slice(a, a + n), slice(k0, k0 + m)
+            w, t = fp.backward(*[x.double() for x in (q[r], k[c], v[c], out[r], dout[r], lse[r])], d ** -0.5, dtype)
+            for dst, src, sl in zip(ref + tol, w + t, (r, c, c) * 2):
+                dst[sl] = src
+        for name, got, w, t in zip(("dq", "dk", "dv"), grads, ref, tol):
+            fp.assert_within(got, w, t, f"{name}, {what}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_no_keys_or_no_rows_at_all(dtype):
     """Calls without any key, or any row, look at both sides' offsets as well."""
