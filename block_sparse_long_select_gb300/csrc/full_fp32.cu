@@ -216,6 +216,7 @@ struct F32Params {
   const float2* rows;  // [Hkv][Tq][hpg]: lse in log2 units, delta (full_common.cu)
   float *out, *lse, *dq, *dk, *dv;
   uint32_t* status;
+  const uint32_t* disorder;
 };
 
 // Row x (token x / hpg, head x % hpg of group g) of a sequence in a [Tq, Hq] array.
@@ -229,20 +230,26 @@ __device__ __forceinline__ int64_t row_of(const F32Params& p, const SeqSpan& s, 
 // every second lap over the SMs. These CTAs are small and most calls put all of
 // them on the SMs at once, a lap after the other, so what counts is that each
 // SM's laps add up alike (three prompts of up to 999 tokens: the busiest SM had
-// 1.7 times the average). More sequences: by slots, late places first. Whole warp.
-__device__ __forceinline__ int find_row_tile(const F32Params& p, int work, int works, int& g, int& tile) {
+// 1.7 times the average). More sequences: by slots, late places first. Sets the
+// status where offsets are out of order. Whole CTA.
+__device__ __forceinline__ int find_row_tile(const F32Params& p, int work, int works, int& g, int& tile, SeqSpan& s) {
   if (p.seq.B > 32) {
+    const bool in_order = cta_in_order(p.seq, p.disorder);
+    if (!in_order && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
     g = work % p.Hkv;
-    return find_slot_tile(p.seq.cu_q, p.seq.B, kA, p.nslots - 1 - work / p.Hkv, tile, p.hpg);
+    return find_tile(p.seq, in_order, false, kA, p.hpg, p.nslots - 1 - work / p.Hkv, tile, s);
   }
   const int lane = threadIdx.x & 31, lap = work / kNumSMs, at = work % kNumSMs;
   const int rank = lap * kNumSMs + (lap & 1 ? min(kNumSMs, works - lap * kNumSMs) - 1 - at : at);
-  int mine = 0;
-  if (lane < p.seq.B) {
-    const SeqSpan s = seq_span(p.seq, lane);
-    mine = s.rows_ok ? (s.Lq * p.hpg + kA - 1) / kA : 0;
-    if (!s.rows_ok && work == 0 && lane < p.seq.B) set_status(p.status, MSA_ERR_BOUNDS);
+  // the warp has all offsets in hand: those out of order cost a prefix maximum, no second way to search
+  SeqSpan own{};
+  if (lane < p.seq.B) own = seq_span(p.seq, lane);
+  if (__any_sync(0xffffffffu, lane < p.seq.B && !span_in_order(p.seq, own))) {
+    SpanFloor floor;
+    floor.apply(p.seq, own);
+    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
   }
+  const int mine = lane < p.seq.B && own.rows_ok ? (own.Lq * p.hpg + kA - 1) / kA : 0;
   // tiles at places >= x, of all heads
   auto from = [&](int x) { return int(__reduce_add_sync(0xffffffffu, max(mine - x, 0))) * p.Hkv; };
   if (rank >= from(0)) return -1;
@@ -258,7 +265,10 @@ __device__ __forceinline__ int find_row_tile(const F32Params& p, int work, int w
   g = (rank - from(hi)) % p.Hkv;
   tile = lo;
   const uint32_t reach = __ballot_sync(0xffffffffu, mine > lo);
-  return __ffs(__ballot_sync(0xffffffffu, mine > lo && __popc(reach & ((1u << lane) - 1u)) == nth)) - 1;
+  const int b = __ffs(__ballot_sync(0xffffffffu, mine > lo && __popc(reach & ((1u << lane) - 1u)) == nth)) - 1;
+  auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, b); };
+  s = SeqSpan{of(own.q0), of(own.Lq), of(own.k0), of(own.Lk), of(own.rows_ok) != 0, of(own.keys_ok) != 0, of(own.ok) != 0};
+  return b;
 }
 
 // ---------------------------------------------------------------------------------
@@ -270,13 +280,9 @@ __global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_kernel(cons
   const uint32_t sq = tc::smem_u32(f32_smem), sk = sq + kA * D * 4, sv = sk + kB * D * 4, sp = sv + kB * D * 4;
   const int tx = tile_x(), ty = tile_y();
   int g, tile;
-  const int b = find_row_tile(p, blockIdx.x, gridDim.x, g, tile);
+  SeqSpan s;
+  const int b = find_row_tile(p, blockIdx.x, gridDim.x, g, tile, s);
   if (b < 0) return;
-  const SeqSpan s = seq_span(p.seq, b);
-  if (!s.rows_ok) {
-    if (threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-    return;
-  }
   const int x0 = tile * kA, x1 = min(x0 + kA, s.Lq * p.hpg);
   const int32_t* table = p.pages.table ? p.pages.table + int64_t(b) * p.pages.max_pages : nullptr;
   bool bad = !s.ok;
@@ -371,11 +377,8 @@ __global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_dq_kernel(c
   const int tx = tile_x(), ty = tile_y();
   const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   int g, tile;
-  const int b = find_row_tile(p, work, gridDim.x / cl, g, tile);
-  if (b < 0) return;
-  const SeqSpan s = seq_span(p.seq, b);
-  if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-  if (!s.rows_ok) return;
+  SeqSpan s;
+  if (find_row_tile(p, work, gridDim.x / cl, g, tile, s) < 0) return;
   const int x0 = tile * kA, x1 = min(x0 + kA, s.Lq * p.hpg);
   const int n = s.ok ? (max(s.Lk - s.Lq + (x1 - 1) / p.hpg + 1, 0) + kB - 1) / kB : 0;
   auto key = [&](const float* base, int j) -> const float* {
@@ -445,12 +448,12 @@ __global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_dkv_kernel(
   const int cl = cluster_size(), rank = cluster_rank(), work = blockIdx.x / cl;
   const int g = work % p.Hkv;
   int tile;
-  const int b = find_slot_tile(p.seq.cu_k, p.seq.B, kA, work / p.Hkv, tile);  // early keys: most rows
-  // also CTAs without work wait: this grid must not be over before the one that still writes the rows' data
-  if (b < 0) return tc::griddep_wait();
-  const SeqSpan s = seq_span(p.seq, b);
-  if (!s.ok && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-  if (!s.keys_ok) return tc::griddep_wait();
+  SeqSpan s;
+  const bool in_order = cta_in_order(p.seq, p.disorder);
+  if (!in_order && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+  // early keys first: most rows. Also CTAs without work wait: this grid must not
+  // be over before the one that still writes the rows' data
+  if (find_tile(p.seq, in_order, true, kA, 1, work / p.Hkv, tile, s) < 0) return tc::griddep_wait();
   const int j0 = tile * kA, off = s.ok ? s.Lk - s.Lq : 0, xn = s.ok ? s.Lq * p.hpg : 0;
   auto key = [&](const float* base, int j) -> const float* {
     return j < s.Lk ? base + ((int64_t(s.k0) + j) * p.Hkv + g) * D : nullptr;
@@ -536,6 +539,7 @@ F32Params params(const FullArgs& a) {
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   p.status = &static_cast<WsHeader*>(a.ws)->status;
+  p.disorder = &static_cast<WsHeader*>(a.ws)->disorder;
   return p;
 }
 
@@ -559,6 +563,7 @@ cudaError_t forward(const FullArgs& a, cudaStream_t stream) {
   F32Params p = params(a);
   p.out = static_cast<float*>(a.out);
   p.lse = a.lse;
+  if (cudaError_t e = launch_order_check(a.seq, a.ws, stream)) return e;
   static KernelReady ready;
   return run("full_f32", ready, full_f32_kernel<D>, p, int(int64_t(a.seq.Tq) * p.hpg / kA) + a.seq.B, 1,
              (kA + 2 * kB) * D * 4 + kA * kPitch * 4, false, stream);
@@ -572,6 +577,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.dq = static_cast<float*>(a.dq);
   p.dk = static_cast<float*>(a.dk);
   p.dv = static_cast<float*>(a.dv);
+  if (cudaError_t e = launch_order_check(f.seq, f.ws, stream)) return e;
   if (cudaError_t e = launch_full_bwd_rows(a, stream)) return e;
   constexpr int m = kA * kPitch * 4;
   static KernelReady dkv, dq;

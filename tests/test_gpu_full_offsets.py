@@ -85,7 +85,7 @@ def _check_prefill(call, want, shape, dtype, ws, what):
 
 
 @pytest.mark.parametrize("side", ["rows", "keys", "both"])
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("B", SIZES)
 def test_prefill(B, dtype, side):
     Hq, Hkv, d = 4, 2, 64
@@ -105,7 +105,7 @@ def test_prefill(B, dtype, side):
                        ws, f"{side} {bad.tolist()[:8]}")
 
 
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("B", SIZES)
 def test_prefill_paged(B, dtype):
     Hq, Hkv, d, page = 8, 2, 64, 16
@@ -126,7 +126,7 @@ def test_prefill_paged(B, dtype):
                        q.shape, dtype, ws, f"{bad.tolist()[:8]}")
 
 
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_prefill_long_sequences(dtype):
     """Few long sequences, whose work is divided into equal shares when the offsets are in order."""
     Hq, Hkv, d, lens = 2, 1, 64, [900, 40, 1700]
@@ -144,7 +144,7 @@ def test_prefill_long_sequences(dtype):
 
 
 @pytest.mark.parametrize("side", ["rows", "keys", "both"])
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("B", SIZES)
 def test_backward(B, dtype, side):
     Hq, Hkv, d = 4, 2, 64
