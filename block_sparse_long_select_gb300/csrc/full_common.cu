@@ -7,7 +7,8 @@ namespace msa {
 namespace {
 
 // Per row: lse in log2 units (+inf where no key is seen, so that the row's
-// weights are 0) and delta = dout . out, laid out as the backward's row tiles,
+// weights are 0; NaN where the output is NaN as well, the weights being
+// undefined) and delta = dout . out, laid out as the backward's row tiles,
 // [Hkv][Tq][hpg]. A thread per 16-byte chunk; bound by HBM (out and dout once).
 constexpr int kRowsPer = 4;
 template <typename T, int D>
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(256) full_bwd_rows_kernel(const uint4* __restr
       const uint32_t t = uint32_t(x) / uint32_t(Hq), h = uint32_t(x) % uint32_t(Hq);
       const float l = lse[x];
       rows[(int64_t(h / uint32_t(hpg)) * Tq + t) * hpg + h % uint32_t(hpg)] =
-          make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+          make_float2(l != -INFINITY ? l * 1.4426950408889634f : s == s ? INFINITY : NAN, s);
     }
   }
 }

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kF32Threads, kF32Ctas<D>) full_f32_kernel(cons
     const int x = x0 + ty * 4 + i;
     if (x >= x1) continue;
     const int64_t row = row_of(p, s, g, x);
-    const bool some = den > 0.f || den != den;
+    const bool some = !bad && vis[i] > 0;  // scores that are all -inf divide 0 by 0, as the formula does
     store_rows<D>(p.out + row * D, acc[i], some ? 1.f / den : 0.f);
     if (p.lse && tx == 0) p.lse[row] = some ? (m[i] + log2f(den)) * kLn2f : -INFINITY;
   }

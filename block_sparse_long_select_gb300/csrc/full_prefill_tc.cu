@@ -547,8 +547,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (valid && p.lse) p.lse[row] = -INFINITY;
         continue;
       }
-      const int vis = off + i + 1;                           // keys this row sees
-      const int j_mask = max(off + first + 1, 0) / kKeys;    // tiles below it are seen whole by every row of the tile
+      const int vis = off + i + 1;  // keys this row sees
+      // a row without any is 0; one whose scores are all -inf divides 0 by 0, as its formula does
+      const bool some = vis > 0;
+      const int j_mask = max(off + first + 1, 0) / kKeys;  // tiles below it are seen whole by every row of the tile
       for (int j = jb; j < jb + n; ++j, ++z) {
         if (!(ok = warp_wait(&s_full[w], z & 1, abort_flag))) break;
         tc::fence_after_sync();
@@ -663,7 +665,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0) tc::mbar_arrive(&o_empty[w]);
       };
       if (mode == 0) {
-        const bool some = l > 0.f || l != l;
         store_rows(row, valid, some ? 1.f / l : 0.f, some, from_tmem);
         release();
         if (valid && p.lse) p.lse[row] = some ? (m + log2f(l)) * kLn2f : -INFINITY;
@@ -722,7 +723,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int y = 0; y < 4; ++y)
           if (y0 + y < parts) den = fmaf(ml[y].x == M ? 1.f : ex2(ml[y].x - M), ml[y].y, den);
       }
-      const bool some = den > 0.f || den != den;
       float acc[D];
 #pragma unroll
       for (int x = 0; x < D; ++x) acc[x] = 0.f;

@@ -319,6 +319,8 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  *  Visibility    query row i of Lq sees keys j <= Lk - Lq + i of Lk: the last
  *                row sees every key. If Lq > Lk the first Lq - Lk rows see
  *                none: their output and gradient are 0 and their lse -inf.
+ *                A row that sees keys, all with a score of -inf, divides 0 by
+ *                0: its output and gradient are NaN, its lse -inf.
  * Supported by all: d in {64, 128}; Hq / Hkv an integer up to 64, Hq up to
  * 65536; BF16 (tensor cores, fp32 accumulation) or FP32 (CUDA cores).
  * Device-side checks: a sequence whose cu, kv_len or page entry is out of
