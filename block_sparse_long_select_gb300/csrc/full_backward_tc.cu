@@ -73,6 +73,15 @@ struct FbBars {
     tail = acc_full + 1;
     done = tail + 1;
   }
+  // One thread per barrier (of `bars`, from b on). 8 epilogue warps hand over P,
+  // dS and the row data's slots, 2 warps fill those; else one arrival.
+  __device__ __forceinline__ void init(uint64_t* b, int slots, int bars) const {
+    if (threadIdx.x >= bars) return;
+    const uint64_t* x = b + threadIdx.x;
+    const bool by_epilogue = x == p_full || x == ds_full || (x >= r_empty && x < r_empty + slots);
+    tc::mbar_init(b + threadIdx.x, by_epilogue ? 8 : x >= r_full && x < r_full + slots ? 2 : 1);
+    tc::fence_barrier_init();
+  }
 };
 
 // bf16 pairs of 64 columns go over the first half of the 64 columns they came
@@ -206,17 +215,8 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* rowd = reinterpret_cast<float*>(fb_smem + SM::oRow);  // slot x: -lse2 [128], -delta [128]
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
-    tc::mbar_init(bar.p_full, 8);
-    tc::mbar_init(bar.ds_full, 8);
-    for (int x = 0; x < NR; ++x) {
-      tc::mbar_init(bar.r_full + x, 2);
-      tc::mbar_init(bar.r_empty + x, 8);
-    }
-    *abort_flag = 0;
-    tc::fence_barrier_init();
-  }
+  bar.init(bars, NR, SM::kBars);
+  if (threadIdx.x == 0) *abort_flag = 0;
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
@@ -525,13 +525,8 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   const FbBars bar(bars, SM::kRowSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
-    tc::mbar_init(bar.p_full, 8);
-    tc::mbar_init(bar.ds_full, 8);
-    *abort_flag = 0;
-    tc::fence_barrier_init();
-  }
+  bar.init(bars, SM::kRowSlots, SM::kBars);
+  if (threadIdx.x == 0) *abort_flag = 0;
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();

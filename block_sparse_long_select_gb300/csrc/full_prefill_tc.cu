@@ -125,13 +125,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;
   if (threadIdx.x == 0) {
-    for (int x = 0; x < SM::kBars; ++x) tc::mbar_init(bars + x, 1);
-    for (int x = 0; x < 2; ++x) {
-      tc::mbar_init(p_full + x, 4);
-      tc::mbar_init(o_empty + x, 4);
-    }
-    for (int x = 0; x < NI; ++x) tc::mbar_init(item_empty + x, 10);  // loads, MMA, 8 softmax warps
-    tc::mbar_init(part_bar, 8);
+    auto init = [](uint64_t* b, int n, uint32_t arrivals) {
+#pragma unroll
+      for (int x = 0; x < n; ++x) tc::mbar_init(b + x, arrivals);
+    };
+    init(bars, int(p_full - bars), 1);
+    init(p_full, 2, 4);  // a row tile's softmax warps
+    init(o_full, 2, 1);
+    init(o_empty, 2, 4);
+    init(item_full, NI, 1);
+    init(item_empty, NI, 10);  // loads, MMA, 8 softmax warps
+    init(part_bar, 1, 8);
+    init(flag_bar, 3, 1);  // flag, tail, done
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
