@@ -42,6 +42,7 @@ struct FbParams {
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* status;
   const uint32_t* disorder;
+  int inject_timeout;  // test hook: every second CTA waits on a barrier nothing completes
 };
 
 template <int D>
@@ -51,12 +52,12 @@ struct FbSmem {
   // two resident tiles, then a ring of two slots for each of two streamed operands
   static constexpr uint32_t oA = 0, oB = kTile, oC = 2 * kTile, oE = 4 * kTile, oRow = 6 * kTile;
   static constexpr uint32_t oBar = oRow + kRowSlots * 2 * kRows * 4;
-  static constexpr int kBars = 1 + 8 + 4 + 2 * kRowSlots + 3;
+  static constexpr int kBars = 1 + 8 + 4 + 2 * kRowSlots + 4;
   static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
 };
 struct FbBars {
   uint64_t *res_full, *c_full, *c_empty, *e_full, *e_empty, *s_full, *p_full, *dp_full, *ds_full, *r_full, *r_empty,
-      *acc_full, *tail, *done;
+      *acc_full, *tail, *done, *never;
   __device__ __forceinline__ FbBars(uint64_t* b, int slots) {
     res_full = b;
     c_full = b + 1;
@@ -72,6 +73,7 @@ struct FbBars {
     acc_full = r_empty + slots;
     tail = acc_full + 1;
     done = tail + 1;
+    never = done + 1;  // no thread arrives on it (timeout injection)
   }
   // One thread per barrier (of `bars`, from b on). 8 epilogue warps hand over P,
   // dS and the row data's slots, 2 warps fill those; else one arrival.
@@ -292,6 +294,8 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
           tc::mbar_arrive(bar.e_full + st);
         }
       }
+      if (p.inject_timeout && i == 0 && blockIdx.x % 2 == 0)
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_for(bar.never, 0, abort_flag, tc::kInjectedWaitCycles));
     }
     if (!ok) {
       fail();
@@ -591,6 +595,8 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
           tc::mbar_arrive(bar.e_full + st);
         }
       }
+      if (p.inject_timeout && j == 0 && blockIdx.x % 2 == 0)
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_for(bar.never, 0, abort_flag, tc::kInjectedWaitCycles));
     }
     if (!ok) {
       fail();
@@ -777,6 +783,7 @@ cudaError_t backward(const FullBwdArgs& a, cudaStream_t stream) {
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.status = &static_cast<WsHeader*>(f.ws)->status;
   p.disorder = &static_cast<WsHeader*>(f.ws)->disorder;
+  p.inject_timeout = debug_inject_timeout() ? 1 : 0;
   p.qslots = f.seq.Tq / p.tpt + f.seq.B;
   p.kslots = f.seq.Tk / kKeys + f.seq.B;
   const int64_t kc = int64_t(p.kslots) * f.Hkv, qc = int64_t(p.qslots) * f.Hkv;

@@ -65,6 +65,7 @@ struct PfParams {
   uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
   uint32_t* queue;     // next item to hand out, zero between calls
   uint32_t* status;
+  int inject_timeout;  // test hook: every second CTA waits on a barrier nothing completes
 };
 
 struct PfItem {
@@ -84,7 +85,7 @@ struct PfSmem {
   static constexpr uint32_t oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile, oStore = oV + kStages * kTile;
   static constexpr uint32_t kStore = 32 * 128;  // per softmax warp: 32 rows x 64 columns
   static constexpr uint32_t oItem = oStore + 8 * kStore, oBar = oItem + kItems * sizeof(PfItem);
-  static constexpr int kBars = 4 + 4 * kStages + 2 + 2 + 4 + 2 * kItems + 2 + 2;
+  static constexpr int kBars = 4 + 4 * kStages + 2 + 2 + 4 + 2 * kItems + 2 + 3;
   static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
 };
 
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t* flag_bar = part_bar + 1;      // whether this CTA is the last of the item's
   uint64_t* tail_bar = flag_bar + 1;      // the copies of a value tile whose last rows are then zeroed
   uint64_t* done_bar = tail_bar + 1;
+  uint64_t* never_bar = done_bar + 1;     // no thread arrives on it (timeout injection)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     init(item_full, NI, 1);
     init(item_empty, NI, 10);  // loads, MMA, 8 softmax warps
     init(part_bar, 1, 8);
-    init(flag_bar, 3, 1);  // flag, tail, done
+    init(flag_bar, 4, 1);  // flag, tail, done, never
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -238,6 +240,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (lane == 0) tc::mbar_arrive(&v_full[st]);
           }
           row = next;
+          if (p.inject_timeout && z == 0 && blockIdx.x % 2 == 0 &&
+              !(ok = __all_sync(0xffffffffu, tc::mbar_wait_for(never_bar, 0, abort_flag, tc::kInjectedWaitCycles))))
+            break;
         }
       }
       if (!ok) {  // let the copies land before the CTA gives its shared memory up
@@ -797,6 +802,7 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
   p.status = &header->status;
   p.arrivals = header->arrivals;
   p.queue = &header->queue;
+  p.inject_timeout = debug_inject_timeout() ? 1 : 0;
   if (int64_t(p.nslots) * a.Hkv >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
   if (pf_splits(a.seq.Tk)) {
     char* w = static_cast<char*>(a.ws) + kWsHeader;

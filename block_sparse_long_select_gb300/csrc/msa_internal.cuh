@@ -75,8 +75,8 @@ __device__ __forceinline__ SeqView seq_view(const int32_t* q_offset, const int32
   return s;
 }
 
-// Test hook (msa_debug_inject_timeout): attention kernels first make one
-// bounded wait that runs out.
+// Test hook (msa_debug_inject_timeout): attention kernels with bounded waits
+// first make one that runs out.
 bool debug_inject_timeout();
 
 // RAII bracket of one kernel launch with a CUDA event pair while profiling is

@@ -33,7 +33,9 @@ int msa_profile_end(msa_kernel_time_t* out, int max_entries);
 /* Test hook for the bounded-wait timeout path (no counterpart in the paper).
  * While enabled (enable != 0), every launch of the prefill attention kernel
  * (tensor-core path) and of the decode attention kernel first waits on a
- * device barrier that nothing completes. That wait gives up after about a
+ * device barrier that nothing completes. So do every second CTA of the bf16
+ * full-attention prefill and backward, behind its first copies, so that the
+ * other CTAs leave their marks in the workspace. That wait gives up after about a
  * millisecond; the kernel then records MSA_ERR_TIMEOUT in the workspace status,
  * lets the copies and matrix products it has in flight finish, frees its
  * tensor memory and returns. The outputs of such a call are unspecified; the
