@@ -241,3 +241,51 @@ def test_append(B, dtype):
             wq[a:a + n], wk[at], wv[at] = q[a:a + n], k[a:a + n], v[a:a + n]
         assert torch.equal(qo.cpu(), wq), f"q_out, {what}"
         assert torch.equal(kc.cpu().flatten(0, 1), wk) and torch.equal(vc.cpu().flatten(0, 1), wv), f"cache, {what}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("B", [40, 300])
+def test_captured(B, dtype):
+    """A graph of append, prefill and backward replayed over offsets that are in
+    order, then not, then again: every replay looks at them anew."""
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    lens = [1 + n % 31 for n in _lens(B, B)]
+    T = sum(lens)
+    g = torch.Generator().manual_seed(7)
+    q, k, v, dout = (_rand(g, T, h, d, dtype).to(DEV) for h in (Hq, Hkv, Hkv, Hq))
+    fine = fp.offsets(lens)
+    broken = fine.clone()
+    broken[B // 2] = T + 5
+    cu, kv = fine.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    table = torch.arange(2 * B, dtype=torch.int32, device=DEV).view(B, 2)
+    kc, vc = (torch.zeros(2 * B, page, Hkv, d, dtype=dtype, device=DEV) for _ in range(2))
+    out, lse, qo = torch.empty_like(q), torch.empty(T, Hq, device=DEV), torch.empty_like(q)
+    grads = [torch.empty_like(x) for x in (q, k, v)]
+    ws = [_workspace(op, B, T, T, Hkv, Hq, d, dtype)
+          for op in (msa.MSA_OP_PAGED_APPEND, msa.MSA_OP_FULL_PREFILL, msa.MSA_OP_FULL_BACKWARD)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        msa.msa_paged_append(q, k, v, None, cu, kv, table, kc, vc, q_out=qo, ws=ws[0])
+        msa.msa_full_attn_prefill(q, k, v, cu, cu, out=out, lse=lse, ws=ws[1])
+        msa.msa_full_attn_backward(q, k, v, out, dout, lse, cu, cu, *grads, ws=ws[2])
+    first = None
+    for now, status in ((fine, 0), (broken, 6), (fine, 0)):
+        cu.copy_(now)
+        everything = [qo, kc, vc, out, lse, *grads]
+        for x in everything:
+            x.fill_(7.0)
+        graph.replay()
+        assert [msa.msa_read_status(w) for w in ws] == [status] * 3
+        if first is None:
+            first = [x.clone() for x in everything]
+        elif status == 0:
+            assert all(torch.equal(a, b) for a, b in zip(first, everything))
+        else:
+            a, e = int(fine[B // 2 - 1]), int(fine[B // 2 + 1])  # rows of the two sequences at the broken offset
+            for x, y in zip((qo, out, lse, *grads), (first[0], first[3], first[4], *first[5:])):
+                assert (x[a:e] == 7.0).all() and torch.equal(x[:a], y[:a]) and torch.equal(x[e:], y[e:])
+            b = B // 2
+            for x, y in zip((kc, vc), first[1:3]):
+                assert (x[2 * b - 2:2 * b + 2] == 7.0).all()
+                assert torch.equal(x[:2 * b - 2], y[:2 * b - 2]) and torch.equal(x[2 * b + 2:], y[2 * b + 2:])

@@ -1,5 +1,5 @@
-"""Rows whose visible scores are all -inf, and long prompts whose items are
-handed out whole."""
+"""Rows whose visible scores are all -inf; long prompts, whose items are handed
+out whole, and the gradients of long documents."""
 import math
 
 import pytest
@@ -94,3 +94,45 @@ def test_gradients_of_rows_without_a_finite_score(dtype):
     w, t = fp.backward(*[x[sl].double() for x in (q, k, v, out.cpu(), dout, lse.cpu())], q.shape[-1] ** -0.5, dtype)
     for name, got, x, y in zip(("dq", "dk", "dv"), (dq, dk, dv), w, t):
         fp.assert_within(got[sl], x, y, name)
+
+
+@pytest.mark.parametrize("heads,lens", [((32, 8, 128), [8192]), ((16, 16, 64), [5000, 1, 3333])])
+def test_long_prompts(heads, lens):
+    """Whole prompts of thousands of tokens: many items of many key tiles each,
+    handed out whole. Rows all over the prompt against the plain form."""
+    Hq, Hkv, d = heads
+    T = sum(lens)
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(T, h, d, generator=g).to(BF16) for h in (Hq, Hkv, Hkv))
+    cu = fp.offsets(lens).to(DEV)
+    lse = torch.empty(T, Hq, device=DEV)
+    out = msa.msa_full_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu, cu, lse=lse).cpu()
+    lse = lse.cpu()
+    q0 = 0
+    for n in lens:
+        for i in sorted({0, min(1, n - 1), n // 3, n // 2, max(n - 130, 0), n - 1} | set(range(min(n, 64) - 1, n, 511))):
+            kk, vv = k[q0:q0 + i + 1], v[q0:q0 + i + 1]
+            w = fp.prefill(q[q0 + i:q0 + i + 1], [kk], [vv], [(0, 1)], d ** -0.5, BF16)
+            fp.assert_within(out[q0 + i:q0 + i + 1], w[0], w[2], f"row {i} of {n}")
+            fp.assert_within(lse[q0 + i:q0 + i + 1], w[1], w[3], f"lse of row {i} of {n}")
+        q0 += n
+
+
+@pytest.mark.parametrize("heads,lens", [((4, 1, 128), [4100]), ((2, 2, 64), [3000, 77, 1500])])
+def test_gradients_of_long_documents(heads, lens):
+    """Walks of dozens of tiles, on key and row tiles alike, against the formula."""
+    Hq, Hkv, d = heads
+    g = torch.Generator().manual_seed(4)
+    q, k, v, dout = (torch.randn(sum(lens), h, d, generator=g).to(BF16).to(DEV) for h in (Hq, Hkv, Hkv, Hq))
+    cu = fp.offsets(lens).to(DEV)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = msa.msa_full_attn_prefill(q, k, v, cu, cu, lse=lse)
+    got = msa.msa_full_attn_backward(q, k, v, out, dout, lse, cu, cu)
+    at = 0
+    for n in lens:
+        sl = slice(at, at + n)
+        with torch.device(DEV):  # 64-bit matrices of n x n scores
+            want, tol = fp.backward(*[x[sl].double() for x in (q, k, v, out, dout, lse)], d ** -0.5, BF16)
+        for name, x, w, t in zip(("dq", "dk", "dv"), got, want, tol):
+            fp.assert_within(x[sl], w.cpu(), t.cpu(), f"{name} of {n}")
+        at += n
