@@ -93,11 +93,6 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
 // 16-byte chunk c of row r of a fp32 partial [rows][D]; chunks are exchanged by
 // the row's low bits, so that a thread per row writes without bank conflicts.
 template <int D>
