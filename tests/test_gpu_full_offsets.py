@@ -154,7 +154,7 @@ def test_backward(B, dtype, side):
     q, k, v, dout = (_rand(g, T, h, d, dtype) for h in (Hq, Hkv, Hkv, Hq))
     fine = fp.offsets(lens)
     ws = _workspace(msa.MSA_OP_FULL_BACKWARD, B, T, T, Hkv, Hq, d, dtype)
-    for bad in cases(lens, T):
+    for bad in cases(lens, T)[::1 if B < 300 else 2]:
         cu_q, cu_k = (bad if side in ("rows", "both") else fine), (bad if side in ("keys", "both") else fine)
         what = f"{side} {bad.tolist()[:8]}"
         want, rows, keys = _want(q, k, v, cu_q, cu_k, dtype)
