@@ -68,6 +68,10 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqMap& m, int b) {
 // looks, 148 us with the grid; 30446 of 1000: 66, 74 and 70; 12473 of 256: 21, then
 // 25 either way).
 constexpr int kSelfChecked = 256;
+// Every CTA goes through the sequences, so that the time grows with their square
+// (estimated at a second or two for gradients of 65536). More than that many out
+// of order are left alone: no sequence counts as found.
+constexpr int kMostScanned = 1 << 16;
 __device__ __forceinline__ bool span_in_order(const SeqMap& m, const SeqSpan& s) {
   return s.rows_ok && (m.kv_len || s.keys_ok);  // a wrong kv_len misleads no search
 }
@@ -104,9 +108,10 @@ struct SpanFloor {
   }
 };
 // f(b, span) with the whole warp for 32 sequences at a time (b >= B: an empty
-// span out of range), until it returns true.
+// span out of range), until it returns true. Not at all beyond kMostScanned.
 template <typename F>
 __device__ __forceinline__ void each_32_seqs(const SeqMap& m, F f) {
+  if (m.B > kMostScanned) return;
   SpanFloor floor;
   for (int b0 = 0; b0 < m.B; b0 += 32) {
     const int b = b0 + int(threadIdx.x & 31);

@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           int tile;
           SeqSpan s;
           const int sb = scan_tile(p.seq, false, w2, 1, i / p.Hkv, tile, s);
-          if (sb < 0 || !s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
+          if (sb < 0) break;  // nor are there any further on
+          if (!s.ok || s.Lk - s.Lq + min((tile + 1) * w2, s.Lq) <= 0) continue;  // no keys: below
           PfItem d{};
           describe(d, sb, i % p.Hkv, tile, s);
           d.n = d.mode == 2 ? 0 : d.tiles;
@@ -465,13 +466,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const bool by_row = disorder || p.seq.B <= ctas;
       SpanFloor floor;
       const int lane_step = by_row ? 1 : ctas;
-      for (int64_t b0 = by_row ? 0 : me; b0 < p.seq.B; b0 += 32 * lane_step) {
+      const int seqs = disorder && p.seq.B > kMostScanned ? 0 : p.seq.B;
+      if (disorder && lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
+      for (int64_t b0 = by_row ? 0 : me; b0 < seqs; b0 += 32 * lane_step) {
         const int64_t b = b0 + int64_t(lane) * lane_step;
         SeqSpan s{};
         int rows = 0;  // of the sequence, from its first on
-        if (b < p.seq.B) s = seq_span(p.seq, int(b));
+        if (b < seqs) s = seq_span(p.seq, int(b));
         if (disorder) floor.apply(p.seq, s);
-        if (b < p.seq.B) {
+        if (b < seqs) {
           if (!s.ok) set_status(p.status, MSA_ERR_BOUNDS);
           if (s.rows_ok) rows = !s.ok || s.Lk == 0 ? s.Lq : s.Lk < s.Lq ? (s.Lq - s.Lk) / w2 * w2 : 0;
         }

@@ -327,7 +327,8 @@ msa_status_t msa_sparse_attn_backward(const void* q, const void* k, const void* 
  * range sets MSA_ERR_BOUNDS in the workspace status and nothing out of range is
  * read or written for it; the other sequences get their results. If its rows
  * are known (its cu is in range) its output rows are 0 and their lse -inf;
- * otherwise they stay as they were.
+ * otherwise they stay as they were. A call of more than 65536 sequences whose
+ * cu are not all in range sets the status and writes nothing.
  * A workspace may serve all operations in turn, if it has the largest size. */
 
 /* Appends the keys and values of T packed new tokens to a paged cache, with

@@ -289,3 +289,32 @@ def test_captured(B, dtype):
             for x, y in zip((kc, vc), first[1:3]):
                 assert (x[2 * b - 2:2 * b + 2] == 7.0).all()
                 assert torch.equal(x[:2 * b - 2], y[:2 * b - 2]) and torch.equal(x[2 * b + 2:], y[2 * b + 2:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_very_many_sequences(dtype):
+    """More than 65536 sequences: served where their offsets are in order, left alone where not."""
+    B, d = 65600, 64
+    q, k, v, dout = (torch.randn(B, 1, d, device=DEV).to(dtype) for _ in range(4))
+    lse = torch.empty(B, 1, device=DEV)
+    fine = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    bad = fine.clone()
+    bad[40000] = -1
+    kv, table = torch.ones(B, dtype=torch.int32, device=DEV), fine[:B, None].contiguous()
+    ws = max((_workspace(op, B, B, B, 1, 1, d, dtype) for op in (msa.MSA_OP_FULL_PREFILL, msa.MSA_OP_FULL_BACKWARD)),
+             key=torch.numel)
+    for cu, status in ((fine, 0), (bad, 6)):
+        out, qo, dq, dk, dv = (torch.full_like(q, 7.0) for _ in range(5))
+        kc, vc = (torch.full((B, 16, 1, d), 7.0, dtype=dtype, device=DEV) for _ in range(2))
+        msa.msa_full_attn_prefill(q, k, v, cu, cu, out=out, lse=lse, ws=ws)
+        assert msa.msa_read_status(ws) == status
+        msa.msa_full_attn_backward(q, k, v, v, dout, lse, cu, cu, dq, dk, dv, ws=ws)
+        assert msa.msa_read_status(ws) == status
+        msa.msa_paged_append(q, k, v, None, cu, kv, table, kc, vc, q_out=qo, ws=ws)
+        assert msa.msa_read_status(ws) == status
+        if status == 0:  # one key each: its weight is 1, in the backward within 2^-17 (|s| < 8, fp32 exponent)
+            assert torch.equal(out, v) and torch.equal(qo, q)
+            assert ((dv - dout).abs() <= 2.0 ** -17 * dout.abs()).all()
+            assert torch.equal(kc[:, 0], k) and torch.equal(vc[:, 0], v)
+        else:
+            assert all((x == 7.0).all() for x in (out, qo, dq, dk, dv, kc, vc))
