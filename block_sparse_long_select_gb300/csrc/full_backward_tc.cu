@@ -18,8 +18,8 @@
 // scores run. P and dS are rounded to bf16 for the products that read them
 // (2^-8 each, averaging out over the sums); sums stay in fp32.
 //
-// Measured (Hq 32, Hkv 8, d 128): 8192 tokens 1.29 ms alone, 1.35 ms in a loop
-// (74 % of the measured tensor rate on the seven products, 52 % on five).
+// Measured (Hq 32, Hkv 8, d 128): 8192 tokens 1.38 ms in a loop (73 % of the
+// measured tensor rate on the seven products, 52 % on five).
 //
 // Warps of both: 0 loads (TMA; zeroes rows of other sequences, whose
 // infinities a weight of 0 would not silence), 1 MMA issue and TMEM, 4-11
