@@ -9,7 +9,8 @@ carry the C names:
     msa_sparse_attn_prefill, msa_sparse_attn_decode, msa_decode_step,
     msa_kl_aux_forward, msa_sparse_attn_backward, msa_paged_append,
     msa_full_attn_decode, msa_full_attn_prefill, msa_full_attn_prefill_paged,
-    msa_full_attn_backward, msa_read_status, msa_status_string
+    msa_full_attn_backward, msa_paged_append_fp8, msa_paged_read_fp8,
+    msa_full_attn_decode_fp8, msa_read_status, msa_status_string
 
 There is no CPU fallback: if ``libmsa.so`` is missing or was not built for
 this GPU, every call raises.
@@ -24,10 +25,13 @@ from ._lib import (  # noqa: F401
     MSA_OP_DECODE_STEP,
     MSA_OP_FULL_BACKWARD,
     MSA_OP_FULL_DECODE,
+    MSA_OP_FULL_DECODE_FP8,
     MSA_OP_FULL_PREFILL,
     MSA_OP_INDEX_SELECT,
     MSA_OP_KL_AUX,
     MSA_OP_PAGED_APPEND,
+    MSA_OP_PAGED_APPEND_FP8,
+    MSA_OP_PAGED_READ_FP8,
     MSA_OP_PREFILL,
     MsaError,
     lib_path,
@@ -35,6 +39,7 @@ from ._lib import (  # noqa: F401
     msa_debug_inject_timeout,
     msa_full_attn_backward,
     msa_full_attn_decode,
+    msa_full_attn_decode_fp8,
     msa_full_attn_prefill,
     msa_full_attn_prefill_paged,
     msa_index_select,
@@ -45,6 +50,8 @@ from ._lib import (  # noqa: F401
     msa_profile_end,
     msa_decode_step,
     msa_paged_append,
+    msa_paged_append_fp8,
+    msa_paged_read_fp8,
     msa_read_status,
     msa_sparse_attn_backward,
     msa_sparse_attn_decode,

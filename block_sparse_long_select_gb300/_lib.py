@@ -8,6 +8,7 @@ from functools import lru_cache
 MSA_BF16, MSA_FP32 = 0, 1
 MSA_OP_INDEX_SELECT, MSA_OP_PREFILL, MSA_OP_DECODE, MSA_OP_DECODE_STEP, MSA_OP_KL_AUX, MSA_OP_BACKWARD = 0, 1, 2, 3, 4, 5
 MSA_OP_FULL_PREFILL, MSA_OP_FULL_BACKWARD, MSA_OP_FULL_DECODE, MSA_OP_PAGED_APPEND = 8, 9, 10, 11
+MSA_OP_PAGED_APPEND_FP8, MSA_OP_PAGED_READ_FP8, MSA_OP_FULL_DECODE_FP8 = 13, 14, 15
 MSA_FORCE_LOCAL, MSA_FORCE_START = 1, 2
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_WORKSPACE",
                 4: "MSA_ERR_CUDA", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_BOUNDS"}
@@ -25,6 +26,9 @@ SIGNATURES = {
     "msa_sparse_attn_backward": (_i32, [_vp] * 9 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "msa_paged_append": (_i32, [_vp] * 7 + [_i32] * 12 + [_vp] * 4 + [_sz, _vp]),
     "msa_full_attn_decode": (_i32, [_vp] * 5 + [_i32] * 7 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "msa_paged_append_fp8": (_i32, [_vp] * 7 + [_i32] * 12 + [_vp] * 6 + [_sz, _vp]),
+    "msa_paged_read_fp8": (_i32, [_vp] * 7 + [_i32] * 8 + [_vp] * 3 + [_sz, _vp]),
+    "msa_full_attn_decode_fp8": (_i32, [_vp] * 7 + [_i32] * 7 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "msa_full_attn_prefill": (_i32, [_vp] * 5 + [_i32] * 6 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "msa_full_attn_prefill_paged": (_i32, [_vp] * 6 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "msa_full_attn_backward": (_i32, [_vp] * 8 + [_i32] * 6 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -452,6 +456,140 @@ def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out
                                                page_size, max_pages, scale, dt, out.data_ptr(), _addr(lse),
                                                ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     _check(code, "msa_full_attn_decode")
+    return out
+
+
+def _need_fp8(k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks the four tensors of a cache in 8 bits; its num_pages, page_size, Hkv and d."""
+    torch = _torch()
+    shape = num_pages, page_size, Hkv, d = _rows("k_cache", k_cache, 4)
+    _need("k_cache", k_cache, torch.float8_e4m3fn, dev, shape)
+    _need("v_cache", v_cache, torch.float8_e4m3fn, dev, shape)
+    _need("k_scale", k_scale, torch.float32, dev, (num_pages, Hkv, page_size))
+    _need("v_scale", v_scale, torch.float32, dev, (num_pages, Hkv, page_size))
+    return num_pages, page_size, Hkv, d
+
+
+def msa_paged_append_fp8(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache, v_cache, k_scale, v_scale,
+                         interleaved=False, q_out=None, ws=None, stream=None):
+    """msa_paged_append into a cache in 8 bits (see include/msa.h): caches
+    [num_pages, page_size, Hkv, d] float8_e4m3fn, scales [num_pages, Hkv, page_size]
+    fp32. Returns the rotated queries (None without q)."""
+    torch = _torch()
+    shape = _rows("k_new", k_new)
+    T, Hkv, d = shape
+    dev, dtype, i32 = k_new.get_device(), k_new.dtype, torch.int32
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_paged_append_fp8(q, k_new, v_new, rope, cu_new, kv_len, page_table, k_cache, v_cache, k_scale,
+                                        v_scale, interleaved, q_out, ws)
+    num_pages, page_size, *heads = _need_fp8(k_cache, v_cache, k_scale, v_scale, dev)
+    if heads != [Hkv, d]:
+        raise ValueError(f"k_cache must be [num_pages, page_size, {Hkv}, {d}]; got {tuple(k_cache.shape)}")
+    B, max_pages = page_table.shape
+    Hq = Hkv
+    if q is not None:
+        Hq = _rows("q", q)[1]
+        _need("q", q, dtype, dev, (T, Hq, d))
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _need("q_out", q_out, dtype, dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _need("v_new", v_new, dtype, dev, shape)
+    if cu_new is not None:
+        _need("cu_new", cu_new, i32, dev, (B + 1,))
+    _need("kv_len", kv_len, i32, dev, (B,))
+    _need("page_table", page_table, i32, dev, (B, max_pages))
+    max_pos = half = 0
+    if rope is not None:
+        max_pos, half, _ = rope.shape
+        _need("rope", rope, torch.float32, dev, (max_pos, half, 2))
+    dt = _dtype_code(k_new)
+    ws = _full_ws(ws, k_new, MSA_OP_PAGED_APPEND_FP8, B, T, 0, Hkv, Hq, d, dt)
+    code = load_library().msa_paged_append_fp8(_addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(rope),
+                                               _addr(cu_new), kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, Hkv,
+                                               d, 2 * half, interleaved, max_pos, num_pages, page_size, max_pages, dt,
+                                               _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                                               k_scale.data_ptr(), v_scale.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                               _raw_stream(dev))
+    _check(code, "msa_paged_append_fp8")
+    return q_out
+
+
+def msa_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, page_table, cu, kv_len, rows, dtype=None, k_out=None,
+                       v_out=None, ws=None, stream=None):
+    """The last cached keys and values of each sequence as ``rows`` packed rows
+    (see include/msa.h): cu [B+1] or None (one row per sequence). Returns
+    (k, v) [rows, Hkv, d] of ``dtype`` (bfloat16 by default)."""
+    torch = _torch()
+    _rows("k_cache", k_cache, 4)
+    dev, i32 = k_cache.get_device(), torch.int32
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, page_table, cu, kv_len, rows, dtype, k_out,
+                                      v_out, ws)
+    num_pages, page_size, Hkv, d = _need_fp8(k_cache, v_cache, k_scale, v_scale, dev)
+    B, max_pages = page_table.shape
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    if k_out is None:
+        k_out = torch.empty((rows, Hkv, d), dtype=dtype, device=k_cache.device)
+    else:
+        _need("k_out", k_out, dtype, dev, (rows, Hkv, d))
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    else:
+        _need("v_out", v_out, dtype, dev, (rows, Hkv, d))
+    if cu is not None:
+        _need("cu", cu, i32, dev, (B + 1,))
+    _need("kv_len", kv_len, i32, dev, (B,))
+    _need("page_table", page_table, i32, dev, (B, max_pages))
+    dt = _dtype_code(k_out)
+    ws = _full_ws(ws, k_out, MSA_OP_PAGED_READ_FP8, B, rows, 0, Hkv, Hkv, d, dt)
+    code = load_library().msa_paged_read_fp8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                             v_scale.data_ptr(), _addr(cu), kv_len.data_ptr(), page_table.data_ptr(),
+                                             B, rows, Hkv, d, num_pages, page_size, max_pages, dt, k_out.data_ptr(),
+                                             v_out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev))
+    _check(code, "msa_paged_read_fp8")
+    return k_out, v_out
+
+
+def msa_full_attn_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, scale=0.0, out=None, lse=None,
+                             ws=None, stream=None):
+    """msa_full_attn_decode over a cache in 8 bits (see include/msa.h)."""
+    torch = _torch()
+    shape = _rows("q", q)
+    B, Hq, d = shape
+    dev, dtype = q.get_device(), q.dtype
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, scale, out, lse,
+                                            ws)
+    num_pages, page_size, Hkv, cached = _need_fp8(k_cache, v_cache, k_scale, v_scale, dev)
+    if cached != d:
+        raise ValueError(f"k_cache holds heads of {cached}, q of {d}")
+    max_pages = page_table.shape[1]
+    _need("kv_len", kv_len, torch.int32, dev, (B,))
+    _need("page_table", page_table, torch.int32, dev, (B, max_pages))
+    if lse is not None:
+        _need("lse", lse, torch.float32, dev, (B, Hq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, dtype, dev, shape)
+    dt = _dtype_code(q)
+    ws = _full_ws(ws, q, MSA_OP_FULL_DECODE_FP8, B, 1, max_pages * page_size, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                   k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+                                                   kv_len.data_ptr(), B, Hq, Hkv, d, num_pages, page_size, max_pages,
+                                                   scale, dt, out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes,
+                                                   _raw_stream(dev))
+    _check(code, "msa_full_attn_decode_fp8")
     return out
 
 

@@ -51,35 +51,23 @@ cudaError_t prefill(const FullArgs& a, cudaStream_t stream) {
 
 inline float scale_or_default(float scale, int d) { return scale > 0.f ? scale : 1.0f / sqrtf(float(d)); }
 
-}  // namespace
-
-size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
-  if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
-  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
-  if (Nq < 0 || !rows_ok(Nq, Hq) || (op == MSA_OP_FULL_BACKWARD && !rows_ok(Nk, Hkv))) return 0;
-  if (op == MSA_OP_FULL_PREFILL && dtype == MSA_BF16) return kWsHeader + full_prefill_ws_bytes(d, Nk);
-  if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
-  return kWsHeader;
-}
-
-}  // namespace msa
-
-using namespace msa;
-
-extern "C" msa_status_t msa_paged_append(const void* q, const void* k_new, const void* v_new, const float* rope,
-                                         const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table,
-                                         int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, int max_pos,
-                                         int num_pages, int page_size, int max_pages, int dtype, void* q_out,
-                                         void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
-                                         cudaStream_t stream) {
-  AppendArgs a{};
+// An append's checks and arguments, for caches of any element type.
+msa_status_t check_append(AppendArgs& a, bool& empty, const void* q, const void* k_new, const void* v_new,
+                          const float* rope, const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table,
+                          int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, int max_pos, int num_pages,
+                          int page_size, int max_pages, int dtype, void* q_out, void* k_cache, void* v_cache, void* ws,
+                          size_t ws_bytes) {
+  empty = false;
   msa_status_t st = check_heads(Hq, Hkv, d, dtype);
   if (st == MSA_OK) st = check_pages(num_pages, page_size, max_pages, &a.pages);
   if (st != MSA_OK) return st;
   if (B < 0 || T < 0 || rot < 0 || rot > d || (interleaved != 0 && interleaved != 1)) return MSA_ERR_INVALID_ARG;
   if (rot % 16 != 0) return MSA_ERR_UNSUPPORTED;
   if (!rows_ok(T, Hq)) return MSA_ERR_UNSUPPORTED;
-  if (B == 0 || T == 0) return MSA_OK;
+  if (B == 0 || T == 0) {
+    empty = true;
+    return MSA_OK;
+  }
   if (!cu_new && T != B) return MSA_ERR_INVALID_ARG;
   if (!k_new || !v_new || !kv_len || !page_table || !k_cache || !v_cache || (!q) != (!q_out)) return MSA_ERR_INVALID_ARG;
   if (rot > 0 && (!rope || max_pos < 1)) return MSA_ERR_INVALID_ARG;
@@ -108,25 +96,25 @@ extern "C" msa_status_t msa_paged_append(const void* q, const void* k_new, const
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.ws = static_cast<WsHeader*>(ws);
-  return launched(launch_paged_append(a, stream));
+  return MSA_OK;
 }
 
-extern "C" msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void* v_cache,
-                                             const int32_t* page_table, const int32_t* kv_len, int B, int Hq, int Hkv,
-                                             int d, int num_pages, int page_size, int max_pages, float scale,
-                                             int dtype, void* out, float* lse, void* ws, size_t ws_bytes,
-                                             cudaStream_t stream) {
-  FullArgs a{};
+// A decode's checks and arguments, but for its workspace.
+msa_status_t check_decode(FullArgs& a, bool& empty, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* page_table, const int32_t* kv_len, int B, int Hq, int Hkv, int d, int num_pages,
+                          int page_size, int max_pages, float scale, int dtype, void* out, float* lse) {
+  empty = false;
   msa_status_t st = check_heads(Hq, Hkv, d, dtype);
   if (st == MSA_OK) st = check_pages(num_pages, page_size, max_pages, &a.pages);
   if (st != MSA_OK) return st;
   if (B < 0) return MSA_ERR_INVALID_ARG;
   if (!rows_ok(B, Hq)) return MSA_ERR_UNSUPPORTED;
-  if (B == 0) return MSA_OK;
+  if (B == 0) {
+    empty = true;
+    return MSA_OK;
+  }
   if (!q || !k_cache || !v_cache || !page_table || !kv_len || !out) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
-  st = check_full_ws(ws, ws_bytes, full_ws_bytes(MSA_OP_FULL_DECODE, B, 1, max_pages * page_size, Hkv, Hq, d, dtype));
-  if (st != MSA_OK) return st;
   a.q = q;
   a.k = k_cache;
   a.v = v_cache;
@@ -139,8 +127,120 @@ extern "C" msa_status_t msa_full_attn_decode(const void* q, const void* k_cache,
   a.scale = scale_or_default(scale, d);
   a.out = out;
   a.lse = lse;
+  return MSA_OK;
+}
+
+}  // namespace
+
+size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
+  if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
+  if (op == MSA_OP_FULL_DECODE || op == MSA_OP_FULL_DECODE_FP8) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
+  if (Nq < 0 || !rows_ok(Nq, Hq) || (op == MSA_OP_FULL_BACKWARD && !rows_ok(Nk, Hkv))) return 0;
+  if (op == MSA_OP_FULL_PREFILL && dtype == MSA_BF16) return kWsHeader + full_prefill_ws_bytes(d, Nk);
+  if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
+  return kWsHeader;
+}
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status_t msa_paged_append(const void* q, const void* k_new, const void* v_new, const float* rope,
+                                         const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table,
+                                         int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, int max_pos,
+                                         int num_pages, int page_size, int max_pages, int dtype, void* q_out,
+                                         void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                                         cudaStream_t stream) {
+  AppendArgs a{};
+  bool empty;
+  const msa_status_t st = check_append(a, empty, q, k_new, v_new, rope, cu_new, kv_len, page_table, B, T, Hq, Hkv, d, rot,
+                                       interleaved, max_pos, num_pages, page_size, max_pages, dtype, q_out, k_cache,
+                                       v_cache, ws, ws_bytes);
+  return st != MSA_OK || empty ? st : launched(launch_paged_append(a, stream));
+}
+
+extern "C" msa_status_t msa_paged_append_fp8(const void* q, const void* k_new, const void* v_new, const float* rope,
+                                             const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table,
+                                             int B, int T, int Hq, int Hkv, int d, int rot, int interleaved,
+                                             int max_pos, int num_pages, int page_size, int max_pages, int dtype,
+                                             void* q_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                             void* ws, size_t ws_bytes, cudaStream_t stream) {
+  AppendArgs a{};
+  bool empty;
+  const msa_status_t st = check_append(a, empty, q, k_new, v_new, rope, cu_new, kv_len, page_table, B, T, Hq, Hkv, d, rot,
+                                       interleaved, max_pos, num_pages, page_size, max_pages, dtype, q_out, k_cache,
+                                       v_cache, ws, ws_bytes);
+  if (st != MSA_OK || empty) return st;
+  if (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)) return MSA_ERR_INVALID_ARG;
+  return launched(launch_paged_append_fp8(a, k_scale, v_scale, stream));
+}
+
+extern "C" msa_status_t msa_paged_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale,
+                                           const float* v_scale, const int32_t* cu, const int32_t* kv_len,
+                                           const int32_t* page_table, int B, int T, int Hkv, int d, int num_pages,
+                                           int page_size, int max_pages, int dtype, void* k_out, void* v_out, void* ws,
+                                           size_t ws_bytes, cudaStream_t stream) {
+  ReadArgs a{};
+  msa_status_t st = check_heads(Hkv, Hkv, d, dtype);
+  if (st == MSA_OK) st = check_pages(num_pages, page_size, max_pages, &a.pages);
+  if (st != MSA_OK) return st;
+  if (B < 0 || T < 0) return MSA_ERR_INVALID_ARG;
+  if (!rows_ok(T, Hkv)) return MSA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return MSA_OK;
+  if (!cu && T != B) return MSA_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !kv_len || !page_table || !k_out || !v_out) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(k_out) ||
+      !aligned16(v_out))
+    return MSA_ERR_INVALID_ARG;
+  st = check_full_ws(ws, ws_bytes, kWsHeader);
+  if (st != MSA_OK) return st;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.cu = cu;
+  a.kv_len = kv_len;
+  a.pages.table = page_table;
+  a.B = B;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.dtype = dtype;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.ws = static_cast<WsHeader*>(ws);
+  return launched(launch_paged_read_fp8(a, stream));
+}
+
+extern "C" msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* page_table, const int32_t* kv_len, int B, int Hq, int Hkv,
+                                             int d, int num_pages, int page_size, int max_pages, float scale,
+                                             int dtype, void* out, float* lse, void* ws, size_t ws_bytes,
+                                             cudaStream_t stream) {
+  FullArgs a{};
+  bool empty;
+  const msa_status_t st = check_decode(a, empty, q, k_cache, v_cache, page_table, kv_len, B, Hq, Hkv, d, num_pages,
+                                       page_size, max_pages, scale, dtype, out, lse);
+  if (st != MSA_OK || empty) return st;
+  const msa_status_t w = check_full_ws(ws, ws_bytes, kWsHeader + full_decode_ws_bytes(d));
   a.ws = ws;
-  return launched(launch_full_decode(a, stream));
+  return w != MSA_OK ? w : launched(launch_full_decode(a, stream));
+}
+
+extern "C" msa_status_t msa_full_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                                 const float* k_scale, const float* v_scale, const int32_t* page_table,
+                                                 const int32_t* kv_len, int B, int Hq, int Hkv, int d, int num_pages,
+                                                 int page_size, int max_pages, float scale, int dtype, void* out,
+                                                 float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  FullArgs a{};
+  bool empty;
+  const msa_status_t st = check_decode(a, empty, q, k_cache, v_cache, page_table, kv_len, B, Hq, Hkv, d, num_pages,
+                                       page_size, max_pages, scale, dtype, out, lse);
+  if (st != MSA_OK || empty) return st;
+  if (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)) return MSA_ERR_INVALID_ARG;
+  const msa_status_t w = check_full_ws(ws, ws_bytes, kWsHeader + full_decode_ws_bytes(d));
+  a.ws = ws;
+  return w != MSA_OK ? w : launched(launch_full_decode_fp8(a, k_scale, v_scale, stream));
 }
 
 extern "C" msa_status_t msa_full_attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,

@@ -1,0 +1,596 @@
+// Decode kernels of full attention: the walk over the keys of a batch, the ring
+// of copies, the joins. What a warp does with 16 keys (element types, products)
+// is its core, which the including file defines; SHARED leaves the keys that a
+// group of sequences has in common to another grid and joins its results in.
+//
+// Work: the keys of every (sequence, key/value head, group of up to 16 query
+// heads) -- an item -- are cut into units of 128 (16 per warp; 64 for fp32 of d
+// 128, which has four warps), the units of all items are numbered through, and
+// each CTA of a fixed grid (one per SM) takes an equal run of them, so ragged
+// lengths balance whatever they are, without the host knowing them.
+// In a unit each warp takes 16 keys, which lie in one page, and works alone:
+// its own ring of cp.async copies (keys past the end arrive as zeros), scores,
+// running maximum and sum, products. Warps meet only where an item ends in the
+// CTA: their states are joined in shared memory. An item that lies in several
+// CTAs leaves a partial (maximum, sum, unnormalised output) per CTA, and the
+// CTA that arrives last joins them in the order of the keys.
+// Many short items: their ends would cost more than their keys (a join takes as
+// long as a unit), so single warps take whole items instead, with nothing to join.
+#pragma once
+
+#include "full_shared.cuh"
+#include "tc_utils.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kSub = 16, kSubLog2 = 4;    // keys of a warp's step: never across a page
+constexpr int kFdMaxHeads = 16;           // query heads of an item
+constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
+// The maximum only moves when a step exceeds it by 2^8: weights stay below
+// 2^8 and their common factor drops out in the division by their sum.
+constexpr float kFdLazy = 8.f;
+
+__device__ __forceinline__ float ex2d(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8x8 b16 matrix across the warp, transposed
+__device__ __forceinline__ uint32_t trans8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float qmax(float x) {  // over the 8 lanes that share lane & 3
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float qsum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Address of 16-byte chunk c of row r in a [rows][row_bytes] tile whose chunks
+// are exchanged within 128 bytes by the row's low bits (conflict-free ldmatrix
+// and vector reads down a column).
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row_bytes, int r, int c) {
+  return base + uint32_t(r * row_bytes) + (uint32_t(c ^ (r & 7)) << 4);
+}
+
+struct FdParams {
+  const void *q, *k, *v;
+  const float *k_scale, *v_scale;  // caches in 8 bits
+  const int32_t* kv_len;
+  PageMap pages;
+  int B, Hq, Hkv, hpg, ngr, cap;  // ngr: head groups (items) per key/value head; cap: most keys
+  float scale_log2;
+  float* part_o;   // [slots][16][D], 2 slots per CTA (SHARED: one per warp)
+  float* part_ml;  // [slots][16][2]: maximum (log2 units), sum; a negative sum marks a page out of range
+  uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
+  void* out;
+  float* lse;
+  uint32_t* status;
+  SharedParams shared;  // SHARED only
+};
+
+// The keys of sequence b that its items walk: [from, L). SHARED: from is where its
+// group's prefix ends, and x the group (-1: none).
+struct Own {
+  int from, L, x;
+  bool ok;
+  __device__ __forceinline__ int units(int unit_log2) const { return ok && L > from ? ((L - from - 1) >> unit_log2) + 1 : 0; }
+};
+template <bool SHARED>
+__device__ __forceinline__ Own own_of(const FdParams& p, int b) {
+  Own o{0, p.kv_len[b], -1, true};
+  o.ok = o.L >= 0 && o.L <= p.cap;
+  if constexpr (SHARED) {
+    if (o.L != 0) {  // 0: a padded entry, in a group or not
+      o.x = p.shared.group_of(b);
+      if (o.x >= 0) o.from = p.shared.prefix_len[o.x];
+      o.ok = o.ok && o.from >= 0 && o.from <= o.L && (o.from & ((1 << p.pages.page_log2) - 1)) == 0;
+    }
+  }
+  return o;
+}
+template <bool SHARED>
+__device__ __forceinline__ int units_of(const FdParams& p, int b, int unit_log2) {
+  return own_of<SHARED>(p, b).units(unit_log2);
+}
+
+// Joins an item's `parts`, in order, into the rows of its heads: out = sum / den,
+// lse. Whole threads [0, threads); a negative sum marks rows without a result.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void join_parts(const FdParams& p, int b, int h0, int heads, int thread, int threads, int parts,
+                                           F part_of) {
+  constexpr int kBatch = 8;  // parts in flight: the loads of a batch do not wait for each other
+  T* out = static_cast<T*>(p.out);
+  for (int o = thread * 4; o < heads * D; o += threads * 4) {
+    const int h = o / D;
+    float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+    bool spoilt = false;
+    for (int y0 = 0; y0 < parts; y0 += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const PartAt s = part_of(min(y0 + x, parts - 1));
+        ml[x] = __ldcg(reinterpret_cast<const float2*>(s.ml) + h);
+        v[x] = __ldcg(reinterpret_cast<const float4*>(s.o + o));
+      }
+      float mn = M;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        spoilt |= ml[x].y < 0.f;
+        mn = fmaxf(mn, ml[x].x);
+      }
+      const float a = M == mn ? 1.f : ex2d(M - mn);
+      M = mn;
+      den *= a;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) sum[y] *= a;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float w = y0 + x >= parts ? 0.f : ml[x].x == M ? 1.f : ex2d(ml[x].x - M);
+        den = fmaf(w, ml[x].y, den);
+        sum[0] = fmaf(w, v[x].x, sum[0]);
+        sum[1] = fmaf(w, v[x].y, sum[1]);
+        sum[2] = fmaf(w, v[x].z, sum[2]);
+        sum[3] = fmaf(w, v[x].w, sum[3]);
+      }
+    }
+    const float inv = 1.f / den;
+    T* dst = out + (int64_t(b) * p.Hq + h0 + h) * D + o % D;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt ? 0.f : sum[y] * inv);
+    if (p.lse && o % D == 0) p.lse[int64_t(b) * p.Hq + h0 + h] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
+  }
+}
+// A sequence that sees no key (whole CTA).
+template <typename T, int D>
+__device__ __forceinline__ void empty_row(const FdParams& p, int b) {
+  T* out = static_cast<T*>(p.out);
+  for (int x = threadIdx.x; x < p.Hq * D; x += blockDim.x) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
+  if (p.lse)
+    for (int x = threadIdx.x; x < p.Hq; x += blockDim.x) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
+}
+
+// A walk over units in order: those of a CTA's run, or (SOLO) of every hop-th item.
+template <bool SHARED>
+struct Walk {
+  int b, it, u, n;  // sequence, item within it, unit within the item, units of the item
+  Own own;          // the sequence's keys; SHARED only (else they are read again: registers are dearer)
+  __device__ __forceinline__ int len(const FdParams& p) const { return SHARED ? own.L : p.kv_len[b]; }
+  __device__ __forceinline__ int from() const { return SHARED ? own.from : 0; }
+  __device__ __forceinline__ int arrive(const FdParams& p, int unit_log2) {  // at sequence b: its units
+    if constexpr (!SHARED) return units_of<false>(p, b, unit_log2);
+    own = own_of<true>(p, b);
+    return own.units(unit_log2);
+  }
+  template <bool SOLO>
+  __device__ __forceinline__ void next(const FdParams& p, int hop, int unit_log2) {
+    if (++u < n) return;
+    u = 0;
+    if constexpr (SOLO) return seek(p, hop, hop);
+    if (++it < p.Hkv * p.ngr) return;
+    it = 0;
+    do {
+      n = ++b < p.B ? arrive(p, unit_log2) : 1;  // past the last sequence the walk is over
+    } while (n == 0);
+  }
+  // To the first item with keys among those `by`, `by` + hop, ... further on.
+  __device__ __forceinline__ void seek(const FdParams& p, int by, int hop) {
+    const int items = p.Hkv * p.ngr;
+    do {
+      it += by;
+      b += it / items;
+      it %= items;
+      by = hop;
+      n = b < p.B ? arrive(p, kSubLog2) : 1;
+    } while (n == 0);
+  }
+};
+
+// One CTA per SM: the copies in flight are what covers HBM's latency.
+template <typename C>
+struct FdShape {
+  static constexpr int kWarps = C::kWarps, kThreads = kWarps * 32;
+  static constexpr int kUnit = kWarps * kSub;  // keys of a unit
+  static constexpr int kStages = C::kStages;
+  static constexpr int kRing = kStages * C::kStage;      // per warp
+  static constexpr int kState = (C::kAcc + 2 * C::kM + 1) * 32;  // floats of a warp's state
+  static constexpr int kJoin = (kWarps - 1) * kState * 4;        // a slot per hand-over
+  static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
+};
+
+// SOLO: whole items for single warps; else the CTA's run of the `total` units.
+template <typename C, bool SOLO, bool SHARED>
+__device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
+  using SH = FdShape<C>;
+  using T = typename C::T;
+  constexpr int D = C::kD;
+  constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads, kUnit = SH::kUnit;
+  extern __shared__ __align__(128) uint8_t fd_smem[];
+  __shared__ int last_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = tc::smem_u32(fd_smem) + warp * SH::kRing;
+  const uint32_t extra = tc::smem_u32(fd_smem) + kFdWarps * SH::kRing + warp * C::kExtra;
+  float* join = reinterpret_cast<float*>(fd_smem + kFdWarps * (SH::kRing + C::kExtra));
+  const int items = p.Hkv * p.ngr;
+  T* out = static_cast<T*>(p.out);
+
+  constexpr int kUnitLog2 = kUnit == 64 ? 6 : 7;
+  static_assert(1 << kUnitLog2 == kUnit, "keys of a unit");
+  constexpr int ulog = SOLO ? kSubLog2 : kUnitLog2;
+  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = SOLO ? 0 : warp * kSub;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t run0 = SOLO ? 0 : blockIdx.x * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);
+  if (run0 >= run1) return;
+  Walk<SHARED> at{};
+  int64_t first = 0;  // number of the walk's sequence's first unit
+  int64_t item_first = 0;  // number of the item's first unit
+  if constexpr (SOLO) {
+    at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop);
+  } else {
+    int ahead = lane < p.B ? units_of<SHARED>(p, lane, kUnitLog2) : 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int mine = ahead;
+      ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, kUnitLog2) : 0;  // in flight during the scan
+      int64_t incl = int64_t(mine) * items;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        at.b = b0 + src;
+        at.n = __shfl_sync(0xffffffffu, mine, src);
+        first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if constexpr (SHARED) at.own = own_of<true>(p, at.b);
+    at.it = int((run0 - first) / at.n);
+    at.u = int((run0 - first) % at.n);
+    item_first = first + int64_t(at.it) * at.n;
+  }
+
+  // ---- copies: the walk `ld` runs ahead of `at` ----
+  Walk<SHARED> ld = at;
+  int64_t ld_left = !SOLO || ld.b < p.B ? run1 - run0 : 0;
+  uint32_t bad_ring = 0;  // stage x's page was out of range
+  auto page_of = [&](const Walk<SHARED>& w) {
+    const int key = w.from() + (w.u << ulog) + sub0;
+    return key < w.len(p) ? p.pages.table[int64_t(w.b) * p.pages.max_pages + (key >> p.pages.page_log2)] : 0;
+  };
+  int page = ld_left > 0 ? page_of(ld) : 0;
+  auto issue = [&](int st) {
+    if (ld_left > 0) {
+      const int key = ld.from() + (ld.u << ulog) + sub0;
+      const int valid = ld.len(p) - key;
+      const bool bad = valid > 0 && (page < 0 || page >= p.pages.num_pages);
+      bad_ring = bad ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
+      C::copy(p, ring + st * C::kStage, bad || valid <= 0 ? 0 : page, key & ((1 << p.pages.page_log2) - 1), ld.it / p.ngr,
+              bad ? 0 : valid);
+      if (--ld_left > 0) {
+        ld.template next<SOLO>(p, hop, ulog);
+        if (!SOLO || ld.b < p.B)
+          page = page_of(ld);
+        else
+          ld_left = 0;
+      }
+    }
+    cp_commit_group();
+  };
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(st);
+
+  C c;
+  bool fresh = true, bad = false;
+  int st = 0;
+  for (int64_t z = run0; z < run1 && (!SOLO || at.b < p.B); ++z) {
+    const int g = at.it / p.ngr, h0 = g * p.hpg + (at.it % p.ngr) * kFdMaxHeads;
+    const int heads = min(p.hpg - (at.it % p.ngr) * kFdMaxHeads, kFdMaxHeads);
+    const int L = at.len(p);
+    if (fresh) {
+      c.start(p, static_cast<const T*>(p.q) + (int64_t(at.b) * p.Hq + h0) * D, heads, extra);
+      fresh = bad = false;
+    }
+    issue((st + NS - 1) % NS);
+    cp_wait<NS - 1>();
+    __syncwarp();
+    bad |= (bad_ring >> st) & 1u;
+    const int valid = L - (at.from() + (at.u << ulog) + sub0);
+    if (valid > 0) c.step(ring + st * C::kStage, extra, valid, p.scale_log2);
+    __syncwarp();
+    st = (st + 1) % NS;
+    const int b = at.b, n = at.n;
+    const bool ends = at.u + 1 == at.n;
+    if (!ends && z + 1 < run1) {
+      ++at.u;
+      continue;
+    }
+    // ---- the item ends here: join the warps' states, halving their number ----
+    fresh = true;
+    c.finish();
+    const Own own = at.own;
+    constexpr int kRegs = C::kAcc + 2 * C::kM + 1;
+    auto put = [&](float* to) {
+#pragma unroll
+      for (int x = 0; x < C::kAcc; ++x) to[x * 32 + lane] = c.acc[x];
+#pragma unroll
+      for (int x = 0; x < C::kM; ++x) {
+        to[(C::kAcc + x) * 32 + lane] = c.m[x];
+        to[(C::kAcc + C::kM + x) * 32 + lane] = c.l[x];
+      }
+      to[(kRegs - 1) * 32 + lane] = bad ? 1.f : 0.f;
+    };
+    auto take = [&](const float* from) {
+      float wa[C::kM], wb[C::kM];
+#pragma unroll
+      for (int x = 0; x < C::kM; ++x) {
+        const float mo = from[(C::kAcc + x) * 32 + lane], mn = fmaxf(c.m[x], mo);
+        wa[x] = c.m[x] == mn ? 1.f : ex2d(c.m[x] - mn);
+        wb[x] = mo == mn ? 1.f : ex2d(mo - mn);
+        c.m[x] = mn;
+        c.l[x] = c.l[x] * wa[x] + from[(C::kAcc + C::kM + x) * 32 + lane] * wb[x];
+      }
+#pragma unroll
+      for (int x = 0; x < C::kAcc; ++x)
+        c.acc[x] = c.acc[x] * wa[C::m_index(x)] + from[x * 32 + lane] * wb[C::m_index(x)];
+      bad |= from[(kRegs - 1) * 32 + lane] != 0.f;
+    };
+    // Every hand-over has a slot of its own: the upper warps may be at the next
+    // item's end while the lower ones still read this one's.
+    if constexpr (!SOLO) {
+#pragma unroll
+      for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
+        if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
+        __syncthreads();
+        if (warp < half) take(join + (slot0 + warp) * SH::kState);
+      }
+    }
+    const bool whole = SOLO || (item_first >= run0 && ends);
+    const int slot = SHARED && SOLO ? int(blockIdx.x) * kFdWarps + warp : 2 * int(blockIdx.x) + (item_first >= run0 ? 1 : 0);
+    if (SOLO || warp == 0) {
+      c.sum_l();
+      if (__any_sync(0xffffffffu, bad)) {
+        bad = true;
+        if (lane == 0) set_status(p.status, MSA_ERR_BOUNDS);
+      }
+      if (whole && !SHARED) {
+        float inv[C::kM];
+#pragma unroll
+        for (int x = 0; x < C::kM; ++x) inv[x] = bad ? 0.f : 1.f / c.l[x];
+        c.each([&](int h, int x, int dim, float val) {
+          if (h < heads)
+            out[(int64_t(b) * p.Hq + h0 + h) * D + dim] = from_f<T>(bad ? 0.f : val * inv[x]);
+        });
+        if (p.lse)
+          c.each_head([&](int h, int x) {
+            if (h < heads) p.lse[int64_t(b) * p.Hq + h0 + h] = bad ? -INFINITY : (c.m[x] + log2f(c.l[x])) * kFdLn2;
+          });
+      } else {
+        float* po = p.part_o + int64_t(slot) * kFdMaxHeads * D;
+        float* pm = p.part_ml + int64_t(slot) * kFdMaxHeads * 2;
+        c.each([&](int h, int, int dim, float val) {
+          if (h < heads) po[h * D + dim] = val;
+        });
+        c.each_head([&](int h, int x) {
+          if (h < heads) {
+            pm[2 * h] = c.m[x];
+            pm[2 * h + 1] = bad ? -1.f : c.l[x];
+          }
+        });
+      }
+    }
+    if constexpr (SHARED && SOLO) {
+      __syncwarp();
+      const PartAt own_part{p.part_o + int64_t(slot) * kFdMaxHeads * D, p.part_ml + int64_t(slot) * kFdMaxHeads * 2};
+      tc::griddep_wait();
+      const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, h0 - g * p.hpg);
+      join_parts<T, D>(p, b, h0, heads, lane, 32, 1 + pre.n,
+                       [&](int y) { return y == 0 ? own_part : pre.part(y - 1); });
+      __syncwarp();  // the parts are read before the next item's go over them
+    } else if (SHARED || !whole) {
+      // the item's units lie in CTAs c0..c1: the last to arrive joins them
+      const int c0 = whole ? int(blockIdx.x) : int(item_first / per);
+      const int c1 = whole ? c0 : int((item_first + n - 1) / per);
+      if (!whole && warp == 0) {
+        __syncwarp();
+        if (lane == 0) {
+          // releases the warp's stores (ordered by __syncwarp), acquires the others'
+          const int sh = 8 * (c0 & 3);
+          uint32_t old;
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+                       : "=r"(old)
+                       : "l"(p.arrivals + (c0 >> 2)), "r"(1u << sh)
+                       : "memory");
+          last_s = int((old >> sh) & 0xffu) == c1 - c0;
+          if (last_s) atomicSub(p.arrivals + (c0 >> 2), uint32_t(c1 - c0 + 1) << sh);  // ready for the next call
+        }
+      }
+      __syncthreads();
+      if (whole || last_s) {
+        auto part_of = [&](int y) {
+          const int cta = c0 + y, s = 2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0);
+          return PartAt{p.part_o + int64_t(s) * kFdMaxHeads * D, p.part_ml + int64_t(s) * kFdMaxHeads * 2};
+        };
+        if constexpr (SHARED) {
+          tc::griddep_wait();
+          const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, h0 - g * p.hpg);
+          const int parts = c1 - c0 + 1;
+          join_parts<T, D>(p, b, h0, heads, threadIdx.x, kFdThreads, parts + pre.n,
+                           [&](int y) { return y < parts ? part_of(y) : pre.part(y - parts); });
+        } else {
+          join_parts<T, D>(p, b, h0, heads, threadIdx.x, kFdThreads, c1 - c0 + 1, part_of);
+        }
+      }
+      __syncthreads();  // last_s and the parts are read before the next item sets them
+    }
+    if (ends) item_first += n;
+    const int was = at.b;
+    at.template next<SOLO>(p, hop, ulog);
+    if (at.b != was) item_first = z + 1;
+  }
+  cp_wait<0>();
+}
+
+template <typename C, bool SHARED>
+__global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(const FdParams p) {
+  using SH = FdShape<C>;
+  using T = typename C::T;
+  constexpr int D = C::kD;
+  constexpr int kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
+  const int lane = threadIdx.x & 31, items = p.Hkv * p.ngr;
+  if constexpr (SHARED) {
+    if (!cta_in_order(p.shared.groups, p.shared.disorder)) {  // whose keys these are is not known
+      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
+      for (int b = blockIdx.x; b < p.B; b += gridDim.x) empty_row<T, D>(p, b);
+      return;
+    }
+  }
+
+  // ---- all units (every warp counts alone) ----
+  int64_t total = 0;
+  int longest = 0;  // in warps' steps
+#pragma unroll 8
+  for (int b = lane; b < p.B; b += 32) {
+    const int steps = units_of<SHARED>(p, b, kSubLog2);
+    total += (steps + kFdWarps - 1) / kFdWarps;
+    longest = max(longest, steps);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  total *= items;
+  // Whole items for single warps, or shared-out units? A unit and a warp's step
+  // both take about 1.1 us, and so does an item's end or start; single warps
+  // come out ahead from 1.25 times the other count on. Measured both ways (Hq 32,
+  // Hkv 8, d 128, bf16; lengths within a factor of 2):
+  //   1280 items up to 64 keys   19 (single) : 29 us     2560 up to 256   65 :  70 us
+  //   10240 items up to 128      99 : 177 us             2560 up to 512  119 : 109 us
+  //   640 items up to 128        18 :  20 us              320 up to 128   17 :  16 us
+  const int warps = int(gridDim.x) * kFdWarps;
+  const int64_t all = int64_t(p.B) * items, rounds = (all + warps - 1) / warps;
+  const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
+  // sequences without keys (SHARED: of their own): nobody's run holds them
+  auto rest = [&]() {
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      const Own o = own_of<SHARED>(p, b);
+      if (o.units(kSubLog2) > 0) continue;
+      if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
+      if constexpr (SHARED) {
+        if (o.ok && o.L > 0) {  // the prefix is all that it sees
+          tc::griddep_wait();
+          for (int it = 0; it < items; ++it) {
+            const int g = it / p.ngr, h = (it % p.ngr) * kFdMaxHeads;
+            const PrefixRows<D> pre = p.shared.rows<D>(o.x, b, g, h);
+            join_parts<T, D>(p, b, g * p.hpg + h, min(p.hpg - h, kFdMaxHeads), threadIdx.x, kFdThreads, pre.n,
+                             [&](int y) { return pre.part(y); });
+          }
+          continue;
+        }
+      }
+      empty_row<T, D>(p, b);
+    }
+  };
+  if constexpr (!SHARED) rest();
+  if (solo)
+    decode_run<C, true, SHARED>(p, total);
+  else
+    decode_run<C, false, SHARED>(p, total);
+  if constexpr (SHARED) rest();  // behind the rest: it waits for the prefixes' grid
+}
+
+int fd_grid() { return kNumSMs; }
+
+// `early`: the grid may start while the one before it ends (SHARED, which waits itself)
+template <typename C, bool SHARED>
+cudaError_t decode(const FdParams& p, const char* name, cudaStream_t stream) {
+  auto kern = full_decode_kernel<C, SHARED>;
+  constexpr int bytes = FdShape<C>::kBytes;
+  static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
+  static KernelReady ready;
+  if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes)) return e;
+  ProfScope pf(name, stream);
+  if constexpr (!SHARED) {
+    kern<<<fd_grid(), FdShape<C>::kThreads, bytes, stream>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(fd_grid());
+  cfg.blockDim = dim3(FdShape<C>::kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+int head_groups(int hpg) { return (hpg + kFdMaxHeads - 1) / kFdMaxHeads; }
+// partials of `slots` slots
+size_t fd_part_bytes(int slots, int d) { return up256(size_t(slots) * kFdMaxHeads * d * 4) + up256(size_t(slots) * kFdMaxHeads * 8); }
+FdParams fd_params(const FullArgs& a, int slots) {
+  FdParams p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.kv_len = a.seq.kv_len;
+  p.pages = a.pages;
+  p.B = a.seq.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.hpg = a.Hq / a.Hkv;
+  p.ngr = head_groups(p.hpg);
+  p.cap = a.seq.Tk;
+  p.scale_log2 = a.scale * kFdLog2e;
+  char* w = static_cast<char*>(a.ws) + kWsHeader;
+  p.part_o = reinterpret_cast<float*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + up256(size_t(slots) * kFdMaxHeads * a.d * 4));
+  p.arrivals = static_cast<WsHeader*>(a.ws)->arrivals;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.status = &static_cast<WsHeader*>(a.ws)->status;
+  return p;
+}
+
+}  // namespace
+}  // namespace msa

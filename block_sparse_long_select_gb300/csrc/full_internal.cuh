@@ -269,6 +269,8 @@ cudaError_t launch_full_zero(const SeqMap& m, bool keys, int heads, int d, int d
                              void* ws, cudaStream_t stream);
 // decode over pages, any dtype
 cudaError_t launch_full_decode(const FullArgs& a, cudaStream_t stream);
+// the same over e4m3 caches, scales [num_pages, Hkv, page_size]
+cudaError_t launch_full_decode_fp8(const FullArgs& a, const float* k_scale, const float* v_scale, cudaStream_t stream);
 // tcgen05 prefill (bf16); needs Tk > 0
 cudaError_t launch_full_prefill_tc(const FullArgs& a, cudaStream_t stream);
 // tcgen05 backward (bf16); needs Tq, Tk > 0
@@ -283,5 +285,17 @@ struct AppendArgs {
   WsHeader* ws;
 };
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream);
+// caches of e4m3 codes, scales [num_pages, Hkv, page_size]
+cudaError_t launch_paged_append_fp8(const AppendArgs& a, float* k_scale, float* v_scale, cudaStream_t stream);
+struct ReadArgs {
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *cu, *kv_len;
+  PageMap pages;
+  int B, T, Hkv, d, dtype;
+  void *k_out, *v_out;
+  WsHeader* ws;
+};
+cudaError_t launch_paged_read_fp8(const ReadArgs& a, cudaStream_t stream);
 
 }  // namespace msa

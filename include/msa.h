@@ -85,7 +85,10 @@ typedef enum {
   MSA_OP_FULL_PREFILL = 8, /* msa_full_attn_prefill and _paged (6 and 7 name no operation) */
   MSA_OP_FULL_BACKWARD = 9,
   MSA_OP_FULL_DECODE = 10,
-  MSA_OP_PAGED_APPEND = 11
+  MSA_OP_PAGED_APPEND = 11,
+  MSA_OP_PAGED_APPEND_FP8 = 13, /* 12 names no operation */
+  MSA_OP_PAGED_READ_FP8 = 14,
+  MSA_OP_FULL_DECODE_FP8 = 15
 } msa_op_t;
 
 /* Bytes of scratch `ws` the entry point `op` needs for these sizes (the same
@@ -93,9 +96,10 @@ typedef enum {
  * the attention ops, Hq and d for MSA_OP_INDEX_SELECT; for MSA_OP_DECODE and
  * MSA_OP_DECODE_STEP, Nq is ignored and Nk is Lmax; MSA_OP_DECODE_STEP and
  * MSA_OP_KL_AUX use every other argument, with G = Hkv; MSA_OP_BACKWARD uses
- * all but di, with G = Hkv; the MSA_OP_FULL_* operations and
- * MSA_OP_PAGED_APPEND use B, Nq = packed rows Tq (T), Nk = packed keys Tk or
- * max_pages * page_size, G = Hkv, Hq, d and dtype). Returns 0 when the
+ * all but di, with G = Hkv; the MSA_OP_FULL_* and MSA_OP_PAGED_* operations
+ * use B, Nq = packed rows Tq (T), Nk = packed keys Tk or
+ * max_pages * page_size, G = Hkv, Hq (MSA_OP_PAGED_READ_FP8: any multiple of
+ * Hkv), d and dtype). Returns 0 when the
  * arguments are invalid or not supported, and 256 for a valid empty batch. */
 size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int Hq, int d, int di, int Bs, int K, int dtype);
 
@@ -371,6 +375,56 @@ msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void
                                   const int32_t* kv_len, int B, int Hq, int Hkv, int d, int num_pages, int page_size,
                                   int max_pages, float scale, int dtype, void* out, float* lse, void* ws,
                                   size_t ws_bytes, cudaStream_t stream);
+
+/* ---- The same caches in 8 bits ----
+ * k_cache, v_cache [num_pages, page_size, Hkv, d] hold e4m3 codes (one byte: 4
+ * exponent and 3 fraction bits), k_scale, v_scale [num_pages, Hkv, page_size]
+ * fp32 a scale per token and head: a row stands for code * scale. Half the
+ * memory of a bf16 cache, and half of what a decode step reads; the codes round
+ * each value by at most 2^-4 of it. A prompt in chunks is appended, read back
+ * as packed rows and attended with msa_full_attn_prefill.
+ * dtype is that of q, k_new, v_new and of the outputs. */
+
+/* msa_paged_append into such a cache, with these scales and codes for a head's
+ * row y of d values (keys: rotated, in fp32, rounded once):
+ *   scale = the smallest power of two >= 2^-126 with max|y| / scale <= 448
+ *   code  = e4m3(y / scale), to nearest even
+ * so that a code is a single rounding of y. A row of zeros has scale 0. A row
+ * that holds an infinity or NaN has scale NaN: it stands for NaN throughout.
+ *  ws: msa_workspace_size(MSA_OP_PAGED_APPEND_FP8, B, T, 0, Hkv, Hq, d, 0, 0, 0, dtype)
+ * All else as there; the caches and scales are 16-byte aligned. */
+msa_status_t msa_paged_append_fp8(const void* q, const void* k_new, const void* v_new, const float* rope,
+                                  const int32_t* cu_new, const int32_t* kv_len, const int32_t* page_table, int B,
+                                  int T, int Hq, int Hkv, int d, int rot, int interleaved, int max_pos, int num_pages,
+                                  int page_size, int max_pages, int dtype, void* q_out, void* k_cache, void* v_cache,
+                                  float* k_scale, float* v_scale, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Reads cached rows back: row i of sequence b's n = cu[b+1] - cu[b] packed rows
+ * is its key and value at position kv_len[b] - n + i, code * scale rounded to
+ * dtype once. With n = kv_len[b] that is all of them, with msa_paged_append_fp8's
+ * cu_new the tokens that it wrote.
+ *  cu       [B + 1] int32, or NULL for one row per sequence (T == B)
+ *  k_out, v_out [T, Hkv, d] (dtype)
+ *  ws: msa_workspace_size(MSA_OP_PAGED_READ_FP8, B, T, 0, Hkv, Hkv, d, 0, 0, 0, dtype)
+ * Any scales are taken. Hkv up to 65536. A position that is negative or past
+ * the table, or a page out of range, sets MSA_ERR_BOUNDS and gives rows of 0. */
+msa_status_t msa_paged_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                                const int32_t* cu, const int32_t* kv_len, const int32_t* page_table, int B, int T,
+                                int Hkv, int d, int num_pages, int page_size, int max_pages, int dtype, void* k_out,
+                                void* v_out, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* msa_full_attn_decode over such a cache. Scales are finite and not negative
+ * (a row of scale NaN makes the heads that see it NaN); all else as there.
+ *  ws: msa_workspace_size(MSA_OP_FULL_DECODE_FP8, B, 1, max_pages * page_size,
+ *  Hkv, Hq, d, 0, 0, 0, dtype)
+ *  Products are exact, sums in fp32; each key's weight is rounded to 11 bits
+ *  before its product with v for BF16, to 22 for FP32 (queries too).
+ *  Deterministic. */
+msa_status_t msa_full_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                      const float* v_scale, const int32_t* page_table, const int32_t* kv_len, int B,
+                                      int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages, float scale,
+                                      int dtype, void* out, float* lse, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream);
 
 /* Prefill: causal attention of packed query rows over packed keys.
  *  q [Tq, Hq, d]; k, v [Tk, Hkv, d]; cu_q, cu_k [B + 1] int32
