@@ -10,7 +10,7 @@ carry the C names:
     msa_kl_aux_forward, msa_sparse_attn_backward, msa_paged_append,
     msa_full_attn_decode, msa_full_attn_prefill, msa_full_attn_prefill_paged,
     msa_full_attn_backward, msa_paged_append_fp8, msa_paged_read_fp8,
-    msa_full_attn_decode_fp8, msa_read_status, msa_status_string
+    msa_full_attn_decode_fp8, msa_full_attn_decode_shared, msa_read_status, msa_status_string
 
 There is no CPU fallback: if ``libmsa.so`` is missing or was not built for
 this GPU, every call raises.
@@ -26,6 +26,7 @@ from ._lib import (  # noqa: F401
     MSA_OP_FULL_BACKWARD,
     MSA_OP_FULL_DECODE,
     MSA_OP_FULL_DECODE_FP8,
+    MSA_OP_FULL_DECODE_SHARED,
     MSA_OP_FULL_PREFILL,
     MSA_OP_INDEX_SELECT,
     MSA_OP_KL_AUX,
@@ -40,6 +41,7 @@ from ._lib import (  # noqa: F401
     msa_full_attn_backward,
     msa_full_attn_decode,
     msa_full_attn_decode_fp8,
+    msa_full_attn_decode_shared,
     msa_full_attn_prefill,
     msa_full_attn_prefill_paged,
     msa_index_select,

@@ -9,6 +9,7 @@ MSA_BF16, MSA_FP32 = 0, 1
 MSA_OP_INDEX_SELECT, MSA_OP_PREFILL, MSA_OP_DECODE, MSA_OP_DECODE_STEP, MSA_OP_KL_AUX, MSA_OP_BACKWARD = 0, 1, 2, 3, 4, 5
 MSA_OP_FULL_PREFILL, MSA_OP_FULL_BACKWARD, MSA_OP_FULL_DECODE, MSA_OP_PAGED_APPEND = 8, 9, 10, 11
 MSA_OP_PAGED_APPEND_FP8, MSA_OP_PAGED_READ_FP8, MSA_OP_FULL_DECODE_FP8 = 13, 14, 15
+MSA_OP_FULL_DECODE_SHARED = 16
 MSA_FORCE_LOCAL, MSA_FORCE_START = 1, 2
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_WORKSPACE",
                 4: "MSA_ERR_CUDA", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_BOUNDS"}
@@ -26,6 +27,7 @@ SIGNATURES = {
     "msa_sparse_attn_backward": (_i32, [_vp] * 9 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "msa_paged_append": (_i32, [_vp] * 7 + [_i32] * 12 + [_vp] * 4 + [_sz, _vp]),
     "msa_full_attn_decode": (_i32, [_vp] * 5 + [_i32] * 7 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "msa_full_attn_decode_shared": (_i32, [_vp] * 7 + [_i32] * 8 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "msa_paged_append_fp8": (_i32, [_vp] * 7 + [_i32] * 12 + [_vp] * 6 + [_sz, _vp]),
     "msa_paged_read_fp8": (_i32, [_vp] * 7 + [_i32] * 8 + [_vp] * 3 + [_sz, _vp]),
     "msa_full_attn_decode_fp8": (_i32, [_vp] * 7 + [_i32] * 7 + [_f32, _i32, _vp, _vp, _vp, _sz, _vp]),
@@ -456,6 +458,44 @@ def msa_full_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=0.0, out
                                                page_size, max_pages, scale, dt, out.data_ptr(), _addr(lse),
                                                ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     _check(code, "msa_full_attn_decode")
+    return out
+
+
+def msa_full_attn_decode_shared(q, k_cache, v_cache, page_table, kv_len, cu_prefix, prefix_len, scale=0.0, out=None,
+                                lse=None, ws=None, stream=None):
+    """msa_full_attn_decode where group x of sequences, [cu_prefix[x], cu_prefix[x+1]),
+    shares its first prefix_len[x] keys (see include/msa.h): cu_prefix [P+1], prefix_len [P]."""
+    torch = _torch()
+    shape = _rows("q", q)
+    B, Hq, d = shape
+    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
+    other = _elsewhere(stream, dev)
+    if other is not None:
+        with other:
+            return msa_full_attn_decode_shared(q, k_cache, v_cache, page_table, kv_len, cu_prefix, prefix_len, scale,
+                                               out, lse, ws)
+    num_pages, page_size, Hkv, _ = _rows("k_cache", k_cache, 4)
+    max_pages, P = page_table.shape[1], prefix_len.shape[0]
+    _need("k_cache", k_cache, dtype, dev, (num_pages, page_size, Hkv, d))
+    _need("v_cache", v_cache, dtype, dev, k_cache.shape)
+    _need("kv_len", kv_len, i32, dev, (B,))
+    _need("page_table", page_table, i32, dev, (B, max_pages))
+    _need("cu_prefix", cu_prefix, i32, dev, (P + 1,))
+    _need("prefix_len", prefix_len, i32, dev, (P,))
+    if lse is not None:
+        _need("lse", lse, torch.float32, dev, (B, Hq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, dtype, dev, shape)
+    dt = _dtype_code(q)
+    ws = _full_ws(ws, q, MSA_OP_FULL_DECODE_SHARED, B, P, max_pages * page_size, Hkv, Hq, d, dt)
+    code = load_library().msa_full_attn_decode_shared(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                      page_table.data_ptr(), kv_len.data_ptr(), cu_prefix.data_ptr(),
+                                                      prefix_len.data_ptr(), B, P, Hq, Hkv, d, num_pages, page_size,
+                                                      max_pages, scale, dt, out.data_ptr(), _addr(lse), ws.data_ptr(),
+                                                      ws.nbytes, _raw_stream(dev))
+    _check(code, "msa_full_attn_decode_shared")
     return out
 
 

@@ -135,6 +135,10 @@ msa_status_t check_decode(FullArgs& a, bool& empty, const void* q, const void* k
 size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
   if (op == MSA_OP_FULL_DECODE || op == MSA_OP_FULL_DECODE_FP8) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
+  if (op == MSA_OP_FULL_DECODE_SHARED) {
+    if (!rows_ok(B, Hq) || Nq < 0 || Nq > B) return 0;
+    return kWsHeader + (Nq == 0 ? full_decode_ws_bytes(d) : full_shared_ws_bytes(B, Nq, Hkv, Hq / Hkv, d, dtype));
+  }
   if (Nq < 0 || !rows_ok(Nq, Hq) || (op == MSA_OP_FULL_BACKWARD && !rows_ok(Nk, Hkv))) return 0;
   if (op == MSA_OP_FULL_PREFILL && dtype == MSA_BF16) return kWsHeader + full_prefill_ws_bytes(d, Nk);
   if (op == MSA_OP_FULL_BACKWARD) return kWsHeader + full_backward_ws_bytes(Nq, Hq);
@@ -241,6 +245,27 @@ extern "C" msa_status_t msa_full_attn_decode_fp8(const void* q, const void* k_ca
   const msa_status_t w = check_full_ws(ws, ws_bytes, kWsHeader + full_decode_ws_bytes(d));
   a.ws = ws;
   return w != MSA_OK ? w : launched(launch_full_decode_fp8(a, k_scale, v_scale, stream));
+}
+
+extern "C" msa_status_t msa_full_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                                    const int32_t* page_table, const int32_t* kv_len,
+                                                    const int32_t* cu_prefix, const int32_t* prefix_len, int B, int P,
+                                                    int Hq, int Hkv, int d, int num_pages, int page_size,
+                                                    int max_pages, float scale, int dtype, void* out, float* lse,
+                                                    void* ws, size_t ws_bytes, cudaStream_t stream) {
+  FullArgs a{};
+  bool empty;
+  const msa_status_t st = check_decode(a, empty, q, k_cache, v_cache, page_table, kv_len, B, Hq, Hkv, d, num_pages,
+                                       page_size, max_pages, scale, dtype, out, lse);
+  if (st != MSA_OK) return st;
+  if (P < 0 || P > B) return MSA_ERR_INVALID_ARG;
+  if (empty) return MSA_OK;
+  if (P > 0 && (!cu_prefix || !prefix_len)) return MSA_ERR_INVALID_ARG;
+  const msa_status_t w = check_full_ws(
+      ws, ws_bytes, full_ws_bytes(MSA_OP_FULL_DECODE_SHARED, B, P, max_pages * page_size, Hkv, Hq, d, dtype));
+  if (w != MSA_OK) return w;
+  a.ws = ws;
+  return launched(P == 0 ? launch_full_decode(a, stream) : launch_decode_shared(a, cu_prefix, prefix_len, P, stream));
 }
 
 extern "C" msa_status_t msa_full_attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,

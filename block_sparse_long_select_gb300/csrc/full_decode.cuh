@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     if (!cta_in_order(p.shared.groups, p.shared.disorder)) {  // whose keys these are is not known
       if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
       for (int b = blockIdx.x; b < p.B; b += gridDim.x) empty_row<T, D>(p, b);
+      tc::griddep_wait();
       return;
     }
   }
@@ -533,7 +534,10 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     decode_run<C, true, SHARED>(p, total);
   else
     decode_run<C, false, SHARED>(p, total);
-  if constexpr (SHARED) rest();  // behind the rest: it waits for the prefixes' grid
+  if constexpr (SHARED) {
+    rest();  // behind the others: it waits for the prefixes' grid
+    tc::griddep_wait();  // which, also without work here, is over when this one is
+  }
 }
 
 int fd_grid() { return kNumSMs; }

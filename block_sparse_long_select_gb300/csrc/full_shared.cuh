@@ -258,9 +258,5 @@ PrefixGeometry prefix_geometry_tc(int hpg);
 PrefixGeometry prefix_geometry_f32(int hpg);
 cudaError_t launch_prefix_tc(const SharedArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_f32(const SharedArgs& a, cudaStream_t stream);
-cudaError_t launch_decode_shared(const SharedArgs& a, cudaStream_t stream);
-size_t full_shared_ws_bytes(int B, int groups, int Hkv, int hpg, int d, int dtype);  // behind the header
-// the regions of such a workspace, for SharedParams
-void full_shared_regions(SharedParams& s, void* ws, int B, int groups, int Hkv, int hpg, int d, int dtype);
 
 }  // namespace msa

@@ -138,8 +138,10 @@ using namespace msa;
 
 extern "C" size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int Hq, int d, int di, int Bs, int K,
                                      int dtype) {
+  if (op == MSA_OP_FULL_DECODE_SHARED && Nq < 0) return 0;  // Nq: groups, of which an empty batch has none
   const bool rowless = op == MSA_OP_DECODE || op == MSA_OP_DECODE_STEP || op == MSA_OP_FULL_DECODE ||
-                       op == MSA_OP_FULL_DECODE_FP8;  // Nq is ignored
+                       op == MSA_OP_FULL_DECODE_FP8 ||
+                       op == MSA_OP_FULL_DECODE_SHARED;  // Nq names no rows
   if (empty_batch(B, rowless ? 1 : Nq)) {
     // only the status header, if the call is valid for one row
     const size_t one = msa_workspace_size(op, 1, 1, one_key_min(Nk), G, Hq, d, di, Bs, K, dtype);
@@ -177,6 +179,7 @@ extern "C" size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int H
     case MSA_OP_FULL_BACKWARD:
     case MSA_OP_FULL_DECODE:
     case MSA_OP_FULL_DECODE_FP8:
+    case MSA_OP_FULL_DECODE_SHARED:
     case MSA_OP_PAGED_APPEND:
     case MSA_OP_PAGED_APPEND_FP8:
     case MSA_OP_PAGED_READ_FP8:

@@ -88,7 +88,8 @@ typedef enum {
   MSA_OP_PAGED_APPEND = 11,
   MSA_OP_PAGED_APPEND_FP8 = 13, /* 12 names no operation */
   MSA_OP_PAGED_READ_FP8 = 14,
-  MSA_OP_FULL_DECODE_FP8 = 15
+  MSA_OP_FULL_DECODE_FP8 = 15,
+  MSA_OP_FULL_DECODE_SHARED = 16
 } msa_op_t;
 
 /* Bytes of scratch `ws` the entry point `op` needs for these sizes (the same
@@ -99,7 +100,7 @@ typedef enum {
  * all but di, with G = Hkv; the MSA_OP_FULL_* and MSA_OP_PAGED_* operations
  * use B, Nq = packed rows Tq (T), Nk = packed keys Tk or
  * max_pages * page_size, G = Hkv, Hq (MSA_OP_PAGED_READ_FP8: any multiple of
- * Hkv), d and dtype). Returns 0 when the
+ * Hkv), d and dtype; for MSA_OP_FULL_DECODE_SHARED Nq is the number of groups). Returns 0 when the
  * arguments are invalid or not supported, and 256 for a valid empty batch. */
 size_t msa_workspace_size(int op, int B, int Nq, int Nk, int G, int Hq, int d, int di, int Bs, int K, int dtype);
 
@@ -375,6 +376,35 @@ msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void
                                   const int32_t* kv_len, int B, int Hq, int Hkv, int d, int num_pages, int page_size,
                                   int max_pages, float scale, int dtype, void* out, float* lse, void* ws,
                                   size_t ws_bytes, cudaStream_t stream);
+
+/* msa_full_attn_decode for sequences that begin with the same pages (a system
+ * prompt, several samples of one prompt): what a group has in common is read
+ * once for all its sequences instead of once for each. The arguments describe
+ * the sequences in full, as there, and the result is that call's, within the
+ * rounding of its sums.
+ *  cu_prefix   [P + 1] int32: group x holds sequences [cu_prefix[x], cu_prefix[x+1]),
+ *              0 <= cu_prefix[x] <= cu_prefix[x+1] <= B; it may be empty, and
+ *              sequences before the first and behind the last belong to none
+ *  prefix_len  [P] int32: the first prefix_len[x] keys of group x's sequences are
+ *              the same; a multiple of page_size, at most the kv_len of every
+ *              sequence of the group but those of length 0 (padded entries).
+ *              They are read by the page_table row of the group's first sequence
+ *              that has keys; the others' entries for them are not read.
+ *  0 <= P <= B; with P = 0 (cu_prefix, prefix_len may be NULL) as msa_full_attn_decode
+ *  ws: msa_workspace_size(MSA_OP_FULL_DECODE_SHARED, B, P, max_pages * page_size,
+ *  Hkv, Hq, d, 0, 0, 0, dtype): 2 d + 4 fp32 values per query head and sequence
+ *  (FP32: d + 2), and up to 60 MB
+ *  A sequence with fewer keys than its group's prefix, or whose group's
+ *  prefix_len is not a multiple of page_size or out of range, sets MSA_ERR_BOUNDS and gives
+ *  out 0 and lse -inf, as does every sequence of a group one of whose prefix's pages is
+ *  out of range. cu_prefix out of order or range: MSA_ERR_BOUNDS, and all
+ *  sequences give out 0 and lse -inf (whose keys are whose is not known).
+ *  Deterministic. BF16 rounds the weights of the prefix's keys as msa_full_attn_prefill does. */
+msa_status_t msa_full_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* page_table, const int32_t* kv_len, const int32_t* cu_prefix,
+                                         const int32_t* prefix_len, int B, int P, int Hq, int Hkv, int d,
+                                         int num_pages, int page_size, int max_pages, float scale, int dtype,
+                                         void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* ---- The same caches in 8 bits ----
  * k_cache, v_cache [num_pages, page_size, Hkv, d] hold e4m3 codes (one byte: 4
