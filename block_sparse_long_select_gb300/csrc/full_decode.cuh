@@ -1,7 +1,9 @@
 // Decode kernels of full attention: the walk over the keys of a batch, the ring
 // of copies, the joins. What a warp does with 16 keys (element types, products)
-// is its core, which the including file defines; SHARED leaves the keys that a
-// group of sequences has in common to another grid and joins its results in.
+// is its core, which the including file defines. With SHARED the keys that a
+// group of sequences has in common are left to another grid, and what a warp has
+// of an item goes to a third that joins it all (full_shared.cuh): warps then work
+// alone throughout, each on an equal run of the steps of 16 keys of all items.
 //
 // Work: the keys of every (sequence, key/value head, group of up to 16 query
 // heads) -- an item -- are cut into units of 128 (16 per warp; 64 for fp32 of d
@@ -30,6 +32,7 @@ constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
 // 2^8 and their common factor drops out in the division by their sum.
 constexpr float kFdLazy = 8.f;
+constexpr int kFdLeast = 4;  // SHARED: steps of a warp's run at least, each item of which is a part to be joined
 
 __device__ __forceinline__ float ex2d(float x) {
   float y;
@@ -94,13 +97,14 @@ struct FdParams {
   PageMap pages;
   int B, Hq, Hkv, hpg, ngr, cap;  // ngr: head groups (items) per key/value head; cap: most keys
   float scale_log2;
-  float* part_o;   // [slots][16][D], 2 slots per CTA (SHARED: one per warp)
-  float* part_ml;  // [slots][16][2]: maximum (log2 units), sum; a negative sum marks a page out of range
+  float* part_o;   // [2 * grid][16][D]; SHARED: [items + warps][heads of an item][D]
+  float* part_ml;  // [2 * grid][16][2]; SHARED: [items + warps][heads of an item][2]: maximum (log2 units), sum; a negative sum marks a page out of range
   uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
   void* out;
   float* lse;
   uint32_t* status;
   SharedParams shared;  // SHARED only
+  int2* item_parts;     // SHARED: [items]: the first of an item's parts, their number
 };
 
 // The keys of sequence b that its items walk: [from, L). SHARED: from is where its
@@ -128,61 +132,48 @@ __device__ __forceinline__ int units_of(const FdParams& p, int b, int unit_log2)
   return own_of<SHARED>(p, b).units(unit_log2);
 }
 
-// Joins an item's `parts`, in order, into the rows of its heads: out = sum / den,
-// lse. Whole threads [0, threads); a negative sum marks rows without a result.
-template <typename T, int D, typename F>
-__device__ __forceinline__ void join_parts(const FdParams& p, int b, int h0, int heads, int thread, int threads, int parts,
-                                           F part_of) {
+// Four values of one head joined over `parts` parts, in order, and its lse. A
+// negative sum marks a head without a result.
+template <typename T, typename F>
+__device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D, int dim, int parts, F part_of) {
   constexpr int kBatch = 8;  // parts in flight: the loads of a batch do not wait for each other
-  T* out = static_cast<T*>(p.out);
-  for (int o = thread * 4; o < heads * D; o += threads * 4) {
-    const int h = o / D;
-    float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
-    bool spoilt = false;
-    for (int y0 = 0; y0 < parts; y0 += kBatch) {
-      float2 ml[kBatch];
-      float4 v[kBatch];
+  float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  bool spoilt = false;
+  for (int y0 = 0; y0 < parts; y0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const PartAt s = part_of(min(y0 + x, parts - 1));
-        ml[x] = __ldcg(reinterpret_cast<const float2*>(s.ml) + h);
-        v[x] = __ldcg(reinterpret_cast<const float4*>(s.o + o));
-      }
-      float mn = M;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        spoilt |= ml[x].y < 0.f;
-        mn = fmaxf(mn, ml[x].x);
-      }
-      const float a = M == mn ? 1.f : ex2d(M - mn);
-      M = mn;
-      den *= a;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) sum[y] *= a;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const float w = y0 + x >= parts ? 0.f : ml[x].x == M ? 1.f : ex2d(ml[x].x - M);
-        den = fmaf(w, ml[x].y, den);
-        sum[0] = fmaf(w, v[x].x, sum[0]);
-        sum[1] = fmaf(w, v[x].y, sum[1]);
-        sum[2] = fmaf(w, v[x].z, sum[2]);
-        sum[3] = fmaf(w, v[x].w, sum[3]);
-      }
+    for (int x = 0; x < kBatch; ++x) {
+      const PartAt s = part_of(min(y0 + x, parts - 1));
+      ml[x] = __ldcg(reinterpret_cast<const float2*>(s.ml));
+      v[x] = __ldcg(reinterpret_cast<const float4*>(s.o + dim));
     }
-    const float inv = 1.f / den;
-    T* dst = out + (int64_t(b) * p.Hq + h0 + h) * D + o % D;
+    float mn = M;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt ? 0.f : sum[y] * inv);
-    if (p.lse && o % D == 0) p.lse[int64_t(b) * p.Hq + h0 + h] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
+    for (int x = 0; x < kBatch; ++x) {
+      spoilt |= ml[x].y < 0.f;
+      mn = fmaxf(mn, ml[x].x);
+    }
+    const float a = M == mn ? 1.f : ex2d(M - mn);
+    M = mn;
+    den *= a;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) sum[y] *= a;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const float w = y0 + x >= parts ? 0.f : ml[x].x == M ? 1.f : ex2d(ml[x].x - M);
+      den = fmaf(w, ml[x].y, den);
+      sum[0] = fmaf(w, v[x].x, sum[0]);
+      sum[1] = fmaf(w, v[x].y, sum[1]);
+      sum[2] = fmaf(w, v[x].z, sum[2]);
+      sum[3] = fmaf(w, v[x].w, sum[3]);
+    }
   }
-}
-// A sequence that sees no key (whole CTA).
-template <typename T, int D>
-__device__ __forceinline__ void empty_row(const FdParams& p, int b) {
-  T* out = static_cast<T*>(p.out);
-  for (int x = threadIdx.x; x < p.Hq * D; x += blockDim.x) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
-  if (p.lse)
-    for (int x = threadIdx.x; x < p.Hq; x += blockDim.x) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
+  const float inv = 1.f / den;
+  T* dst = static_cast<T*>(p.out) + row * D + dim;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt ? 0.f : sum[y] * inv);
+  if (p.lse && dim == 0) p.lse[row] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
 }
 
 // A walk over units in order: those of a CTA's run, or (SOLO) of every hop-th item.
@@ -233,7 +224,8 @@ struct FdShape {
   static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
 };
 
-// SOLO: whole items for single warps; else the CTA's run of the `total` units.
+// SOLO: whole items for single warps; SHARED: the warp's run of the `total` steps
+// of 16 keys; else the CTA's run of the `total` units.
 template <typename C, bool SOLO, bool SHARED>
 __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   using SH = FdShape<C>;
@@ -251,10 +243,14 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
 
   constexpr int kUnitLog2 = kUnit == 64 ? 6 : 7;
   static_assert(1 << kUnitLog2 == kUnit, "keys of a unit");
-  constexpr int ulog = SOLO ? kSubLog2 : kUnitLog2;
-  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = SOLO ? 0 : warp * kSub;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t run0 = SOLO ? 0 : blockIdx.x * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);
+  constexpr bool ALONE = SOLO || SHARED;
+  constexpr int ulog = ALONE ? kSubLog2 : kUnitLog2;
+  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * kSub;
+  // runs in the order of the SMs, so that few of them lie on many
+  const int runs = int(gridDim.x) * (SHARED ? kFdWarps : 1), run = SHARED ? warp * int(gridDim.x) + int(blockIdx.x) : int(blockIdx.x);
+  int64_t per = (total + runs - 1) / runs;
+  if (SHARED && per < kFdLeast) per = kFdLeast;
+  const int64_t run0 = SOLO ? 0 : run * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);
   if (run0 >= run1) return;
   Walk<SHARED> at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
@@ -262,10 +258,10 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   if constexpr (SOLO) {
     at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop);
   } else {
-    int ahead = lane < p.B ? units_of<SHARED>(p, lane, kUnitLog2) : 0;
+    int ahead = lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int mine = ahead;
-      ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, kUnitLog2) : 0;  // in flight during the scan
+      ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, ulog) : 0;  // in flight during the scan
       int64_t incl = int64_t(mine) * items;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -346,7 +342,6 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     // ---- the item ends here: join the warps' states, halving their number ----
     fresh = true;
     c.finish();
-    const Own own = at.own;
     constexpr int kRegs = C::kAcc + 2 * C::kM + 1;
     auto put = [&](float* to) {
 #pragma unroll
@@ -375,7 +370,7 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     };
     // Every hand-over has a slot of its own: the upper warps may be at the next
     // item's end while the lower ones still read this one's.
-    if constexpr (!SOLO) {
+    if constexpr (!ALONE) {
 #pragma unroll
       for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
         if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
@@ -384,8 +379,10 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
       }
     }
     const bool whole = SOLO || (item_first >= run0 && ends);
-    const int slot = SHARED && SOLO ? int(blockIdx.x) * kFdWarps + warp : 2 * int(blockIdx.x) + (item_first >= run0 ? 1 : 0);
-    if (SOLO || warp == 0) {
+    // SHARED: parts in the order of the items, those of one item in the order of the runs
+    const int item = at.b * items + at.it, item_heads = SHARED ? min(p.hpg, kFdMaxHeads) : kFdMaxHeads;
+    const int slot = SHARED ? item + run : 2 * run + (item_first >= run0 ? 1 : 0);
+    if (ALONE || warp == 0) {
       c.sum_l();
       if (__any_sync(0xffffffffu, bad)) {
         bad = true;
@@ -404,8 +401,10 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
             if (h < heads) p.lse[int64_t(b) * p.Hq + h0 + h] = bad ? -INFINITY : (c.m[x] + log2f(c.l[x])) * kFdLn2;
           });
       } else {
-        float* po = p.part_o + int64_t(slot) * kFdMaxHeads * D;
-        float* pm = p.part_ml + int64_t(slot) * kFdMaxHeads * 2;
+        float* po = p.part_o + int64_t(slot) * item_heads * D;
+        float* pm = p.part_ml + int64_t(slot) * item_heads * 2;
+        if (SHARED && lane == 0 && item_first >= run0)
+          p.item_parts[item] = make_int2(slot, int((item_first + n - 1) / per) - run + 1);
         c.each([&](int h, int, int dim, float val) {
           if (h < heads) po[h * D + dim] = val;
         });
@@ -417,19 +416,10 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
         });
       }
     }
-    if constexpr (SHARED && SOLO) {
-      __syncwarp();
-      const PartAt own_part{p.part_o + int64_t(slot) * kFdMaxHeads * D, p.part_ml + int64_t(slot) * kFdMaxHeads * 2};
-      tc::griddep_wait();
-      const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, h0 - g * p.hpg);
-      join_parts<T, D>(p, b, h0, heads, lane, 32, 1 + pre.n,
-                       [&](int y) { return y == 0 ? own_part : pre.part(y - 1); });
-      __syncwarp();  // the parts are read before the next item's go over them
-    } else if (SHARED || !whole) {
+    if (!SHARED && !whole) {
       // the item's units lie in CTAs c0..c1: the last to arrive joins them
-      const int c0 = whole ? int(blockIdx.x) : int(item_first / per);
-      const int c1 = whole ? c0 : int((item_first + n - 1) / per);
-      if (!whole && warp == 0) {
+      const int c0 = int(item_first / per), c1 = int((item_first + n - 1) / per);
+      if (warp == 0) {
         __syncwarp();
         if (lane == 0) {
           // releases the warp's stores (ordered by __syncwarp), acquires the others'
@@ -444,22 +434,14 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
         }
       }
       __syncthreads();
-      if (whole || last_s) {
-        auto part_of = [&](int y) {
-          const int cta = c0 + y, s = 2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0);
-          return PartAt{p.part_o + int64_t(s) * kFdMaxHeads * D, p.part_ml + int64_t(s) * kFdMaxHeads * 2};
-        };
-        if constexpr (SHARED) {
-          tc::griddep_wait();
-          const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, h0 - g * p.hpg);
-          const int parts = c1 - c0 + 1;
-          join_parts<T, D>(p, b, h0, heads, threadIdx.x, kFdThreads, parts + pre.n,
-                           [&](int y) { return y < parts ? part_of(y) : pre.part(y - parts); });
-        } else {
-          join_parts<T, D>(p, b, h0, heads, threadIdx.x, kFdThreads, c1 - c0 + 1, part_of);
-        }
-      }
-      __syncthreads();  // last_s and the parts are read before the next item sets them
+      if (last_s)
+        for (int o = threadIdx.x * 4; o < heads * D; o += kFdThreads * 4)
+          join_head<T>(p, int64_t(b) * p.Hq + h0 + o / D, D, o % D, c1 - c0 + 1, [&](int y) {
+            const int cta = c0 + y, s = 2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0);
+            const int64_t head = int64_t(s) * kFdMaxHeads + o / D;
+            return PartAt{p.part_o + head * D, p.part_ml + head * 2};
+          });
+      __syncthreads();  // last_s is read before the next item sets it
     }
     if (ends) item_first += n;
     const int was = at.b;
@@ -476,10 +458,10 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   constexpr int D = C::kD;
   constexpr int kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
   const int lane = threadIdx.x & 31, items = p.Hkv * p.ngr;
+  [[maybe_unused]] T* out = static_cast<T*>(p.out);
   if constexpr (SHARED) {
+    tc::griddep_launch_dependents();  // the joins' grid, which waits for this one
     if (!cta_in_order(p.shared.groups, p.shared.disorder)) {  // whose keys these are is not known
-      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, MSA_ERR_BOUNDS);
-      for (int b = blockIdx.x; b < p.B; b += gridDim.x) empty_row<T, D>(p, b);
       tc::griddep_wait();
       return;
     }
@@ -491,7 +473,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
 #pragma unroll 8
   for (int b = lane; b < p.B; b += 32) {
     const int steps = units_of<SHARED>(p, b, kSubLog2);
-    total += (steps + kFdWarps - 1) / kFdWarps;
+    total += SHARED ? steps : (steps + kFdWarps - 1) / kFdWarps;
     longest = max(longest, steps);
   }
 #pragma unroll
@@ -508,41 +490,26 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   const int warps = int(gridDim.x) * kFdWarps;
   const int64_t all = int64_t(p.B) * items, rounds = (all + warps - 1) / warps;
   const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
-  // sequences without keys (SHARED: of their own): nobody's run holds them
-  auto rest = [&]() {
+  if constexpr (!SHARED) {  // sequences without keys: nobody's run holds them
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      const Own o = own_of<SHARED>(p, b);
+      const Own o = own_of<false>(p, b);
       if (o.units(kSubLog2) > 0) continue;
       if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
-      if constexpr (SHARED) {
-        if (o.ok && o.L > 0) {  // the prefix is all that it sees
-          tc::griddep_wait();
-          for (int it = 0; it < items; ++it) {
-            const int g = it / p.ngr, h = (it % p.ngr) * kFdMaxHeads;
-            const PrefixRows<D> pre = p.shared.rows<D>(o.x, b, g, h);
-            join_parts<T, D>(p, b, g * p.hpg + h, min(p.hpg - h, kFdMaxHeads), threadIdx.x, kFdThreads, pre.n,
-                             [&](int y) { return pre.part(y); });
-          }
-          continue;
-        }
-      }
-      empty_row<T, D>(p, b);
+      for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
+      if (p.lse)
+        for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
     }
-  };
-  if constexpr (!SHARED) rest();
-  if (solo)
-    decode_run<C, true, SHARED>(p, total);
+  }
+  if (!SHARED && solo)
+    decode_run<C, !SHARED, SHARED>(p, total);
   else
     decode_run<C, false, SHARED>(p, total);
-  if constexpr (SHARED) {
-    rest();  // behind the others: it waits for the prefixes' grid
-    tc::griddep_wait();  // which, also without work here, is over when this one is
-  }
+  if constexpr (SHARED) tc::griddep_wait();  // this grid is not over before the prefixes' grid is
 }
 
 int fd_grid() { return kNumSMs; }
 
-// `early`: the grid may start while the one before it ends (SHARED, which waits itself)
+// SHARED: the grid may start while the one before it ends
 template <typename C, bool SHARED>
 cudaError_t decode(const FdParams& p, const char* name, cudaStream_t stream) {
   auto kern = full_decode_kernel<C, SHARED>;

@@ -1,30 +1,94 @@
 // Decode over shared prefixes: each sequence's own keys by the decode kernel's
-// walk (full_decode.cuh), whose joins take in the parts that the prefixes' grid
-// left (full_prefix_tc.cu, full_prefix_fp32.cu). The grid starts while that one
-// ends and waits for it before its first join.
+// walk (full_decode.cuh), and the join of its parts with those that the
+// prefixes' grid left (full_prefix_tc.cu, full_prefix_fp32.cu). Each of the three
+// grids starts while the one before it ends.
 #include "full_decode_cores.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kSharedSlots = kNumSMs * 8;  // a slot for every warp
+// A thread per four values of a query head; D / 4 of them a head. Bound by the
+// latency of five dependent loads and, for many parts, by L2.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) full_join_kernel(const FdParams p) {
+  constexpr int kLanes = D / 4;
+  const int64_t row = int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+  const int dim = (threadIdx.x % kLanes) * 4;
+  const bool in_order = cta_in_order(p.shared.groups, p.shared.disorder);
+  const bool mine = row < int64_t(p.B) * p.Hq;
+  const int b = mine ? int(row / p.Hq) : 0, h = mine ? int(row % p.Hq) : 0, g = h / p.hpg, hg = h - g * p.hpg;
+  Own own{0, 0, -1, false};
+  if (in_order) own = own_of<true>(p, b);
+  tc::griddep_wait();
+  if (!mine) return;
+  if (!own.ok || own.L == 0) {
+    if (!own.ok && dim == 0) set_status(p.status, MSA_ERR_BOUNDS);
+    T* dst = static_cast<T*>(p.out) + row * D + dim;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(0.f);
+    if (p.lse && dim == 0) p.lse[row] = -INFINITY;
+    return;
+  }
+  const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, hg);
+  const int heads = min(p.hpg, kFdMaxHeads);
+  int2 parts = make_int2(0, 0);  // of its own keys
+  if (own.L > own.from) parts = __ldcg(p.item_parts + (b * p.Hkv + g) * p.ngr + hg / heads);
+  join_head<T>(p, row, D, dim, parts.y + pre.n, [&](int y) {
+    if (y >= parts.y) return pre.part(y - parts.y);
+    const int64_t head = int64_t(parts.x + y) * heads + hg % heads;
+    return PartAt{p.part_o + head * D, p.part_ml + head * 2};
+  });
+}
 
+template <typename T, int D>
+cudaError_t join(const FdParams& p, cudaStream_t stream) {
+  ProfScope pf("full_join", stream);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned((int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, full_join_kernel<T, D>, p);
+}
 template <typename T, int D, int H>
 cudaError_t run(const FdParams& p, cudaStream_t stream) {
-  return decode<Core<T, D, H>, true>(p, "full_decode_shared", stream);
+  if (cudaError_t e = decode<Core<T, D, H>, true>(p, "full_decode_shared", stream)) return e;
+  return join<T, D>(p, stream);
 }
+
 PrefixGeometry geometry(int hpg, int dtype) { return dtype == MSA_BF16 ? prefix_geometry_tc(hpg) : prefix_geometry_f32(hpg); }
-// most rows of all parts: every item's (an alt item's twice), and a block for every CTA that an item goes on in
-size_t part_rows(const PrefixGeometry& g, int B, int Hkv) {
-  return size_t(B) * Hkv * g.groups * g.heads * (g.half > 0 ? 2 : 1) + size_t(g.grid) * g.block;
-}
+// The workspace behind the header.
+struct Regions {
+  size_t recs, items, stat, part, own_stat, own_part, end;
+  Regions(const PrefixGeometry& g, int B, int groups, int Hkv, int hpg, int d) {
+    // every item's rows, and a block for every CTA that an item goes on in
+    const size_t rows = size_t(B) * Hkv * g.groups * g.heads + size_t(g.grid) * g.block;
+    const size_t own_items = size_t(B) * Hkv * head_groups(hpg), own_rows = (own_items + fd_grid() * 8) * (hpg < kFdMaxHeads ? hpg : kFdMaxHeads);
+    size_t at = kWsHeader;
+    auto take = [&](size_t bytes) {
+      const size_t r = at;
+      at += up256(bytes);
+      return r;
+    };
+    recs = take(size_t(groups) * sizeof(PrefixRec));
+    items = take(own_items * sizeof(int2));
+    stat = take(rows * sizeof(float2));
+    part = take(rows * d * sizeof(float));
+    own_stat = take(own_rows * sizeof(float2));
+    own_part = take(own_rows * d * sizeof(float));
+    end = at;
+  }
+};
 
 }  // namespace
 
 size_t full_shared_ws_bytes(int B, int groups, int Hkv, int hpg, int d, int dtype) {
-  const size_t rows = part_rows(geometry(hpg, dtype), B, Hkv);
-  return fd_part_bytes(kSharedSlots, d) + up256(size_t(groups) * sizeof(PrefixRec)) + up256(rows * sizeof(float2)) +
-         up256(rows * d * sizeof(float));
+  return Regions(geometry(hpg, dtype), B, groups, Hkv, hpg, d).end - kWsHeader;
 }
 
 cudaError_t launch_decode_shared(const FullArgs& a, const int32_t* cu_prefix, const int32_t* prefix_len, int groups,
@@ -35,16 +99,19 @@ cudaError_t launch_decode_shared(const FullArgs& a, const int32_t* cu_prefix, co
   s.prefix_len = prefix_len;
   s.disorder = &static_cast<WsHeader*>(a.ws)->disorder;
   s.geo = geometry(hpg, a.dtype);
-  char* w = static_cast<char*>(a.ws) + kWsHeader + fd_part_bytes(kSharedSlots, a.d);
-  s.recs = reinterpret_cast<PrefixRec*>(w);
-  w += up256(size_t(groups) * sizeof(PrefixRec));
-  s.stat = reinterpret_cast<float2*>(w);
-  s.part = reinterpret_cast<float*>(w + up256(part_rows(s.geo, B, a.Hkv) * sizeof(float2)));
+  const Regions at(s.geo, B, groups, a.Hkv, hpg, a.d);
+  char* w = static_cast<char*>(a.ws);
+  s.recs = reinterpret_cast<PrefixRec*>(w + at.recs);
+  s.stat = reinterpret_cast<float2*>(w + at.stat);
+  s.part = reinterpret_cast<float*>(w + at.part);
   if (cudaError_t e = launch_order_check(s.groups, a.ws, stream)) return e;
   const SharedArgs args{a, s};
   if (cudaError_t e = a.dtype == MSA_BF16 ? launch_prefix_tc(args, stream) : launch_prefix_f32(args, stream)) return e;
-  FdParams p = fd_params(a, kSharedSlots);
+  FdParams p = fd_params(a, 0);
   p.shared = s;
+  p.item_parts = reinterpret_cast<int2*>(w + at.items);
+  p.part_ml = reinterpret_cast<float*>(w + at.own_stat);
+  p.part_o = reinterpret_cast<float*>(w + at.own_part);
   const bool wide = hpg > 8, few = hpg <= 4;  // as in full_decode.cu
   if (a.dtype == MSA_BF16) {
     if (a.d == 128) return wide ? run<__nv_bfloat16, 128, 16>(p, stream) : run<__nv_bfloat16, 128, 8>(p, stream);

@@ -12,7 +12,8 @@
 // Either the tiles are different rows and take every key tile in turn (one copy
 // of it serves both), or, where the rows fit into one tile, they are the same
 // rows and take the key tiles alternately, each with a maximum, sum and output
-// of its own. The maximum only moves when a tile exceeds it by more than 2^8;
+// of its own; the two warpgroups then join them, half the columns each. K and V
+// tiles come through one ring in the order in which the products need them. The maximum only moves when a tile exceeds it by more than 2^8;
 // P is rounded to bf16 for its product, the sum takes it unrounded.
 //
 // Bound: HBM for up to 128 rows (64 KB of keys and values for 2 d 128^2 products
@@ -52,15 +53,38 @@ struct PxItem {
 
 template <int D>
 struct PxSmem {
-  static constexpr int kStages = D == 128 ? 2 : 4;  // K ring and V ring
+  static constexpr int kStages = D == 128 ? 5 : 10;  // ring of K and V tiles
   static constexpr int kItems = 2;
   static constexpr uint32_t kTile = kRows * D * 2;
-  static constexpr uint32_t oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile, oStore = oV + kStages * kTile;
-  static constexpr uint32_t kStore = 32 * 128;  // per softmax warp: 32 rows x 32 columns
-  static constexpr uint32_t oItem = oStore + 8 * kStore, oBar = (oItem + kItems * sizeof(PxItem) + 15) & ~15u;
-  static constexpr int kBars = 4 + 4 * kStages + 8 + 2 * kItems + 3;
+  static constexpr uint32_t oQ = 0, oRing = 2 * kTile, oStat = oRing + kStages * kTile;
+  static constexpr uint32_t kStat = 2 * kRows * sizeof(float2);  // [half][row]: maximum, sum
+  static constexpr uint32_t oItem = oStat + kStat, oBar = (oItem + kItems * sizeof(PxItem) + 15) & ~15u;
+  static constexpr int kBars = 4 + 2 * kStages + 8 + 2 * kItems + 4;
   static constexpr uint32_t kTotal = oBar + kBars * 8 + 16;
 };
+// The order of a part's 2 n tiles in the ring: K_0 V_0 K_1 V_1 ..., or, where the
+// halves take key tiles alternately, K_0 K_1 V_0 K_2 V_1 ... V_(n-1): the
+// scores of tile t + 2 follow the products with V_t.
+__device__ __forceinline__ int k_place(bool alt, int j) { return !alt ? 2 * j : j < 2 ? j : 2 * j - 1; }
+__device__ __forceinline__ int v_place(bool alt, int j, int n) { return !alt || j == n - 1 ? 2 * j + 1 : 2 * j + 2; }
+// the key tile of a place; whether it is V's
+__device__ __forceinline__ int at_place(bool alt, int x, int n, bool& is_v) {
+  if (!alt || x == 2 * n - 1) {
+    is_v = x & 1;
+    return x >> 1;
+  }
+  is_v = x >= 2 && !(x & 1);
+  return is_v ? (x - 2) >> 1 : x < 2 ? x : (x + 1) >> 1;
+}
+// Eight floats to global memory: one whole 32-byte sector
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void arrive_twice(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(tc::smem_u32(bar)) : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPxThreads, 1)
@@ -83,17 +107,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(px_smem + SM::oBar);
   uint64_t* q_full = bars;                // [2]
   uint64_t* q_empty = bars + 2;           // [2]
-  uint64_t* k_full = bars + 4;            // [NS]
-  uint64_t* k_empty = k_full + NS;        // [NS]
-  uint64_t* v_full = k_empty + NS;        // [NS]
-  uint64_t* v_empty = v_full + NS;        // [NS]
-  uint64_t* s_full = v_empty + NS;        // [2]
+  uint64_t* t_full = bars + 4;            // [NS]
+  uint64_t* t_empty = t_full + NS;        // [NS]
+  uint64_t* s_full = t_empty + NS;        // [2]
   uint64_t* p_full = s_full + 2;          // [2]
   uint64_t* o_full = p_full + 2;          // [2]
   uint64_t* o_empty = o_full + 2;         // [2]
   uint64_t* item_full = o_empty + 2;      // [NI]
   uint64_t* item_empty = item_full + NI;  // [NI]
-  uint64_t* tail_bar = item_empty + NI;   // the copies of a value tile whose last rows are then zeroed
+  uint64_t* both_bar = item_empty + NI;   // both halves' outputs, maxima and sums are there
+  uint64_t* tail_bar = both_bar + 1;      // the copies of a value tile whose last rows are then zeroed
   uint64_t* done_bar = tail_bar + 1;
   uint64_t* never_bar = done_bar + 1;     // no thread arrives on it (timeout injection)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -106,9 +129,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     init(bars, int(p_full - bars), 1);
     init(p_full, 2, 4);  // a row tile's softmax warps
     init(o_full, 2, 1);
-    init(o_empty, 2, 4);
+    init(o_empty, 2, 8);  // both softmax warpgroups, or one twice
     init(item_full, NI, 1);
     init(item_empty, NI, 10);  // loads, MMA, 8 softmax warps
+    init(both_bar, 1, 8);
     init(tail_bar, 3, 1);      // tail, done, never
     *abort_flag = 0;
     tc::fence_barrier_init();
@@ -146,7 +170,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
       };
       bool ok = true;
-      int z = 0, nv = 0, nk = 0, tails = 0, nq0 = 0, nq1 = 0;  // z: tiles so far; the rest: loads issued
+      int z = 0, issued = 0, tails = 0, nq0 = 0, nq1 = 0;  // z: places so far; the rest: loads issued
       for (int it = 0; ok; ++it) {
         if (!(ok = warp_wait(&item_full[it % NI], (it / NI) & 1, abort_flag))) break;
         const PrefixPart s = items[it % NI].d;
@@ -157,8 +181,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (mode == 2) continue;
         const int np = s.Lk >> p.pages.page_log2;
         const int32_t* table = p.pages.table + int64_t(s.leader) * p.pages.max_pages;
-        auto first_row = [&](int j) {  // this lane's box of the part's tile j: its first row, -1 if it has none
-          const int pi = (s.jb + j) * per + lane;
+        bool is_v;
+        auto first_row = [&](int x) {  // this lane's box of the tile at place x: its first row, -1 if it has none
+          const int pi = (s.jb + at_place(s.alt, x, s.n, is_v)) * per + lane;
           return lane < per && pi < np ? table[pi] << p.pages.page_log2 : -1;
         };
         auto load_q = [&](int w, int use) {
@@ -175,38 +200,37 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         load_q(0, nq0);
         if (!ok) break;
         ++nq0;
-        for (int j = 0; j < s.n; ++j, ++z) {
-          const int st = z % NS, ph = (z / NS) & 1;
-          const int next = j + 1 < s.n ? first_row(j + 1) : -1;  // in flight while this tile is issued
-          if (!(ok = warp_wait(&k_empty[st], ph ^ 1, abort_flag))) break;
-          boxes(px_smem + SM::oK + st * SM::kTile, &tmK, &k_full[st], s.g, row);
-          nk = z + 1;
-          if (j == 0 && !s.alt) {
-            load_q(1, nq1);
-            if (!ok) break;
-            ++nq1;
-          }
-          if (!(ok = warp_wait(&v_empty[st], ph ^ 1, abort_flag))) break;
-          uint8_t* vt = px_smem + SM::oV + st * SM::kTile;
-          const int valid = s.Lk - (s.jb + j) * kKeys;
-          if (valid >= kKeys) {
-            boxes(vt, &tmV, &v_full[st], s.g, row);
-            nv = z + 1;
+        for (int x = 0; x < 2 * s.n; ++x, ++z) {
+          const int st = z % NS;
+          const int next = x + 1 < 2 * s.n ? first_row(x + 1) : -1;  // in flight while this tile is issued
+          const int j = s.jb + at_place(s.alt, x, s.n, is_v);
+          if (!(ok = warp_wait(&t_empty[st], ((z / NS) & 1) ^ 1, abort_flag))) break;
+          uint8_t* dst = px_smem + SM::oRing + st * SM::kTile;
+          const int valid = s.Lk - j * kKeys;
+          if (!is_v || valid >= kKeys) {
+            boxes(dst, is_v ? &tmV : &tmK, &t_full[st], s.g, row);
+            issued = z + 1;
           } else {
             // weight 0 does not silence an infinity or NaN that an earlier tile left: those rows become zeros
-            boxes(vt, &tmV, tail_bar, s.g, row);
+            boxes(dst, &tmV, tail_bar, s.g, row);
             if (!(ok = warp_wait(tail_bar, tails & 1, abort_flag))) {
               int zero = 0;
               tc::mbar_wait(tail_bar, tails & 1, &zero);
               break;
             }
             ++tails;
-            zero_rows<NH>(vt, valid, kKeys);
+            zero_rows<NH>(dst, valid, kKeys);
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&v_full[st]);
+            if (lane == 0) tc::mbar_arrive(&t_full[st]);
+            issued = z + 1;
           }
           row = next;
+          if (x == 0 && !s.alt) {
+            load_q(1, nq1);
+            if (!ok) break;
+            ++nq1;
+          }
           if (p.inject_timeout && z == 0 && blockIdx.x % 2 == 0 &&
               !(ok = __all_sync(0xffffffffu, tc::mbar_wait_for(never_bar, 0, abort_flag, tc::kInjectedWaitCycles))))
             break;
@@ -217,8 +241,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         int zero = 0;
         if (nq0 > 0) tc::mbar_wait(&q_full[0], (nq0 - 1) & 1, &zero);
         if (nq1 > 0) tc::mbar_wait(&q_full[1], (nq1 - 1) & 1, &zero);
-        for (int x = max(nk - NS, 0); x < nk; ++x) tc::mbar_wait(&k_full[x % NS], (x / NS) & 1, &zero);
-        for (int x = max(nv - NS, 0); x < nv; ++x) tc::mbar_wait(&v_full[x % NS], (x / NS) & 1, &zero);
+        for (int x = max(issued - NS, 0); x < issued; ++x) tc::mbar_wait(&t_full[x % NS], (x / NS) & 1, &zero);
       }
     } else if (warp == 1) {
       // ----------------------------- MMA issue -----------------------------
@@ -227,20 +250,23 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (lane == 0) {
         constexpr uint32_t kHi = tc::smem_desc_hi(1024, 2);
         const uint32_t qa = tc::smem_desc_lo(tc::smem_u32(px_smem + SM::oQ), 16);
-        const uint32_t ka = tc::smem_desc_lo(tc::smem_u32(px_smem + SM::oK), 16);
-        const uint32_t va = tc::smem_desc_lo(tc::smem_u32(px_smem + SM::oV), kHalfTile);
+        const uint32_t ka = tc::smem_desc_lo(tc::smem_u32(px_smem + SM::oRing), 16);
+        const uint32_t va = tc::smem_desc_lo(tc::smem_u32(px_smem + SM::oRing), kHalfTile);
         bool ok = true;
-        uint32_t z = 0, qu0 = 0, qu1 = 0, ou0 = 0, ou1 = 0, sp0 = 0, sp1 = 0;  // tiles; uses of Q, of O; steps
+        uint32_t z = 0, qu0 = 0, qu1 = 0, ou0 = 0, ou1 = 0, sp0 = 0, sp1 = 0;  // places; uses of Q, of O; steps
         for (int it = 0; ok; ++it) {
           if (!(ok = tc::mbar_wait(&item_full[it % NI], (it / NI) & 1, abort_flag))) break;
-          const int mode = items[it % NI].mode, n = items[it % NI].d.n, alt = items[it % NI].d.alt;
+          const int mode = items[it % NI].mode, n = items[it % NI].d.n;
+          const bool alt = items[it % NI].d.alt;
           tc::mbar_arrive(&item_empty[it % NI]);
           if (mode == 3) break;
           if (mode == 2) continue;
           const int steps = alt ? n : 2 * n;
-          auto tile = [&](int t) { return z + uint32_t(alt ? t : t >> 1); };
+          auto k_at = [&](int t) { return z + uint32_t(k_place(alt, alt ? t : t >> 1)); };
+          auto v_at = [&](int t) { return z + uint32_t(v_place(alt, alt ? t : t >> 1, n)); };
+          auto full = [&](uint32_t x) { return tc::mbar_wait(&t_full[x % NS], (x / NS) & 1, abort_flag); };
           auto scores = [&](int t) {  // S_w = Q K^T, and what it is the last to read falls free
-            const uint32_t w = t & 1, st = tile(t) % NS;
+            const uint32_t w = t & 1, st = k_at(t) % NS;
             const uint32_t q0 = qa + (alt ? 0u : (w * SM::kTile) >> 4), k0 = ka + ((st * SM::kTile) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -248,13 +274,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tc::mma_f16_ss_lo<kHi>(tmem + w * 128, q0 + off, k0 + off, kIdS, kk > 0 ? 1u : 0u);
             }
             tc::mma_commit(&s_full[w]);
-            if (alt || w == 1) tc::mma_commit(&k_empty[st]);
+            if (alt || w == 1) tc::mma_commit(&t_empty[st]);
             if (alt ? t + 1 == steps : t + 2 >= steps) tc::mma_commit(&q_empty[alt ? 0 : w]);
           };
           for (int t = 0; t < 2 && t < steps; ++t) {
             // the first scores go over the last weights of the part before, behind the products that read them
-            if (!(ok = (t == 1 && alt ? true : tc::mbar_wait(&q_full[t], (t ? qu1 : qu0) & 1, abort_flag)) &&
-                       tc::mbar_wait(&k_full[tile(t) % NS], (tile(t) / NS) & 1, abort_flag)))
+            if (!(ok = (t == 1 && alt ? true : tc::mbar_wait(&q_full[t], (t ? qu1 : qu0) & 1, abort_flag)) && full(k_at(t))))
               break;
             tc::fence_after_sync();
             scores(t);
@@ -262,11 +287,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           ++qu0;
           if (!alt) ++qu1;
           for (int t = 0; t < steps && ok; ++t) {
-            const uint32_t w = t & 1, st = tile(t) % NS;
+            const uint32_t w = t & 1, st = v_at(t) % NS;
             // what is ready early is waited for first: every wait between products costs the pipe
-            if (!(ok = tc::mbar_wait(&v_full[st], (tile(t) / NS) & 1, abort_flag) &&
-                       (t + 2 >= steps || tc::mbar_wait(&k_full[tile(t + 2) % NS], (tile(t + 2) / NS) & 1, abort_flag))))
-              break;
+            if (!(ok = full(v_at(t)) && (t + 2 >= steps || full(k_at(t + 2))))) break;
             const uint32_t v0 = va + ((st * SM::kTile) >> 4);
             // O of the part before has been read
             if (t < 2 && !(ok = tc::mbar_wait(&o_empty[w], ((w ? ou1 : ou0) & 1) ^ 1, abort_flag))) break;
@@ -277,15 +300,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             for (int kk = 0; kk < kKeys / 16; ++kk)  // O_w += P_w V
               tc::mma_f16_ts_lo<kHi>(tmem + kColO + w * D, tmem + w * 128 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdO,
                                      t > 1 || kk > 0 ? 1u : 0u);
+            if (alt || w == 1) tc::mma_commit(&t_empty[st]);
             if (t + 2 < steps) {
               scores(t + 2);  // in issue order behind the product that reads P: S may go over it
             } else {
               tc::mma_commit(&o_full[w]);
               w ? ++ou1 : ++ou0;
             }
-            if (alt || w == 1) tc::mma_commit(&v_empty[st]);
           }
-          z += n;
+          z += 2 * n;
         }
         if (!ok) fail();
         int zero = 0;
@@ -334,10 +357,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t sbase = tmem + (uint32_t(quarter * 32) << 16) + w * 128;
     const uint32_t obase = tmem + (uint32_t(quarter * 32) << 16) + kColO + w * D;
-    const uint32_t stage = tc::smem_u32(px_smem + SM::oStore + (warp - 4) * SM::kStore);
+    float2* stats = reinterpret_cast<float2*>(px_smem + SM::oStat);
     const int row_seq = r / p.hpg;
     bool ok = true;
-    int z = 0, used = 0;  // steps and parts of this row tile
+    int z = 0, used = 0, alts = 0;  // steps and parts of this row tile; parts of alternate key tiles
     for (int it = 0; ok; ++it) {
       if (!(ok = warp_wait(&item_full[it % NI], (it / NI) & 1, abort_flag))) break;
       const PxItem* sp = items + it % NI;
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (lane == 0) tc::mbar_arrive(&item_empty[it % NI]);
       if (mode == 3) break;
       const bool valid = r < p.tpt * p.hpg && row_seq + (alt ? 0 : w * p.tpt) < count;
-      const int64_t row = row0 + (alt ? w * count : w * p.tpt) * p.hpg + r;  // of the part's
+      const int64_t row = row0 + (alt ? 0 : w * p.tpt) * p.hpg + r;  // of the part's
       if (mode == 2) {
         if (valid) p.s.stat[row] = make_float2(-INFINITY, -1.f);
         continue;
@@ -456,46 +479,61 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
       }
       if (!ok) break;
-      if (valid) p.s.stat[row] = make_float2(m, l);
       if (steps > 0) {
         if (!(ok = warp_wait(&o_full[w], used & 1, abort_flag))) break;
         ++used;
         tc::fence_after_sync();
       }
-      // the rows' output, 32 columns at a time through shared memory, so that 8 lanes store 128 contiguous bytes
+      if (!alt) {
+        if (valid) p.s.stat[row] = make_float2(m, l);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        if (steps > 0) {
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
           tc::tmem_ld_32x32b_x32(obase + c * 32, reinterpret_cast<uint32_t*>(o));
           tc::tmem_ld_wait();
-        } else {  // a single key tile: the other half has none, and 0 counts for nothing
+          if (valid) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+            for (int x = 0; x < 4; ++x) store8(p.s.part + row * D + c * 32 + x * 8, o + x * 8);
+          }
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (uint32_t(x ^ (lane & 7)) << 4)),
-                       "f"(o[4 * x]), "f"(o[4 * x + 1]), "f"(o[4 * x + 2]), "f"(o[4 * x + 3])
-                       : "memory");
+        tc::fence_before_sync();  // the next part's products may go over O
         __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int rr = x * 4 + (lane >> 3), cc = lane & 7;
-          const int64_t to = __shfl_sync(0xffffffffu, valid ? row : int64_t(-1), rr);
-          float4 f;
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                       : "r"(stage + rr * 128 + (uint32_t(cc ^ (rr & 7)) << 4))
-                       : "memory");
-          if (to >= 0) reinterpret_cast<float4*>(p.s.part + to * D + c * 32)[cc] = f;
-        }
-        __syncwarp();
+        if (lane == 0) arrive_twice(&o_empty[w]);
+        continue;
       }
-      if (steps > 0) {  // the next part's products may go over O
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&o_empty[w]);
+      // ---- both halves' states of the same rows: joined, each warpgroup half the columns ----
+      // A half writes its statistics behind products that waited for everybody to release its last output,
+      // which they do behind reading the last statistics; a half without steps, which waits for nothing, writes none.
+      if (steps > 0) stats[w * kRows + r] = make_float2(m, l);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(both_bar);
+      if (!(ok = warp_wait(both_bar, alts & 1, abort_flag))) break;
+      ++alts;
+      tc::fence_after_sync();
+      const float2 s0 = stats[r], s1 = n > 1 ? stats[kRows + r] : make_float2(-INFINITY, 0.f);
+      const float M = fmaxf(s0.x, s1.x);
+      const float a0 = s0.x == M ? 1.f : ex2(s0.x - M), a1 = s1.x == M ? 1.f : ex2(s1.x - M);
+      if (valid && w == 0) p.s.stat[row] = make_float2(M, s0.y * a0 + s1.y * a1);
+      const uint32_t o0 = tmem + (uint32_t(quarter * 32) << 16) + kColO + w * (D / 2), o1 = o0 + D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float x0[16], x1[16];
+        tc::tmem_ld_32x32b_x16(o0 + c * 16, reinterpret_cast<uint32_t*>(x0));
+        if (n > 1) tc::tmem_ld_32x32b_x16(o1 + c * 16, reinterpret_cast<uint32_t*>(x1));
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) x0[x] = n > 1 ? fmaf(x1[x], a1, x0[x] * a0) : x0[x];
+        if (valid) {
+          store8(p.s.part + row * D + w * (D / 2) + c * 16, x0);
+          store8(p.s.part + row * D + w * (D / 2) + c * 16 + 8, x0 + 8);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&o_empty[0]);
+        if (n > 1) tc::mbar_arrive(&o_empty[1]);
       }
     }
     if (!ok) fail();

@@ -11,6 +11,10 @@
 // runs, so an item may lie in several consecutive CTAs; each leaves a part: its
 // rows' maximum (log2 units), sum and unnormalised output. The reader finds the
 // parts in closed form, so nothing is counted, and nothing waits, inside the grid.
+// The decode grid leaves parts of the sequences' own keys, and a third grid
+// joins them all, a thread per four values: joined at each item's end inside the
+// decode grid, 97 sequences of 1300 own keys behind 12 K shared ones took 190 us,
+// of which its copies stood still for half.
 #pragma once
 
 #include "full_internal.cuh"
@@ -21,7 +25,7 @@ constexpr int kPxKeys = 128;  // keys of a tile
 
 // How rows are cut into items. bf16: two row tiles of `half` sequences, which
 // share each key tile; an item whose sequences fit into one takes the key tiles
-// two at a time instead, one per half, and leaves two parts per CTA (`alt`).
+// two at a time instead, one per half (`alt`).
 struct PrefixGeometry {
   int heads, groups;  // heads of an item; items' head groups per key/value head
   int seqs, half;     // sequences of an item; of a row tile (0: an item is one row tile)
@@ -46,7 +50,7 @@ struct PrefixItem {
 };
 __host__ __device__ __forceinline__ PrefixItem prefix_item(const PrefixGeometry& g, int count, int n) {
   const bool alt = g.half > 0 && count <= g.half;
-  return {alt ? (n + 1) / 2 : n, count * g.heads * (alt ? 2 : 1), alt};
+  return {alt ? (n + 1) / 2 : n, count * g.heads, alt};
 }
 // Of all items of a group for one key/value head and head group
 struct PrefixTiles {
@@ -99,17 +103,16 @@ template <int D>
 struct PrefixRows {
   const float* o;
   const float2* ml;
-  int n, block, second;  // parts; rows from one part to the next, and to an alt part's second half (0: none)
+  int n, block;  // parts; rows from one to the next
   __device__ __forceinline__ PartAt part(int y) const {
-    const int64_t row = second ? int64_t(y >> 1) * block + (y & 1) * second : int64_t(y) * block;
-    return {o + row * D, reinterpret_cast<const float*>(ml + row)};
+    return {o + int64_t(y) * block * D, reinterpret_cast<const float*>(ml + int64_t(y) * block)};
   }
 };
 
 // Behind the prefixes' grid (griddepcontrol.wait).
 template <int D>
 __device__ __forceinline__ PrefixRows<D> SharedParams::rows(int x, int b, int g, int h) const {
-  PrefixRows<D> r{nullptr, nullptr, 0, 0, 0};
+  PrefixRows<D> r{nullptr, nullptr, 0, 0};
   if (x < 0) return r;
   const int64_t* w = reinterpret_cast<const int64_t*>(recs + x);
   const int64_t unit0 = __ldcg(w), row0 = __ldcg(w + 1), per = __ldcg(w + 2), bc = __ldcg(w + 3), nl = __ldcg(w + 4);
@@ -125,8 +128,7 @@ __device__ __forceinline__ PrefixRows<D> SharedParams::rows(int x, int b, int g,
   r.o = part + row * D;
   r.ml = stat + row;
   r.block = geo.block;
-  r.second = mine.alt ? mine.rows / 2 : 0;
-  r.n = int(c1 - c0 + 1) * (mine.alt ? 2 : 1);
+  r.n = int(c1 - c0 + 1);
   return r;
 }
 
@@ -170,8 +172,9 @@ struct PrefixPlan {
   __device__ __forceinline__ bool init(int cta, bool write) {
     const int lane = threadIdx.x & 31, all = Hkv * p.geo.groups;
     int64_t total = 0;
+    int t = 0, f = 0, c = 0, l = 0;
     for (int x0 = 0; x0 < p.groups.B; x0 += 32) {
-      int t = 0, f, c, l;
+      t = 0;
       if (x0 + lane < p.groups.B) look(x0 + lane, t, f, c, l);
       int64_t u = t > 0 ? prefix_tiles(p.geo, c, t).units * all : 0;
 #pragma unroll
@@ -185,8 +188,10 @@ struct PrefixPlan {
     bool found = false;
     int64_t units = 0, rows = 0;
     for (int x0 = 0; x0 < p.groups.B && (write || !found); x0 += 32) {
-      int t = 0, f = 0, c = 0, l = 0;
-      if (x0 + lane < p.groups.B) look(x0 + lane, t, f, c, l);
+      if (p.groups.B > 32) {  // else they are in hand
+        t = 0;
+        if (x0 + lane < p.groups.B) look(x0 + lane, t, f, c, l);
+      }
       PrefixTiles pt{0, 0, 0};
       if (t > 0) pt = prefix_tiles(p.geo, c, t);
       int64_t u = pt.units * all, r = pt.rows * all;
