@@ -3,14 +3,14 @@
 // is its core, which the including file defines. With SHARED the keys that a
 // group of sequences has in common are left to another grid, and what a warp has
 // of an item goes to a third that joins it all (full_shared.cuh): warps then work
-// alone throughout, each on an equal run of the steps of 16 keys of all items.
+// alone throughout, each on an equal run of the steps (of 16 keys) of all items.
 //
 // Work: the keys of every (sequence, key/value head, group of up to 16 query
 // heads) -- an item -- are cut into units of 128 (16 per warp; 64 for fp32 of d
-// 128, which has four warps), the units of all items are numbered through, and
+// 128, which has four warps; 256 for caches in 8 bits, 32 per warp), the units of all items are numbered through, and
 // each CTA of a fixed grid (one per SM) takes an equal run of them, so ragged
 // lengths balance whatever they are, without the host knowing them.
-// In a unit each warp takes 16 keys, which lie in one page, and works alone:
+// In a unit each warp takes 16 keys, which lie in one page (or two such tiles), and works alone:
 // its own ring of cp.async copies (keys past the end arrive as zeros), scores,
 // running maximum and sum, products. Warps meet only where an item ends in the
 // CTA: their states are joined in shared memory. An item that lies in several
@@ -26,7 +26,7 @@
 namespace msa {
 namespace {
 
-constexpr int kSub = 16, kSubLog2 = 4;    // keys of a warp's step: never across a page
+constexpr int kSub = 16;                  // keys of a tile: never across a page
 constexpr int kFdMaxHeads = 16;           // query heads of an item
 constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
@@ -192,7 +192,7 @@ struct Walk {
   __device__ __forceinline__ void next(const FdParams& p, int hop, int unit_log2) {
     if (++u < n) return;
     u = 0;
-    if constexpr (SOLO) return seek(p, hop, hop);
+    if constexpr (SOLO) return seek(p, hop, hop, unit_log2);
     if (++it < p.Hkv * p.ngr) return;
     it = 0;
     do {
@@ -200,14 +200,14 @@ struct Walk {
     } while (n == 0);
   }
   // To the first item with keys among those `by`, `by` + hop, ... further on.
-  __device__ __forceinline__ void seek(const FdParams& p, int by, int hop) {
+  __device__ __forceinline__ void seek(const FdParams& p, int by, int hop, int step_log2) {
     const int items = p.Hkv * p.ngr;
     do {
       it += by;
       b += it / items;
       it %= items;
       by = hop;
-      n = b < p.B ? arrive(p, kSubLog2) : 1;
+      n = b < p.B ? arrive(p, step_log2) : 1;
     } while (n == 0);
   }
 };
@@ -216,11 +216,16 @@ struct Walk {
 template <typename C>
 struct FdShape {
   static constexpr int kWarps = C::kWarps, kThreads = kWarps * 32;
-  static constexpr int kUnit = kWarps * kSub;  // keys of a unit
+  static constexpr int kStep = C::kTiles * kSub, kUnit = kWarps * kStep;  // keys of a warp's step, of a unit
+  static constexpr int kStepLog2 = C::kTiles == 1 ? 4 : 5, kUnitLog2 = kStepLog2 + (kWarps == 8 ? 3 : 2);
+  static_assert(1 << kStepLog2 == kStep && 1 << kUnitLog2 == kUnit, "keys of a step and of a unit");
   static constexpr int kStages = C::kStages;
   static constexpr int kRing = kStages * C::kStage;      // per warp
   static constexpr int kState = (C::kAcc + 2 * C::kM + 1) * 32;  // floats of a warp's state
-  static constexpr int kJoin = (kWarps - 1) * kState * 4;        // a slot per hand-over
+  // A slot per hand-over, but that the last of three takes the slot that its
+  // warp read itself: it is not written again before the next item's first barrier.
+  static constexpr int kSlots = kWarps == 8 ? 6 : kWarps - 1;
+  static constexpr int kJoin = kSlots * kState * 4;
   static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
 };
 
@@ -231,7 +236,7 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
-  constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads, kUnit = SH::kUnit;
+  constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
   extern __shared__ __align__(128) uint8_t fd_smem[];
   __shared__ int last_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -241,11 +246,9 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   const int items = p.Hkv * p.ngr;
   T* out = static_cast<T*>(p.out);
 
-  constexpr int kUnitLog2 = kUnit == 64 ? 6 : 7;
-  static_assert(1 << kUnitLog2 == kUnit, "keys of a unit");
   constexpr bool ALONE = SOLO || SHARED;
-  constexpr int ulog = ALONE ? kSubLog2 : kUnitLog2;
-  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * kSub;
+  constexpr int ulog = ALONE ? SH::kStepLog2 : SH::kUnitLog2;
+  const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * SH::kStep;
   // runs in the order of the SMs, so that few of them lie on many
   const int runs = int(gridDim.x) * (SHARED ? kFdWarps : 1), run = SHARED ? warp * int(gridDim.x) + int(blockIdx.x) : int(blockIdx.x);
   int64_t per = (total + runs - 1) / runs;
@@ -256,7 +259,7 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   int64_t first = 0;  // number of the walk's sequence's first unit
   int64_t item_first = 0;  // number of the item's first unit
   if constexpr (SOLO) {
-    at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop);
+    at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop, ulog);
   } else {
     int ahead = lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -288,23 +291,33 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   Walk<SHARED> ld = at;
   int64_t ld_left = !SOLO || ld.b < p.B ? run1 - run0 : 0;
   uint32_t bad_ring = 0;  // stage x's page was out of range
-  auto page_of = [&](const Walk<SHARED>& w) {
+  int page[C::kTiles];
+  auto pages_of = [&](const Walk<SHARED>& w) {
     const int key = w.from() + (w.u << ulog) + sub0;
-    return key < w.len(p) ? p.pages.table[int64_t(w.b) * p.pages.max_pages + (key >> p.pages.page_log2)] : 0;
+#pragma unroll
+    for (int x = 0; x < C::kTiles; ++x)
+      page[x] = key + x * kSub < w.len(p)
+                    ? p.pages.table[int64_t(w.b) * p.pages.max_pages + ((key + x * kSub) >> p.pages.page_log2)]
+                    : 0;
   };
-  int page = ld_left > 0 ? page_of(ld) : 0;
+  if (ld_left > 0) pages_of(ld);
   auto issue = [&](int st) {
     if (ld_left > 0) {
-      const int key = ld.from() + (ld.u << ulog) + sub0;
-      const int valid = ld.len(p) - key;
-      const bool bad = valid > 0 && (page < 0 || page >= p.pages.num_pages);
-      bad_ring = bad ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
-      C::copy(p, ring + st * C::kStage, bad || valid <= 0 ? 0 : page, key & ((1 << p.pages.page_log2) - 1), ld.it / p.ngr,
-              bad ? 0 : valid);
+      const int key0 = ld.from() + (ld.u << ulog) + sub0;
+      bool spoilt = false;
+#pragma unroll
+      for (int x = 0; x < C::kTiles; ++x) {
+        const int key = key0 + x * kSub, valid = ld.len(p) - key;
+        const bool bad = valid > 0 && (page[x] < 0 || page[x] >= p.pages.num_pages);
+        spoilt |= bad;
+        C::copy(p, ring + st * C::kStage + x * (C::kStage / C::kTiles), bad || valid <= 0 ? 0 : page[x],
+                key & ((1 << p.pages.page_log2) - 1), ld.it / p.ngr, bad ? 0 : valid);
+      }
+      bad_ring = spoilt ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
       if (--ld_left > 0) {
         ld.template next<SOLO>(p, hop, ulog);
         if (!SOLO || ld.b < p.B)
-          page = page_of(ld);
+          pages_of(ld);
         else
           ld_left = 0;
       }
@@ -373,6 +386,7 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     if constexpr (!ALONE) {
 #pragma unroll
       for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
+        if (half == 1) slot0 = SH::kSlots - 1;
         if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
         __syncthreads();
         if (warp < half) take(join + (slot0 + warp) * SH::kState);
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   int longest = 0;  // in warps' steps
 #pragma unroll 8
   for (int b = lane; b < p.B; b += 32) {
-    const int steps = units_of<SHARED>(p, b, kSubLog2);
+    const int steps = units_of<SHARED>(p, b, SH::kStepLog2);
     total += SHARED ? steps : (steps + kFdWarps - 1) / kFdWarps;
     longest = max(longest, steps);
   }
@@ -493,7 +507,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   if constexpr (!SHARED) {  // sequences without keys: nobody's run holds them
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
       const Own o = own_of<false>(p, b);
-      if (o.units(kSubLog2) > 0) continue;
+      if (o.units(SH::kStepLog2) > 0) continue;
       if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
       for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
       if (p.lse)

@@ -38,7 +38,7 @@ struct Core;
 template <int D, int H>
 struct Core<__nv_bfloat16, D, H> {
   using T = __nv_bfloat16;
-  static constexpr int kD = D, kWarps = 8, kStages = D == 64 ? (H <= 8 ? 6 : 4) : H <= 8 ? 3 : 2;
+  static constexpr int kD = D, kTiles = 1, kWarps = 8, kStages = D == 64 ? (H <= 8 ? 6 : 4) : H <= 8 ? 3 : 2;
   static constexpr int HN = (H + 7) / 8;
   static constexpr int kRow = D * 2, kTile = kSub * kRow, kStage = 2 * kTile, kExtra = 0;
   static constexpr int kM = 2 * HN, kAcc = HN * D / 4;
@@ -168,7 +168,7 @@ template <int D, int H>
 struct Core<float, D, H> {
   using T = float;
   static constexpr bool kWide = D == 128;
-  static constexpr int kD = D, kWarps = kWide ? 4 : 8, kStages = kWide ? 2 : H <= 4 ? 3 : 2;
+  static constexpr int kD = D, kTiles = 1, kWarps = kWide ? 4 : 8, kStages = kWide ? 2 : H <= 4 ? 3 : 2;
   static constexpr int P = D / 32;
   static constexpr int kRow = D * 4, kTile = kSub * kRow, kStage = 2 * kTile;
   static constexpr int kExtra = (H * D + kSub * H) * 4;  // per warp: queries, weights

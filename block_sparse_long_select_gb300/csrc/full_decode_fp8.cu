@@ -46,6 +46,11 @@ __device__ __forceinline__ uint32_t high2(uint32_t x) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(y) : "r"(x));
   return y;
 }
+__device__ __forceinline__ float lg2(float x) {  // -inf of 0
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
@@ -74,10 +79,11 @@ __device__ __forceinline__ float lds1(uint32_t a) {
 template <typename T_, int D, int H>
 struct Core8 {
   using T = T_;
-  static constexpr int kD = D, kWarps = 8, kStages = D == 64 ? 8 : H <= 8 ? 5 : 4;
+  static constexpr int kD = D, kWarps = 8, kTiles = 2, kStages = D == 64 ? 4 : H <= 8 ? 3 : 2;
   static constexpr int HN = (H + 7) / 8, kTerms = sizeof(T) == 4 ? 2 : 1;
-  // K codes | V codes | 16 K scales | 16 V scales
-  static constexpr int kTile = kSub * D, kScales = 2 * kTile, kStage = 2 * kTile + 2 * kSub * 4, kExtra = 0;
+  // two of: K codes | V codes | 16 K scales | 16 V scales
+  static constexpr int kTile = kSub * D, kScales = 2 * kTile, kTileStage = 2 * kTile + 2 * kSub * 4;
+  static constexpr int kStage = kTiles * kTileStage, kExtra = 0;
   static constexpr int kM = 2 * HN, kAcc = HN * D / 4, kWords = D / 16;  // 4-byte words of a lane's quarter of a row
   uint32_t qf[HN][kTerms][kWords][2];
   float qs[kM];  // the scores' factors: scale, log2 e and the queries' power of two
@@ -157,41 +163,52 @@ struct Core8 {
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
-  __device__ __forceinline__ void step(uint32_t kt, uint32_t, int valid, float) {
+  __device__ __forceinline__ void step(uint32_t stage, uint32_t, int valid, float) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const uint32_t vt = kt + kTile, sc = kt + kScales;
-    float s[HN][4];
+    float s[kTiles][HN][4], lv[kTiles][2];
 #pragma unroll
-    for (int t = 0; t < HN; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    for (int i = 0; i < kTiles; ++i) {
+      const uint32_t kt = stage + i * kTileStage, sc = kt + kScales;
 #pragma unroll
-    for (int c = 0; c < kWords / 4; ++c) {  // keys gq and gq + 8
-      const uint4 lo = lds16(at(kt, gq, tq * (kWords / 4) + c)), hi = lds16(at(kt, gq + 8, tq * (kWords / 4) + c));
-      const uint32_t r0[4] = {lo.x, lo.y, lo.z, lo.w}, r1[4] = {hi.x, hi.y, hi.z, hi.w};
+      for (int t = 0; t < HN; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a[4] = {low2(r0[w]), low2(r1[w]), high2(r0[w]), high2(r1[w])};
+      for (int c = 0; c < kWords / 4; ++c) {  // keys gq and gq + 8
+        const uint4 lo = lds16(at(kt, gq, tq * (kWords / 4) + c)), hi = lds16(at(kt, gq + 8, tq * (kWords / 4) + c));
+        const uint32_t r0[4] = {lo.x, lo.y, lo.z, lo.w}, r1[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int t = 0; t < HN; ++t)
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a[4] = {low2(r0[w]), low2(r1[w]), high2(r0[w]), high2(r1[w])};
 #pragma unroll
-          for (int y = 0; y < kTerms; ++y) mma16816h(s[t], a, qf[t][y][c * 4 + w][0], qf[t][y][c * 4 + w][1]);
+          for (int t = 0; t < HN; ++t)
+#pragma unroll
+            for (int y = 0; y < kTerms; ++y) mma16816h(s[i][t], a, qf[t][y][c * 4 + w][0], qf[t][y][c * 4 + w][1]);
+        }
       }
+      const float ks[2] = {lds1(sc + gq * 4), lds1(sc + gq * 4 + 32)};
+      lv[i][0] = lg2(lds1(sc + 64 + gq * 4));
+      lv[i][1] = lg2(lds1(sc + 64 + gq * 4 + 32));
+#pragma unroll
+      for (int t = 0; t < HN; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[i][t][e] = i * kSub + gq + 8 * (e >> 1) < valid ? s[i][t][e] * qs[2 * t + (e & 1)] * ks[e >> 1] : -INFINITY;
     }
-    const float ks[2] = {lds1(sc + gq * 4), lds1(sc + gq * 4 + 32)};
-    const float lv[2] = {log2f(lds1(sc + 64 + gq * 4)), log2f(lds1(sc + 64 + gq * 4 + 32))};
     float mt[kM], mv[kM];
     bool up = false;
 #pragma unroll
-    for (int t = 0; t < HN; ++t) {
+    for (int x = 0; x < kM; ++x) {
+      const int t = x >> 1, e = x & 1;
+      mt[x] = fmaxf(s[0][t][e], s[0][t][2 + e]);
+      mv[x] = fmaxf(s[0][t][e] + lv[0][0], s[0][t][2 + e] + lv[0][1]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = gq + 8 * (e >> 1) < valid ? s[t][e] * qs[2 * t + (e & 1)] * ks[e >> 1] : -INFINITY;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * t + x;
-        mt[i] = qmax(fmaxf(s[t][x], s[t][2 + x]));
-        mv[i] = qmax(fmaxf(s[t][x] + lv[0], s[t][2 + x] + lv[1])) - kTop;
-        up |= mt[i] > m[i] + kFdLazy || (m[i] == -INFINITY && mt[i] > -INFINITY);
-        up |= mv[i] > mw[i] + kFdLazy || (mw[i] == -INFINITY && mv[i] > -INFINITY);
+      for (int i = 1; i < kTiles; ++i) {
+        mt[x] = tc::fmax3(mt[x], s[i][t][e], s[i][t][2 + e]);
+        mv[x] = tc::fmax3(mv[x], s[i][t][e] + lv[i][0], s[i][t][2 + e] + lv[i][1]);
       }
+      mt[x] = qmax(mt[x]);
+      mv[x] = qmax(mv[x]) - kTop;
+      up |= mt[x] > m[x] + kFdLazy || (m[x] == -INFINITY && mt[x] > -INFINITY);
+      up |= mv[x] > mw[x] + kFdLazy || (mw[x] == -INFINITY && mv[x] > -INFINITY);
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -208,48 +225,52 @@ struct Core8 {
         }
       }
     }
-    uint32_t b[HN][kTerms][2];
 #pragma unroll
-    for (int t = 0; t < HN; ++t) {
-      float w[4];
+    for (int i = 0; i < kTiles; ++i) {
+      const uint32_t vt = stage + i * kTileStage + kTile;
+      uint32_t b[HN][kTerms][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 2 * t + (e & 1);
-        l[i] += ex2d(s[t][e] - (m[i] == -INFINITY ? 0.f : m[i]));
-        w[e] = ex2d((s[t][e] - (mw[i] == -INFINITY ? 0.f : mw[i])) + lv[e >> 1]);
+      for (int t = 0; t < HN; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 2 * t + (e & 1);
+          l[x] += ex2d(s[i][t][e] - (m[x] == -INFINITY ? 0.f : m[x]));
+          w[e] = ex2d((s[i][t][e] - (mw[x] == -INFINITY ? 0.f : mw[x])) + lv[i][e >> 1]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t hi = pack_f16(w[2 * y], w[2 * y + 1]);
+          b[t][0][y] = trans8(hi);
+          if constexpr (kTerms == 2) b[t][1][y] = trans8(rest_f16(hi, w[2 * y], w[2 * y + 1]));
+        }
+      }
+      // lane (gq, tq): keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, dims [gq D / 8, ...)
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int r = 2 * tq + (y & 1) + 8 * (y >> 1);
+        if constexpr (D == 128) {
+          const uint4 f = lds16(at(vt, r, gq));
+          v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+        } else {
+          const uint2 f = lds8(at(vt, r, gq >> 1) + (gq & 1) * 8);
+          v[y][0] = f.x, v[y][1] = f.y;
+        }
       }
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const uint32_t hi = pack_f16(w[2 * y], w[2 * y + 1]);
-        b[t][0][y] = trans8(hi);
-        if constexpr (kTerms == 2) b[t][1][y] = trans8(rest_f16(hi, w[2 * y], w[2 * y + 1]));
-      }
-    }
-    // lane (gq, tq): keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, dims [gq D / 8, ...)
-    uint32_t v[4][D / 32];
+      for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int r = 2 * tq + (y & 1) + 8 * (y >> 1);
-      if constexpr (D == 128) {
-        const uint4 f = lds16(at(vt, r, gq));
-        v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
-      } else {
-        const uint2 f = lds8(at(vt, r, gq >> 1) + (gq & 1) * 8);
-        v[y][0] = f.x, v[y][1] = f.y;
-      }
-    }
+        for (int y = 0; y < 2; ++y) {  // dims 4 w + 2 y (rows gq of the product) and 4 w + 2 y + 1 (rows gq + 8)
+          const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+          const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+          const uint32_t a[4] = {low2(lo), high2(lo), low2(hi), high2(hi)};
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
+          for (int t = 0; t < HN; ++t) {
+            float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[(t * (D / 16) + 2 * w + y) * 4]);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {  // dims 4 w + 2 y (rows gq of the product) and 4 w + 2 y + 1 (rows gq + 8)
-        const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
-        const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-        const uint32_t a[4] = {low2(lo), high2(lo), low2(hi), high2(hi)};
-#pragma unroll
-        for (int t = 0; t < HN; ++t) {
-          float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[(t * (D / 16) + 2 * w + y) * 4]);
-#pragma unroll
-          for (int z = 0; z < kTerms; ++z) mma16816h(c, a, b[t][z][0], b[t][z][1]);
+            for (int z = 0; z < kTerms; ++z) mma16816h(c, a, b[t][z][0], b[t][z][1]);
+          }
         }
       }
     }
