@@ -11,8 +11,8 @@
 // each CTA of a fixed grid (one per SM) takes an equal run of them, so ragged
 // lengths balance whatever they are, without the host knowing them.
 // In a unit each warp takes 16 keys, which lie in one page (or two such tiles), and works alone:
-// its own ring of cp.async copies (keys past the end arrive as zeros), scores,
-// running maximum and sum, products. Warps meet only where an item ends in the
+// its own ring of copies (cp.async, keys past the end arriving as zeros, or TMA
+// with bounded waits), scores, running maximum and sum, products. Warps meet only where an item ends in the
 // CTA: their states are joined in shared memory. An item that lies in several
 // CTAs leaves a partial (maximum, sum, unnormalised output) per CTA, and the
 // CTA that arrives last joins them in the order of the keys.
@@ -179,13 +179,11 @@ __device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D,
 // A walk over units in order: those of a CTA's run, or (SOLO) of every hop-th item.
 template <bool SHARED>
 struct Walk {
-  int b, it, u, n;  // sequence, item within it, unit within the item, units of the item
-  Own own;          // the sequence's keys; SHARED only (else they are read again: registers are dearer)
-  __device__ __forceinline__ int len(const FdParams& p) const { return SHARED ? own.L : p.kv_len[b]; }
+  int b, g, hg, u, n;  // sequence, key/value head, head group, unit within the item, units of the item
+  Own own;             // the sequence's keys
   __device__ __forceinline__ int from() const { return SHARED ? own.from : 0; }
   __device__ __forceinline__ int arrive(const FdParams& p, int unit_log2) {  // at sequence b: its units
-    if constexpr (!SHARED) return units_of<false>(p, b, unit_log2);
-    own = own_of<true>(p, b);
+    own = own_of<SHARED>(p, b);
     return own.units(unit_log2);
   }
   template <bool SOLO>
@@ -193,8 +191,10 @@ struct Walk {
     if (++u < n) return;
     u = 0;
     if constexpr (SOLO) return seek(p, hop, hop, unit_log2);
-    if (++it < p.Hkv * p.ngr) return;
-    it = 0;
+    if (++hg < p.ngr) return;
+    hg = 0;
+    if (++g < p.Hkv) return;
+    g = 0;
     do {
       n = ++b < p.B ? arrive(p, unit_log2) : 1;  // past the last sequence the walk is over
     } while (n == 0);
@@ -202,6 +202,7 @@ struct Walk {
   // To the first item with keys among those `by`, `by` + hop, ... further on.
   __device__ __forceinline__ void seek(const FdParams& p, int by, int hop, int step_log2) {
     const int items = p.Hkv * p.ngr;
+    int it = g * p.ngr + hg;
     do {
       it += by;
       b += it / items;
@@ -209,6 +210,8 @@ struct Walk {
       by = hop;
       n = b < p.B ? arrive(p, step_log2) : 1;
     } while (n == 0);
+    g = it / p.ngr;
+    hg = it % p.ngr;
   }
 };
 
@@ -224,21 +227,27 @@ struct FdShape {
   static constexpr int kState = (C::kAcc + 2 * C::kM + 1) * 32;  // floats of a warp's state
   // A slot per hand-over, but that the last of three takes the slot that its
   // warp read itself: it is not written again before the next item's first barrier.
-  static constexpr int kSlots = kWarps == 8 ? 6 : kWarps - 1;
-  static constexpr int kJoin = kSlots * kState * 4;
-  static constexpr int kBytes = kWarps * (kRing + C::kExtra) + kJoin;
+  // Bulk copies: the values go through the stage just used, which is not filled
+  // again before a barrier, and only the rest through a slot per warp.
+  static constexpr int kSlots = kWarps == 8 ? 6 : kWarps - 1, kRest = (2 * C::kM + 1) * 32;
+  static constexpr int kJoin = C::kBulk ? kWarps * kRest * 4 : kSlots * kState * 4;
+  static_assert(!C::kBulk || C::kAcc * 128 <= C::kStage, "a stage holds a warp's values");
+  // barriers of the copies' stages, one that nothing completes; two flags
+  static constexpr int kBars = C::kBulk ? (kWarps * kStages + 1) * 8 : 0;
+  static constexpr int kFlags = kWarps * (kRing + C::kExtra) + kJoin + kBars;
+  static constexpr int kBytes = kFlags + 16;
 };
 
 // SOLO: whole items for single warps; SHARED: the warp's run of the `total` steps
 // of 16 keys; else the CTA's run of the `total` units.
 template <typename C, bool SOLO, bool SHARED>
-__device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
+__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
   constexpr int NS = SH::kStages, kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
-  extern __shared__ __align__(128) uint8_t fd_smem[];
-  __shared__ int last_s;
+  extern __shared__ __align__(1024) uint8_t fd_smem[];
+  int& last_s = *reinterpret_cast<int*>(fd_smem + SH::kFlags);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = tc::smem_u32(fd_smem) + warp * SH::kRing;
   const uint32_t extra = tc::smem_u32(fd_smem) + kFdWarps * SH::kRing + warp * C::kExtra;
@@ -281,10 +290,12 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
       }
       first += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if constexpr (SHARED) at.own = own_of<true>(p, at.b);
-    at.it = int((run0 - first) / at.n);
+    at.own = own_of<SHARED>(p, at.b);
+    const int it = int((run0 - first) / at.n);
+    at.g = it / p.ngr;
+    at.hg = it % p.ngr;
     at.u = int((run0 - first) % at.n);
-    item_first = first + int64_t(at.it) * at.n;
+    item_first = first + int64_t(it) * at.n;
   }
 
   // ---- copies: the walk `ld` runs ahead of `at` ----
@@ -296,22 +307,52 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     const int key = w.from() + (w.u << ulog) + sub0;
 #pragma unroll
     for (int x = 0; x < C::kTiles; ++x)
-      page[x] = key + x * kSub < w.len(p)
+      page[x] = key + x * kSub < w.own.L
                     ? p.pages.table[int64_t(w.b) * p.pages.max_pages + ((key + x * kSub) >> p.pages.page_log2)]
                     : 0;
   };
   if (ld_left > 0) pages_of(ld);
+  [[maybe_unused]] uint64_t* bars = reinterpret_cast<uint64_t*>(fd_smem + SH::kFlags - SH::kBars) + warp * NS;
+  [[maybe_unused]] volatile int* abort_flag = &last_s + 1;
+  [[maybe_unused]] int64_t issued = 0, landed = 0;  // bulk copies' stages
+  if constexpr (C::kBulk) {
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x < NS; ++x) tc::mbar_init(bars + x, 1);
+      tc::fence_barrier_init();
+    }
+    __syncwarp();
+  }
   auto issue = [&](int st) {
     if (ld_left > 0) {
-      const int key0 = ld.from() + (ld.u << ulog) + sub0;
-      bool spoilt = false;
+      const int key0 = ld.from() + (ld.u << ulog) + sub0, g = ld.g;
+      bool spoilt = false, in[C::kTiles];
 #pragma unroll
       for (int x = 0; x < C::kTiles; ++x) {
-        const int key = key0 + x * kSub, valid = ld.len(p) - key;
+        const int valid = ld.own.L - key0 - x * kSub;
         const bool bad = valid > 0 && (page[x] < 0 || page[x] >= p.pages.num_pages);
         spoilt |= bad;
-        C::copy(p, ring + st * C::kStage + x * (C::kStage / C::kTiles), bad || valid <= 0 ? 0 : page[x],
-                key & ((1 << p.pages.page_log2) - 1), ld.it / p.ngr, bad ? 0 : valid);
+        in[x] = valid > 0 && !bad;
+        if constexpr (!C::kBulk)
+          C::copy(p, ring + st * C::kStage + x * (C::kStage / C::kTiles), in[x] ? page[x] : 0,
+                  (key0 + x * kSub) & ((1 << p.pages.page_log2) - 1), g, in[x] ? valid : 0);
+      }
+      if constexpr (C::kBulk) {
+        if (lane == 0) {
+          int tiles = 0;
+#pragma unroll
+          for (int x = 0; x < C::kTiles; ++x) tiles += in[x];
+          if (tiles)
+            tc::mbar_arrive_expect_tx(bars + st, tiles * C::kTileBytes);
+          else
+            tc::mbar_arrive(bars + st);
+#pragma unroll
+          for (int x = 0; x < C::kTiles; ++x)
+            if (in[x])
+              C::copy(p, ring, extra, st * C::kTiles + x, bars + st, page[x],
+                      (key0 + x * kSub) & ((1 << p.pages.page_log2) - 1), g);
+        }
+        ++issued;
       }
       bad_ring = spoilt ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
       if (--ld_left > 0) {
@@ -322,7 +363,7 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
           ld_left = 0;
       }
     }
-    cp_commit_group();
+    if constexpr (!C::kBulk) cp_commit_group();
   };
 #pragma unroll
   for (int st = 0; st < NS - 1; ++st) issue(st);
@@ -330,20 +371,39 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
   C c;
   bool fresh = true, bad = false;
   int st = 0;
+  [[maybe_unused]] uint32_t parity = 0;
+  [[maybe_unused]] bool dead = false;  // a wait ran out: nothing more is copied or read, but everybody is met
+  if constexpr (C::kBulk) {
+    if (p.inject_timeout && blockIdx.x % 2 == 0 && warp == 0)
+      dead = !tc::mbar_wait_for(reinterpret_cast<uint64_t*>(fd_smem + SH::kFlags) - 1, 0, abort_flag, tc::kInjectedWaitCycles);
+  }
+  int h0 = 0, heads = 0;
   for (int64_t z = run0; z < run1 && (!SOLO || at.b < p.B); ++z) {
-    const int g = at.it / p.ngr, h0 = g * p.hpg + (at.it % p.ngr) * kFdMaxHeads;
-    const int heads = min(p.hpg - (at.it % p.ngr) * kFdMaxHeads, kFdMaxHeads);
-    const int L = at.len(p);
     if (fresh) {
+      h0 = at.g * p.hpg + at.hg * kFdMaxHeads;
+      heads = min(p.hpg - at.hg * kFdMaxHeads, kFdMaxHeads);
       c.start(p, static_cast<const T*>(p.q) + (int64_t(at.b) * p.Hq + h0) * D, heads, extra);
       fresh = bad = false;
     }
-    issue((st + NS - 1) % NS);
-    cp_wait<NS - 1>();
-    __syncwarp();
+    if constexpr (C::kBulk) {
+      if (!dead) {
+        issue((st + NS - 1) % NS);
+        dead = !__all_sync(0xffffffffu, tc::mbar_wait(bars + st, parity, abort_flag));
+        if (dead)
+          *abort_flag = 1;
+        else
+          ++landed;
+      }
+      if (st == NS - 1) parity ^= 1;
+    } else {
+      issue((st + NS - 1) % NS);
+      cp_wait<NS - 1>();
+      __syncwarp();
+    }
     bad |= (bad_ring >> st) & 1u;
-    const int valid = L - (at.from() + (at.u << ulog) + sub0);
-    if (valid > 0) c.step(ring + st * C::kStage, extra, valid, p.scale_log2);
+    int valid = at.own.L - (at.from() + (at.u << ulog) + sub0);
+    if (C::kBulk && dead) valid = 0;
+    if (valid > 0) c.step(ring + st * C::kStage, extra, st, valid, p.scale_log2);
     __syncwarp();
     st = (st + 1) % NS;
     const int b = at.b, n = at.n;
@@ -355,46 +415,57 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     // ---- the item ends here: join the warps' states, halving their number ----
     fresh = true;
     c.finish();
-    constexpr int kRegs = C::kAcc + 2 * C::kM + 1;
-    auto put = [&](float* to) {
+    // values to or from v, maxima, sums and whether a page was out of range to or from r
+    auto put = [&](float* v, float* r) {
 #pragma unroll
-      for (int x = 0; x < C::kAcc; ++x) to[x * 32 + lane] = c.acc[x];
+      for (int x = 0; x < C::kAcc; ++x) v[x * 32 + lane] = c.acc[x];
 #pragma unroll
       for (int x = 0; x < C::kM; ++x) {
-        to[(C::kAcc + x) * 32 + lane] = c.m[x];
-        to[(C::kAcc + C::kM + x) * 32 + lane] = c.l[x];
+        r[x * 32 + lane] = c.m[x];
+        r[(C::kM + x) * 32 + lane] = c.l[x];
       }
-      to[(kRegs - 1) * 32 + lane] = bad ? 1.f : 0.f;
+      r[2 * C::kM * 32 + lane] = bad ? 1.f : 0.f;
     };
-    auto take = [&](const float* from) {
+    auto take = [&](const float* v, const float* r) {
       float wa[C::kM], wb[C::kM];
 #pragma unroll
       for (int x = 0; x < C::kM; ++x) {
-        const float mo = from[(C::kAcc + x) * 32 + lane], mn = fmaxf(c.m[x], mo);
+        const float mo = r[x * 32 + lane], mn = fmaxf(c.m[x], mo);
         wa[x] = c.m[x] == mn ? 1.f : ex2d(c.m[x] - mn);
         wb[x] = mo == mn ? 1.f : ex2d(mo - mn);
         c.m[x] = mn;
-        c.l[x] = c.l[x] * wa[x] + from[(C::kAcc + C::kM + x) * 32 + lane] * wb[x];
+        c.l[x] = c.l[x] * wa[x] + r[(C::kM + x) * 32 + lane] * wb[x];
       }
 #pragma unroll
       for (int x = 0; x < C::kAcc; ++x)
-        c.acc[x] = c.acc[x] * wa[C::m_index(x)] + from[x * 32 + lane] * wb[C::m_index(x)];
-      bad |= from[(kRegs - 1) * 32 + lane] != 0.f;
+        c.acc[x] = c.acc[x] * wa[C::m_index(x)] + v[x * 32 + lane] * wb[C::m_index(x)];
+      bad |= r[2 * C::kM * 32 + lane] != 0.f;
     };
-    // Every hand-over has a slot of its own: the upper warps may be at the next
-    // item's end while the lower ones still read this one's.
-    if constexpr (!ALONE) {
+    if constexpr (!ALONE && C::kBulk) {
+      float* mine = reinterpret_cast<float*>(fd_smem + warp * SH::kRing + (st == 0 ? NS - 1 : st - 1) * C::kStage);
+#pragma unroll
+      for (int half = kFdWarps / 2; half > 0; half >>= 1) {
+        if (warp >= half && warp < 2 * half) put(mine, join + warp * SH::kRest);
+        __syncthreads();
+        if (warp < half) take(mine + half * (SH::kRing / 4), join + (warp + half) * SH::kRest);
+      }
+      tc::fence_proxy_async_smem();  // before the next copy into the stage
+      __syncthreads();
+    } else if constexpr (!ALONE) {
+      // Every hand-over has a slot of its own: the upper warps may be at the next
+      // item's end while the lower ones still read this one's.
 #pragma unroll
       for (int half = kFdWarps / 2, slot0 = 0; half > 0; slot0 += half, half >>= 1) {
         if (half == 1) slot0 = SH::kSlots - 1;
-        if (warp >= half && warp < 2 * half) put(join + (slot0 + warp - half) * SH::kState);
+        float* slot = join + (slot0 + warp % half) * SH::kState;
+        if (warp >= half && warp < 2 * half) put(slot, slot + C::kAcc * 32);
         __syncthreads();
-        if (warp < half) take(join + (slot0 + warp) * SH::kState);
+        if (warp < half) take(slot, slot + C::kAcc * 32);
       }
     }
     const bool whole = SOLO || (item_first >= run0 && ends);
     // SHARED: parts in the order of the items, those of one item in the order of the runs
-    const int item = at.b * items + at.it, item_heads = SHARED ? min(p.hpg, kFdMaxHeads) : kFdMaxHeads;
+    const int item = at.b * items + at.g * p.ngr + at.hg, item_heads = SHARED ? min(p.hpg, kFdMaxHeads) : kFdMaxHeads;
     const int slot = SHARED ? item + run : 2 * run + (item_first >= run0 ? 1 : 0);
     if (ALONE || warp == 0) {
       c.sum_l();
@@ -462,11 +533,19 @@ __device__ __forceinline__ void decode_run(const FdParams& p, int64_t total) {
     at.template next<SOLO>(p, hop, ulog);
     if (at.b != was) item_first = z + 1;
   }
-  cp_wait<0>();
+  if constexpr (C::kBulk) {
+    if (dead && issued > 0) {  // let the copies land before the CTA gives its shared memory up
+      if (lane == 0) set_status(p.status, MSA_ERR_TIMEOUT);
+      int zero = 0;
+      for (int64_t x = landed; x < issued; ++x) tc::mbar_wait(bars + x % NS, uint32_t(x / NS) & 1, &zero);
+    }
+  } else {
+    cp_wait<0>();
+  }
 }
 
 template <typename C, bool SHARED>
-__global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(const FdParams p) {
+__global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(const __grid_constant__ typename C::Params p) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
@@ -479,6 +558,21 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
       tc::griddep_wait();
       return;
     }
+  }
+
+  if constexpr (C::kBulk) {
+    extern __shared__ __align__(1024) uint8_t fd_smem[];
+    if (tc::smem_u32(fd_smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+      if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
+      return;
+    }
+    if (threadIdx.x == 0) {
+      tc::mbar_init(reinterpret_cast<uint64_t*>(fd_smem + SH::kFlags) - 1, 1);
+      reinterpret_cast<int*>(fd_smem + SH::kFlags)[1] = 0;  // no wait has run out
+      tc::fence_barrier_init();
+      C::prefetch(p);
+    }
+    __syncthreads();
   }
 
   // ---- all units (every warp counts alone) ----
@@ -525,7 +619,7 @@ int fd_grid() { return kNumSMs; }
 
 // SHARED: the grid may start while the one before it ends
 template <typename C, bool SHARED>
-cudaError_t decode(const FdParams& p, const char* name, cudaStream_t stream) {
+cudaError_t decode(const typename C::Params& p, const char* name, cudaStream_t stream) {
   auto kern = full_decode_kernel<C, SHARED>;
   constexpr int bytes = FdShape<C>::kBytes;
   static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");

@@ -38,6 +38,8 @@ struct Core;
 template <int D, int H>
 struct Core<__nv_bfloat16, D, H> {
   using T = __nv_bfloat16;
+  using Params = FdParams;
+  static constexpr bool kBulk = false;
   static constexpr int kD = D, kTiles = 1, kWarps = 8, kStages = D == 64 ? (H <= 8 ? 6 : 4) : H <= 8 ? 3 : 2;
   static constexpr int HN = (H + 7) / 8;
   static constexpr int kRow = D * 2, kTile = kSub * kRow, kStage = 2 * kTile, kExtra = 0;
@@ -64,7 +66,7 @@ struct Core<__nv_bfloat16, D, H> {
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
-  __device__ __forceinline__ void step(uint32_t kt, uint32_t, int valid, float scale_log2) {
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t, int, int valid, float scale_log2) {
     const int lane = threadIdx.x & 31, gq = lane >> 2;
     const uint32_t vt = kt + kTile;
     float s[HN][4];
@@ -168,6 +170,8 @@ template <int D, int H>
 struct Core<float, D, H> {
   using T = float;
   static constexpr bool kWide = D == 128;
+  using Params = FdParams;
+  static constexpr bool kBulk = false;
   static constexpr int kD = D, kTiles = 1, kWarps = kWide ? 4 : 8, kStages = kWide ? 2 : H <= 4 ? 3 : 2;
   static constexpr int P = D / 32;
   static constexpr int kRow = D * 4, kTile = kSub * kRow, kStage = 2 * kTile;
@@ -196,7 +200,7 @@ struct Core<float, D, H> {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
   }
-  __device__ __forceinline__ void step(uint32_t kt, uint32_t extra, int valid, float scale_log2) {
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t extra, int, int valid, float scale_log2) {
     const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
     const uint32_t vt = kt + kTile, ps = extra + H * D * 4;
     float s[H];

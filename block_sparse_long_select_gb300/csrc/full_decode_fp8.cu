@@ -46,9 +46,9 @@ __device__ __forceinline__ uint32_t high2(uint32_t x) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float lg2(float x) {  // -inf of 0
+__device__ __forceinline__ float lg2(float x) {  // -inf of 0 and of what is below 2^-126
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -76,61 +76,78 @@ __device__ __forceinline__ float lds1(uint32_t a) {
   return v;
 }
 
-template <typename T_, int D, int H>
+struct Fd8Params : FdParams {
+  CUtensorMap tmK, tmV;  // codes as [rows][Hkv][d] bytes, boxes of 16 rows of a head
+  int kv_heads, group;   // key/value heads, query heads of one: what Hkv and hpg say of pairs where those are items
+  int inject_timeout;    // test hook: a warp of every second CTA waits on a barrier nothing completes
+};
+
+// H: most query heads of a key/value head in an item; KT: tiles of 16 keys in a
+// step; HT: key/value heads in an item, 2 where there is an even number of them.
+// Neighbouring heads' rows lie together in memory, and 256 bytes at a time come
+// from HBM faster than 128 (8 key/value heads, d 128: 6.6 TB/s instead of 5.4).
+template <typename T_, int D, int H, int KT, int HT>
 struct Core8 {
   using T = T_;
-  static constexpr int kD = D, kWarps = 8, kTiles = 2, kStages = D == 64 ? 4 : H <= 8 ? 3 : 2;
-  static constexpr int HN = (H + 7) / 8, kTerms = sizeof(T) == 4 ? 2 : 1;
-  // two of: K codes | V codes | 16 K scales | 16 V scales
-  static constexpr int kTile = kSub * D, kScales = 2 * kTile, kTileStage = 2 * kTile + 2 * kSub * 4;
-  static constexpr int kStage = kTiles * kTileStage, kExtra = 0;
-  static constexpr int kM = 2 * HN, kAcc = HN * D / 4, kWords = D / 16;  // 4-byte words of a lane's quarter of a row
-  uint32_t qf[HN][kTerms][kWords][2];
+  using Params = Fd8Params;
+  static constexpr bool kBulk = true;
+  static constexpr int kD = D, kWarps = 8, kTiles = KT;
+  static constexpr int HN = (H + 7) / 8, kTerms = sizeof(T) == 4 ? 2 : 1, kCols = HT * HN;  // columns of 8 heads
+  // a stage: for every tile of keys and head K codes | V codes; beside the ring, likewise, 16 K scales | 16 V scales
+  static constexpr int kTile = kSub * D, kScales = 2 * kSub * 4, kBoth = KT * HT;
+  static constexpr int kStage = kBoth * 2 * kTile, kTileBytes = HT * (2 * kTile + kScales);
+  static constexpr int kM = 2 * kCols, kAcc = kCols * D / 4, kWords = D / 16;  // 4-byte words of a lane's quarter of a row
+  static constexpr int kStages = (227 * 1024 - 8 * (2 * kM + 1) * 128 - 512) / (8 * (kStage + kBoth * kScales));
+  static_assert(kStages >= 2 && (H <= 8 || HT == 1) && HT * H <= kFdMaxHeads, "items");
+  static constexpr int kExtra = kStages * kBoth * kScales;
+  uint32_t qf[kCols][kTerms][kWords][2];
   float qs[kM];  // the scores' factors: scale, log2 e and the queries' power of two
   float m[kM], l[kM], mw[kM], acc[kAcc];  // acc[(t * D / 16 + mt) * 4 + e]; mw: less kTop
+  float nm[kM], nw[kM];  // -m and -mw, 0 as long as those are -inf
+  int per;               // query heads of a key/value head
 
-  // 16-byte chunk c of row r: exchanged so that 8 lanes that read chunks of
-  // neighbouring (K) or every second row (V) hit all banks.
+  // 16-byte chunk c of row r, as TMA exchanges them within 128 (64) bytes: 8 lanes
+  // that read chunks of neighbouring rows (K) or, for d 128, of every second row (V) hit all banks.
   __device__ __forceinline__ static uint32_t at(uint32_t tile, int r, int c) {
     if (D == 128) return chunk_at(tile, 128, r, c);
-    return tile + uint32_t((r >> 1) * 128 + ((r ^ (r >> 2)) & 1) * 64 + ((c ^ (r & 2)) << 4));
+    return tile + uint32_t(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
   }
-  __device__ __forceinline__ static void copy(const FdParams& p, uint32_t dst, int page, int row, int g, int valid) {
-    constexpr int kCpr = D / 16;
-    const int lane = threadIdx.x & 31;
-    if (valid <= 0) row = 0;
-    const int64_t head = (int64_t(page) << p.pages.page_log2) + row;
-    const uint8_t* kp = static_cast<const uint8_t*>(p.k) + (head * p.Hkv + g) * D;
-    const uint8_t* vp = static_cast<const uint8_t*>(p.v) + (head * p.Hkv + g) * D;
+  __device__ __forceinline__ static void prefetch(const Params& p) {
+    tc::tma_prefetch(&p.tmK);
+    tc::tma_prefetch(&p.tmV);
+  }
+  // tile x of keys in the ring (one thread); g: the item's key/value head or pair
+  __device__ __forceinline__ static void copy(const Params& p, uint32_t ring, uint32_t extra, int x, uint64_t* bar, int page,
+                                              int row, int g) {
+    const int r0 = (page << p.pages.page_log2) + row;
 #pragma unroll
-    for (int x = lane; x < kSub * kCpr; x += 32) {
-      const int r = x / kCpr, c = x % kCpr;
-      const bool in = r < valid;
-      cp16z(at(dst, r, c), kp + (in ? int64_t(r) * p.Hkv * D + c * 16 : 0), in);
+    for (int y = 0; y < HT; ++y) {
+      const int at = x * HT + y, head = g * HT + y;
+      const int64_t sc = ((int64_t(page) * p.kv_heads + head) << p.pages.page_log2) + row;  // scales: [page][head][row]
+      tma_tile(ring + at * 2 * kTile, &p.tmK, bar, head, r0);
+      tma_tile(ring + at * 2 * kTile + kTile, &p.tmV, bar, head, r0);
+      tc::bulk_load(extra + at * kScales, p.k_scale + sc, kScales / 2, bar);
+      tc::bulk_load(extra + at * kScales + kScales / 2, p.v_scale + sc, kScales / 2, bar);
     }
-#pragma unroll
-    for (int x = lane; x < kSub * kCpr; x += 32) {
-      const int r = x / kCpr, c = x % kCpr;
-      const bool in = r < valid;
-      cp16z(at(dst + kTile, r, c), vp + (in ? int64_t(r) * p.Hkv * D + c * 16 : 0), in);
-    }
-    if (lane < 8) {  // scales: [page][head][row], four to a copy; those past the end arrive as zeros
-      const int c = lane & 3;
-      const float* src = (lane < 4 ? p.k_scale : p.v_scale) + (((int64_t(page) * p.Hkv + g) << p.pages.page_log2) + row);
-      const int n = min(max(valid - 4 * c, 0), 4);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kScales + lane * 16),
-                   "l"(src + (n > 0 ? 4 * c : 0)), "r"(4 * n)
-                   : "memory");
-    }
+  }
+  __device__ __forceinline__ static void tma_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int g, int r0) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(0), "r"(g), "r"(r0)
+        : "memory");
   }
   // B fragments of the scores: lane (gq, tq) has dims [tq D / 4, ...) of head gq
-  __device__ __forceinline__ void start(const FdParams& p, const T* q, int heads, uint32_t) {
+  __device__ __forceinline__ void start(const Params& p, const T* q, int heads, uint32_t) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    heads /= HT;  // of each
+    per = heads;
 #pragma unroll
-    for (int t = 0; t < HN; ++t) {
+    for (int t = 0; t < kCols; ++t) {
       float x[4 * kWords], top = 0.f;
-      const T* qh = q + (t * 8 + gq) * D + tq * (D / 4);
-      const bool in = t * 8 + gq < heads;
+      const int h = (t % HN) * 8 + gq;
+      const T* qh = q + ((t / HN) * heads + h) * D + tq * (D / 4);
+      const bool in = h < heads;
 #pragma unroll
       for (int i = 0; i < 4 * kWords; i += 16 / int(sizeof(T))) {
         uint4 raw = make_uint4(0, 0, 0, 0);
@@ -159,65 +176,89 @@ struct Core8 {
       for (int y = 0; y < 2; ++y) qs[2 * t + y] = __shfl_sync(0xffffffffu, up, (2 * tq + y) * 4) * p.scale_log2;
     }
 #pragma unroll
-    for (int x = 0; x < kM; ++x) m[x] = mw[x] = -INFINITY, l[x] = 0.f;
+    for (int x = 0; x < kM; ++x) m[x] = mw[x] = -INFINITY, l[x] = nm[x] = nw[x] = 0.f;
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
-  __device__ __forceinline__ void step(uint32_t stage, uint32_t, int valid, float) {
+  __device__ __forceinline__ void step(uint32_t stage, uint32_t extra, int st, int valid, float) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    float s[kTiles][HN][4], lv[kTiles][2];
+    extra += st * kBoth * kScales;
+    if (valid < KT * kSub) {
+      // rows behind the end may hold anything, and weight 0 does not silence a NaN: they and their scales become zeros
+      for (int x = lane; x < kBoth * kTile / 16; x += 32) {
+        const int at = x / (kTile / 16), r = x % (kTile / 16) / (D / 16);
+        const uint32_t at_k = stage + at * 2 * kTile + x % (kTile / 16) * 16;
+        if ((at / HT) * kSub + r >= valid)
+          asm volatile("st.shared.v4.b32 [%0], {%2, %2, %2, %2};\n\tst.shared.v4.b32 [%1], {%2, %2, %2, %2};" ::"r"(at_k),
+                       "r"(at_k + kTile), "r"(0)
+                       : "memory");
+      }
+      for (int x = lane; x < kBoth * kSub; x += 32) {
+        const int at = x / kSub, r = x % kSub;
+        const uint32_t at_s = extra + at * kScales + r * 4;
+        if ((at / HT) * kSub + r >= valid)
+          asm volatile("st.shared.b32 [%0], %2;\n\tst.shared.b32 [%1], %2;" ::"r"(at_s), "r"(at_s + kScales / 2), "r"(0)
+                       : "memory");
+      }
+      tc::fence_proxy_async_smem();  // before the next copy into the stage
+      __syncwarp();
+    }
+    float s[KT][kCols][4], lv[KT][HT][2];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const uint32_t kt = stage + i * kTileStage, sc = kt + kScales;
+    for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int t = 0; t < HN; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
+      for (int z = 0; z < HT; ++z) {
+        const uint32_t kt = stage + (i * HT + z) * 2 * kTile, sc = extra + (i * HT + z) * kScales;
 #pragma unroll
-      for (int c = 0; c < kWords / 4; ++c) {  // keys gq and gq + 8
-        const uint4 lo = lds16(at(kt, gq, tq * (kWords / 4) + c)), hi = lds16(at(kt, gq + 8, tq * (kWords / 4) + c));
-        const uint32_t r0[4] = {lo.x, lo.y, lo.z, lo.w}, r1[4] = {hi.x, hi.y, hi.z, hi.w};
+        for (int t = z * HN; t < (z + 1) * HN; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a[4] = {low2(r0[w]), low2(r1[w]), high2(r0[w]), high2(r1[w])};
+        for (int c = 0; c < kWords / 4; ++c) {  // keys gq and gq + 8
+          const uint4 lo = lds16(at(kt, gq, tq * (kWords / 4) + c)), hi = lds16(at(kt, gq + 8, tq * (kWords / 4) + c));
+          const uint32_t r0[4] = {lo.x, lo.y, lo.z, lo.w}, r1[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int t = 0; t < HN; ++t)
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a[4] = {low2(r0[w]), low2(r1[w]), high2(r0[w]), high2(r1[w])};
 #pragma unroll
-            for (int y = 0; y < kTerms; ++y) mma16816h(s[i][t], a, qf[t][y][c * 4 + w][0], qf[t][y][c * 4 + w][1]);
+            for (int t = z * HN; t < (z + 1) * HN; ++t)
+#pragma unroll
+              for (int y = 0; y < kTerms; ++y) mma16816h(s[i][t], a, qf[t][y][c * 4 + w][0], qf[t][y][c * 4 + w][1]);
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          lv[i][z][y] = lg2(lds1(sc + kScales / 2 + gq * 4 + 32 * y));
+          const float ks = lds1(sc + gq * 4 + 32 * y), hidden = i * kSub + gq + 8 * y < valid ? 0.f : -INFINITY;
+#pragma unroll
+          for (int t = z * HN; t < (z + 1) * HN; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[i][t][2 * y + e] = fmaf(s[i][t][2 * y + e], qs[2 * t + e] * ks, hidden);
         }
       }
-      const float ks[2] = {lds1(sc + gq * 4), lds1(sc + gq * 4 + 32)};
-      lv[i][0] = lg2(lds1(sc + 64 + gq * 4));
-      lv[i][1] = lg2(lds1(sc + 64 + gq * 4 + 32));
-#pragma unroll
-      for (int t = 0; t < HN; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[i][t][e] = i * kSub + gq + 8 * (e >> 1) < valid ? s[i][t][e] * qs[2 * t + (e & 1)] * ks[e >> 1] : -INFINITY;
-    }
+    // The maxima are only looked for across the lanes when some score is beyond 2^8 of its own.
     float mt[kM], mv[kM];
     bool up = false;
 #pragma unroll
     for (int x = 0; x < kM; ++x) {
-      const int t = x >> 1, e = x & 1;
+      const int t = x >> 1, e = x & 1, z = t / HN;
       mt[x] = fmaxf(s[0][t][e], s[0][t][2 + e]);
-      mv[x] = fmaxf(s[0][t][e] + lv[0][0], s[0][t][2 + e] + lv[0][1]);
+      mv[x] = fmaxf(s[0][t][e] + lv[0][z][0], s[0][t][2 + e] + lv[0][z][1]);
 #pragma unroll
-      for (int i = 1; i < kTiles; ++i) {
+      for (int i = 1; i < KT; ++i) {
         mt[x] = tc::fmax3(mt[x], s[i][t][e], s[i][t][2 + e]);
-        mv[x] = tc::fmax3(mv[x], s[i][t][e] + lv[i][0], s[i][t][2 + e] + lv[i][1]);
+        mv[x] = tc::fmax3(mv[x], s[i][t][e] + lv[i][z][0], s[i][t][2 + e] + lv[i][z][1]);
       }
-      mt[x] = qmax(mt[x]);
-      mv[x] = qmax(mv[x]) - kTop;
-      up |= mt[x] > m[x] + kFdLazy || (m[x] == -INFINITY && mt[x] > -INFINITY);
-      up |= mv[x] > mw[x] + kFdLazy || (mw[x] == -INFINITY && mv[x] > -INFINITY);
+      up |= mt[x] > m[x] + kFdLazy || mv[x] > mw[x] + (kFdLazy + kTop);
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
-        const float mn = fmaxf(m[i], mt[i]), wn = fmaxf(mw[i], mv[i]);
+        const float mn = fmaxf(m[i], qmax(mt[i])), wn = fmaxf(mw[i], qmax(mv[i]) - kTop);
         l[i] *= mn == m[i] ? 1.f : ex2d(m[i] - mn);
         const float a = wn == mw[i] ? 1.f : ex2d(mw[i] - wn);
         m[i] = mn;
         mw[i] = wn;
+        nm[i] = mn == -INFINITY ? 0.f : -mn;
+        nw[i] = wn == -INFINITY ? 0.f : -wn;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           acc[((i >> 1) * (D / 16) + k) * 4 + (i & 1)] *= a;
@@ -226,54 +267,57 @@ struct Core8 {
       }
     }
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const uint32_t vt = stage + i * kTileStage + kTile;
-      uint32_t b[HN][kTerms][2];
+    for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int t = 0; t < HN; ++t) {
-        float w[4];
+      for (int z = 0; z < HT; ++z) {
+        const uint32_t vt = stage + (i * HT + z) * 2 * kTile + kTile;
+        uint32_t b[HN][kTerms][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = 2 * t + (e & 1);
-          l[x] += ex2d(s[i][t][e] - (m[x] == -INFINITY ? 0.f : m[x]));
-          w[e] = ex2d((s[i][t][e] - (mw[x] == -INFINITY ? 0.f : mw[x])) + lv[i][e >> 1]);
+        for (int n = 0; n < HN; ++n) {
+          const int t = z * HN + n;
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 2 * t + (e & 1);
+            l[x] += ex2d(s[i][t][e] + nm[x]);
+            w[e] = ex2d((s[i][t][e] + nw[x]) + lv[i][z][e >> 1]);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t hi = pack_f16(w[2 * y], w[2 * y + 1]);
+            b[n][0][y] = trans8(hi);
+            if constexpr (kTerms == 2) b[n][1][y] = trans8(rest_f16(hi, w[2 * y], w[2 * y + 1]));
+          }
+        }
+        // lane (gq, tq): keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, dims [gq D / 8, ...)
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int r = 2 * tq + (y & 1) + 8 * (y >> 1);
+          if constexpr (D == 128) {
+            const uint4 f = lds16(at(vt, r, gq));
+            v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+          } else {
+            const uint2 f = lds8(at(vt, r, gq >> 1) + (gq & 1) * 8);
+            v[y][0] = f.x, v[y][1] = f.y;
+          }
         }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t hi = pack_f16(w[2 * y], w[2 * y + 1]);
-          b[t][0][y] = trans8(hi);
-          if constexpr (kTerms == 2) b[t][1][y] = trans8(rest_f16(hi, w[2 * y], w[2 * y + 1]));
-        }
-      }
-      // lane (gq, tq): keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, dims [gq D / 8, ...)
-      uint32_t v[4][D / 32];
+        for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int r = 2 * tq + (y & 1) + 8 * (y >> 1);
-        if constexpr (D == 128) {
-          const uint4 f = lds16(at(vt, r, gq));
-          v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
-        } else {
-          const uint2 f = lds8(at(vt, r, gq >> 1) + (gq & 1) * 8);
-          v[y][0] = f.x, v[y][1] = f.y;
-        }
-      }
+          for (int y = 0; y < 2; ++y) {  // dims 4 w + 2 y (rows gq of the product) and 4 w + 2 y + 1 (rows gq + 8)
+            const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+            const uint32_t a[4] = {low2(lo), high2(lo), low2(hi), high2(hi)};
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
+            for (int n = 0; n < HN; ++n) {
+              float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[((z * HN + n) * (D / 16) + 2 * w + y) * 4]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {  // dims 4 w + 2 y (rows gq of the product) and 4 w + 2 y + 1 (rows gq + 8)
-          const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
-          const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-          const uint32_t a[4] = {low2(lo), high2(lo), low2(hi), high2(hi)};
-#pragma unroll
-          for (int t = 0; t < HN; ++t) {
-            float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[(t * (D / 16) + 2 * w + y) * 4]);
-#pragma unroll
-            for (int z = 0; z < kTerms; ++z) mma16816h(c, a, b[t][z][0], b[t][z][1]);
+              for (int q = 0; q < kTerms; ++q) mma16816h(c, a, b[n][q][0], b[n][q][1]);
+            }
           }
         }
       }
-    }
   }
   // the weights' own maximum is taken out again: from here on a state is as any other's
   __device__ __forceinline__ void finish() {
@@ -287,16 +331,26 @@ struct Core8 {
       }
     }
   }
+  // head h of column t, or -1
+  __device__ __forceinline__ int head(int t, int h) const {
+    const int x = (t % HN) * 8 + h;
+    return HT == 1 ? x : x < per ? (t / HN) * per + x : -1;
+  }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
 #pragma unroll
-    for (int t = 0; t < HN; ++t)
+    for (int t = 0; t < kCols; ++t)
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int e = 0; e < 2; ++e) {
+        const int h = head(t, 2 * tq + e);
+        if (HT > 1 && h < 0) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f(t * 8 + 2 * tq + (e & 1), 2 * t + (e & 1), gq * (D / 8) + 2 * k + (e >> 1), acc[(t * (D / 16) + k) * 4 + e]);
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            f(h, 2 * t + e, gq * (D / 8) + 2 * k + y, acc[(t * (D / 16) + k) * 4 + 2 * y + e]);
+      }
   }
   __device__ __forceinline__ void sum_l() {
 #pragma unroll
@@ -307,26 +361,58 @@ struct Core8 {
     const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
     if (gq == 0) {
 #pragma unroll
-      for (int x = 0; x < kM; ++x) f((x >> 1) * 8 + 2 * tq + (x & 1), x);
+      for (int x = 0; x < kM; ++x) {
+        const int h = head(x >> 1, 2 * tq + (x & 1));
+        if (HT == 1 || h >= 0) f(h, x);
+      }
     }
   }
   __device__ __forceinline__ static int m_index(int x) { return 2 * (x / (D / 4)) + (x & 1); }
 };
 
-template <typename T, int D>
-cudaError_t run(const FdParams& p, cudaStream_t stream) {
-  return p.hpg > 8 ? decode<Core8<T, D, 16>, false>(p, "full_decode_fp8", stream)
-                   : decode<Core8<T, D, 8>, false>(p, "full_decode_fp8", stream);
+bool map_codes(CUtensorMap* m, const void* p, uint64_t rows, int Hkv, int d) {
+  const uint64_t D = d;
+  const uint64_t dims[3] = {D, uint64_t(Hkv), rows};
+  const uint64_t strides[2] = {D, D * Hkv};
+  const uint32_t box[3] = {uint32_t(d), 1, kSub};
+  return make_tmap_u8(m, p, 3, dims, strides, box, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+template <typename C>
+cudaError_t run(const Fd8Params& p, cudaStream_t stream) {
+  return decode<C, false>(p, "full_decode_fp8", stream);
+}
+// Up to 8 query heads to a key/value head: a step has two tiles, of neighbouring
+// heads or of 32 keys, and for d 64 four of both. More: two of keys.
+template <int D>
+cudaError_t run_bf16(Fd8Params& p, cudaStream_t stream) {
+  using T = __nv_bfloat16;
+  if (p.group > 8) return run<Core8<T, D, 16, 2, 1>>(p, stream);
+  if (p.kv_heads % 2) return run<Core8<T, D, 8, 2, 1>>(p, stream);
+  p.Hkv = p.kv_heads / 2;  // pairs, as the items' heads
+  p.hpg = 2 * p.group;
+  p.ngr = 1;
+  return run<Core8<T, D, 8, D == 64 ? 2 : 1, 2>>(p, stream);
+}
+// fp32 queries are two terms, whose registers leave no room for pairs
+template <int D>
+cudaError_t run_f32(const Fd8Params& p, cudaStream_t stream) {
+  return p.group > 8 ? run<Core8<float, D, 16, 2, 1>>(p, stream) : run<Core8<float, D, 8, 2, 1>>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_full_decode_fp8(const FullArgs& a, const float* k_scale, const float* v_scale, cudaStream_t stream) {
-  FdParams p = fd_params(a, 2 * fd_grid());
+  Fd8Params p{};
+  static_cast<FdParams&>(p) = fd_params(a, 2 * fd_grid());
   p.k_scale = k_scale;
   p.v_scale = v_scale;
-  if (a.dtype == MSA_BF16) return a.d == 128 ? run<__nv_bfloat16, 128>(p, stream) : run<__nv_bfloat16, 64>(p, stream);
-  return a.d == 128 ? run<float, 128>(p, stream) : run<float, 64>(p, stream);
+  p.kv_heads = p.Hkv;
+  p.group = p.hpg;
+  p.inject_timeout = debug_inject_timeout() ? 1 : 0;
+  const uint64_t rows = uint64_t(a.pages.num_pages) << a.pages.page_log2;
+  if (!map_codes(&p.tmK, a.k, rows, a.Hkv, a.d) || !map_codes(&p.tmV, a.v, rows, a.Hkv, a.d)) return cudaErrorInvalidValue;
+  if (a.dtype == MSA_BF16) return a.d == 128 ? run_bf16<128>(p, stream) : run_bf16<64>(p, stream);
+  return a.d == 128 ? run_f32<128>(p, stream) : run_f32<64>(p, stream);
 }
 
 }  // namespace msa

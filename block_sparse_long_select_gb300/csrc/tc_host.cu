@@ -15,7 +15,8 @@ std::once_flag g_encode_once;
 
 namespace {
 bool make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+               CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -35,7 +36,7 @@ bool make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, in
   }
   for (int i = 0; i + 1 < rank; ++i) s[i] = cuuint64_t(strides[i]);
   CUresult r = g_encode(map, dtype, cuuint32_t(rank), const_cast<void*>(base), d, s, b, e,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -49,6 +50,13 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t
 bool make_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                    const uint32_t* box, CUtensorMapSwizzle swizzle) {
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rank, dims, strides, box, swizzle);
+}
+
+bool make_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  // no more than a row: what follows it in memory is another head's
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box, swizzle,
+                   box[0] >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
 }
 
 }  // namespace msa

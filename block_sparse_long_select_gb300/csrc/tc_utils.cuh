@@ -82,6 +82,13 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned;
+// completion is counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 // 3-D tiled load of the box at (c0, c1, c2) into shared memory; completion is
 // counted in bytes on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
@@ -388,6 +395,8 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // ---- host: tensor maps ------------------------------------------------------
 // Encodes a tiled TMA descriptor for a bf16 tensor of rank `rank` (dims
 // innermost first, byte strides of dims 1..rank-1). Returns false on failure.
+bool make_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box, CUtensorMapSwizzle swizzle);
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                     const uint32_t* box, CUtensorMapSwizzle swizzle);
 // The same for an fp32 tensor.

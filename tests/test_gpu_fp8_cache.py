@@ -429,3 +429,25 @@ def test_other_stream_and_workspace_of_another_operation():
         assert torch.equal(out, again)
     assert torch.equal(kr.cpu(), torch.cat([(c.float() * x[..., None]).to(BF16) for c, x in zip(parts[0], parts[2])]))
     assert msa.msa_read_status(ws) == 0
+
+
+def test_decode_timeout_then_recovers():
+    """A warp of every second CTA lets a wait run out: reported, nothing hangs, the next call is right."""
+    g = torch.Generator().manual_seed(50)
+    lens = [5000, 1, 300]
+    parts, laid = _cache(lens, 2, 64, 16, g)
+    q = torch.randn(3, 8, 64, generator=g).to(BF16)
+    want = f8.decode(q, *parts, 0.125, BF16)
+    args = [x.to(DEV) for x in (q, *laid, torch.tensor(lens, dtype=torch.int32))]
+    ws = msa.workspace(msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE_FP8, 3, 1, laid[4].shape[1] * 16, 2, 8, 64, 0, 0, 0,
+                                              msa.MSA_BF16), DEV)
+    msa.msa_debug_inject_timeout(True)
+    try:
+        msa.msa_full_attn_decode_fp8(*args, ws=ws)
+        assert msa.msa_read_status(ws) == 5
+    finally:
+        msa.msa_debug_inject_timeout(False)
+    for _ in range(2):
+        out = msa.msa_full_attn_decode_fp8(*args, ws=ws)
+        assert msa.msa_read_status(ws) == 0
+        fp.assert_within(out, want[0], want[2], "out")
