@@ -13,10 +13,12 @@
 // on the order of two roundings: keys are rotated with the products' and sums'
 // errors carried along and rounded to fp32 once.
 //
-// Append: streaming, bound by HBM. A head's row is L = d e / 16 lanes with 16
-// bytes each, so that its maximum is L - 1 exchanges, and a lane's pairs of the
-// rotation are the same for every row of the token: their cosines are loaded
-// once. One CTA per token; a decode step's tokens get a thread per 16 bytes.
+// Append: streaming, bound by HBM. A lane holds two 16-byte chunks of a head's
+// row, which are both halves of its pairs; a lane's pairs are the same for every
+// row of the token, so their cosines are loaded once, and the row's maximum takes
+// log2(d e / 32) exchanges. Many tokens: a warp each, so that the search for the
+// sequence and the rotation's loads are a warp's; few (a decode step): a CTA each,
+// so that all loads are in flight at once.
 // Read: streaming. A CTA has 16 packed rows, whose cache rows 16 threads look up
 // at once; a thread's unit is 16 bytes of output.
 #include "full_internal.cuh"
@@ -61,123 +63,173 @@ __device__ __forceinline__ int64_t cache_row(const PageMap& m, int b, int64_t po
   return (int64_t(page) << m.page_log2) + (pos & ((1 << m.page_log2) - 1));
 }
 
-template <typename T, int D>
+// A lane's two chunks of a row, as fp32.
+template <typename T>
+struct TwoChunks {
+  static constexpr int N = 16 / int(sizeof(T));
+  uint4 raw[2];
+  float x[2][N];
+  __device__ __forceinline__ void load(const T* row, int c0, int c1) {
+    raw[0] = reinterpret_cast<const uint4*>(row)[c0];
+    raw[1] = reinterpret_cast<const uint4*>(row)[c1];
+  }
+  __device__ __forceinline__ void clear() { raw[0] = raw[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void widen() {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const T* e = reinterpret_cast<const T*>(&raw[y]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[y][i] = to_f(e[i]);
+    }
+  }
+  // f(a, b, pair): the pair (a, b) and its number among the lane's N
+  template <bool IL, typename F>
+  __device__ __forceinline__ void pairs(F f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (IL)
+        f(x[2 * i / N][2 * i % N], x[2 * i / N][2 * i % N + 1], i);
+      else
+        f(x[0][i], x[1][i], i);
+    }
+  }
+};
+
+template <typename T, int D, bool IL>
 __global__ void __launch_bounds__(kAppMostThreads)
-    paged_append_fp8_kernel(const AppendArgs a, float* __restrict__ k_scale, float* __restrict__ v_scale) {
-  constexpr int N = 16 / int(sizeof(T)), L = D / N, kPer = 32 / L;  // elements of a lane, lanes of a row, rows of a warp
-  const int t = blockIdx.x;
+    paged_append_fp8_kernel(const AppendArgs a, float* __restrict__ k_scale, float* __restrict__ v_scale, bool few) {
+  constexpr int N = 16 / int(sizeof(T)), L = D / N / 2, kPer = 32 / L;  // elements of a chunk, lanes of a row, rows of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = few ? blockIdx.x : blockIdx.x * (kAppThreads / 32) + warp;
+  const int me = few ? warp : 0, warps = few ? blockDim.x >> 5 : 1;  // of the token's warps
   int b = t;
-  if (a.cu_new) {  // every warp finds the token's sequence itself
+  if (a.cu_new) {  // every warp finds its token's sequence itself
     const SeqMap m = seqs_of(a);
     if (cta_in_order(m, &a.ws->disorder)) {
-      b = find_row_seq(a.cu_new, a.B, t);
+      b = t < a.T ? find_row_seq(a.cu_new, a.B, t) : -1;
     } else {
       if (threadIdx.x == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
-      b = scan_row_seq(m, false, t);
+      b = t < a.T ? scan_row_seq(m, false, t) : -1;
     }
-    if (b < 0) return;
   }
+  if (b < 0 || t >= a.T) return;
   const int last = a.cu_new ? a.cu_new[b + 1] : t + 1;
   const int64_t pos = int64_t(a.kv_len[b]) - (last - t);
   const int64_t row = a.rot == 0 || pos < a.max_pos ? cache_row(a.pages, b, pos) : -1;
-  if (row < 0 && threadIdx.x == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
-  const int qh = a.q ? a.Hq : 0;
-  if (row < 0 && !a.q) return;
+  if (row < 0 && me == 0 && lane == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, c = lane % L;
-  const int half = a.rot / 2 / N;  // 16-byte chunks of half the rotated dims
-  // this lane's part of the rotation: out = x cc + partner ss
-  const bool turns = c < 2 * half && row >= 0;
-  const int partner = turns && !a.interleaved ? (c < half ? lane + half : lane - half) : lane;
+  const int sub = lane / L, j = lane % L;
+  const int half = a.rot / 2 / N;  // chunks of half the rotated dims
+  const bool turns = j < half && row >= 0;
+  const int c0 = j < half ? j : 2 * j, c1 = j < half ? j + half : 2 * j + 1;
   float cc[N], ss[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) cc[i] = 1.f, ss[i] = 0.f;
   if (turns) {
     const float* cs = a.rope + pos * a.rot;
-    if (a.interleaved) {  // pairs (2i, 2i + 1) of the chunk
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float2 f = __ldg(reinterpret_cast<const float2*>(cs) + c * (N / 2) + i);
-        cc[2 * i] = cc[2 * i + 1] = f.x;
-        ss[2 * i] = -f.y;
-        ss[2 * i + 1] = f.y;
+    for (int i = 0; i < N / 2; ++i) {  // two pairs each: c0 N + 2 i, or of either chunk
+      const float4 f = __ldg(reinterpret_cast<const float4*>(cs) +
+                             (!IL ? c0 * (N / 2) + i : i < N / 4 ? c0 * (N / 4) + i : c1 * (N / 4) + i - N / 4));
+      cc[2 * i] = f.x;
+      ss[2 * i] = f.y;
+      cc[2 * i + 1] = f.z;
+      ss[2 * i + 1] = f.w;
+    }
+  }
+  constexpr int kBatch = 4;  // rows of a lane in flight
+  // ---- queries ----
+  if (a.q) {
+    const T* src = static_cast<const T*>(a.q) + int64_t(t) * a.Hq * D;
+    T* dst = static_cast<T*>(a.q_out) + int64_t(t) * a.Hq * D;
+    for (int r0 = me * kPer + sub; r0 < a.Hq + sub; r0 += kBatch * warps * kPer) {
+      TwoChunks<T> v[kBatch];
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const int r = r0 + y * warps * kPer;
+        if (r < a.Hq) v[y].load(src + r * D, c0, c1);
       }
-    } else {
-      const float sign = c < half ? -1.f : 1.f;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + 2 * (c < half ? c : c - half) * N) + i);
-        cc[2 * i] = f.x;
-        ss[2 * i] = sign * f.y;
-        cc[2 * i + 1] = f.z;
-        ss[2 * i + 1] = sign * f.w;
+      for (int y = 0; y < kBatch; ++y) {
+        const int r = r0 + y * warps * kPer;
+        if (r >= a.Hq) continue;
+        if (row < 0) v[y].clear();
+        if (turns) {
+          v[y].widen();
+          v[y].template pairs<IL>([&](float& p, float& q, int i) {
+            const float x = p * cc[i] - q * ss[i];
+            q = q * cc[i] + p * ss[i];
+            p = x;
+          });
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            T* w = reinterpret_cast<T*>(&v[y].raw[z]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = from_f<T>(v[y].x[z][i]);
+          }
+        }
+        reinterpret_cast<uint4*>(dst + r * D)[c0] = v[y].raw[0];
+        reinterpret_cast<uint4*>(dst + r * D)[c1] = v[y].raw[1];
       }
     }
   }
+  if (row < 0) return;
+  // ---- keys, then values ----
   const int64_t page = row >> a.pages.page_log2, in_page = row & ((1 << a.pages.page_log2) - 1);
-  const int rows = qh + 2 * a.Hkv, step = int(blockDim.x >> 5) * kPer;
-  constexpr int kBatch = 4;  // rows in flight
-  for (int r0 = warp * kPer; r0 < rows; r0 += kBatch * step) {
-    uint4 raw[kBatch];
+  const int passes = (a.Hkv + kPer - 1) / kPer;  // of a warp, for each
+  for (int p0 = me; p0 < 2 * passes; p0 += kBatch * warps) {
+    TwoChunks<T> v[kBatch];
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
-      const int r = r0 + y * step + sub;
-      const T* src = r < qh ? static_cast<const T*>(a.q) + (int64_t(t) * a.Hq + r) * D
-                     : r < qh + a.Hkv ? static_cast<const T*>(a.k_new) + (int64_t(t) * a.Hkv + r - qh) * D
-                                      : static_cast<const T*>(a.v_new) + (int64_t(t) * a.Hkv + r - qh - a.Hkv) * D;
-      raw[y] = r < rows ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+      const int p = p0 + y * warps;
+      const bool is_k = p < passes;
+      const int h = (is_k ? p : p - passes) * kPer + sub;
+      const T* src = static_cast<const T*>(is_k ? a.k_new : a.v_new) + (int64_t(t) * a.Hkv + h) * D;
+      if (p < 2 * passes && h < a.Hkv)
+        v[y].load(src, c0, c1);
+      else
+        v[y].clear();
     }
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
-      if (r0 + y * step >= rows) break;  // the whole warp's
-      const int r = r0 + y * step + sub;
-      const bool is_q = r < qh, is_k = !is_q && r < qh + a.Hkv;
-      uint4 other = raw[y];
-      if (!a.interleaved) {
-        other.x = __shfl_sync(0xffffffffu, raw[y].x, partner);
-        other.y = __shfl_sync(0xffffffffu, raw[y].y, partner);
-        other.z = __shfl_sync(0xffffffffu, raw[y].z, partner);
-        other.w = __shfl_sync(0xffffffffu, raw[y].w, partner);
-      }
-      const T *e = reinterpret_cast<const T*>(&raw[y]), *eo = reinterpret_cast<const T*>(&other);
-      float x[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] = to_f(e[i]);
-        if (turns && (is_q || is_k)) {
-          const float z = to_f(a.interleaved ? e[i ^ 1] : eo[i]);
-          x[i] = is_k ? dot2(x[i], cc[i], z, ss[i]) : fmaf(x[i], cc[i], z * ss[i]);
-        }
-      }
+      const int p = p0 + y * warps;
+      if (p >= 2 * passes) break;  // the whole warp's
+      const bool is_k = p < passes;
+      const int h = (is_k ? p : p - passes) * kPer + sub;
+      v[y].widen();
+      if (is_k && half > 0)  // the warp's; lanes that do not turn have cos 1, sin 0
+        v[y].template pairs<IL>([&](float& p, float& q, int i) {
+          const float x = dot2(p, cc[i], q, -ss[i]);
+          q = dot2(q, cc[i], p, ss[i]);
+          p = x;
+        });
       uint32_t top = 0;  // as bits: a NaN is above infinity above all else
 #pragma unroll
-      for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(v[y].x[z][i]) & 0x7fffffffu);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (r >= rows) continue;
-      if (is_q) {
-        uint4 u;
-        T* w = reinterpret_cast<T*>(&u);
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = from_f<T>(row < 0 ? 0.f : x[i]);
-        if (row >= 0 && !turns) u = raw[y];  // copied
-        reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + (int64_t(t) * a.Hq + r) * D)[c] = u;
-        continue;
-      }
-      if (row < 0) continue;
-      const int h = r - qh - (is_k ? 0 : a.Hkv);
+      if (h >= a.Hkv) continue;
       // 448 = 1.75 * 2^8: the exponent field of top, one more if its fraction is above 1.75, less 8
       const uint32_t field = max(int((top + 0x1fffffu) >> 23) - 8, 1);
       const bool fine = top < 0x7f800000u;
-      const float inv = __uint_as_float((254u - field) << 23);
-      uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + (row * a.Hkv + h) * D + c * N;
-      uint32_t w[N / 4];
+      const float inv = fine ? __uint_as_float((254u - field) << 23) : 0.f;  // satfinite: codes of a row of scale NaN mean nothing
+      uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + (row * a.Hkv + h) * D;
 #pragma unroll
-      for (int i = 0; i < N / 4; ++i)
-        w[i] = !fine ? 0u : e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
-      if constexpr (N == 8)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      else
-        *reinterpret_cast<uint32_t*>(dst) = w[0];
-      if (c == 0)
+      for (int z = 0; z < 2; ++z) {
+        const float* x = v[y].x[z];
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+          w[i] = e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+        uint8_t* to = dst + (z ? c1 : c0) * N;
+        if constexpr (N == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(to) = w[0];
+      }
+      if (j == 0)
         (is_k ? k_scale : v_scale)[((page * a.Hkv + h) << a.pages.page_log2) + in_page] =
             !fine ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : __uint_as_float(field << 23);
     }
@@ -186,13 +238,15 @@ __global__ void __launch_bounds__(kAppMostThreads)
 
 template <typename T, int D>
 cudaError_t append(const AppendArgs& a, float* k_scale, float* v_scale, cudaStream_t stream) {
-  constexpr int L = D * int(sizeof(T)) / 16;
-  const int total = ((a.q ? a.Hq : 0) + 2 * a.Hkv) * L;
-  const int threads = a.T > kAppFewTokens ? kAppThreads : total >= kAppMostThreads ? kAppMostThreads : (total + 31) / 32 * 32;
+  constexpr int L = D * int(sizeof(T)) / 32, kPer = 32 / L;
+  const bool few = a.T <= kAppFewTokens;
+  const int total = (((a.q ? a.Hq : 0) + kPer - 1) / kPer + 2 * ((a.Hkv + kPer - 1) / kPer)) * 32;
+  const int threads = !few ? kAppThreads : total < kAppMostThreads ? total : kAppMostThreads;
   if (a.cu_new)
     if (cudaError_t e = launch_order_check(seqs_of(a), a.ws, stream)) return e;
   ProfScope pf("paged_append_fp8", stream);
-  paged_append_fp8_kernel<T, D><<<a.T, threads, 0, stream>>>(a, k_scale, v_scale);
+  auto kern = a.interleaved ? paged_append_fp8_kernel<T, D, true> : paged_append_fp8_kernel<T, D, false>;
+  kern<<<few ? a.T : (a.T + kAppThreads / 32 - 1) / (kAppThreads / 32), threads, 0, stream>>>(a, k_scale, v_scale, few);
   return cudaGetLastError();
 }
 
