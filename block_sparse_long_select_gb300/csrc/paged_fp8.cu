@@ -19,8 +19,11 @@
 // log2(d e / 32) exchanges. Many tokens: a warp each, so that the search for the
 // sequence and the rotation's loads are a warp's; few (a decode step): a CTA each,
 // so that all loads are in flight at once.
-// Read: streaming. A CTA has 16 packed rows, whose cache rows 16 threads look up
-// at once; a thread's unit is 16 bytes of output.
+// Read: streaming, bound by HBM. A CTA has up to 16 packed rows, whose cache rows
+// as many threads look up at once; a thread's unit is 16 codes, whose values it
+// stores in whole 32-byte sectors.
+#include <algorithm>
+
 #include "full_internal.cuh"
 
 namespace msa {
@@ -252,11 +255,18 @@ cudaError_t append(const AppendArgs& a, float* k_scale, float* v_scale, cudaStre
 
 __host__ __device__ SeqMap seqs_of(const ReadArgs& a) { return SeqMap{a.cu, nullptr, a.kv_len, a.B, a.T, 0}; }
 
+// Eight words to global memory: one whole sector
+__device__ __forceinline__ void store8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const ReadArgs a, const SmallDiv by_rows) {
-  constexpr int N = 16 / int(sizeof(T)), L = D / N;  // elements of a unit, units of a head's row
-  __shared__ int64_t row_s[kReadRows];               // cache row; -1: out of range, -2: nobody's
-  const int t0 = blockIdx.x * kReadRows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const ReadArgs a, int rows, const SmallDiv by_heads, bool sectors) {
+  constexpr int N = 16, L = D / N;          // codes of a unit, units of a head's row
+  __shared__ int64_t row_s[kReadRows];      // cache row; -1: out of range, -2: nobody's
+  const int t0 = blockIdx.x * rows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool in_order = !a.cu || cta_in_order(seqs_of(a), &a.ws->disorder);
   auto look = [&](int t, int b) {
     if (b < 0) return int64_t(-2);
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const Read
   };
   if (in_order) {
     const int t = t0 + int(threadIdx.x);
-    if (threadIdx.x < kReadRows) {
+    if (threadIdx.x < rows) {
       int b = t < a.T ? t : -1;
       if (a.cu && t < a.T) {  // the last sequence that starts at or before t
         int n = a.B;
@@ -286,59 +296,66 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const Read
     }
   } else {
     if (threadIdx.x == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
-    for (int x = warp; x < kReadRows; x += kReadThreads / 32) {
+    for (int x = warp; x < rows; x += kReadThreads / 32) {
       const int t = t0 + x, b = t < a.T ? scan_row_seq(seqs_of(a), false, t) : -1;
       if (lane == 0) row_s[x] = look(t, b);
     }
   }
   __syncthreads();
   const int heads = 2 * a.Hkv, c = threadIdx.x % L;
-  constexpr int kBatch = 8, kStep = kReadThreads / L;  // units in flight; head rows of a pass
-  const int all = kReadRows * heads;
+  constexpr int kBatch = 4, kStep = kReadThreads / L;  // units in flight; head rows of a pass
+  const int all = rows * heads;
   for (int r0 = threadIdx.x / L; r0 < all; r0 += kBatch * kStep) {
-    uint32_t code[kBatch][N / 4];
+    uint4 code[kBatch];
     float scale[kBatch];
-    int64_t to[kBatch];
+    T* to[kBatch];
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
       const int r = min(r0 + y * kStep, all - 1);
-      int x = by_rows.of(r);
+      int x = by_heads.of(r);
       x -= x * heads > r;  // beyond 8192 key/value heads the reciprocal's quotient can be one too large
       const int hh = r - x * heads;
       const bool is_v = hh >= a.Hkv;
       const int h = is_v ? hh - a.Hkv : hh;
       const int64_t row = row_s[x], src = max(row, int64_t(0));
-      const uint8_t* p = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) + (src * a.Hkv + h) * D + c * N;
-      if constexpr (N == 8) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-        code[y][0] = u.x, code[y][1] = u.y;
-      } else {
-        code[y][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-      }
+      code[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+                                                     (src * a.Hkv + h) * D) + c);
       const int64_t s = (((src >> a.pages.page_log2) * a.Hkv + h) << a.pages.page_log2) + (src & ((1 << a.pages.page_log2) - 1));
       scale[y] = __ldg((is_v ? a.v_scale : a.k_scale) + s);
       if (row < 0) {  // out of range: zeros
         scale[y] = 0.f;
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) code[y][i] = 0;
+        code[y] = make_uint4(0, 0, 0, 0);
       }
-      to[y] = row == -2 || r0 + y * kStep >= all ? -1 : (int64_t(t0 + x) * a.Hkv + h) * 2 + is_v;
+      to[y] = row == -2 || r0 + y * kStep >= all
+                  ? nullptr
+                  : static_cast<T*>(is_v ? a.v_out : a.k_out) + (int64_t(t0 + x) * a.Hkv + h) * D + c * N;
     }
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
-      if (to[y] < 0) continue;
-      uint4 u;
-      T* w = reinterpret_cast<T*>(&u);
+      if (!to[y]) continue;
+      const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
+      constexpr int kWords = N * int(sizeof(T)) / 4;
+      uint32_t out[kWords];
+      T* o = reinterpret_cast<T*>(out);
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
         uint32_t f;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(uint16_t(code[y][i / 2] >> (16 * (i & 1)))));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(uint16_t(w[i / 2] >> (16 * (i & 1)))));
         float lo, hi;
         asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(f));
-        w[2 * i] = from_f<T>(lo * scale[y]);
-        w[2 * i + 1] = from_f<T>(hi * scale[y]);
+        o[2 * i] = from_f<T>(lo * scale[y]);
+        o[2 * i + 1] = from_f<T>(hi * scale[y]);
       }
-      reinterpret_cast<uint4*>(static_cast<T*>(to[y] & 1 ? a.v_out : a.k_out) + (to[y] >> 1) * D)[c] = u;
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(to[y]) + i;
+        if (sectors) {
+          store8(p, out + i);
+        } else {
+          reinterpret_cast<uint4*>(p)[0] = make_uint4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+          reinterpret_cast<uint4*>(p)[1] = make_uint4(out[i + 4], out[i + 5], out[i + 6], out[i + 7]);
+        }
+      }
     }
   }
 }
@@ -347,8 +364,11 @@ template <typename T, int D>
 cudaError_t read(const ReadArgs& a, cudaStream_t stream) {
   if (a.cu)
     if (cudaError_t e = launch_order_check(seqs_of(a), a.ws, stream)) return e;
+  // fewer rows to a CTA where there would be fewer than two CTAs to an SM
+  const int rows = std::max(1, std::min(kReadRows, a.T / (2 * kNumSMs)));
+  const bool sectors = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31u) == 0;
   ProfScope pf("paged_read_fp8", stream);
-  paged_read_fp8_kernel<T, D><<<(a.T + kReadRows - 1) / kReadRows, kReadThreads, 0, stream>>>(a, SmallDiv(2 * a.Hkv));
+  paged_read_fp8_kernel<T, D><<<(a.T + rows - 1) / rows, kReadThreads, 0, stream>>>(a, rows, SmallDiv(2 * a.Hkv), sectors);
   return cudaGetLastError();
 }
 

@@ -451,3 +451,33 @@ def test_decode_timeout_then_recovers():
         out = msa.msa_full_attn_decode_fp8(*args, ws=ws)
         assert msa.msa_read_status(ws) == 0
         fp.assert_within(out, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_least_aligned_tensors(dtype):
+    """Every tensor 16 bytes behind a coarser boundary, which is all that the calls ask for."""
+    g = torch.Generator().manual_seed(60)
+
+    def off(x):
+        raw = torch.zeros(x.nbytes + 272, dtype=torch.uint8, device=DEV)
+        at = (-raw.data_ptr()) % 256 + 16
+        y = raw[at:at + x.nbytes].view(x.dtype).view(x.shape)
+        y.copy_(x)
+        return y
+
+    lens = [40, 3]
+    k, v = (torch.randn(43, 2, 64, generator=g).to(dtype) for _ in range(2))
+    q = off(torch.randn(2, 8, 64, generator=g).to(dtype))
+    cache = [off(torch.zeros(4, 16, 2, 64).to(f8.E4M3)) for _ in range(2)] + [off(torch.zeros(4, 2, 16)) for _ in range(2)]
+    table, kv, cu = (off(i) for i in (torch.tensor([[3, 0, 1], [2, 9, 9]], dtype=torch.int32),
+                                      torch.tensor(lens, dtype=torch.int32), fp.offsets(lens)))
+    msa.msa_paged_append_fp8(None, off(k), off(v), None, cu, kv, table, *cache)
+    out = [off(torch.zeros(43, 2, 64).to(dtype)) for _ in range(2)]
+    msa.msa_paged_read_fp8(*cache, table, cu, kv, 43, k_out=out[0], v_out=out[1])
+    parts = [f8.quantise(x.float()) for x in (k, v)]
+    for x, (c, s) in zip(out, parts):
+        assert torch.equal(x.cpu(), (c.float() * s[..., None]).to(dtype))
+    cut = lambda x: [x[:40], x[40:]]  # noqa: E731
+    want = f8.decode(q.cpu(), cut(parts[0][0]), cut(parts[1][0]), cut(parts[0][1]), cut(parts[1][1]), 0.125, dtype)
+    got = msa.msa_full_attn_decode_fp8(q, *cache, table, kv, out=off(torch.zeros(2, 8, 64).to(dtype)))
+    fp.assert_within(got, want[0], want[2], "out")
