@@ -32,7 +32,7 @@ constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
 // 2^8 and their common factor drops out in the division by their sum.
 constexpr float kFdLazy = 8.f;
-constexpr int kFdLeast = 4;  // SHARED: steps of a warp's run at least, each item of which is a part to be joined
+constexpr int kFdLeast = 2;  // SHARED: steps of a warp's run at least, each item of which is a part to be joined
 
 __device__ __forceinline__ float ex2d(float x) {
   float y;
@@ -134,9 +134,8 @@ __device__ __forceinline__ int units_of(const FdParams& p, int b, int unit_log2)
 
 // Four values of one head joined over `parts` parts, in order, and its lse. A
 // negative sum marks a head without a result.
-template <typename T, typename F>
+template <typename T, int kBatch = 8, typename F>  // kBatch: parts in flight, the loads of which do not wait for each other
 __device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D, int dim, int parts, F part_of) {
-  constexpr int kBatch = 8;  // parts in flight: the loads of a batch do not wait for each other
   float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
   bool spoilt = false;
   for (int y0 = 0; y0 < parts; y0 += kBatch) {

@@ -9,9 +9,9 @@ namespace {
 
 // A thread per four values of a query head; D / 4 of them a head. Bound by the
 // latency of five dependent loads and, for many parts, by L2.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) full_join_kernel(const FdParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdParams p) {
   constexpr int kLanes = D / 4;
   const int64_t row = int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
   const int dim = (threadIdx.x % kLanes) * 4;
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kJoinThreads) full_join_kernel(const FdParams 
   const int heads = min(p.hpg, kFdMaxHeads);
   int2 parts = make_int2(0, 0);  // of its own keys
   if (own.L > own.from) parts = __ldcg(p.item_parts + (b * p.Hkv + g) * p.ngr + hg / heads);
-  join_head<T>(p, row, D, dim, parts.y + pre.n, [&](int y) {
+  join_head<T, 10>(p, row, D, dim, parts.y + pre.n, [&](int y) {
     if (y >= parts.y) return pre.part(y - parts.y);
     const int64_t head = int64_t(parts.x + y) * heads + hg % heads;
     return PartAt{p.part_o + head * D, p.part_ml + head * 2};
