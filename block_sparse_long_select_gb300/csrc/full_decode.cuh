@@ -257,8 +257,15 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   constexpr bool ALONE = SOLO || SHARED;
   constexpr int ulog = ALONE ? SH::kStepLog2 : SH::kUnitLog2;
   const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * SH::kStep;
-  // runs in the order of the SMs, so that few of them lie on many
-  const int runs = int(gridDim.x) * (SHARED ? kFdWarps : 1), run = SHARED ? warp * int(gridDim.x) + int(blockIdx.x) : int(blockIdx.x);
+  // SHARED: runs in the order of the SMs, so that few of them lie on many; other SMs may be the prefixes'
+  int ctas = gridDim.x;
+  if constexpr (SHARED) {
+    int t, f, n, l;
+    const PrefixLoad load = prefix_load(p.shared, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1, t, f, n, l);
+    if (p.shared.geo.beside && load.ctas < ctas) ctas -= load.ctas;
+    if (int(blockIdx.x) >= ctas) return;
+  }
+  const int runs = ctas * (SHARED ? kFdWarps : 1), run = SHARED ? warp * ctas + int(blockIdx.x) : int(blockIdx.x);
   int64_t per = (total + runs - 1) / runs;
   if (SHARED && per < kFdLeast) per = kFdLeast;
   const int64_t run0 = SOLO ? 0 : run * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);

@@ -46,6 +46,7 @@ struct Core<__nv_bfloat16, D, H> {
   static constexpr int kM = 2 * HN, kAcc = HN * D / 4;
   uint32_t qf[HN][D / 16][2];
   float m[kM], l[kM], acc[kAcc];  // acc[(t * D / 16 + mt) * 4 + e]
+  float nm[kM];                   // -m, 0 as long as that is -inf
 
   __device__ __forceinline__ static void copy(const FdParams& p, uint32_t dst, int page, int row, int g, int valid) {
     copy_rows<T, D>(p.k, p.v, dst, (int64_t(page) << p.pages.page_log2) + (valid > 0 ? row : 0), p.Hkv, g, valid);
@@ -62,7 +63,7 @@ struct Core<__nv_bfloat16, D, H> {
           qf[t][ks][x] = t * 8 + gq < heads ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 2 * tq + 8 * x) : 0u;
     }
 #pragma unroll
-    for (int x = 0; x < kM; ++x) m[x] = -INFINITY, l[x] = 0.f;
+    for (int x = 0; x < kM; ++x) m[x] = -INFINITY, l[x] = nm[x] = 0.f;
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
@@ -87,19 +88,21 @@ struct Core<__nv_bfloat16, D, H> {
       for (int e = 0; e < 4; ++e) s[t][e] = gq + 8 * (e >> 1) < valid ? s[t][e] * scale_log2 : -INFINITY;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        mt[2 * t + x] = qmax(fmaxf(s[t][x], s[t][2 + x]));
-        up |= mt[2 * t + x] > m[2 * t + x] + kFdLazy || (m[2 * t + x] == -INFINITY && mt[2 * t + x] > -INFINITY);
+        mt[2 * t + x] = fmaxf(s[t][x], s[t][2 + x]);
+        up |= mt[2 * t + x] > m[2 * t + x] + kFdLazy;
       }
     }
+    // the maxima are only looked for across the lanes when some score is beyond 2^8 of its own
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int t = 0; t < HN; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int i = 2 * t + x;
-          const float mn = fmaxf(m[i], mt[i]);
+          const float mn = fmaxf(m[i], qmax(mt[i]));
           const float a = mn == m[i] ? 1.f : ex2d(m[i] - mn);
           m[i] = mn;
+          nm[i] = mn == -INFINITY ? 0.f : -mn;
           l[i] *= a;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -114,8 +117,7 @@ struct Core<__nv_bfloat16, D, H> {
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float mm = m[2 * t + (e & 1)];
-        p[e] = ex2d(s[t][e] - (mm == -INFINITY ? 0.f : mm));
+        p[e] = ex2d(s[t][e] + nm[2 * t + (e & 1)]);
         l[2 * t + (e & 1)] += p[e];  // unrounded; the product below takes bf16 weights
       }
       const __nv_bfloat162 lo = __floats2bfloat162_rn(p[0], p[1]), hi = __floats2bfloat162_rn(p[2], p[3]);

@@ -581,7 +581,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 
 PrefixGeometry prefix_geometry_tc(int hpg) {
   const int tpt = kRows / hpg;
-  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2};
+  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2, 28};
 }
 
 cudaError_t launch_prefix_tc(const SharedArgs& a, cudaStream_t stream) {

@@ -32,6 +32,7 @@ struct PrefixGeometry {
   int block;          // most rows of a part
   int grid;           // CTAs
   int least;          // units that a CTA takes at least
+  int beside;         // what a unit takes in the decode grid's steps of all SMs together; 0: no grids side by side
 };
 // A group's items.
 struct PrefixRec {
@@ -132,6 +133,68 @@ __device__ __forceinline__ PrefixRows<D> SharedParams::rows(int x, int b, int g,
   return r;
 }
 
+// ---- both grids side by side -------------------------------------------------------
+// The sequences' own keys are bound by HBM, which three quarters of the SMs keep
+// busy; the prefixes are bound by the chain from scores to weights. So where the
+// former take much longer, the latter get as few CTAs as still end with them, and
+// the decode grid, whose other CTAs start at once, only uses the SMs left (97
+// sequences of 1300 own keys behind three prefixes, 20 K keys: 130 us one after the
+// other, BESIDE us with the prefixes on a fifth of the SMs). Else every SM serves both in turn.
+constexpr int kLeastOwn = 8;  // SMs
+struct PrefixLoad {
+  int64_t units;  // of all groups
+  int ctas;       // that work on them
+  int64_t per;    // units of each but the last
+};
+// Group i's key tiles (0: nothing to compute), sequences and leader.
+__device__ __forceinline__ void look_at_group(const SharedParams& p, const int32_t* kv_len, int cap, int page_mask, int i,
+                                              int& tiles, int& first, int& cnt, int& lead) {
+  first = p.groups.cu_q[i];
+  cnt = p.groups.cu_q[i + 1] - first;
+  const int len = p.prefix_len[i];
+  tiles = 0;
+  lead = first;
+  if (cnt <= 0 || len <= 0 || len > cap || (len & page_mask)) return;
+  for (int b = first; b < first + cnt; ++b) {
+    const int L = kv_len[b];
+    if (L >= len && L <= cap) {  // the others see nothing of it
+      lead = b;
+      tiles = (len - 1) / kPxKeys + 1;
+      return;
+    }
+  }
+}
+// Whole warp. `heads`: key/value heads. t, f, c, l: of group `lane`, where there are up to 32.
+__device__ __forceinline__ PrefixLoad prefix_load(const SharedParams& p, const int32_t* kv_len, int heads, int cap,
+                                                  int page_mask, int& t, int& f, int& c, int& l) {
+  const int lane = threadIdx.x & 31;
+  int64_t units = 0, own = 0;
+  if (p.geo.beside)
+#pragma unroll 4
+    for (int b = lane; b < p.groups.Tq; b += 32) own += min(max(kv_len[b], 0), cap);
+  for (int x0 = 0; x0 < p.groups.B; x0 += 32) {
+    t = 0;
+    if (x0 + lane < p.groups.B) look_at_group(p, kv_len, cap, page_mask, x0 + lane, t, f, c, l);
+    if (t > 0) {
+      units += prefix_tiles(p.geo, c, t).units * heads * p.geo.groups;
+      own -= int64_t(c) * t * kPxKeys;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    own += __shfl_xor_sync(0xffffffffu, own, o);
+  }
+  PrefixLoad r{units, p.geo.grid, max((units + p.geo.grid - 1) / p.geo.grid, int64_t(p.geo.least))};
+  if (p.geo.beside && own > 0 && units > 0) {
+    const int64_t work = units * p.geo.beside, steps = own / 16 * heads + 1;
+    const int64_t most = max(min(kNumSMs * work / (work + steps), int64_t(kNumSMs - kLeastOwn)), int64_t(1));
+    r.per = max((units + most - 1) / most, int64_t(p.geo.least));
+    r.ctas = int((units + r.per - 1) / r.per);
+  }
+  return r;
+}
+
 // ---- the prefixes' grid: a CTA's run of units ------------------------------------
 // One part to compute.
 struct PrefixPart {
@@ -150,39 +213,14 @@ struct PrefixPlan {
   int64_t at, end, per, unit0, row0;
   int x, n, b0, count, leader;
 
-  // Group x's key tiles (0: nothing to compute), sequences and leader.
-  __device__ __forceinline__ void look(int i, int& tiles, int& first, int& cnt, int& lead) const {
-    first = p.groups.cu_q[i];
-    cnt = p.groups.cu_q[i + 1] - first;
-    const int len = p.prefix_len[i];
-    tiles = 0;
-    lead = first;
-    if (cnt <= 0 || len <= 0 || len > cap || (len & page_mask)) return;
-    for (int b = first; b < first + cnt; ++b) {
-      const int L = kv_len[b];
-      if (L >= len && L <= cap) {  // the others see nothing of it
-        lead = b;
-        tiles = (len - 1) / kPxKeys + 1;
-        return;
-      }
-    }
-  }
   // Whole warp: measures all groups, leaves their records (`write`), and finds
   // this CTA's run. False: it has none.
   __device__ __forceinline__ bool init(int cta, bool write) {
     const int lane = threadIdx.x & 31, all = Hkv * p.geo.groups;
-    int64_t total = 0;
     int t = 0, f = 0, c = 0, l = 0;
-    for (int x0 = 0; x0 < p.groups.B; x0 += 32) {
-      t = 0;
-      if (x0 + lane < p.groups.B) look(x0 + lane, t, f, c, l);
-      int64_t u = t > 0 ? prefix_tiles(p.geo, c, t).units * all : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-      total += u;
-    }
-    per = (total + p.geo.grid - 1) / p.geo.grid;
-    if (per < p.geo.least) per = p.geo.least;
+    const PrefixLoad load = prefix_load(p, kv_len, Hkv, cap, page_mask, t, f, c, l);
+    const int64_t total = load.units;
+    per = load.per;
     at = int64_t(cta) * per;
     end = min(at + per, total);
     bool found = false;
@@ -190,7 +228,7 @@ struct PrefixPlan {
     for (int x0 = 0; x0 < p.groups.B && (write || !found); x0 += 32) {
       if (p.groups.B > 32) {  // else they are in hand
         t = 0;
-        if (x0 + lane < p.groups.B) look(x0 + lane, t, f, c, l);
+        if (x0 + lane < p.groups.B) look_at_group(p, kv_len, cap, page_mask, x0 + lane, t, f, c, l);
       }
       PrefixTiles pt{0, 0, 0};
       if (t > 0) pt = prefix_tiles(p.geo, c, t);
@@ -227,7 +265,7 @@ struct PrefixPlan {
       unit0 += t.units * all;
       row0 += t.rows * all;
       do {
-        look(++x, n, b0, count, leader);
+        look_at_group(p, kv_len, cap, page_mask, ++x, n, b0, count, leader);
       } while (n == 0);
       t = prefix_tiles(p.geo, count, n);
     }
