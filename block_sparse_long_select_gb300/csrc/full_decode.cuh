@@ -32,6 +32,7 @@ constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
 // 2^8 and their common factor drops out in the division by their sum.
 constexpr float kFdLazy = 8.f;
+constexpr int kFdKept = 4;   // SHARED: rounds of 32 sequences whose units are kept, as it takes three loads to find them
 constexpr int kFdLeast = 2;  // SHARED: steps of a warp's run at least, each item of which is a part to be joined
 
 __device__ __forceinline__ float ex2d(float x) {
@@ -240,7 +241,7 @@ struct FdShape {
 // SOLO: whole items for single warps; SHARED: the warp's run of the `total` steps
 // of 16 keys; else the CTA's run of the `total` units.
 template <typename C, bool SOLO, bool SHARED>
-__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total) {
+__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total, const int (&first_units)[kFdKept]) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
@@ -260,8 +261,8 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   // SHARED: runs in the order of the SMs, so that few of them lie on many; other SMs may be the prefixes'
   int ctas = gridDim.x;
   if constexpr (SHARED) {
-    int t, f, n, l;
-    const PrefixLoad load = prefix_load(p.shared, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1, t, f, n, l);
+    PrefixGroup unused;
+    const PrefixLoad load = prefix_load(p.shared, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1, unused);
     if (p.shared.geo.beside && load.ctas < ctas) ctas -= load.ctas;
     if (int(blockIdx.x) >= ctas) return;
   }
@@ -276,10 +277,16 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   if constexpr (SOLO) {
     at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop, ulog);
   } else {
-    int ahead = lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
+    int ahead = SHARED ? 0 : lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int mine = ahead;
-      ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, ulog) : 0;  // in flight during the scan
+      int mine = ahead;
+      if constexpr (SHARED) {
+        const int kept = b0 / 32;
+        mine = kept == 0 ? first_units[0] : kept == 1 ? first_units[1] : kept == 2 ? first_units[2] : first_units[3];
+        if (kept >= kFdKept) mine = b0 + lane < p.B ? units_of<SHARED>(p, b0 + lane, ulog) : 0;
+      } else {
+        ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, ulog) : 0;  // in flight during the scan
+      }
       int64_t incl = int64_t(mine) * items;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -584,12 +591,20 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   // ---- all units (every warp counts alone) ----
   int64_t total = 0;
   int longest = 0;  // in warps' steps
-#pragma unroll 8
-  for (int b = lane; b < p.B; b += 32) {
+  int kept[kFdKept] = {0, 0, 0, 0};
+  auto count = [&](int b) {
     const int steps = units_of<SHARED>(p, b, SH::kStepLog2);
     total += SHARED ? steps : (steps + kFdWarps - 1) / kFdWarps;
     longest = max(longest, steps);
+    return steps;
+  };
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int x = 0; x < kFdKept; ++x)
+      if (lane + 32 * x < p.B) kept[x] = count(lane + 32 * x);
   }
+#pragma unroll 8
+  for (int b = lane + (SHARED ? 32 * kFdKept : 0); b < p.B; b += 32) count(b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   longest = __reduce_max_sync(0xffffffffu, longest);
@@ -615,9 +630,9 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     }
   }
   if (!SHARED && solo)
-    decode_run<C, !SHARED, SHARED>(p, total);
+    decode_run<C, !SHARED, SHARED>(p, total, kept);
   else
-    decode_run<C, false, SHARED>(p, total);
+    decode_run<C, false, SHARED>(p, total, kept);
   if constexpr (SHARED) tc::griddep_wait();  // this grid is not over before the prefixes' grid is
 }
 

@@ -66,8 +66,8 @@ PrefixGeometry geometry(int hpg, int dtype) { return dtype == MSA_BF16 ? prefix_
 struct Regions {
   size_t recs, items, stat, part, own_stat, own_part, end;
   Regions(const PrefixGeometry& g, int B, int groups, int Hkv, int hpg, int d) {
-    // every item's rows, and a block for every CTA that an item goes on in
-    const size_t rows = size_t(B) * Hkv * g.groups * g.heads + size_t(g.grid) * g.block;
+    // every item's rows, and a block for every part beyond its first
+    const size_t rows = size_t(B) * Hkv * g.groups * g.heads + size_t(prefix_most_parts(g)) * g.block;
     const size_t own_items = size_t(B) * Hkv * head_groups(hpg), own_rows = (own_items + fd_grid() * 8) * (hpg < kFdMaxHeads ? hpg : kFdMaxHeads);
     size_t at = kWsHeader;
     auto take = [&](size_t bytes) {

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) full_prefix_f32_kernel(const P
     if (warp == 0) {
       int state = 2;
       if (some && plan.at < plan.end) {
-        const PrefixPart d = plan.next(blockIdx.x);
+        const PrefixPart d = plan.next();
         const int32_t* row = p.pages.table + int64_t(d.leader) * p.pages.max_pages;
         const int per = kPxKeys >> p.pages.page_log2, to = min((d.jb + d.n) * per, d.Lk >> p.pages.page_log2);
         bool bad = false;
@@ -154,7 +154,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 
 PrefixGeometry prefix_geometry_f32(int hpg) {
   const int heads = hpg < 16 ? hpg : 16;
-  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 1, 0};
+  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 2, 0};
 }
 
 cudaError_t launch_prefix_f32(const SharedArgs& a, cudaStream_t stream) {

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (plan.init(blockIdx.x, blockIdx.x == 0)) {
         while (ok && plan.at < plan.end) {
           PxItem d;
-          d.d = plan.next(blockIdx.x);
+          d.d = plan.next();
           // the part's own pages in range; if not, the decode grid finds its rows marked
           const int32_t* row = p.pages.table + int64_t(d.d.leader) * p.pages.max_pages;
           const int per = kKeys >> p.pages.page_log2, to = min((d.d.jb + d.d.n) * per, d.d.Lk >> p.pages.page_log2);
@@ -363,22 +363,29 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     int z = 0, used = 0, alts = 0;  // steps and parts of this row tile; parts of alternate key tiles
     for (int it = 0; ok; ++it) {
       if (!(ok = warp_wait(&item_full[it % NI], (it / NI) & 1, abort_flag))) break;
+      // the item's slot is given back at its end: what is only wanted there is read there
       const PxItem* sp = items + it % NI;
-      const int n = sp->d.n, mode = sp->mode, jb = sp->d.jb, alt = sp->d.alt, Lk = sp->d.Lk, count = sp->d.count;
-      const int64_t row0 = sp->d.row;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&item_empty[it % NI]);
+      const int n = sp->d.n, mode = sp->mode, alt = sp->d.alt;
+      auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&item_empty[it % NI]);
+      };
       if (mode == 3) break;
-      const bool valid = r < p.tpt * p.hpg && row_seq + (alt ? 0 : w * p.tpt) < count;
-      const int64_t row = row0 + (alt ? 0 : w * p.tpt) * p.hpg + r;  // of the part's
+      auto my_row = [&](bool& valid) {
+        valid = r < p.tpt * p.hpg && row_seq + (alt ? 0 : w * p.tpt) < sp->d.count;
+        return sp->d.row + (alt ? 0 : w * p.tpt) * p.hpg + r;  // of the part's
+      };
       if (mode == 2) {
+        bool valid;
+        const int64_t row = my_row(valid);
         if (valid) p.s.stat[row] = make_float2(-INFINITY, -1.f);
+        give_back();
         continue;
       }
+      int lim = sp->d.Lk - (sp->d.jb + (alt ? w : 0)) * kKeys;  // columns of the tile below it are keys
       float m = -INFINITY, l = 0.f;
       const int steps = alt ? (n - w + 1) / 2 : n;
-      for (int i = 0; i < steps; ++i, ++z) {
-        const int lim = Lk - (jb + (alt ? 2 * i + w : i)) * kKeys;  // columns below it are keys
+      for (int i = 0; i < steps; ++i, ++z, lim -= alt ? 2 * kKeys : kKeys) {
         if (!(ok = warp_wait(&s_full[w], z & 1, abort_flag))) break;
         tc::fence_after_sync();
         // O follows a raised maximum: S is complete, so is the product before it, and O is at rest
@@ -484,16 +491,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         ++used;
         tc::fence_after_sync();
       }
+      bool valid;
+      const int64_t row = my_row(valid);
+      give_back();
       if (!alt) {
         if (valid) p.s.stat[row] = make_float2(m, l);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tc::tmem_ld_32x32b_x32(obase + c * 32, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          float o[64];
+          tc::tmem_ld_32x32b_x32(obase + c * 64, reinterpret_cast<uint32_t*>(o));
+          tc::tmem_ld_32x32b_x32(obase + c * 64 + 32, reinterpret_cast<uint32_t*>(o + 32));
           tc::tmem_ld_wait();
           if (valid) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) store8(p.s.part + row * D + c * 32 + x * 8, o + x * 8);
+            for (int x = 0; x < 8; ++x) store8(p.s.part + row * D + c * 64 + x * 8, o + x * 8);
           }
         }
         tc::fence_before_sync();  // the next part's products may go over O
@@ -516,17 +527,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       const float a0 = s0.x == M ? 1.f : ex2(s0.x - M), a1 = s1.x == M ? 1.f : ex2(s1.x - M);
       if (valid && w == 0) p.s.stat[row] = make_float2(M, s0.y * a0 + s1.y * a1);
       const uint32_t o0 = tmem + (uint32_t(quarter * 32) << 16) + kColO + w * (D / 2), o1 = o0 + D;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float x0[16], x1[16];
-        tc::tmem_ld_32x32b_x16(o0 + c * 16, reinterpret_cast<uint32_t*>(x0));
-        if (n > 1) tc::tmem_ld_32x32b_x16(o1 + c * 16, reinterpret_cast<uint32_t*>(x1));
-        tc::tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) x0[x] = n > 1 ? fmaf(x1[x], a1, x0[x] * a0) : x0[x];
+      for (int c = 0; c < D / 64; ++c) {
+        float x0[32], x1[32];
+        tc::tmem_ld_32x32b_x32(o0 + c * 32, reinterpret_cast<uint32_t*>(x0));
+        tc::tmem_ld_32x32b_x32(o1 + c * 32, reinterpret_cast<uint32_t*>(x1));  // anything, if n == 1
+        tc::tmem_ld_wait();
         if (valid) {
-          store8(p.s.part + row * D + w * (D / 2) + c * 16, x0);
-          store8(p.s.part + row * D + w * (D / 2) + c * 16 + 8, x0 + 8);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float o[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) o[y] = n > 1 ? fmaf(x1[8 * x + y], a1, x0[8 * x + y] * a0) : x0[8 * x + y];
+            store8(p.s.part + row * D + w * (D / 2) + c * 32 + x * 8, o);
+          }
         }
       }
       tc::fence_before_sync();
@@ -581,7 +595,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 
 PrefixGeometry prefix_geometry_tc(int hpg) {
   const int tpt = kRows / hpg;
-  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2, 28};
+  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2, 24};
 }
 
 cudaError_t launch_prefix_tc(const SharedArgs& a, cudaStream_t stream) {
