@@ -263,7 +263,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   if constexpr (SHARED) {
     PrefixGroup unused;
     const PrefixLoad load = prefix_load(p.shared, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1, unused);
-    if (p.shared.geo.beside && load.ctas < ctas) ctas -= load.ctas;
+    if (load.beside) ctas -= load.ctas;
     if (int(blockIdx.x) >= ctas) return;
   }
   const int runs = ctas * (SHARED ? kFdWarps : 1), run = SHARED ? warp * ctas + int(blockIdx.x) : int(blockIdx.x);

@@ -176,6 +176,7 @@ struct PrefixLoad {
   int per;  // units of a run, at most
   int64_t runs;
   int each, ctas;  // runs of a CTA, CTAs that have any
+  bool beside;     // the decode grid has the other SMs to itself
 };
 // Whole warp. `heads`: key/value heads; mine: group `lane`, where there are up to 32.
 __device__ __forceinline__ PrefixLoad prefix_load(const SharedParams& p, const int32_t* kv_len, int heads, int cap,
@@ -184,7 +185,10 @@ __device__ __forceinline__ PrefixLoad prefix_load(const SharedParams& p, const i
   int64_t units = 0, items = 0, own = 0;
   if (p.geo.beside)
 #pragma unroll 4
-    for (int b = lane; b < p.groups.Tq; b += 32) own += min(max(kv_len[b], 0), cap);
+    for (int b = lane; b < p.groups.Tq; b += 32) {
+      const int L = kv_len[b], x = p.group_of(b), from = x >= 0 ? p.prefix_len[x] : 0;
+      if (L <= cap && from >= 0 && L > from) own += L - from;
+    }
   mine.n = 0;
   for (int x0 = 0; x0 < p.groups.B; x0 += 32) {
     PrefixGroup g{0, 0, 0, 0};
@@ -194,23 +198,20 @@ __device__ __forceinline__ PrefixLoad prefix_load(const SharedParams& p, const i
       const PrefixTiles t = prefix_tiles(p.geo, g.count, g.n, 1);
       units += t.units * all;
       items += int64_t(t.tiles) * all;
-      own -= int64_t(g.count) * g.n * kPxKeys;
     }
   }
   units = warp_sum(units);
   items = warp_sum(items);
+  own = warp_sum(own);
   int64_t ctas = p.geo.grid;
-  if (p.geo.beside) {
-    own = warp_sum(own);
-    const int64_t work = units * p.geo.beside;
-    if (own > 0 && units > 0)
-      ctas = max(min(ctas * work / (work + own / 16 * heads + 1), ctas - kLeastOwn), int64_t(1));
-  }
+  const int64_t work = units * p.geo.beside;
+  const bool beside = work > 0 && own > 0;
+  if (beside) ctas = max(min(ctas * work / (work + own / 16 * heads + 1), ctas - kLeastOwn), int64_t(1));
   // Few items: no CTA has two runs (its second starts behind the end of its first, about 3 us).
   // Many: runs of half a CTA's share. Either way at most 2 ctas runs beyond the items.
   const int64_t want = 2 * items <= ctas ? ctas - items : 2 * ctas;
   // (an item has up to 2^23 units)
-  PrefixLoad r{int(min(max((units + want - 1) / want, int64_t(p.geo.least)), int64_t(1) << 24)), 0, 0, 0};
+  PrefixLoad r{int(min(max((units + want - 1) / want, int64_t(p.geo.least)), int64_t(1) << 24)), 0, 0, 0, beside};
   for (int x0 = 0; x0 < p.groups.B; x0 += 32) {
     PrefixGroup g = mine;
     if (p.groups.B > 32) {

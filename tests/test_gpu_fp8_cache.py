@@ -481,3 +481,21 @@ def test_least_aligned_tensors(dtype):
     want = f8.decode(q.cpu(), cut(parts[0][0]), cut(parts[1][0]), cut(parts[0][1]), cut(parts[1][1]), 0.125, dtype)
     got = msa.msa_full_attn_decode_fp8(q, *cache, table, kv, out=off(torch.zeros(2, 8, 64).to(dtype)))
     fp.assert_within(got, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [5, 900])
+def test_append_in_place(T, dtype):
+    """q_out == q, with a CTA and with a warp per token: the bits of the other call."""
+    g = torch.Generator().manual_seed(70)
+    q = torch.randn(T, 8, 128, generator=g).to(dtype).to(DEV)
+    k = torch.randn(T, 2, 128, generator=g).to(dtype).to(DEV)
+    pages = -(-T // 16)
+    cache = [torch.zeros(pages, 16, 2, 128, device=DEV).to(f8.E4M3) for _ in range(2)]
+    cache += [torch.zeros(pages, 2, 16, device=DEV) for _ in range(2)]
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, pages)
+    cu, kv = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, T], [T]))
+    rope = fp.rope_table(T, 96).to(DEV)
+    want = msa.msa_paged_append_fp8(q, k, k, rope, cu, kv, table, *cache)
+    got = msa.msa_paged_append_fp8(q, k, k, rope, cu, kv, table, *cache, q_out=q)
+    assert got is q and torch.equal(got, want)

@@ -298,3 +298,10 @@ def test_timeout_then_recovers():
         out = msa.msa_full_attn_decode_shared(*args, ws=ws)
         assert msa.msa_read_status(ws) == 0
         fp.assert_within(out, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("own", [1, 3, 40])
+def test_padded_batches(own):
+    """Mostly padded groups, and own keys that a prefix's last key tile would outnumber."""
+    check([(16, [None] * 40 + [own] * 3), (400, [own] + [None] * 70), (48, [own] * 90)], 8, 2, 64, BF16, 16, 20)
+    check([(4096, [None] * 30 + [own, 2000])], 4, 2, 128, BF16, 64, 21)
