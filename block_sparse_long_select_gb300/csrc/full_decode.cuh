@@ -32,8 +32,6 @@ constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
 // 2^8 and their common factor drops out in the division by their sum.
 constexpr float kFdLazy = 8.f;
-constexpr int kFdKept = 4;   // SHARED: rounds of 32 sequences whose units are kept, as it takes three loads to find them
-constexpr int kFdLeast = 2;  // SHARED: steps of a warp's run at least, each item of which is a part to be joined
 
 __device__ __forceinline__ float ex2d(float x) {
   float y;
@@ -105,7 +103,6 @@ struct FdParams {
   float* lse;
   uint32_t* status;
   SharedParams shared;  // SHARED only
-  int2* item_parts;     // SHARED: [items]: the first of an item's parts, their number
 };
 
 // The keys of sequence b that its items walk: [from, L). SHARED: from is where its
@@ -118,13 +115,13 @@ struct Own {
 template <bool SHARED>
 __device__ __forceinline__ Own own_of(const FdParams& p, int b) {
   Own o{0, p.kv_len[b], -1, true};
-  o.ok = o.L >= 0 && o.L <= p.cap;
   if constexpr (SHARED) {
-    if (o.L != 0) {  // 0: a padded entry, in a group or not
-      o.x = p.shared.group_of(b);
-      if (o.x >= 0) o.from = p.shared.prefix_len[o.x];
-      o.ok = o.ok && o.from >= 0 && o.from <= o.L && (o.from & ((1 << p.pages.page_log2) - 1)) == 0;
-    }
+    const SharedSeq q = p.shared.get_seq(b);
+    o.from = q.from;
+    o.x = q.group;
+    o.ok = q.from >= 0;
+  } else {
+    o.ok = o.L >= 0 && o.L <= p.cap;
   }
   return o;
 }
@@ -241,7 +238,7 @@ struct FdShape {
 // SOLO: whole items for single warps; SHARED: the warp's run of the `total` steps
 // of 16 keys; else the CTA's run of the `total` units.
 template <typename C, bool SOLO, bool SHARED>
-__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total, const int (&first_units)[kFdKept]) {
+__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
@@ -259,16 +256,15 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   constexpr int ulog = ALONE ? SH::kStepLog2 : SH::kUnitLog2;
   const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * SH::kStep;
   // SHARED: runs in the order of the SMs, so that few of them lie on many; other SMs may be the prefixes'
-  int ctas = gridDim.x;
+  int run = blockIdx.x;
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
   if constexpr (SHARED) {
-    PrefixGroup unused;
-    const PrefixLoad load = prefix_load(p.shared, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1, unused);
-    if (load.beside) ctas -= load.ctas;
-    if (int(blockIdx.x) >= ctas) return;
+    const SharedHead head = p.shared.get_head();
+    if (head.disorder || int(blockIdx.x) >= head.own_ctas) return;
+    run = warp * head.own_ctas + int(blockIdx.x);
+    per = head.own_per;
+    total = head.steps;
   }
-  const int runs = ctas * (SHARED ? kFdWarps : 1), run = SHARED ? warp * ctas + int(blockIdx.x) : int(blockIdx.x);
-  int64_t per = (total + runs - 1) / runs;
-  if (SHARED && per < kFdLeast) per = kFdLeast;
   const int64_t run0 = SOLO ? 0 : run * per, run1 = SOLO ? INT64_MAX : min(run0 + per, total);
   if (run0 >= run1) return;
   Walk<SHARED> at{};
@@ -277,33 +273,34 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   if constexpr (SOLO) {
     at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop, ulog);
   } else {
-    int ahead = SHARED ? 0 : lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int mine = ahead;
-      if constexpr (SHARED) {
-        const int kept = b0 / 32;
-        mine = kept == 0 ? first_units[0] : kept == 1 ? first_units[1] : kept == 2 ? first_units[2] : first_units[3];
-        if (kept >= kFdKept) mine = b0 + lane < p.B ? units_of<SHARED>(p, b0 + lane, ulog) : 0;
-      } else {
+    if constexpr (SHARED) {
+      // the last sequence that starts at or before the run: those without steps are passed over
+      at.b = warp_count_true(p.B - 1, [&](int i) { return __ldcg(p.shared.step0 + i) <= run0; });
+      first = __ldcg(p.shared.step0 + at.b);
+    } else {
+      int ahead = lane < p.B ? units_of<SHARED>(p, lane, ulog) : 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int mine = ahead;
         ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, ulog) : 0;  // in flight during the scan
-      }
-      int64_t incl = int64_t(mine) * items;
+        int64_t incl = int64_t(mine) * items;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          at.b = b0 + src;
+          at.n = __shfl_sync(0xffffffffu, mine, src);
+          first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
+          break;
+        }
+        first += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > run0);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        at.b = b0 + src;
-        at.n = __shfl_sync(0xffffffffu, mine, src);
-        first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
-        break;
-      }
-      first += __shfl_sync(0xffffffffu, incl, 31);
     }
     at.own = own_of<SHARED>(p, at.b);
+    if constexpr (SHARED) at.n = at.own.units(ulog);
     const int it = int((run0 - first) / at.n);
     at.g = it / p.ngr;
     at.hg = it % p.ngr;
@@ -501,8 +498,6 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       } else {
         float* po = p.part_o + int64_t(slot) * item_heads * D;
         float* pm = p.part_ml + int64_t(slot) * item_heads * 2;
-        if (SHARED && lane == 0 && item_first >= run0)
-          p.item_parts[item] = make_int2(slot, int((item_first + n - 1) / per) - run + 1);
         c.each([&](int h, int, int dim, float val) {
           if (h < heads) po[h * D + dim] = val;
         });
@@ -567,12 +562,10 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   [[maybe_unused]] T* out = static_cast<T*>(p.out);
   if constexpr (SHARED) {
     tc::griddep_launch_dependents();  // the joins' grid, which waits for this one
-    if (!cta_in_order(p.shared.groups, p.shared.disorder)) {  // whose keys these are is not known
-      tc::griddep_wait();
-      return;
-    }
+    decode_run<C, false, true>(p, 0);
+    tc::griddep_wait();  // this grid is not over before the prefixes' grid is
+    return;
   }
-
   if constexpr (C::kBulk) {
     extern __shared__ __align__(1024) uint8_t fd_smem[];
     if (tc::smem_u32(fd_smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
@@ -591,20 +584,12 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   // ---- all units (every warp counts alone) ----
   int64_t total = 0;
   int longest = 0;  // in warps' steps
-  int kept[kFdKept] = {0, 0, 0, 0};
-  auto count = [&](int b) {
-    const int steps = units_of<SHARED>(p, b, SH::kStepLog2);
-    total += SHARED ? steps : (steps + kFdWarps - 1) / kFdWarps;
-    longest = max(longest, steps);
-    return steps;
-  };
-  if constexpr (SHARED) {
-#pragma unroll
-    for (int x = 0; x < kFdKept; ++x)
-      if (lane + 32 * x < p.B) kept[x] = count(lane + 32 * x);
-  }
 #pragma unroll 8
-  for (int b = lane + (SHARED ? 32 * kFdKept : 0); b < p.B; b += 32) count(b);
+  for (int b = lane; b < p.B; b += 32) {
+    const int steps = units_of<SHARED>(p, b, SH::kStepLog2);
+    total += (steps + kFdWarps - 1) / kFdWarps;
+    longest = max(longest, steps);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   longest = __reduce_max_sync(0xffffffffu, longest);
@@ -619,21 +604,19 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   const int warps = int(gridDim.x) * kFdWarps;
   const int64_t all = int64_t(p.B) * items, rounds = (all + warps - 1) / warps;
   const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
-  if constexpr (!SHARED) {  // sequences without keys: nobody's run holds them
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      const Own o = own_of<false>(p, b);
-      if (o.units(SH::kStepLog2) > 0) continue;
-      if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
-      for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
-      if (p.lse)
-        for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
-    }
+  // sequences without keys: nobody's run holds them
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Own o = own_of<SHARED>(p, b);
+    if (o.units(SH::kStepLog2) > 0) continue;
+    if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
+    for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
+    if (p.lse)
+      for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
   }
-  if (!SHARED && solo)
-    decode_run<C, !SHARED, SHARED>(p, total, kept);
+  if (solo)
+    decode_run<C, true, SHARED>(p, total);
   else
-    decode_run<C, false, SHARED>(p, total, kept);
-  if constexpr (SHARED) tc::griddep_wait();  // this grid is not over before the prefixes' grid is
+    decode_run<C, false, SHARED>(p, total);
 }
 
 int fd_grid() { return kNumSMs; }
@@ -651,17 +634,7 @@ cudaError_t decode(const typename C::Params& p, const char* name, cudaStream_t s
     kern<<<fd_grid(), FdShape<C>::kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(fd_grid());
-  cfg.blockDim = dim3(FdShape<C>::kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_early(kern, fd_grid(), FdShape<C>::kThreads, bytes, stream, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

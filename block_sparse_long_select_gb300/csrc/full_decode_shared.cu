@@ -7,22 +7,38 @@
 namespace msa {
 namespace {
 
-// A thread per four values of a query head; D / 4 of them a head. Bound by the
-// latency of five dependent loads and, for many parts, by L2.
+// A thread per four values of a query head; D / 4 of them a head. All but the
+// parts is known before the grids that leave them end. Bound by latency and, for
+// many parts, by L2. Small CTAs with few registers fit beside the decode grid's.
 constexpr int kJoinThreads = 128;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdParams p) {
   constexpr int kLanes = D / 4;
   const int64_t row = int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
   const int dim = (threadIdx.x % kLanes) * 4;
-  const bool in_order = cta_in_order(p.shared.groups, p.shared.disorder);
-  const bool mine = row < int64_t(p.B) * p.Hq;
-  const int b = mine ? int(row / p.Hq) : 0, h = mine ? int(row % p.Hq) : 0, g = h / p.hpg, hg = h - g * p.hpg;
+  if (row >= int64_t(p.B) * p.Hq) {
+    tc::griddep_wait();
+    return;
+  }
+  const int b = int(row / p.Hq), h = int(row % p.Hq), g = h / p.hpg, hg = h - g * p.hpg;
+  const SharedHead head = p.shared.get_head();
   Own own{0, 0, -1, false};
-  if (in_order) own = own_of<true>(p, b);
+  if (!head.disorder) own = own_of<true>(p, b);
+  PrefixRows<D> pre{nullptr, nullptr, 0, 0};
+  const int heads = min(p.hpg, kFdMaxHeads);
+  int64_t part0 = 0;  // the parts of its own keys
+  int parts = 0;
+  if (own.ok && own.L > 0) {
+    pre = p.shared.rows<D>(own.x, b, g, hg, head.per);
+    if (const int n = own.units(4)) {
+      const int it = g * p.ngr + hg / heads;
+      const int64_t at = __ldcg(p.shared.step0 + b) + int64_t(it) * n, c0 = at / head.own_per;
+      part0 = int64_t(b) * p.Hkv * p.ngr + it + c0;
+      parts = int((at + n - 1) / head.own_per - c0) + 1;
+    }
+  }
   tc::griddep_wait();
-  if (!mine) return;
-  if (!own.ok || own.L == 0) {
+  if (parts + pre.n == 0) {
     if (!own.ok && dim == 0) set_status(p.status, MSA_ERR_BOUNDS);
     T* dst = static_cast<T*>(p.out) + row * D + dim;
 #pragma unroll
@@ -30,30 +46,18 @@ __global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdPara
     if (p.lse && dim == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const PrefixRows<D> pre = p.shared.rows<D>(own.x, b, g, hg);
-  const int heads = min(p.hpg, kFdMaxHeads);
-  int2 parts = make_int2(0, 0);  // of its own keys
-  if (own.L > own.from) parts = __ldcg(p.item_parts + (b * p.Hkv + g) * p.ngr + hg / heads);
-  join_head<T, 10>(p, row, D, dim, parts.y + pre.n, [&](int y) {
-    if (y >= parts.y) return pre.part(y - parts.y);
-    const int64_t head = int64_t(parts.x + y) * heads + hg % heads;
-    return PartAt{p.part_o + head * D, p.part_ml + head * 2};
+  join_head<T, 10>(p, row, D, dim, parts + pre.n, [&](int y) {
+    if (y >= parts) return pre.part(y - parts);
+    const int64_t at = (part0 + y) * heads + hg % heads;
+    return PartAt{p.part_o + at * D, p.part_ml + at * 2};
   });
 }
 
 template <typename T, int D>
 cudaError_t join(const FdParams& p, cudaStream_t stream) {
   ProfScope pf("full_join", stream);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned((int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, full_join_kernel<T, D>, p);
+  return launch_early(full_join_kernel<T, D>, (int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads, kJoinThreads,
+                      0, stream, p);
 }
 template <typename T, int D, int H>
 cudaError_t run(const FdParams& p, cudaStream_t stream) {
@@ -64,7 +68,7 @@ cudaError_t run(const FdParams& p, cudaStream_t stream) {
 PrefixGeometry geometry(int hpg, int dtype) { return dtype == MSA_BF16 ? prefix_geometry_tc(hpg) : prefix_geometry_f32(hpg); }
 // The workspace behind the header.
 struct Regions {
-  size_t recs, items, stat, part, own_stat, own_part, end;
+  size_t head, seqs, step0, recs, stat, part, own_stat, own_part, end;
   Regions(const PrefixGeometry& g, int B, int groups, int Hkv, int hpg, int d) {
     // every item's rows, and a block for every part beyond its first
     const size_t rows = size_t(B) * Hkv * g.groups * g.heads + size_t(prefix_most_parts(g)) * g.block;
@@ -75,8 +79,10 @@ struct Regions {
       at += up256(bytes);
       return r;
     };
+    head = take(sizeof(SharedHead));
+    seqs = take(size_t(B) * sizeof(SharedSeq));
+    step0 = take(size_t(B) * sizeof(int64_t));
     recs = take(size_t(groups) * sizeof(PrefixRec));
-    items = take(own_items * sizeof(int2));
     stat = take(rows * sizeof(float2));
     part = take(rows * d * sizeof(float));
     own_stat = take(own_rows * sizeof(float2));
@@ -97,19 +103,21 @@ cudaError_t launch_decode_shared(const FullArgs& a, const int32_t* cu_prefix, co
   SharedParams s{};
   s.groups = SeqMap{cu_prefix, nullptr, prefix_len, groups, B, a.seq.Tk};
   s.prefix_len = prefix_len;
-  s.disorder = &static_cast<WsHeader*>(a.ws)->disorder;
   s.geo = geometry(hpg, a.dtype);
   const Regions at(s.geo, B, groups, a.Hkv, hpg, a.d);
   char* w = static_cast<char*>(a.ws);
+  s.head = reinterpret_cast<SharedHead*>(w + at.head);
+  s.seqs = reinterpret_cast<SharedSeq*>(w + at.seqs);
+  s.step0 = reinterpret_cast<int64_t*>(w + at.step0);
   s.recs = reinterpret_cast<PrefixRec*>(w + at.recs);
   s.stat = reinterpret_cast<float2*>(w + at.stat);
   s.part = reinterpret_cast<float*>(w + at.part);
-  if (cudaError_t e = launch_order_check(s.groups, a.ws, stream)) return e;
   const SharedArgs args{a, s};
+  const int warps = a.dtype == MSA_FP32 && a.d == 128 ? Core<float, 128, 4>::kWarps : Core<__nv_bfloat16, 128, 8>::kWarps;
+  if (cudaError_t e = launch_shared_plan(args, warps, a.Hkv * head_groups(hpg), stream)) return e;
   if (cudaError_t e = a.dtype == MSA_BF16 ? launch_prefix_tc(args, stream) : launch_prefix_f32(args, stream)) return e;
   FdParams p = fd_params(a, 0);
   p.shared = s;
-  p.item_parts = reinterpret_cast<int2*>(w + at.items);
   p.part_ml = reinterpret_cast<float*>(w + at.own_stat);
   p.part_o = reinterpret_cast<float*>(w + at.own_part);
   const bool wide = hpg > 8, few = hpg <= 4;  // as in full_decode.cu

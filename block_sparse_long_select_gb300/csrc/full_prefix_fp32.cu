@@ -11,9 +11,8 @@ namespace {
 struct PfxParams {
   SharedParams s;
   PageMap pages;
-  const int32_t* kv_len;
   const float *q, *k, *v;
-  int Hq, Hkv, hpg, cap;
+  int Hq, Hkv, hpg;
   float scale_log2;
   uint32_t* status;
 };
@@ -25,11 +24,11 @@ __global__ void __launch_bounds__(kF32Threads, 2) full_prefix_f32_kernel(const P
   __shared__ int state_s;  // 0: a part to compute, 1: one with bad pages, 2: no more
   const uint32_t sq = tc::smem_u32(pfx_smem), sk = sq + kA * D * 4, sv = sk + kB * D * 4, sp = sv + kB * D * 4;
   const int tx = tile_x(), ty = tile_y(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tc::griddep_launch_dependents();
-  if (!cta_in_order(p.s.groups, p.s.disorder)) return;  // the decode grid reports it
-  PrefixPlan plan{p.s, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1};
+  tc::griddep_wait();               // the plan
+  tc::griddep_launch_dependents();  // behind it, so that the decode grid, which may start now, has it as well
+  PrefixRuns plan{p.s, p.Hkv};
   bool some = false;
-  if (warp == 0) some = plan.init(blockIdx.x, blockIdx.x == 0);
+  if (warp == 0) some = plan.init(p.s.get_head(), blockIdx.x);
   const int psz = 1 << p.pages.page_log2, heads = p.s.geo.heads;
   for (;;) {
     if (warp == 0) {
@@ -131,14 +130,12 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
   PfxParams p{};
   p.s = a.s;
   p.pages = f.pages;
-  p.kv_len = f.seq.kv_len;
   p.q = static_cast<const float*>(f.q);
   p.k = static_cast<const float*>(f.k);
   p.v = static_cast<const float*>(f.v);
   p.Hq = f.Hq;
   p.Hkv = f.Hkv;
   p.hpg = f.Hq / f.Hkv;
-  p.cap = f.seq.Tk;
   p.scale_log2 = f.scale * kLog2e;
   p.status = &static_cast<WsHeader*>(f.ws)->status;
   auto kern = full_prefix_f32_kernel<D>;
@@ -146,15 +143,14 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
   static KernelReady ready;
   if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes)) return e;
   ProfScope pf("full_prefix", stream);
-  kern<<<a.s.geo.grid, kF32Threads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(kern, a.s.geo.grid, kF32Threads, bytes, stream, p);
 }
 
 }  // namespace
 
 PrefixGeometry prefix_geometry_f32(int hpg) {
   const int heads = hpg < 16 ? hpg : 16;
-  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 2, 0};
+  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 1, 0};
 }
 
 cudaError_t launch_prefix_f32(const SharedArgs& a, cudaStream_t stream) {

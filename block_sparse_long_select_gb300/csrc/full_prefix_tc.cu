@@ -40,8 +40,7 @@ static_assert(kPxKeys == kKeys, "key tiles");
 struct PxParams {
   SharedParams s;
   PageMap pages;
-  const int32_t* kv_len;
-  int Hkv, hpg, tpt, cap;
+  int Hkv, hpg, tpt;
   float scale_log2;
   uint32_t* status;
   int inject_timeout;  // test hook: every second CTA waits on a barrier nothing completes
@@ -97,12 +96,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   constexpr uint32_t kColO = 256;
   extern __shared__ __align__(1024) uint8_t px_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tc::griddep_launch_dependents();  // the decode grid may start as SMs fall free; it waits for this one's parts
   if (tc::smem_u32(px_smem) & 1023u) {  // the swizzled operands need 1024-byte alignment
     if (threadIdx.x == 0) set_status(p.status, MSA_ERR_CUDA);
     return;
   }
-  if (!cta_in_order(p.s.groups, p.s.disorder)) return;  // the decode grid reports it
   PxItem* items = reinterpret_cast<PxItem*>(px_smem + SM::oItem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(px_smem + SM::oBar);
   uint64_t* q_full = bars;                // [2]
@@ -144,6 +141,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  tc::griddep_wait();               // the plan
+  tc::griddep_launch_dependents();  // behind it, so that the decode grid, which may start now, has it as well
   auto fail = [&]() {
     *abort_flag = 1;
     set_status(p.status, MSA_ERR_TIMEOUT);
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
     } else if (warp == 2) {
       // ------------------------------ parts ------------------------------
-      PrefixPlan plan{p.s, p.kv_len, p.Hkv, p.cap, (1 << p.pages.page_log2) - 1};
+      PrefixRuns plan{p.s, p.Hkv};
       bool ok = true;
       int it = 0;
       auto publish = [&](const PxItem& d) {
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         ++it;
       };
-      if (plan.init(blockIdx.x, blockIdx.x == 0)) {
+      if (plan.init(p.s.get_head(), blockIdx.x)) {
         while (ok && plan.at < plan.end) {
           PxItem d;
           d.d = plan.next();
@@ -566,11 +565,9 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
   PxParams p{};
   p.s = a.s;
   p.pages = f.pages;
-  p.kv_len = f.seq.kv_len;
   p.Hkv = f.Hkv;
   p.hpg = f.Hq / f.Hkv;
   p.tpt = kRows / p.hpg;
-  p.cap = f.seq.Tk;
   p.scale_log2 = f.scale * kLog2e;
   p.status = &static_cast<WsHeader*>(f.ws)->status;
   p.inject_timeout = debug_inject_timeout() ? 1 : 0;
@@ -587,8 +584,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
   static KernelReady ready;
   if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes, int(kRegsLaunch))) return e;
   ProfScope pf("full_prefix", stream);
-  kern<<<kNumSMs, kPxThreads, bytes, stream>>>(tmQ, tmK, tmV, p);
-  return cudaGetLastError();
+  return launch_early(kern, kNumSMs, kPxThreads, bytes, stream, tmQ, tmK, tmV, p);
 }
 
 }  // namespace
