@@ -106,19 +106,22 @@ struct FdParams {
 };
 
 // The keys of sequence b that its items walk: [from, L). SHARED: from is where its
-// group's prefix ends, and x the group (-1: none).
+// group's prefix ends, if that is left to the other grid, and x the group (-1:
+// none); else the prefix's keys, up to `upto`, are found by the leader's page table.
 struct Own {
-  int from, L, x;
+  int from, L, x, leader, upto;
   bool ok;
   __device__ __forceinline__ int units(int unit_log2) const { return ok && L > from ? ((L - from - 1) >> unit_log2) + 1 : 0; }
 };
 template <bool SHARED>
 __device__ __forceinline__ Own own_of(const FdParams& p, int b) {
-  Own o{0, p.kv_len[b], -1, true};
+  Own o{0, p.kv_len[b], -1, 0, 0, true};
   if constexpr (SHARED) {
     const SharedSeq q = p.shared.get_seq(b);
     o.from = q.from;
     o.x = q.group;
+    o.leader = q.leader;
+    o.upto = q.upto;
     o.ok = q.from >= 0;
   } else {
     o.ok = o.L >= 0 && o.L <= p.cap;
@@ -318,7 +321,8 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
 #pragma unroll
     for (int x = 0; x < C::kTiles; ++x)
       page[x] = key + x * kSub < w.own.L
-                    ? p.pages.table[int64_t(w.b) * p.pages.max_pages + ((key + x * kSub) >> p.pages.page_log2)]
+                    ? p.pages.table[int64_t(SHARED && key < w.own.upto ? w.own.leader : w.b) * p.pages.max_pages +
+                                    ((key + x * kSub) >> p.pages.page_log2)]
                     : 0;
   };
   if (ld_left > 0) pages_of(ld);

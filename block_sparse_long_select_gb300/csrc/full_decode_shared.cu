@@ -8,11 +8,12 @@ namespace msa {
 namespace {
 
 // A thread per four values of a query head; D / 4 of them a head. All but the
-// parts is known before the grids that leave them end. Bound by latency and, for
-// many parts, by L2. Small CTAs with few registers fit beside the decode grid's.
+// parts is known before the grids that leave them end. Bound by latency: few rows
+// have ten parts in flight, many rows fewer registers and so more warps (128 000
+// rows 101 us, 158 with ten). Small CTAs fit beside the decode grid's.
 constexpr int kJoinThreads = 128;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdParams p) {
+template <typename T, int D, int BATCH, int CTAS>
+__global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdParams p) {
   constexpr int kLanes = D / 4;
   const int64_t row = int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
   const int dim = (threadIdx.x % kLanes) * 4;
@@ -22,7 +23,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdPara
   }
   const int b = int(row / p.Hq), h = int(row % p.Hq), g = h / p.hpg, hg = h - g * p.hpg;
   const SharedHead head = p.shared.get_head();
-  Own own{0, 0, -1, false};
+  Own own{0, 0, -1, 0, 0, false};
   if (!head.disorder) own = own_of<true>(p, b);
   PrefixRows<D> pre{nullptr, nullptr, 0, 0};
   const int heads = min(p.hpg, kFdMaxHeads);
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdPara
     if (p.lse && dim == 0) p.lse[row] = -INFINITY;
     return;
   }
-  join_head<T, 10>(p, row, D, dim, parts + pre.n, [&](int y) {
+  join_head<T, BATCH>(p, row, D, dim, parts + pre.n, [&](int y) {
     if (y >= parts) return pre.part(y - parts);
     const int64_t at = (part0 + y) * heads + hg % heads;
     return PartAt{p.part_o + at * D, p.part_ml + at * 2};
@@ -56,7 +57,8 @@ __global__ void __launch_bounds__(kJoinThreads, 6) full_join_kernel(const FdPara
 template <typename T, int D>
 cudaError_t join(const FdParams& p, cudaStream_t stream) {
   ProfScope pf("full_join", stream);
-  return launch_early(full_join_kernel<T, D>, (int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads, kJoinThreads,
+  const int64_t ctas = (int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads;
+  return launch_early(ctas <= 8 * kNumSMs ? full_join_kernel<T, D, 10, 6> : full_join_kernel<T, D, 4, 12>, ctas, kJoinThreads,
                       0, stream, p);
 }
 template <typename T, int D, int H>

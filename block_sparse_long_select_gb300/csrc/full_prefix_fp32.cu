@@ -150,7 +150,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 
 PrefixGeometry prefix_geometry_f32(int hpg) {
   const int heads = hpg < 16 ? hpg : 16;
-  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 1, 0};
+  return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 1, 0, 1};
 }
 
 cudaError_t launch_prefix_f32(const SharedArgs& a, cudaStream_t stream) {

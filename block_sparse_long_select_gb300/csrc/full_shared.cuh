@@ -34,6 +34,7 @@ struct PrefixGeometry {
   int grid;           // CTAs
   int least;          // units of a run at least; 2 or more where there are alt items
   int beside;         // what a unit takes in steps of the decode grid; 0: no grids side by side
+  int worth;          // key tiles times sequences beyond the first that make an item
 };
 // A group's items; runs, rows and parts beyond the items' first ones of the groups before it.
 struct PrefixRec {
@@ -50,9 +51,11 @@ struct SharedHead {
   int per, each, ctas, own_ctas;  // units of a prefix's run at most; runs of a CTA, CTAs with runs; of the decode grid
 };
 static_assert(sizeof(SharedHead) == 48, "read as three 16-byte words");
-// A sequence: where its own keys begin (-1: its length is out of range) and its group (-1: none).
+// A sequence: where the keys that it walks by itself begin (-1: its length is out
+// of range), the group whose parts it takes (-1: none), and whose page table holds
+// its first keys, up to where.
 struct SharedSeq {
-  int from, group;
+  int from, group, leader, upto;
 };
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -116,8 +119,8 @@ struct SharedParams {
     return {a.x, a.y, b.x, b.y, c.x, c.y, c.z, c.w};
   }
   __device__ __forceinline__ SharedSeq get_seq(int b) const {
-    const int2 v = __ldcg(reinterpret_cast<const int2*>(seqs + b));
-    return {v.x, v.y};
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(seqs + b));
+    return {v.x, v.y, v.z, v.w};
   }
   __device__ __forceinline__ PrefixRec get_rec(int x) const {
     const int4* w = reinterpret_cast<const int4*>(recs + x);

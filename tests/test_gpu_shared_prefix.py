@@ -305,3 +305,12 @@ def test_padded_batches(own):
     """Mostly padded groups, and own keys that a prefix's last key tile would outnumber."""
     check([(16, [None] * 40 + [own] * 3), (400, [own] + [None] * 70), (48, [own] * 90)], 8, 2, 64, BF16, 16, 20)
     check([(4096, [None] * 30 + [own, 2000])], 4, 2, 128, BF16, 64, 21)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_small_groups(dtype):
+    """Groups too small or prefixes too short to be shared: walked by each sequence, by the leader's table."""
+    for n in (1, 2, 3, 4, 9):
+        for pre in (16, 128, 256, 1040):
+            check([(pre, [x % 3 for x in range(n)]), (32, [None, 0, 5]), (pre, [7])], 8, 2, 64, dtype, 16, n + pre, repeat=1)
+    check([(256, [100, 30, None, 5])] * 40, 4, 2, 128, dtype, 32, 30)
