@@ -9,7 +9,7 @@ namespace {
 
 // A thread per four values of a query head; D / 4 of them a head. All but the
 // parts is known before the grids that leave them end. Bound by latency: few rows
-// have ten parts in flight, many rows fewer registers and so more warps (128 000
+// have twenty parts in flight, many rows fewer registers and so more warps (128 000
 // rows 101 us, 158 with ten). Small CTAs fit beside the decode grid's.
 constexpr int kJoinThreads = 128;
 template <typename T, int D, int BATCH, int CTAS>
@@ -22,18 +22,19 @@ __global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdP
     return;
   }
   const int b = int(row / p.Hq), h = int(row % p.Hq), g = h / p.hpg, hg = h - g * p.hpg;
+  const int64_t step0 = __ldcg(p.shared.step0 + b);  // in flight with the others
   const SharedHead head = p.shared.get_head();
-  Own own{0, 0, -1, 0, 0, false};
-  if (!head.disorder) own = own_of<true>(p, b);
+  Own own = own_of<true>(p, b);
+  own.ok &= !head.disorder;
   PrefixRows<D> pre{nullptr, nullptr, 0, 0};
   const int heads = min(p.hpg, kFdMaxHeads);
   int64_t part0 = 0;  // the parts of its own keys
   int parts = 0;
-  if (own.ok && own.L > 0) {
+  if (own.ok && own.L > 0) {  // (nothing else holds where cu_prefix is out of order)
     pre = p.shared.rows<D>(own.x, b, g, hg, head.per);
     if (const int n = own.units(4)) {
       const int it = g * p.ngr + hg / heads;
-      const int64_t at = __ldcg(p.shared.step0 + b) + int64_t(it) * n, c0 = at / head.own_per;
+      const int64_t at = step0 + int64_t(it) * n, c0 = at / head.own_per;
       part0 = int64_t(b) * p.Hkv * p.ngr + it + c0;
       parts = int((at + n - 1) / head.own_per - c0) + 1;
     }
@@ -58,8 +59,10 @@ template <typename T, int D>
 cudaError_t join(const FdParams& p, cudaStream_t stream) {
   ProfScope pf("full_join", stream);
   const int64_t ctas = (int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads;
-  return launch_early(ctas <= 8 * kNumSMs ? full_join_kernel<T, D, 10, 6> : full_join_kernel<T, D, 4, 12>, ctas, kJoinThreads,
-                      0, stream, p);
+  return launch_early(ctas <= 3 * kNumSMs   ? full_join_kernel<T, D, 20, 3>
+                      : ctas <= 8 * kNumSMs ? full_join_kernel<T, D, 10, 6>
+                                            : full_join_kernel<T, D, 4, 12>,
+                      ctas, kJoinThreads, 0, stream, p);
 }
 template <typename T, int D, int H>
 cudaError_t run(const FdParams& p, cudaStream_t stream) {

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(NT) shared_plan_kernel(const PlanParams p) {
     if (g.leader < g.b0 + g.count) g.n = n;
     return g;
   };
+  const Group first = look(threadIdx.x);  // in flight under the sequences
   // ---- sequences ----
   auto group_of = [&](int b) {  // the last group that starts at or before it, so that empty ones are passed over
     int lo = 0, n = groups;
@@ -146,7 +147,6 @@ __global__ void __launch_bounds__(NT) shared_plan_kernel(const PlanParams p) {
     steps += all[0];
   }
   const int all_heads = p.Hkv * s.geo.groups;
-  const Group first = look(threadIdx.x);
   int64_t work[2] = {0, 0}, sums[2];  // units, items
   for (int x = threadIdx.x; x < groups; x += NT) {
     const Group g = x == int(threadIdx.x) ? first : look(x);
