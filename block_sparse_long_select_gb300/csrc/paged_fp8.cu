@@ -105,6 +105,27 @@ __global__ void __launch_bounds__(kAppMostThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = few ? blockIdx.x : blockIdx.x * (kAppThreads / 32) + warp;
   const int me = few ? warp : 0, warps = few ? blockDim.x >> 5 : 1;  // of the token's warps
+  const int sub = lane / L, j = lane % L;
+  const int half = a.rot / 2 / N;  // chunks of half the rotated dims
+  const int c0 = j < half ? j : 2 * j, c1 = j < half ? j + half : 2 * j + 1;
+  // Passes of kPer rows: queries, keys, values. A batch is loaded while the one
+  // before it is worked on, and the first while the token's place is looked up.
+  const int nq = a.q ? (a.Hq + kPer - 1) / kPer : 0, nk = (a.Hkv + kPer - 1) / kPer, passes = nq + 2 * nk;
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  auto fetch = [&](TwoChunks<T>(&v)[kBatch], int p0) {
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int p = p0 + y * warps;
+      const bool is_q = p < nq, is_k = !is_q && p < nq + nk;
+      const int h = (p - (is_q ? 0 : is_k ? nq : nq + nk)) * kPer + sub, heads = is_q ? a.Hq : a.Hkv;
+      if (p < passes && h < heads)
+        v[y].load(static_cast<const T*>(is_q ? a.q : is_k ? a.k_new : a.v_new) + (int64_t(t) * heads + h) * D, c0, c1);
+      else
+        v[y].clear();
+    }
+  };
+  TwoChunks<T> next[kBatch];
+  if (t < a.T) fetch(next, me);
   int b = t;
   if (a.cu_new) {  // every warp finds its token's sequence itself
     const SeqMap m = seqs_of(a);
@@ -121,10 +142,7 @@ __global__ void __launch_bounds__(kAppMostThreads)
   const int64_t row = a.rot == 0 || pos < a.max_pos ? cache_row(a.pages, b, pos) : -1;
   if (row < 0 && me == 0 && lane == 0) set_status(&a.ws->status, MSA_ERR_BOUNDS);
 
-  const int sub = lane / L, j = lane % L;
-  const int half = a.rot / 2 / N;  // chunks of half the rotated dims
   const bool turns = j < half && row >= 0;
-  const int c0 = j < half ? j : 2 * j, c1 = j < half ? j + half : 2 * j + 1;
   float cc[N], ss[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) cc[i] = 1.f, ss[i] = 0.f;
@@ -140,21 +158,18 @@ __global__ void __launch_bounds__(kAppMostThreads)
       ss[2 * i + 1] = f.w;
     }
   }
-  constexpr int kBatch = 4;  // rows of a lane in flight
-  // ---- queries ----
-  if (a.q) {
-    const T* src = static_cast<const T*>(a.q) + int64_t(t) * a.Hq * D;
-    T* dst = static_cast<T*>(a.q_out) + int64_t(t) * a.Hq * D;
-    for (int r0 = me * kPer + sub; r0 < a.Hq + sub; r0 += kBatch * warps * kPer) {
-      TwoChunks<T> v[kBatch];
+  const int64_t page = row >> a.pages.page_log2, in_page = row & ((1 << a.pages.page_log2) - 1);
+  for (int p0 = me; p0 < passes; p0 += kBatch * warps) {
+    TwoChunks<T> v[kBatch];
 #pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        const int r = r0 + y * warps * kPer;
-        if (r < a.Hq) v[y].load(src + r * D, c0, c1);
-      }
+    for (int y = 0; y < kBatch; ++y) v[y].raw[0] = next[y].raw[0], v[y].raw[1] = next[y].raw[1];
+    if (p0 + kBatch * warps < passes) fetch(next, p0 + kBatch * warps);
 #pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        const int r = r0 + y * warps * kPer;
+    for (int y = 0; y < kBatch; ++y) {
+      const int p = p0 + y * warps;  // one kind of rows for the whole warp
+      if (p >= passes) break;
+      if (p < nq) {  // ---- queries ----
+        const int r = p * kPer + sub;
         if (r >= a.Hq) continue;
         if (row < 0) v[y].clear();
         if (turns) {
@@ -171,34 +186,15 @@ __global__ void __launch_bounds__(kAppMostThreads)
             for (int i = 0; i < N; ++i) w[i] = from_f<T>(v[y].x[z][i]);
           }
         }
-        reinterpret_cast<uint4*>(dst + r * D)[c0] = v[y].raw[0];
-        reinterpret_cast<uint4*>(dst + r * D)[c1] = v[y].raw[1];
+        T* dst = static_cast<T*>(a.q_out) + (int64_t(t) * a.Hq + r) * D;
+        reinterpret_cast<uint4*>(dst)[c0] = v[y].raw[0];
+        reinterpret_cast<uint4*>(dst)[c1] = v[y].raw[1];
+        continue;
       }
-    }
-  }
-  if (row < 0) return;
-  // ---- keys, then values ----
-  const int64_t page = row >> a.pages.page_log2, in_page = row & ((1 << a.pages.page_log2) - 1);
-  const int passes = (a.Hkv + kPer - 1) / kPer;  // of a warp, for each
-  for (int p0 = me; p0 < 2 * passes; p0 += kBatch * warps) {
-    TwoChunks<T> v[kBatch];
-#pragma unroll
-    for (int y = 0; y < kBatch; ++y) {
-      const int p = p0 + y * warps;
-      const bool is_k = p < passes;
-      const int h = (is_k ? p : p - passes) * kPer + sub;
-      const T* src = static_cast<const T*>(is_k ? a.k_new : a.v_new) + (int64_t(t) * a.Hkv + h) * D;
-      if (p < 2 * passes && h < a.Hkv)
-        v[y].load(src, c0, c1);
-      else
-        v[y].clear();
-    }
-#pragma unroll
-    for (int y = 0; y < kBatch; ++y) {
-      const int p = p0 + y * warps;
-      if (p >= 2 * passes) break;  // the whole warp's
-      const bool is_k = p < passes;
-      const int h = (is_k ? p : p - passes) * kPer + sub;
+      // ---- keys and values ----
+      if (row < 0) return;
+      const bool is_k = p < nq + nk;
+      const int h = (p - (is_k ? nq : nq + nk)) * kPer + sub;
       v[y].widen();
       if (is_k && half > 0)  // the warp's; lanes that do not turn have cos 1, sin 0
         v[y].template pairs<IL>([&](float& p, float& q, int i) {

@@ -314,3 +314,42 @@ def test_small_groups(dtype):
         for pre in (16, 128, 256, 1040):
             check([(pre, [x % 3 for x in range(n)]), (32, [None, 0, 5]), (pre, [7])], 8, 2, 64, dtype, 16, n + pre, repeat=1)
     check([(256, [100, 30, None, 5])] * 40, 4, 2, 128, dtype, 32, 30)
+
+
+def test_thousands_of_sequences():
+    """More sequences and groups than the plan's threads."""
+    groups = [(32 if x % 3 else 512, [(x + y) % 5 for y in range(1 + x % 4)]) for x in range(1100)]
+    check(groups, 2, 1, 64, BF16, 32, 31, before=[3, 0, 70])
+
+
+def test_two_calls_at_once():
+    """On two streams, a workspace each; and the same two as graphs replayed side by side."""
+    calls = []
+    for seed in (32, 33):
+        *args, want = make([(1040, [5, 70, 1] * 8), (64, [9, 300])], 8, 2, 128, BF16, 16, seed)
+        ws = workspace(26, 2, args[3], 16, 2, 8, 128, BF16)
+        calls.append(([x.to(DEV) for x in args], want, ws, torch.empty(26, 8, 128, dtype=BF16, device=DEV),
+                      torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(12):
+        args, _, ws, out, s = calls[i % 2]
+        msa.msa_full_attn_decode_shared(*args, out=out, ws=ws, stream=s)
+    torch.cuda.synchronize()
+    for args, want, ws, out, s in calls:
+        assert msa.msa_read_status(ws) == 0
+        fp.assert_within(out, want[0], want[2], "out")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+            for _ in range(3):
+                msa.msa_full_attn_decode_shared(*args, out=out, ws=ws)
+        graphs.append(graph)
+        out.zero_()
+    torch.cuda.synchronize()
+    for i in range(12):
+        with torch.cuda.stream(calls[i % 2][4]):
+            graphs[i % 2].replay()
+    torch.cuda.synchronize()
+    for args, want, ws, out, s in calls:
+        assert msa.msa_read_status(ws) == 0
+        fp.assert_within(out, want[0], want[2], "replayed")
