@@ -220,7 +220,7 @@ template <typename C>
 struct FdShape {
   static constexpr int kWarps = C::kWarps, kThreads = kWarps * 32;
   static constexpr int kStep = C::kTiles * kSub, kUnit = kWarps * kStep;  // keys of a warp's step, of a unit
-  static constexpr int kStepLog2 = C::kTiles == 1 ? 4 : 5, kUnitLog2 = kStepLog2 + (kWarps == 8 ? 3 : 2);
+  static constexpr int kStepLog2 = C::kTiles == 1 ? 4 : C::kTiles == 2 ? 5 : 6, kUnitLog2 = kStepLog2 + (kWarps == 8 ? 3 : 2);
   static_assert(1 << kStepLog2 == kStep && 1 << kUnitLog2 == kUnit, "keys of a step and of a unit");
   static constexpr int kStages = C::kStages;
   static constexpr int kRing = kStages * C::kStage;      // per warp
@@ -556,20 +556,21 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   }
 }
 
-template <typename C, bool SHARED>
+template <typename C>
+__global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_shared_kernel(const __grid_constant__ typename C::Params p) {
+  tc::griddep_launch_dependents();  // the joins' grid, which waits for this one
+  decode_run<C, false, true>(p, 0);
+  tc::griddep_wait();  // this grid is not over before the prefixes' grid is
+}
+
+template <typename C>
 __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(const __grid_constant__ typename C::Params p) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
   constexpr int kFdWarps = SH::kWarps, kFdThreads = SH::kThreads;
   const int lane = threadIdx.x & 31, items = p.Hkv * p.ngr;
-  [[maybe_unused]] T* out = static_cast<T*>(p.out);
-  if constexpr (SHARED) {
-    tc::griddep_launch_dependents();  // the joins' grid, which waits for this one
-    decode_run<C, false, true>(p, 0);
-    tc::griddep_wait();  // this grid is not over before the prefixes' grid is
-    return;
-  }
+  T* out = static_cast<T*>(p.out);
   if constexpr (C::kBulk) {
     extern __shared__ __align__(1024) uint8_t fd_smem[];
     if (tc::smem_u32(fd_smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   int longest = 0;  // in warps' steps
 #pragma unroll 8
   for (int b = lane; b < p.B; b += 32) {
-    const int steps = units_of<SHARED>(p, b, SH::kStepLog2);
+    const int steps = units_of<false>(p, b, SH::kStepLog2);
     total += (steps + kFdWarps - 1) / kFdWarps;
     longest = max(longest, steps);
   }
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
   // sequences without keys: nobody's run holds them
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Own o = own_of<SHARED>(p, b);
+    const Own o = own_of<false>(p, b);
     if (o.units(SH::kStepLog2) > 0) continue;
     if (threadIdx.x == 0 && !o.ok) set_status(p.status, MSA_ERR_BOUNDS);
     for (int x = threadIdx.x; x < p.Hq * D; x += kFdThreads) out[int64_t(b) * p.Hq * D + x] = from_f<T>(0.f);
@@ -618,9 +619,9 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
       for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
   }
   if (solo)
-    decode_run<C, true, SHARED>(p, total);
+    decode_run<C, true, false>(p, total);
   else
-    decode_run<C, false, SHARED>(p, total);
+    decode_run<C, false, false>(p, total);
 }
 
 int fd_grid() { return kNumSMs; }
@@ -628,17 +629,23 @@ int fd_grid() { return kNumSMs; }
 // SHARED: the grid may start while the one before it ends
 template <typename C, bool SHARED>
 cudaError_t decode(const typename C::Params& p, const char* name, cudaStream_t stream) {
-  auto kern = full_decode_kernel<C, SHARED>;
+  constexpr auto kern = [] {
+    if constexpr (SHARED)
+      return full_decode_shared_kernel<C>;
+    else
+      return full_decode_kernel<C>;
+  }();
   constexpr int bytes = FdShape<C>::kBytes;
   static_assert(bytes <= 227 * 1024 - 16, "shared memory of one CTA");
   static KernelReady ready;
   if (cudaError_t e = ready.on_device(reinterpret_cast<const void*>(kern), bytes)) return e;
   ProfScope pf(name, stream);
-  if constexpr (!SHARED) {
+  if constexpr (SHARED) {
+    return launch_early(kern, fd_grid(), FdShape<C>::kThreads, bytes, stream, p);
+  } else {
     kern<<<fd_grid(), FdShape<C>::kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
   }
-  return launch_early(kern, fd_grid(), FdShape<C>::kThreads, bytes, stream, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -382,12 +382,15 @@ cudaError_t run(const Fd8Params& p, cudaStream_t stream) {
   return decode<C, false>(p, "full_decode_fp8", stream);
 }
 // Up to 8 query heads to a key/value head: a step has two tiles, of neighbouring
-// heads or of 32 keys, and for d 64 four of both. More: two of keys.
+// heads or of 32 keys, for d 64 four (a step's waits and look-ups cost as much as
+// for d 128: one key/value head 456 us, with two tiles 559). More: two of keys.
+// d 64 does not reach HBM's rate, 5.3 TB/s: the scores and weights of a key take
+// as long as for d 128, its bytes half. (Four heads of one tile: 4.9.)
 template <int D>
 cudaError_t run_bf16(Fd8Params& p, cudaStream_t stream) {
   using T = __nv_bfloat16;
   if (p.group > 8) return run<Core8<T, D, 16, 2, 1>>(p, stream);
-  if (p.kv_heads % 2) return run<Core8<T, D, 8, 2, 1>>(p, stream);
+  if (p.kv_heads % 2) return run<Core8<T, D, 8, D == 64 ? 4 : 2, 1>>(p, stream);
   p.Hkv = p.kv_heads / 2;  // pairs, as the items' heads
   p.hpg = 2 * p.group;
   p.ngr = 1;

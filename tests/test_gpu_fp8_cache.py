@@ -212,6 +212,13 @@ def test_decode_heads(heads, dtype):
     check_decode([40, 1, 530], *heads, dtype, 16, 5)
 
 
+@pytest.mark.parametrize("heads", [(3, 3, 64), (8, 1, 64), (32, 1, 64), (9, 3, 128)])
+def test_decode_ends_of_steps(heads):
+    """Lengths about the ends of 16-key tiles and of a warp's 32- or 64-key steps, with an odd number of heads."""
+    check_decode([31, 32, 33, 47, 48, 49, 63, 64, 65, 0, 79, 80, 81, 511, 512, 513, 575, 1089], *heads, BF16, 16, 14)
+    check_decode([(29 * b) % 150 for b in range(500)], *heads, BF16, 32, 15)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_scales_and_sizes(d, dtype):

@@ -353,3 +353,15 @@ def test_two_calls_at_once():
     for args, want, ws, out, s in calls:
         assert msa.msa_read_status(ws) == 0
         fp.assert_within(out, want[0], want[2], "replayed")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_caches_past_32_bits(dtype):
+    """Prefix and own pages beyond 2^32 bytes."""
+    *args, want = make([(2048, [5, 300, 1] * 3)], 8, 8, 128, dtype, 128, 34)
+    q, kc, vc, table, kv, cu, pre = [x.to(DEV) for x in args]
+    pages = kc.shape[0] + (5 << 30) // (128 * 8 * 128 * dtype.itemsize)
+    there = lambda x: torch.cat([torch.empty(pages - x.shape[0], *x.shape[1:], dtype=dtype, device=DEV), x])  # noqa: E731
+    table = torch.where((table >= 0) & (table < kc.shape[0]), table + (pages - kc.shape[0]), table).to(torch.int32)
+    out = msa.msa_full_attn_decode_shared(q, there(kc), there(vc), table, kv, cu, pre)
+    fp.assert_within(out, want[0], want[2], "out")
