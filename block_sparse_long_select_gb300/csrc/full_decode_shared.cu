@@ -1,7 +1,11 @@
 // Decode over shared prefixes: each sequence's own keys by the decode kernel's
 // walk (full_decode.cuh), and the join of its parts with those that the
 // prefixes' grid left (full_prefix_tc.cu, full_prefix_fp32.cu). Each of the three
-// grids starts while the one before it ends.
+// grids starts while the one before it ends. Bound: HBM while both walks run, and
+// about 20 us of plan, first loads and joins. Measured, whole calls (Hq 32, Hkv 8,
+// d 128, bf16; bytes that have to be read at the copy rate: 87, 87, 7 us): 97
+// sequences of 1300 own keys behind three prefixes, 20 K keys, 109 us; 24 behind
+// 128 K keys 106; 32 of 100 behind 8 K 28.
 #include "full_decode_cores.cuh"
 
 namespace msa {

