@@ -593,7 +593,7 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 
 PrefixGeometry prefix_geometry_tc(int hpg) {
   const int tpt = kRows / hpg;
-  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2, 24, 8};
+  return {hpg, 1, 2 * tpt, tpt, 2 * kRows, kNumSMs, 2, 24, 4};
 }
 
 cudaError_t launch_prefix_tc(const SharedArgs& a, cudaStream_t stream) {

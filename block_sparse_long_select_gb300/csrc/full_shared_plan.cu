@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(NT) shared_plan_kernel(const PlanParams p) {
   // Whether a prefix of n key tiles is worth an item's start and end (bf16: about 7 us
   // beside 1.1 us a tile; a sequence walks a tile in as much by itself, out of L2
   // from the second on). 512 sequences of 200 keys, each a group behind 512: 374 us
-  // as items, 279 by themselves; 64 in sixteen groups behind 2048: 69 and 70 us.
+  // as items, 279 by themselves; 4000 of 100 keys in 1000 groups of about four behind
+  // 256: 646 with all groups of three as items (`worth` 4), 679 (6), 738 (8), 894 (16).
   auto worth = [&](int count, int n) { return int64_t(n) * (count - 1) >= s.geo.worth; };
   auto look = [&](int x) {
     Group g{0, 0, 0, 0};
