@@ -7,10 +7,11 @@
 //
 // Work: the keys of every (sequence, key/value head, group of up to 16 query
 // heads) -- an item -- are cut into units of 128 (16 per warp; 64 for fp32 of d
-// 128, which has four warps; 256 for caches in 8 bits, 32 per warp), the units of all items are numbered through, and
-// each CTA of a fixed grid (one per SM) takes an equal run of them, so ragged
-// lengths balance whatever they are, without the host knowing them.
-// In a unit each warp takes 16 keys, which lie in one page (or two such tiles), and works alone:
+// 128, which has four warps; caches in 8 bits: 16 to 64 per warp), the units of
+// all items are numbered through, and each CTA of a fixed grid (one per SM) takes
+// an equal run of them, so ragged lengths balance whatever they are, without the
+// host knowing them.
+// In a unit each warp takes 16 keys, which lie in one page (in 8 bits one to four such tiles), and works alone:
 // its own ring of copies (cp.async, keys past the end arriving as zeros, or TMA
 // with bounded waits), scores, running maximum and sum, products. Warps meet only where an item ends in the
 // CTA: their states are joined in shared memory. An item that lies in several
@@ -353,17 +354,18 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       }
       if constexpr (C::kBulk) {
         if (lane == 0) {
-          int tiles = 0;
+          const int box = C::kTiles == 1 ? 1 : 1 << (C::box_of(p) - 4);  // tiles of a copy, which lie in one page
+          int boxes = 0;
 #pragma unroll
-          for (int x = 0; x < C::kTiles; ++x) tiles += in[x];
-          if (tiles)
-            tc::mbar_arrive_expect_tx(bars + st, tiles * C::kTileBytes);
+          for (int x = 0; x < C::kTiles; ++x) boxes += in[x] && (x & (box - 1)) == 0;
+          if (boxes)
+            tc::mbar_arrive_expect_tx(bars + st, boxes * box * C::kTileBytes);
           else
             tc::mbar_arrive(bars + st);
 #pragma unroll
           for (int x = 0; x < C::kTiles; ++x)
-            if (in[x])
-              C::copy(p, ring, extra, st * C::kTiles + x, bars + st, page[x],
+            if (in[x] && (x & (box - 1)) == 0)
+              C::copy(p, ring + st * C::kStage, extra, st, x, bars + st, page[x],
                       (key0 + x * kSub) & ((1 << p.pages.page_log2) - 1), g);
         }
         ++issued;
@@ -417,7 +419,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
     bad |= (bad_ring >> st) & 1u;
     int valid = at.own.L - (at.from() + (at.u << ulog) + sub0);
     if (C::kBulk && dead) valid = 0;
-    if (valid > 0) c.step(ring + st * C::kStage, extra, st, valid, p.scale_log2);
+    if (valid > 0) c.step(p, ring + st * C::kStage, extra, st, valid);
     __syncwarp();
     st = (st + 1) % NS;
     const int b = at.b, n = at.n;

@@ -67,7 +67,8 @@ struct Core<__nv_bfloat16, D, H> {
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
-  __device__ __forceinline__ void step(uint32_t kt, uint32_t, int, int valid, float scale_log2) {
+  __device__ __forceinline__ void step(const Params& p, uint32_t kt, uint32_t, int, int valid) {
+    const float scale_log2 = p.scale_log2;
     const int lane = threadIdx.x & 31, gq = lane >> 2;
     const uint32_t vt = kt + kTile;
     float s[HN][4];
@@ -202,7 +203,8 @@ struct Core<float, D, H> {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
   }
-  __device__ __forceinline__ void step(uint32_t kt, uint32_t extra, int, int valid, float scale_log2) {
+  __device__ __forceinline__ void step(const Params& p, uint32_t kt, uint32_t extra, int, int valid) {
+    const float scale_log2 = p.scale_log2;
     const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
     const uint32_t vt = kt + kTile, ps = extra + H * D * 4;
     float s[H];

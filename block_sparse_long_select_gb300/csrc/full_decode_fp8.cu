@@ -6,7 +6,7 @@
 // Bound: HBM, d + 4 bytes per key and per value where bf16 takes 2 d. Walk,
 // copies and joins: full_decode.cuh. Measured (Hq 32, Hkv 8, d 128, bf16): 16
 // sequences of 4 K to 128 K keys 303 to 319 us, 6.2 to 6.6 TB/s (92 to 97 % of the
-// copy rate); one of 777 keys 10.5 us, latency. d 64: 5.0 to 5.3 TB/s, instructions.
+// copy rate); one of 777 keys 10.7 us, latency. d 64: 6.0 to 6.6 TB/s, instructions.
 //
 // Products: mma.sync m16n8k16 in f16, which holds every e4m3 code exactly (bf16
 // would as well, but the hardware converts e4m3 to f16 in one instruction for
@@ -24,6 +24,8 @@
 #include "full_decode.cuh"
 
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 namespace msa {
 namespace {
@@ -79,7 +81,9 @@ __device__ __forceinline__ float lds1(uint32_t a) {
 }
 
 struct Fd8Params : FdParams {
-  CUtensorMap tmK, tmV;  // codes as [rows][Hkv][d] bytes, boxes of 16 rows of a head
+  CUtensorMap tmK, tmV;    // codes as [rows][Hkv][d] bytes, boxes of rows of a head
+  CUtensorMap tmKs, tmVs;  // scales as [pages][Hkv][page_size], boxes of the same rows of a pair of heads (d 64)
+  int box_log2;            // rows of a box: those of a step, if they lie in one page
   int kv_heads, group;   // key/value heads, query heads of one: what Hkv and hpg say of pairs where those are items
   int inject_timeout;    // test hook: a warp of every second CTA waits on a barrier nothing completes
 };
@@ -95,13 +99,19 @@ struct Core8 {
   static constexpr bool kBulk = true;
   static constexpr int kD = D, kWarps = 8, kTiles = KT;
   static constexpr int HN = (H + 7) / 8, kTerms = sizeof(T) == 4 ? 2 : 1, kCols = HT * HN;  // columns of 8 heads
-  // a stage: for every tile of keys and head K codes | V codes; beside the ring, likewise, 16 K scales | 16 V scales
-  static constexpr int kTile = kSub * D, kScales = 2 * kSub * 4, kBoth = KT * HT;
-  static constexpr int kStage = kBoth * 2 * kTile, kTileBytes = HT * (2 * kTile + kScales);
+  // a stage: for every head K codes | V codes of the step's keys; beside the ring K scales | V scales, of a box's heads in turn
+  static constexpr int kTile = kSub * D, kScales = 2 * kSub * 4, kBoth = KT * HT, kHead = 2 * KT * kTile;
+  static constexpr int kStage = HT * kHead, kTileBytes = HT * (2 * kTile + kScales);  // bytes of a tile with its scales
   static constexpr int kM = 2 * kCols, kAcc = kCols * D / 4, kWords = D / 16;  // 4-byte words of a lane's quarter of a row
   static constexpr int kStages = (227 * 1024 - 8 * (2 * kM + 1) * 128 - 512) / (8 * (kStage + kBoth * kScales));
   static_assert(kStages >= 2 && (H <= 8 || HT == 1) && HT * H <= kFdMaxHeads, "items");
   static constexpr int kExtra = kStages * kBoth * kScales;
+  // A copy takes an instruction stream of one lane, a third of all instructions for
+  // d 64, where few bytes hide them: there a copy takes the step's rows as far as
+  // they lie in one page, and both heads' scales (32 sequences of 64 K keys, Hq 32, Hkv 8:
+  // 355 us, 433 with 16 rows and a head's scales to a copy; pages of 16: 390). For
+  // d 128 the large copies come in slower (16 sequences: 368 us, 352 with the small ones).
+  static constexpr bool kBig = D == 64, kPairScales = kBig && HT == 2;
   uint32_t qf[kCols][kTerms][kWords][2];
   float qs[kM];  // the scores' factors: scale, log2 e and the queries' power of two
   float m[kM], l[kM], mw[kM], acc[kAcc];  // acc[(t * D / 16 + mt) * 4 + e]; mw: less kTop
@@ -117,26 +127,44 @@ struct Core8 {
   __device__ __forceinline__ static void prefetch(const Params& p) {
     tc::tma_prefetch(&p.tmK);
     tc::tma_prefetch(&p.tmV);
-  }
-  // tile x of keys in the ring (one thread); g: the item's key/value head or pair
-  __device__ __forceinline__ static void copy(const Params& p, uint32_t ring, uint32_t extra, int x, uint64_t* bar, int page,
-                                              int row, int g) {
-    const int r0 = (page << p.pages.page_log2) + row;
-#pragma unroll
-    for (int y = 0; y < HT; ++y) {
-      const int at = x * HT + y, head = g * HT + y;
-      const int64_t sc = ((int64_t(page) * p.kv_heads + head) << p.pages.page_log2) + row;  // scales: [page][head][row]
-      tma_tile(ring + at * 2 * kTile, &p.tmK, bar, head, r0);
-      tma_tile(ring + at * 2 * kTile + kTile, &p.tmV, bar, head, r0);
-      tc::bulk_load(extra + at * kScales, p.k_scale + sc, kScales / 2, bar);
-      tc::bulk_load(extra + at * kScales + kScales / 2, p.v_scale + sc, kScales / 2, bar);
+    if constexpr (kPairScales) {
+      tc::tma_prefetch(&p.tmKs);
+      tc::tma_prefetch(&p.tmVs);
     }
   }
-  __device__ __forceinline__ static void tma_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int g, int r0) {
+  __device__ __forceinline__ static int box_of(const Params& p) { return kBig ? p.box_log2 : 4; }
+  // the box that begins with tile x of a stage (one thread); g: the item's key/value head or pair
+  __device__ __forceinline__ static void copy(const Params& p, uint32_t stage, uint32_t extra, int st, int x, uint64_t* bar,
+                                              int page, int row, int g) {
+    const int r0 = (page << p.pages.page_log2) + row;
+    extra += st * kBoth * kScales + x * HT * kSub * 4;
+#pragma unroll
+    for (int z = 0; z < HT; ++z) {
+      const int head = g * HT + z;
+      tma_tile(stage + z * kHead + x * kTile, &p.tmK, bar, 0, head, r0);
+      tma_tile(stage + z * kHead + (KT + x) * kTile, &p.tmV, bar, 0, head, r0);
+      if constexpr (!kPairScales) {
+        const int64_t sc = ((int64_t(page) * p.kv_heads + head) << p.pages.page_log2) + row;  // scales: [page][head][row]
+        const uint32_t bytes = 4 << box_of(p);
+        tc::bulk_load(extra + z * bytes, p.k_scale + sc, bytes, bar);
+        tc::bulk_load(extra + z * bytes + kBoth * kScales / 2, p.v_scale + sc, bytes, bar);
+      }
+    }
+    if constexpr (kPairScales) {
+      tma_tile(extra, &p.tmKs, bar, row, g * HT, page);
+      tma_tile(extra + kBoth * kScales / 2, &p.tmVs, bar, row, g * HT, page);
+    }
+  }
+  // where key k of head z of a step has its K scale
+  __device__ __forceinline__ static uint32_t scale_at(const Params& p, uint32_t extra, int z, int k) {
+    if constexpr (KT == 1 || HT == 1) return extra + (z * kSub * KT + k) * 4;
+    return extra + (((((k >> box_of(p)) * HT) + z) << box_of(p)) + (k & ((1 << box_of(p)) - 1))) * 4;
+  }
+  __device__ __forceinline__ static void tma_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
         "[%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(0), "r"(g), "r"(r0)
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
   }
   // B fragments of the scores: lane (gq, tq) has dims [tq D / 4, ...) of head gq
@@ -182,24 +210,25 @@ struct Core8 {
 #pragma unroll
     for (int x = 0; x < kAcc; ++x) acc[x] = 0.f;
   }
-  __device__ __forceinline__ void step(uint32_t stage, uint32_t extra, int st, int valid, float) {
+  __device__ __forceinline__ void step(const Params& p, uint32_t stage, uint32_t extra, int st, int valid) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     extra += st * kBoth * kScales;
     if (valid < KT * kSub) {
       // rows behind the end may hold anything, and weight 0 does not silence a NaN: they and their scales become zeros
       for (int x = lane; x < kBoth * kTile / 16; x += 32) {
-        const int at = x / (kTile / 16), r = x % (kTile / 16) / (D / 16);
-        const uint32_t at_k = stage + at * 2 * kTile + x % (kTile / 16) * 16;
-        if ((at / HT) * kSub + r >= valid)
+        const int z = x / (KT * kTile / 16), in_head = x % (KT * kTile / 16);
+        const uint32_t at_k = stage + z * kHead + in_head * 16;
+        if (in_head / (D / 16) >= valid)
           asm volatile("st.shared.v4.b32 [%0], {%2, %2, %2, %2};\n\tst.shared.v4.b32 [%1], {%2, %2, %2, %2};" ::"r"(at_k),
-                       "r"(at_k + kTile), "r"(0)
+                       "r"(at_k + KT * kTile), "r"(0)
                        : "memory");
       }
       for (int x = lane; x < kBoth * kSub; x += 32) {
-        const int at = x / kSub, r = x % kSub;
-        const uint32_t at_s = extra + at * kScales + r * 4;
-        if ((at / HT) * kSub + r >= valid)
-          asm volatile("st.shared.b32 [%0], %2;\n\tst.shared.b32 [%1], %2;" ::"r"(at_s), "r"(at_s + kScales / 2), "r"(0)
+        const int k = x % (KT * kSub);
+        const uint32_t at_s = scale_at(p, extra, x / (KT * kSub), k);
+        if (k >= valid)
+          asm volatile("st.shared.b32 [%0], %2;\n\tst.shared.b32 [%1], %2;" ::"r"(at_s), "r"(at_s + kBoth * kScales / 2),
+                       "r"(0)
                        : "memory");
       }
       tc::fence_proxy_async_smem();  // before the next copy into the stage
@@ -210,7 +239,7 @@ struct Core8 {
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int z = 0; z < HT; ++z) {
-        const uint32_t kt = stage + (i * HT + z) * 2 * kTile, sc = extra + (i * HT + z) * kScales;
+        const uint32_t kt = stage + z * kHead + i * kTile, sc = scale_at(p, extra, z, i * kSub) + gq * 4;
 #pragma unroll
         for (int t = z * HN; t < (z + 1) * HN; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
 #pragma unroll
@@ -228,8 +257,8 @@ struct Core8 {
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          lv[i][z][y] = lg2(lds1(sc + kScales / 2 + gq * 4 + 32 * y));
-          const float ks = lds1(sc + gq * 4 + 32 * y), hidden = i * kSub + gq + 8 * y < valid ? 0.f : -INFINITY;
+          lv[i][z][y] = lg2(lds1(sc + kBoth * kScales / 2 + 32 * y));
+          const float ks = lds1(sc + 32 * y), hidden = i * kSub + gq + 8 * y < valid ? 0.f : -INFINITY;
 #pragma unroll
           for (int t = z * HN; t < (z + 1) * HN; ++t)
 #pragma unroll
@@ -272,7 +301,7 @@ struct Core8 {
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int z = 0; z < HT; ++z) {
-        const uint32_t vt = stage + (i * HT + z) * 2 * kTile + kTile;
+        const uint32_t vt = stage + z * kHead + (KT + i) * kTile;
         uint32_t b[HN][kTerms][2];
 #pragma unroll
         for (int n = 0; n < HN; ++n) {
@@ -372,36 +401,51 @@ struct Core8 {
   __device__ __forceinline__ static int m_index(int x) { return 2 * (x / (D / 4)) + (x & 1); }
 };
 
-bool map_codes(CUtensorMap* m, const void* p, uint64_t rows, int Hkv, int d) {
+bool map_codes(CUtensorMap* m, const void* p, uint64_t rows, int Hkv, int d, int box_rows) {
   const uint64_t D = d;
   const uint64_t dims[3] = {D, uint64_t(Hkv), rows};
   const uint64_t strides[2] = {D, D * Hkv};
-  const uint32_t box[3] = {uint32_t(d), 1, kSub};
+  const uint32_t box[3] = {uint32_t(d), 1, uint32_t(box_rows)};
   return make_tmap_u8(m, p, 3, dims, strides, box, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
-template <typename C>
-cudaError_t run(const Fd8Params& p, cudaStream_t stream) {
+bool map_scales(CUtensorMap* m, const float* p, const PageMap& pages, int Hkv, int box_rows) {
+  const uint64_t size = uint64_t(1) << pages.page_log2;
+  const uint64_t dims[3] = {size, uint64_t(Hkv), uint64_t(pages.num_pages)};
+  const uint64_t strides[2] = {size * 4, size * 4 * Hkv};
+  const uint32_t box[3] = {uint32_t(box_rows), 2, 1};
+  return make_tmap_f32(m, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+template <typename T, int D, int H, int KT, int HT>
+cudaError_t run(Fd8Params& p, cudaStream_t stream) {
+  using C = Core8<T, D, H, KT, HT>;
+  p.box_log2 = C::kBig ? std::min(p.pages.page_log2, FdShape<C>::kStepLog2) : 4;
+  const int box = 1 << p.box_log2;
+  const uint64_t rows = uint64_t(p.pages.num_pages) << p.pages.page_log2;
+  if (!map_codes(&p.tmK, p.k, rows, p.kv_heads, D, box) || !map_codes(&p.tmV, p.v, rows, p.kv_heads, D, box))
+    return cudaErrorInvalidValue;
+  if (C::kPairScales && (!map_scales(&p.tmKs, p.k_scale, p.pages, p.kv_heads, box) || !map_scales(&p.tmVs, p.v_scale, p.pages, p.kv_heads, box)))
+    return cudaErrorInvalidValue;
   return decode<C, false>(p, "full_decode_fp8", stream);
 }
 // Up to 8 query heads to a key/value head: a step has two tiles, of neighbouring
 // heads or of 32 keys, for d 64 four (a step's waits and look-ups cost as much as
-// for d 128: one key/value head 456 us, with two tiles 559). More: two of keys.
-// d 64 does not reach HBM's rate, 5.3 TB/s: the scores and weights of a key take
-// as long as for d 128, its bytes half. (Four heads of one tile: 4.9.)
+// for d 128: one key/value head 456 us, with two tiles 559, before copies took whole steps). More: two of keys.
+// d 64: 6.0 to 6.6 TB/s (a key's scores and weights take as long as for d 128, its
+// bytes half; four heads of one tile instead of two of two: 7 % slower).
 template <int D>
 cudaError_t run_bf16(Fd8Params& p, cudaStream_t stream) {
   using T = __nv_bfloat16;
-  if (p.group > 8) return run<Core8<T, D, 16, 2, 1>>(p, stream);
-  if (p.kv_heads % 2) return run<Core8<T, D, 8, D == 64 ? 4 : 2, 1>>(p, stream);
+  if (p.group > 8) return run<T, D, 16, 2, 1>(p, stream);
+  if (p.kv_heads % 2) return run<T, D, 8, D == 64 ? 4 : 2, 1>(p, stream);
   p.Hkv = p.kv_heads / 2;  // pairs, as the items' heads
   p.hpg = 2 * p.group;
   p.ngr = 1;
-  return run<Core8<T, D, 8, D == 64 ? 2 : 1, 2>>(p, stream);
+  return run<T, D, 8, D == 64 ? 2 : 1, 2>(p, stream);
 }
 // fp32 queries are two terms, whose registers leave no room for pairs
 template <int D>
-cudaError_t run_f32(const Fd8Params& p, cudaStream_t stream) {
-  return p.group > 8 ? run<Core8<float, D, 16, 2, 1>>(p, stream) : run<Core8<float, D, 8, 2, 1>>(p, stream);
+cudaError_t run_f32(Fd8Params& p, cudaStream_t stream) {
+  return p.group > 8 ? run<float, D, 16, 2, 1>(p, stream) : run<float, D, 8, 2, 1>(p, stream);
 }
 
 }  // namespace
@@ -414,8 +458,6 @@ cudaError_t launch_full_decode_fp8(const FullArgs& a, const float* k_scale, cons
   p.kv_heads = p.Hkv;
   p.group = p.hpg;
   p.inject_timeout = debug_inject_timeout() ? 1 : 0;
-  const uint64_t rows = uint64_t(a.pages.num_pages) << a.pages.page_log2;
-  if (!map_codes(&p.tmK, a.k, rows, a.Hkv, a.d) || !map_codes(&p.tmV, a.v, rows, a.Hkv, a.d)) return cudaErrorInvalidValue;
   if (a.dtype == MSA_BF16) return a.d == 128 ? run_bf16<128>(p, stream) : run_bf16<64>(p, stream);
   return a.d == 128 ? run_f32<128>(p, stream) : run_f32<64>(p, stream);
 }
