@@ -134,7 +134,9 @@ msa_status_t check_decode(FullArgs& a, bool& empty, const void* q, const void* k
 
 size_t full_ws_bytes(int op, int B, int Nq, int Nk, int Hkv, int Hq, int d, int dtype) {
   if (B < 1 || Nk < 0 || check_heads(Hq, Hkv, d, dtype) != MSA_OK) return 0;
-  if (op == MSA_OP_FULL_DECODE || op == MSA_OP_FULL_DECODE_FP8) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
+  if (op == MSA_OP_FULL_DECODE) return rows_ok(B, Hq) ? kWsHeader + full_decode_ws_bytes(d) : 0;
+  if (op == MSA_OP_FULL_DECODE_FP8)
+    return rows_ok(B, Hq) ? kWsHeader + full_decode_fp8_ws_bytes(Hkv, Hq / Hkv, d, dtype) : 0;
   if (op == MSA_OP_FULL_DECODE_SHARED) {
     if (!rows_ok(B, Hq) || Nq < 0 || Nq > B) return 0;
     return kWsHeader + (Nq == 0 ? full_decode_ws_bytes(d) : full_shared_ws_bytes(B, Nq, Hkv, Hq / Hkv, d, dtype));
@@ -242,7 +244,7 @@ extern "C" msa_status_t msa_full_attn_decode_fp8(const void* q, const void* k_ca
                                        page_size, max_pages, scale, dtype, out, lse);
   if (st != MSA_OK || empty) return st;
   if (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)) return MSA_ERR_INVALID_ARG;
-  const msa_status_t w = check_full_ws(ws, ws_bytes, kWsHeader + full_decode_ws_bytes(d));
+  const msa_status_t w = check_full_ws(ws, ws_bytes, kWsHeader + full_decode_fp8_ws_bytes(Hkv, Hq / Hkv, d, dtype));
   a.ws = ws;
   return w != MSA_OK ? w : launched(launch_full_decode_fp8(a, k_scale, v_scale, stream));
 }

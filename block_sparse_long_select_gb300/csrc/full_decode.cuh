@@ -18,7 +18,9 @@
 // CTAs leaves a partial (maximum, sum, unnormalised output) per CTA, and the
 // CTA that arrives last joins them in the order of the keys.
 // Many short items: their ends would cost more than their keys (a join takes as
-// long as a unit), so single warps take whole items instead, with nothing to join.
+// long as a unit), so single warps take whole items instead, with nothing to join, or
+// (caches in 8 bits) equal runs of the steps of all items: at the end each CTA joins
+// the items that lie in several of its warps, and the last CTA those that lie in several.
 #pragma once
 
 #include "full_shared.cuh"
@@ -29,6 +31,9 @@ namespace {
 
 constexpr int kSub = 16;                  // keys of a tile: never across a page
 constexpr int kFdMaxHeads = 16;           // query heads of an item
+// What an item's beginning and end count beside its steps where warps take runs of
+// them (1000 sequences of 10 to 120 keys: 0 steps 74 us, 2 57, 4 58, 7 59).
+constexpr int kFdItemSteps = 2;
 constexpr float kFdLog2e = 1.4426950408889634f, kFdLn2 = 0.6931471805599453f;
 // The maximum only moves when a step exceeds it by 2^8: weights stay below
 // 2^8 and their common factor drops out in the division by their sum.
@@ -239,10 +244,24 @@ struct FdShape {
   static constexpr int kBytes = kFlags + 16;
 };
 
-// SOLO: whole items for single warps; SHARED: the warp's run of the `total` steps
-// of 16 keys; else the CTA's run of the `total` units.
-template <typename C, bool SOLO, bool SHARED>
-__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total) {
+// Steps of a warp's run of `total`
+template <typename C>
+__device__ __forceinline__ int64_t run_steps(int64_t total) {
+  const int64_t runs = int64_t(gridDim.x) * C::kWarps;
+  return (total + runs - 1) / runs;
+}
+// An item of which a warp has the beginning or (the CTA's first warp) a later part.
+struct SplitItem {
+  int64_t first;  // number of its first step
+  int n;          // its steps; 0: none
+  int row, heads; // its first row of the output, its heads
+};
+
+// SOLO: whole items for single warps; SHARED, RUNS: the warp's run of the `total`
+// steps; else the CTA's run of the `total` units. RUNS: `begun` is the item that
+// begins in the run and goes on behind it, `came` the one that goes on into it.
+template <typename C, bool SOLO, bool SHARED, bool RUNS>
+__device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t total, SplitItem& came, SplitItem& begun) {
   using SH = FdShape<C>;
   using T = typename C::T;
   constexpr int D = C::kD;
@@ -256,12 +275,16 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   const int items = p.Hkv * p.ngr;
   T* out = static_cast<T*>(p.out);
 
-  constexpr bool ALONE = SOLO || SHARED;
+  constexpr bool ALONE = SOLO || SHARED || RUNS;
   constexpr int ulog = ALONE ? SH::kStepLog2 : SH::kUnitLog2;
   const int hop = SOLO ? int(gridDim.x) * kFdWarps : 0, sub0 = ALONE ? 0 : warp * SH::kStep;
   // SHARED: runs in the order of the SMs, so that few of them lie on many; other SMs may be the prefixes'
   int run = blockIdx.x;
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if constexpr (RUNS) {
+    run = blockIdx.x * kFdWarps + warp;
+    per = run_steps<C>(total);
+  }
   if constexpr (SHARED) {
     const SharedHead head = p.shared.get_head();
     if (head.disorder || int(blockIdx.x) >= head.own_ctas) return;
@@ -274,6 +297,8 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   Walk<SHARED> at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
   int64_t item_first = 0;  // number of the item's first unit
+  constexpr int E = RUNS ? kFdItemSteps : 0;  // counted ahead of an item's own
+  int skip = 0;            // of those at the run's beginning
   if constexpr (SOLO) {
     at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop, ulog);
   } else {
@@ -286,7 +311,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int mine = ahead;
         ahead = b0 + 32 + lane < p.B ? units_of<SHARED>(p, b0 + 32 + lane, ulog) : 0;  // in flight during the scan
-        int64_t incl = int64_t(mine) * items;
+        int64_t incl = mine > 0 ? int64_t(mine + E) * items : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -297,7 +322,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
           const int src = __ffs(hit) - 1;
           at.b = b0 + src;
           at.n = __shfl_sync(0xffffffffu, mine, src);
-          first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n) * items;
+          first += __shfl_sync(0xffffffffu, incl, src) - int64_t(at.n + E) * items;
           break;
         }
         first += __shfl_sync(0xffffffffu, incl, 31);
@@ -305,16 +330,19 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
     }
     at.own = own_of<SHARED>(p, at.b);
     if constexpr (SHARED) at.n = at.own.units(ulog);
-    const int it = int((run0 - first) / at.n);
+    const int it = int((run0 - first) / (at.n + E));
     at.g = it / p.ngr;
     at.hg = it % p.ngr;
-    at.u = int((run0 - first) % at.n);
-    item_first = first + int64_t(it) * at.n;
+    const int in_item = int((run0 - first) % (at.n + E));
+    at.u = max(in_item - E, 0);
+    skip = max(E - in_item, 0);
+    item_first = first + int64_t(it) * (at.n + E) + E;
+    if (RUNS && run0 + skip >= run1) return;
   }
 
   // ---- copies: the walk `ld` runs ahead of `at` ----
   Walk<SHARED> ld = at;
-  int64_t ld_left = !SOLO || ld.b < p.B ? run1 - run0 : 0;
+  int64_t ld_left = !SOLO || ld.b < p.B ? run1 - run0 - skip : 0;
   uint32_t bad_ring = 0;  // stage x's page was out of range
   int page[C::kTiles];
   auto pages_of = [&](const Walk<SHARED>& w) {
@@ -373,7 +401,8 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       bad_ring = spoilt ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
       if (--ld_left > 0) {
         ld.template next<SOLO>(p, hop, ulog);
-        if (!SOLO || ld.b < p.B)
+        if (RUNS && ld.u == 0) ld_left = max(ld_left - E, int64_t(0));
+        if (RUNS ? ld_left > 0 : !SOLO || ld.b < p.B)
           pages_of(ld);
         else
           ld_left = 0;
@@ -394,7 +423,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       dead = !tc::mbar_wait_for(reinterpret_cast<uint64_t*>(fd_smem + SH::kFlags) - 1, 0, abort_flag, tc::kInjectedWaitCycles);
   }
   int h0 = 0, heads = 0;
-  for (int64_t z = run0; z < run1 && (!SOLO || at.b < p.B); ++z) {
+  for (int64_t z = run0 + skip; z < run1 && (!SOLO || at.b < p.B); ++z) {
     if (fresh) {
       h0 = at.g * p.hpg + at.hg * kFdMaxHeads;
       heads = min(p.hpg - at.hg * kFdMaxHeads, kFdMaxHeads);
@@ -481,7 +510,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
     }
     const bool whole = SOLO || (item_first >= run0 && ends);
     // SHARED: parts in the order of the items, those of one item in the order of the runs
-    const int item = at.b * items + at.g * p.ngr + at.hg, item_heads = SHARED ? min(p.hpg, kFdMaxHeads) : kFdMaxHeads;
+    const int item = at.b * items + at.g * p.ngr + at.hg, item_heads = SHARED || C::kBulk ? min(p.hpg, kFdMaxHeads) : kFdMaxHeads;
     const int slot = SHARED ? item + run : 2 * run + (item_first >= run0 ? 1 : 0);
     if (ALONE || warp == 0) {
       c.sum_l();
@@ -493,10 +522,22 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
         float inv[C::kM];
 #pragma unroll
         for (int x = 0; x < C::kM; ++x) inv[x] = bad ? 0.f : 1.f / c.l[x];
-        c.each([&](int h, int x, int dim, float val) {
-          if (h < heads)
-            out[(int64_t(b) * p.Hq + h0 + h) * D + dim] = from_f<T>(bad ? 0.f : val * inv[x]);
-        });
+        if constexpr (C::kBulk) {
+          c.each_run([&](int h, int x, int dim, float(&val)[C::kRunDims]) {
+            if (h >= heads) return;
+            uint4 w[C::kRunDims * sizeof(T) / 16];
+#pragma unroll
+            for (int y = 0; y < C::kRunDims; ++y) reinterpret_cast<T*>(w)[y] = from_f<T>(bad ? 0.f : val[y] * inv[x]);
+            uint4* dst = reinterpret_cast<uint4*>(out + (int64_t(b) * p.Hq + h0 + h) * D + dim);
+#pragma unroll
+            for (int y = 0; y < int(sizeof(w) / 16); ++y) dst[y] = w[y];
+          });
+        } else {
+          c.each([&](int h, int x, int dim, float val) {
+            if (h < heads)
+              out[(int64_t(b) * p.Hq + h0 + h) * D + dim] = from_f<T>(bad ? 0.f : val * inv[x]);
+          });
+        }
         if (p.lse)
           c.each_head([&](int h, int x) {
             if (h < heads) p.lse[int64_t(b) * p.Hq + h0 + h] = bad ? -INFINITY : (c.m[x] + log2f(c.l[x])) * kFdLn2;
@@ -504,9 +545,19 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       } else {
         float* po = p.part_o + int64_t(slot) * item_heads * D;
         float* pm = p.part_ml + int64_t(slot) * item_heads * 2;
-        c.each([&](int h, int, int dim, float val) {
-          if (h < heads) po[h * D + dim] = val;
-        });
+        if constexpr (C::kBulk) {
+          c.each_run([&](int h, int, int dim, float(&val)[C::kRunDims]) {
+            if (h >= heads) return;
+            float4* dst = reinterpret_cast<float4*>(po + h * D + dim);
+#pragma unroll
+            for (int y = 0; y < C::kRunDims / 4; ++y)
+              dst[y] = make_float4(val[4 * y], val[4 * y + 1], val[4 * y + 2], val[4 * y + 3]);
+          });
+        } else {
+          c.each([&](int h, int, int dim, float val) {
+            if (h < heads) po[h * D + dim] = val;
+          });
+        }
         c.each_head([&](int h, int x) {
           if (h < heads) {
             pm[2 * h] = c.m[x];
@@ -515,7 +566,10 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
         });
       }
     }
-    if (!SHARED && !whole) {
+    if constexpr (RUNS) {
+      if (!whole) (item_first >= run0 ? begun : came) = SplitItem{item_first, n, b * p.Hq + h0, heads};
+    }
+    if (!ALONE && !whole) {
       // the item's units lie in CTAs c0..c1: the last to arrive joins them
       const int c0 = int(item_first / per), c1 = int((item_first + n - 1) / per);
       if (warp == 0) {
@@ -537,15 +591,16 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
         for (int o = threadIdx.x * 4; o < heads * D; o += kFdThreads * 4)
           join_head<T>(p, int64_t(b) * p.Hq + h0 + o / D, D, o % D, c1 - c0 + 1, [&](int y) {
             const int cta = c0 + y, s = 2 * cta + (cta == c0 && item_first >= c0 * per ? 1 : 0);
-            const int64_t head = int64_t(s) * kFdMaxHeads + o / D;
+            const int64_t head = int64_t(s) * item_heads + o / D;
             return PartAt{p.part_o + head * D, p.part_ml + head * 2};
           });
       __syncthreads();  // last_s is read before the next item sets it
     }
-    if (ends) item_first += n;
+    if (ends) item_first += n + E;
     const int was = at.b;
     at.template next<SOLO>(p, hop, ulog);
-    if (at.b != was) item_first = z + 1;
+    if (at.b != was) item_first = z + 1 + E;
+    if (RUNS) z += E;
   }
   if constexpr (C::kBulk) {
     if (dead && issued > 0) {  // let the copies land before the CTA gives its shared memory up
@@ -558,10 +613,67 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   }
 }
 
+// RUNS: joins the items that lie in several warps' runs of `per` steps: those that
+// lie in this CTA, and of those that lie in several CTAs the ones that it is the last of.
+template <typename C>
+__device__ __forceinline__ void join_runs(const typename C::Params& p, int64_t per, const SplitItem& came, const SplitItem& begun) {
+  using T = typename C::T;
+  constexpr int D = C::kD, W = C::kWarps;
+  extern __shared__ __align__(1024) uint8_t fd_smem[];
+  int& last_s = *reinterpret_cast<int*>(fd_smem + FdShape<C>::kFlags);
+  // where warps' states would be joined: each warp's item in this CTA; the one from before, the one to behind
+  SplitItem* split = reinterpret_cast<SplitItem*>(fd_smem + W * (FdShape<C>::kRing + C::kExtra));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = min(p.hpg, kFdMaxHeads);
+  auto cta_of = [&](int64_t step) { return int(step / per) / W; };
+  auto join = [&](const SplitItem& s, int o) {  // four values
+    const int r0 = int(s.first / per), parts = int((s.first + s.n - 1) / per) - r0 + 1;
+    join_head<T, 4>(p, s.row + o / D, D, o % D, parts, [&](int y) {
+      const int64_t head = int64_t(2 * (r0 + y) + (y == 0 ? 1 : 0)) * heads + o / D;
+      return PartAt{p.part_o + head * D, p.part_ml + head * 2};
+    });
+  };
+  if (lane == 0) {
+    const bool here = begun.n > 0 && cta_of(begun.first + begun.n - 1) == int(blockIdx.x);
+    const SplitItem none{};
+    split[warp] = here ? begun : none;
+    if (warp == 0) split[W] = came;  // the CTA's first step is its first warp's
+    if (warp == 0) split[W + 1].n = 0;
+  }
+  __syncthreads();
+  if (lane == 0 && begun.n > 0 && split[warp].n == 0) split[W + 1] = begun;
+  const int each = heads * (D / 4);
+  for (int o = threadIdx.x; o < W * each; o += W * 32) {
+    const SplitItem& s = split[o / each];
+    if (s.n > 0 && o % each < s.heads * (D / 4)) join(s, o % each * 4);
+  }
+  __syncthreads();
+  for (int x = 0; x < 2; ++x) {
+    const SplitItem s = split[W + x];
+    if (s.n == 0) continue;
+    const int c0 = cta_of(s.first), c1 = cta_of(s.first + s.n - 1);
+    if (threadIdx.x == 0) {
+      // releases the CTA's stores (ordered by the barrier), acquires the others'
+      const int sh = 8 * (c0 & 3);
+      uint32_t old;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+                   : "=r"(old)
+                   : "l"(p.arrivals + (c0 >> 2)), "r"(1u << sh)
+                   : "memory");
+      last_s = int((old >> sh) & 0xffu) == c1 - c0;
+      if (last_s) atomicSub(p.arrivals + (c0 >> 2), uint32_t(c1 - c0 + 1) << sh);  // ready for the next call
+    }
+    __syncthreads();
+    if (last_s)
+      for (int o = threadIdx.x; o < s.heads * (D / 4); o += W * 32) join(s, o * 4);
+    __syncthreads();  // last_s is read before it is set again
+  }
+}
+
 template <typename C>
 __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_shared_kernel(const __grid_constant__ typename C::Params p) {
   tc::griddep_launch_dependents();  // the joins' grid, which waits for this one
-  decode_run<C, false, true>(p, 0);
+  SplitItem none{};
+  decode_run<C, false, true, false>(p, 0, none, none);
   tc::griddep_wait();  // this grid is not over before the prefixes' grid is
 }
 
@@ -589,28 +701,45 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
   }
 
   // ---- all units (every warp counts alone) ----
-  int64_t total = 0;
+  int64_t total = 0, steps = 0;
   int longest = 0;  // in warps' steps
 #pragma unroll 8
   for (int b = lane; b < p.B; b += 32) {
-    const int steps = units_of<false>(p, b, SH::kStepLog2);
-    total += (steps + kFdWarps - 1) / kFdWarps;
-    longest = max(longest, steps);
+    const int n = units_of<false>(p, b, SH::kStepLog2);
+    total += (n + kFdWarps - 1) / kFdWarps;
+    if (n > 0) steps += n + kFdItemSteps;
+    longest = max(longest, n);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  longest = __reduce_max_sync(0xffffffffu, longest);
   total *= items;
-  // Whole items for single warps, or shared-out units? A unit and a warp's step
-  // both take about 1.1 us, and so does an item's end or start; single warps
-  // come out ahead from 1.25 times the other count on. Measured both ways (Hq 32,
-  // Hkv 8, d 128, bf16; lengths within a factor of 2):
-  //   1280 items up to 64 keys   19 (single) : 29 us     2560 up to 256   65 :  70 us
-  //   10240 items up to 128      99 : 177 us             2560 up to 512  119 : 109 us
-  //   640 items up to 128        18 :  20 us              320 up to 128   17 :  16 us
-  const int warps = int(gridDim.x) * kFdWarps;
-  const int64_t all = int64_t(p.B) * items, rounds = (all + warps - 1) / warps;
-  const bool solo = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
+  const int64_t all = int64_t(p.B) * items;
+  bool alone;  // warps work alone, on whole items or (kBulk) on runs of steps
+  if constexpr (C::kBulk) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
+    steps *= items;
+    // Runs of steps for single warps, or shared-out units? In runs warps meet once, at
+    // the end; units cost a join by all warps per item. Measured both ways (d 128, bf16):
+    //   200 sequences of 100 to 500 keys, 800 items   43 (runs) : 78 us
+    //   128 of 2000 to 8000, 512                      226 : 240 us
+    //   64 of 4096, 256                               100 : 100 us     40 of 2000, 160    45 : 41 us
+    //   128 of 50 to 4000, one head, 128               39 :  33 us     1 of 777, 4        17 : 10 us
+    //   16 of 4 K to 128 K, 64 (long runs of warps lie far apart in memory)  338 : 320 us
+    alone = all >= int64_t(gridDim.x) && total <= 64 * all;
+  } else {
+    // Whole items for single warps, or shared-out units? A unit and a warp's step
+    // both take about 1.1 us, and so does an item's end or start; single warps
+    // come out ahead from 1.25 times the other count on. Measured both ways (Hq 32,
+    // Hkv 8, d 128, bf16; lengths within a factor of 2):
+    //   1280 items up to 64 keys   19 (single) : 29 us     2560 up to 256   65 :  70 us
+    //   10240 items up to 128      99 : 177 us             2560 up to 512  119 : 109 us
+    //   640 items up to 128        18 :  20 us              320 up to 128   17 :  16 us
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const int warps = int(gridDim.x) * kFdWarps;
+    const int64_t rounds = (all + warps - 1) / warps;
+    alone = 4 * rounds * (1 + longest) * int64_t(gridDim.x) <= 5 * (total + all);
+  }
   // sequences without keys: nobody's run holds them
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const Own o = own_of<false>(p, b);
@@ -620,10 +749,15 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     if (p.lse)
       for (int x = threadIdx.x; x < p.Hq; x += kFdThreads) p.lse[int64_t(b) * p.Hq + x] = -INFINITY;
   }
-  if (solo)
-    decode_run<C, true, false>(p, total);
-  else
-    decode_run<C, false, false>(p, total);
+  SplitItem came{}, begun{};
+  if (!alone) {
+    decode_run<C, false, false, false>(p, total, came, begun);
+  } else if constexpr (!C::kBulk) {
+    decode_run<C, true, false, false>(p, total, came, begun);
+  } else {
+    decode_run<C, false, false, true>(p, steps, came, begun);
+    join_runs<C>(p, run_steps<C>(steps), came, begun);
+  }
 }
 
 int fd_grid() { return kNumSMs; }

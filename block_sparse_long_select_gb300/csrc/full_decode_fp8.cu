@@ -367,8 +367,10 @@ struct Core8 {
     const int x = (t % HN) * 8 + h;
     return HT == 1 ? x : x < per ? (t / HN) * per + x : -1;
   }
+  // dims that a lane has of a head, which lie together
+  static constexpr int kRunDims = D / 8;
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each_run(F f) const {
     const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
 #pragma unroll
     for (int t = 0; t < kCols; ++t)
@@ -376,11 +378,10 @@ struct Core8 {
       for (int e = 0; e < 2; ++e) {
         const int h = head(t, 2 * tq + e);
         if (HT > 1 && h < 0) continue;
+        float v[kRunDims];
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            f(h, 2 * t + e, gq * (D / 8) + 2 * k + y, acc[(t * (D / 16) + k) * 4 + 2 * y + e]);
+        for (int k = 0; k < kRunDims; ++k) v[k] = acc[(t * (D / 16) + (k >> 1)) * 4 + 2 * (k & 1) + e];
+        f(h, 2 * t + e, gq * kRunDims, v);
       }
   }
   __device__ __forceinline__ void sum_l() {
@@ -427,6 +428,13 @@ cudaError_t run(Fd8Params& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   return decode<C, false>(p, "full_decode_fp8", stream);
 }
+// Whether items are pairs of key/value heads. fp32 queries are two terms, whose registers leave no room for them.
+bool in_pairs(int Hkv, int group, int dtype) { return dtype == MSA_BF16 && group <= 8 && Hkv % 2 == 0; }
+// Floats of the partials: two to a warp's run, of an item's heads
+size_t part_floats(int Hkv, int group, int d, int dtype) {
+  const int heads = std::min(in_pairs(Hkv, group, dtype) ? 2 * group : group, kFdMaxHeads);
+  return size_t(2) * fd_grid() * 8 * heads * d;
+}
 // Up to 8 query heads to a key/value head: a step has two tiles, of neighbouring
 // heads or of 32 keys, for d 64 four (a step's waits and look-ups cost as much as
 // for d 128: one key/value head 456 us, with two tiles 559, before copies took whole steps). More: two of keys.
@@ -436,13 +444,12 @@ template <int D>
 cudaError_t run_bf16(Fd8Params& p, cudaStream_t stream) {
   using T = __nv_bfloat16;
   if (p.group > 8) return run<T, D, 16, 2, 1>(p, stream);
-  if (p.kv_heads % 2) return run<T, D, 8, D == 64 ? 4 : 2, 1>(p, stream);
+  if (!in_pairs(p.kv_heads, p.group, MSA_BF16)) return run<T, D, 8, D == 64 ? 4 : 2, 1>(p, stream);
   p.Hkv = p.kv_heads / 2;  // pairs, as the items' heads
   p.hpg = 2 * p.group;
   p.ngr = 1;
   return run<T, D, 8, D == 64 ? 2 : 1, 2>(p, stream);
 }
-// fp32 queries are two terms, whose registers leave no room for pairs
 template <int D>
 cudaError_t run_f32(Fd8Params& p, cudaStream_t stream) {
   return p.group > 8 ? run<float, D, 16, 2, 1>(p, stream) : run<float, D, 8, 2, 1>(p, stream);
@@ -450,9 +457,15 @@ cudaError_t run_f32(Fd8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
+size_t full_decode_fp8_ws_bytes(int Hkv, int hpg, int d, int dtype) {
+  const size_t n = part_floats(Hkv, hpg, d, dtype);
+  return up256(n * 4) + up256(n / d * 8);
+}
+
 cudaError_t launch_full_decode_fp8(const FullArgs& a, const float* k_scale, const float* v_scale, cudaStream_t stream) {
   Fd8Params p{};
-  static_cast<FdParams&>(p) = fd_params(a, 2 * fd_grid());
+  static_cast<FdParams&>(p) = fd_params(a, 0);
+  p.part_ml = p.part_o + up256(part_floats(p.Hkv, p.hpg, a.d, a.dtype) * 4) / 4;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.kv_heads = p.Hkv;

@@ -255,6 +255,7 @@ struct FullBwdArgs {
   void *dq, *dk, *dv;
 };
 size_t full_decode_ws_bytes(int d);  // behind the header
+size_t full_decode_fp8_ws_bytes(int Hkv, int hpg, int d, int dtype);
 size_t full_backward_ws_bytes(int Tq, int Hq);  // behind the header
 size_t full_prefill_ws_bytes(int d, int64_t most_keys);  // bf16, behind the header
 // WsHeader::disorder for the calls of more than kSelfChecked sequences

@@ -237,6 +237,15 @@ def test_decode_many_sequences(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64), (6, 3, 64), (16, 1, 128), (64, 2, 128), (4, 4, 64)])
+def test_decode_runs_of_warps(heads, dtype):
+    """More items than SMs: items that end in a warp's run, lie in several warps' or in several CTAs'; two lengths of them."""
+    check_decode([(53 * b) % 300 for b in range(170)], *heads, dtype, 16, 16)
+    check_decode([5000, 1, 0, 2500] + [1 + b % 40 for b in range(160)], *heads, dtype, 64, 17)
+    check_decode([17] * 400, *heads, dtype, 32, 18)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_decode_growing_scores(dtype):
     """Keys whose scores rise along the sequence while their values' scales fall, and the other way round."""
     n, d = 600, 64
@@ -448,6 +457,28 @@ def test_decode_timeout_then_recovers():
     args = [x.to(DEV) for x in (q, *laid, torch.tensor(lens, dtype=torch.int32))]
     ws = msa.workspace(msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE_FP8, 3, 1, laid[4].shape[1] * 16, 2, 8, 64, 0, 0, 0,
                                               msa.MSA_BF16), DEV)
+    msa.msa_debug_inject_timeout(True)
+    try:
+        msa.msa_full_attn_decode_fp8(*args, ws=ws)
+        assert msa.msa_read_status(ws) == 5
+    finally:
+        msa.msa_debug_inject_timeout(False)
+    for _ in range(2):
+        out = msa.msa_full_attn_decode_fp8(*args, ws=ws)
+        assert msa.msa_read_status(ws) == 0
+        fp.assert_within(out, want[0], want[2], "out")
+
+
+def test_decode_timeout_of_many_items_then_recovers():
+    """The same where warps take runs of steps and items lie in several CTAs."""
+    g = torch.Generator().manual_seed(51)
+    lens = [1 + (61 * b) % 400 for b in range(180)]
+    parts, laid = _cache(lens, 2, 64, 16, g)
+    q = torch.randn(180, 8, 64, generator=g).to(BF16)
+    want = f8.decode(q, *parts, 0.125, BF16)
+    args = [x.to(DEV) for x in (q, *laid, torch.tensor(lens, dtype=torch.int32))]
+    ws = msa.workspace(msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE_FP8, 180, 1, laid[4].shape[1] * 16, 2, 8, 64, 0, 0,
+                                              0, msa.MSA_BF16), DEV)
     msa.msa_debug_inject_timeout(True)
     try:
         msa.msa_full_attn_decode_fp8(*args, ws=ws)
