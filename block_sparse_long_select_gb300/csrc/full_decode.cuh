@@ -139,47 +139,62 @@ __device__ __forceinline__ int units_of(const FdParams& p, int b, int unit_log2)
   return own_of<SHARED>(p, b).units(unit_log2);
 }
 
-// Four values of one head joined over `parts` parts, in order, and its lse. A
-// negative sum marks a head without a result.
-template <typename T, int kBatch = 8, typename F>  // kBatch: parts in flight, the loads of which do not wait for each other
+// Four values of each of ROWS heads joined over `parts` parts, in order, and their
+// lse. A negative sum marks a head without a result.
+template <typename T, int kBatch = 8, int ROWS = 1, typename F>  // kBatch: parts in flight, the loads of which do not wait for each other
 __device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D, int dim, int parts, F part_of) {
-  float M = -INFINITY, den = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
-  bool spoilt = false;
+  float M[ROWS], den[ROWS], sum[ROWS][4];
+  bool spoilt[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    M[r] = -INFINITY;
+    den[r] = sum[r][0] = sum[r][1] = sum[r][2] = sum[r][3] = 0.f;
+    spoilt[r] = false;
+  }
   for (int y0 = 0; y0 < parts; y0 += kBatch) {
-    float2 ml[kBatch];
-    float4 v[kBatch];
+    float2 ml[ROWS][kBatch];
+    float4 v[ROWS][kBatch];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
       const PartAt s = part_of(min(y0 + x, parts - 1));
-      ml[x] = __ldcg(reinterpret_cast<const float2*>(s.ml));
-      v[x] = __ldcg(reinterpret_cast<const float4*>(s.o + dim));
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        ml[r][x] = __ldcg(reinterpret_cast<const float2*>(s.ml) + r);
+        v[r][x] = __ldcg(reinterpret_cast<const float4*>(s.o + r * D + dim));
+      }
     }
-    float mn = M;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      spoilt |= ml[x].y < 0.f;
-      mn = fmaxf(mn, ml[x].x);
-    }
-    const float a = M == mn ? 1.f : ex2d(M - mn);
-    M = mn;
-    den *= a;
+    for (int r = 0; r < ROWS; ++r) {
+      float mn = M[r];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) sum[y] *= a;
+      for (int x = 0; x < kBatch; ++x) {
+        spoilt[r] |= ml[r][x].y < 0.f;
+        mn = fmaxf(mn, ml[r][x].x);
+      }
+      const float a = M[r] == mn ? 1.f : ex2d(M[r] - mn);
+      M[r] = mn;
+      den[r] *= a;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const float w = y0 + x >= parts ? 0.f : ml[x].x == M ? 1.f : ex2d(ml[x].x - M);
-      den = fmaf(w, ml[x].y, den);
-      sum[0] = fmaf(w, v[x].x, sum[0]);
-      sum[1] = fmaf(w, v[x].y, sum[1]);
-      sum[2] = fmaf(w, v[x].z, sum[2]);
-      sum[3] = fmaf(w, v[x].w, sum[3]);
+      for (int y = 0; y < 4; ++y) sum[r][y] *= a;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float w = y0 + x >= parts ? 0.f : ml[r][x].x == mn ? 1.f : ex2d(ml[r][x].x - mn);
+        den[r] = fmaf(w, ml[r][x].y, den[r]);
+        sum[r][0] = fmaf(w, v[r][x].x, sum[r][0]);
+        sum[r][1] = fmaf(w, v[r][x].y, sum[r][1]);
+        sum[r][2] = fmaf(w, v[r][x].z, sum[r][2]);
+        sum[r][3] = fmaf(w, v[r][x].w, sum[r][3]);
+      }
     }
   }
-  const float inv = 1.f / den;
-  T* dst = static_cast<T*>(p.out) + row * D + dim;
 #pragma unroll
-  for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt ? 0.f : sum[y] * inv);
-  if (p.lse && dim == 0) p.lse[row] = spoilt ? -INFINITY : (M + log2f(den)) * kFdLn2;
+  for (int r = 0; r < ROWS; ++r) {
+    const float inv = 1.f / den[r];
+    T* dst = static_cast<T*>(p.out) + (row + r) * D + dim;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(spoilt[r] ? 0.f : sum[r][y] * inv);
+    if (p.lse && dim == 0) p.lse[row + r] = spoilt[r] ? -INFINITY : (M[r] + log2f(den[r])) * kFdLn2;
+  }
 }
 
 // A walk over units in order: those of a CTA's run, or (SOLO) of every hop-th item.
@@ -297,7 +312,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   Walk<SHARED> at{};
   int64_t first = 0;  // number of the walk's sequence's first unit
   int64_t item_first = 0;  // number of the item's first unit
-  constexpr int E = RUNS ? kFdItemSteps : 0;  // counted ahead of an item's own
+  constexpr int E = RUNS ? kFdItemSteps : SHARED ? kOwnItemSteps : 0;  // counted ahead of an item's own
   int skip = 0;            // of those at the run's beginning
   if constexpr (SOLO) {
     at.seek(p, warp * int(gridDim.x) + int(blockIdx.x), hop, ulog);
@@ -337,7 +352,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
     at.u = max(in_item - E, 0);
     skip = max(E - in_item, 0);
     item_first = first + int64_t(it) * (at.n + E) + E;
-    if (RUNS && run0 + skip >= run1) return;
+    if ((RUNS || SHARED) && run0 + skip >= run1) return;
   }
 
   // ---- copies: the walk `ld` runs ahead of `at` ----
@@ -401,8 +416,8 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       bad_ring = spoilt ? bad_ring | (1u << st) : bad_ring & ~(1u << st);
       if (--ld_left > 0) {
         ld.template next<SOLO>(p, hop, ulog);
-        if (RUNS && ld.u == 0) ld_left = max(ld_left - E, int64_t(0));
-        if (RUNS ? ld_left > 0 : !SOLO || ld.b < p.B)
+        if ((RUNS || SHARED) && ld.u == 0) ld_left = max(ld_left - E, int64_t(0));
+        if (RUNS || SHARED ? ld_left > 0 : !SOLO || ld.b < p.B)
           pages_of(ld);
         else
           ld_left = 0;
@@ -600,7 +615,7 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
     const int was = at.b;
     at.template next<SOLO>(p, hop, ulog);
     if (at.b != was) item_first = z + 1 + E;
-    if (RUNS) z += E;
+    z += E;
   }
   if constexpr (C::kBulk) {
     if (dead && issued > 0) {  // let the copies land before the CTA gives its shared memory up

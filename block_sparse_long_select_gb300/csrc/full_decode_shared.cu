@@ -11,15 +11,16 @@
 namespace msa {
 namespace {
 
-// A thread per four values of a query head; D / 4 of them a head. All but the
-// parts is known before the grids that leave them end. Bound by latency: few rows
-// have twenty parts in flight, many rows fewer registers and so more warps (128 000
-// rows 101 us, 158 with ten). Small CTAs fit beside the decode grid's.
+// A thread per four values of a query head, or of four heads of one key/value head;
+// D / 4 of them a head. All but the parts is known before the grids that leave
+// them end. Bound by latency: few rows have twenty parts in flight, many rows four
+// of four heads, whose places are found once (128 000 rows 74 us; 102 with a head to a
+// thread, 158 with ten parts in flight). Small CTAs fit beside the decode grid's.
 constexpr int kJoinThreads = 128;
-template <typename T, int D, int BATCH, int CTAS>
+template <typename T, int D, int BATCH, int CTAS, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdParams p) {
   constexpr int kLanes = D / 4;
-  const int64_t row = int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+  const int64_t row = (int64_t(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes) * ROWS;
   const int dim = (threadIdx.x % kLanes) * 4;
   if (row >= int64_t(p.B) * p.Hq) {
     tc::griddep_wait();
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdP
     pre = p.shared.rows<D>(own.x, b, g, hg, head.per);
     if (const int n = own.units(4)) {
       const int it = g * p.ngr + hg / heads;
-      const int64_t at = step0 + int64_t(it) * n, c0 = at / head.own_per;
+      const int64_t at = step0 + int64_t(it) * (n + kOwnItemSteps) + kOwnItemSteps, c0 = at / head.own_per;
       part0 = int64_t(b) * p.Hkv * p.ngr + it + c0;
       parts = int((at + n - 1) / head.own_per - c0) + 1;
     }
@@ -46,27 +47,35 @@ __global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdP
   tc::griddep_wait();
   if (parts + pre.n == 0) {
     if (!own.ok && dim == 0) set_status(p.status, MSA_ERR_BOUNDS);
-    T* dst = static_cast<T*>(p.out) + row * D + dim;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(0.f);
-    if (p.lse && dim == 0) p.lse[row] = -INFINITY;
+    for (int r = 0; r < ROWS; ++r) {
+      T* dst = static_cast<T*>(p.out) + (row + r) * D + dim;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) dst[y] = from_f<T>(0.f);
+      if (p.lse && dim == 0) p.lse[row + r] = -INFINITY;
+    }
     return;
   }
-  join_head<T, BATCH>(p, row, D, dim, parts + pre.n, [&](int y) {
+  join_head<T, BATCH, ROWS>(p, row, D, dim, parts + pre.n, [&](int y) {
     if (y >= parts) return pre.part(y - parts);
     const int64_t at = (part0 + y) * heads + hg % heads;
     return PartAt{p.part_o + at * D, p.part_ml + at * 2};
   });
 }
 
+template <typename T, int D, int BATCH, int CTAS, int ROWS>
+cudaError_t launch_join(const FdParams& p, cudaStream_t stream) {
+  ProfScope pf("full_join", stream);
+  const int64_t threads = int64_t(p.B) * p.Hq / ROWS * (D / 4);
+  return launch_early(full_join_kernel<T, D, BATCH, CTAS, ROWS>, (threads + kJoinThreads - 1) / kJoinThreads, kJoinThreads, 0,
+                      stream, p);
+}
 template <typename T, int D>
 cudaError_t join(const FdParams& p, cudaStream_t stream) {
-  ProfScope pf("full_join", stream);
-  const int64_t ctas = (int64_t(p.B) * p.Hq * (D / 4) + kJoinThreads - 1) / kJoinThreads;
-  return launch_early(ctas <= 3 * kNumSMs   ? full_join_kernel<T, D, 20, 3>
-                      : ctas <= 8 * kNumSMs ? full_join_kernel<T, D, 10, 6>
-                                            : full_join_kernel<T, D, 4, 12>,
-                      ctas, kJoinThreads, 0, stream, p);
+  const int64_t ctas = int64_t(p.B) * p.Hq * (D / 4) / kJoinThreads;
+  if (ctas < 3 * kNumSMs) return launch_join<T, D, 20, 3, 1>(p, stream);
+  if (ctas < 8 * kNumSMs) return launch_join<T, D, 10, 6, 1>(p, stream);
+  return p.hpg % 4 == 0 ? launch_join<T, D, 4, 4, 4>(p, stream) : launch_join<T, D, 4, 12, 1>(p, stream);
 }
 template <typename T, int D, int H>
 cudaError_t run(const FdParams& p, cudaStream_t stream) {

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(NT) shared_plan_kernel(const PlanParams p) {
         }
       }
       s.seqs[b] = q;
-      if (q.from >= 0 && L > q.from) mine[0] = int64_t((L - q.from - 1) / kStepKeys + 1) * p.items;
+      if (q.from >= 0 && L > q.from) mine[0] = int64_t((L - q.from - 1) / kStepKeys + 1 + kOwnItemSteps) * p.items;
     }
     scan<NT>(mine, all);
     if (b < seqs) s.step0[b] = steps + mine[0];
