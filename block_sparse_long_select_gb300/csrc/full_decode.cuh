@@ -267,9 +267,8 @@ __device__ __forceinline__ int64_t run_steps(int64_t total) {
 }
 // An item of which a warp has the beginning or (the CTA's first warp) a later part.
 struct SplitItem {
-  int64_t first;  // number of its first step
-  int n;          // its steps; 0: none
-  int row, heads; // its first row of the output, its heads
+  int run, parts;  // the run that it begins in; the runs that it lies in, 0: no item
+  int row, heads;  // its first row of the output, its heads
 };
 
 // SOLO: whole items for single warps; SHARED, RUNS: the warp's run of the `total`
@@ -582,7 +581,10 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
       }
     }
     if constexpr (RUNS) {
-      if (!whole) (item_first >= run0 ? begun : came) = SplitItem{item_first, n, b * p.Hq + h0, heads};
+      if (!whole) {
+        const int r0 = int(item_first / per);
+        (item_first >= run0 ? begun : came) = SplitItem{r0, int((item_first + n - 1) / per) - r0 + 1, b * p.Hq + h0, heads};
+      }
     }
     if (!ALONE && !whole) {
       // the item's units lie in CTAs c0..c1: the last to arrive joins them
@@ -628,10 +630,10 @@ __device__ __forceinline__ void decode_run(const typename C::Params& p, int64_t 
   }
 }
 
-// RUNS: joins the items that lie in several warps' runs of `per` steps: those that
+// RUNS: joins the items that lie in several warps' runs: those that
 // lie in this CTA, and of those that lie in several CTAs the ones that it is the last of.
 template <typename C>
-__device__ __forceinline__ void join_runs(const typename C::Params& p, int64_t per, const SplitItem& came, const SplitItem& begun) {
+__device__ __forceinline__ void join_runs(const typename C::Params& p, const SplitItem& came, const SplitItem& begun) {
   using T = typename C::T;
   constexpr int D = C::kD, W = C::kWarps;
   extern __shared__ __align__(1024) uint8_t fd_smem[];
@@ -639,33 +641,31 @@ __device__ __forceinline__ void join_runs(const typename C::Params& p, int64_t p
   // where warps' states would be joined: each warp's item in this CTA; the one from before, the one to behind
   SplitItem* split = reinterpret_cast<SplitItem*>(fd_smem + W * (FdShape<C>::kRing + C::kExtra));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = min(p.hpg, kFdMaxHeads);
-  auto cta_of = [&](int64_t step) { return int(step / per) / W; };
   auto join = [&](const SplitItem& s, int o) {  // four values
-    const int r0 = int(s.first / per), parts = int((s.first + s.n - 1) / per) - r0 + 1;
-    join_head<T, 4>(p, s.row + o / D, D, o % D, parts, [&](int y) {
-      const int64_t head = int64_t(2 * (r0 + y) + (y == 0 ? 1 : 0)) * heads + o / D;
+    join_head<T, 4>(p, s.row + o / D, D, o % D, s.parts, [&](int y) {
+      const int64_t head = int64_t(2 * (s.run + y) + (y == 0 ? 1 : 0)) * heads + o / D;
       return PartAt{p.part_o + head * D, p.part_ml + head * 2};
     });
   };
   if (lane == 0) {
-    const bool here = begun.n > 0 && cta_of(begun.first + begun.n - 1) == int(blockIdx.x);
+    const bool here = begun.parts > 0 && (begun.run + begun.parts - 1) / W == int(blockIdx.x);
     const SplitItem none{};
     split[warp] = here ? begun : none;
     if (warp == 0) split[W] = came;  // the CTA's first step is its first warp's
-    if (warp == 0) split[W + 1].n = 0;
+    if (warp == 0) split[W + 1] = none;
   }
   __syncthreads();
-  if (lane == 0 && begun.n > 0 && split[warp].n == 0) split[W + 1] = begun;
+  if (lane == 0 && begun.parts > 0 && split[warp].parts == 0) split[W + 1] = begun;
   const int each = heads * (D / 4);
   for (int o = threadIdx.x; o < W * each; o += W * 32) {
-    const SplitItem& s = split[o / each];
-    if (s.n > 0 && o % each < s.heads * (D / 4)) join(s, o % each * 4);
+    const SplitItem s = split[o / each];
+    if (s.parts > 0 && o % each < s.heads * (D / 4)) join(s, o % each * 4);
   }
   __syncthreads();
   for (int x = 0; x < 2; ++x) {
     const SplitItem s = split[W + x];
-    if (s.n == 0) continue;
-    const int c0 = cta_of(s.first), c1 = cta_of(s.first + s.n - 1);
+    if (s.parts == 0) continue;
+    const int c0 = s.run / W, c1 = (s.run + s.parts - 1) / W;
     if (threadIdx.x == 0) {
       // releases the CTA's stores (ordered by the barrier), acquires the others'
       const int sh = 8 * (c0 & 3);
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     steps *= items;
     // Runs of steps for single warps, or shared-out units? In runs warps meet once, at
     // the end; units cost a join by all warps per item. Measured both ways (d 128, bf16):
-    //   200 sequences of 100 to 500 keys, 800 items   43 (runs) : 78 us
+    //   200 sequences of 100 to 500 keys, 800 items   41 (runs) : 78 us
     //   128 of 2000 to 8000, 512                      226 : 240 us
     //   64 of 4096, 256                               100 : 100 us     40 of 2000, 160    45 : 41 us
     //   128 of 50 to 4000, one head, 128               39 :  33 us     1 of 777, 4        17 : 10 us
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(FdShape<C>::kThreads, 1) full_decode_kernel(co
     decode_run<C, true, false, false>(p, total, came, begun);
   } else {
     decode_run<C, false, false, true>(p, steps, came, begun);
-    join_runs<C>(p, run_steps<C>(steps), came, begun);
+    join_runs<C>(p, came, begun);
   }
 }
 

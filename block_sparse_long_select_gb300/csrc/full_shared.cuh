@@ -49,7 +49,7 @@ struct PrefixRec {
 static_assert(sizeof(PrefixRec) == 48, "read as three 16-byte words");
 // What the planning CTA says of the whole call.
 struct SharedHead {
-  int64_t runs, steps;            // prefixes' runs; own keys' steps of all items
+  int64_t runs, steps;            // prefixes' runs; own keys' steps of all items, what their ends count among them
   int64_t own_per, disorder;      // steps of a warp; whether cu_prefix is out of order: then nothing else counts
   int per, each, ctas, own_ctas;  // units of a prefix's run at most; runs of a CTA, CTAs with runs; of the decode grid
 };
