@@ -156,11 +156,12 @@ __device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D,
     float4 v[ROWS][kBatch];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
-      const PartAt s = part_of(min(y0 + x, parts - 1));
+      const bool in = y0 + x < parts;  // places behind the last part hold zeros: weight 0 does not silence an infinity
+      const PartAt s = part_of(in ? y0 + x : 0);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        ml[r][x] = __ldcg(reinterpret_cast<const float2*>(s.ml) + r);
-        v[r][x] = __ldcg(reinterpret_cast<const float4*>(s.o + r * D + dim));
+        ml[r][x] = in ? __ldcg(reinterpret_cast<const float2*>(s.ml) + r) : make_float2(-INFINITY, 0.f);
+        v[r][x] = in ? __ldcg(reinterpret_cast<const float4*>(s.o + r * D + dim)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
 #pragma unroll
@@ -178,7 +179,7 @@ __device__ __forceinline__ void join_head(const FdParams& p, int64_t row, int D,
       for (int y = 0; y < 4; ++y) sum[r][y] *= a;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        const float w = y0 + x >= parts ? 0.f : ml[r][x].x == mn ? 1.f : ex2d(ml[r][x].x - mn);
+        const float w = ml[r][x].x == mn ? 1.f : ex2d(ml[r][x].x - mn);
         den[r] = fmaf(w, ml[r][x].y, den[r]);
         sum[r][0] = fmaf(w, v[r][x].x, sum[r][0]);
         sum[r][1] = fmaf(w, v[r][x].y, sum[r][1]);

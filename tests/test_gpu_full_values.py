@@ -136,3 +136,18 @@ def test_gradients_of_long_documents(heads, lens):
         for name, x, w, t in zip(("dq", "dk", "dv"), got, want, tol):
             fp.assert_within(x[sl], w.cpu(), t.cpu(), f"{name} of {n}")
         at += n
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_split_decode_of_infinite_values(d, dtype):
+    """An infinite value makes its element infinite, also where it lies in the last
+    of an item's parts, and leaves the other elements alone."""
+    g = torch.Generator().manual_seed(3)
+    for n in (6000, 700, 128 * 9 + 1, 40):
+        q, k, v = (torch.randn(x, h, d, generator=g).to(dtype) for x, h in ((1, 4), (n, 1), (n, 1)))
+        v[-1, 0, 3], v[-1, 0, 5], v[n // 2, 0, 9] = math.inf, -math.inf, math.inf
+        want = fp.prefill(q, [k], [v], [(0, 1)], d ** -0.5, dtype)
+        kc, vc, table = (x.to(DEV) for x in fp.paged([k], [v], 16, g))
+        out = msa.msa_full_attn_decode(q.to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+        fp.assert_within(out, want[0], want[2], f"{n} keys")

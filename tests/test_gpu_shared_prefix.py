@@ -365,3 +365,28 @@ def test_caches_past_32_bits(dtype):
     table = torch.where((table >= 0) & (table < kc.shape[0]), table + (pages - kc.shape[0]), table).to(torch.int32)
     out = msa.msa_full_attn_decode_shared(q, there(kc), there(vc), table, kv, cu, pre)
     fp.assert_within(out, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (8, 2, 128), (5, 1, 64)])
+def test_infinite_values(heads, dtype):
+    """Values of the prefix and of own keys that are infinite make their elements so, as
+    msa_full_attn_decode's, and leave the others alone: few rows and many, whose joins differ."""
+    for groups in ([(1040, [5, 0, 300])], [(272, [9, 1])] * 30, [(272, [9, 1, 40] * 40)], [(16, [700])]):
+        *args, _ = make(groups, *heads, dtype, 16, 40)
+        q, kc, vc, table, kv, cu, pre = args
+        full = table.clone()  # every sequence's pages
+        for x, (n, _) in enumerate(groups):
+            a, e = int(cu[x]), int(cu[x + 1])
+            full[a:e, :n // 16] = table[a, :n // 16]
+            vc[table[a, n // 16 - 1].long(), 15, :, 3] = math.inf  # the prefix's last key
+            for b in range(a, e, 2):
+                last = int(kv[b]) - 1
+                if last >= n:
+                    vc[table[b, last // 16].long(), last % 16, :, 5] = -math.inf
+        B = q.shape[0]
+        ks, vs = ([x[full[b, :-(-int(kv[b]) // 16)].long()].flatten(0, 1)[:int(kv[b])] for b in range(B)] for x in (kc, vc))
+        want = fp.prefill(q, ks, vs, [(b, 1) for b in range(B)], heads[2] ** -0.5, dtype)
+        assert want[0].isinf().any() and not want[0].isnan().any()
+        out = msa.msa_full_attn_decode_shared(*[x.to(DEV) for x in args])
+        fp.assert_within(out, want[0], want[2], "out")
