@@ -30,6 +30,7 @@
 namespace msa {
 namespace {
 
+constexpr float kLeast = -100.f;  // log2 of the least factor that is taken at once
 constexpr float kTop = 7.f;  // weights reach 2^(kTop + kFdLazy): what f16 drops below 2^-24 is 2^-39 of the largest
 
 __device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -350,16 +351,27 @@ struct Core8 {
         }
       }
   }
-  // the weights' own maximum is taken out again: from here on a state is as any other's
+  // The weights' own maximum is taken out again: from here on a state is as any other's.
+  // Scales down to 2^-126 make a factor below fp32's normal numbers of values that
+  // are normal, so what is below 2^-100 of it comes second.
   __device__ __forceinline__ void finish() {
-#pragma unroll
-    for (int i = 0; i < kM; ++i) {
-      const float a = mw[i] == -INFINITY ? 1.f : ex2d(mw[i] - m[i]);
+    bool low = false;
+    auto times = [&](int i, float a) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         acc[((i >> 1) * (D / 16) + k) * 4 + (i & 1)] *= a;
         acc[((i >> 1) * (D / 16) + k) * 4 + 2 + (i & 1)] *= a;
       }
+    };
+#pragma unroll
+    for (int i = 0; i < kM; ++i) {
+      mw[i] = mw[i] == -INFINITY ? 0.f : mw[i] - m[i];
+      low |= mw[i] < kLeast;
+      times(i, ex2d(fmaxf(mw[i], kLeast)));
+    }
+    if (__any_sync(0xffffffffu, low)) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i) times(i, ex2d(fminf(mw[i] - kLeast, 0.f)));
     }
   }
   // head h of column t, or -1

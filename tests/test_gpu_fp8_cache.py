@@ -537,3 +537,52 @@ def test_append_in_place(T, dtype):
     want = msa.msa_paged_append_fp8(q, k, k, rope, cu, kv, table, *cache)
     got = msa.msa_paged_append_fp8(q, k, k, rope, cu, kv, table, *cache, q_out=q)
     assert got is q and torch.equal(got, want)
+
+
+def check_parts(q, parts, dtype, scale, page=16, seed=0, floor=0.0, copies=1):
+    """Decode over given codes and scales; `copies`: that many sequences read the same pages."""
+    g = torch.Generator().manual_seed(seed)
+    kc, vc, ks, vs, table = f8.paged(*parts, page, g)
+    out_w, lse_w, tol, ltol = f8.decode(q, *parts, scale, dtype)
+    lens = torch.tensor([x.shape[0] for x in parts[0]], dtype=torch.int32)
+    q, table, lens = (x.repeat(copies, *[1] * (x.dim() - 1)) for x in (q, table, lens))
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = msa.msa_full_attn_decode_fp8(*[x.to(DEV) for x in (q, kc, vc, ks, vs, table, lens)], scale=scale, lse=lse)
+    many = lambda x: x.repeat(copies, *[1] * (x.dim() - 1))  # noqa: E731
+    fp.assert_within(out, many(out_w), many(tol) + floor, "out")
+    fp.assert_within(lse, many(lse_w), many(ltol), "lse")
+
+
+def subnormal_floor(n, dtype):
+    """Behind the last factor each of up to n / 16 + 8 sums rounds by half of fp32's
+    least step, 2^-149; a bf16 output by half of 2^-133."""
+    return (n // 16 + 8) * 2.0 ** -150 + (2.0 ** -134 if dtype == BF16 else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64), (3, 3, 64), (16, 1, 128)])
+def test_decode_least_value_scales(heads, dtype):
+    """Value scales down to 2^-126, which is what an append writes for the smallest
+    rows: codes up to 448 make normal numbers of them."""
+    Hq, Hkv, d = heads
+    for top, lens, copies in ((-126, [40, 1, 530], 1), (-120, [300], 1), (-100, [40, 700], 1), (-126, [37, 5], 200)):
+        g = torch.Generator().manual_seed(80 - top)
+        q = torch.randn(len(lens), Hq, d, generator=g).to(dtype)
+        (ck, cv, sk, sv), _ = _cache(lens, Hkv, d, 16, g)
+        sv = [torch.exp2(torch.randint(-126, top + 1, x.shape, generator=g).float()) for x in sv]
+        check_parts(q, (ck, cv, sk, sv), dtype, d ** -0.5, floor=subnormal_floor(max(lens), dtype), copies=copies)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_largest_weight_without_values(dtype):
+    """Keys with most of the weight and values of 0, beside others with small scales."""
+    n, d = 150, 64
+    g = torch.Generator().manual_seed(90)
+    kcode = torch.zeros(n, 1, d).to(f8.E4M3)
+    kcode[:, :, 0] = torch.ones(n, 1).to(f8.E4M3)
+    vcode = torch.randn(n, 1, d, generator=g).to(f8.E4M3)
+    ks, vs = torch.rand(n, 1, generator=g), torch.full((n, 1), 2.0 ** -112)
+    ks[::30], vs[::30] = 10.0, 0.0  # 2^-13 of theirs
+    q = torch.zeros(1, 2, d)
+    q[..., 0] = 1.0
+    check_parts(q.to(dtype), ([kcode], [vcode], [ks], [vs]), dtype, 1.0, floor=subnormal_floor(n, dtype))
