@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t high2(uint32_t x) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float lg2(float x) {  // -inf of 0 and of what is below 2^-126
+__device__ __forceinline__ float lg2(float x) {  // of subnormal scales as well: their values need not be
   float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {

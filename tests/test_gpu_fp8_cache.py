@@ -586,3 +586,15 @@ def test_decode_largest_weight_without_values(dtype):
     q = torch.zeros(1, 2, d)
     q[..., 0] = 1.0
     check_parts(q.to(dtype), ([kcode], [vcode], [ks], [vs]), dtype, 1.0, floor=subnormal_floor(n, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_subnormal_value_scales(dtype):
+    """Another writer's scales below 2^-126: finite and not negative, so they are taken."""
+    lens, d = [40, 300], 128
+    g = torch.Generator().manual_seed(91)
+    q = torch.randn(2, 8, d, generator=g).to(dtype)
+    (ck, cv, sk, sv), _ = _cache(lens, 2, d, 16, g)
+    sv = [torch.randint(1 << 18, 1 << 23, x.shape, generator=g).double().mul(2.0 ** -149).float() for x in sv]
+    assert all(((x > 0) & (x < 2.0 ** -126)).all() for x in sv)
+    check_parts(q, (ck, cv, sk, sv), dtype, d ** -0.5, floor=subnormal_floor(300, dtype))
