@@ -15,9 +15,13 @@
 // with a running maximum mw of its own, so that w fits f16 whatever the scales
 // are. The sum of the weights keeps to exp2(s_j - m).
 //   q: each head's row is multiplied by a power of two that takes its largest
-//      element to [2^14, 2^15): bf16 values are exact in f16 within 2^-28 of
-//      that; fp32 queries are two f16 terms (22 bits).
-//   w: one f16 term (2^-11) for bf16, two for fp32.
+//      element to [2^14, 2^15): bf16 values are exact in f16 down to 2^-28 of that,
+//      smaller ones within 2^-39 of it; fp32 queries are two f16 terms (22 bits).
+//   w: one f16 term (11 bits) for bf16, two for fp32 (22).
+// A second term is held times 2^11, as it would soon be below f16's least step (fp32
+// weights of 2^-18 of the largest would have 13 bits), and its products of a tile are
+// added to the first term's as a whole. fp32, 16 sequences of 4 K to 128 K keys: 422 us,
+// 404 with second terms as they are, 440 with the values times 2^-11 in their place.
 // A contraction does not care for the order of its index, so each lane takes
 // the bytes that lie together: 16-byte reads of K rows are the scores' operand
 // as they stand, and of V rows after pairing the bytes of two keys.
@@ -31,7 +35,9 @@ namespace msa {
 namespace {
 
 constexpr float kLeast = -100.f;  // log2 of the least factor that is taken at once
-constexpr float kTop = 7.f;  // weights reach 2^(kTop + kFdLazy): what f16 drops below 2^-24 is 2^-39 of the largest
+// Weights reach 2^(kTop + kFdLazy), and the largest so far is 2^kTop at least: half of
+// f16's least step, 2^-25, is 2^-32 of it at most (2^-40 at best).
+constexpr float kTop = 7.f;
 
 __device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -60,10 +66,12 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
 }
-// what an f16 pair leaves of a and b (nothing of an infinity)
+// What an f16 pair leaves of a and b (nothing of an infinity), times 2^11, which makes
+// it no larger than the pair: as it is, f16's least step would take its bits from
+// weights of 2^-10 of the largest on.
 __device__ __forceinline__ uint32_t rest_f16(uint32_t packed, float a, float b) {
   const float2 f = __half22float2(reinterpret_cast<const __half2&>(packed));
-  return pack_f16(fabsf(f.x) < INFINITY ? a - f.x : 0.f, fabsf(f.y) < INFINITY ? b - f.y : 0.f);
+  return pack_f16(fabsf(f.x) < INFINITY ? (a - f.x) * 2048.f : 0.f, fabsf(f.y) < INFINITY ? (b - f.y) * 2048.f : 0.f);
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -243,6 +251,7 @@ struct Core8 {
         const uint32_t kt = stage + z * kHead + i * kTile, sc = scale_at(p, extra, z, i * kSub) + gq * 4;
 #pragma unroll
         for (int t = z * HN; t < (z + 1) * HN; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
+        [[maybe_unused]] float rest[HN][4] = {};  // of the queries' second terms, 2^11 times as large
 #pragma unroll
         for (int c = 0; c < kWords / 4; ++c) {  // keys gq and gq + 8
           const uint4 lo = lds16(at(kt, gq, tq * (kWords / 4) + c)), hi = lds16(at(kt, gq + 8, tq * (kWords / 4) + c));
@@ -251,10 +260,19 @@ struct Core8 {
           for (int w = 0; w < 4; ++w) {
             const uint32_t a[4] = {low2(r0[w]), low2(r1[w]), high2(r0[w]), high2(r1[w])};
 #pragma unroll
-            for (int t = z * HN; t < (z + 1) * HN; ++t)
+            for (int t = z * HN; t < (z + 1) * HN; ++t) mma16816h(s[i][t], a, qf[t][0][c * 4 + w][0], qf[t][0][c * 4 + w][1]);
+            if constexpr (kTerms == 2) {
 #pragma unroll
-              for (int y = 0; y < kTerms; ++y) mma16816h(s[i][t], a, qf[t][y][c * 4 + w][0], qf[t][y][c * 4 + w][1]);
+              for (int t = 0; t < HN; ++t)
+                mma16816h(rest[t], a, qf[z * HN + t][1][c * 4 + w][0], qf[z * HN + t][1][c * 4 + w][1]);
+            }
           }
+        }
+        if constexpr (kTerms == 2) {
+#pragma unroll
+          for (int t = 0; t < HN; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][z * HN + t][e] = fmaf(rest[t][e], 1.f / 2048.f, s[i][z * HN + t][e]);
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
@@ -341,11 +359,19 @@ struct Core8 {
             const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
             const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
             const uint32_t a[4] = {low2(lo), high2(lo), low2(hi), high2(hi)};
+            auto sum = [&](int n) -> float(&)[4] {
+              return reinterpret_cast<float(&)[4]>(acc[((z * HN + n) * (D / 16) + 2 * w + y) * 4]);
+            };
 #pragma unroll
-            for (int n = 0; n < HN; ++n) {
-              float(&c)[4] = reinterpret_cast<float(&)[4]>(acc[((z * HN + n) * (D / 16) + 2 * w + y) * 4]);
+            for (int n = 0; n < HN; ++n) mma16816h(sum(n), a, b[n][0][0], b[n][0][1]);
+            if constexpr (kTerms == 2) {
 #pragma unroll
-              for (int q = 0; q < kTerms; ++q) mma16816h(c, a, b[n][q][0], b[n][q][1]);
+              for (int n = 0; n < HN; ++n) {
+                float rest[4] = {};
+                mma16816h(rest, a, b[n][1][0], b[n][1][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum(n)[e] = fmaf(rest[e], 1.f / 2048.f, sum(n)[e]);
+              }
             }
           }
         }

@@ -447,9 +447,11 @@ msa_status_t msa_paged_read_fp8(const void* k_cache, const void* v_cache, const 
  * (a row of scale NaN makes the heads that see it NaN); all else as there.
  *  ws: msa_workspace_size(MSA_OP_FULL_DECODE_FP8, B, 1, max_pages * page_size,
  *  Hkv, Hq, d, 0, 0, 0, dtype)
- *  Products are exact, sums in fp32; each key's weight is rounded to 11 bits
- *  before its product with v for BF16, to 22 for FP32 (queries too).
- *  Deterministic. */
+ *  Products are exact, sums in fp32. A key's weight times its value's scale is
+ *  rounded before its product with v: to 11 bits for BF16, 22 for FP32; below
+ *  2^-21 of the largest one to 2^-32 (FP32: 2^-43) of that. Query elements below
+ *  2^-28 of their head's largest are rounded to 2^-39 (FP32: 2^-50) of that, FP32
+ *  ones above it to 22 bits. Deterministic. */
 msa_status_t msa_full_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                                       const float* v_scale, const int32_t* page_table, const int32_t* kv_len, int B,
                                       int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages, float scale,

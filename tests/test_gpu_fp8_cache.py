@@ -598,3 +598,58 @@ def test_decode_subnormal_value_scales(dtype):
     sv = [torch.randint(1 << 18, 1 << 23, x.shape, generator=g).double().mul(2.0 ** -149).float() for x in sv]
     assert all(((x > 0) & (x < 2.0 ** -126)).all() for x in sv)
     check_parts(q, (ck, cv, sk, sv), dtype, d ** -0.5, floor=subnormal_floor(300, dtype))
+
+
+# What a weight's terms leave of it, of the largest weight (times its value's scale) that the warp has seen, which
+# stands between 2^7 and 2^15: half of f16's least step, 2^-25, or that of a second term 2^11 times as large, 2^-36.
+WEIGHT_FLOOR = {BF16: 2.0 ** -32, FP32: 2.0 ** -43}
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("steps", [0.4, 5.5, 32.5, 2048.5])
+@pytest.mark.parametrize("n,copies", [(400, 1300), (20000, 1300)])
+def test_decode_flat_tail_behind_large_weights(n, copies, steps, dtype):
+    """A few keys with nearly all of the weight, whose values are 0 in half of the
+    dims, and a long tail of equal small weights, each `steps` times f16's least step:
+    in those dims the output is the tail's. Enough sequences that a warp walks the
+    tail behind a large weight."""
+    d, tail = 64, math.log(2.0 ** 7 / (steps * 2.0 ** -24))
+    g = torch.Generator().manual_seed(92)
+    kcode = torch.zeros(n, 1, d).to(f8.E4M3)
+    kcode[:, :, 0] = torch.ones(n, 1).to(f8.E4M3)
+    vcode = (1 + torch.rand(n, 1, d, generator=g)).to(f8.E4M3)
+    ks, vs = torch.zeros(n, 1), torch.ones(n, 1)
+    large = torch.arange(0, 256, 32)  # one for each warp of a CTA
+    ks[large] = tail
+    vcode[large, :, 32:] = torch.zeros(8, 1, 32).to(f8.E4M3)
+    q = torch.zeros(1, 1, d)
+    q[..., 0] = 1.0
+    # f8.decode's bound but for what is below the weights' least steps: that is in proportion to the tail's own values
+    out, lse, _, ltol = f8.decode(q.to(dtype), [kcode], [vcode], [ks], [vs], 1.0, dtype)
+    x = ks[:, 0].double()
+    p = torch.exp(x - lse[0, 0])
+    v = vcode[:, 0].double()
+    es = ((d + 4) * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22) * tail
+    ep = 2 * es + 2.0 ** -21 + 2.0 ** -22 * (tail / math.log(2) + 16)
+    tol = fp.U[dtype] * out[0, 0].abs() + (p[:, None] * v).sum(0) * (f8.U_W[dtype] + ep + n * 2.0 ** -23)
+    tol = tol + WEIGHT_FLOOR[dtype] * p.max() * v.sum(0)
+    kc, vc, ksp, vsp, table = f8.paged([kcode], [vcode], [ks], [vs], 64, g)
+    kv = torch.full((copies,), n, dtype=torch.int32)
+    args = [x.to(DEV) for x in (q.to(dtype).repeat(copies, 1, 1), kc, vc, ksp, vsp, table.repeat(copies, 1), kv)]
+    lse_got = torch.empty(copies, 1, device=DEV)
+    got = msa.msa_full_attn_decode_fp8(*args, scale=1.0, lse=lse_got)
+    fp.assert_within(got, out.expand(copies, 1, d), tol.expand(copies, 1, d), "out")
+    fp.assert_within(lse_got, lse.expand(copies, 1), ltol.expand(copies, 1), "lse")
+
+
+def test_decode_small_query_elements():
+    """fp32 queries, one element 2^28 times the others, where all keys are 0: the
+    others keep 22 bits (2^-50 of the largest)."""
+    g = torch.Generator().manual_seed(93)
+    for d in (64, 128):
+        q = torch.randn(2, 8, d, generator=g)
+        q[..., 7] = 2.0 ** 28
+        (ck, cv, sk, sv), _ = _cache([40, 300], 2, d, 16, g)
+        for x in ck:
+            x.view(torch.uint8)[..., 7] = 0
+        check_parts(q, (ck, cv, sk, sv), FP32, d ** -0.5)
