@@ -392,8 +392,9 @@ msa_status_t msa_full_attn_decode(const void* q, const void* k_cache, const void
  *              that has keys; the others' entries for them are not read.
  *  0 <= P <= B; with P = 0 (cu_prefix, prefix_len may be NULL) as msa_full_attn_decode
  *  ws: msa_workspace_size(MSA_OP_FULL_DECODE_SHARED, B, P, max_pages * page_size,
- *  Hkv, Hq, d, 0, 0, 0, dtype): 2 d + 4 fp32 values per query head and sequence,
- *  and up to 60 MB
+ *  Hkv, Hq, d, 0, 0, 0, dtype): 2 d + 4 fp32 values per query head and sequence
+ *  (of more than 16 heads to a key/value head as many as the next multiple of 16),
+ *  24 bytes per sequence, 48 per group, and up to 52 MB
  *  A sequence with fewer keys than its group's prefix, or whose group's
  *  prefix_len is not a multiple of page_size or out of range, sets MSA_ERR_BOUNDS and gives
  *  out 0 and lse -inf, as does every sequence of a group one of whose prefix's pages is

@@ -58,3 +58,19 @@ def test_binding_refuses_wrong_tensors():
     i = torch.tensor([0, 4], dtype=torch.int32)
     with pytest.raises(ValueError):
         msa.msa_full_attn_decode_shared(q, k, k, torch.zeros(4, 1, dtype=torch.int32), i, i, i[1:])
+
+
+def test_workspace_is_as_large_as_stated():
+    """2 d + 4 fp32 values per query head and sequence, a key/value head's heads beyond
+    16 counted in sixteens, 24 bytes per sequence, 48 per group, and up to 52 MB."""
+    for dt in (BF16, FP32):
+        for d in (64, 128):
+            for hpg in (1, 2, 3, 4, 7, 8, 15, 16, 17, 24, 33, 48, 49, 64):
+                for Hkv in (1, 3, 8):
+                    for B, G in ((1, 1), (97, 3), (4000, 1000), (4000, 4000), (65536, 65536), (1 << 20, 1 << 20)):
+                        n = msa.msa_workspace_size(msa.MSA_OP_FULL_DECODE_SHARED, B, G, 1000, Hkv, Hkv * hpg, d, 0, 0, 0,
+                                                   dt)
+                        if B * Hkv * hpg > 1 << 26 and n == 0:
+                            continue  # more rows than a call takes
+                        heads = Hkv * (hpg if hpg <= 16 else -(-hpg // 16) * 16)
+                        assert B * heads * d * 4 < n <= B * heads * (2 * d + 4) * 4 + 24 * B + 48 * G + 52e6
