@@ -261,6 +261,18 @@ __device__ __forceinline__ void store8(void* p, const uint32_t* v) {
                : "memory");
 }
 
+// code * scale as bf16, rounded once. The product has up to 28 bits, so by way of fp32
+// it would be rounded twice. It goes by the next fp32 number towards 0 instead, whose
+// last bit is set if the product lies beyond it (rounding to odd): bf16 then rounds to
+// the side on which the product is.
+template <typename T>
+__device__ __forceinline__ T rounded_once(float code, float scale) {
+  const float a = fabsf(code), b = fabsf(scale), near = __fmul_rz(a, b);
+  const uint32_t beyond = __fmaf_ru(a, b, -near) > 0.f ? 1u : 0u;  // also of what is below the least step; not of NaN
+  const uint32_t sign = (__float_as_uint(code) ^ __float_as_uint(scale)) & 0x80000000u;
+  return from_f<T>(__uint_as_float(__float_as_uint(near) | beyond | sign));
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const ReadArgs a, int rows, const SmallDiv by_heads, bool sectors) {
   constexpr int N = 16, L = D / N;          // codes of a unit, units of a head's row
@@ -329,33 +341,43 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_fp8_kernel(const Read
                   ? nullptr
                   : static_cast<T*>(is_v ? a.v_out : a.k_out) + (int64_t(t0 + x) * a.Hkv + h) * D + c * N;
     }
+    auto store = [&](auto value) {
 #pragma unroll
-    for (int y = 0; y < kBatch; ++y) {
-      if (!to[y]) continue;
-      const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
-      constexpr int kWords = N * int(sizeof(T)) / 4;
-      uint32_t out[kWords];
-      T* o = reinterpret_cast<T*>(out);
+      for (int y = 0; y < kBatch; ++y) {
+        if (!to[y]) continue;
+        const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
+        constexpr int kWords = N * int(sizeof(T)) / 4;
+        uint32_t out[kWords];
+        T* o = reinterpret_cast<T*>(out);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        uint32_t f;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(uint16_t(w[i / 2] >> (16 * (i & 1)))));
-        float lo, hi;
-        asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(f));
-        o[2 * i] = from_f<T>(lo * scale[y]);
-        o[2 * i + 1] = from_f<T>(hi * scale[y]);
-      }
+        for (int i = 0; i < N / 2; ++i) {
+          uint32_t f;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(uint16_t(w[i / 2] >> (16 * (i & 1)))));
+          float lo, hi;
+          asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(f));
+          o[2 * i] = value(lo, scale[y]);
+          o[2 * i + 1] = value(hi, scale[y]);
+        }
 #pragma unroll
-      for (int i = 0; i < kWords; i += 8) {
-        uint32_t* p = reinterpret_cast<uint32_t*>(to[y]) + i;
-        if (sectors) {
-          store8(p, out + i);
-        } else {
-          reinterpret_cast<uint4*>(p)[0] = make_uint4(out[i], out[i + 1], out[i + 2], out[i + 3]);
-          reinterpret_cast<uint4*>(p)[1] = make_uint4(out[i + 4], out[i + 5], out[i + 6], out[i + 7]);
+        for (int i = 0; i < kWords; i += 8) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(to[y]) + i;
+          if (sectors) {
+            store8(p, out + i);
+          } else {
+            reinterpret_cast<uint4*>(p)[0] = make_uint4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+            reinterpret_cast<uint4*>(p)[1] = make_uint4(out[i + 4], out[i + 5], out[i + 6], out[i + 7]);
+          }
         }
       }
-    }
+    };
+    // powers of two, as appends write them, have exact products (the longer way for all: 50 us in place of 46)
+    uint32_t fraction = 0;
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) fraction |= __float_as_uint(scale[y]) << 9;
+    if (sizeof(T) == 4 || fraction == 0)
+      store([](float c, float s) { return from_f<T>(c * s); });
+    else
+      store([](float c, float s) { return rounded_once<T>(c, s); });
   }
 }
 

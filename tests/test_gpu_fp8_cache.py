@@ -653,3 +653,63 @@ def test_decode_small_query_elements():
         for x in ck:
             x.view(torch.uint8)[..., 7] = 0
         check_parts(q, (ck, cv, sk, sv), FP32, d ** -0.5)
+
+
+def to_bf16_once(x):
+    """64-bit values rounded to bf16, to nearest even, once (a cast goes by way of fp32)."""
+    bits = x.view(torch.int64)
+    y = (bits + (1 << 44) - 1 + ((bits >> 45) & 1)) & ~((1 << 45) - 1)
+    y = y.view(torch.float64)
+    least = 2.0 ** -133
+    y = torch.where(x.abs() < 2.0 ** -126, torch.round(x / least) * least, y)
+    y = torch.where(y.abs() >= 2.0 ** 128, torch.copysign(torch.full_like(y, math.inf), y), y)
+    assert torch.equal(y.float().to(BF16).double()[y.isfinite()], y[y.isfinite()])
+    return y.float().to(BF16)
+
+
+def _read_back(codes, scale, dtype):
+    """Packed codes [T, Hkv, d] and scales [T, Hkv] as one sequence's cache, read whole."""
+    T, Hkv, d = codes.shape
+    g = torch.Generator().manual_seed(94)
+    kc, vc, ks, vs, table = f8.paged([codes], [codes], [scale], [scale.flip(0)], 16, g)
+    cu, kv = torch.tensor([0, T], dtype=torch.int32), torch.tensor([T], dtype=torch.int32)
+    k, v = msa.msa_paged_read_fp8(*[x.to(DEV) for x in (kc, vc, ks, vs, table, cu, kv)], T, dtype=dtype)
+    for got, s in ((k, scale), (v, scale.flip(0))):
+        exact = codes.double() * s.double()[..., None]  # 28 bits
+        want = to_bf16_once(exact) if dtype == BF16 else exact.float()
+        got = got.cpu()
+        assert torch.equal(got.isnan(), want.isnan())
+        same = (got == want) | got.isnan()
+        assert same.all(), f"{int((~same).sum())} of {same.numel()} are rounded twice"
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_read_rounds_once(dtype):
+    """Scales that are no powers of two: 28 bits of code times scale are rounded to
+    the output's type at once. Here code 9/8 times scale lies next to the middle of two
+    bf16 numbers, closer to it than fp32 can tell."""
+    near = []
+    for k in range(128, 256):  # (2 k + 1) 2^-8: between k and k + 1
+        for e in (1, 2, 3, -1, -2, -3):
+            if ((2 * k + 1) * 2 ** 18 + e) % 9 == 0:
+                near.append(((2 * k + 1) * 2 ** 18 + e) // 9 * 2.0 ** -23)  # 9 scale = middle + e 2^-26
+    scale = torch.tensor(near, dtype=torch.float64)
+    assert len(near) > 60 and torch.equal(scale.float().double(), scale)
+    scale = scale.float()[:, None].repeat(1, 2)
+    codes = torch.full((len(near), 2, 64), 1.125).to(f8.E4M3)
+    codes[:, 1, ::2] = torch.full((len(near), 32), -1.125).to(f8.E4M3)
+    for z in (0, -60, 100, -126):
+        _read_back(codes, scale * 2.0 ** z, dtype)
+    _read_back(codes, -scale, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_read_any_scales(dtype):
+    """All codes, with scales over fp32's whole range, subnormal ones, 0, infinity and NaN."""
+    g = torch.Generator().manual_seed(95)
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 4, 64).repeat(300, 1, 1).view(f8.E4M3)
+    bits = torch.randint(-2 ** 31, 2 ** 31, (300, 4), generator=g).to(torch.int32)
+    bits[:40] &= 0x007fffff
+    scale = bits.view(torch.float32)
+    scale[40:44, 0] = torch.tensor([0.0, math.inf, -math.inf, math.nan])
+    _read_back(codes, scale, dtype)
