@@ -102,8 +102,10 @@ struct FdParams {
   PageMap pages;
   int B, Hq, Hkv, hpg, ngr, cap;  // ngr: head groups (items) per key/value head; cap: most keys
   float scale_log2;
-  float* part_o;   // [2 * grid][16][D]; SHARED: [items + warps][heads of an item][D]
-  float* part_ml;  // [2 * grid][16][2]; SHARED: [items + warps][heads of an item][2]: maximum (log2 units), sum; a negative sum marks a page out of range
+  // Partials. Slots: two of 16 heads for each CTA; caches in 8 bits: two for each warp, SHARED: one for
+  // each item and warp, of as many heads as an item has.
+  float* part_o;   // [slots][heads][D]
+  float* part_ml;  // [slots][heads][2]: maximum (log2 units), sum; a negative sum marks a page out of range
   uint32_t* arrivals;  // a byte per CTA, zero between calls: the parts of the split item that it holds the first of
   void* out;
   float* lse;

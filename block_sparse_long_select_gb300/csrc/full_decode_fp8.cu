@@ -6,7 +6,8 @@
 // Bound: HBM, d + 4 bytes per key and per value where bf16 takes 2 d. Walk,
 // copies and joins: full_decode.cuh. Measured (Hq 32, Hkv 8, d 128, bf16): 16
 // sequences of 4 K to 128 K keys 303 to 319 us, 6.2 to 6.6 TB/s (92 to 97 % of the
-// copy rate); one of 777 keys 10.7 us, latency. d 64: 6.0 to 6.6 TB/s, instructions.
+// copy rate); one of 777 keys 10.3 us, latency. fp32 queries: 422 us, the second terms'
+// products; d 64: instructions (at run_bf16).
 //
 // Products: mma.sync m16n8k16 in f16, which holds every e4m3 code exactly (bf16
 // would as well, but the hardware converts e4m3 to f16 in one instruction for
@@ -476,8 +477,8 @@ size_t part_floats(int Hkv, int group, int d, int dtype) {
 // Up to 8 query heads to a key/value head: a step has two tiles, of neighbouring
 // heads or of 32 keys, for d 64 four (a step's waits and look-ups cost as much as
 // for d 128: one key/value head 456 us, with two tiles 559, before copies took whole steps). More: two of keys.
-// d 64: 6.0 to 6.6 TB/s (a key's scores and weights take as long as for d 128, its
-// bytes half; four heads of one tile instead of two of two: 7 % slower).
+// d 64: 6.0 to 6.6 TB/s, bound by instructions: a key's scores and weights take as many
+// as for d 128, its bytes half (four heads of one tile instead of two of two: 7 % slower).
 template <int D>
 cudaError_t run_bf16(Fd8Params& p, cudaStream_t stream) {
   using T = __nv_bfloat16;

@@ -1,11 +1,13 @@
 // Decode over shared prefixes: each sequence's own keys by the decode kernel's
 // walk (full_decode.cuh), and the join of its parts with those that the
 // prefixes' grid left (full_prefix_tc.cu, full_prefix_fp32.cu). Each of the three
-// grids starts while the one before it ends. Bound: HBM while both walks run, and
-// about 20 us of plan, first loads and joins. Measured, whole calls (Hq 32, Hkv 8,
-// d 128, bf16; bytes that have to be read at the copy rate: 87, 87, 7 us): 97
-// sequences of 1300 own keys behind three prefixes, 20 K keys, 109 us; 24 behind
-// 128 K keys 106; 32 of 100 behind 8 K 28.
+// grids behind the plan starts while the one before it ends. Bound: HBM while both
+// walks run, and about 20 us of plan, first loads and joins. Measured, whole calls (Hq 32,
+// Hkv 8, d 128, bf16; bytes that have to be read at the copy rate: 87, 87, 7 us): 97
+// sequences of 1300 own keys behind three prefixes, 20 K keys, 108 us; 24 behind
+// 128 K keys 107; 32 of up to 200 behind 8 K 28. The 20 us are there however little is
+// shared: full_decode.cu's one grid is as fast up to about 16 K keys of prefix times
+// sequences (16 sequences behind 1 K: 19 us both; 4 behind 8 K: 24 and 23).
 #include "full_decode_cores.cuh"
 
 namespace msa {
@@ -14,8 +16,9 @@ namespace {
 // A thread per four values of a query head, or of four heads of one key/value head;
 // D / 4 of them a head. All but the parts is known before the grids that leave
 // them end. Bound by latency: few rows have twenty parts in flight, many rows four
-// of four heads, whose places are found once (128 000 rows 74 us; 102 with a head to a
-// thread, 158 with ten parts in flight). Small CTAs fit beside the decode grid's.
+// of four heads, whose places are found once (128 000 rows 62 us; a head to a thread
+// took 1.4, ten parts in flight 2.1 times as long). Ten parts in 80 registers spill
+// 56 bytes, a head to a thread in 40 registers 96. Small CTAs fit beside the decode grid's.
 constexpr int kJoinThreads = 128;
 template <typename T, int D, int BATCH, int CTAS, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads, CTAS) full_join_kernel(const FdParams p) {

@@ -276,7 +276,7 @@ cudaError_t launch_full_decode_fp8(const FullArgs& a, const float* k_scale, cons
 cudaError_t launch_full_prefill_tc(const FullArgs& a, cudaStream_t stream);
 // tcgen05 backward (bf16); needs Tq, Tk > 0
 cudaError_t launch_full_backward_tc(const FullBwdArgs& a, cudaStream_t stream);
-// decode where groups of sequences share a prefix: two grids; needs groups > 0
+// decode where groups of sequences share a prefix: four grids (plan, prefixes, own keys, joins); needs groups > 0
 size_t full_shared_ws_bytes(int B, int groups, int Hkv, int hpg, int d, int dtype);  // behind the header
 cudaError_t launch_decode_shared(const FullArgs& a, const int32_t* cu_prefix, const int32_t* prefix_len, int groups,
                                  cudaStream_t stream);

@@ -151,6 +151,9 @@ cudaError_t prefix(const SharedArgs& a, cudaStream_t stream) {
 }  // namespace
 
 PrefixGeometry prefix_geometry_f32(int hpg) {
+  // Every group of two or more is items. Measured (Hq 8, Hkv 2, d 64; `worth` 1, 4, 16): 1000 sequences of 100 keys in
+  // 250 groups behind 128 keys 67, 61, 67 us, behind 512 112, 112, 114; 512 of 200 in 256 behind 256 67, 67, 58; 200 of
+  // 100 in 50 behind 1024 61, 61, 56; ten in two groups behind up to 600 19, 19, 15; 32 of 100 behind 8 K 38 with each.
   const int heads = hpg < 16 ? hpg : 16;
   return {heads, ceil_div(hpg, heads), kA / heads, 0, kA, 2 * kNumSMs, 1, 0, 1};
 }

@@ -14,7 +14,9 @@
 // rows and take the key tiles alternately, each with a maximum, sum and output
 // of its own; the two warpgroups then join them, half the columns each. K and V
 // tiles come through one ring in the order in which the products need them. The maximum only moves when a tile exceeds it by more than 2^8;
-// P is rounded to bf16 for its product, the sum takes it unrounded.
+// P is rounded to bf16 for its product, the sum takes it unrounded: the operands of a
+// product have one type, and a second term for what that drops would be a second product with V. Prefill and decode
+// do the same (outputs 0.0023 from 64 bits, 0.0017 of it their own rounding).
 //
 // Bound: HBM for up to 128 rows (64 KB of keys and values for 2 d 128^2 products
 // of each kind), the tensor cores and the chain from scores to weights above.
@@ -24,7 +26,7 @@
 // Warps: 0 loads (TMA; zeroes value rows behind the prefix's end), 1 MMA issue
 // and TMEM, 2 the parts of this CTA's run (3 idles), 4-7 and 8-11 the two
 // softmax warpgroups, one thread per row. Every wait is bounded. Nothing waits
-// for another CTA: the decode grid joins the parts.
+// for another CTA: a grid of their own joins the parts.
 #include "full_shared.cuh"
 #include "full_tc.cuh"
 
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         while (ok && plan.at < plan.end) {
           PxItem d;
           d.d = plan.next();
-          // the part's own pages in range; if not, the decode grid finds its rows marked
+          // the part's own pages in range; if not, the joins find its rows marked
           const int32_t* row = p.pages.table + int64_t(d.d.leader) * p.pages.max_pages;
           const int per = kKeys >> p.pages.page_log2, to = min((d.d.jb + d.d.n) * per, d.d.Lk >> p.pages.page_log2);
           bool bad = false;

@@ -24,7 +24,7 @@ namespace msa {
 
 constexpr int kPxKeys = 128;  // keys of a tile
 // What an item's beginning and end count beside its steps in the decode grid (4000
-// sequences of 100 keys in 1000 groups behind 512: 0 steps 922 us, 2 852, 4 857).
+// sequences of 100 keys in 1000 groups behind 512: 0 steps 866 us, 2 794, 4 800).
 constexpr int kOwnItemSteps = 2;
 
 // How rows are cut into items. bf16: two row tiles of `half` sequences, which

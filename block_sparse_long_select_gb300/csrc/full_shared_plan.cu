@@ -15,12 +15,14 @@ constexpr int kOwnLeast = 2;   // steps of a warp at least: each item of its run
 // scores to weights. So each grid gets as many SMs as its work says: the
 // prefixes' other CTAs leave at once, the decode grid's take their place and share
 // out what there is among as many as fit. Measured, one after the other and side
-// by side (Hq 32, Hkv 8, d 128):
-//   97 sequences, 1300 own keys behind 3 prefixes, 20 K   130 : 112 us
-//   32 sequences, 100 behind 8 K                           36 :  29 us
-//   64 sequences, 500 behind 8 K                           64 :  50 us
-//   64 sequences, 4000 behind 8 K                         204 : 189 us
-// (`beside` 24; 13 leaves the prefixes too few, 144, 29, 52, 247 us; 42: 115, 35, 54, 190.)
+// by side (bf16, Hq 32, Hkv 8, d 128; no other heads):
+//   97 sequences, 1300 own keys behind 3 prefixes, 20 K   117 : 109 us
+//   32 sequences, 100 behind 8 K                           27 :  24 us
+//   64 sequences, 500 behind 8 K                           58 :  47 us
+//   64 sequences, 4000 behind 8 K                         197 : 184 us
+//   4000 sequences, 100 in 1000 groups behind 512         703 : 794 us
+// (`beside` 24; 13 leaves the prefixes too few, 169, 24, 57, 248, 705 us; 42: 112, 24, 53, 184, 1028.
+// The fp32 grid has two CTAs to an SM and counts no SMs of its own: one after the other.)
 constexpr int kLeastOwn = 8;  // SMs of the decode grid
 
 // Sums over the CTA: what the threads before this one have, and all (whole CTA).
@@ -91,9 +93,9 @@ __global__ void __launch_bounds__(NT) shared_plan_kernel(const PlanParams p) {
   };
   // Whether a prefix of n key tiles is worth an item's start and end (bf16: about 7 us
   // beside 1.1 us a tile; a sequence walks a tile in as much by itself, out of L2
-  // from the second on). 512 sequences of 200 keys, each a group behind 512: 374 us
-  // as items, 279 by themselves; 4000 of 100 keys in 1000 groups of about four behind
-  // 256: 646 with all groups of three as items (`worth` 4), 679 (6), 738 (8), 894 (16).
+  // from the second on). 512 sequences of 200 keys, each a group behind 512: 298 us
+  // as items, 258 by themselves; 4000 of 100 keys in 1000 groups of about four behind
+  // 256: 580 with all groups of three as items (`worth` 4), 672 (8), 828 (16).
   auto worth = [&](int count, int n) { return int64_t(n) * (count - 1) >= s.geo.worth; };
   auto look = [&](int x) {
     Group g{0, 0, 0, 0};

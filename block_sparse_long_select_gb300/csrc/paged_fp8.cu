@@ -32,6 +32,12 @@
 namespace msa {
 namespace {
 
+// Up to kAppFewTokens tokens get a CTA each. Single tokens, a CTA : a warp for each, us:
+//   tokens               64         304         608         912        1216        4864
+//   bf16 32/8/128    4.0 : 6.3   8.3 : 8.1  13.9 : 8.4  19.4 : 9.3  25.1 : 9.5  102 : 26
+//   fp32 8/2/64      3.4 : 4.1   5.2 : 5.6   5.4 : 5.8   5.6 : 6.1   6.0 : 6.2   14 : 9
+//   fp32 32/8/128    3.8 : 9.7   6.1 : 12    9.1 : 12     12 : 13     15 : 13    65 : 44
+// One limit for all; bf16 rows of many heads would be best off with about 300.
 constexpr int kAppThreads = 128, kAppMostThreads = 512, kAppFewTokens = 4 * kNumSMs;
 constexpr int kReadThreads = 256, kReadRows = 16;
 
@@ -42,7 +48,8 @@ struct SmallDiv {
   __device__ __forceinline__ int of(int x) const { return d == 1 ? x : int(__umulhi(uint32_t(x), m)); }
 };
 
-// a b + c d, rounded to fp32 once but for errors below 2^-45 of the larger product
+// a b + c d, rounded to fp32 once but for errors below 2^-45 of the larger product:
+// Dekker's exact products (by FMA) and Knuth's exact sum
 __device__ __forceinline__ float dot2(float a, float b, float c, float d) {
   const float p = __fmul_rn(a, b), q = __fmul_rn(c, d);
   const float ep = __fmaf_rn(a, b, -p), eq = __fmaf_rn(c, d, -q);  // exact errors of the products
