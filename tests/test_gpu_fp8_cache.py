@@ -713,3 +713,12 @@ def test_read_any_scales(dtype):
     scale = bits.view(torch.float32)
     scale[40:44, 0] = torch.tensor([0.0, math.inf, -math.inf, math.nan])
     _read_back(codes, scale, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_many_heads(dtype):
+    """More key/value heads than a reciprocal divides exactly by, more items than warps."""
+    check_append([3, 1], [14, 0], 9000, 9000, 64, dtype, 16, 32, False, 96, behind=1)
+    check_append([1, 1], [14, 0], 20000, 20000, 64, dtype, 16, 0, False, 97, cu_given=False, with_q=False)
+    for heads in ((1024, 1024, 64), (512, 64, 128), (2100, 700, 64), (701, 701, 64)):
+        check_decode([40, 1, 130], *heads, dtype, 16, 98)

@@ -390,3 +390,10 @@ def test_infinite_values(heads, dtype):
         assert want[0].isinf().any() and not want[0].isnan().any()
         out = msa.msa_full_attn_decode_shared(*[x.to(DEV) for x in args])
         fp.assert_within(out, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads", [(1024, 1024, 64), (512, 64, 128), (2100, 700, 64)])
+def test_many_heads(heads, dtype):
+    """More items of one sequence than there are CTAs or warps."""
+    check([(144, [5, 1, 64]), (32, [17, None])], *heads, dtype, 16, 41, before=[33])
