@@ -278,13 +278,22 @@ struct Core8 {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           lv[i][z][y] = lg2(lds1(sc + kBoth * kScales / 2 + 32 * y));
-          const float ks = lds1(sc + 32 * y), hidden = i * kSub + gq + 8 * y < valid ? 0.f : -INFINITY;
+          const float ks = lds1(sc + 32 * y);
 #pragma unroll
           for (int t = z * HN; t < (z + 1) * HN; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s[i][t][2 * y + e] = fmaf(s[i][t][2 * y + e], qs[2 * t + e] * ks, hidden);
+            for (int e = 0; e < 2; ++e) s[i][t][2 * y + e] *= qs[2 * t + e] * ks;
         }
       }
+    if (valid < KT * kSub) {  // whatever an infinite query makes of the zeros behind the end
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int t = 0; t < kCols; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i * kSub + gq + 8 * (e >> 1) >= valid) s[i][t][e] = -INFINITY;
+    }
     // The maxima are only looked for across the lanes when some score is beyond 2^8 of its own.
     float mt[kM], mv[kM];
     bool up = false;

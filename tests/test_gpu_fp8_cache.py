@@ -722,3 +722,37 @@ def test_many_heads(dtype):
     check_append([1, 1], [14, 0], 20000, 20000, 64, dtype, 16, 0, False, 97, cu_given=False, with_q=False)
     for heads in ((1024, 1024, 64), (512, 64, 128), (2100, 700, 64), (701, 701, 64)):
         check_decode([40, 1, 130], *heads, dtype, 16, 98)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_rows_without_a_finite_score(d, dtype):
+    """Scores that overflow to -inf, or are -inf by an infinite query: NaN where there are no
+    others, -inf as the sum's logarithm, also where keys end inside a step."""
+    g = torch.Generator().manual_seed(99)
+    lens = [40, 300, 5, 64]
+    q = (torch.randn(4, 8, d, generator=g).abs() + 1) * 2.0 ** 60
+    (ck, cv, sk, sv), _ = _cache(lens, 2, d, 16, g)
+    for b, n in ((0, 40), (1, 130)):
+        ck[b][:n] = torch.full((n, 2, d), -448.0).to(f8.E4M3)
+        sk[b][:n] = 2.0 ** 64  # scores of -2^130 and below
+    sk[1][130:] *= 2.0 ** -60
+    for b in (2, 3):  # 0 in all dims but the first, where every key is positive
+        q[b] = 0.0
+        q[b, 1::2, 0] = -math.inf
+        ck[b][:, :, 0] = torch.ones(lens[b], 2).to(f8.E4M3)
+    q = q.to(dtype)
+    kc, vc, ks, vs, table = f8.paged(ck, cv, sk, sv, 16, g)
+    kv = torch.tensor(lens, dtype=torch.int32)
+    lse = torch.empty(4, 8, device=DEV)
+    out = msa.msa_full_attn_decode_fp8(*[x.to(DEV) for x in (q, kc, vc, ks, vs, table, kv)], lse=lse)
+    undefined = torch.zeros(4, 8, dtype=torch.bool)
+    undefined[0], undefined[2:, 1::2] = True, True
+    assert out.cpu()[undefined].isnan().all() and (lse.cpu()[undefined] == -math.inf).all()
+    cut = lambda x: [x[1][130:], x[2], x[3]]  # noqa: E731
+    q[2:, 1::2] = 0.0
+    want = f8.decode(q[1:], cut(ck), cut(cv), cut(sk), cut(sv), d ** -0.5, dtype)
+    for w in want:
+        w[undefined[1:]] = math.nan
+    fp.assert_within(out[1:], want[0], want[2], "out")
+    fp.assert_within(lse[1:], want[1], want[3], "lse")
